@@ -299,6 +299,138 @@ int klt_route_noalloc(const float* logits, int32_t M, int32_t E, int32_t topk, i
                       float* weights, int32_t* cnt, int32_t* off, int32_t* gidx,
                       int32_t* slot, int32_t* pos, void* stream);
 
+/* ------------------------------------------------- operators around the tail
+ *
+ * The steps between layers and the dense FP8 layers beside the mixture-of-experts ones, in
+ * the tail's own formats: bf16 (or fp32) activations, and e4m3 codes with one fp32 scale
+ * per row and 128 columns (activations) or per 128 x 128 block (weights).  Calls are
+ * asynchronous on `stream`, make no host synchronisation and can be captured in CUDA
+ * graphs; none of them keeps state between calls, so calls on several streams may overlap
+ * as long as their outputs differ.  Strides (ld_*) count elements from one row to the next;
+ * columns are contiguous.  Tensors of these calls need the alignment of their element type
+ * only, except where a rule is given; rows that start on 16 bytes are faster. */
+
+/* Element types of activations. */
+enum klt_dtype {
+  KLT_DT_BF16 = 0,
+  KLT_DT_F32 = 1,
+  KLT_DT_E4M3 = 2 /* e4m3 codes with a scale per row and 128 columns (outputs only)      */
+};
+
+/* Quantise x [M, K] (bf16 or fp32) to e4m3 codes q [M, K] and fp32 scales s
+ * [M, ceil(K / 128)] (contiguous): per row and 128 columns s = amax / 448 in fp32 (1 where
+ * that is 0), codes e4m3(fp32(x / s)), nearest even, saturating; the last group may be
+ * short.  The same values as the tail's own latent quantisation.  A group that
+ * holds an infinity or a NaN gets a scale that is not finite.
+ * Any K >= 1; M == 0 launches nothing.  Bytes of q between K and ld_q are left as they are.
+ * Errors: KLT_ERR_INVALID_ARG (M < 0, K < 1, null pointer, negative or overlapping output
+ * stride), KLT_ERR_UNSUPPORTED (unknown x_dtype, more than 2^31 launch blocks),
+ * KLT_ERR_ALIGN (element alignment), KLT_ERR_CUDA. */
+int klt_quantize(const void* x, int32_t x_dtype, int64_t ld_x, int32_t M, int32_t K,
+                 uint8_t* q, int64_t ld_q, float* s, void* stream);
+
+/* Largest row klt_block_norm accepts. */
+#define KLT_BLOCK_NORM_MAX_H 16384
+
+/* The norms before and after a block, fused with its gate and residual scale: for a row of
+ * the residual stream h and of the block's output y,
+ *   u  = y / sqrt(mean(y^2) + eps) * gamma_post       (u = y when gamma_post is NULL)
+ *   h' = res_scale * h + branch_scale * g * u         (h' = res_scale * h when y is NULL)
+ *   n  = h' / sqrt(mean(h'^2) + eps) * gamma_pre      (n = h' when gamma_pre is NULL)
+ * with g = gate, or 1 / (1 + e^-gate) with gate_sigmoid, or 1 when gate is NULL.  Everything
+ * is fp32 until the outputs, each rounded once; n and its codes come from the unrounded h'.
+ * So one call leaves a block and enters the next one; y == NULL enters the first block. */
+typedef struct klt_block_norm_args {
+  int32_t M, H;           /* rows; columns, 1 <= H <= KLT_BLOCK_NORM_MAX_H               */
+  int32_t h_dtype;        /* of h and h_out: KLT_DT_BF16 or KLT_DT_F32                    */
+  int32_t y_dtype;        /* KLT_DT_BF16 or KLT_DT_F32                                    */
+  int32_t gate_dtype;     /* KLT_DT_BF16 or KLT_DT_F32                                    */
+  int32_t gate_sigmoid;   /* non-zero: g = sigmoid(gate)                                  */
+  float eps, res_scale, branch_scale;
+  const void* h;          /* [M, H] residual stream                                       */
+  const void* y;          /* [M, H] block output, or NULL                                 */
+  const void* gate;       /* element (m, c) at m * gate_row + c * gate_col, or NULL: strides
+                             (0, 1) one gate per channel, (1, 0) one per token            */
+  const void* gamma_post; /* bf16 [H] or NULL                                             */
+  const void* gamma_pre;  /* bf16 [H] or NULL                                             */
+  void* h_out;            /* h' [M, H], or NULL; may be h itself with the same stride     */
+  void* n;                /* bf16 [M, H], or NULL; may be y (bf16) with the same stride   */
+  uint8_t* q;             /* e4m3 codes of n [M, H], or NULL (as klt_quantize, from the
+                             unrounded n)                                                 */
+  float* s;               /* scales of q [M, ceil(H / 128)], with q                       */
+  int64_t ld_h, ld_y, gate_row, gate_col, ld_h_out, ld_n, ld_q;
+} klt_block_norm_args;
+
+/* Run klt_block_norm_args on `stream`.  M == 0 launches nothing.  Outputs overlap each
+ * other or the inputs only as the fields above allow.
+ * Errors: KLT_ERR_INVALID_ARG (null args or h, M < 0, H < 1, eps negative or NaN, no output
+ * at all, q without s or s without q, gate or gamma_post without y, negative stride, output
+ * rows that overlap), KLT_ERR_UNSUPPORTED (H too large, unknown dtype), KLT_ERR_ALIGN
+ * (element alignment), KLT_ERR_CUDA. */
+int klt_block_norm(const klt_block_norm_args* a, void* stream);
+
+/* A linear layer with FP8 weights, y = x W^T:  out[m, o] = sum over k of
+ * (xq[m, k] xs[m, k / 128]) (wq[o, k] ws[o / 128, k / 128]); products of 128 columns are
+ * summed by the tensor core in fp32, scaled and added up in fp32, and rounded once. */
+enum klt_linear_act {
+  KLT_ACT_NONE = 0,
+  KLT_ACT_SWIGLU = 1 /* out[m, i] = silu(y[m, i]) * y[m, N/2 + i]: the gate rows of W come
+                        first, as in the expert weights; N a multiple of 256              */
+};
+typedef struct klt_linear_dims {
+  int32_t N;         /* rows of W (outputs; for SwiGLU twice the outputs), >= 1           */
+  int32_t K;         /* columns of W, >= 1                                                */
+  int32_t act;       /* enum klt_linear_act                                               */
+  int32_t out_dtype; /* KLT_DT_BF16; KLT_DT_F32 (KLT_ACT_NONE only); KLT_DT_E4M3
+                        (KLT_ACT_SWIGLU only): codes and scales as klt_quantize of the
+                        unrounded fp32 result                                             */
+} klt_linear_dims;
+
+typedef struct klt_linear klt_linear;
+
+/* Test and tuning hooks of klt_linear_forward (NULL or zeros = none). */
+typedef struct klt_linear_debug {
+  int32_t stall_after_kblocks; /* > 0: every copy producer stops after that many k-blocks, so
+                                  the waits on its data run out (klt_linear_status)       */
+  int32_t timeout_ms;          /* bound of every on-device wait (0 = 1000 ms)             */
+  int32_t force_tile;          /* token tile: 16, 32, 64, 128 = feature-major kernel, 256 =
+                                  token-major kernel, 0 = chosen from the sizes           */
+  int32_t force_split;         /* parts that K is split into: 1, 2, 4, 8; 0 = chosen      */
+} klt_linear_debug;
+
+/* Create a linear layer on the current device.  w: e4m3 [N, K] row-major; w_scale: fp32
+ * [ceil(N / 128), ceil(K / 128)]; both device memory, copied (re-laid out) into memory the
+ * handle owns; the caller's buffers are not referenced after the call returns.
+ * Synchronous.  Errors: KLT_ERR_INVALID_ARG (null pointer), KLT_ERR_UNSUPPORTED (shape or
+ * format rules above; N or K above 2^20; device is not compute capability 10.3),
+ * KLT_ERR_ALIGN (w_scale not 4-byte aligned), KLT_ERR_OOM, KLT_ERR_CUDA.  On error *out is
+ * left NULL. */
+int klt_linear_create(const klt_linear_dims* d, const void* w, const float* w_scale,
+                      klt_linear** out);
+
+/* out = act(x W^T) for M tokens.  xq: e4m3 [M, K], 16-byte aligned, ld_xq a multiple of 16;
+ * xs: fp32 [M, ceil(K / 128)] contiguous; out: [M, N] (SwiGLU: [M, N/2]) of out_dtype;
+ * out_s: fp32 [M, N / 256] for KLT_DT_E4M3, else ignored.  M == 0 launches nothing.  The
+ * handle has no workspace: calls on several streams may overlap.  One launch.
+ * Errors: KLT_ERR_INVALID_ARG (null handle or pointer, M < 0 or M > 2^22, a stride shorter
+ * than a row, another device current than at creation, bad debug value), KLT_ERR_UNSUPPORTED
+ * (debug: a tile and split that do not go together), KLT_ERR_ALIGN (xq or ld_xq not 16-byte,
+ * out not element aligned), KLT_ERR_CUDA.  Expired device waits: klt_linear_status. */
+int klt_linear_forward(klt_linear* h, const uint8_t* xq, int64_t ld_xq, const float* xs,
+                       int32_t M, void* out, int64_t ld_out, float* out_s,
+                       const klt_linear_debug* dbg, void* stream);
+
+/* Kernel configuration klt_linear_forward chooses for M tokens: the token tile (as
+ * force_tile) plus 1000 times the K split, or the negated status code. */
+int klt_linear_tile(const klt_linear* h, int32_t M);
+
+/* Sticky device status, as klt_status: KLT_OK or KLT_ERR_DEVICE_TIMEOUT, read
+ * synchronously; call it after the forward's stream has been synchronised. */
+int klt_linear_status(klt_linear* h);
+
+/* Free everything the handle owns (synchronises the device first).  NULL is a no-op. */
+int klt_linear_destroy(klt_linear* h);
+
 #ifdef __cplusplus
 }
 #endif

@@ -28,9 +28,17 @@ KLT_FMT_NVFP4_W4A4 = 3
 KLT_FLAG_NO_PDL = 1
 KLT_FLAG_PHASED = 2
 KLT_FLAG_DETERMINISTIC = 4
+KLT_DT_BF16 = 0
+KLT_DT_F32 = 1
+KLT_DT_E4M3 = 2
+KLT_ACT_NONE = 0
+KLT_ACT_SWIGLU = 1
+KLT_BLOCK_NORM_MAX_H = 16384
 
 EXPORTS = ("klt_create", "klt_forward", "klt_forward_hidden", "klt_status", "klt_destroy",
-           "klt_strerror", "klt_launch_count", "klt_gemm_tile", "klt_route_noalloc")
+           "klt_strerror", "klt_launch_count", "klt_gemm_tile", "klt_route_noalloc",
+           "klt_quantize", "klt_block_norm", "klt_linear_create", "klt_linear_forward",
+           "klt_linear_tile", "klt_linear_status", "klt_linear_destroy")
 
 
 class KltDims(ctypes.Structure):
@@ -59,6 +67,27 @@ class KltDebug(ctypes.Structure):
                 ("trace", ctypes.c_void_p), ("trace_entries", ctypes.c_int32),
                 ("force_bn", ctypes.c_int32), ("z", ctypes.c_void_p),
                 ("logits", ctypes.c_void_p), ("zsx", ctypes.c_void_p)]
+
+
+class KltBlockNormArgs(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int32), ("H", ctypes.c_int32), ("h_dtype", ctypes.c_int32),
+                ("y_dtype", ctypes.c_int32), ("gate_dtype", ctypes.c_int32),
+                ("gate_sigmoid", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("res_scale", ctypes.c_float), ("branch_scale", ctypes.c_float)] + [
+        (n, ctypes.c_void_p) for n in ("h", "y", "gate", "gamma_post", "gamma_pre", "h_out",
+                                       "n", "q", "s")] + [
+        (n, ctypes.c_int64) for n in ("ld_h", "ld_y", "gate_row", "gate_col", "ld_h_out",
+                                      "ld_n", "ld_q")]
+
+
+class KltLinearDims(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int32), ("K", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32)]
+
+
+class KltLinearDebug(ctypes.Structure):
+    _fields_ = [("stall_after_kblocks", ctypes.c_int32), ("timeout_ms", ctypes.c_int32),
+                ("force_tile", ctypes.c_int32), ("force_split", ctypes.c_int32)]
 
 
 _LIB: Optional[ctypes.CDLL] = None
@@ -104,6 +133,23 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.klt_route_noalloc.argtypes = [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32,
                                       ctypes.c_int32] + [ctypes.c_void_p] * 8
     lib.klt_route_noalloc.restype = ctypes.c_int
+    vp, i32, i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+    lib.klt_quantize.argtypes = [vp, i32, i64, i32, i32, vp, i64, vp, vp]
+    lib.klt_quantize.restype = ctypes.c_int
+    lib.klt_block_norm.argtypes = [ctypes.POINTER(KltBlockNormArgs), vp]
+    lib.klt_block_norm.restype = ctypes.c_int
+    lib.klt_linear_create.argtypes = [ctypes.POINTER(KltLinearDims), vp, vp,
+                                      ctypes.POINTER(vp)]
+    lib.klt_linear_create.restype = ctypes.c_int
+    lib.klt_linear_forward.argtypes = [vp, vp, i64, vp, i32, vp, i64, vp,
+                                       ctypes.POINTER(KltLinearDebug), vp]
+    lib.klt_linear_forward.restype = ctypes.c_int
+    lib.klt_linear_tile.argtypes = [vp, i32]
+    lib.klt_linear_tile.restype = ctypes.c_int
+    lib.klt_linear_status.argtypes = [vp]
+    lib.klt_linear_status.restype = ctypes.c_int
+    lib.klt_linear_destroy.argtypes = [vp]
+    lib.klt_linear_destroy.restype = ctypes.c_int
     _LIB = lib
     return lib
 
@@ -243,6 +289,261 @@ class LatentMoETail:
     def close(self):
         if self.handle is not None and self.handle.value:
             klt_destroy(self.handle)
+        self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+# ---------------------------------------------------------------- operators around the tail
+
+def _matrix(t, name: str, dtypes, rows: int, cols: int, device: int) -> int:
+    """Check one [rows, cols] operand (its columns contiguous); returns its row stride."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype}, not one of {dtypes}")
+    if tuple(t.shape) != (rows, cols):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, not {(rows, cols)}")
+    if t.get_device() != device:
+        raise ValueError(f"{name}: on {t.device}, not on CUDA device {device}")
+    ld, unit = t.stride()
+    if unit != 1 and cols > 1:
+        raise ValueError(f"{name}: columns are not contiguous")
+    return ld
+
+
+def _contiguous(t, name: str, dtypes, rows: int, cols: int, device: int):
+    if _matrix(t, name, dtypes, rows, cols, device) != cols and rows > 1:
+        raise ValueError(f"{name}: not contiguous")
+
+
+def _device_of(t, name: str) -> int:
+    if not t.is_cuda:
+        raise ValueError(f"{name}: not a CUDA tensor")
+    return t.get_device()
+
+
+def _on_device(device: int, stream, call):
+    """call(stream) with `device` current; stream None = the current stream of `device`."""
+    import torch
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(device)
+    if torch._C._cuda_getDevice() == device:
+        return call(stream)
+    with torch.cuda.device(device):
+        return call(stream)
+
+
+def fp8_codes(M: int, K: int, device):
+    """An uninitialised e4m3 tensor [M, K] whose rows start on 16 bytes, as the linear layer
+    reads and the quantiser and the norms may write it."""
+    import torch
+    wide = torch.empty((M, -(-K // 16) * 16), dtype=torch.float8_e4m3fn, device=device)
+    return wide[:, :K]
+
+
+_TORCH: Dict = {}
+
+
+def _dtypes() -> Dict:
+    if not _TORCH:
+        import torch
+        _TORCH.update(act=(torch.bfloat16, torch.float32), bf16=(torch.bfloat16,),
+                      f32=(torch.float32,), codes=(torch.float8_e4m3fn, torch.uint8),
+                      code=torch.float8_e4m3fn,
+                      of={torch.bfloat16: KLT_DT_BF16, torch.float32: KLT_DT_F32})
+    return _TORCH
+
+
+def quantize_fp8(x, q=None, s=None, stream: Optional[int] = None):
+    """e4m3 codes q [M, K] and fp32 scales s [M, ceil(K/128)] of x [M, K] (bf16 or fp32; rows
+    may be strided) per row and 128 columns (klt_quantize)."""
+    import torch
+    dt = _dtypes()
+    dev = _device_of(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x: not a matrix")
+    M, K = x.shape
+    ld = _matrix(x, "x", dt["act"], M, K, dev)
+    if q is None:
+        q = fp8_codes(M, K, x.device)
+    if s is None:
+        s = torch.empty((M, -(-K // 128)), dtype=torch.float32, device=x.device)
+    ld_q = _matrix(q, "q", dt["codes"], M, K, dev)
+    _contiguous(s, "s", dt["f32"], M, -(-K // 128), dev)
+    lib = _LIB or load_library()
+    rc = _on_device(dev, stream, lambda st: lib.klt_quantize(
+        x.data_ptr(), dt["of"][x.dtype], ld, M, K, q.data_ptr(), ld_q, s.data_ptr(), st))
+    if rc != KLT_OK:
+        raise KltError(rc, "klt_quantize")
+    return q, s
+
+
+class BlockNorm:
+    """The norms before and after a block with its gate and residual scale (klt_block_norm).
+
+    gamma_post, gamma_pre: bf16 [H] or None (that norm is left out).  The object keeps the
+    weights and scales; it has no other state."""
+
+    def __init__(self, H: int, gamma_post=None, gamma_pre=None, eps: float = 1e-6,
+                 res_scale: float = 1.0, branch_scale: float = 1.0,
+                 gate_sigmoid: bool = False):
+        dt = _dtypes()
+        self.H = H
+        self.gamma_post, self.gamma_pre = gamma_post, gamma_pre
+        self.device = None
+        for name, g in (("gamma_post", gamma_post), ("gamma_pre", gamma_pre)):
+            if g is None:
+                continue
+            dev = _device_of(g, name)
+            if g.dtype not in dt["bf16"] or tuple(g.shape) != (H,) or not g.is_contiguous():
+                raise ValueError(f"{name}: not a contiguous bf16 vector of {H}")
+            if self.device is not None and dev != self.device:
+                raise ValueError("gamma_post and gamma_pre are on different devices")
+            self.device = dev
+        self._args = KltBlockNormArgs(H=H, gate_sigmoid=int(gate_sigmoid), eps=eps,
+                                      res_scale=res_scale, branch_scale=branch_scale,
+                                      gamma_post=_ptr(gamma_post), gamma_pre=_ptr(gamma_pre))
+        self._lib = load_library()
+
+    def forward(self, h, y=None, gate=None, *, h_out=None, n=None, q=None, s=None,
+                stream: Optional[int] = None):
+        """h [M, H] bf16/fp32 residual stream, y [M, H] bf16/fp32 block output or None, gate
+        broadcastable to [M, H] or None.  Writes the outputs that are given: h_out (h's
+        dtype; may be h), n (bf16; may be y), q and s (e4m3 codes and fp32 scales of n);
+        when none is given, h_out (with y) and n are allocated.  Without y the norm after
+        the block is skipped.  Returns (h_out, n, q, s)."""
+        import torch
+        dt = _dtypes()
+        of = dt["of"]
+        dev = _device_of(h, "h")
+        if self.device is not None and dev != self.device:
+            raise ValueError("h: not on the weights' device")
+        M, H = h.shape[0], self.H
+        a = KltBlockNormArgs.from_buffer_copy(self._args)
+        a.M = M
+        a.ld_h = _matrix(h, "h", dt["act"], M, H, dev)
+        a.h_dtype = of[h.dtype]
+        a.h = h.data_ptr()
+        if h_out is None and n is None and q is None and s is None:
+            if y is not None:
+                h_out = torch.empty((M, H), dtype=h.dtype, device=h.device)
+            n = torch.empty((M, H), dtype=torch.bfloat16, device=h.device)
+        if y is not None:
+            a.ld_y = _matrix(y, "y", dt["act"], M, H, dev)
+            a.y_dtype = of[y.dtype]
+            a.y = y.data_ptr()
+            if gate is not None:
+                if gate.dtype not in dt["act"] or gate.get_device() != dev:
+                    raise ValueError("gate: not a bf16 or fp32 tensor on h's device")
+                g = gate.expand(M, H)
+                a.gate_row, a.gate_col = g.stride()
+                a.gate_dtype = of[gate.dtype]
+                a.gate = gate.data_ptr()
+        else:
+            if gate is not None:
+                raise ValueError("gate: given without y")
+            a.gamma_post = None
+        if h_out is not None:
+            a.ld_h_out = _matrix(h_out, "h_out", (h.dtype,), M, H, dev)
+            a.h_out = h_out.data_ptr()
+        if n is not None:
+            a.ld_n = _matrix(n, "n", dt["bf16"], M, H, dev)
+            a.n = n.data_ptr()
+        if q is not None:
+            a.ld_q = _matrix(q, "q", dt["codes"], M, H, dev)
+            a.q = q.data_ptr()
+        if s is not None:
+            _contiguous(s, "s", dt["f32"], M, -(-H // 128), dev)
+            a.s = s.data_ptr()
+        lib = self._lib
+        rc = _on_device(dev, stream, lambda st: lib.klt_block_norm(a, st))
+        if rc != KLT_OK:
+            raise KltError(rc, "klt_block_norm")
+        return h_out, n, q, s
+
+    __call__ = forward
+
+
+class Fp8Linear:
+    """y = x W^T with e4m3 weights and a scale per 128 x 128 block (klt_linear_*); owns a
+    handle with its own copy of the weights, on the weights' device.
+
+    w_q: e4m3 (or uint8 codes) [N, K]; w_s: fp32 [ceil(N/128), ceil(K/128)].  act "none" or
+    "swiglu" (gate rows first; N/2 outputs); out "bf16", "f32" or, for SwiGLU, "fp8"."""
+
+    def __init__(self, w_q, w_s, act: str = "none", out: str = "bf16"):
+        import torch
+        dt = _dtypes()
+        self.handle = None
+        acts = {"none": KLT_ACT_NONE, "swiglu": KLT_ACT_SWIGLU}
+        outs = {"bf16": KLT_DT_BF16, "f32": KLT_DT_F32, "fp8": KLT_DT_E4M3}
+        if act not in acts or out not in outs:
+            raise ValueError(f"act {act!r}, out {out!r}: not known")
+        self.device = _device_of(w_q, "w_q")
+        if w_q.dim() != 2:
+            raise ValueError("w_q: not a matrix")
+        self.N, self.K = w_q.shape
+        _contiguous(w_q, "w_q", dt["codes"], self.N, self.K, self.device)
+        _contiguous(w_s, "w_s", dt["f32"], -(-self.N // 128), -(-self.K // 128), self.device)
+        self.width = self.N // 2 if act == "swiglu" else self.N
+        self.fp8 = out == "fp8"
+        self._out = dt["codes"] if self.fp8 else dt["f32"] if out == "f32" else dt["bf16"]
+        self._lib = load_library()
+        d = KltLinearDims(self.N, self.K, acts[act], outs[out])
+        h = ctypes.c_void_p()
+        # the create copies on the legacy default stream; what wrote the weights may have run
+        # on another
+        torch.cuda.current_stream(self.device).synchronize()
+        with torch.cuda.device(self.device):
+            rc = self._lib.klt_linear_create(ctypes.byref(d), w_q.data_ptr(), w_s.data_ptr(),
+                                             ctypes.byref(h))
+        if rc != KLT_OK:
+            raise KltError(rc, "klt_linear_create")
+        self.handle = h
+
+    def forward(self, xq, xs, out=None, out_s=None, stream: Optional[int] = None,
+                debug: Optional[KltLinearDebug] = None):
+        """xq e4m3 (or uint8) [M, K] whose rows start on 16 bytes, xs fp32 [M, ceil(K/128)].
+        Returns out [M, N] (SwiGLU: [M, N/2]), or (codes, scales) with out "fp8"."""
+        import torch
+        dt = _dtypes()
+        dev = self.device
+        M, K, width = xq.shape[0], self.K, self.width
+        ld = _matrix(xq, "xq", dt["codes"], M, K, dev)
+        if M <= 1:  # the stride of a single row says nothing
+            ld = -(-K // 16) * 16
+        _contiguous(xs, "xs", dt["f32"], M, -(-K // 128), dev)
+        if out is None:
+            out = fp8_codes(M, width, xq.device) if self.fp8 else \
+                torch.empty((M, width), dtype=self._out[0], device=xq.device)
+        ld_out = _matrix(out, "out", self._out, M, width, dev)
+        if self.fp8:
+            if out_s is None:
+                out_s = torch.empty((M, width // 128), dtype=torch.float32, device=xq.device)
+            _contiguous(out_s, "out_s", dt["f32"], M, width // 128, dev)
+        lib = self._lib
+        rc = _on_device(dev, stream, lambda st: lib.klt_linear_forward(
+            self.handle, xq.data_ptr(), ld, xs.data_ptr(), M, out.data_ptr(), ld_out,
+            out_s.data_ptr() if self.fp8 else None, debug, st))
+        if rc != KLT_OK:
+            raise KltError(rc, "klt_linear_forward")
+        return (out, out_s) if self.fp8 else out
+
+    __call__ = forward
+
+    def tile(self, M: int) -> int:
+        """Token tile plus 1000 times the K split that a call with M tokens uses."""
+        return self._lib.klt_linear_tile(self.handle, M)
+
+    def status(self) -> int:
+        return self._lib.klt_linear_status(self.handle)
+
+    def close(self):
+        if self.handle is not None and self.handle.value:
+            self._lib.klt_linear_destroy(self.handle)
         self.handle = None
 
     def __del__(self):

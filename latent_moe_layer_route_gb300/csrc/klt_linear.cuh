@@ -1,0 +1,143 @@
+// Shared parts of the FP8 linear layer's two kernels: the parameters, and the cluster and
+// CTA-pair forms of barriers, copies and tensor-core instructions.  Inline PTX only.
+#pragma once
+
+#include "klt_device.cuh"
+
+namespace klt {
+
+// The weights are kept tile-major: row block rb (128 rows) and k-block kb (128 columns) is
+// one contiguous 16 KB image in the 128-byte swizzle, at ((rb * KB + kb) * 16384); rows and
+// columns past N and K are zero codes.
+constexpr int LIN_TILE = 128;
+constexpr int LIN_TILE_BYTES = LIN_TILE * LIN_TILE;
+
+struct LinParams {
+  const uint8_t* w;   // tile-major image
+  const float* ws;    // [NB, KB]
+  const float* xs;    // [M, KB]
+  void* out;          // bf16 / fp32 / e4m3
+  float* out_s;       // e4m3 outputs: [M, width / 128]
+  int64_t ld_out;     // elements
+  int M, KB, NB;      // tokens, k-blocks, row blocks of W
+  int width;          // output columns (N; N / 2 for SwiGLU)
+  int up;             // SwiGLU: row block of the up tile minus that of the gate tile
+  int out_dtype;      // enum klt_dtype
+  bool out_wide;      // output rows start on 16 bytes
+  int stall;          // test hook: producers stop after this many k-blocks (0 = never)
+  int* err;
+  long long timeout;  // SM cycles
+};
+
+// ------------------------------------------------------------------ clusters
+KLT_DEV uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+KLT_DEV void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+KLT_DEV void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+// Address of this CTA's shared-memory address `saddr` in CTA `rank` of the cluster.
+KLT_DEV uint32_t map_to_rank(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+KLT_DEV float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+// Arrive on a barrier of any CTA of the cluster (`addr` from map_to_rank).
+KLT_DEV void mbar_arrive_cluster(uint32_t addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr)
+               : "memory");
+}
+
+// ------------------------------------------------------------------ CTA pairs
+// 2-D tiled load into this CTA's shared memory, completing on a barrier of either CTA of the
+// pair (`bar` from map_to_rank).
+KLT_DEV void tma_load_2d_pair(void* dst, const CUtensorMap* map, uint32_t bar, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".cta_group::2 [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+      : "memory");
+}
+KLT_DEV void tmem_alloc_pair(uint32_t* dst_smem, uint32_t ncols) {  // a warp of both CTAs
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                   smem_u32(dst_smem)),
+               "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+KLT_DEV void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {  // a warp of both CTAs
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr),
+               "r"(ncols)
+               : "memory");
+}
+// Arrive once on the barrier at the same offset in both CTAs of the pair when every MMA
+// issued so far by this thread has completed.
+KLT_DEV void tc_commit_pair(uint64_t* bar) {
+  const uint16_t both = 3;
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%0], %1;" ::"r"(smem_u32(bar)),
+      "h"(both)
+      : "memory");
+}
+// The four MMAs of one 128-byte K block over both CTAs' tiles (M = 256: 128 rows in each
+// CTA; N = 256: 128 rows of B in each CTA), replacing the accumulator.
+KLT_DEV void mma4_fp8_pair(uint32_t d, uint64_t da, uint64_t db, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, 0, 0;\n\tsetp.eq.b32 q, 0, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %4, %5, %3, q;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %6, %7, %3, q;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %8, %9, %3, q;\n\t}" ::"r"(d),
+      "l"(da), "l"(db), "r"(idesc), "l"(da + 2), "l"(db + 2), "l"(da + 4), "l"(db + 4),
+      "l"(da + 6), "l"(db + 6)
+      : "memory");
+}
+
+// ------------------------------------------------------------------ arithmetic
+// Two fp32 fused multiply-adds in one instruction: a += p * s, each lane rounded as fmaf.
+KLT_DEV void fma2(unsigned long long& a, unsigned long long p, unsigned long long s) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(a) : "l"(p), "l"(s));
+}
+KLT_DEV unsigned long long pack2(float lo, float hi) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+KLT_DEV void unpack2(unsigned long long v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+
+// The scale of a quantised group from the bit pattern of its largest magnitude (a NaN is
+// above infinity, infinity above every number); a scale that is zero becomes 1.
+KLT_DEV float group_scale(uint32_t amax_bits) {
+  const float s = __uint_as_float(amax_bits) / 448.0f;
+  return s == 0.f ? 1.0f : s;
+}
+// Whether scale s and its reciprocal are normal with room to spare, so that quotients by it
+// come from quot_rn; by division otherwise (tiny, huge and non-finite scales).
+KLT_DEV bool quot_fast(float s) { return s > 1e-30f && s < 1e30f; }
+// fp32(x / s), correctly rounded, for s > 0 (the correction would turn -0 into 0).
+KLT_DEV float quot_group(float x, float s, float inv, bool fast) {
+  return fast ? copysignf(quot_rn(x, s, inv), x) : x / s;
+}
+
+// ------------------------------------------------------------------ launches
+cudaError_t launch_linear_narrow(const CUtensorMap& tok, const LinParams& p, int bn, int split,
+                                 bool swiglu, cudaStream_t s);
+cudaError_t launch_linear_wide(const CUtensorMap& tok, const CUtensorMap& wmap,
+                               const LinParams& p, bool swiglu, int num_sms, cudaStream_t s);
+bool linear_wide_regs_ok();
+
+}  // namespace klt
