@@ -414,7 +414,8 @@ int klt_linear_create(const klt_linear_dims* d, const void* w, const float* w_sc
  * handle has no workspace: calls on several streams may overlap.  One launch.
  * Errors: KLT_ERR_INVALID_ARG (null handle or pointer, M < 0 or M > 2^22, a stride shorter
  * than a row, another device current than at creation, bad debug value), KLT_ERR_UNSUPPORTED
- * (debug: a tile and split that do not go together), KLT_ERR_ALIGN (xq or ld_xq not 16-byte,
+ * (M * ceil(K / 128) above 2^31 - 1; debug: a tile and split that do not go together),
+ * KLT_ERR_ALIGN (xq or ld_xq not 16-byte,
  * out not element aligned), KLT_ERR_CUDA.  Expired device waits: klt_linear_status. */
 int klt_linear_forward(klt_linear* h, const uint8_t* xq, int64_t ld_xq, const float* xs,
                        int32_t M, void* out, int64_t ld_out, float* out_s,

@@ -89,12 +89,12 @@ KLT_DEV uint2 quant8(const float* v, float& s_out) {
   for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
 #pragma unroll
   for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-  const float s = group_scale(m), inv = 1.0f / s;
-  const bool fast = quot_fast(s);
+  float s = group_scale(m);
   s_out = s;
+  const float k = rescale(s), inv = 1.0f / s;
   float t[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) t[i] = quot_group(v[i], s, inv, fast);
+  for (int i = 0; i < 8; ++i) t[i] = quot_group(v[i] * k, s, inv);
   return make_uint2(f32x2_to_e4m3x2(t[0], t[1]) | (f32x2_to_e4m3x2(t[2], t[3]) << 16),
                     f32x2_to_e4m3x2(t[4], t[5]) | (f32x2_to_e4m3x2(t[6], t[7]) << 16));
 }

@@ -17,7 +17,7 @@ struct klt_linear {
   int num_sms;
   int NB, KB;      // row blocks and k-blocks of W
   uint8_t* w;      // tile-major image [NB, KB, 16384]
-  float* ws;       // [NB, KB]
+  float* ws;       // [NB + 1, KB], the last row zero
   int* err;        // device error word
   CUtensorMap wmap;  // the image as [NB * KB * 128, 128] bytes
 };
@@ -41,19 +41,19 @@ EncodeTiledFn get_encode() {
   return fn;
 }
 
-// Rows of `cols` bytes `ld` bytes apart; box 128 bytes x box_rows; bytes outside read as 0.
+// Rows of `cols` bytes `ld` bytes apart; box of box_bytes x box_rows; bytes outside read as 0
+// and are not written.
 bool encode_bytes(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint64_t ld,
-                  uint32_t box_rows, bool swizzle) {
+                  uint32_t box_bytes, uint32_t box_rows, CUtensorMapSwizzle swizzle) {
   EncodeTiledFn enc = get_encode();
   if (!enc) return false;
   const cuuint64_t dims[2] = {cols, rows};
   const cuuint64_t strides[1] = {ld};
-  const cuuint32_t box[2] = {128, box_rows};
+  const cuuint32_t box[2] = {box_bytes, box_rows};
   const cuuint32_t estr[2] = {1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
              estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -153,7 +153,7 @@ int klt_linear_create(const klt_linear_dims* d, const void* w, const float* w_sc
   h->KB = (d->K + 127) / 128;
   const int64_t tiles = static_cast<int64_t>(h->NB) * h->KB;
   if (cudaMalloc(reinterpret_cast<void**>(&h->w), tiles * LIN_TILE_BYTES) != cudaSuccess ||
-      cudaMalloc(reinterpret_cast<void**>(&h->ws), tiles * 4) != cudaSuccess ||
+      cudaMalloc(reinterpret_cast<void**>(&h->ws), (tiles + h->KB) * 4) != cudaSuccess ||
       cudaMalloc(reinterpret_cast<void**>(&h->err), 4) != cudaSuccess) {
     cudaGetLastError();  // the failed allocation is reported here, not to the caller's next call
     free_all(h);
@@ -165,9 +165,10 @@ int klt_linear_create(const klt_linear_dims* d, const void* w, const float* w_sc
   relayout_kernel<<<blocks, 256>>>(static_cast<const uint8_t*>(w), h->w, d->N, d->K, h->KB,
                                    chunks);
   if (cudaGetLastError() != cudaSuccess ||
+      cudaMemsetAsync(h->ws + tiles, 0, h->KB * 4ll, 0) != cudaSuccess ||
       cudaMemcpyAsync(h->ws, w_scale, tiles * 4, cudaMemcpyDeviceToDevice, 0) != cudaSuccess ||
       cudaMemsetAsync(h->err, 0, 4, 0) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess ||
-      !encode_bytes(&h->wmap, h->w, tiles * 128, 128, 128, 128, false)) {
+      !encode_bytes(&h->wmap, h->w, tiles * 128, 128, 128, 128, 128, CU_TENSOR_MAP_SWIZZLE_NONE)) {
     free_all(h);
     return KLT_ERR_CUDA;
   }
@@ -190,6 +191,8 @@ int klt_linear_forward(klt_linear* h, const uint8_t* xq, int64_t ld_xq, const fl
   if (!aligned(xq, 16) || ld_xq % 16 || !aligned(xs, 4) || !aligned(out, es) ||
       (codes && !aligned(out_s, 4)))
     return KLT_ERR_ALIGN;
+  // 32-bit offsets of the scales: beyond, xq alone would be 256 GB
+  if (static_cast<int64_t>(M) * h->KB > 0x7FFFFFFF) return KLT_ERR_UNSUPPORTED;
   if (ld_xq < h->d.K || (M > 1 && ld_out < width)) return KLT_ERR_INVALID_ARG;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return KLT_ERR_CUDA;
@@ -230,11 +233,22 @@ int klt_linear_forward(klt_linear* h, const uint8_t* xq, int64_t ld_xq, const fl
   p.timeout = static_cast<long long>(dbg && dbg->timeout_ms > 0 ? dbg->timeout_ms : 1000) *
               2000000LL;
   CUtensorMap tok;
-  if (!encode_bytes(&tok, xq, M, h->d.K, ld_xq, tile == 256 ? 128 : tile, true))
+  if (!encode_bytes(&tok, xq, M, h->d.K, ld_xq, 128, tile == 256 ? 128 : tile,
+                    CU_TENSOR_MAP_SWIZZLE_128B))
     return KLT_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = tile == 256 ? launch_linear_wide(tok, h->wmap, p, act, h->num_sms, s)
-                                    : launch_linear_narrow(tok, p, tile, split, act, s);
+  cudaError_t e;
+  if (tile == 256) {
+    // 32 rows x 64 bytes are stored at a time, where the output's rows allow bulk copies
+    CUtensorMap omap = {};
+    if (p.out_wide &&
+        !encode_bytes(&omap, out, M, width * es, M > 1 ? ld_out * es : (width * es + 15) / 16 * 16,
+                      64, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+      return KLT_ERR_CUDA;
+    e = launch_linear_wide(tok, h->wmap, omap, p, act, h->num_sms, s);
+  } else {
+    e = launch_linear_narrow(tok, p, tile, split, act, s);
+  }
   return e == cudaSuccess ? KLT_OK : KLT_ERR_CUDA;
 }
 

@@ -14,7 +14,7 @@ constexpr int LIN_TILE_BYTES = LIN_TILE * LIN_TILE;
 
 struct LinParams {
   const uint8_t* w;   // tile-major image
-  const float* ws;    // [NB, KB]
+  const float* ws;    // [NB (rounded up to even), KB]
   const float* xs;    // [M, KB]
   void* out;          // bf16 / fp32 / e4m3
   float* out_s;       // e4m3 outputs: [M, width / 128]
@@ -23,6 +23,9 @@ struct LinParams {
   int width;          // output columns (N; N / 2 for SwiGLU)
   int up;             // SwiGLU: row block of the up tile minus that of the gate tile
   int out_dtype;      // enum klt_dtype
+  // token-major kernel: tiles of 256 tokens and of 256 rows of W, the step from one tile of a
+  // CTA pair to its next, and from the first weight tile's scales to the second's
+  int tiles_m, tiles_n, step_m, step_n, step_ws;
   bool out_wide;      // output rows start on 16 bytes
   int stall;          // test hook: producers stop after this many k-blocks (0 = never)
   int* err;
@@ -72,6 +75,26 @@ KLT_DEV void tma_load_2d_pair(void* dst, const CUtensorMap* map, uint32_t bar, i
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
       : "memory");
 }
+// Stores the shared-memory box at (c0 = inner element index, c1 = row) of a tensor; parts
+// outside of it are not written.  Completion is tracked per thread (bulk groups).
+KLT_DEV void tma_store_2d(const CUtensorMap* map, const void* src, int c0, int c1) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(smem_u32(src)), "r"(c0), "r"(c1)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// All but this thread's last N bulk stores have read their shared memory.
+template <int N>
+KLT_DEV void tma_store_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+// All of this thread's bulk stores are complete.
+KLT_DEV void tma_store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+// Orders this thread's shared-memory writes before later bulk copies that read them.
+KLT_DEV void fence_proxy_async_shared() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
 KLT_DEV void tmem_alloc_pair(uint32_t* dst_smem, uint32_t ncols) {  // a warp of both CTAs
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                    smem_u32(dst_smem)),
@@ -94,8 +117,8 @@ KLT_DEV void tc_commit_pair(uint64_t* bar) {
       "h"(both)
       : "memory");
 }
-// The four MMAs of one 128-byte K block over both CTAs' tiles (M = 256: 128 rows in each
-// CTA; N = 256: 128 rows of B in each CTA), replacing the accumulator.
+// The four MMAs of one 128-byte K block over both CTAs' tiles (M = 256: 128 rows of A in each
+// CTA; half of B's rows in each CTA), replacing the accumulator.
 KLT_DEV void mma4_fp8_pair(uint32_t d, uint64_t da, uint64_t db, uint32_t idesc) {
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, 0, 0;\n\tsetp.eq.b32 q, 0, 0;\n\t"
@@ -122,25 +145,40 @@ KLT_DEV void unpack2(unsigned long long v, float& lo, float& hi) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
 }
 
+// SiLU g / (1 + e^-g) with the fast exponential and reciprocal (each within 2 ulp); the
+// exponent is clamped so that the divisor stays finite (below -80 the result is under 1e-32).
+KLT_DEV float silu_rcp(float g) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + __expf(-fmaxf(g, -80.0f))));
+  return g * r;
+}
+
 // The scale of a quantised group from the bit pattern of its largest magnitude (a NaN is
 // above infinity, infinity above every number); a scale that is zero becomes 1.
 KLT_DEV float group_scale(uint32_t amax_bits) {
   const float s = __uint_as_float(amax_bits) / 448.0f;
   return s == 0.f ? 1.0f : s;
 }
-// Whether scale s and its reciprocal are normal with room to spare, so that quotients by it
-// come from quot_rn; by division otherwise (tiny, huge and non-finite scales).
-KLT_DEV bool quot_fast(float s) { return s > 1e-30f && s < 1e30f; }
-// fp32(x / s), correctly rounded, for s > 0 (the correction would turn -0 into 0).
-KLT_DEV float quot_group(float x, float s, float inv, bool fast) {
-  return fast ? copysignf(quot_rn(x, s, inv), x) : x / s;
+// quot_rn needs the scale, its reciprocal and the residual in the normal range.  Brings a scale
+// far from 1 there by a power of two, which it returns: the group's values times that power
+// (exact as far as a code can tell) divided by the new scale have the same quotients.  A scale
+// that is not finite stays so and turns every code of its group into NaN.
+KLT_DEV float rescale(float& s) {
+  float k = 1.0f;
+  if (s < 1e-30f) k = 0x1p100f;
+  if (s > 1e30f) k = 0x1p-60f;
+  s *= k;
+  return k;
 }
+// fp32(x / s), correctly rounded, for s > 0 (the correction would turn -0 into 0).
+KLT_DEV float quot_group(float x, float s, float inv) { return copysignf(quot_rn(x, s, inv), x); }
 
 // ------------------------------------------------------------------ launches
 cudaError_t launch_linear_narrow(const CUtensorMap& tok, const LinParams& p, int bn, int split,
                                  bool swiglu, cudaStream_t s);
 cudaError_t launch_linear_wide(const CUtensorMap& tok, const CUtensorMap& wmap,
-                               const LinParams& p, bool swiglu, int num_sms, cudaStream_t s);
+                               const CUtensorMap& omap, const LinParams& p, bool swiglu,
+                               int num_sms, cudaStream_t s);
 bool linear_wide_regs_ok();
 
 }  // namespace klt

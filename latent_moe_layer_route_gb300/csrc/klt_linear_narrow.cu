@@ -274,13 +274,11 @@ __global__ void __launch_bounds__(THREADS)
           const uint32_t b1 = __float_as_uint(v.y) & 0x7FFFFFFFu;
           const uint32_t b2 = __float_as_uint(v.z) & 0x7FFFFFFFu;
           const uint32_t b3 = __float_as_uint(v.w) & 0x7FFFFFFFu;
-          const float s = group_scale(__reduce_max_sync(0xFFFFFFFFu, max(max(b0, b1), max(b2, b3))));
-          const float inv = 1.0f / s;
-          const bool fast = quot_fast(s);
-          const float q0 = quot_group(v.x, s, inv, fast);
-          const float q1 = quot_group(v.y, s, inv, fast);
-          const float q2 = quot_group(v.z, s, inv, fast);
-          const float q3 = quot_group(v.w, s, inv, fast);
+          float s = group_scale(__reduce_max_sync(0xFFFFFFFFu, max(max(b0, b1), max(b2, b3))));
+          if (lane == 0) p.out_s[m * (p.width / 128) + rb] = s;
+          const float k = rescale(s), inv = 1.0f / s;
+          const float q0 = quot_group(v.x * k, s, inv), q1 = quot_group(v.y * k, s, inv);
+          const float q2 = quot_group(v.z * k, s, inv), q3 = quot_group(v.w * k, s, inv);
           const uint32_t codes = f32x2_to_e4m3x2(q0, q1) | (f32x2_to_e4m3x2(q2, q3) << 16);
           uint8_t* o = static_cast<uint8_t*>(p.out) + m * p.ld_out + c;
           if (p.out_wide) {
@@ -289,7 +287,6 @@ __global__ void __launch_bounds__(THREADS)
 #pragma unroll
             for (int j = 0; j < 4; ++j) o[j] = static_cast<uint8_t>(codes >> (8 * j));
           }
-          if (lane == 0) p.out_s[m * (p.width / 128) + rb] = s;
         } else {
           store4(p, m, c, v);
         }

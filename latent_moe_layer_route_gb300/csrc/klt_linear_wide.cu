@@ -20,26 +20,31 @@ namespace klt {
 namespace {
 
 constexpr int THREADS = 384;  // warps 0 copies, 1 MMA, 2 TMEM, 3 idle, 4-11 epilogue
-constexpr int STAGES = 6;
+constexpr int STAGES = 5;
 constexpr int STAGE_BYTES = 2 * LIN_TILE_BYTES;
 constexpr int RING_BYTES = STAGES * STAGE_BYTES;
-constexpr int SMEM = 1024 + RING_BYTES + 1024 + 256;
+constexpr int BOX_BYTES = 32 * 64;         // stored at a time by a warp: 32 rows x 64 bytes
+constexpr int BOXES = 4;                   // per epilogue warp
+constexpr int OUT_BYTES = 8 * BOXES * BOX_BYTES;
+constexpr int AMAX_BYTES = 2 * 128 * 4;
+constexpr int SMEM = 1024 + RING_BYTES + OUT_BYTES + AMAX_BYTES + 256;
+static_assert(SMEM <= 232448, "shared memory of a block");
 
 struct Smem {
-  uint8_t* ring;
-  float* amax;  // [2][128]
-  uint64_t *full, *empty, *tfull, *tempty, *drain;
+  uint8_t *ring, *stage;
+  uint32_t* amax;  // [2][128]
+  uint64_t *full, *done, *tempty, *drain;
   uint32_t* tmem_holder;
   volatile int* abort_flag;
 };
 
-// 32 consecutive fp32 columns of this thread's TMEM lane, waited for.
-KLT_DEV void tmem_ld32(uint32_t taddr, uint32_t* r) {
+// Starts the load of 32 consecutive fp32 columns of this thread's TMEM lane; the registers
+// hold them after tmem_wait_ld32 on the same array.
+KLT_DEV void tmem_start_ld32(uint32_t taddr, uint32_t* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
         "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
@@ -49,38 +54,86 @@ KLT_DEV void tmem_ld32(uint32_t taddr, uint32_t* r) {
       : "r"(taddr)
       : "memory");
 }
+// Waits for this thread's TMEM loads; the registers pass through, so that no use of them
+// moves above the wait.
+KLT_DEV void tmem_wait_ld32(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
 
-// Stores 64 consecutive outputs (columns c .. c + 63) of row m.
-KLT_DEV void store_row64(const LinParams& p, int64_t m, int c, const float* v) {
-  if (p.out_dtype == KLT_DT_F32) {
-    float* o = static_cast<float*>(p.out) + m * p.ld_out + c;
-    if (p.out_wide && c + 64 <= p.width) {
+// An output box of a warp: this thread's 64 bytes (w) of row m0 + lane, at byte `col` of the
+// output, staged in buffer `buf` in the output map's swizzle (no bank conflicts) and stored by
+// a bulk copy, which cuts off what lies outside the output and runs on while the warp goes on.
+// Lane 0 issues all of a warp's copies.
+KLT_DEV void store_box(uint8_t* buf, const CUtensorMap* omap, const uint32_t* w, int col, int m0) {
+  const int lane = lane_id(), x = (lane >> 1) & 3;
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        reinterpret_cast<float4*>(o)[i] =
-            make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-    } else {
+  for (int j = 0; j < 4; ++j)
+    *reinterpret_cast<uint4*>(buf + lane * 64 + (j ^ x) * 16) =
+        make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+  fence_proxy_async_shared();
+  __syncwarp();
+  if (lane == 0) tma_store_2d(omap, buf, col, m0);
+}
+// The warp's buffers are free: its bulk copies have read them.
+KLT_DEV void boxes_free() {
+  tma_store_wait_read<0>();
+  __syncwarp();
+}
+// A warp's 64 columns c .. c + 63 of its 32 rows from m0 on (this thread's row in v, two
+// values each), through the four buffers at `buf` (bf16: two of them, the first or the last).
+KLT_DEV void store_rows64(const LinParams& p, const CUtensorMap* omap, uint8_t* buf, int m0,
+                          int c, const unsigned long long* v, bool last) {
+  if (m0 >= p.M || c >= p.width) return;  // a bulk store starts inside the output
+  const bool f32 = p.out_dtype == KLT_DT_F32;
+  if (p.out_wide && f32) {
+    boxes_free();
 #pragma unroll
-      for (int i = 0; i < 64; ++i)
-        if (c + i < p.width) o[i] = v[i];
-    }
-  } else {
-    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + m * p.ld_out + c;
-    if (p.out_wide && c + 64 <= p.width) {
+    for (int h = 0; h < 4; ++h) {
+      uint32_t w[16];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const __nv_bfloat162 b = __floats2bfloat162_rn(v[8 * i + 2 * j], v[8 * i + 2 * j + 1]);
-          w[j] = *reinterpret_cast<const uint32_t*>(&b);
-        }
-        reinterpret_cast<uint4*>(o)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        w[2 * i] = static_cast<uint32_t>(v[h * 8 + i]);
+        w[2 * i + 1] = static_cast<uint32_t>(v[h * 8 + i] >> 32);
       }
-    } else {
+      if (c + h * 16 < p.width) store_box(buf + h * BOX_BYTES, omap, w, (c + h * 16) * 4, m0);
+    }
+  } else if (p.out_wide) {
+    if (!last) boxes_free();
 #pragma unroll
-      for (int i = 0; i < 64; ++i)
-        if (c + i < p.width) o[i] = __float2bfloat16(v[i]);
+    for (int h = 0; h < 2; ++h) {
+      uint32_t w[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        float lo, hi;
+        unpack2(v[h * 16 + i], lo, hi);
+        const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
+        w[i] = *reinterpret_cast<const uint32_t*>(&t);
+      }
+      if (c + h * 32 < p.width)
+        store_box(buf + (last * 2 + h) * BOX_BYTES, omap, w, (c + h * 32) * 2, m0);
+    }
+  } else if (m0 + lane_id() < p.M) {
+    const int es = f32 ? 4 : 2;
+    char* o = static_cast<char*>(p.out) + ((m0 + lane_id()) * p.ld_out + c) * es;
+#pragma unroll
+    for (int i = 0; i < 64; ++i, o += es) {
+      float lo, hi;
+      unpack2(v[i / 2], lo, hi);
+      const float x = i % 2 ? hi : lo;
+      if (c + i < p.width) {
+        if (f32)
+          *reinterpret_cast<float*>(o) = x;
+        else
+          *reinterpret_cast<__nv_bfloat16*>(o) = __float2bfloat16(x);
+      }
     }
   }
 }
@@ -89,33 +142,39 @@ KLT_DEV void store_row64(const LinParams& p, int64_t m, int c, const float* v) {
 template <int ACT>
 __global__ void __launch_bounds__(THREADS, 1)
     wide_kernel(const __grid_constant__ CUtensorMap tok, const __grid_constant__ CUtensorMap wmap,
-                const LinParams p, int tiles_m, int tiles) {
+                const __grid_constant__ CUtensorMap omap, const LinParams p) {
   extern __shared__ uint8_t smem_raw[];
   Smem sm;
   sm.ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  sm.amax = reinterpret_cast<float*>(sm.ring + RING_BYTES);
-  sm.full = reinterpret_cast<uint64_t*>(sm.ring + RING_BYTES + 1024);
-  sm.empty = sm.full + STAGES;
-  sm.tfull = sm.empty + STAGES;
-  sm.tempty = sm.tfull + 2;
+  sm.stage = sm.ring + RING_BYTES;
+  sm.amax = reinterpret_cast<uint32_t*>(sm.stage + OUT_BYTES);
+  sm.full = reinterpret_cast<uint64_t*>(sm.stage + OUT_BYTES + AMAX_BYTES);
+  sm.done = sm.full + STAGES;
+  sm.tempty = sm.done + STAGES;
   sm.drain = sm.tempty + 2;
   sm.tmem_holder = reinterpret_cast<uint32_t*>(sm.drain + 1);
   sm.abort_flag = reinterpret_cast<volatile int*>(sm.tmem_holder + 1);
-  static_assert((2 * STAGES + 5) * 8 + 8 <= 256, "barrier space");
+  static_assert((2 * STAGES + 3) * 8 + 8 <= 256, "barrier space");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
-  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  // this pair's tiles: the first one, then steps of the number of pairs
+  const int pair = blockIdx.x >> 1;
+  int tm = pair % p.tiles_m, tn = pair / p.tiles_m;
+  auto next_tile = [&]() {
+    tm += p.step_m;
+    tn += p.step_n;
+    if (tm >= p.tiles_m) tm -= p.tiles_m, ++tn;
+  };
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES; ++i) {
       mbar_init(&sm.full[i], 1);   // first CTA's: bytes of both CTAs
-      mbar_init(&sm.empty[i], 1);  // each CTA's: the MMAs that read the stage are done
+      mbar_init(&sm.done[i], 1);   // each CTA's: the MMAs that read the stage are done, so
+                                   // the stage is free and the slot full
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm.tfull[i], 1);
+    for (int i = 0; i < 2; ++i)
       mbar_init(&sm.tempty[i], 16);  // first CTA's: the epilogue warps of both CTAs
-    }
     mbar_init(sm.drain, 1);
     *sm.abort_flag = 0;
     fence_barrier_init();
@@ -130,14 +189,13 @@ __global__ void __launch_bounds__(THREADS, 1)
   pdl_trigger();
 
   if (warp < 4) {
-    regs_dec<72>();
+    regs_dec<56>();
     if (warp == 0 && lane == 0) {
       pdl_wait();
       const uint32_t full0 = map_to_rank(smem_u32(sm.full), 0);
       int it = 0;
       bool ok = true;
-      for (int tile = pair; tile < tiles && ok; tile += pairs) {
-        const int tm = tile % tiles_m, tn = tile / tiles_m;
+      for (; tn < p.tiles_n && ok; next_tile()) {
         const int row0 = tm * 256 + static_cast<int>(rank) * 128;
         const int rb = ACT ? tn + static_cast<int>(rank) * p.up : tn * 2 + static_cast<int>(rank);
         for (int kb = 0; kb < p.KB; ++kb, ++it) {
@@ -146,7 +204,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             break;
           }
           const int st = it % STAGES;
-          if (!mbar_wait_spin(&sm.empty[st], ((it / STAGES) & 1) ^ 1, sm.abort_flag, p.err,
+          if (!mbar_wait_spin(&sm.done[st], ((it / STAGES) & 1) ^ 1, sm.abort_flag, p.err,
                               p.timeout)) {
             ok = false;
             break;
@@ -168,139 +226,154 @@ __global__ void __launch_bounds__(THREADS, 1)
       constexpr uint32_t idesc = idesc_make(0, 256, 256);
       int it = 0;
       bool ok = true;
-      for (int tile = pair; tile < tiles && ok; tile += pairs) {
+      for (; tn < p.tiles_n && ok; next_tile())
         for (int kb = 0; kb < p.KB; ++kb, ++it) {
           const int st = it % STAGES, slot = it & 1;
-          if (!mbar_wait_spin(&sm.tempty[slot], ((it >> 1) & 1) ^ 1, sm.abort_flag, p.err,
-                              p.timeout) ||
-              !mbar_wait_spin(&sm.full[st], (it / STAGES) & 1, sm.abort_flag, p.err,
-                              p.timeout)) {
-            ok = false;
-            break;
-          }
+          ok = mbar_wait_spin(&sm.full[st], (it / STAGES) & 1, sm.abort_flag, p.err, p.timeout) &&
+               mbar_wait_spin(&sm.tempty[slot], ((it >> 1) & 1) ^ 1, sm.abort_flag, p.err,
+                              p.timeout);
+          if (!ok) break;
           tc_fence_after();
           const uint32_t base = smem_u32(sm.ring + st * STAGE_BYTES);
           mma4_fp8_pair(tmem + slot * 256, sdesc_sw128(base), sdesc_sw128(base + LIN_TILE_BYTES),
                         idesc);
-          tc_commit_pair(&sm.empty[st]);
-          tc_commit_pair(&sm.tfull[slot]);
+          tc_commit_pair(&sm.done[st]);
         }
-      }
       tc_commit_pair(sm.drain);  // no MMA of the pair runs past this point
       int none = 0;
       mbar_wait(sm.drain, 0, &none, p.err, p.timeout);
     }
     __syncwarp();
   } else {
-    regs_inc<216>();
+    regs_inc<224>();
     pdl_wait();
     const int quad = warp & 3, half = (warp - 4) >> 2;
     const int row = quad * 32 + lane;
+    uint8_t* boxes = sm.stage + (warp - 4) * BOXES * BOX_BYTES;
     const uint32_t tempty0 = map_to_rank(smem_u32(sm.tempty), 0);
-    // this thread's columns of a slot: 128 neighbouring ones, or 64 gate and the 64 matching
-    // up columns
+    // this thread's columns of a slot: 64 of the first CTA's weight rows (SwiGLU: gate), 64 of
+    // the second's (the matching up rows)
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    const int c0 = ACT ? half * 64 : half * 128;
-    const int c1 = ACT ? 128 + half * 64 : half * 128 + 64;
+    const int c0 = half * 64, c1 = 128 + half * 64;
     int it = 0;
     bool ok = true;  // of the whole warp; a warp that gave up still meets the others' barriers
-    for (int tile = pair; tile < tiles; tile += pairs) {
-      const int tm = tile % tiles_m, tn = tile / tiles_m;
-      const int64_t m = static_cast<int64_t>(tm) * 256 + rank * 128 + row;
-      const float* xs = p.xs + (m < p.M ? m : 0) * p.KB;
-      const int rb0 = ACT ? tn : tn * 2 + half, rb1 = ACT ? tn + p.up : rb0;
-      const float* ws0 = p.ws + static_cast<int64_t>(rb0 < p.NB ? rb0 : 0) * p.KB;
-      const float* ws1 = p.ws + static_cast<int64_t>(rb1 < p.NB ? rb1 : 0) * p.KB;
+    // the scales of this thread's row and of the two weight tiles, loaded one k-block (at the
+    // end of a tile: one tile) ahead
+    int xo, wo;
+    float x, w0, w1;
+    auto first_scales = [&]() {
+      const int m = tm * 256 + static_cast<int>(rank) * 128 + row;
+      xo = (m < p.M ? m : 0) * p.KB;
+      wo = (ACT ? tn : tn * 2) * p.KB;
+      x = p.xs[xo];
+      w0 = p.ws[wo];
+      w1 = p.ws[wo + p.step_ws];
+    };
+    first_scales();
+    while (tn < p.tiles_n) {
       unsigned long long acc[2][32];
 #pragma unroll
       for (int i = 0; i < 32; ++i) acc[0][i] = acc[1][i] = 0ull;
-      float x = xs[0], w0 = ws0[0], w1 = ws1[0];
       for (int kb = 0; kb < p.KB; ++kb, ++it) {
         const int slot = it & 1;
         const float f0 = x * w0, f1 = x * w1;
         const unsigned long long s0 = pack2(f0, f0), s1 = pack2(f1, f1);
         if (kb + 1 < p.KB) {
-          x = xs[kb + 1];
-          w0 = ws0[kb + 1];
-          w1 = ws1[kb + 1];
+          x = p.xs[xo + kb + 1];
+          w0 = p.ws[wo + kb + 1];
+          w1 = p.ws[wo + kb + 1 + p.step_ws];
         }
-        ok = ok && mbar_wait_spin(&sm.tfull[slot], (it >> 1) & 1, sm.abort_flag, p.err, p.timeout);
+        ok = ok && mbar_wait_spin(&sm.done[it % STAGES], (it / STAGES) & 1, sm.abort_flag, p.err,
+                                  p.timeout);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
         tc_fence_after();
+        // four loads of 32 columns, each started before the products of the one before it;
+        // the slot is handed back before the last products
         const uint32_t ta = lane_base + slot * 256;
+        uint32_t v[2][32];
+        tmem_start_ld32(ta + c0, v[0]);
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int c = 0; c < 64; c += 32) {
-            uint32_t v[32];
-            tmem_ld32(ta + (h ? c1 : c0) + c, v);
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              fma2(acc[h][c / 2 + j], pack2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])),
-                   h ? s1 : s0);
+        for (int c = 0; c < 4; ++c) {
+          uint32_t* r = v[c & 1];
+          tmem_wait_ld32(r);
+          if (c < 3) {
+            tmem_start_ld32(ta + (c < 1 ? c0 : c1) + (c + 1) % 2 * 32, v[(c + 1) & 1]);
+          } else {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(tempty0 + slot * 8);
           }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(tempty0 + slot * 8);
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            fma2(acc[c >> 1][(c & 1) * 16 + i],
+                 pack2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])),
+                 c < 2 ? s0 : s1);
+        }
       }
+      const int m0 = tm * 256 + static_cast<int>(rank) * 128 + quad * 32, m = m0 + lane, tn0 = tn;
+      next_tile();
+      if (tn < p.tiles_n) first_scales();
       if (ACT) {
-        float v[64];
         uint32_t big = 0;
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
           float g0, g1, u0, u1;
           unpack2(acc[0][i], g0, g1);
           unpack2(acc[1][i], u0, u1);
-          v[2 * i] = silu_fast(g0) * u0;
-          v[2 * i + 1] = silu_fast(g1) * u1;
-          big = max(big, max(__float_as_uint(v[2 * i]) & 0x7FFFFFFFu,
-                             __float_as_uint(v[2 * i + 1]) & 0x7FFFFFFFu));
+          const float a0 = silu_rcp(g0) * u0, a1 = silu_rcp(g1) * u1;
+          big = max(big, max(__float_as_uint(a0) & 0x7FFFFFFFu, __float_as_uint(a1) & 0x7FFFFFFFu));
+          acc[0][i] = pack2(a0, a1);
         }
         if (p.out_dtype == KLT_DT_E4M3) {
           // the group's other 64 columns are in the thread of the other half
-          sm.amax[half * 128 + row] = __uint_as_float(big);
+          sm.amax[half * 128 + row] = big;
           named_bar_sync(1, 256);
-          big = max(big, __float_as_uint(sm.amax[(half ^ 1) * 128 + row]));
-          const float s = group_scale(big);
-          const float inv = 1.0f / s;
-          const bool fast = quot_fast(s);
-          if (ok && m < p.M) {
-            uint8_t* o = static_cast<uint8_t*>(p.out) + m * p.ld_out + tn * 128 + half * 64;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t w[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                float q[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) q[e] = quot_group(v[16 * i + 4 * j + e], s, inv, fast);
-                w[j] = f32x2_to_e4m3x2(q[0], q[1]) | (f32x2_to_e4m3x2(q[2], q[3]) << 16);
-              }
-              if (p.out_wide) {
-                reinterpret_cast<uint4*>(o)[i] = make_uint4(w[0], w[1], w[2], w[3]);
-              } else {
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                  o[16 * i + j] = static_cast<uint8_t>(w[j / 4] >> (8 * (j % 4)));
-              }
-            }
-            if (half == 0) p.out_s[m * (p.width / 128) + tn] = s;
-          }
+          big = max(big, sm.amax[(half ^ 1) * 128 + row]);
           named_bar_sync(1, 256);  // amax is free for the next tile
-        } else if (ok && m < p.M) {
-          store_row64(p, m, tn * 128 + half * 64, v);
-        }
-      } else if (ok && m < p.M) {
+          float s = group_scale(big);
+          if (ok && half == 0 && m < p.M)
+            p.out_s[static_cast<int64_t>(m) * (p.width / 128) + tn0] = s;
+          const float k = rescale(s), inv = 1.0f / s;
+          if (k != 1.0f) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float v[64];
+            for (int i = 0; i < 32; ++i) {
+              float q0, q1;
+              unpack2(acc[0][i], q0, q1);
+              acc[0][i] = pack2(q0 * k, q1 * k);
+            }
+          }
+          uint32_t w[16];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) unpack2(acc[h][i], v[2 * i], v[2 * i + 1]);
-          store_row64(p, m, tn * 256 + half * 128 + h * 64, v);
+          for (int j = 0; j < 16; ++j) {
+            float q[4];
+            unpack2(acc[0][2 * j], q[0], q[1]);
+            unpack2(acc[0][2 * j + 1], q[2], q[3]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) q[e] = quot_group(q[e], s, inv);
+            w[j] = f32x2_to_e4m3x2(q[0], q[1]) | (f32x2_to_e4m3x2(q[2], q[3]) << 16);
+          }
+          if (ok && m0 < p.M) {
+            const int c = tn0 * 128 + half * 64;
+            if (p.out_wide) {
+              boxes_free();
+              store_box(boxes, &omap, w, c, m0);
+            } else if (m < p.M) {
+              uint8_t* o = static_cast<uint8_t*>(p.out) + static_cast<int64_t>(m) * p.ld_out + c;
+#pragma unroll
+              for (int j = 0; j < 64; ++j) o[j] = static_cast<uint8_t>(w[j / 4] >> (8 * (j % 4)));
+            }
+          }
+        } else if (ok) {
+          store_rows64(p, &omap, boxes, m0, tn0 * 128 + half * 64, acc[0], false);
         }
+      } else if (ok) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          store_rows64(p, &omap, boxes, m0, tn0 * 256 + h * 128 + half * 64, acc[h], h == 1);
       }
     }
+    tma_store_wait();
     tc_fence_before();
     __syncwarp();
   }
@@ -314,14 +387,18 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 template <int ACT>
-cudaError_t launch(const CUtensorMap& tok, const CUtensorMap& wmap, const LinParams& p,
-                   int num_sms, cudaStream_t s) {
+cudaError_t launch(const CUtensorMap& tok, const CUtensorMap& wmap, const CUtensorMap& omap,
+                   LinParams p, int num_sms, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(wide_kernel<ACT>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
   if (e != cudaSuccess) return e;
-  const int tiles_m = (p.M + 255) / 256;
-  const int tiles = tiles_m * (ACT ? p.width / 128 : (p.NB + 1) / 2);
-  const int pairs = tiles < num_sms / 2 ? tiles : num_sms / 2;
+  p.tiles_m = (p.M + 255) / 256;
+  p.tiles_n = ACT ? p.width / 128 : (p.NB + 1) / 2;
+  const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
+  const int pairs = tiles < num_sms / 2 ? static_cast<int>(tiles) : num_sms / 2;
+  p.step_m = pairs % p.tiles_m;
+  p.step_n = pairs / p.tiles_m;
+  p.step_ws = ACT ? p.up * p.KB : p.KB;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * pairs);
   cfg.blockDim = dim3(THREADS);
@@ -336,21 +413,23 @@ cudaError_t launch(const CUtensorMap& tok, const CUtensorMap& wmap, const LinPar
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, wide_kernel<ACT>, tok, wmap, p, tiles_m, tiles);
+  return cudaLaunchKernelEx(&cfg, wide_kernel<ACT>, tok, wmap, omap, p);
 }
 
 }  // namespace
 
 bool linear_wide_regs_ok() {
-  // setmaxnreg moves registers between the warpgroups: 72 + 2 x 216 = 3 x 168 at launch
+  // setmaxnreg moves registers between the warpgroups: 56 + 2 x 224 = 3 x 168 at launch
   cudaFuncAttributes a;
   return cudaFuncGetAttributes(&a, wide_kernel<0>) == cudaSuccess && a.numRegs >= 168 &&
          cudaFuncGetAttributes(&a, wide_kernel<1>) == cudaSuccess && a.numRegs >= 168;
 }
 
 cudaError_t launch_linear_wide(const CUtensorMap& tok, const CUtensorMap& wmap,
-                               const LinParams& p, bool swiglu, int num_sms, cudaStream_t s) {
-  return swiglu ? launch<1>(tok, wmap, p, num_sms, s) : launch<0>(tok, wmap, p, num_sms, s);
+                               const CUtensorMap& omap, const LinParams& p, bool swiglu,
+                               int num_sms, cudaStream_t s) {
+  return swiglu ? launch<1>(tok, wmap, omap, p, num_sms, s)
+                : launch<0>(tok, wmap, omap, p, num_sms, s);
 }
 
 }  // namespace klt
