@@ -68,71 +68,84 @@ KLT_DEV void tmem_wait_ld32(uint32_t* r) {
                : "memory");
 }
 
-// An output box of a warp: this thread's 64 bytes (w) of row m0 + lane, at byte `col` of the
-// output, staged in buffer `buf` in the output map's swizzle (no bank conflicts) and stored by
-// a bulk copy, which cuts off what lies outside the output and runs on while the warp goes on.
-// Lane 0 issues all of a warp's copies.
-KLT_DEV void store_box(uint8_t* buf, const CUtensorMap* omap, const uint32_t* w, int col, int m0) {
-  const int lane = lane_id(), x = (lane >> 1) & 3;
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    *reinterpret_cast<uint4*>(buf + lane * 64 + (j ^ x) * 16) =
-        make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-  fence_proxy_async_shared();
-  __syncwarp();
-  if (lane == 0) tma_store_2d(omap, buf, col, m0);
-}
-// The warp's buffers are free: its bulk copies have read them.
-KLT_DEV void boxes_free() {
+// The output leaves through a warp's four boxes of 32 rows x 64 bytes: staged in the output
+// map's swizzle (no bank conflicts) and stored by bulk copies, which cut off what lies outside
+// the output and run on while the warp goes on.  Lane b issues the copy of box b.
+KLT_DEV void boxes_free() {  // the warp's copies have read their boxes
   tma_store_wait_read<0>();
   __syncwarp();
 }
-// A warp's 64 columns c .. c + 63 of its 32 rows from m0 on (this thread's row in v, two
-// values each), through the four buffers at `buf` (bf16: two of them, the first or the last).
-KLT_DEV void store_rows64(const LinParams& p, const CUtensorMap* omap, uint8_t* buf, int m0,
-                          int c, const unsigned long long* v, bool last) {
-  if (m0 >= p.M || c >= p.width) return;  // a bulk store starts inside the output
-  const bool f32 = p.out_dtype == KLT_DT_F32;
-  if (p.out_wide && f32) {
-    boxes_free();
+// This thread's 64 bytes (w) of row `lane` of a box.
+KLT_DEV void fill_box(uint8_t* box, const uint32_t* w) {
+  const int lane = lane_id(), x = (lane >> 1) & 3;
 #pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      uint32_t w[16];
+  for (int j = 0; j < 4; ++j)
+    *reinterpret_cast<uint4*>(box + lane * 64 + (j ^ x) * 16) =
+        make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+}
+// Stores the filled boxes to rows m0 .. m0 + 31: lane b holds box b's byte column, or one that
+// is past the row's `bytes` (then it issues none: a copy starts inside the output).
+KLT_DEV void store_boxes(const uint8_t* boxes, const CUtensorMap* omap, int col, int bytes,
+                         int m0) {
+  fence_proxy_async_shared();
+  __syncwarp();
+  if (col < bytes) tma_store_2d(omap, boxes + lane_id() * BOX_BYTES, col, m0);
+}
+// A warp's 2 x 64 columns (128 apart, from c on) of its 32 rows from m0 on; this thread's row
+// in v, two values each.  COUNT = 1: the first 64 only.
+template <int COUNT>
+KLT_DEV void store_rows(const LinParams& p, const CUtensorMap* omap, uint8_t* boxes, int m0,
+                        int c, const unsigned long long (*v)[32]) {
+  if (m0 >= p.M) return;
+  const int lane = lane_id();
+  if (p.out_wide && p.out_dtype == KLT_DT_F32) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        w[2 * i] = static_cast<uint32_t>(v[h * 8 + i]);
-        w[2 * i + 1] = static_cast<uint32_t>(v[h * 8 + i] >> 32);
+    for (int g = 0; g < COUNT; ++g) {
+      boxes_free();
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          w[2 * i] = static_cast<uint32_t>(v[g][b * 8 + i]);
+          w[2 * i + 1] = static_cast<uint32_t>(v[g][b * 8 + i] >> 32);
+        }
+        fill_box(boxes + b * BOX_BYTES, w);
       }
-      if (c + h * 16 < p.width) store_box(buf + h * BOX_BYTES, omap, w, (c + h * 16) * 4, m0);
+      store_boxes(boxes, omap, lane < 4 ? (c + g * 128 + lane * 16) * 4 : p.width * 4,
+                  p.width * 4, m0);
     }
   } else if (p.out_wide) {
-    if (!last) boxes_free();
+    boxes_free();
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int b = 0; b < 2 * COUNT; ++b) {
       uint32_t w[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         float lo, hi;
-        unpack2(v[h * 16 + i], lo, hi);
+        unpack2(v[b >> 1][(b & 1) * 16 + i], lo, hi);
         const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
         w[i] = *reinterpret_cast<const uint32_t*>(&t);
       }
-      if (c + h * 32 < p.width)
-        store_box(buf + (last * 2 + h) * BOX_BYTES, omap, w, (c + h * 32) * 2, m0);
+      fill_box(boxes + b * BOX_BYTES, w);
     }
-  } else if (m0 + lane_id() < p.M) {
-    const int es = f32 ? 4 : 2;
-    char* o = static_cast<char*>(p.out) + ((m0 + lane_id()) * p.ld_out + c) * es;
+    store_boxes(boxes, omap,
+                lane < 2 * COUNT ? (c + (lane >> 1) * 128 + (lane & 1) * 32) * 2 : p.width * 2,
+                p.width * 2, m0);
+  } else if (m0 + lane < p.M) {
+    const bool f32 = p.out_dtype == KLT_DT_F32;
+    const int64_t row = (m0 + lane) * p.ld_out;
 #pragma unroll
-    for (int i = 0; i < 64; ++i, o += es) {
+    for (int i = 0; i < 64 * COUNT; ++i) {
+      const int col = c + (i >> 6) * 128 + (i & 63);
       float lo, hi;
-      unpack2(v[i / 2], lo, hi);
+      unpack2(v[i >> 6][(i & 63) / 2], lo, hi);
       const float x = i % 2 ? hi : lo;
-      if (c + i < p.width) {
+      if (col < p.width) {
         if (f32)
-          *reinterpret_cast<float*>(o) = x;
+          static_cast<float*>(p.out)[row + col] = x;
         else
-          *reinterpret_cast<__nv_bfloat16*>(o) = __float2bfloat16(x);
+          static_cast<__nv_bfloat16*>(p.out)[row + col] = __float2bfloat16(x);
       }
     }
   }
@@ -357,7 +370,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int c = tn0 * 128 + half * 64;
             if (p.out_wide) {
               boxes_free();
-              store_box(boxes, &omap, w, c, m0);
+              fill_box(boxes, w);
+              store_boxes(boxes, &omap, lane == 0 ? c : p.width, p.width, m0);
             } else if (m < p.M) {
               uint8_t* o = static_cast<uint8_t*>(p.out) + static_cast<int64_t>(m) * p.ld_out + c;
 #pragma unroll
@@ -365,12 +379,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
           }
         } else if (ok) {
-          store_rows64(p, &omap, boxes, m0, tn0 * 128 + half * 64, acc[0], false);
+          store_rows<1>(p, &omap, boxes, m0, tn0 * 128 + half * 64, acc);
         }
       } else if (ok) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          store_rows64(p, &omap, boxes, m0, tn0 * 256 + h * 128 + half * 64, acc[h], h == 1);
+        store_rows<2>(p, &omap, boxes, m0, tn0 * 256 + half * 64, acc);
       }
     }
     tma_store_wait();
