@@ -16,97 +16,180 @@
 namespace klt {
 namespace {
 
-// ------------------------------------------------------------------ eight values of a row
-// A row of C elements is handled in vectors of eight.  `wide` says that the row's start is
-// 16-byte aligned, so a whole vector is one (bf16) or two (fp32) 16-byte accesses; the last
-// partial vector and unaligned rows go element by element.  Elements past C read as 0.
-// Plain loads, not the read-only path: the launch may begin while the kernel that writes
-// these tensors still runs, and h_out may be h.
-KLT_DEV void load8(const void* base, bool f32, int64_t off, int col, int C, bool wide, float* v) {
-  if (f32) {
-    const float* p = static_cast<const float*>(base) + off + col;
-    if (wide && col + 8 <= C) {
-      const float4 a = reinterpret_cast<const float4*>(p)[0];
-      const float4 b = reinterpret_cast<const float4*>(p)[1];
+// ------------------------------------------------------------------ 128 columns of a row
+// A half warp holds one group of 128 columns of a row, eight neighbouring ones per lane.
+// Where the tensor's rows start on 16 bytes (8 for codes) a lane's eight are one or two vector
+// accesses.  Else, and for the short group at a row's end, the half warp moves them element by
+// element, neighbouring lanes neighbouring elements (whole sectors: written eight apart, a
+// ragged 1021 x 2901 batch took 26 us), through 512 bytes of shared memory.  Plain loads, not
+// the read-only path: the launch may begin while the kernel that writes these tensors still
+// runs, and h_out may be h.
+struct Half {
+  uint32_t mask;  // the lanes of this half warp
+  int lane;       // 0 .. 15
+  float* buf;     // 128 floats of its own
+};
+KLT_DEV Half half_warp(float* bufs) {
+  const int h = threadIdx.x >> 4;
+  return {0xFFFFu << (16 * (h & 1)), static_cast<int>(threadIdx.x & 15), bufs + h * 128};
+}
+
+// This lane's eight values of columns c .. c + 127 (c < C) of the row at element `off`; those
+// past C are 0.
+KLT_DEV void load8(const Half& hw, const void* base, bool f32, int64_t off, int c, int C, bool wide,
+                   float* v) {
+  if (wide && c + 128 <= C) {
+    off += c + hw.lane * 8;
+    if (f32) {
+      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + off);
+      const float4 a = p[0], b = p[1];
       v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
       v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
     } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = col + i < C ? p[i] : 0.f;
-    }
-  } else {
-    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(base) + off + col;
-    if (wide && col + 8 <= C) {
-      const uint4 a = *reinterpret_cast<const uint4*>(p);
+      const uint4 a =
+          *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + off);
       const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         v[2 * i] = __uint_as_float(w[i] << 16);
         v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = col + i < C ? __bfloat162float(p[i]) : 0.f;
     }
+    return;
   }
-}
-KLT_DEV void store8(void* base, bool f32, int64_t off, int col, int C, bool wide,
-                    const float* v) {
-  if (f32) {
-    float* p = static_cast<float*>(base) + off + col;
-    if (wide && col + 8 <= C) {
-      reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-      reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
+  const float* pf = static_cast<const float*>(base) + off + c;
+  const __nv_bfloat16* pb = static_cast<const __nv_bfloat16*>(base) + off + c;
+  float t[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (col + i < C) p[i] = v[i];
-    }
-  } else {
-    __nv_bfloat16* p = static_cast<__nv_bfloat16*>(base) + off + col;
-    if (wide && col + 8 <= C) {
+  for (int i = 0; i < 8; ++i) {
+    const int e = i * 16 + hw.lane;
+    t[i] = c + e < C ? (f32 ? pf[e] : __bfloat162float(pb[e])) : 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) hw.buf[i * 16 + hw.lane] = t[i];
+  __syncwarp(hw.mask);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = hw.buf[hw.lane * 8 + i];
+  __syncwarp(hw.mask);
+}
+KLT_DEV void store8(const Half& hw, void* base, bool f32, int64_t off, int c, int C, bool wide,
+                    const float* v) {
+  if (wide && c + 128 <= C) {
+    off += c + hw.lane * 8;
+    if (f32) {
+      float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + off);
+      p[0] = make_float4(v[0], v[1], v[2], v[3]);
+      p[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
       uint32_t w[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
         w[i] = *reinterpret_cast<const uint32_t*>(&b);
       }
-      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
+      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(base) + off) =
+          make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    return;
+  }
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (col + i < C) p[i] = __float2bfloat16(v[i]);
+  for (int i = 0; i < 8; ++i) hw.buf[hw.lane * 8 + i] = v[i];
+  __syncwarp(hw.mask);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int e = i * 16 + hw.lane;
+    if (c + e < C) {
+      if (f32)
+        static_cast<float*>(base)[off + c + e] = hw.buf[e];
+      else
+        static_cast<__nv_bfloat16*>(base)[off + c + e] = __float2bfloat16(hw.buf[e]);
     }
   }
+  __syncwarp(hw.mask);
+}
+KLT_DEV void store_codes(const Half& hw, uint8_t* q, int64_t off, int c, int C, bool wide,
+                         uint2 codes) {
+  if (wide && c + 128 <= C) {
+    *reinterpret_cast<uint2*>(q + off + c + hw.lane * 8) = codes;
+    return;
+  }
+  reinterpret_cast<uint2*>(hw.buf)[hw.lane] = codes;
+  __syncwarp(hw.mask);
+  const uint8_t* b = reinterpret_cast<const uint8_t*>(hw.buf);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int e = i * 16 + hw.lane;
+    if (c + e < C) q[off + c + e] = b[e];
+  }
+  __syncwarp(hw.mask);
 }
 
-// The group's scale and this lane's eight codes: the 16 lanes of a half warp hold one group
-// of 128 columns.  The largest magnitude is taken on the bit patterns, so a group that holds
-// an infinity or a NaN gets a scale that is not finite and dequantises to NaN as a whole.
-KLT_DEV uint2 quant8(const float* v, float& s_out) {
-  uint32_t m = 0;
+// The largest magnitude of a group, NaN if it holds one.
+KLT_DEV float group_amax(const Half& hw, const float* v) {
+  float m = max_nan(max_nan(max_nan(v[0], v[1]), max_nan(v[2], v[3])),
+                    max_nan(max_nan(v[4], v[5]), max_nan(v[6], v[7])));
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-#pragma unroll
-  for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-  float s = group_scale(m);
-  s_out = s;
-  const float k = rescale(s), inv = 1.0f / s;
+  for (int o = 8; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(hw.mask, m, o));
+  return m;
+}
+// Codes of eight values of a group with scale s.
+KLT_DEV uint2 codes8(const float* v, float s) {
   float t[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) t[i] = quot_group(v[i] * k, s, inv);
+  for (int i = 0; i < 8; ++i) t[i] = v[i];
+  const float k = rescale(s), inv = __frcp_rn(s);
+  if (k != 1.0f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] *= k;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) t[i] = quot_group(t[i], s, inv);
   return make_uint2(f32x2_to_e4m3x2(t[0], t[1]) | (f32x2_to_e4m3x2(t[2], t[3]) << 16),
                     f32x2_to_e4m3x2(t[4], t[5]) | (f32x2_to_e4m3x2(t[6], t[7]) << 16));
 }
-KLT_DEV void store_codes(uint8_t* q, int64_t off, int col, int C, bool wide, uint2 c) {
-  uint8_t* p = q + off + col;
-  if (wide && col + 8 <= C) {
-    *reinterpret_cast<uint2*>(p) = c;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (col + i < C) p[i] = static_cast<uint8_t>((i < 4 ? c.x : c.y) >> (8 * (i & 3)));
+
+// Eight neighbouring values as they lie in memory, of a tensor whose rows are vectors: the
+// loads of a whole row are issued before the first value is unpacked.
+template <bool F32>
+struct Raw8 {
+  uint4 w[F32 ? 2 : 1];
+  KLT_DEV void load(const void* base, int64_t off) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(base) +
+                                                    off * (F32 ? 4 : 2));
+    w[0] = p[0];
+    if (F32) w[F32 ? 1 : 0] = p[1];
   }
+  KLT_DEV void get(float* v) const {
+    if (F32) {
+      const uint32_t t[8] = {w[0].x, w[0].y, w[0].z, w[0].w,
+                             w[F32].x, w[F32].y, w[F32].z, w[F32].w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(t[i]);
+    } else {
+      const uint32_t t[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(t[i] << 16);
+        v[2 * i + 1] = __uint_as_float(t[i] & 0xFFFF0000u);
+      }
+    }
+  }
+};
+template <bool F32>
+KLT_DEV void put8(void* base, int64_t off, const float* v) {
+  uint4* p = reinterpret_cast<uint4*>(static_cast<char*>(base) + off * (F32 ? 4 : 2));
+  uint32_t t[8];
+#pragma unroll
+  for (int i = 0; i < (F32 ? 8 : 4); ++i) {
+    if (F32) {
+      t[i] = __float_as_uint(v[i]);
+    } else {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      t[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+  }
+  p[0] = make_uint4(t[0], t[1], t[2], t[3]);
+  if (F32) p[1] = make_uint4(t[4], t[5], t[6], t[7]);
 }
 
 // ------------------------------------------------------------------ the quantiser
@@ -115,45 +198,57 @@ struct QuantParams {
   uint8_t* q;
   float* s;
   int64_t ld_x, ld_q;
-  int64_t items;  // rows x groups
-  int K, G;
+  uint32_t items;  // rows x groups, below 2^31
+  uint32_t magic;  // row of item i = (i * magic) >> shift
+  int shift, K, G;
   bool f32, wide_x, wide_q;
 };
 
-// One half warp per group of 128 columns, U groups per half warp with their loads in flight
-// together.
-template <int U>
+KLT_DEV void quant_item(const QuantParams& p, uint32_t it, uint32_t& row, int& c) {
+  row = static_cast<uint32_t>((static_cast<uint64_t>(it) * p.magic) >> p.shift);
+  c = static_cast<int>(it - row * p.G) * 128;
+}
+KLT_DEV void quant_store(const Half& hw, const QuantParams& p, uint32_t it, uint32_t row, int c,
+                         const float* v) {
+  const float s = group_scale(group_amax(hw, v));
+  store_codes(hw, p.q, row * p.ld_q, c, p.K, p.wide_q, codes8(v, s));
+  if (hw.lane == 0) p.s[it] = s;
+}
+// Any strides and widths: one group of 128 columns per half warp.
 __global__ void __launch_bounds__(256) quant_kernel(QuantParams p) {
+  __shared__ float bufs[16 * 128];
   pdl_trigger();
   pdl_wait();
-  const int hw = threadIdx.x >> 4, lane = threadIdx.x & 15;
-  const int64_t base = static_cast<int64_t>(blockIdx.x) * (16 * U) + hw;
-  float v[U][8];
-  int64_t row[U];
-  int col[U];
+  const Half hw = half_warp(bufs);
+  const uint32_t it = blockIdx.x * 16u + (threadIdx.x >> 4);
+  if (it >= p.items) return;
+  uint32_t row;
+  int c;
+  float v[8];
+  quant_item(p, it, row, c);
+  load8(hw, p.x, p.f32, row * p.ld_x, c, p.K, p.wide_x, v);
+  quant_store(hw, p, it, row, c, v);
+}
+// Vectors throughout (K a multiple of 128, aligned rows): U groups per half warp, their loads
+// in flight together.
+template <int U, bool F32>
+__global__ void __launch_bounds__(256) quant_vec_kernel(QuantParams p) {
+  pdl_trigger();
+  const Half hw = half_warp(nullptr);
+  const uint32_t base = blockIdx.x * (16u * U) + (threadIdx.x >> 4);
+  Raw8<F32> raw[U];
+  uint32_t row[U];
+  int c[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) quant_item(p, min(base + 16 * u, p.items - 1), row[u], c[u]);
+  pdl_wait();
+#pragma unroll
+  for (int u = 0; u < U; ++u) raw[u].load(p.x, row[u] * p.ld_x + c[u] + hw.lane * 8);
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int64_t it = base + 16 * u;
-    if (it < p.items) {
-      row[u] = it / p.G;
-      col[u] = static_cast<int>(it - row[u] * p.G) * 128 + lane * 8;
-      load8(p.x, p.f32, row[u] * p.ld_x, col[u], p.K, p.wide_x, v[u]);
-    }
-  }
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int64_t it = base + 16 * u;
-    // both halves of a warp take part in the shuffles; a half past the end holds zeros
-    if (it >= p.items) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[u][i] = 0.f;
-    }
-    float s;
-    const uint2 c = quant8(v[u], s);
-    if (it < p.items) {
-      store_codes(p.q, row[u] * p.ld_q, col[u], p.K, p.wide_q, c);
-      if (lane == 0) p.s[it] = s;
-    }
+    float v[8];
+    raw[u].get(v);
+    if (base + 16 * u < p.items) quant_store(hw, p, base + 16 * u, row[u], c[u], v);
   }
 }
 
@@ -182,122 +277,223 @@ KLT_DEV float block_sum(float v, float* part) {
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   return v;
 }
+KLT_DEV float row_rms_inverse(const float (*v)[8], int vpt, int H, float eps, float* part) {
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < vpt; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
+  return 1.0f / sqrtf(block_sum(ss, part) / static_cast<float>(H) + eps);
+}
+KLT_DEV float gate_value(float g, bool sigmoid) {
+  // the divisor of the fast divide stays in its range: for g < -80 the gate is below 2e-35
+  return sigmoid ? __fdividef(1.0f, 1.0f + __expf(-fmaxf(g, -80.0f))) : g;
+}
+KLT_DEV float load1(const void* p, bool f32, int64_t i) {
+  return f32 ? static_cast<const float*>(p)[i]
+             : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
 
-// One block per row, VPT vectors of eight columns per thread.
+// Codes and scale of a group of n = t r (t = h' gamma): t against its own largest magnitude,
+// so r enters the scale alone.
+KLT_DEV void store_norm_codes(const Half& hw, const NormParams& p, int64_t row, int c, float r,
+                              const float* t) {
+  const float d = over_448(group_amax(hw, t));
+  float s = d * r;
+  uint2 codes = codes8(t, d == 0.f ? 1.0f : d);
+  if (s == 0.f) s = 1.0f, codes = make_uint2(0, 0);  // n is 0 throughout, or rounds to it
+  store_codes(hw, p.q, row * p.ld_q, c, p.H, p.wide_q, codes);
+  if (hw.lane == 0) p.s[row * p.G + c / 128] = s;
+}
+
+// One block per row, VPT groups of 128 columns per half warp.  The row's scalars (1/rms and
+// the scales) multiply last: y gamma gate is exact up to its final rounding for bf16 tensors,
+// and h' is one multiply-add of it.
 template <int VPT>
-__global__ void __launch_bounds__(1024 / (VPT > 1 ? 2 : 1)) norm_kernel(NormParams p) {
+__global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) norm_kernel(NormParams p) {
   __shared__ float part[2][32];
-  pdl_trigger();
+  extern __shared__ float bufs[];  // 128 per half warp where a row needs them
+  const Half hw = half_warp(bufs);
   const int64_t row = blockIdx.x;
-  const int nt = blockDim.x;
-  float u[VPT][8], h[VPT][8];
+  const int c0 = static_cast<int>(threadIdx.x >> 4) * 128, step = static_cast<int>(blockDim.x) * 8;
+  float u[VPT][8], h[VPT][8], g[8];
+  pdl_trigger();
   pdl_wait();
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int c = (threadIdx.x + i * nt) * 8;
+    const int c = c0 + i * step;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) u[i][j] = h[i][j] = 0.f;
     if (c < p.H) {
-      if (p.y) load8(p.y, p.y_f32, row * p.ld_y, c, p.H, p.wide_y, u[i]);
-      load8(p.h, p.h_f32, row * p.ld_h, c, p.H, p.wide_h, h[i]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) u[i][j] = h[i][j] = 0.f;
+      if (p.y) load8(hw, p.y, p.y_f32, row * p.ld_y, c, p.H, p.wide_y, u[i]);
+      load8(hw, p.h, p.h_f32, row * p.ld_h, c, p.H, p.wide_h, h[i]);
     }
   }
-  if (p.y) {
-    float r = 1.0f;
-    if (p.gamma_post) {
-      float ss = 0.f;
+  float scale = p.branch_scale;
+  if (p.gamma_post) scale *= row_rms_inverse(u, VPT, p.H, p.eps, part[0]);
+  if (p.gate && p.gate_col == 0)
+    scale *= gate_value(load1(p.gate, p.gate_f32, row * p.gate_row), p.sigmoid);
 #pragma unroll
-      for (int i = 0; i < VPT; ++i)
+  for (int i = 0; i < VPT; ++i) {
+    const int c = c0 + i * step;
+    if (c < p.H) {
+      if (p.gamma_post) {
+        load8(hw, p.gamma_post, false, 0, c, p.H, p.wide_gpost, g);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(u[i][j], u[i][j], ss);
-      r = 1.0f / sqrtf(block_sum(ss, part[0]) / static_cast<float>(p.H) + p.eps);
-    }
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int c = (threadIdx.x + i * nt) * 8;
-      if (c < p.H) {
-        float g[8];
-        if (p.gamma_post) {
-          load8(p.gamma_post, false, 0, c, p.H, p.wide_gpost, g);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) u[i][j] = u[i][j] * r * g[j];
-        }
-        if (p.gate) {
-          if (p.gate_col == 1) {
-            load8(p.gate, p.gate_f32, row * p.gate_row, c, p.H, p.wide_gate, g);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const int64_t o =
-                  row * p.gate_row + static_cast<int64_t>(min(c + j, p.H - 1)) * p.gate_col;
-              g[j] = p.gate_f32 ? static_cast<const float*>(p.gate)[o]
-                                : __bfloat162float(static_cast<const __nv_bfloat16*>(p.gate)[o]);
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            u[i][j] *= p.sigmoid ? 1.0f / (1.0f + expf(-g[j])) : g[j];
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          h[i][j] = c + j < p.H ? fmaf(p.branch_scale, u[i][j], p.res_scale * h[i][j]) : 0.f;
+        for (int j = 0; j < 8; ++j) u[i][j] *= g[j];
       }
-    }
-  } else {
+      if (p.gate && p.gate_col != 0) {
+        if (p.gate_col == 1) {
+          load8(hw, p.gate, p.gate_f32, row * p.gate_row, c, p.H, p.wide_gate, g);
+        } else {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int c = (threadIdx.x + i * nt) * 8;
+          for (int j = 0; j < 8; ++j) {
+            const int e = c + hw.lane * 8 + j;
+            g[j] = e < p.H ? load1(p.gate, p.gate_f32, row * p.gate_row + e * p.gate_col) : 0.f;
+          }
+        }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) h[i][j] = c + j < p.H ? p.res_scale * h[i][j] : 0.f;
-    }
-  }
-  if (p.h_out) {
+        for (int j = 0; j < 8; ++j) u[i][j] *= gate_value(g[j], p.sigmoid);
+      }
+      // columns past H are 0 in every operand; they stay 0 whatever the scales are
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int c = (threadIdx.x + i * nt) * 8;
-      if (c < p.H) store8(p.h_out, p.h_f32, row * p.ld_h_out, c, p.H, p.wide_h_out, h[i]);
+      for (int j = 0; j < 8; ++j) {
+        const float r = p.res_scale * h[i][j];
+        h[i][j] = c + hw.lane * 8 + j < p.H ? (p.y ? fmaf(scale, u[i][j], r) : r) : 0.f;
+      }
+      if (p.h_out) store8(hw, p.h_out, p.h_f32, row * p.ld_h_out, c, p.H, p.wide_h_out, h[i]);
     }
   }
   if (!p.n && !p.q) return;
-  if (p.gamma_pre) {
-    float ss = 0.f;
+  const float r = p.gamma_pre ? row_rms_inverse(h, VPT, p.H, p.eps, part[1]) : 1.0f;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i)
+  for (int i = 0; i < VPT; ++i) {
+    const int c = c0 + i * step;
+    if (c < p.H) {
+      if (p.gamma_pre) {
+        load8(hw, p.gamma_pre, false, 0, c, p.H, p.wide_gpre, g);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(h[i][j], h[i][j], ss);
-    const float r = 1.0f / sqrtf(block_sum(ss, part[1]) / static_cast<float>(p.H) + p.eps);
+        for (int j = 0; j < 8; ++j) h[i][j] *= g[j];
+      }
+      if (p.q) store_norm_codes(hw, p, row, c, r, h[i]);
+      if (p.n) {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int c = (threadIdx.x + i * nt) * 8;
-      if (c < p.H) {
-        float g[8];
-        load8(p.gamma_pre, false, 0, c, p.H, p.wide_gpre, g);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) h[i][j] = c + j < p.H ? h[i][j] * r * g[j] : 0.f;
+        for (int j = 0; j < 8; ++j) h[i][j] *= r;
+        store8(hw, p.n, false, row * p.ld_n, c, p.H, p.wide_n, h[i]);
       }
     }
   }
+}
+
+// The same for rows that are vectors throughout (H a multiple of 128, aligned; y and gates
+// across channels in bf16): the row's loads are in flight together and stay packed until used.
+template <int VPT, bool HF32>
+__global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) norm_vec_kernel(NormParams p) {
+  __shared__ float part[2][32];
+  const Half hw = half_warp(nullptr);
+  const int64_t row = blockIdx.x;
+  const int c0 = static_cast<int>(threadIdx.x) * 8, step = static_cast<int>(blockDim.x) * 8;
+  Raw8<HF32> hr[VPT];
+  Raw8<false> yr[VPT], g1[VPT], g2[VPT], gt[VPT];
+  pdl_trigger();
+  pdl_wait();
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    const int c = (threadIdx.x + i * nt) * 8;
-    if (p.n && c < p.H) store8(p.n, false, row * p.ld_n, c, p.H, p.wide_n, h[i]);
-    if (p.q) {  // 16 neighbouring threads hold one group of 128 columns
-      float s;
-      const uint2 codes = quant8(h[i], s);
-      if (c < p.H) {
-        store_codes(p.q, row * p.ld_q, c, p.H, p.wide_q, codes);
-        if ((threadIdx.x & 15) == 0) p.s[row * p.G + c / 128] = s;
+    const int c = c0 + i * step;
+    hr[i].w[0] = yr[i].w[0] = make_uint4(0, 0, 0, 0);
+    if (HF32) hr[i].w[HF32] = make_uint4(0, 0, 0, 0);
+    if (c < p.H) {
+      if (p.y) yr[i].load(p.y, row * p.ld_y + c);
+      hr[i].load(p.h, row * p.ld_h + c);
+      if (VPT == 1) {  // a short row's weights too
+        if (p.gamma_post) g1[i].load(p.gamma_post, c);
+        if (p.gamma_pre) g2[i].load(p.gamma_pre, c);
+        if (p.gate && p.gate_col != 0) gt[i].load(p.gate, row * p.gate_row + c);
+      }
+    }
+  }
+  float scale = p.branch_scale;
+  if (p.gamma_post) {
+    float ss = 0.f, v[8];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      yr[i].get(v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
+    }
+    scale *= 1.0f / sqrtf(block_sum(ss, part[0]) / static_cast<float>(p.H) + p.eps);
+  }
+  if (p.gate && p.gate_col == 0)
+    scale *= gate_value(load1(p.gate, p.gate_f32, row * p.gate_row), p.sigmoid);
+  float h[VPT][8], ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int c = c0 + i * step;
+    float u[8], g[8];
+    hr[i].get(h[i]);
+    if (c < p.H) {
+      if (p.y) {
+        yr[i].get(u);
+        if (p.gamma_post) {
+          if (VPT > 1) g1[i].load(p.gamma_post, c);
+          g1[i].get(g);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) u[j] *= g[j];
+        }
+        if (p.gate && p.gate_col != 0) {
+          if (VPT > 1) gt[i].load(p.gate, row * p.gate_row + c);
+          gt[i].get(g);
+          if (p.sigmoid) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) g[j] = gate_value(g[j], true);
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) u[j] *= g[j];
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[i][j] = fmaf(scale, u[j], p.res_scale * h[i][j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[i][j] *= p.res_scale;
+      }
+      if (p.h_out) put8<HF32>(p.h_out, row * p.ld_h_out + c, h[i]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss = fmaf(h[i][j], h[i][j], ss);
+    }
+  }
+  if (!p.n && !p.q) return;
+  const float r =
+      p.gamma_pre
+          ? 1.0f / sqrtf(block_sum(ss, part[1]) / static_cast<float>(p.H) + p.eps)
+          : 1.0f;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int c = c0 + i * step;
+    if (c < p.H) {
+      if (p.gamma_pre) {
+        float g[8];
+        if (VPT > 1) g2[i].load(p.gamma_pre, c);
+        g2[i].get(g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[i][j] *= g[j];
+      }
+      if (p.q) store_norm_codes(hw, p, row, c - hw.lane * 8, r, h[i]);
+      if (p.n) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[i][j] *= r;
+        put8<false>(p.n, row * p.ld_n + c, h[i]);
       }
     }
   }
 }
 
 template <typename Kernel, typename Params>
-cudaError_t launch_pdl(Kernel k, unsigned grid, unsigned block, cudaStream_t s, const Params& p) {
+cudaError_t launch_pdl(Kernel k, unsigned grid, unsigned block, size_t smem, cudaStream_t s,
+                       const Params& p) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -340,18 +536,30 @@ extern "C" int klt_quantize(const void* x, int32_t x_dtype, int64_t ld_x, int32_
   p.ld_q = ld_q;
   p.K = K;
   p.G = (K + 127) / 128;
-  p.items = static_cast<int64_t>(M) * p.G;
+  const int64_t items = static_cast<int64_t>(M) * p.G;
+  if (items > 0x7FFFFF00) return KLT_ERR_UNSUPPORTED;
+  p.items = static_cast<uint32_t>(items);
+  // i / G for i < 2^31 by multiplication: magic = ceil(2^(31 + l) / G), l = ceil(log2 G)
+  int l = 0;
+  while ((1ll << l) < p.G) ++l;
+  p.shift = 31 + l;
+  p.magic = static_cast<uint32_t>(((1ull << p.shift) + p.G - 1) / p.G);
   p.f32 = x_dtype == KLT_DT_F32;
   p.wide_x = wide(x, ld_x, esize(x_dtype), 16);
   p.wide_q = wide(q, ld_q, 1, 8);
-  // four groups per half warp hide the load latency once the groups fill the device
-  // anyway; below that one group each spreads them over more SMs
-  const bool many = p.items >= 4 * 16 * 152 * 4;
-  const int64_t blocks = (p.items + (many ? 64 : 16) - 1) / (many ? 64 : 16);
-  if (blocks > 0x7FFFFFFF) return KLT_ERR_UNSUPPORTED;
+  // vectors throughout, and enough groups to fill the device four times over: four per half
+  // warp, which hides the load latency; else one each, which spreads them over more SMs
+  const bool many = K % 128 == 0 && p.wide_x && p.wide_q && items >= 4 * 16 * 152 * 4;
+  const int64_t blocks = (items + (many ? 64 : 16) - 1) / (many ? 64 : 16);
+  const unsigned grid = static_cast<unsigned>(blocks);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = many ? launch_pdl(quant_kernel<4>, static_cast<unsigned>(blocks), 256, st, p)
-                             : launch_pdl(quant_kernel<1>, static_cast<unsigned>(blocks), 256, st, p);
+  cudaError_t e;
+  if (!many)
+    e = launch_pdl(quant_kernel, grid, 256, 0, st, p);
+  else if (p.f32)
+    e = launch_pdl(quant_vec_kernel<4, true>, grid, 256, 0, st, p);
+  else
+    e = launch_pdl(quant_vec_kernel<4, false>, grid, 256, 0, st, p);
   return e == cudaSuccess ? KLT_OK : KLT_ERR_CUDA;
 }
 
@@ -410,15 +618,39 @@ extern "C" int klt_block_norm(const klt_block_norm_args* a, void* stream) {
   p.wide_h_out = wide(a->h_out, a->ld_h_out, he, 16);
   p.wide_n = wide(a->n, a->ld_n, 2, 16);
   p.wide_q = wide(a->q, a->ld_q, 1, 8);
-  // one vector per thread while the row's vectors fit in a block, four above
-  const int vecs = (H + 7) / 8;
-  const int vpt = vecs <= 1024 ? 1 : 4;
-  const int threads = ((vecs + vpt - 1) / vpt + 31) / 32 * 32;
+  // few rows: one group per half warp, the shortest path through a row; many rows: more groups
+  // per half warp, so that several rows share an SM and their loads and reductions overlap
+  int vpt = M <= 2 * 152 ? 1 : 4;
+  while (p.G > vpt * (vpt == 1 ? 64 : 32)) vpt *= 2;
+  const int threads = ((p.G + vpt - 1) / vpt * 16 + 31) / 32 * 32;
+  const unsigned grid = static_cast<unsigned>(M);
+  // element-by-element rows pass through shared memory
+  const bool vectors = H % 128 == 0 && p.wide_h && (!p.y || p.wide_y) &&
+                       (!p.gate || p.gate_col != 1 || p.wide_gate) && p.wide_gpost &&
+                       p.wide_gpre && (!p.h_out || p.wide_h_out) && (!p.n || p.wide_n) &&
+                       (!p.q || p.wide_q);
+  const bool plain = (a->y && p.y_f32) || (a->gate && p.gate_col != 0 && (p.gate_col != 1 || p.gate_f32));
+  const size_t smem = vectors ? 0 : threads / 16 * 512;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (vpt == 1)
-    e = launch_pdl(norm_kernel<1>, static_cast<unsigned>(M), threads, st, p);
-  else
-    e = launch_pdl(norm_kernel<4>, static_cast<unsigned>(M), threads, st, p);
+  if (!vectors || plain) {
+    switch (vpt) {
+      case 1: e = launch_pdl(norm_kernel<1>, grid, threads, smem, st, p); break;
+      case 2: e = launch_pdl(norm_kernel<2>, grid, threads, smem, st, p); break;
+      default: e = launch_pdl(norm_kernel<4>, grid, threads, smem, st, p); break;
+    }
+  } else if (p.h_f32) {
+    switch (vpt) {
+      case 1: e = launch_pdl(norm_vec_kernel<1, true>, grid, threads, 0, st, p); break;
+      case 2: e = launch_pdl(norm_vec_kernel<2, true>, grid, threads, 0, st, p); break;
+      default: e = launch_pdl(norm_vec_kernel<4, true>, grid, threads, 0, st, p); break;
+    }
+  } else {
+    switch (vpt) {
+      case 1: e = launch_pdl(norm_vec_kernel<1, false>, grid, threads, 0, st, p); break;
+      case 2: e = launch_pdl(norm_vec_kernel<2, false>, grid, threads, 0, st, p); break;
+      default: e = launch_pdl(norm_vec_kernel<4, false>, grid, threads, 0, st, p); break;
+    }
+  }
   return e == cudaSuccess ? KLT_OK : KLT_ERR_CUDA;
 }

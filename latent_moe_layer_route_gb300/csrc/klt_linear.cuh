@@ -153,10 +153,18 @@ KLT_DEV float silu_rcp(float g) {
   return g * r;
 }
 
-// The scale of a quantised group from the bit pattern of its largest magnitude (a NaN is
-// above infinity, infinity above every number); a scale that is zero becomes 1.
-KLT_DEV float group_scale(uint32_t amax_bits) {
-  const float s = __uint_as_float(amax_bits) / 448.0f;
+// amax / 448, correctly rounded: the quotient by the rounded 1/448 corrected by its residual,
+// or by division where that would leave the normal range.
+KLT_DEV float over_448(float amax) {
+  if (amax > 1e-25f && amax < 1e38f) {
+    const float q0 = amax * (1.0f / 448.0f);
+    return fmaf(-fmaf(q0, 448.0f, -amax), 1.0f / 448.0f, q0);
+  }
+  return amax / 448.0f;
+}
+// The scale of a quantised group from its largest magnitude; a scale that is zero becomes 1.
+KLT_DEV float group_scale(float amax) {
+  const float s = over_448(amax);
   return s == 0.f ? 1.0f : s;
 }
 // quot_rn needs the scale, its reciprocal and the residual in the normal range.  Brings a scale
@@ -164,14 +172,23 @@ KLT_DEV float group_scale(uint32_t amax_bits) {
 // (exact as far as a code can tell) divided by the new scale have the same quotients.  A scale
 // that is not finite stays so and turns every code of its group into NaN.
 KLT_DEV float rescale(float& s) {
-  float k = 1.0f;
-  if (s < 1e-30f) k = 0x1p100f;
-  if (s > 1e30f) k = 0x1p-60f;
+  if (s > 1e-30f && s < 1e30f) return 1.0f;
+  const float k = s < 1.0f ? 0x1p100f : 0x1p-60f;
   s *= k;
   return k;
 }
-// fp32(x / s), correctly rounded, for s > 0 (the correction would turn -0 into 0).
-KLT_DEV float quot_group(float x, float s, float inv) { return copysignf(quot_rn(x, s, inv), x); }
+// fp32(x / s), correctly rounded, for s > 0 and inv = 1/s correctly rounded (Markstein's
+// correction, the residual taken as q0 s - x so that a zero keeps its sign).
+KLT_DEV float quot_group(float x, float s, float inv) {
+  const float q0 = x * inv;
+  return fmaf(-fmaf(q0, s, -x), inv, q0);
+}
+// The larger magnitude; a NaN wins over every number.
+KLT_DEV float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+  return r;
+}
 
 // ------------------------------------------------------------------ launches
 cudaError_t launch_linear_narrow(const CUtensorMap& tok, const LinParams& p, int bn, int split,

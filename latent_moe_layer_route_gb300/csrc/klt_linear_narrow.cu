@@ -268,15 +268,14 @@ __global__ void __launch_bounds__(THREADS)
         const float4 v = make_float4(silu_fast(g.x) * u.x, silu_fast(g.y) * u.y,
                                      silu_fast(g.z) * u.z, silu_fast(g.w) * u.w);
         if (p.out_dtype == KLT_DT_E4M3) {
-          // the warp holds one group of 128 columns; the magnitudes compare as bit patterns,
-          // where a NaN is largest
-          const uint32_t b0 = __float_as_uint(v.x) & 0x7FFFFFFFu;
-          const uint32_t b1 = __float_as_uint(v.y) & 0x7FFFFFFFu;
-          const uint32_t b2 = __float_as_uint(v.z) & 0x7FFFFFFFu;
-          const uint32_t b3 = __float_as_uint(v.w) & 0x7FFFFFFFu;
-          float s = group_scale(__reduce_max_sync(0xFFFFFFFFu, max(max(b0, b1), max(b2, b3))));
+          // the warp holds one group of 128 columns
+          float amax = max_nan(max_nan(v.x, v.y), max_nan(v.z, v.w));
+#pragma unroll
+          for (int o = 16; o; o >>= 1)
+            amax = max_nan(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+          float s = group_scale(amax);
           if (lane == 0) p.out_s[m * (p.width / 128) + rb] = s;
-          const float k = rescale(s), inv = 1.0f / s;
+          const float k = rescale(s), inv = __frcp_rn(s);
           const float q0 = quot_group(v.x * k, s, inv), q1 = quot_group(v.y * k, s, inv);
           const float q2 = quot_group(v.z * k, s, inv), q3 = quot_group(v.w * k, s, inv);
           const uint32_t codes = f32x2_to_e4m3x2(q0, q1) | (f32x2_to_e4m3x2(q2, q3) << 16);

@@ -32,7 +32,7 @@ static_assert(SMEM <= 232448, "shared memory of a block");
 
 struct Smem {
   uint8_t *ring, *stage;
-  uint32_t* amax;  // [2][128]
+  float* amax;  // [2][128]
   uint64_t *full, *done, *tempty, *drain;
   uint32_t* tmem_holder;
   volatile int* abort_flag;
@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   Smem sm;
   sm.ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   sm.stage = sm.ring + RING_BYTES;
-  sm.amax = reinterpret_cast<uint32_t*>(sm.stage + OUT_BYTES);
+  sm.amax = reinterpret_cast<float*>(sm.stage + OUT_BYTES);
   sm.full = reinterpret_cast<uint64_t*>(sm.stage + OUT_BYTES + AMAX_BYTES);
   sm.done = sm.full + STAGES;
   sm.tempty = sm.done + STAGES;
@@ -328,26 +328,26 @@ __global__ void __launch_bounds__(THREADS, 1)
       next_tile();
       if (tn < p.tiles_n) first_scales();
       if (ACT) {
-        uint32_t big = 0;
+        float big = 0.f;
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
           float g0, g1, u0, u1;
           unpack2(acc[0][i], g0, g1);
           unpack2(acc[1][i], u0, u1);
           const float a0 = silu_rcp(g0) * u0, a1 = silu_rcp(g1) * u1;
-          big = max(big, max(__float_as_uint(a0) & 0x7FFFFFFFu, __float_as_uint(a1) & 0x7FFFFFFFu));
+          big = max_nan(big, max_nan(a0, a1));
           acc[0][i] = pack2(a0, a1);
         }
         if (p.out_dtype == KLT_DT_E4M3) {
           // the group's other 64 columns are in the thread of the other half
           sm.amax[half * 128 + row] = big;
           named_bar_sync(1, 256);
-          big = max(big, sm.amax[(half ^ 1) * 128 + row]);
+          big = max_nan(big, sm.amax[(half ^ 1) * 128 + row]);
           named_bar_sync(1, 256);  // amax is free for the next tile
           float s = group_scale(big);
           if (ok && half == 0 && m < p.M)
             p.out_s[static_cast<int64_t>(m) * (p.width / 128) + tn0] = s;
-          const float k = rescale(s), inv = 1.0f / s;
+          const float k = rescale(s), inv = __frcp_rn(s);
           if (k != 1.0f) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
