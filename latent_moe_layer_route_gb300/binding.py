@@ -299,41 +299,73 @@ class LatentMoETail:
 
 
 # ---------------------------------------------------------------- operators around the tail
+#
+# The checks here are those that C cannot make of bare pointers: types, shapes, devices.  A
+# call costs about as much as its launch, so each tensor is looked at once.
 
-def _matrix(t, name: str, dtypes, rows: int, cols: int, device: int) -> int:
-    """Check one [rows, cols] operand (its columns contiguous); returns its row stride."""
+class _Types:
+    """torch and its dtypes, looked up on first use (this module imports without torch)."""
+    torch = None
+
+    @classmethod
+    def load(cls):
+        import torch
+        cls.bf16, cls.f32 = torch.bfloat16, torch.float32
+        cls.act = {torch.bfloat16: KLT_DT_BF16, torch.float32: KLT_DT_F32}
+        cls.codes = (torch.float8_e4m3fn, torch.uint8)
+        cls.raw_stream = torch._C._cuda_getCurrentRawStream
+        cls.current_device = torch._C._cuda_getDevice
+        cls.torch = torch
+
+
+def _refuse(t, name: str, dtypes, rows: int, cols: int, device: int, contiguous: bool):
+    """What is wrong with an operand that did not pass its check."""
     if t.dtype not in dtypes:
-        raise TypeError(f"{name}: dtype {t.dtype}, not one of {dtypes}")
+        raise TypeError(f"{name}: dtype {t.dtype}, not one of {tuple(dtypes)}")
     if tuple(t.shape) != (rows, cols):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, not {(rows, cols)}")
     if t.get_device() != device:
         raise ValueError(f"{name}: on {t.device}, not on CUDA device {device}")
-    ld, unit = t.stride()
-    if unit != 1 and cols > 1:
-        raise ValueError(f"{name}: columns are not contiguous")
+    raise ValueError(f"{name}: not contiguous" if contiguous else
+                     f"{name}: columns are not contiguous")
+
+
+def _rows(t, name: str, dtypes, rows: int, cols: int, device: int) -> int:
+    """Check a [rows, cols] operand whose columns are contiguous; returns its row stride."""
+    ld, unit = t.stride() if t.dim() == 2 else (0, 0)
+    if t.dtype not in dtypes or t.shape != (rows, cols) or t.get_device() != device or \
+            (unit != 1 and cols > 1):
+        _refuse(t, name, dtypes, rows, cols, device, False)
     return ld
 
 
 def _contiguous(t, name: str, dtypes, rows: int, cols: int, device: int):
-    if _matrix(t, name, dtypes, rows, cols, device) != cols and rows > 1:
-        raise ValueError(f"{name}: not contiguous")
+    if t.dtype not in dtypes or t.shape != (rows, cols) or t.get_device() != device or \
+            not t.is_contiguous():
+        _refuse(t, name, dtypes, rows, cols, device, True)
 
 
 def _device_of(t, name: str) -> int:
+    if _Types.torch is None:
+        _Types.load()
     if not t.is_cuda:
         raise ValueError(f"{name}: not a CUDA tensor")
     return t.get_device()
 
 
-def _on_device(device: int, stream, call):
-    """call(stream) with `device` current; stream None = the current stream of `device`."""
-    import torch
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(device)
-    if torch._C._cuda_getDevice() == device:
-        return call(stream)
-    with torch.cuda.device(device):
-        return call(stream)
+class _On:
+    """Makes `device` current for one call where another one is."""
+
+    def __init__(self, device: int):
+        self.guard = _Types.torch.cuda.device(device)
+
+    def __call__(self, fn, *args):
+        with self.guard:
+            return fn(*args)
+
+
+def _direct(fn, *args):
+    return fn(*args)
 
 
 def fp8_codes(M: int, K: int, device):
@@ -344,38 +376,27 @@ def fp8_codes(M: int, K: int, device):
     return wide[:, :K]
 
 
-_TORCH: Dict = {}
-
-
-def _dtypes() -> Dict:
-    if not _TORCH:
-        import torch
-        _TORCH.update(act=(torch.bfloat16, torch.float32), bf16=(torch.bfloat16,),
-                      f32=(torch.float32,), codes=(torch.float8_e4m3fn, torch.uint8),
-                      code=torch.float8_e4m3fn,
-                      of={torch.bfloat16: KLT_DT_BF16, torch.float32: KLT_DT_F32})
-    return _TORCH
-
-
 def quantize_fp8(x, q=None, s=None, stream: Optional[int] = None):
     """e4m3 codes q [M, K] and fp32 scales s [M, ceil(K/128)] of x [M, K] (bf16 or fp32; rows
     may be strided) per row and 128 columns (klt_quantize)."""
-    import torch
-    dt = _dtypes()
+    T = _Types
     dev = _device_of(x, "x")
     if x.dim() != 2:
         raise ValueError("x: not a matrix")
     M, K = x.shape
-    ld = _matrix(x, "x", dt["act"], M, K, dev)
+    G = -(-K // 128)
+    ld = _rows(x, "x", T.act, M, K, dev)
     if q is None:
         q = fp8_codes(M, K, x.device)
     if s is None:
-        s = torch.empty((M, -(-K // 128)), dtype=torch.float32, device=x.device)
-    ld_q = _matrix(q, "q", dt["codes"], M, K, dev)
-    _contiguous(s, "s", dt["f32"], M, -(-K // 128), dev)
-    lib = _LIB or load_library()
-    rc = _on_device(dev, stream, lambda st: lib.klt_quantize(
-        x.data_ptr(), dt["of"][x.dtype], ld, M, K, q.data_ptr(), ld_q, s.data_ptr(), st))
+        s = T.torch.empty((M, G), dtype=T.f32, device=x.device)
+    ld_q = _rows(q, "q", T.codes, M, K, dev)
+    _contiguous(s, "s", (T.f32,), M, G, dev)
+    if stream is None:
+        stream = T.raw_stream(dev)
+    call = _direct if T.current_device() == dev else _On(dev)
+    rc = call((_LIB or load_library()).klt_quantize, x.data_ptr(), T.act[x.dtype], ld, M, K,
+              q.data_ptr(), ld_q, s.data_ptr(), stream)
     if rc != KLT_OK:
         raise KltError(rc, "klt_quantize")
     return q, s
@@ -390,7 +411,6 @@ class BlockNorm:
     def __init__(self, H: int, gamma_post=None, gamma_pre=None, eps: float = 1e-6,
                  res_scale: float = 1.0, branch_scale: float = 1.0,
                  gate_sigmoid: bool = False):
-        dt = _dtypes()
         self.H = H
         self.gamma_post, self.gamma_pre = gamma_post, gamma_pre
         self.device = None
@@ -398,7 +418,7 @@ class BlockNorm:
             if g is None:
                 continue
             dev = _device_of(g, name)
-            if g.dtype not in dt["bf16"] or tuple(g.shape) != (H,) or not g.is_contiguous():
+            if g.dtype != _Types.bf16 or tuple(g.shape) != (H,) or not g.is_contiguous():
                 raise ValueError(f"{name}: not a contiguous bf16 vector of {H}")
             if self.device is not None and dev != self.device:
                 raise ValueError("gamma_post and gamma_pre are on different devices")
@@ -415,51 +435,50 @@ class BlockNorm:
         dtype; may be h), n (bf16; may be y), q and s (e4m3 codes and fp32 scales of n);
         when none is given, h_out (with y) and n are allocated.  Without y the norm after
         the block is skipped.  Returns (h_out, n, q, s)."""
-        import torch
-        dt = _dtypes()
-        of = dt["of"]
+        T = _Types
         dev = _device_of(h, "h")
         if self.device is not None and dev != self.device:
             raise ValueError("h: not on the weights' device")
         M, H = h.shape[0], self.H
         a = KltBlockNormArgs.from_buffer_copy(self._args)
         a.M = M
-        a.ld_h = _matrix(h, "h", dt["act"], M, H, dev)
-        a.h_dtype = of[h.dtype]
+        a.ld_h = _rows(h, "h", T.act, M, H, dev)
+        a.h_dtype = T.act[h.dtype]
         a.h = h.data_ptr()
         if h_out is None and n is None and q is None and s is None:
             if y is not None:
-                h_out = torch.empty((M, H), dtype=h.dtype, device=h.device)
-            n = torch.empty((M, H), dtype=torch.bfloat16, device=h.device)
+                h_out = T.torch.empty((M, H), dtype=h.dtype, device=h.device)
+            n = T.torch.empty((M, H), dtype=T.bf16, device=h.device)
         if y is not None:
-            a.ld_y = _matrix(y, "y", dt["act"], M, H, dev)
-            a.y_dtype = of[y.dtype]
+            a.ld_y = _rows(y, "y", T.act, M, H, dev)
+            a.y_dtype = T.act[y.dtype]
             a.y = y.data_ptr()
             if gate is not None:
-                if gate.dtype not in dt["act"] or gate.get_device() != dev:
+                if gate.dtype not in T.act or gate.get_device() != dev:
                     raise ValueError("gate: not a bf16 or fp32 tensor on h's device")
-                g = gate.expand(M, H)
-                a.gate_row, a.gate_col = g.stride()
-                a.gate_dtype = of[gate.dtype]
+                a.gate_row, a.gate_col = gate.expand(M, H).stride()
+                a.gate_dtype = T.act[gate.dtype]
                 a.gate = gate.data_ptr()
         else:
             if gate is not None:
                 raise ValueError("gate: given without y")
             a.gamma_post = None
         if h_out is not None:
-            a.ld_h_out = _matrix(h_out, "h_out", (h.dtype,), M, H, dev)
+            a.ld_h_out = _rows(h_out, "h_out", (h.dtype,), M, H, dev)
             a.h_out = h_out.data_ptr()
         if n is not None:
-            a.ld_n = _matrix(n, "n", dt["bf16"], M, H, dev)
+            a.ld_n = _rows(n, "n", (T.bf16,), M, H, dev)
             a.n = n.data_ptr()
         if q is not None:
-            a.ld_q = _matrix(q, "q", dt["codes"], M, H, dev)
+            a.ld_q = _rows(q, "q", T.codes, M, H, dev)
             a.q = q.data_ptr()
         if s is not None:
-            _contiguous(s, "s", dt["f32"], M, -(-H // 128), dev)
+            _contiguous(s, "s", (T.f32,), M, -(-H // 128), dev)
             a.s = s.data_ptr()
-        lib = self._lib
-        rc = _on_device(dev, stream, lambda st: lib.klt_block_norm(a, st))
+        if stream is None:
+            stream = T.raw_stream(dev)
+        call = _direct if T.current_device() == dev else _On(dev)
+        rc = call(self._lib.klt_block_norm, a, stream)
         if rc != KLT_OK:
             raise KltError(rc, "klt_block_norm")
         return h_out, n, q, s
@@ -475,8 +494,7 @@ class Fp8Linear:
     "swiglu" (gate rows first; N/2 outputs); out "bf16", "f32" or, for SwiGLU, "fp8"."""
 
     def __init__(self, w_q, w_s, act: str = "none", out: str = "bf16"):
-        import torch
-        dt = _dtypes()
+        T = _Types
         self.handle = None
         acts = {"none": KLT_ACT_NONE, "swiglu": KLT_ACT_SWIGLU}
         outs = {"bf16": KLT_DT_BF16, "f32": KLT_DT_F32, "fp8": KLT_DT_E4M3}
@@ -486,18 +504,20 @@ class Fp8Linear:
         if w_q.dim() != 2:
             raise ValueError("w_q: not a matrix")
         self.N, self.K = w_q.shape
-        _contiguous(w_q, "w_q", dt["codes"], self.N, self.K, self.device)
-        _contiguous(w_s, "w_s", dt["f32"], -(-self.N // 128), -(-self.K // 128), self.device)
+        _contiguous(w_q, "w_q", T.codes, self.N, self.K, self.device)
+        self._groups = -(-self.K // 128)
+        _contiguous(w_s, "w_s", (T.f32,), -(-self.N // 128), self._groups, self.device)
         self.width = self.N // 2 if act == "swiglu" else self.N
         self.fp8 = out == "fp8"
-        self._out = dt["codes"] if self.fp8 else dt["f32"] if out == "f32" else dt["bf16"]
+        self._f32 = (T.f32,)
+        self._out = T.codes if self.fp8 else (T.f32,) if out == "f32" else (T.bf16,)
         self._lib = load_library()
         d = KltLinearDims(self.N, self.K, acts[act], outs[out])
         h = ctypes.c_void_p()
         # the create copies on the legacy default stream; what wrote the weights may have run
         # on another
-        torch.cuda.current_stream(self.device).synchronize()
-        with torch.cuda.device(self.device):
+        T.torch.cuda.current_stream(self.device).synchronize()
+        with T.torch.cuda.device(self.device):
             rc = self._lib.klt_linear_create(ctypes.byref(d), w_q.data_ptr(), w_s.data_ptr(),
                                              ctypes.byref(h))
         if rc != KLT_OK:
@@ -508,26 +528,28 @@ class Fp8Linear:
                 debug: Optional[KltLinearDebug] = None):
         """xq e4m3 (or uint8) [M, K] whose rows start on 16 bytes, xs fp32 [M, ceil(K/128)].
         Returns out [M, N] (SwiGLU: [M, N/2]), or (codes, scales) with out "fp8"."""
-        import torch
-        dt = _dtypes()
+        T = _Types
         dev = self.device
         M, K, width = xq.shape[0], self.K, self.width
-        ld = _matrix(xq, "xq", dt["codes"], M, K, dev)
+        ld = _rows(xq, "xq", T.codes, M, K, dev)
         if M <= 1:  # the stride of a single row says nothing
             ld = -(-K // 16) * 16
-        _contiguous(xs, "xs", dt["f32"], M, -(-K // 128), dev)
+        _contiguous(xs, "xs", self._f32, M, self._groups, dev)
         if out is None:
             out = fp8_codes(M, width, xq.device) if self.fp8 else \
-                torch.empty((M, width), dtype=self._out[0], device=xq.device)
-        ld_out = _matrix(out, "out", self._out, M, width, dev)
+                T.torch.empty((M, width), dtype=self._out[0], device=xq.device)
+        ld_out = _rows(out, "out", self._out, M, width, dev)
+        scales = None
         if self.fp8:
             if out_s is None:
-                out_s = torch.empty((M, width // 128), dtype=torch.float32, device=xq.device)
-            _contiguous(out_s, "out_s", dt["f32"], M, width // 128, dev)
-        lib = self._lib
-        rc = _on_device(dev, stream, lambda st: lib.klt_linear_forward(
-            self.handle, xq.data_ptr(), ld, xs.data_ptr(), M, out.data_ptr(), ld_out,
-            out_s.data_ptr() if self.fp8 else None, debug, st))
+                out_s = T.torch.empty((M, width // 128), dtype=T.f32, device=xq.device)
+            _contiguous(out_s, "out_s", self._f32, M, width // 128, dev)
+            scales = out_s.data_ptr()
+        if stream is None:
+            stream = T.raw_stream(dev)
+        call = _direct if T.current_device() == dev else _On(dev)
+        rc = call(self._lib.klt_linear_forward, self.handle, xq.data_ptr(), ld, xs.data_ptr(), M,
+                  out.data_ptr(), ld_out, scales, debug, stream)
         if rc != KLT_OK:
             raise KltError(rc, "klt_linear_forward")
         return (out, out_s) if self.fp8 else out

@@ -142,7 +142,7 @@ int klt_linear_create(const klt_linear_dims* d, const void* w, const float* w_sc
   if (cudaGetDeviceProperties(&prop, dev) != cudaSuccess) return KLT_ERR_CUDA;
   if (prop.major != 10 || prop.minor != 3) return KLT_ERR_UNSUPPORTED;
   if (!get_encode()) return KLT_ERR_CUDA;
-  if (!linear_wide_regs_ok()) return KLT_ERR_UNSUPPORTED;
+  if (!prepare_linear_narrow() || !prepare_linear_wide()) return KLT_ERR_UNSUPPORTED;
 
   klt_linear* h = new (std::nothrow) klt_linear();
   if (!h) return KLT_ERR_OOM;

@@ -196,6 +196,9 @@ cudaError_t launch_linear_narrow(const CUtensorMap& tok, const LinParams& p, int
 cudaError_t launch_linear_wide(const CUtensorMap& tok, const CUtensorMap& wmap,
                                const CUtensorMap& omap, const LinParams& p, bool swiglu,
                                int num_sms, cudaStream_t s);
-bool linear_wide_regs_ok();
+// Once per device, before the first launch: shared-memory sizes, and whether the kernels are
+// what their launches expect.
+bool prepare_linear_narrow();
+bool prepare_linear_wide();
 
 }  // namespace klt

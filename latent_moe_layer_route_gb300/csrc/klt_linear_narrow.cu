@@ -309,12 +309,16 @@ __global__ void __launch_bounds__(THREADS)
 }
 
 template <int BN, int ACT>
-cudaError_t launch(const CUtensorMap& tok, const LinParams& p, int split, cudaStream_t s) {
+bool prepare() {
   using C = Narrow<BN, ACT>;
   static_assert(C::SMEM <= 232448, "shared memory of a block");
-  cudaError_t e = cudaFuncSetAttribute(narrow_kernel<BN, ACT>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(narrow_kernel<BN, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              C::SMEM) == cudaSuccess;
+}
+
+template <int BN, int ACT>
+cudaError_t launch(const CUtensorMap& tok, const LinParams& p, int split, cudaStream_t s) {
+  using C = Narrow<BN, ACT>;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(split, (p.M + BN - 1) / BN, ACT ? p.width / 128 : p.NB);
   cfg.blockDim = dim3(THREADS);
@@ -333,6 +337,11 @@ cudaError_t launch(const CUtensorMap& tok, const LinParams& p, int split, cudaSt
 }
 
 }  // namespace
+
+bool prepare_linear_narrow() {
+  return prepare<16, 0>() && prepare<32, 0>() && prepare<64, 0>() && prepare<128, 0>() &&
+         prepare<16, 1>() && prepare<32, 1>() && prepare<64, 1>();
+}
 
 cudaError_t launch_linear_narrow(const CUtensorMap& tok, const LinParams& p, int bn, int split,
                                  bool swiglu, cudaStream_t s) {

@@ -401,9 +401,6 @@ __global__ void __launch_bounds__(THREADS, 1)
 template <int ACT>
 cudaError_t launch(const CUtensorMap& tok, const CUtensorMap& wmap, const CUtensorMap& omap,
                    LinParams p, int num_sms, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(wide_kernel<ACT>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-  if (e != cudaSuccess) return e;
   p.tiles_m = (p.M + 255) / 256;
   p.tiles_n = ACT ? p.width / 128 : (p.NB + 1) / 2;
   const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
@@ -430,11 +427,15 @@ cudaError_t launch(const CUtensorMap& tok, const CUtensorMap& wmap, const CUtens
 
 }  // namespace
 
-bool linear_wide_regs_ok() {
-  // setmaxnreg moves registers between the warpgroups: 56 + 2 x 224 = 3 x 168 at launch
-  cudaFuncAttributes a;
-  return cudaFuncGetAttributes(&a, wide_kernel<0>) == cudaSuccess && a.numRegs >= 168 &&
-         cudaFuncGetAttributes(&a, wide_kernel<1>) == cudaSuccess && a.numRegs >= 168;
+bool prepare_linear_wide() {
+  for (auto k : {wide_kernel<0>, wide_kernel<1>}) {
+    // setmaxnreg moves registers between the warpgroups: 56 + 2 x 224 = 3 x 168 at launch
+    cudaFuncAttributes a;
+    if (cudaFuncGetAttributes(&a, k) != cudaSuccess || a.numRegs < 168 ||
+        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) != cudaSuccess)
+      return false;
+  }
+  return true;
 }
 
 cudaError_t launch_linear_wide(const CUtensorMap& tok, const CUtensorMap& wmap,
