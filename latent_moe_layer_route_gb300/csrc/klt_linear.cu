@@ -118,10 +118,12 @@ void choose(const klt_linear* h, int M, int* tile, int* split) {
   int bn = 16;
   while (bn < M && bn < most) bn *= 2;
   *tile = bn;
-  // as many parts of K as keep every CTA resident at once, each with two k-blocks or more
-  const int resident = (bn == 16 && !act ? 3 : bn <= 32 || (bn == 64 && !act) ? 2 : 1) * h->num_sms;
+  // Parts of K while the CTAs stay below 256, about 1.7 per SM (one per SM for the tiles that
+  // run alone on theirs): all resident at once, with room for the first CTAs of the next launch
+  const bool alone = act ? bn == 64 : bn == 128;
   const int64_t units = static_cast<int64_t>(units_n) * ((M + bn - 1) / bn);
-  while (*split < 8 && units * *split * 2 <= resident && h->KB >= *split * 4) *split *= 2;
+  while (*split < 8 && units * *split * 2 <= (alone ? 152 : 256) && h->KB >= *split * 2)
+    *split *= 2;
 }
 
 }  // namespace

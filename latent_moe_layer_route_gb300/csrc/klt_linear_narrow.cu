@@ -1,15 +1,18 @@
 // FP8 linear layer, feature-major kernel: few tokens (sm_103a).
 //
 // A CTA multiplies 128 weight rows (SwiGLU: 128 gate and the 128 matching up rows) by one
-// tile of BN tokens over a part of K; the CTAs of a cluster share K and add their parts
-// through distributed shared memory in rank order, so there is no workspace, no atomic and
-// the result does not depend on timing.  At these sizes the weight stream is the cost: the
+// tile of BN tokens over a part of K; the CTAs of a cluster share K, store their parts into the
+// shared memory of the CTA that finishes a token (asynchronous stores that complete on its
+// barrier), and that one adds them in rank order, so there is no workspace, no atomic and the
+// result does not depend on timing.  At these sizes the weight stream is the cost: the
 // weights are the MMA's M side (128 rows per instruction however few the tokens are), every
 // tile is one contiguous bulk copy, and the copies of the first stages start before the
 // wait for the kernel that writes the activations.
 //
 // The scales are general fp32 per 128 columns, so each k-block's product is read from TMEM
-// and added into registers times xs[t, kb] * ws[rb, kb] (staged in shared memory).
+// and added into registers times xs[t, kb] * ws[rb, kb] (staged in shared memory).  Eight warps
+// do so from 32 columns on: with four, 128 columns took 1600 cycles per k-block, six times
+// their multiplication.
 #include "klt_linear.cuh"
 
 #include "../../include/klt.h"
@@ -17,23 +20,28 @@
 namespace klt {
 namespace {
 
-constexpr int THREADS = 192;  // warps 0-3 epilogue (one per TMEM quadrant), 4 copies, 5 MMA
-constexpr int SCALE_KB = 16;  // k-blocks whose scales are staged at once
-
 template <int BN, int ACT>
 struct Narrow {
   static constexpr int AT = ACT ? 2 : 1;  // weight tiles per k-block
   static constexpr int STAGE_BYTES = AT * LIN_TILE_BYTES + BN * 128;
-  // the ring also holds the CTA's fp32 partial result once the products are done
-  static constexpr int PART_BYTES = AT * BN * 128 * 4;
-  static constexpr int STAGES = ACT && BN < 64 ? 3 : 4;
-  static constexpr int RING_BYTES =
-      STAGES * STAGE_BYTES > PART_BYTES ? STAGES * STAGE_BYTES : PART_BYTES;
-  static constexpr int SLOTS = BN >= 128 ? 2 : 4;
-  static constexpr int SLOT_COLS = AT * BN;
-  static constexpr int TMEM_COLS = SLOTS * SLOT_COLS;  // a power of two, 64 .. 512
-  static constexpr int SCALE_BYTES = AT * SCALE_KB * BN * 4;
-  static constexpr int SMEM = 1024 + RING_BYTES + SCALE_BYTES + 256;
+  static constexpr int SLOTS = 4;  // with two, 128 tokens took 652 cycles per k-block
+  static constexpr int COLS = AT * BN;  // columns of a slot: token t of tile a at a * BN + t
+  static constexpr int TMEM_COLS = SLOTS * COLS;  // a power of two, 64 .. 512
+  // warps: epilogue (two per TMEM quadrant, half of the columns each, from 32 columns on),
+  // then copies, then MMA
+  static constexpr int EPI = COLS >= 32 ? 8 : 4;
+  static constexpr int THREADS = (EPI + 2) * 32;
+  static constexpr int WC = COLS * 4 / EPI;         // columns of a warp
+  static constexpr int CHUNK = WC >= 32 ? 32 : 16;  // loaded at a time
+  // as many stages as leave room for two CTAs per SM, so that the next launch's CTAs are
+  // resident and copy weights while this one's finish; the largest tiles run alone
+  static constexpr int STAGES = ACT ? (BN < 64 ? 2 : 3) : (BN == 64 ? 3 : 4);
+  static constexpr int RING_BYTES = STAGES * STAGE_BYTES;
+  static constexpr int PART_BYTES = COLS * 128 * 4;  // all parts of the tokens finished here
+  static constexpr int SCALE_KB = BN == 128 ? 32 : 16;  // k-blocks of scales staged at once
+  static constexpr int SCALE_LD = COLS + 4;             // floats per k-block of scales
+  static constexpr int SCALE_BYTES = SCALE_KB * SCALE_LD * 4;
+  static constexpr int SMEM = 1024 + RING_BYTES + PART_BYTES + SCALE_BYTES + 256;
 };
 
 // Writes four neighbouring outputs (columns c .. c+3) of row m.
@@ -66,27 +74,35 @@ KLT_DEV void store4(const LinParams& p, int64_t m, int c, float4 v) {
 
 // grid (split, token tiles, row blocks), cluster (split, 1, 1)
 template <int BN, int ACT>
-__global__ void __launch_bounds__(THREADS)
+__global__ void __launch_bounds__(Narrow<BN, ACT>::THREADS)
     narrow_kernel(const __grid_constant__ CUtensorMap tok, const LinParams p) {
   using C = Narrow<BN, ACT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  float* scales = reinterpret_cast<float*>(ring + C::RING_BYTES);  // [AT][SCALE_KB][BN]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(ring + C::RING_BYTES + C::SCALE_BYTES);
+  // [tokens finished here][weight tile][rank][128 rows]
+  float* parts = reinterpret_cast<float*>(ring + C::RING_BYTES);
+  float* scales = reinterpret_cast<float*>(ring + C::RING_BYTES + C::PART_BYTES);
+  uint64_t* bars =
+      reinterpret_cast<uint64_t*>(ring + C::RING_BYTES + C::PART_BYTES + C::SCALE_BYTES);
   uint64_t* full = bars;
   uint64_t* empty = full + C::STAGES;
   uint64_t* tfull = empty + C::STAGES;
   uint64_t* tempty = tfull + C::SLOTS;
   uint64_t* drain = tempty + C::SLOTS;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* got = drain + 1;  // the other CTAs' parts have arrived
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(got + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
-  static_assert((2 * C::STAGES + 2 * C::SLOTS + 1) * 8 + 8 <= 256, "barrier space");
+  static_assert((2 * C::STAGES + 2 * C::SLOTS + 2) * 8 + 8 <= 256, "barrier space");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = gridDim.x, rank = blockIdx.x;
   const int t0 = blockIdx.y * BN, rb = blockIdx.z;
   const int k0 = static_cast<int>(static_cast<int64_t>(p.KB) * rank / split);
   const int nk = static_cast<int>(static_cast<int64_t>(p.KB) * (rank + 1) / split) - k0;
+  // tokens rank, rank + split, ... of the tile are this CTA's to finish
+  const int tokens = p.M - t0 < BN ? p.M - t0 : BN;
+  const int log_split = __ffs(split) - 1;
+  const int mine = (tokens - rank + split - 1) >> log_split;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
@@ -95,29 +111,26 @@ __global__ void __launch_bounds__(THREADS)
     }
     for (int i = 0; i < C::SLOTS; ++i) {
       mbar_init(&tfull[i], 1);
-      mbar_init(&tempty[i], 4);
+      mbar_init(&tempty[i], C::EPI);
     }
     mbar_init(drain, 1);
+    mbar_init(got, 1);
     *abort_flag = 0;
     fence_barrier_init();
+    mbar_arrive_expect_tx(got, mine * C::AT * (split - 1) * 512);
   }
-  if (warp == 5) {
+  if (warp == C::EPI + 1) {
     tmem_alloc(tmem_holder, C::TMEM_COLS);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
+  cluster_arrive_relaxed();  // this CTA's barriers exist: waited for before storing to another
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   pdl_trigger();  // this CTA holds its TMEM: a dependent's CTAs cannot take it away
 
-  float acc[C::AT][BN];
-#pragma unroll
-  for (int a = 0; a < C::AT; ++a)
-#pragma unroll
-    for (int t = 0; t < BN; ++t) acc[a][t] = 0.f;
-
-  if (warp == 4) {
+  if (warp == C::EPI) {
     if (lane == 0) {
       const uint64_t pol = gridDim.y > 1 ? policy_evict_normal() : policy_evict_first();
       const uint64_t keep = policy_evict_normal();
@@ -152,7 +165,7 @@ __global__ void __launch_bounds__(THREADS)
         mbar_wait(&full[j % C::STAGES], (j / C::STAGES) & 1, &none, p.err, p.timeout);
     }
     __syncwarp();
-  } else if (warp == 5) {
+  } else if (warp == C::EPI + 1) {
     if (lane == 0) {
       constexpr uint32_t idesc = idesc_make(0, 128, BN);
       int i = 0;
@@ -167,7 +180,7 @@ __global__ void __launch_bounds__(THREADS)
         const uint64_t db = sdesc_sw128(base + C::AT * LIN_TILE_BYTES);
 #pragma unroll
         for (int a = 0; a < C::AT; ++a)
-          mma4_fp8(tmem + slot * C::SLOT_COLS + a * BN, sdesc_sw128(base + a * LIN_TILE_BYTES),
+          mma4_fp8(tmem + slot * C::COLS + a * BN, sdesc_sw128(base + a * LIN_TILE_BYTES),
                    db, idesc, 0);
         tc_commit(&empty[st]);
         tc_commit(&tfull[slot]);
@@ -178,88 +191,140 @@ __global__ void __launch_bounds__(THREADS)
     }
     __syncwarp();
   } else {
+    const int row = (warp & 3) * 32 + lane, col = (warp >> 2) * C::WC;
+    // scales of the k-blocks from i on: neighbouring lanes = k-blocks.  Those of the weights
+    // are nobody's output and do not wait for the launch before
+    constexpr int TW = 32 / C::SCALE_KB;  // tokens of a warp at a time
+    const int skb = lane % C::SCALE_KB, st0 = warp * TW + lane / C::SCALE_KB;
+    float w[C::AT];
+    auto weight_scales = [&](int i) {
+#pragma unroll
+      for (int a = 0; a < C::AT; ++a)
+        w[a] = i + skb < nk ? p.ws[static_cast<int64_t>(rb + a * p.up) * p.KB + k0 + i + skb]
+                            : 0.f;
+    };
+    auto stage_scales = [&](int i) {
+      constexpr int STEP = C::EPI * TW;
+      float x[BN / STEP];
+#pragma unroll
+      for (int j = 0; j < BN / STEP; ++j) {
+        const int t = st0 + j * STEP;
+        x[j] = i + skb < nk && t < tokens
+                   ? p.xs[static_cast<int64_t>(t0 + t) * p.KB + k0 + i + skb]
+                   : 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < BN / STEP; ++j)
+#pragma unroll
+        for (int a = 0; a < C::AT; ++a)
+          scales[skb * C::SCALE_LD + a * BN + st0 + j * STEP] = x[j] * w[a];
+    };
+    weight_scales(0);
     pdl_wait();
-    const int row = warp * 32 + lane;
+    stage_scales(0);
+    named_bar_sync(1, C::EPI * 32);
+    unsigned long long acc[C::WC / 2];
+#pragma unroll
+    for (int i = 0; i < C::WC / 2; ++i) acc[i] = 0ull;
     bool ok = true;  // of the whole warp; a warp that gave up still meets the others' barriers
     for (int i = 0; i < nk; ++i) {
-      if (i % SCALE_KB == 0) {
-        // xs[t, kb] * ws[rb, kb] of the next k-blocks, once per CTA
-        const int cnt = nk - i < SCALE_KB ? nk - i : SCALE_KB;
-        named_bar_sync(1, 128);
-        for (int e = row; e < BN * SCALE_KB; e += 128) {
-          const int t = e / SCALE_KB, kb = e % SCALE_KB;
-          if (kb < cnt) {
-            const int64_t m = t0 + t;
-            const float x = m < p.M ? p.xs[m * p.KB + k0 + i + kb] : 0.f;
-#pragma unroll
-            for (int a = 0; a < C::AT; ++a)
-              scales[(a * SCALE_KB + kb) * BN + t] =
-                  x * p.ws[static_cast<int64_t>(rb + a * p.up) * p.KB + k0 + i + kb];
-          }
-        }
-        named_bar_sync(1, 128);
+      if (i > 0 && i % C::SCALE_KB == 0) {
+        weight_scales(i);
+        named_bar_sync(1, C::EPI * 32);
+        stage_scales(i);
+        named_bar_sync(1, C::EPI * 32);
       }
       const int slot = i % C::SLOTS;
       ok = ok && mbar_wait_spin(&tfull[slot], (i / C::SLOTS) & 1, abort_flag, p.err, p.timeout);
       ok = __all_sync(0xFFFFFFFFu, ok);
       if (!ok) continue;
       tc_fence_after();
-      const uint32_t ta = tmem + (static_cast<uint32_t>(warp * 32) << 16) + slot * C::SLOT_COLS;
-      const float* sc = scales + (i % SCALE_KB) * BN;
+      const uint32_t ta =
+          tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + slot * C::COLS + col;
+      const ulonglong2* sc =
+          reinterpret_cast<const ulonglong2*>(scales + (i % C::SCALE_KB) * C::SCALE_LD + col);
+      // each load is started before the products of the one before it
+      uint32_t v[2][C::CHUNK];
+      auto start = [&](int c) {
+        if (C::CHUNK == 32)
+          tmem_start_ld32(ta + c * 32, v[c & 1]);
+        else
+          tmem_start_ld16(ta + c * 16, v[c & 1]);
+      };
+      start(0);
 #pragma unroll
-      for (int a = 0; a < C::AT; ++a)
-#pragma unroll
-        for (int c = 0; c < BN; c += 16) {
-          float v[16];
-          tmem_ld16(ta + a * BN + c, v);
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            acc[a][c + j] = fmaf(v[j], sc[a * SCALE_KB * BN + c + j], acc[a][c + j]);
+      for (int c = 0; c < C::WC / C::CHUNK; ++c) {
+        uint32_t* r = v[c & 1];
+        if (C::CHUNK == 32)
+          tmem_wait_ld32(r);
+        else
+          tmem_wait_ld16(r);
+        if (c + 1 < C::WC / C::CHUNK) {
+          start(c + 1);
+        } else {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tempty[slot]);
         }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&tempty[slot]);
-    }
-    // every product of this CTA is in registers (the last slot's barrier follows all MMAs),
-    // so the ring is free for the partial result, [a][token][row]
-    if (ok) {
-      float* part = reinterpret_cast<float*>(ring);
 #pragma unroll
-      for (int a = 0; a < C::AT; ++a)
-#pragma unroll
-        for (int t = 0; t < BN; ++t)
-          if (t0 + t < p.M) part[(a * BN + t) * 128 + row] = acc[a][t];
+        for (int e = 0; e < C::CHUNK / 4; ++e) {
+          const ulonglong2 f = sc[c * (C::CHUNK / 4) + e];
+          unsigned long long* a = acc + c * (C::CHUNK / 2) + 2 * e;
+          fma2(a[0], pack2(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1])), f.x);
+          fma2(a[1], pack2(__uint_as_float(r[4 * e + 2]), __uint_as_float(r[4 * e + 3])), f.y);
+        }
+      }
     }
-  }
-
-  if (split > 1) {
-    cluster_arrive();
+    // This CTA's part to the CTAs that finish its tokens (after a wait that ran out too: they
+    // count on it).  Four columns of four neighbouring lanes are transposed, so that a lane
+    // stores four neighbouring rows of one token.
     cluster_wait();
-  } else {
-    __syncthreads();
-  }
-  if (warp < 4 && !*abort_flag) {
-    // tokens rank, rank + split, ... of the tile are this CTA's to finish: one warp per
-    // token, four rows per lane, the parts added in rank order
-    const int tokens = p.M - t0 < BN ? p.M - t0 : BN;
-    const uint32_t part = smem_u32(ring) + lane * 16;
-    for (int t = rank + warp * split; t < tokens; t += 4 * split) {
+    const uint32_t bar = smem_u32(got);
+    const bool odd = lane & 1, high = lane & 2;
+#pragma unroll
+    for (int i = 0; i < C::WC; i += 4) {
+      float v0, v1, v2, v3;
+      unpack2(acc[i / 2], v0, v1);
+      unpack2(acc[i / 2 + 1], v2, v3);
+      const float a = __shfl_xor_sync(0xFFFFFFFFu, odd ? v0 : v1, 1);
+      const float b = __shfl_xor_sync(0xFFFFFFFFu, odd ? v2 : v3, 1);
+      (odd ? v0 : v1) = a;
+      (odd ? v2 : v3) = b;
+      const float c = __shfl_xor_sync(0xFFFFFFFFu, high ? v0 : v2, 2);
+      const float e = __shfl_xor_sync(0xFFFFFFFFu, high ? v1 : v3, 2);
+      (high ? v0 : v2) = c;
+      (high ? v1 : v3) = e;
+      const int t = (col + i) % BN + (lane & 3), tile = (col + i) / BN;
+      if (t < tokens) {
+        const int owner = t & (split - 1);
+        const int part = (((t >> log_split) * C::AT + tile) << log_split) + rank;
+        float* dst = parts + part * 128 + (row & ~31) + (lane >> 2) * 4;
+        if (owner == rank)
+          *reinterpret_cast<float4*>(dst) = make_float4(v0, v1, v2, v3);
+        else
+          st_async_f4(map_to_rank(smem_u32(dst), owner), v0, v1, v2, v3,
+                      map_to_rank(bar, owner));
+      }
+    }
+    cluster_arrive();  // no store of this CTA to another's memory is still to come
+    named_bar_sync(1, C::EPI * 32);
+    ok = ok && mbar_wait_spin(got, 0, abort_flag, p.err, p.timeout);
+    ok = __all_sync(0xFFFFFFFFu, ok);
+    // one warp per token, four rows per lane, the parts added in rank order
+    for (int i = warp; ok && i < mine; i += C::EPI) {
+      const int t = rank + i * split;
       float4 sum[C::AT];
 #pragma unroll
       for (int a = 0; a < C::AT; ++a) {
-        float4 v[8];
-#pragma unroll
-        for (int r = 0; r < 8; ++r)
-          if (r < split) v[r] = ld_cluster_f4(map_to_rank(part + (a * BN + t) * 512, r));
+        const float4* v =
+            reinterpret_cast<const float4*>(parts + (i * C::AT + a) * split * 128) + lane;
         sum[a] = v[0];
-#pragma unroll
-        for (int r = 1; r < 8; ++r)
-          if (r < split) {
-            sum[a].x += v[r].x;
-            sum[a].y += v[r].y;
-            sum[a].z += v[r].z;
-            sum[a].w += v[r].w;
-          }
+        for (int r = 1; r < split; ++r) {
+          sum[a].x += v[r * 32].x;
+          sum[a].y += v[r * 32].y;
+          sum[a].z += v[r * 32].z;
+          sum[a].w += v[r * 32].w;
+        }
       }
       const int64_t m = t0 + t;
       const int c = rb * 128 + lane * 4;
@@ -294,15 +359,14 @@ __global__ void __launch_bounds__(THREADS)
       }
     }
   }
-  __syncwarp();
-  tc_fence_before();
-  if (split > 1) {  // the other CTAs have read this one's part
-    cluster_arrive();
+  if (warp >= C::EPI) {
     cluster_wait();
-  } else {
-    __syncthreads();
+    cluster_arrive();
   }
-  if (warp == 5) {
+  tc_fence_before();
+  __syncwarp();
+  cluster_wait();  // nothing more is stored into this CTA's memory, and its TMEM has been read
+  if (warp == C::EPI + 1) {
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM_COLS);
   }
@@ -321,7 +385,7 @@ cudaError_t launch(const CUtensorMap& tok, const LinParams& p, int split, cudaSt
   using C = Narrow<BN, ACT>;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(split, (p.M + BN - 1) / BN, ACT ? p.width / 128 : p.NB);
-  cfg.blockDim = dim3(THREADS);
+  cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];

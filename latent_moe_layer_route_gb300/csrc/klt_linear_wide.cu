@@ -38,36 +38,6 @@ struct Smem {
   volatile int* abort_flag;
 };
 
-// Starts the load of 32 consecutive fp32 columns of this thread's TMEM lane; the registers
-// hold them after tmem_wait_ld32 on the same array.
-KLT_DEV void tmem_start_ld32(uint32_t taddr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-        "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
-        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
-        "=r"(r[31])
-      : "r"(taddr)
-      : "memory");
-}
-// Waits for this thread's TMEM loads; the registers pass through, so that no use of them
-// moves above the wait.
-KLT_DEV void tmem_wait_ld32(uint32_t* r) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
-                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
-                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
-                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
-                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
-                 "+r"(r[30]), "+r"(r[31])
-               :
-               : "memory");
-}
-
 // The output leaves through a warp's four boxes of 32 rows x 64 bytes: staged in the output
 // map's swizzle (no bank conflicts) and stored by bulk copies, which cut off what lies outside
 // the output and run on while the warp goes on.  Lane b issues the copy of box b.
@@ -132,21 +102,38 @@ KLT_DEV void store_rows(const LinParams& p, const CUtensorMap* omap, uint8_t* bo
     store_boxes(boxes, omap,
                 lane < 2 * COUNT ? (c + (lane >> 1) * 128 + (lane & 1) * 32) * 2 : p.width * 2,
                 p.width * 2, m0);
-  } else if (m0 + lane < p.M) {
+  } else {
+    // rows that are not vectors: 64 columns at a time through the boxes, then row by row,
+    // neighbouring lanes neighbouring columns (each thread its own row: 1003 x 777 fp32 spent
+    // 20 us here)
     const bool f32 = p.out_dtype == KLT_DT_F32;
-    const int64_t row = (m0 + lane) * p.ld_out;
+    float* t = reinterpret_cast<float*>(boxes);  // [32][64], columns rotated by the row
+    const int rows = p.M - m0 < 32 ? p.M - m0 : 32;
 #pragma unroll
-    for (int i = 0; i < 64 * COUNT; ++i) {
-      const int col = c + (i >> 6) * 128 + (i & 63);
-      float lo, hi;
-      unpack2(v[i >> 6][(i & 63) / 2], lo, hi);
-      const float x = i % 2 ? hi : lo;
-      if (col < p.width) {
-        if (f32)
-          static_cast<float*>(p.out)[row + col] = x;
-        else
-          static_cast<__nv_bfloat16*>(p.out)[row + col] = __float2bfloat16(x);
+    for (int g = 0; g < COUNT; ++g) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        float lo, hi;
+        unpack2(v[g][i], lo, hi);
+        t[lane * 64 + ((2 * i + lane) & 63)] = lo;
+        t[lane * 64 + ((2 * i + 1 + lane) & 63)] = hi;
       }
+      __syncwarp();
+      for (int r = 0; r < rows; ++r) {
+        const int64_t row = (m0 + r) * p.ld_out;
+#pragma unroll
+        for (int h = 0; h < 64; h += 32) {
+          const int col = c + g * 128 + h + lane;
+          const float x = t[r * 64 + ((h + lane + r) & 63)];
+          if (col < p.width) {
+            if (f32)
+              static_cast<float*>(p.out)[row + col] = x;
+            else
+              static_cast<__nv_bfloat16*>(p.out)[row + col] = __float2bfloat16(x);
+          }
+        }
+      }
+      __syncwarp();
     }
   }
 }
