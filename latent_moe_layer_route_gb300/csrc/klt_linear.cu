@@ -15,6 +15,7 @@ struct klt_linear {
   klt_linear_dims d;
   int device;
   int num_sms;
+  int max_tiles;   // tiles of the token-major kernel that two pairs each share at once
   int NB, KB;      // row blocks and k-blocks of W
   uint8_t* w;      // tile-major image [NB, KB, 16384]
   float* ws;       // [NB + 1, KB], the last row zero
@@ -105,25 +106,44 @@ void free_all(klt_linear* h) {
   delete h;
 }
 
-// Token tile and K split for M tokens.
+// Token tile and K split for M tokens: the fastest by a model of the three ways, in us, whose
+// constants are fits to measurements (the largest of 26 sizes off by 25 %; the runner-up is
+// close wherever it picks the wrong one):
+//   narrow kernel, tile bn:  a wave of CTAs costs 2.5 + its k-blocks x the time of one, which
+//     grows with the tokens (0.20 for 16, 0.34 for 128), + 1.5 to bring the parts together;
+//   wide kernel: 1.5 + 0.43 per k-block and wave of pairs; + 3.5 where two pairs share a tile.
+// E.g. 256 x 7168 x 7168: narrow 25.5, wide 27.9, wide by two pairs 21.0 us; 777 x 1003 x 2090:
+// 9.4, 14.3 and 14.9 us; 1024 x 2048 x 3584: 15.5, 15.7 and 14.4 us.
 void choose(const klt_linear* h, int M, int* tile, int* split) {
   const bool act = h->d.act == KLT_ACT_SWIGLU;
-  const int units_n = act ? h->NB / 2 : h->NB;
-  *split = 1;
-  if (M > 256) {
-    *tile = 256;
-    return;
-  }
   const int most = act ? 64 : 128;
   int bn = 16;
   while (bn < M && bn < most) bn *= 2;
+  // two tiles of 32 SwiGLU tokens share an SM, a tile of 64 runs alone (64 x 4096 x 7168: 10.3
+  // and 12.1 us)
+  if (act && M > 32 && M <= 64) bn = 32;
   *tile = bn;
+  *split = 1;
   // Parts of K while the CTAs stay below 256, about 1.7 per SM (one per SM for the tiles that
-  // run alone on theirs): all resident at once, with room for the first CTAs of the next launch
-  const bool alone = act ? bn == 64 : bn == 128;
-  const int64_t units = static_cast<int64_t>(units_n) * ((M + bn - 1) / bn);
-  while (*split < 8 && units * *split * 2 <= (alone ? 152 : 256) && h->KB >= *split * 2)
+  // run alone on theirs, half in clusters of 8, which have to fit in their part of the chip):
+  // all resident at once, with room for the first CTAs of the next launch (1 x 7168 x 2048: 4
+  // parts, 224 CTAs, 4.8 us; 8 parts, 448 CTAs, 6.9 us; 2 parts 5.2 us).
+  const bool alone = bn == most;
+  const int64_t units = static_cast<int64_t>(act ? h->NB / 2 : h->NB) * ((M + bn - 1) / bn);
+  while (*split < 8 && h->KB >= *split * 2 &&
+         units * *split * 2 <= (!alone ? 256 : *split < 4 ? h->num_sms : h->num_sms / 2))
     *split *= 2;
+  if (M <= 128) return;
+
+  const int64_t waves = (units * *split + h->num_sms - 1) / h->num_sms;
+  const double narrow = waves * (2.5 + 0.34 * h->KB / *split) + (*split > 1 ? 1.5 : 0.0);
+  const int64_t tiles = static_cast<int64_t>((M + 255) / 256) * ((h->NB + 1) / 2);
+  const int64_t pairs = h->num_sms / 2;
+  const double wide = (tiles + pairs - 1) / pairs * (1.5 + 0.43 * h->KB);
+  const double shared = tiles <= h->max_tiles && h->KB >= 4 ? 5.0 + 0.43 * h->KB / 2 : wide;
+  if (narrow < wide && narrow < shared) return;
+  *tile = 256;
+  *split = shared < wide ? 2 : 1;
 }
 
 }  // namespace
@@ -144,13 +164,15 @@ int klt_linear_create(const klt_linear_dims* d, const void* w, const float* w_sc
   if (cudaGetDeviceProperties(&prop, dev) != cudaSuccess) return KLT_ERR_CUDA;
   if (prop.major != 10 || prop.minor != 3) return KLT_ERR_UNSUPPORTED;
   if (!get_encode()) return KLT_ERR_CUDA;
-  if (!prepare_linear_narrow() || !prepare_linear_wide()) return KLT_ERR_UNSUPPORTED;
+  int max_tiles = 0;
+  if (!prepare_linear_narrow() || !prepare_linear_wide(&max_tiles)) return KLT_ERR_UNSUPPORTED;
 
   klt_linear* h = new (std::nothrow) klt_linear();
   if (!h) return KLT_ERR_OOM;
   h->d = *d;
   h->device = dev;
   h->num_sms = prop.multiProcessorCount;
+  h->max_tiles = max_tiles;
   h->NB = (d->N + 127) / 128;
   h->KB = (d->K + 127) / 128;
   const int64_t tiles = static_cast<int64_t>(h->NB) * h->KB;
@@ -212,7 +234,7 @@ int klt_linear_forward(klt_linear* h, const uint8_t* xq, int64_t ld_xq, const fl
     }
     if (dbg->force_split) split = dbg->force_split;
     if (split != 1 && split != 2 && split != 4 && split != 8) return KLT_ERR_INVALID_ARG;
-    if (split > h->KB || (tile == 256 && split != 1)) return KLT_ERR_UNSUPPORTED;
+    if (split > h->KB || (tile == 256 && split > 2)) return KLT_ERR_UNSUPPORTED;
   }
 
   LinParams p = {};
@@ -247,7 +269,7 @@ int klt_linear_forward(klt_linear* h, const uint8_t* xq, int64_t ld_xq, const fl
         !encode_bytes(&omap, out, M, width * es, M > 1 ? ld_out * es : (width * es + 15) / 16 * 16,
                       64, 32, CU_TENSOR_MAP_SWIZZLE_64B))
       return KLT_ERR_CUDA;
-    e = launch_linear_wide(tok, h->wmap, omap, p, act, h->num_sms, s);
+    e = launch_linear_wide(tok, h->wmap, omap, p, act, split, h->num_sms, s);
   } else {
     e = launch_linear_narrow(tok, p, tile, split, act, s);
   }

@@ -62,6 +62,16 @@ KLT_DEV void st_async_f4(uint32_t addr, float a, float b, float c, float d, uint
       "r"(__float_as_uint(d)), "r"(bar)
       : "memory");
 }
+KLT_DEV ulonglong2 ld_shared_u64x2(uint32_t addr) {
+  ulonglong2 v;
+  asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(v.x), "=l"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+KLT_DEV void st_cluster_f4(uint32_t addr, float a, float b, float c, float d) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b),
+               "f"(c), "f"(d)
+               : "memory");
+}
 // Arrive on a barrier of any CTA of the cluster (`addr` from map_to_rank).  For hand-offs of
 // TMEM, whose reads have completed: nothing written to memory is published, so the release
 // stays at CTA scope (at cluster scope it is a memory barrier, and the wide kernel stood in
@@ -113,14 +123,13 @@ KLT_DEV void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {  // a warp of b
                "r"(ncols)
                : "memory");
 }
-// Arrive once on the barrier at the same offset in both CTAs of the pair when every MMA
-// issued so far by this thread has completed.
-KLT_DEV void tc_commit_pair(uint64_t* bar) {
-  const uint16_t both = 3;
+// Arrive once on the barrier at the same offset in the CTAs of `mask` (bit = rank) when every
+// MMA issued so far by this thread has completed.
+KLT_DEV void tc_commit_pair(uint64_t* bar, uint16_t mask) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
       " [%0], %1;" ::"r"(smem_u32(bar)),
-      "h"(both)
+      "h"(mask)
       : "memory");
 }
 // The four MMAs of one 128-byte K block over both CTAs' tiles (M = 256: 128 rows of A in each
@@ -193,6 +202,9 @@ KLT_DEV void tmem_wait_ld16(uint32_t* r) {
 KLT_DEV void fma2(unsigned long long& a, unsigned long long p, unsigned long long s) {
   asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(a) : "l"(p), "l"(s));
 }
+KLT_DEV void add2(unsigned long long& a, unsigned long long b) {
+  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a) : "l"(b));
+}
 KLT_DEV unsigned long long pack2(float lo, float hi) {
   unsigned long long r;
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
@@ -252,10 +264,10 @@ cudaError_t launch_linear_narrow(const CUtensorMap& tok, const LinParams& p, int
                                  bool swiglu, cudaStream_t s);
 cudaError_t launch_linear_wide(const CUtensorMap& tok, const CUtensorMap& wmap,
                                const CUtensorMap& omap, const LinParams& p, bool swiglu,
-                               int num_sms, cudaStream_t s);
+                               int parts, int num_sms, cudaStream_t s);
 // Once per device, before the first launch: shared-memory sizes, and whether the kernels are
 // what their launches expect.
 bool prepare_linear_narrow();
-bool prepare_linear_wide();
+bool prepare_linear_wide(int* max_tiles);  // tiles that two pairs each share at once
 
 }  // namespace klt

@@ -11,7 +11,10 @@
 // k-block, two 256-column slots in turn), not the multiplication, bounds the kernel.
 //
 // Persistent: one pair per two SMs, tiles dealt round robin, token tiles fastest (the pairs
-// that run together share weight tiles in L2).
+// that run together share weight tiles in L2).  Where there are too few tiles for that, two
+// pairs form a cluster and share one tile's K; at the end each warp's 32 rows go to the pair
+// that finishes them, through distributed shared memory, and are added in rank order (four
+// pairs, clusters of 8 CTAs that fill their SMs, were slower at every size).
 #include "klt_linear.cuh"
 
 #include "../../include/klt.h"
@@ -26,6 +29,7 @@ constexpr int RING_BYTES = STAGES * STAGE_BYTES;
 constexpr int BOX_BYTES = 32 * 64;         // stored at a time by a warp: 32 rows x 64 bytes
 constexpr int BOXES = 4;                   // per epilogue warp
 constexpr int OUT_BYTES = 8 * BOXES * BOX_BYTES;
+constexpr int PART_BYTES = 32 * 128 * 4;  // a warp's 32 rows x 128 columns, fp32
 constexpr int AMAX_BYTES = 2 * 128 * 4;
 constexpr int SMEM = 1024 + RING_BYTES + OUT_BYTES + AMAX_BYTES + 256;
 static_assert(SMEM <= 232448, "shared memory of a block");
@@ -138,8 +142,8 @@ KLT_DEV void store_rows(const LinParams& p, const CUtensorMap* omap, uint8_t* bo
   }
 }
 
-// grid 2 x pairs, cluster 2
-template <int ACT>
+// grid 2 x pairs, cluster 2; PARTS of K > 1: grid tiles x 2 x PARTS, cluster 2 x PARTS
+template <int ACT, int PARTS>
 __global__ void __launch_bounds__(THREADS, 1)
     wide_kernel(const __grid_constant__ CUtensorMap tok, const __grid_constant__ CUtensorMap wmap,
                 const __grid_constant__ CUtensorMap omap, const LinParams p) {
@@ -157,9 +161,15 @@ __global__ void __launch_bounds__(THREADS, 1)
   static_assert((2 * STAGES + 3) * 8 + 8 <= 256, "barrier space");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_rank();
+  // this CTA's half of the pair's tokens and weight rows, the pair's first CTA, its part of K
+  const uint32_t crank = cluster_rank(), rank = crank & 1, leader = PARTS > 1 ? crank & ~1u : 0;
+  const uint16_t both = static_cast<uint16_t>(3u << leader);
+  const int part = PARTS > 1 ? static_cast<int>(crank >> 1) : 0;
+  const int k0 = PARTS > 1 ? static_cast<int>(static_cast<int64_t>(p.KB) * part / PARTS) : 0;
+  const int k1 =
+      PARTS > 1 ? static_cast<int>(static_cast<int64_t>(p.KB) * (part + 1) / PARTS) : p.KB;
   // this pair's tiles: the first one, then steps of the number of pairs
-  const int pair = blockIdx.x >> 1;
+  const int pair = blockIdx.x / (2 * PARTS);
   int tm = pair % p.tiles_m, tn = pair / p.tiles_m;
   auto next_tile = [&]() {
     tm += p.step_m;
@@ -192,13 +202,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     regs_dec<56>();
     if (warp == 0 && lane == 0) {
       pdl_wait();
-      const uint32_t full0 = map_to_rank(smem_u32(sm.full), 0);
+      const uint32_t full0 = map_to_rank(smem_u32(sm.full), leader);
       int it = 0;
       bool ok = true;
       for (; tn < p.tiles_n && ok; next_tile()) {
         const int row0 = tm * 256 + static_cast<int>(rank) * 128;
         const int rb = ACT ? tn + static_cast<int>(rank) * p.up : tn * 2 + static_cast<int>(rank);
-        for (int kb = 0; kb < p.KB; ++kb, ++it) {
+        for (int kb = k0; kb < k1; ++kb, ++it) {
           if (p.stall > 0 && it >= p.stall) {
             ok = false;
             break;
@@ -227,7 +237,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       int it = 0;
       bool ok = true;
       for (; tn < p.tiles_n && ok; next_tile())
-        for (int kb = 0; kb < p.KB; ++kb, ++it) {
+        for (int kb = k0; kb < k1; ++kb, ++it) {
           const int st = it % STAGES, slot = it & 1;
           ok = mbar_wait_spin(&sm.full[st], (it / STAGES) & 1, sm.abort_flag, p.err, p.timeout) &&
                mbar_wait_spin(&sm.tempty[slot], ((it >> 1) & 1) ^ 1, sm.abort_flag, p.err,
@@ -237,20 +247,24 @@ __global__ void __launch_bounds__(THREADS, 1)
           const uint32_t base = smem_u32(sm.ring + st * STAGE_BYTES);
           mma4_fp8_pair(tmem + slot * 256, sdesc_sw128(base), sdesc_sw128(base + LIN_TILE_BYTES),
                         idesc);
-          tc_commit_pair(&sm.done[st]);
+          tc_commit_pair(&sm.done[st], both);
         }
-      tc_commit_pair(sm.drain);  // no MMA of the pair runs past this point
+      tc_commit_pair(sm.drain, both);  // no MMA of the pair runs past this point
       int none = 0;
       mbar_wait(sm.drain, 0, &none, p.err, p.timeout);
     }
     __syncwarp();
+    for (int i = 0; PARTS > 1 && i < 2; ++i) {  // the epilogue's two
+      cluster_arrive();
+      cluster_wait();
+    }
   } else {
     regs_inc<224>();
     pdl_wait();
     const int quad = warp & 3, half = (warp - 4) >> 2;
     const int row = quad * 32 + lane;
     uint8_t* boxes = sm.stage + (warp - 4) * BOXES * BOX_BYTES;
-    const uint32_t tempty0 = map_to_rank(smem_u32(sm.tempty), 0);
+    const uint32_t tempty0 = map_to_rank(smem_u32(sm.tempty), leader);
     // this thread's columns of a slot: 64 of the first CTA's weight rows (SwiGLU: gate), 64 of
     // the second's (the matching up rows)
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
@@ -263,8 +277,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     float x, w0, w1;
     auto first_scales = [&]() {
       const int m = tm * 256 + static_cast<int>(rank) * 128 + row;
-      xo = (m < p.M ? m : 0) * p.KB;
-      wo = (ACT ? tn : tn * 2) * p.KB;
+      xo = (m < p.M ? m : 0) * p.KB + k0;
+      wo = (ACT ? tn : tn * 2) * p.KB + k0;
       x = p.xs[xo];
       w0 = p.ws[wo];
       w1 = p.ws[wo + p.step_ws];
@@ -274,11 +288,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       unsigned long long acc[2][32];
 #pragma unroll
       for (int i = 0; i < 32; ++i) acc[0][i] = acc[1][i] = 0ull;
-      for (int kb = 0; kb < p.KB; ++kb, ++it) {
+      for (int kb = 0; kb < k1 - k0; ++kb, ++it) {
         const int slot = it & 1;
         const float f0 = x * w0, f1 = x * w1;
         const unsigned long long s0 = pack2(f0, f0), s1 = pack2(f1, f1);
-        if (kb + 1 < p.KB) {
+        if (kb + 1 < k1 - k0) {
           x = p.xs[xo + kb + 1];
           w0 = p.ws[wo + kb + 1];
           w1 = p.ws[wo + kb + 1 + p.step_ws];
@@ -314,6 +328,54 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int m0 = tm * 256 + static_cast<int>(rank) * 128 + quad * 32, m = m0 + lane, tn0 = tn;
       next_tile();
       if (tn < p.tiles_n) first_scales();
+      bool finish = ok;
+      if (PARTS > 1) {
+        // Every product of the cluster's pairs is in registers once all have arrived, and their
+        // stages are free: each warp's rows go to the pair that finishes them (quadrant q: pair
+        // q * PARTS / 4), as 32 pieces of 4 columns x 32 rows, and are added in rank order.
+        cluster_arrive();
+        cluster_wait();
+        constexpr int OWNED = 4 / PARTS;
+        const int owner = quad / OWNED;
+        // where `owner` keeps these rows of part `from` (its own: any)
+        auto piece = [&](int from) {
+          const int slot = ((from - (from > owner)) * OWNED + quad % OWNED) * 2 + half;
+          return smem_u32(sm.ring) + (from == owner ? 0 : slot) * PART_BYTES + lane * 16;
+        };
+        if (owner != part) {
+          const uint32_t dst = map_to_rank(piece(part), owner * 2 + rank);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            float a, b, c, e;
+            unpack2(acc[i >> 4][(i & 15) * 2], a, b);
+            unpack2(acc[i >> 4][(i & 15) * 2 + 1], c, e);
+            st_cluster_f4(dst + i * 512, a, b, c, e);
+          }
+          finish = false;
+        }
+        cluster_arrive();  // the rows are where they are finished
+        cluster_wait();
+        // (the other warps add up what they find and store nothing)
+        uint32_t src[PARTS];
+#pragma unroll
+        for (int r = 0; r < PARTS; ++r) src[r] = piece(r);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          unsigned long long* a = &acc[i >> 4][(i & 15) * 2];
+          unsigned long long s0 = 0, s1 = 0;
+#pragma unroll
+          for (int r = 0; r < PARTS; ++r) {
+            ulonglong2 v = ld_shared_u64x2(src[r] + i * 512);
+            if (r == part) v = make_ulonglong2(a[0], a[1]);
+            if (r == 0)
+              s0 = v.x, s1 = v.y;
+            else
+              add2(s0, v.x), add2(s1, v.y);
+          }
+          a[0] = s0;
+          a[1] = s1;
+        }
+      }
       if (ACT) {
         float big = 0.f;
 #pragma unroll
@@ -332,7 +394,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           big = max_nan(big, sm.amax[(half ^ 1) * 128 + row]);
           named_bar_sync(1, 256);  // amax is free for the next tile
           float s = group_scale(big);
-          if (ok && half == 0 && m < p.M)
+          if (finish && half == 0 && m < p.M)
             p.out_s[static_cast<int64_t>(m) * (p.width / 128) + tn0] = s;
           const float k = rescale(s), inv = __frcp_rn(s);
           if (k != 1.0f) {
@@ -353,7 +415,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int e = 0; e < 4; ++e) q[e] = quot_group(q[e], s, inv);
             w[j] = f32x2_to_e4m3x2(q[0], q[1]) | (f32x2_to_e4m3x2(q[2], q[3]) << 16);
           }
-          if (ok && m0 < p.M) {
+          if (finish && m0 < p.M) {
             const int c = tn0 * 128 + half * 64;
             if (p.out_wide) {
               boxes_free();
@@ -365,10 +427,10 @@ __global__ void __launch_bounds__(THREADS, 1)
               for (int j = 0; j < 64; ++j) o[j] = static_cast<uint8_t>(w[j / 4] >> (8 * (j % 4)));
             }
           }
-        } else if (ok) {
+        } else if (finish) {
           store_rows<1>(p, &omap, boxes, m0, tn0 * 128 + half * 64, acc);
         }
-      } else if (ok) {
+      } else if (finish) {
         store_rows<2>(p, &omap, boxes, m0, tn0 * 256 + half * 64, acc);
       }
     }
@@ -385,51 +447,78 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
+void config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute attr[2], int clusters, int parts,
+            cudaStream_t s) {
+  cfg->gridDim = dim3(2 * parts * clusters);
+  cfg->blockDim = dim3(THREADS);
+  cfg->dynamicSmemBytes = SMEM;
+  cfg->stream = s;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2 * parts;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg->attrs = attr;
+  cfg->numAttrs = 2;
+}
+
 template <int ACT>
 cudaError_t launch(const CUtensorMap& tok, const CUtensorMap& wmap, const CUtensorMap& omap,
-                   LinParams p, int num_sms, cudaStream_t s) {
+                   LinParams p, int parts, int num_sms, cudaStream_t s) {
   p.tiles_m = (p.M + 255) / 256;
   p.tiles_n = ACT ? p.width / 128 : (p.NB + 1) / 2;
+  p.step_ws = ACT ? p.up * p.KB : p.KB;
   const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  if (parts > 1) {  // one tile per cluster
+    if (tiles > 0x7FFFFFF) return cudaErrorInvalidValue;
+    p.step_m = 0;
+    p.step_n = p.tiles_n;
+    config(&cfg, attr, static_cast<int>(tiles), parts, s);
+    return cudaLaunchKernelEx(&cfg, wide_kernel<ACT, 2>, tok, wmap, omap, p);
+  }
   const int pairs = tiles < num_sms / 2 ? static_cast<int>(tiles) : num_sms / 2;
   p.step_m = pairs % p.tiles_m;
   p.step_n = pairs / p.tiles_m;
-  p.step_ws = ACT ? p.up * p.KB : p.KB;
+  config(&cfg, attr, pairs, 1, s);
+  return cudaLaunchKernelEx(&cfg, wide_kernel<ACT, 1>, tok, wmap, omap, p);
+}
+
+// max_tiles: lowered to the clusters of PARTS pairs that run at once.
+template <int ACT, int PARTS>
+bool prepare(int* max_tiles) {
+  // setmaxnreg moves registers between the warpgroups: 56 + 2 x 224 = 3 x 168 at launch
+  auto k = wide_kernel<ACT, PARTS>;
+  cudaFuncAttributes a;
+  if (cudaFuncGetAttributes(&a, k) != cudaSuccess || a.numRegs < 168 ||
+      cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) != cudaSuccess)
+    return false;
+  if (PARTS == 1) return true;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * pairs);
-  cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = SMEM;
-  cfg.stream = s;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, wide_kernel<ACT>, tok, wmap, omap, p);
+  config(&cfg, attr, 1, PARTS, 0);
+  cfg.numAttrs = 1;  // the cluster alone
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, k, &cfg) != cudaSuccess) return false;
+  if (n < *max_tiles) *max_tiles = n;
+  return true;
 }
 
 }  // namespace
 
-bool prepare_linear_wide() {
-  for (auto k : {wide_kernel<0>, wide_kernel<1>}) {
-    // setmaxnreg moves registers between the warpgroups: 56 + 2 x 224 = 3 x 168 at launch
-    cudaFuncAttributes a;
-    if (cudaFuncGetAttributes(&a, k) != cudaSuccess || a.numRegs < 168 ||
-        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) != cudaSuccess)
-      return false;
-  }
-  return true;
+bool prepare_linear_wide(int* max_tiles) {
+  *max_tiles = 1 << 20;
+  return prepare<0, 1>(nullptr) && prepare<1, 1>(nullptr) && prepare<0, 2>(max_tiles) &&
+         prepare<1, 2>(max_tiles);
 }
 
 cudaError_t launch_linear_wide(const CUtensorMap& tok, const CUtensorMap& wmap,
                                const CUtensorMap& omap, const LinParams& p, bool swiglu,
-                               int num_sms, cudaStream_t s) {
-  return swiglu ? launch<1>(tok, wmap, omap, p, num_sms, s)
-                : launch<0>(tok, wmap, omap, p, num_sms, s);
+                               int parts, int num_sms, cudaStream_t s) {
+  return swiglu ? launch<1>(tok, wmap, omap, p, parts, num_sms, s)
+                : launch<0>(tok, wmap, omap, p, parts, num_sms, s);
 }
 
 }  // namespace klt

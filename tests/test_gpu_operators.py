@@ -373,9 +373,8 @@ class Lin:
     (17, 384, 1000, "none", "bf16"), (33, 512, 896, "swiglu", "fp8"), (40, 1003, 2090, "none", "f32"),
     (64, 256, 1536, "none", "bf16"), (100, 513, 333, "none", "bf16"), (128, 640, 512, "none", "f32"),
     (129, 512, 130, "swiglu", "fp8"), (200, 300, 520, "none", "bf16")])
-def test_linear_narrow(M, N, K, act, out):
+def test_linear(M, N, K, act, out):
     c = Lin(M, N, K, act, out)
-    assert c.layer.tile(M) % 1000 < 256
     c.check(c.layer(c.xq, c.xs))
     c.close()
 
@@ -407,6 +406,22 @@ def test_linear_wide(M, N, K, act, out):
     c.close()
 
 
+@pytest.mark.parametrize("M,N,K,act,out", [
+    (1, 256, 512, "none", "bf16"), (300, 256, 640, "swiglu", "fp8"), (129, 300, 2090, "none", "f32"),
+    (256, 129, 1030, "none", "bf16"), (700, 768, 1024, "swiglu", "bf16"), (513, 1003, 900, "none", "f32"),
+    (2100, 2560, 384, "none", "bf16")])
+def test_linear_wide_split(M, N, K, act, out):
+    """A tile's K shared by two CTA pairs, evenly and not, also with more tiles than fit."""
+    c = Lin(M, N, K, act, out)
+    dbg = B.KltLinearDebug(force_tile=256, force_split=2)
+    got = c.layer(c.xq, c.xs, debug=dbg)
+    c.check(got)
+    again = c.layer(c.xq, c.xs, debug=dbg)
+    for a, b in zip(*((g if out == "fp8" else (g,)) for g in (got, again))):
+        assert _same(a, b)
+    c.close()
+
+
 @pytest.mark.parametrize("tile,M", [(16, 9), (64, 70), (256, 300)])
 def test_linear_strides_and_untouched_rows(tile, M):
     """Inputs and outputs in wider buffers; what lies outside the result stays."""
@@ -431,8 +446,8 @@ def test_linear_rows_do_not_depend_on_the_batch():
     """A row's result is the same bits alone and in a batch of the same kernel, and a batch's
     the same bits every time."""
     c = Lin(300, 384, 1536, "none", "f32")
-    for tile in (32, 256):
-        dbg = B.KltLinearDebug(force_tile=tile, force_split=0 if tile == 256 else 4)
+    for tile, split in ((32, 4), (256, 1), (256, 2)):
+        dbg = B.KltLinearDebug(force_tile=tile, force_split=split)
         full = c.layer(c.xq, c.xs, debug=dbg)
         for _ in range(5):
             assert _same(c.layer(c.xq, c.xs, debug=dbg), full)
@@ -477,7 +492,7 @@ def test_linear_refusals():
     assert e.value.code == B.KLT_ERR_INVALID_ARG
     for dbg, code in ((dict(force_tile=128), B.KLT_ERR_UNSUPPORTED),
                       (dict(force_tile=48), B.KLT_ERR_INVALID_ARG),
-                      (dict(force_tile=256, force_split=2), B.KLT_ERR_UNSUPPORTED),
+                      (dict(force_tile=256, force_split=4), B.KLT_ERR_UNSUPPORTED),
                       (dict(force_split=4), B.KLT_ERR_UNSUPPORTED),  # 2 k-blocks
                       (dict(force_split=3), B.KLT_ERR_INVALID_ARG),
                       (dict(timeout_ms=-1), B.KLT_ERR_INVALID_ARG)):
@@ -495,7 +510,7 @@ def test_linear_refusals():
         f(c.xq, c.xs)
 
 
-@pytest.mark.parametrize("tile,split", [(16, 1), (32, 2), (256, 0)])
+@pytest.mark.parametrize("tile,split", [(16, 1), (32, 2), (256, 1), (256, 2)])
 def test_linear_bounded_wait_expires(tile, split):
     """The copies stop after one k-block: the waits on their data run out, every CTA returns
     and the handle reports it; another handle is not affected."""
