@@ -313,6 +313,7 @@ class _Types:
         cls.bf16, cls.f32 = torch.bfloat16, torch.float32
         cls.act = {torch.bfloat16: KLT_DT_BF16, torch.float32: KLT_DT_F32}
         cls.codes = (torch.float8_e4m3fn, torch.uint8)
+        cls.bf16s, cls.f32s = (torch.bfloat16,), (torch.float32,)
         cls.raw_stream = torch._C._cuda_getCurrentRawStream
         cls.current_device = torch._C._cuda_getDevice
         cls.torch = torch
@@ -337,6 +338,26 @@ def _rows(t, name: str, dtypes, rows: int, cols: int, device: int) -> int:
             (unit != 1 and cols > 1):
         _refuse(t, name, dtypes, rows, cols, device, False)
     return ld
+
+
+def _like(t, name: str, dtypes, size, device: int) -> int:
+    """As _rows, for an operand of the size of one that passed."""
+    if t.shape != size or t.dtype not in dtypes or t.get_device() != device:
+        _refuse(t, name, dtypes, size[0], size[1], device, False)
+    ld, unit = t.stride()
+    if unit != 1 and size[1] > 1:
+        _refuse(t, name, dtypes, size[0], size[1], device, False)
+    return ld
+
+
+def _broadcast(t, rows: int, cols: int):
+    """(row, column) strides of t broadcast to [rows, cols]."""
+    shape, strides = t.shape, t.stride()
+    if len(shape) < 2:
+        shape, strides = (1,) * (2 - len(shape)) + tuple(shape), (0,) * (2 - len(shape)) + strides
+    if len(shape) != 2 or shape[0] not in (1, rows) or shape[1] not in (1, cols):
+        raise ValueError(f"gate: shape {tuple(t.shape)} does not broadcast to {(rows, cols)}")
+    return (0 if shape[0] == 1 else strides[0]), (0 if shape[1] == 1 else strides[1])
 
 
 def _contiguous(t, name: str, dtypes, rows: int, cols: int, device: int):
@@ -391,7 +412,7 @@ def quantize_fp8(x, q=None, s=None, stream: Optional[int] = None):
     if s is None:
         s = T.torch.empty((M, G), dtype=T.f32, device=x.device)
     ld_q = _rows(q, "q", T.codes, M, K, dev)
-    _contiguous(s, "s", (T.f32,), M, G, dev)
+    _contiguous(s, "s", T.f32s, M, G, dev)
     if stream is None:
         stream = T.raw_stream(dev)
     call = _direct if T.current_device() == dev else _On(dev)
@@ -411,7 +432,7 @@ class BlockNorm:
     def __init__(self, H: int, gamma_post=None, gamma_pre=None, eps: float = 1e-6,
                  res_scale: float = 1.0, branch_scale: float = 1.0,
                  gate_sigmoid: bool = False):
-        self.H = H
+        self.H, self._groups = H, -(-H // 128)
         self.gamma_post, self.gamma_pre = gamma_post, gamma_pre
         self.device = None
         for name, g in (("gamma_post", gamma_post), ("gamma_pre", gamma_pre)):
@@ -436,44 +457,46 @@ class BlockNorm:
         when none is given, h_out (with y) and n are allocated.  Without y the norm after
         the block is skipped.  Returns (h_out, n, q, s)."""
         T = _Types
+        act = T.act
         dev = _device_of(h, "h")
         if self.device is not None and dev != self.device:
             raise ValueError("h: not on the weights' device")
-        M, H = h.shape[0], self.H
+        size = h.shape
+        M, H = size[0], self.H
         a = KltBlockNormArgs.from_buffer_copy(self._args)
         a.M = M
-        a.ld_h = _rows(h, "h", T.act, M, H, dev)
-        a.h_dtype = T.act[h.dtype]
+        a.ld_h = _rows(h, "h", act, M, H, dev)
+        a.h_dtype = act[h.dtype]
         a.h = h.data_ptr()
         if h_out is None and n is None and q is None and s is None:
             if y is not None:
                 h_out = T.torch.empty((M, H), dtype=h.dtype, device=h.device)
             n = T.torch.empty((M, H), dtype=T.bf16, device=h.device)
         if y is not None:
-            a.ld_y = _rows(y, "y", T.act, M, H, dev)
-            a.y_dtype = T.act[y.dtype]
+            a.ld_y = _like(y, "y", act, size, dev)
+            a.y_dtype = act[y.dtype]
             a.y = y.data_ptr()
             if gate is not None:
-                if gate.dtype not in T.act or gate.get_device() != dev:
+                if gate.dtype not in act or gate.get_device() != dev:
                     raise ValueError("gate: not a bf16 or fp32 tensor on h's device")
-                a.gate_row, a.gate_col = gate.expand(M, H).stride()
-                a.gate_dtype = T.act[gate.dtype]
+                a.gate_row, a.gate_col = _broadcast(gate, M, H)
+                a.gate_dtype = act[gate.dtype]
                 a.gate = gate.data_ptr()
         else:
             if gate is not None:
                 raise ValueError("gate: given without y")
             a.gamma_post = None
         if h_out is not None:
-            a.ld_h_out = _rows(h_out, "h_out", (h.dtype,), M, H, dev)
+            a.ld_h_out = _like(h_out, "h_out", (h.dtype,), size, dev)
             a.h_out = h_out.data_ptr()
         if n is not None:
-            a.ld_n = _rows(n, "n", (T.bf16,), M, H, dev)
+            a.ld_n = _like(n, "n", T.bf16s, size, dev)
             a.n = n.data_ptr()
         if q is not None:
-            a.ld_q = _rows(q, "q", T.codes, M, H, dev)
+            a.ld_q = _like(q, "q", T.codes, size, dev)
             a.q = q.data_ptr()
         if s is not None:
-            _contiguous(s, "s", (T.f32,), M, -(-H // 128), dev)
+            _contiguous(s, "s", T.f32s, M, self._groups, dev)
             a.s = s.data_ptr()
         if stream is None:
             stream = T.raw_stream(dev)
@@ -506,11 +529,10 @@ class Fp8Linear:
         self.N, self.K = w_q.shape
         _contiguous(w_q, "w_q", T.codes, self.N, self.K, self.device)
         self._groups = -(-self.K // 128)
-        _contiguous(w_s, "w_s", (T.f32,), -(-self.N // 128), self._groups, self.device)
+        _contiguous(w_s, "w_s", T.f32s, -(-self.N // 128), self._groups, self.device)
         self.width = self.N // 2 if act == "swiglu" else self.N
         self.fp8 = out == "fp8"
-        self._f32 = (T.f32,)
-        self._out = T.codes if self.fp8 else (T.f32,) if out == "f32" else (T.bf16,)
+        self._out = T.codes if self.fp8 else T.f32s if out == "f32" else T.bf16s
         self._lib = load_library()
         d = KltLinearDims(self.N, self.K, acts[act], outs[out])
         h = ctypes.c_void_p()
@@ -534,7 +556,7 @@ class Fp8Linear:
         ld = _rows(xq, "xq", T.codes, M, K, dev)
         if M <= 1:  # the stride of a single row says nothing
             ld = -(-K // 16) * 16
-        _contiguous(xs, "xs", self._f32, M, self._groups, dev)
+        _contiguous(xs, "xs", T.f32s, M, self._groups, dev)
         if out is None:
             out = fp8_codes(M, width, xq.device) if self.fp8 else \
                 T.torch.empty((M, width), dtype=self._out[0], device=xq.device)
@@ -543,7 +565,7 @@ class Fp8Linear:
         if self.fp8:
             if out_s is None:
                 out_s = T.torch.empty((M, width // 128), dtype=T.f32, device=xq.device)
-            _contiguous(out_s, "out_s", self._f32, M, width // 128, dev)
+            _contiguous(out_s, "out_s", T.f32s, M, width // 128, dev)
             scales = out_s.data_ptr()
         if stream is None:
             stream = T.raw_stream(dev)

@@ -192,6 +192,91 @@ KLT_DEV void put8(void* base, int64_t off, const float* v) {
   if (F32) p[1] = make_uint4(t[4], t[5], t[6], t[7]);
 }
 
+// ------------------------------------------------------------------ sixteen values per lane
+// The kernels for many rows give a lane 16 neighbouring values, eight lanes a group of 128, and
+// compute on pairs: what a group costs beside its values (the scale, the shuffles) is shared
+// by more of them, and an instruction does two.
+typedef unsigned long long f32x2;
+
+template <bool F32>
+struct Raw16 {
+  uint4 w[F32 ? 4 : 2];
+  KLT_DEV void load(const void* base, int64_t off) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(base) +
+                                                    off * (F32 ? 4 : 2));
+#pragma unroll
+    for (int i = 0; i < (F32 ? 4 : 2); ++i) w[i] = p[i];
+  }
+  KLT_DEV void clear() {
+#pragma unroll
+    for (int i = 0; i < (F32 ? 4 : 2); ++i) w[i] = make_uint4(0, 0, 0, 0);
+  }
+  KLT_DEV f32x2 get(int i) const {  // values 2i and 2i + 1
+    if (F32) {
+      const uint4& q = w[i >> 1];
+      return i & 1 ? pack2(__uint_as_float(q.z), __uint_as_float(q.w))
+                   : pack2(__uint_as_float(q.x), __uint_as_float(q.y));
+    }
+    const uint4& q = w[i >> 2];
+    const uint32_t t = (i & 3) == 0 ? q.x : (i & 3) == 1 ? q.y : (i & 3) == 2 ? q.z : q.w;
+    return pack2(__uint_as_float(t << 16), __uint_as_float(t & 0xFFFF0000u));
+  }
+};
+template <bool F32>
+KLT_DEV void put16(void* base, int64_t off, const f32x2* v) {
+  uint4* p = reinterpret_cast<uint4*>(static_cast<char*>(base) + off * (F32 ? 4 : 2));
+#pragma unroll
+  for (int i = 0; i < (F32 ? 4 : 2); ++i) {
+    uint32_t t[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float lo, hi;
+      if (F32) {
+        unpack2(v[2 * i + j / 2], lo, hi);
+        t[j] = __float_as_uint(j & 1 ? hi : lo);
+      } else {
+        unpack2(v[4 * i + j], lo, hi);
+        const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+        t[j] = *reinterpret_cast<const uint32_t*>(&b);
+      }
+    }
+    p[i] = make_uint4(t[0], t[1], t[2], t[3]);
+  }
+}
+// The largest magnitude of the group that this lane's eight lanes hold, NaN if it holds one.
+KLT_DEV float group_amax16(const f32x2* v) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float lo, hi;
+    unpack2(v[i], lo, hi);
+    m = max_nan(m, max_nan(lo, hi));
+  }
+#pragma unroll
+  for (int o = 4; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  return m;
+}
+KLT_DEV uint4 codes16(const f32x2* v, float s) {
+  f32x2 t[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) t[i] = v[i];
+  const float k = rescale(s), ninv = -__frcp_rn(s);
+  if (k != 1.0f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = mul2(t[i], pack2(k, k));
+  }
+  const f32x2 s2 = pack2(s, s), ninv2 = pack2(ninv, ninv);
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a, b, e, f;
+    unpack2(neg_quot_group2(t[2 * i], s2, ninv2), a, b);
+    unpack2(neg_quot_group2(t[2 * i + 1], s2, ninv2), e, f);
+    c[i] = (f32x2_to_e4m3x2(a, b) | (f32x2_to_e4m3x2(e, f) << 16)) ^ 0x80808080u;
+  }
+  return make_uint4(c[0], c[1], c[2], c[3]);
+}
+
 // ------------------------------------------------------------------ the quantiser
 struct QuantParams {
   const void* x;
@@ -229,26 +314,32 @@ __global__ void __launch_bounds__(256) quant_kernel(QuantParams p) {
   load8(hw, p.x, p.f32, row * p.ld_x, c, p.K, p.wide_x, v);
   quant_store(hw, p, it, row, c, v);
 }
-// Vectors throughout (K a multiple of 128, aligned rows): U groups per half warp, their loads
-// in flight together.
+// Vectors throughout (K a multiple of 128, aligned rows): eight lanes per group, U groups each,
+// their loads in flight together.
 template <int U, bool F32>
 __global__ void __launch_bounds__(256) quant_vec_kernel(QuantParams p) {
   pdl_trigger();
-  const Half hw = half_warp(nullptr);
-  const uint32_t base = blockIdx.x * (16u * U) + (threadIdx.x >> 4);
-  Raw8<F32> raw[U];
+  const uint32_t base = blockIdx.x * (32u * U) + (threadIdx.x >> 3);
+  const int lane = threadIdx.x & 7;
+  Raw16<F32> raw[U];
   uint32_t row[U];
   int c[U];
 #pragma unroll
-  for (int u = 0; u < U; ++u) quant_item(p, min(base + 16 * u, p.items - 1), row[u], c[u]);
+  for (int u = 0; u < U; ++u) quant_item(p, min(base + 32 * u, p.items - 1), row[u], c[u]);
   pdl_wait();
 #pragma unroll
-  for (int u = 0; u < U; ++u) raw[u].load(p.x, row[u] * p.ld_x + c[u] + hw.lane * 8);
+  for (int u = 0; u < U; ++u) raw[u].load(p.x, row[u] * p.ld_x + c[u] + lane * 16);
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    float v[8];
-    raw[u].get(v);
-    if (base + 16 * u < p.items) quant_store(hw, p, base + 16 * u, row[u], c[u], v);
+    f32x2 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = raw[u].get(i);
+    const float s = group_scale(group_amax16(v));
+    const uint4 codes = codes16(v, s);
+    if (base + 32 * u < p.items) {
+      *reinterpret_cast<uint4*>(p.q + row[u] * p.ld_q + c[u] + lane * 16) = codes;
+      if (lane == 0) p.s[base + 32 * u] = s;
+    }
   }
 }
 
@@ -260,7 +351,7 @@ struct NormParams {
   float* s;
   int64_t ld_h, ld_y, gate_row, gate_col, ld_h_out, ld_n, ld_q;
   int H, G;
-  float eps, res_scale, branch_scale;
+  float eps, inv_h, res_scale, branch_scale;
   bool h_f32, y_f32, gate_f32, sigmoid;
   bool wide_h, wide_y, wide_gate, wide_gpost, wide_gpre, wide_h_out, wide_n, wide_q;
 };
@@ -277,13 +368,17 @@ KLT_DEV float block_sum(float v, float* part) {
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   return v;
 }
-KLT_DEV float row_rms_inverse(const float (*v)[8], int vpt, int H, float eps, float* part) {
+// 1 / sqrt(sum / H + eps) by the fast reciprocal square root (2 ulp, the same for a whole row).
+KLT_DEV float rms_inverse(float sum, float inv_h, float eps) {
+  return rsqrtf(fmaf(sum, inv_h, eps));
+}
+KLT_DEV float row_rms_inverse(const float (*v)[8], int vpt, float inv_h, float eps, float* part) {
   float ss = 0.f;
 #pragma unroll
   for (int i = 0; i < vpt; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
-  return 1.0f / sqrtf(block_sum(ss, part) / static_cast<float>(H) + eps);
+  return rms_inverse(block_sum(ss, part), inv_h, eps);
 }
 KLT_DEV float gate_value(float g, bool sigmoid) {
   // the divisor of the fast divide stays in its range: for g < -80 the gate is below 2e-35
@@ -330,7 +425,7 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) norm_kernel(NormParams 
     }
   }
   float scale = p.branch_scale;
-  if (p.gamma_post) scale *= row_rms_inverse(u, VPT, p.H, p.eps, part[0]);
+  if (p.gamma_post) scale *= row_rms_inverse(u, VPT, p.inv_h, p.eps, part[0]);
   if (p.gate && p.gate_col == 0)
     scale *= gate_value(load1(p.gate, p.gate_f32, row * p.gate_row), p.sigmoid);
 #pragma unroll
@@ -365,7 +460,7 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) norm_kernel(NormParams 
     }
   }
   if (!p.n && !p.q) return;
-  const float r = p.gamma_pre ? row_rms_inverse(h, VPT, p.H, p.eps, part[1]) : 1.0f;
+  const float r = p.gamma_pre ? row_rms_inverse(h, VPT, p.inv_h, p.eps, part[1]) : 1.0f;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int c = c0 + i * step;
@@ -421,7 +516,7 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) norm_vec_kernel(NormPar
 #pragma unroll
       for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
     }
-    scale *= 1.0f / sqrtf(block_sum(ss, part[0]) / static_cast<float>(p.H) + p.eps);
+    scale *= rms_inverse(block_sum(ss, part[0]), p.inv_h, p.eps);
   }
   if (p.gate && p.gate_col == 0)
     scale *= gate_value(load1(p.gate, p.gate_f32, row * p.gate_row), p.sigmoid);
@@ -463,9 +558,7 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) norm_vec_kernel(NormPar
   }
   if (!p.n && !p.q) return;
   const float r =
-      p.gamma_pre
-          ? 1.0f / sqrtf(block_sum(ss, part[1]) / static_cast<float>(p.H) + p.eps)
-          : 1.0f;
+      p.gamma_pre ? rms_inverse(block_sum(ss, part[1]), p.inv_h, p.eps) : 1.0f;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int c = c0 + i * step;
@@ -487,9 +580,123 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) norm_vec_kernel(NormPar
   }
 }
 
-template <typename Kernel, typename Params>
+// Many rows of vectors (1024 <= H <= 8192): persistent blocks, a thread 16 fixed columns.  The
+// weights of a column (gamma_post, times a gate that all rows share) wait as fp32 in shared
+// memory, and the next row is loaded while this one is finished.
+template <bool HF32, bool FULL_GATE>
+__global__ void __launch_bounds__(512, 2) norm_rows_kernel(NormParams p, int M) {
+  __shared__ float part[2][2][32];
+  // [2: after y, before n][4][threads] float4: the 16 columns of a thread, free of conflicts
+  extern __shared__ float4 weights[];
+  const int c = static_cast<int>(threadIdx.x) * 16;
+  const bool mine = c < p.H;
+  const int64_t stride = gridDim.x;
+  int64_t row = blockIdx.x;
+  const int nt = static_cast<int>(blockDim.x);
+  const ulonglong2* w1 = reinterpret_cast<const ulonglong2*>(weights) + threadIdx.x;
+  const ulonglong2* w2 = w1 + 4 * nt;
+  pdl_trigger();
+  pdl_wait();
+  for (int e = threadIdx.x; e < p.H; e += blockDim.x) {
+    float w = p.gamma_post ? load1(p.gamma_post, false, e) : 1.0f;
+    if (!FULL_GATE && p.gate && p.gate_col != 0)
+      w *= gate_value(load1(p.gate, p.gate_f32, e * p.gate_col), p.sigmoid);
+    float* at = reinterpret_cast<float*>(weights + (e % 16 / 4) * nt + e / 16) + e % 4;
+    at[0] = w;
+    at[16 * nt] = p.gamma_pre ? load1(p.gamma_pre, false, e) : 1.0f;
+  }
+  Raw16<HF32> hr;
+  Raw16<false> yr, gr;
+  yr.clear();
+  hr.clear();
+  if (FULL_GATE) gr.clear();
+  auto load = [&](int64_t r) {
+    if (!mine) return;
+    if (p.y) yr.load(p.y, r * p.ld_y + c);
+    hr.load(p.h, r * p.ld_h + c);
+    if (FULL_GATE) gr.load(p.gate, r * p.gate_row + c);
+  };
+  if (row < M) load(row);
+  __syncthreads();
+  for (int odd = 0; row < M; row += stride, odd ^= 1) {
+    float scale = p.branch_scale;
+    f32x2 y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = yr.get(i);
+    if (p.gamma_post) {
+      f32x2 ss = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = fmaf2(y[i], y[i], ss);
+      float lo, hi;
+      unpack2(ss, lo, hi);
+      scale *= rms_inverse(block_sum(lo + hi, part[odd][0]), p.inv_h, p.eps);
+    }
+    if (p.gate && p.gate_col == 0)
+      scale *= gate_value(load1(p.gate, p.gate_f32, row * p.gate_row), p.sigmoid);
+    const f32x2 scale2 = pack2(scale, scale), res2 = pack2(p.res_scale, p.res_scale);
+    f32x2 h[8], ss = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = mul2(hr.get(i), res2);
+    if (p.y && mine) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const ulonglong2 w = w1[k * nt];
+#pragma unroll
+        for (int i = 2 * k; i < 2 * k + 2; ++i) {
+          f32x2 u = mul2(y[i], i & 1 ? w.y : w.x);
+          if (FULL_GATE) {
+            float lo, hi;
+            unpack2(gr.get(i), lo, hi);
+            u = mul2(u, pack2(gate_value(lo, p.sigmoid), gate_value(hi, p.sigmoid)));
+          }
+          h[i] = fmaf2(scale2, u, h[i]);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (!mine) h[i] = 0;  // whatever the scales are
+      ss = fmaf2(h[i], h[i], ss);
+    }
+    if (row + stride < M) load(row + stride);
+    if (p.h_out && mine) put16<HF32>(p.h_out, row * p.ld_h_out + c, h);
+    if (!p.n && !p.q) continue;
+    float r = 1.0f;
+    if (p.gamma_pre) {
+      float lo, hi;
+      unpack2(ss, lo, hi);
+      r = rms_inverse(block_sum(lo + hi, part[odd][1]), p.inv_h, p.eps);
+      if (mine) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const ulonglong2 w = w2[k * nt];
+          h[2 * k] = mul2(h[2 * k], w.x);
+          h[2 * k + 1] = mul2(h[2 * k + 1], w.y);
+        }
+      }
+    }
+    if (p.q) {  // as store_norm_codes
+      const float d = over_448(group_amax16(h));
+      float s = d * r;
+      uint4 codes = codes16(h, d == 0.f ? 1.0f : d);
+      if (s == 0.f) s = 1.0f, codes = make_uint4(0, 0, 0, 0);
+      if (mine) {
+        *reinterpret_cast<uint4*>(p.q + row * p.ld_q + c) = codes;
+        if ((threadIdx.x & 7) == 0) p.s[row * p.G + c / 128] = s;
+      }
+    }
+    if (p.n && mine) {
+      const f32x2 r2 = pack2(r, r);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[i] = mul2(h[i], r2);
+      put16<false>(p.n, row * p.ld_n + c, h);
+    }
+  }
+}
+
+template <typename Kernel, typename... Params>
 cudaError_t launch_pdl(Kernel k, unsigned grid, unsigned block, size_t smem, cudaStream_t s,
-                       const Params& p) {
+                       const Params&... p) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(block);
@@ -500,7 +707,18 @@ cudaError_t launch_pdl(Kernel k, unsigned grid, unsigned block, size_t smem, cud
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k, p);
+  return cudaLaunchKernelEx(&cfg, k, p...);
+}
+
+template <bool HF32, bool FULL_GATE>
+cudaError_t launch_rows(const NormParams& p, int M, cudaStream_t s) {
+  const unsigned threads = (p.H / 16 + 31) / 32 * 32;
+  const size_t bytes = 128 * static_cast<size_t>(threads);
+  auto k = norm_rows_kernel<HF32, FULL_GATE>;
+  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(bytes));
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k, 2 * 152, threads, bytes, s, p, M);
 }
 
 bool aligned(const void* p, uintptr_t bytes) {
@@ -547,9 +765,9 @@ extern "C" int klt_quantize(const void* x, int32_t x_dtype, int64_t ld_x, int32_
   p.f32 = x_dtype == KLT_DT_F32;
   p.wide_x = wide(x, ld_x, esize(x_dtype), 16);
   p.wide_q = wide(q, ld_q, 1, 8);
-  // vectors throughout, and enough groups to fill the device four times over: four per half
-  // warp, which hides the load latency; else one each, which spreads them over more SMs
-  const bool many = K % 128 == 0 && p.wide_x && p.wide_q && items >= 4 * 16 * 152 * 4;
+  // vectors throughout, and enough groups to fill the device four times over: 16 values per
+  // lane and two groups in flight; else one group per half warp, spread over more SMs
+  const bool many = K % 128 == 0 && p.wide_x && wide(q, ld_q, 1, 16) && items >= 4 * 16 * 152 * 4;
   const int64_t blocks = (items + (many ? 64 : 16) - 1) / (many ? 64 : 16);
   const unsigned grid = static_cast<unsigned>(blocks);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -557,9 +775,9 @@ extern "C" int klt_quantize(const void* x, int32_t x_dtype, int64_t ld_x, int32_
   if (!many)
     e = launch_pdl(quant_kernel, grid, 256, 0, st, p);
   else if (p.f32)
-    e = launch_pdl(quant_vec_kernel<4, true>, grid, 256, 0, st, p);
+    e = launch_pdl(quant_vec_kernel<2, true>, grid, 256, 0, st, p);
   else
-    e = launch_pdl(quant_vec_kernel<4, false>, grid, 256, 0, st, p);
+    e = launch_pdl(quant_vec_kernel<2, false>, grid, 256, 0, st, p);
   return e == cudaSuccess ? KLT_OK : KLT_ERR_CUDA;
 }
 
@@ -604,6 +822,7 @@ extern "C" int klt_block_norm(const klt_block_norm_args* a, void* stream) {
   p.H = H;
   p.G = (H + 127) / 128;
   p.eps = a->eps;
+  p.inv_h = 1.0f / static_cast<float>(H);
   p.res_scale = a->res_scale;
   p.branch_scale = a->branch_scale;
   p.h_f32 = a->h_dtype == KLT_DT_F32;
@@ -633,7 +852,18 @@ extern "C" int klt_block_norm(const klt_block_norm_args* a, void* stream) {
   const size_t smem = vectors ? 0 : threads / 16 * 512;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (!vectors || plain) {
+  // Many rows: persistent blocks, two per SM (8192 x 7168, codes: XX us, one block per row
+  // 100 us); the codes of a lane are 16 bytes there.
+  const bool full = a->gate && p.gate_col != 0 && p.gate_row != 0;
+  if (M > 4 * 152 && H >= 1024 && H <= 8192 && H % 128 == 0 && p.wide_h &&
+      (!a->y || (p.wide_y && !p.y_f32)) && (!a->h_out || p.wide_h_out) && (!a->n || p.wide_n) &&
+      (!a->q || wide(a->q, a->ld_q, 1, 16)) &&
+      (!full || (p.gate_col == 1 && !p.gate_f32 && p.wide_gate))) {
+    if (p.h_f32)
+      e = full ? launch_rows<true, true>(p, M, st) : launch_rows<true, false>(p, M, st);
+    else
+      e = full ? launch_rows<false, true>(p, M, st) : launch_rows<false, false>(p, M, st);
+  } else if (!vectors || plain) {
     switch (vpt) {
       case 1: e = launch_pdl(norm_kernel<1>, grid, threads, smem, st, p); break;
       case 2: e = launch_pdl(norm_kernel<2>, grid, threads, smem, st, p); break;

@@ -202,6 +202,17 @@ KLT_DEV void tmem_wait_ld16(uint32_t* r) {
 KLT_DEV void fma2(unsigned long long& a, unsigned long long p, unsigned long long s) {
   asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(a) : "l"(p), "l"(s));
 }
+KLT_DEV unsigned long long mul2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+KLT_DEV unsigned long long fmaf2(unsigned long long a, unsigned long long b,
+                                 unsigned long long c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
 KLT_DEV void add2(unsigned long long& a, unsigned long long b) {
   asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a) : "l"(b));
 }
@@ -251,6 +262,13 @@ KLT_DEV float rescale(float& s) {
 KLT_DEV float quot_group(float x, float s, float inv) {
   const float q0 = x * inv;
   return fmaf(-fmaf(q0, s, -x), inv, q0);
+}
+// The negatives of quot_group of two values, signs of zero included, from s and -1/s in both
+// halves: a packed operation has no operand signs, a code's sign is one bit.
+KLT_DEV unsigned long long neg_quot_group2(unsigned long long x, unsigned long long s,
+                                           unsigned long long ninv) {
+  const unsigned long long q0 = mul2(x, ninv);
+  return fmaf2(fmaf2(q0, s, x), ninv, q0);
 }
 // The larger magnitude; a NaN wins over every number.
 KLT_DEV float max_nan(float a, float b) {

@@ -85,7 +85,7 @@ def _quant_ref(x32):
 
 
 @pytest.mark.parametrize("M,K,dtype,pad", [
-    (1, 128, BF16, 0), (1, 1, BF16, 0), (3, 127, F32, 0), (5, 129, BF16, 3), (16, 3584, BF16, 0),
+    (700, 7168, F32, 0), (3001, 2048, BF16, 16), (3000, 2048, BF16, 8), (1, 128, BF16, 0), (1, 1, BF16, 0), (3, 127, F32, 0), (5, 129, BF16, 3), (16, 3584, BF16, 0),
     (7, 1000, F32, 8), (33, 136, BF16, 8), (2, 8, F32, 1), (700, 7168, BF16, 0),
     (300, 4099, F32, 5)])
 def test_quantize(M, K, dtype, pad):
@@ -180,6 +180,15 @@ CASES = [  # M, H, h dtype, y dtype, gate shape, gate dtype, sigmoid, post, pre,
     (6, 640, F32, None, None, BF16, False, False, True, "nqs", 8),
     (6, 640, BF16, None, None, BF16, False, False, False, "hn", 0),
     (2, 256, BF16, BF16, "x", BF16, False, False, True, "n", 0),
+    # many rows: persistent blocks
+    (700, 1024, F32, BF16, "f", BF16, True, True, True, "hnqs", 0),
+    (613, 1152, BF16, BF16, "t", F32, True, True, True, "hnqs", 128),
+    (1300, 2048, F32, BF16, "x", BF16, False, True, True, "hnqs", 0),
+    (650, 8192, F32, BF16, "c", F32, True, False, True, "hnqs", 0),
+    (650, 1280, BF16, None, None, BF16, False, False, True, "nqs", 0),
+    (650, 1024, BF16, BF16, "f", BF16, False, True, False, "hqs", 0),
+    (620, 1408, F32, BF16, None, BF16, False, False, False, "hnqs", 0),
+    (650, 1024, BF16, F32, "f", F32, True, True, True, "hnqs", 16),
 ]
 
 
@@ -291,8 +300,9 @@ def test_block_norm_refusals():
         n(h, None, g)
     with pytest.raises(ValueError):
         n(h, h.cpu())
-    with pytest.raises(RuntimeError):
-        n(h, h, torch.zeros((3, 256), device="cuda", dtype=BF16))
+    for shape in ((3, 256), (4, 128), (4,), (1, 4, 256)):
+        with pytest.raises(ValueError):
+            n(h, h, torch.zeros(shape, device="cuda", dtype=BF16))
     with pytest.raises(B.KltError):
         n(h, h, q=B.fp8_codes(4, 256, "cuda"))  # codes without scales
     with pytest.raises(B.KltError):
