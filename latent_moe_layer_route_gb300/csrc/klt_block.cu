@@ -35,9 +35,10 @@ KLT_DEV Half half_warp(float* bufs) {
 }
 
 // This lane's eight values of columns c .. c + 127 (c < C) of the row at element `off`; those
-// past C are 0.
-KLT_DEV void load8(const Half& hw, const void* base, bool f32, int64_t off, int c, int C, bool wide,
-                   float* v) {
+// past C are 0.  In two steps, so that the loads of a whole row are in flight together: fetch8
+// as they are loaded, settle8 to their lanes.
+KLT_DEV void fetch8(const Half& hw, const void* base, bool f32, int64_t off, int c, int C,
+                    bool wide, float* v) {
   if (wide && c + 128 <= C) {
     off += c + hw.lane * 8;
     if (f32) {
@@ -55,22 +56,32 @@ KLT_DEV void load8(const Half& hw, const void* base, bool f32, int64_t off, int 
         v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
       }
     }
-    return;
+  } else if (f32) {
+    const float* p = static_cast<const float*>(base) + off + c;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = c + i * 16 + hw.lane < C ? p[i * 16 + hw.lane] : 0.f;
+  } else {
+    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(base) + off + c;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      v[i] = c + i * 16 + hw.lane < C ? __bfloat162float(p[i * 16 + hw.lane]) : 0.f;
   }
-  const float* pf = static_cast<const float*>(base) + off + c;
-  const __nv_bfloat16* pb = static_cast<const __nv_bfloat16*>(base) + off + c;
-  float t[8];
+}
+KLT_DEV void settle8(const Half& hw, int c, int C, bool wide, float* v) {
+  if (wide && c + 128 <= C) return;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int e = i * 16 + hw.lane;
-    t[i] = c + e < C ? (f32 ? pf[e] : __bfloat162float(pb[e])) : 0.f;
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) hw.buf[i * 16 + hw.lane] = t[i];
+  for (int i = 0; i < 8; ++i) hw.buf[i * 16 + hw.lane] = v[i];
   __syncwarp(hw.mask);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = hw.buf[hw.lane * 8 + i];
+  const float4 a = reinterpret_cast<const float4*>(hw.buf)[hw.lane * 2];
+  const float4 b = reinterpret_cast<const float4*>(hw.buf)[hw.lane * 2 + 1];
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+  v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
   __syncwarp(hw.mask);
+}
+KLT_DEV void load8(const Half& hw, const void* base, bool f32, int64_t off, int c, int C, bool wide,
+                   float* v) {
+  fetch8(hw, base, f32, off, c, C, wide, v);
+  settle8(hw, c, C, wide, v);
 }
 KLT_DEV void store8(const Half& hw, void* base, bool f32, int64_t off, int c, int C, bool wide,
                     const float* v) {
@@ -92,8 +103,8 @@ KLT_DEV void store8(const Half& hw, void* base, bool f32, int64_t off, int c, in
     }
     return;
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) hw.buf[hw.lane * 8 + i] = v[i];
+  reinterpret_cast<float4*>(hw.buf)[hw.lane * 2] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(hw.buf)[hw.lane * 2 + 1] = make_float4(v[4], v[5], v[6], v[7]);
   __syncwarp(hw.mask);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -201,11 +212,23 @@ typedef unsigned long long f32x2;
 template <bool F32>
 struct Raw16 {
   uint4 w[F32 ? 4 : 2];
+  // WIDE: the rows start on 32 bytes, and a lane's values are one (fp32: two) 32-byte accesses
+  template <bool WIDE = false>
   KLT_DEV void load(const void* base, int64_t off) {
-    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(base) +
-                                                    off * (F32 ? 4 : 2));
+    const char* p = static_cast<const char*>(base) + off * (F32 ? 4 : 2);
 #pragma unroll
-    for (int i = 0; i < (F32 ? 4 : 2); ++i) w[i] = p[i];
+    for (int i = 0; i < (F32 ? 4 : 2); i += 2) {
+      if (WIDE) {
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w),
+                       "=r"(w[i + 1].x), "=r"(w[i + 1].y), "=r"(w[i + 1].z), "=r"(w[i + 1].w)
+                     : "l"(p + i * 16)
+                     : "memory");
+      } else {
+        w[i] = reinterpret_cast<const uint4*>(p)[i];
+        w[i + 1] = reinterpret_cast<const uint4*>(p)[i + 1];
+      }
+    }
   }
   KLT_DEV void clear() {
 #pragma unroll
@@ -223,24 +246,27 @@ struct Raw16 {
   }
 };
 template <bool F32>
-KLT_DEV void put16(void* base, int64_t off, const f32x2* v) {
-  uint4* p = reinterpret_cast<uint4*>(static_cast<char*>(base) + off * (F32 ? 4 : 2));
+KLT_DEV void put16(void* base, int64_t off, const f32x2* v) {  // rows on 32 bytes
+  char* p = static_cast<char*>(base) + off * (F32 ? 4 : 2);
 #pragma unroll
-  for (int i = 0; i < (F32 ? 4 : 2); ++i) {
-    uint32_t t[4];
+  for (int i = 0; i < (F32 ? 2 : 1); ++i) {
+    uint32_t t[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 8; ++j) {
       float lo, hi;
       if (F32) {
-        unpack2(v[2 * i + j / 2], lo, hi);
+        unpack2(v[4 * i + j / 2], lo, hi);
         t[j] = __float_as_uint(j & 1 ? hi : lo);
       } else {
-        unpack2(v[4 * i + j], lo, hi);
+        unpack2(v[j], lo, hi);
         const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
         t[j] = *reinterpret_cast<const uint32_t*>(&b);
       }
     }
-    p[i] = make_uint4(t[0], t[1], t[2], t[3]);
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p + i * 32),
+                 "r"(t[0]), "r"(t[1]), "r"(t[2]), "r"(t[3]), "r"(t[4]), "r"(t[5]), "r"(t[6]),
+                 "r"(t[7])
+                 : "memory");
   }
 }
 // The largest magnitude of the group that this lane's eight lanes hold, NaN if it holds one.
@@ -420,8 +446,16 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) norm_kernel(NormParams 
 #pragma unroll
     for (int j = 0; j < 8; ++j) u[i][j] = h[i][j] = 0.f;
     if (c < p.H) {
-      if (p.y) load8(hw, p.y, p.y_f32, row * p.ld_y, c, p.H, p.wide_y, u[i]);
-      load8(hw, p.h, p.h_f32, row * p.ld_h, c, p.H, p.wide_h, h[i]);
+      if (p.y) fetch8(hw, p.y, p.y_f32, row * p.ld_y, c, p.H, p.wide_y, u[i]);
+      fetch8(hw, p.h, p.h_f32, row * p.ld_h, c, p.H, p.wide_h, h[i]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int c = c0 + i * step;
+    if (c < p.H) {
+      if (p.y) settle8(hw, c, p.H, p.wide_y, u[i]);
+      settle8(hw, c, p.H, p.wide_h, h[i]);
     }
   }
   float scale = p.branch_scale;
@@ -580,116 +614,109 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) norm_vec_kernel(NormPar
   }
 }
 
-// Many rows of vectors (1024 <= H <= 8192): persistent blocks, a thread 16 fixed columns.  The
-// weights of a column (gamma_post, times a gate that all rows share) wait as fp32 in shared
-// memory, and the next row is loaded while this one is finished.
-template <bool HF32, bool FULL_GATE>
-__global__ void __launch_bounds__(512, 2) norm_rows_kernel(NormParams p, int M) {
-  __shared__ float part[2][2][32];
-  // [2: after y, before n][4][threads] float4: the 16 columns of a thread, free of conflicts
-  extern __shared__ float4 weights[];
-  const int c = static_cast<int>(threadIdx.x) * 16;
-  const bool mine = c < p.H;
-  const int64_t stride = gridDim.x;
-  int64_t row = blockIdx.x;
-  const int nt = static_cast<int>(blockDim.x);
-  const ulonglong2* w1 = reinterpret_cast<const ulonglong2*>(weights) + threadIdx.x;
-  const ulonglong2* w2 = w1 + 4 * nt;
+// Many rows of vectors that start on 32 bytes: one block per row, VPT times 16 columns per
+// thread, pairs throughout.
+template <int VPT, bool HF32>
+__global__ void __launch_bounds__(512) norm_many_kernel(NormParams p) {
+  __shared__ float part[2][32];
+  const int64_t row = blockIdx.x;
+  const int c0 = static_cast<int>(threadIdx.x) * 16, step = static_cast<int>(blockDim.x) * 16;
+  Raw16<HF32> hr[VPT];
+  Raw16<false> yr[VPT], g;
   pdl_trigger();
   pdl_wait();
-  for (int e = threadIdx.x; e < p.H; e += blockDim.x) {
-    float w = p.gamma_post ? load1(p.gamma_post, false, e) : 1.0f;
-    if (!FULL_GATE && p.gate && p.gate_col != 0)
-      w *= gate_value(load1(p.gate, p.gate_f32, e * p.gate_col), p.sigmoid);
-    float* at = reinterpret_cast<float*>(weights + (e % 16 / 4) * nt + e / 16) + e % 4;
-    at[0] = w;
-    at[16 * nt] = p.gamma_pre ? load1(p.gamma_pre, false, e) : 1.0f;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int c = c0 + i * step;
+    hr[i].clear();
+    yr[i].clear();
+    if (c < p.H) {
+      if (p.y) yr[i].template load<true>(p.y, row * p.ld_y + c);
+      hr[i].template load<true>(p.h, row * p.ld_h + c);
+    }
   }
-  Raw16<HF32> hr;
-  Raw16<false> yr, gr;
-  yr.clear();
-  hr.clear();
-  if (FULL_GATE) gr.clear();
-  auto load = [&](int64_t r) {
-    if (!mine) return;
-    if (p.y) yr.load(p.y, r * p.ld_y + c);
-    hr.load(p.h, r * p.ld_h + c);
-    if (FULL_GATE) gr.load(p.gate, r * p.gate_row + c);
-  };
-  if (row < M) load(row);
-  __syncthreads();
-  for (int odd = 0; row < M; row += stride, odd ^= 1) {
-    float scale = p.branch_scale;
-    f32x2 y[8];
+  float lo, hi, scale = p.branch_scale;
+  if (p.gamma_post) {
+    f32x2 ss = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = yr.get(i);
-    if (p.gamma_post) {
-      f32x2 ss = 0;
+    for (int i = 0; i < VPT; ++i)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf2(y[i], y[i], ss);
-      float lo, hi;
-      unpack2(ss, lo, hi);
-      scale *= rms_inverse(block_sum(lo + hi, part[odd][0]), p.inv_h, p.eps);
-    }
-    if (p.gate && p.gate_col == 0)
-      scale *= gate_value(load1(p.gate, p.gate_f32, row * p.gate_row), p.sigmoid);
-    const f32x2 scale2 = pack2(scale, scale), res2 = pack2(p.res_scale, p.res_scale);
-    f32x2 h[8], ss = 0;
+      for (int j = 0; j < 8; ++j) {
+        const f32x2 v = yr[i].get(j);
+        ss = fmaf2(v, v, ss);
+      }
+    unpack2(ss, lo, hi);
+    scale *= rms_inverse(block_sum(lo + hi, part[0]), p.inv_h, p.eps);
+  }
+  if (p.gate && p.gate_col == 0)
+    scale *= gate_value(load1(p.gate, p.gate_f32, row * p.gate_row), p.sigmoid);
+  const f32x2 scale2 = pack2(scale, scale), res2 = pack2(p.res_scale, p.res_scale);
+  f32x2 h[VPT][8], ss = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = mul2(hr.get(i), res2);
-    if (p.y && mine) {
+  for (int i = 0; i < VPT; ++i) {
+    const int c = c0 + i * step;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const ulonglong2 w = w1[k * nt];
+    for (int j = 0; j < 8; ++j) h[i][j] = 0;
+    if (c < p.H) {
 #pragma unroll
-        for (int i = 2 * k; i < 2 * k + 2; ++i) {
-          f32x2 u = mul2(y[i], i & 1 ? w.y : w.x);
-          if (FULL_GATE) {
-            float lo, hi;
-            unpack2(gr.get(i), lo, hi);
-            u = mul2(u, pack2(gate_value(lo, p.sigmoid), gate_value(hi, p.sigmoid)));
+      for (int j = 0; j < 8; ++j) h[i][j] = mul2(hr[i].get(j), res2);
+      if (p.y) {
+        f32x2 u[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[j] = yr[i].get(j);
+        if (p.gamma_post) {
+          g.load(p.gamma_post, c);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) u[j] = mul2(u[j], g.get(j));
+        }
+        if (p.gate && p.gate_col != 0) {
+          g.load(p.gate, row * p.gate_row + c);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            f32x2 w = g.get(j);
+            if (p.sigmoid) {
+              unpack2(w, lo, hi);
+              w = pack2(gate_value(lo, true), gate_value(hi, true));
+            }
+            u[j] = mul2(u[j], w);
           }
-          h[i] = fmaf2(scale2, u, h[i]);
         }
-      }
-    }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (!mine) h[i] = 0;  // whatever the scales are
-      ss = fmaf2(h[i], h[i], ss);
-    }
-    if (row + stride < M) load(row + stride);
-    if (p.h_out && mine) put16<HF32>(p.h_out, row * p.ld_h_out + c, h);
-    if (!p.n && !p.q) continue;
-    float r = 1.0f;
-    if (p.gamma_pre) {
-      float lo, hi;
-      unpack2(ss, lo, hi);
-      r = rms_inverse(block_sum(lo + hi, part[odd][1]), p.inv_h, p.eps);
-      if (mine) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const ulonglong2 w = w2[k * nt];
-          h[2 * k] = mul2(h[2 * k], w.x);
-          h[2 * k + 1] = mul2(h[2 * k + 1], w.y);
-        }
+        for (int j = 0; j < 8; ++j) h[i][j] = fmaf2(scale2, u[j], h[i][j]);
       }
+      if (p.h_out) put16<HF32>(p.h_out, row * p.ld_h_out + c, h[i]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss = fmaf2(h[i][j], h[i][j], ss);
+    }
+  }
+  if (!p.n && !p.q) return;
+  float r = 1.0f;
+  if (p.gamma_pre) {
+    unpack2(ss, lo, hi);
+    r = rms_inverse(block_sum(lo + hi, part[1]), p.inv_h, p.eps);
+  }
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int c = c0 + i * step;
+    if (p.gamma_pre && c < p.H) {
+      g.load(p.gamma_pre, c);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[i][j] = mul2(h[i][j], g.get(j));
     }
     if (p.q) {  // as store_norm_codes
-      const float d = over_448(group_amax16(h));
+      const float d = over_448(group_amax16(h[i]));
       float s = d * r;
-      uint4 codes = codes16(h, d == 0.f ? 1.0f : d);
+      uint4 codes = codes16(h[i], d == 0.f ? 1.0f : d);
       if (s == 0.f) s = 1.0f, codes = make_uint4(0, 0, 0, 0);
-      if (mine) {
+      if (c < p.H) {
         *reinterpret_cast<uint4*>(p.q + row * p.ld_q + c) = codes;
         if ((threadIdx.x & 7) == 0) p.s[row * p.G + c / 128] = s;
       }
     }
-    if (p.n && mine) {
-      const f32x2 r2 = pack2(r, r);
+    if (p.n && c < p.H) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) h[i] = mul2(h[i], r2);
-      put16<false>(p.n, row * p.ld_n + c, h);
+      for (int j = 0; j < 8; ++j) h[i][j] = mul2(h[i][j], pack2(r, r));
+      put16<false>(p.n, row * p.ld_n + c, h[i]);
     }
   }
 }
@@ -708,17 +735,6 @@ cudaError_t launch_pdl(Kernel k, unsigned grid, unsigned block, size_t smem, cud
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, k, p...);
-}
-
-template <bool HF32, bool FULL_GATE>
-cudaError_t launch_rows(const NormParams& p, int M, cudaStream_t s) {
-  const unsigned threads = (p.H / 16 + 31) / 32 * 32;
-  const size_t bytes = 128 * static_cast<size_t>(threads);
-  auto k = norm_rows_kernel<HF32, FULL_GATE>;
-  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(bytes));
-  if (e != cudaSuccess) return e;
-  return launch_pdl(k, 2 * 152, threads, bytes, s, p, M);
 }
 
 bool aligned(const void* p, uintptr_t bytes) {
@@ -837,9 +853,10 @@ extern "C" int klt_block_norm(const klt_block_norm_args* a, void* stream) {
   p.wide_h_out = wide(a->h_out, a->ld_h_out, he, 16);
   p.wide_n = wide(a->n, a->ld_n, 2, 16);
   p.wide_q = wide(a->q, a->ld_q, 1, 8);
-  // few rows: one group per half warp, the shortest path through a row; many rows: more groups
-  // per half warp, so that several rows share an SM and their loads and reductions overlap
-  int vpt = M <= 2 * 152 ? 1 : 4;
+  // Up to 8 rows per SM: one group per half warp, the shortest path through a row (1021 x 2901
+  // ragged: 14.5 us, two groups 15.9, four 23.6); more: two, which leave fewer blocks to start
+  // and stop (4000 x 7001 ragged: 178 us, one group 201, four 258)
+  int vpt = M <= 8 * 152 ? 1 : 2;
   while (p.G > vpt * (vpt == 1 ? 64 : 32)) vpt *= 2;
   const int threads = ((p.G + vpt - 1) / vpt * 16 + 31) / 32 * 32;
   const unsigned grid = static_cast<unsigned>(M);
@@ -852,17 +869,24 @@ extern "C" int klt_block_norm(const klt_block_norm_args* a, void* stream) {
   const size_t smem = vectors ? 0 : threads / 16 * 512;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  // Many rows: persistent blocks, two per SM (8192 x 7168, codes: XX us, one block per row
-  // 100 us); the codes of a lane are 16 bytes there.
-  const bool full = a->gate && p.gate_col != 0 && p.gate_row != 0;
-  if (M > 4 * 152 && H >= 1024 && H <= 8192 && H % 128 == 0 && p.wide_h &&
-      (!a->y || (p.wide_y && !p.y_f32)) && (!a->h_out || p.wide_h_out) && (!a->n || p.wide_n) &&
-      (!a->q || wide(a->q, a->ld_q, 1, 16)) &&
-      (!full || (p.gate_col == 1 && !p.gate_f32 && p.wide_gate))) {
+  // Enough values to fill the device (160 x 7168: 3.6 us, eight per thread 4.6; 400 x 2048: 3.3
+  // and 2.9 us), in rows that start on 32 bytes: 16 per thread, and twice that once there are
+  // many long rows (8192 x 7168 to codes 79 and 91 us, 8192 x 2048 23.5 and 22.9 us).
+  const bool many = M > 152 && static_cast<int64_t>(M) * H > 1 << 20 && vectors && !plain &&
+                    wide(a->h, a->ld_h, he, 32) &&
+                    (!a->y || wide(a->y, a->ld_y, ye, 32)) &&
+                    (!a->h_out || wide(a->h_out, a->ld_h_out, he, 32)) &&
+                    (!a->n || wide(a->n, a->ld_n, 2, 32)) && (!a->q || wide(a->q, a->ld_q, 1, 16));
+  if (many) {
+    const bool twice = H > 8192 || (M > 8 * 152 && H > (p.h_f32 ? 6144 : 2560));
+    const int per = twice ? 32 : 16;
+    const unsigned lanes = ((H + per - 1) / per + 31) / 32 * 32;
     if (p.h_f32)
-      e = full ? launch_rows<true, true>(p, M, st) : launch_rows<true, false>(p, M, st);
+      e = twice ? launch_pdl(norm_many_kernel<2, true>, grid, lanes, 0, st, p)
+                : launch_pdl(norm_many_kernel<1, true>, grid, lanes, 0, st, p);
     else
-      e = full ? launch_rows<false, true>(p, M, st) : launch_rows<false, false>(p, M, st);
+      e = twice ? launch_pdl(norm_many_kernel<2, false>, grid, lanes, 0, st, p)
+                : launch_pdl(norm_many_kernel<1, false>, grid, lanes, 0, st, p);
   } else if (!vectors || plain) {
     switch (vpt) {
       case 1: e = launch_pdl(norm_kernel<1>, grid, threads, smem, st, p); break;
