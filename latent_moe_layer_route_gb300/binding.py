@@ -1,4 +1,4 @@
-"""Thin ctypes binding of libklt.so, with the same names as the C ABI in include/klt.h.
+"""Thin binding of libklt.so, with the same names as the C ABI in include/klt.h.
 
 Argument marshalling only: every step of the tail runs in the library's CUDA kernels.
 PyTorch supplies device memory and the stream.  There is no fallback path: if the
@@ -10,7 +10,7 @@ import ctypes
 import os
 from typing import Dict, Optional
 
-from .build import LIB_PATH
+from .build import LIB_PATH, MARSHAL_PATH
 
 KLT_OK = 0
 KLT_ERR_INVALID_ARG = 1
@@ -91,6 +91,7 @@ class KltLinearDebug(ctypes.Structure):
 
 
 _LIB: Optional[ctypes.CDLL] = None
+_marshal = None  # the CPython module of the operators around the tail, loaded with the library
 
 
 class KltError(RuntimeError):
@@ -101,10 +102,10 @@ class KltError(RuntimeError):
 
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load libklt.so (built by ``build.build()``); raises if it is missing."""
-    global _LIB
+    global _LIB, _marshal
     if _LIB is not None:
         return _LIB
-    if not os.path.exists(path):
+    if not os.path.exists(path) or not os.path.exists(MARSHAL_PATH):
         raise RuntimeError(f"libklt.so not built at {path}; run "
                            "latent_moe_layer_route_gb300.build.build() first")
     lib = ctypes.CDLL(path)
@@ -150,6 +151,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.klt_linear_status.restype = ctypes.c_int
     lib.klt_linear_destroy.argtypes = [vp]
     lib.klt_linear_destroy.restype = ctypes.c_int
+    from . import _marshal as marshal
+    _marshal = marshal
     _LIB = lib
     return lib
 
@@ -300,94 +303,8 @@ class LatentMoETail:
 
 # ---------------------------------------------------------------- operators around the tail
 #
-# The checks here are those that C cannot make of bare pointers: types, shapes, devices.  A
-# call costs about as much as its launch, so each tensor is looked at once.
-
-class _Types:
-    """torch and its dtypes, looked up on first use (this module imports without torch)."""
-    torch = None
-
-    @classmethod
-    def load(cls):
-        import torch
-        cls.bf16, cls.f32 = torch.bfloat16, torch.float32
-        cls.act = {torch.bfloat16: KLT_DT_BF16, torch.float32: KLT_DT_F32}
-        cls.codes = (torch.float8_e4m3fn, torch.uint8)
-        cls.bf16s, cls.f32s = (torch.bfloat16,), (torch.float32,)
-        cls.raw_stream = torch._C._cuda_getCurrentRawStream
-        cls.current_device = torch._C._cuda_getDevice
-        cls.torch = torch
-
-
-def _refuse(t, name: str, dtypes, rows: int, cols: int, device: int, contiguous: bool):
-    """What is wrong with an operand that did not pass its check."""
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name}: dtype {t.dtype}, not one of {tuple(dtypes)}")
-    if tuple(t.shape) != (rows, cols):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, not {(rows, cols)}")
-    if t.get_device() != device:
-        raise ValueError(f"{name}: on {t.device}, not on CUDA device {device}")
-    raise ValueError(f"{name}: not contiguous" if contiguous else
-                     f"{name}: columns are not contiguous")
-
-
-def _rows(t, name: str, dtypes, rows: int, cols: int, device: int) -> int:
-    """Check a [rows, cols] operand whose columns are contiguous; returns its row stride."""
-    ld, unit = t.stride() if t.dim() == 2 else (0, 0)
-    if t.dtype not in dtypes or t.shape != (rows, cols) or t.get_device() != device or \
-            (unit != 1 and cols > 1):
-        _refuse(t, name, dtypes, rows, cols, device, False)
-    return ld
-
-
-def _like(t, name: str, dtypes, size, device: int) -> int:
-    """As _rows, for an operand of the size of one that passed."""
-    if t.shape != size or t.dtype not in dtypes or t.get_device() != device:
-        _refuse(t, name, dtypes, size[0], size[1], device, False)
-    ld, unit = t.stride()
-    if unit != 1 and size[1] > 1:
-        _refuse(t, name, dtypes, size[0], size[1], device, False)
-    return ld
-
-
-def _broadcast(t, rows: int, cols: int):
-    """(row, column) strides of t broadcast to [rows, cols]."""
-    shape, strides = t.shape, t.stride()
-    if len(shape) < 2:
-        shape, strides = (1,) * (2 - len(shape)) + tuple(shape), (0,) * (2 - len(shape)) + strides
-    if len(shape) != 2 or shape[0] not in (1, rows) or shape[1] not in (1, cols):
-        raise ValueError(f"gate: shape {tuple(t.shape)} does not broadcast to {(rows, cols)}")
-    return (0 if shape[0] == 1 else strides[0]), (0 if shape[1] == 1 else strides[1])
-
-
-def _contiguous(t, name: str, dtypes, rows: int, cols: int, device: int):
-    if t.dtype not in dtypes or t.shape != (rows, cols) or t.get_device() != device or \
-            not t.is_contiguous():
-        _refuse(t, name, dtypes, rows, cols, device, True)
-
-
-def _device_of(t, name: str) -> int:
-    if _Types.torch is None:
-        _Types.load()
-    if not t.is_cuda:
-        raise ValueError(f"{name}: not a CUDA tensor")
-    return t.get_device()
-
-
-class _On:
-    """Makes `device` current for one call where another one is."""
-
-    def __init__(self, device: int):
-        self.guard = _Types.torch.cuda.device(device)
-
-    def __call__(self, fn, *args):
-        with self.guard:
-            return fn(*args)
-
-
-def _direct(fn, *args):
-    return fn(*args)
-
+# The checks that C cannot make of bare pointers (types, shapes, devices) and the calls are in
+# the _marshal module; what is here allocates what the caller did not give.
 
 def fp8_codes(M: int, K: int, device):
     """An uninitialised e4m3 tensor [M, K] whose rows start on 16 bytes, as the linear layer
@@ -400,25 +317,19 @@ def fp8_codes(M: int, K: int, device):
 def quantize_fp8(x, q=None, s=None, stream: Optional[int] = None):
     """e4m3 codes q [M, K] and fp32 scales s [M, ceil(K/128)] of x [M, K] (bf16 or fp32; rows
     may be strided) per row and 128 columns (klt_quantize)."""
-    T = _Types
-    dev = _device_of(x, "x")
-    if x.dim() != 2:
-        raise ValueError("x: not a matrix")
-    M, K = x.shape
-    G = -(-K // 128)
-    ld = _rows(x, "x", T.act, M, K, dev)
-    if q is None:
-        q = fp8_codes(M, K, x.device)
-    if s is None:
-        s = T.torch.empty((M, G), dtype=T.f32, device=x.device)
-    ld_q = _rows(q, "q", T.codes, M, K, dev)
-    _contiguous(s, "s", T.f32s, M, G, dev)
-    if stream is None:
-        stream = T.raw_stream(dev)
-    call = _direct if T.current_device() == dev else _On(dev)
-    rc = call((_LIB or load_library()).klt_quantize, x.data_ptr(), T.act[x.dtype], ld, M, K,
-              q.data_ptr(), ld_q, s.data_ptr(), stream)
-    if rc != KLT_OK:
+    if _LIB is None:
+        load_library()
+    if q is None or s is None:
+        import torch
+        if x.dim() != 2:
+            raise ValueError("x: not a matrix")
+        M, K = x.shape
+        if q is None:
+            q = fp8_codes(M, K, x.device)
+        if s is None:
+            s = torch.empty((M, -(-K // 128)), dtype=torch.float32, device=x.device)
+    rc = _marshal.quantize(x, q, s, stream)
+    if rc:
         raise KltError(rc, "klt_quantize")
     return q, s
 
@@ -432,22 +343,24 @@ class BlockNorm:
     def __init__(self, H: int, gamma_post=None, gamma_pre=None, eps: float = 1e-6,
                  res_scale: float = 1.0, branch_scale: float = 1.0,
                  gate_sigmoid: bool = False):
-        self.H, self._groups = H, -(-H // 128)
+        import torch
+        load_library()
+        self.H = H
         self.gamma_post, self.gamma_pre = gamma_post, gamma_pre
-        self.device = None
+        self._device = -1
         for name, g in (("gamma_post", gamma_post), ("gamma_pre", gamma_pre)):
             if g is None:
                 continue
-            dev = _device_of(g, name)
-            if g.dtype != _Types.bf16 or tuple(g.shape) != (H,) or not g.is_contiguous():
-                raise ValueError(f"{name}: not a contiguous bf16 vector of {H}")
-            if self.device is not None and dev != self.device:
+            if g.dtype != torch.bfloat16 or tuple(g.shape) != (H,) or not g.is_contiguous() \
+                    or not g.is_cuda:
+                raise ValueError(f"{name}: not a contiguous bf16 CUDA vector of {H}")
+            if self._device >= 0 and g.get_device() != self._device:
                 raise ValueError("gamma_post and gamma_pre are on different devices")
-            self.device = dev
+            self._device = g.get_device()
         self._args = KltBlockNormArgs(H=H, gate_sigmoid=int(gate_sigmoid), eps=eps,
                                       res_scale=res_scale, branch_scale=branch_scale,
                                       gamma_post=_ptr(gamma_post), gamma_pre=_ptr(gamma_pre))
-        self._lib = load_library()
+        self._address = ctypes.addressof(self._args)
 
     def forward(self, h, y=None, gate=None, *, h_out=None, n=None, q=None, s=None,
                 stream: Optional[int] = None):
@@ -456,53 +369,13 @@ class BlockNorm:
         dtype; may be h), n (bf16; may be y), q and s (e4m3 codes and fp32 scales of n);
         when none is given, h_out (with y) and n are allocated.  Without y the norm after
         the block is skipped.  Returns (h_out, n, q, s)."""
-        T = _Types
-        act = T.act
-        dev = _device_of(h, "h")
-        if self.device is not None and dev != self.device:
-            raise ValueError("h: not on the weights' device")
-        size = h.shape
-        M, H = size[0], self.H
-        a = KltBlockNormArgs.from_buffer_copy(self._args)
-        a.M = M
-        a.ld_h = _rows(h, "h", act, M, H, dev)
-        a.h_dtype = act[h.dtype]
-        a.h = h.data_ptr()
         if h_out is None and n is None and q is None and s is None:
+            import torch
             if y is not None:
-                h_out = T.torch.empty((M, H), dtype=h.dtype, device=h.device)
-            n = T.torch.empty((M, H), dtype=T.bf16, device=h.device)
-        if y is not None:
-            a.ld_y = _like(y, "y", act, size, dev)
-            a.y_dtype = act[y.dtype]
-            a.y = y.data_ptr()
-            if gate is not None:
-                if gate.dtype not in act or gate.get_device() != dev:
-                    raise ValueError("gate: not a bf16 or fp32 tensor on h's device")
-                a.gate_row, a.gate_col = _broadcast(gate, M, H)
-                a.gate_dtype = act[gate.dtype]
-                a.gate = gate.data_ptr()
-        else:
-            if gate is not None:
-                raise ValueError("gate: given without y")
-            a.gamma_post = None
-        if h_out is not None:
-            a.ld_h_out = _like(h_out, "h_out", (h.dtype,), size, dev)
-            a.h_out = h_out.data_ptr()
-        if n is not None:
-            a.ld_n = _like(n, "n", T.bf16s, size, dev)
-            a.n = n.data_ptr()
-        if q is not None:
-            a.ld_q = _like(q, "q", T.codes, size, dev)
-            a.q = q.data_ptr()
-        if s is not None:
-            _contiguous(s, "s", T.f32s, M, self._groups, dev)
-            a.s = s.data_ptr()
-        if stream is None:
-            stream = T.raw_stream(dev)
-        call = _direct if T.current_device() == dev else _On(dev)
-        rc = call(self._lib.klt_block_norm, a, stream)
-        if rc != KLT_OK:
+                h_out = torch.empty((h.shape[0], self.H), dtype=h.dtype, device=h.device)
+            n = torch.empty((h.shape[0], self.H), dtype=torch.bfloat16, device=h.device)
+        rc = _marshal.block_norm(self._address, self._device, h, y, gate, h_out, n, q, s, stream)
+        if rc:
             raise KltError(rc, "klt_block_norm")
         return h_out, n, q, s
 
@@ -517,62 +390,55 @@ class Fp8Linear:
     "swiglu" (gate rows first; N/2 outputs); out "bf16", "f32" or, for SwiGLU, "fp8"."""
 
     def __init__(self, w_q, w_s, act: str = "none", out: str = "bf16"):
-        T = _Types
+        import torch
         self.handle = None
+        self._lib = load_library()
         acts = {"none": KLT_ACT_NONE, "swiglu": KLT_ACT_SWIGLU}
         outs = {"bf16": KLT_DT_BF16, "f32": KLT_DT_F32, "fp8": KLT_DT_E4M3}
         if act not in acts or out not in outs:
             raise ValueError(f"act {act!r}, out {out!r}: not known")
-        self.device = _device_of(w_q, "w_q")
-        if w_q.dim() != 2:
-            raise ValueError("w_q: not a matrix")
+        if w_q.dim() != 2 or w_q.dtype not in (torch.float8_e4m3fn, torch.uint8) or \
+                not w_q.is_cuda or not w_q.is_contiguous():
+            raise ValueError("w_q: not a contiguous CUDA matrix of e4m3 codes")
+        self.device = w_q.get_device()
         self.N, self.K = w_q.shape
-        _contiguous(w_q, "w_q", T.codes, self.N, self.K, self.device)
-        self._groups = -(-self.K // 128)
-        _contiguous(w_s, "w_s", T.f32s, -(-self.N // 128), self._groups, self.device)
+        blocks = (-(-self.N // 128), -(-self.K // 128))
+        if tuple(w_s.shape) != blocks or w_s.dtype != torch.float32 or \
+                w_s.get_device() != self.device or not w_s.is_contiguous():
+            raise ValueError(f"w_s: not a contiguous fp32 matrix {blocks} on the weights' device")
         self.width = self.N // 2 if act == "swiglu" else self.N
         self.fp8 = out == "fp8"
-        self._out = T.codes if self.fp8 else T.f32s if out == "f32" else T.bf16s
-        self._lib = load_library()
+        self._dtype = outs[out]
+        self._torch_dtype = torch.float32 if out == "f32" else torch.bfloat16
         d = KltLinearDims(self.N, self.K, acts[act], outs[out])
         h = ctypes.c_void_p()
         # the create copies on the legacy default stream; what wrote the weights may have run
         # on another
-        T.torch.cuda.current_stream(self.device).synchronize()
-        with T.torch.cuda.device(self.device):
+        torch.cuda.current_stream(self.device).synchronize()
+        with torch.cuda.device(self.device):
             rc = self._lib.klt_linear_create(ctypes.byref(d), w_q.data_ptr(), w_s.data_ptr(),
                                              ctypes.byref(h))
         if rc != KLT_OK:
             raise KltError(rc, "klt_linear_create")
         self.handle = h
+        self._address = h.value
 
     def forward(self, xq, xs, out=None, out_s=None, stream: Optional[int] = None,
                 debug: Optional[KltLinearDebug] = None):
         """xq e4m3 (or uint8) [M, K] whose rows start on 16 bytes, xs fp32 [M, ceil(K/128)].
         Returns out [M, N] (SwiGLU: [M, N/2]), or (codes, scales) with out "fp8"."""
-        T = _Types
-        dev = self.device
-        M, K, width = xq.shape[0], self.K, self.width
-        ld = _rows(xq, "xq", T.codes, M, K, dev)
-        if M <= 1:  # the stride of a single row says nothing
-            ld = -(-K // 16) * 16
-        _contiguous(xs, "xs", T.f32s, M, self._groups, dev)
-        if out is None:
-            out = fp8_codes(M, width, xq.device) if self.fp8 else \
-                T.torch.empty((M, width), dtype=self._out[0], device=xq.device)
-        ld_out = _rows(out, "out", self._out, M, width, dev)
-        scales = None
-        if self.fp8:
-            if out_s is None:
-                out_s = T.torch.empty((M, width // 128), dtype=T.f32, device=xq.device)
-            _contiguous(out_s, "out_s", T.f32s, M, width // 128, dev)
-            scales = out_s.data_ptr()
-        if stream is None:
-            stream = T.raw_stream(dev)
-        call = _direct if T.current_device() == dev else _On(dev)
-        rc = call(self._lib.klt_linear_forward, self.handle, xq.data_ptr(), ld, xs.data_ptr(), M,
-                  out.data_ptr(), ld_out, scales, debug, stream)
-        if rc != KLT_OK:
+        if out is None or (self.fp8 and out_s is None):
+            import torch
+            M = xq.shape[0]
+            if out is None:
+                out = fp8_codes(M, self.width, xq.device) if self.fp8 else \
+                    torch.empty((M, self.width), dtype=self._torch_dtype, device=xq.device)
+            if self.fp8 and out_s is None:
+                out_s = torch.empty((M, self.width // 128), dtype=torch.float32,
+                                    device=xq.device)
+        rc = _marshal.linear(self._address, self.device, self.K, self.width, self._dtype, xq, xs,
+                             out, out_s, 0 if debug is None else ctypes.addressof(debug), stream)
+        if rc:
             raise KltError(rc, "klt_linear_forward")
         return (out, out_s) if self.fp8 else out
 
@@ -588,7 +454,7 @@ class Fp8Linear:
     def close(self):
         if self.handle is not None and self.handle.value:
             self._lib.klt_linear_destroy(self.handle)
-        self.handle = None
+        self.handle, self._address = None, 0
 
     def __del__(self):
         try:

@@ -3,7 +3,8 @@
 Each .cu file compiles to an object in parallel, then one shared-library link.  The
 library links the CUDA runtime dynamically and reaches the driver's tensor-map encoder
 through the runtime's entry-point query, so it loads on a machine without a GPU driver
-(its entry points then fail with a CUDA status instead of refusing to load).
+(its entry points then fail with a CUDA status instead of refusing to load).  A small CPython
+module beside it marshals the arguments of the operators around the tail.
 """
 from __future__ import annotations
 
@@ -11,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -18,6 +20,7 @@ ROOT = os.path.dirname(PKG_DIR)
 CSRC = os.path.join(PKG_DIR, "csrc")
 OUT_DIR = os.path.join(PKG_DIR, "_build")
 LIB_PATH = os.path.join(PKG_DIR, "libklt.so")
+MARSHAL_PATH = os.path.join(PKG_DIR, "_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))
 SOURCES = ["klt_api.cu", "klt_route.cu", "klt_gemm.cu", "klt_wide.cu", "klt_noalloc.cu",
            "klt_block.cu", "klt_linear.cu", "klt_linear_narrow.cu", "klt_linear_wide.cu"]
 HEADERS = ["klt_device.cuh", "klt_internal.h", "klt_linear.cuh"]
@@ -66,6 +69,15 @@ def build(verbose: bool = False, force: bool = False, ptxas_info: bool = False) 
         res = subprocess.run(cmd, capture_output=True, text=True)
         if res.returncode != 0:
             raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
+    marshal = os.path.join(CSRC, "klt_marshal.cpp")
+    if force or _stale(MARSHAL_PATH, [marshal, LIB_PATH]):
+        cmd = [nvcc, "-O2", "-std=c++17", "-shared", "-cudart", "shared", "-Xcompiler",
+               "-fPIC,-Wall", "-I" + sysconfig.get_paths()["include"], marshal, "-o",
+               MARSHAL_PATH, "-L" + PKG_DIR, "-Xlinker", "-l:libklt.so", "-Xlinker",
+               "-rpath=$ORIGIN"]
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError(f"nvcc failed for klt_marshal.cpp:\n{res.stdout}\n{res.stderr}")
     return LIB_PATH
 
 
