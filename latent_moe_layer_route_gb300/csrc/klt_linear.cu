@@ -263,11 +263,12 @@ int klt_linear_forward(klt_linear* h, const uint8_t* xq, int64_t ld_xq, const fl
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (tile == 256) {
-    // 32 rows x 64 bytes are stored at a time, where the output's rows allow bulk copies
+    // 32 rows x 128 bytes (64 of codes) are stored at a time, where the rows allow bulk copies
     CUtensorMap omap = {};
     if (p.out_wide &&
         !encode_bytes(&omap, out, M, width * es, M > 1 ? ld_out * es : (width * es + 15) / 16 * 16,
-                      64, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+                      codes ? 64 : 128, 32,
+                      codes ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B))
       return KLT_ERR_CUDA;
     e = launch_linear_wide(tok, h->wmap, omap, p, act, split, h->num_sms, s);
   } else {

@@ -30,6 +30,7 @@ struct Narrow {
   // warps: epilogue (two per TMEM quadrant, half of the columns each, from 32 columns on),
   // then copies, then MMA
   static constexpr int EPI = COLS >= 32 ? 8 : 4;
+  static constexpr bool ALONE = COLS == 128 && BN >= 64;  // one CTA per SM
   static constexpr int THREADS = (EPI + 2) * 32;
   static constexpr int WC = COLS * 4 / EPI;         // columns of a warp
   static constexpr int CHUNK = WC >= 32 ? 32 : 16;  // loaded at a time
@@ -147,9 +148,16 @@ __global__ void __launch_bounds__(Narrow<BN, ACT>::THREADS)
         tma_load_2d(ring + st * C::STAGE_BYTES + C::AT * LIN_TILE_BYTES, &tok, &full[st],
                     (k0 + i) * 128, t0, keep);
       };
-      // the weights are nobody's output: their first copies do not wait for the launch before
+      // The weights are nobody's output: their first copies do not wait for the launch before,
+      // and where that one's CTAs leave room for these, the others are already on their way to
+      // L2 (16 x 4096 x 7168 SwiGLU 8.4 -> 7.2 us).
       const int pre = n < C::STAGES ? n : C::STAGES;
       for (int i = 0; i < pre; ++i) weights(i, i);
+      if (!C::ALONE && blockIdx.y == 0)
+        for (int a = 0; a < C::AT && pre < n; ++a)
+          bulk_prefetch_l2(
+              p.w + (static_cast<int64_t>(rb + a * p.up) * p.KB + k0 + pre) * LIN_TILE_BYTES,
+              (n - pre) * LIN_TILE_BYTES);
       pdl_wait();
       for (int i = 0; i < pre; ++i) tokens(i, i);
       int st = pre % C::STAGES, ph = pre / C::STAGES, i = pre;

@@ -26,8 +26,8 @@ constexpr int THREADS = 384;  // warps 0 copies, 1 MMA, 2 TMEM, 3 idle, 4-11 epi
 constexpr int STAGES = 5;
 constexpr int STAGE_BYTES = 2 * LIN_TILE_BYTES;
 constexpr int RING_BYTES = STAGES * STAGE_BYTES;
-constexpr int BOX_BYTES = 32 * 64;         // stored at a time by a warp: 32 rows x 64 bytes
-constexpr int BOXES = 4;                   // per epilogue warp
+constexpr int BOX_BYTES = 32 * 128;        // stored at a time by a warp: 32 rows x 128 bytes
+constexpr int BOXES = 2;                   // per epilogue warp
 constexpr int OUT_BYTES = 8 * BOXES * BOX_BYTES;
 constexpr int PART_BYTES = 32 * 128 * 4;  // a warp's 32 rows x 128 columns, fp32
 constexpr int AMAX_BYTES = 2 * 128 * 4;
@@ -42,19 +42,21 @@ struct Smem {
   volatile int* abort_flag;
 };
 
-// The output leaves through a warp's four boxes of 32 rows x 64 bytes: staged in the output
-// map's swizzle (no bank conflicts) and stored by bulk copies, which cut off what lies outside
-// the output and run on while the warp goes on.  Lane b issues the copy of box b.
+// The output leaves through a warp's two boxes of 32 rows x 128 bytes (codes: one of 64 bytes):
+// staged in the output map's swizzle (no bank conflicts) and stored by bulk copies, which cut
+// off what lies outside the output and run on while the warp goes on.  Few and large ones: the
+// copies queue behind the loads, some 400 cycles each.  Lane b issues the copy of box b.
 KLT_DEV void boxes_free() {  // the warp's copies have read their boxes
   tma_store_wait_read<0>();
   __syncwarp();
 }
-// This thread's 64 bytes (w) of row `lane` of a box.
+// This thread's BYTES (64 or 128, in w) of row `lane` of a box.
+template <int BYTES>
 KLT_DEV void fill_box(uint8_t* box, const uint32_t* w) {
-  const int lane = lane_id(), x = (lane >> 1) & 3;
+  const int lane = lane_id(), x = BYTES == 128 ? lane & 7 : (lane >> 1) & 3;
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    *reinterpret_cast<uint4*>(box + lane * 64 + (j ^ x) * 16) =
+  for (int j = 0; j < BYTES / 16; ++j)
+    *reinterpret_cast<uint4*>(box + lane * BYTES + (j ^ x) * 16) =
         make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
 }
 // Stores the filled boxes to rows m0 .. m0 + 31: lane b holds box b's byte column, or one that
@@ -77,35 +79,33 @@ KLT_DEV void store_rows(const LinParams& p, const CUtensorMap* omap, uint8_t* bo
     for (int g = 0; g < COUNT; ++g) {
       boxes_free();
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        uint32_t w[16];
+      for (int b = 0; b < 2; ++b) {
+        uint32_t w[32];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          w[2 * i] = static_cast<uint32_t>(v[g][b * 8 + i]);
-          w[2 * i + 1] = static_cast<uint32_t>(v[g][b * 8 + i] >> 32);
+        for (int i = 0; i < 16; ++i) {
+          w[2 * i] = static_cast<uint32_t>(v[g][b * 16 + i]);
+          w[2 * i + 1] = static_cast<uint32_t>(v[g][b * 16 + i] >> 32);
         }
-        fill_box(boxes + b * BOX_BYTES, w);
+        fill_box<128>(boxes + b * BOX_BYTES, w);
       }
-      store_boxes(boxes, omap, lane < 4 ? (c + g * 128 + lane * 16) * 4 : p.width * 4,
+      store_boxes(boxes, omap, lane < 2 ? (c + g * 128 + lane * 32) * 4 : p.width * 4,
                   p.width * 4, m0);
     }
   } else if (p.out_wide) {
     boxes_free();
 #pragma unroll
-    for (int b = 0; b < 2 * COUNT; ++b) {
-      uint32_t w[16];
+    for (int b = 0; b < COUNT; ++b) {
+      uint32_t w[32];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
+      for (int i = 0; i < 32; ++i) {
         float lo, hi;
-        unpack2(v[b >> 1][(b & 1) * 16 + i], lo, hi);
+        unpack2(v[b][i], lo, hi);
         const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
         w[i] = *reinterpret_cast<const uint32_t*>(&t);
       }
-      fill_box(boxes + b * BOX_BYTES, w);
+      fill_box<128>(boxes + b * BOX_BYTES, w);
     }
-    store_boxes(boxes, omap,
-                lane < 2 * COUNT ? (c + (lane >> 1) * 128 + (lane & 1) * 32) * 2 : p.width * 2,
-                p.width * 2, m0);
+    store_boxes(boxes, omap, lane < COUNT ? (c + lane * 128) * 2 : p.width * 2, p.width * 2, m0);
   } else {
     // rows that are not vectors: 64 columns at a time through the boxes, then row by row,
     // neighbouring lanes neighbouring columns (each thread its own row: 1003 x 777 fp32 spent
@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int c = tn0 * 128 + half * 64;
             if (p.out_wide) {
               boxes_free();
-              fill_box(boxes, w);
+              fill_box<64>(boxes, w);
               store_boxes(boxes, &omap, lane == 0 ? c : p.width, p.width, m0);
             } else if (m < p.M) {
               uint8_t* o = static_cast<uint8_t*>(p.out) + static_cast<int64_t>(m) * p.ld_out + c;
