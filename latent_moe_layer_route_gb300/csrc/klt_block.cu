@@ -737,6 +737,11 @@ cudaError_t launch_pdl(Kernel k, unsigned grid, unsigned block, size_t smem, cud
   return cudaLaunchKernelEx(&cfg, k, p...);
 }
 
+int status_of(cudaError_t e) {
+  if (e == cudaSuccess) return KLT_OK;
+  cudaGetLastError();  // reported here, not to the caller's next call
+  return KLT_ERR_CUDA;
+}
 bool aligned(const void* p, uintptr_t bytes) {
   return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0;
 }
@@ -794,7 +799,7 @@ extern "C" int klt_quantize(const void* x, int32_t x_dtype, int64_t ld_x, int32_
     e = launch_pdl(quant_vec_kernel<2, true>, grid, 256, 0, st, p);
   else
     e = launch_pdl(quant_vec_kernel<2, false>, grid, 256, 0, st, p);
-  return e == cudaSuccess ? KLT_OK : KLT_ERR_CUDA;
+  return status_of(e);
 }
 
 extern "C" int klt_block_norm(const klt_block_norm_args* a, void* stream) {
@@ -906,5 +911,5 @@ extern "C" int klt_block_norm(const klt_block_norm_args* a, void* stream) {
       default: e = launch_pdl(norm_vec_kernel<4, false>, grid, threads, 0, st, p); break;
     }
   }
-  return e == cudaSuccess ? KLT_OK : KLT_ERR_CUDA;
+  return status_of(e);
 }

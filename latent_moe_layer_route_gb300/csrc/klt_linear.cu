@@ -141,7 +141,7 @@ void choose(const klt_linear* h, int M, int* tile, int* split) {
   const int64_t pairs = h->num_sms / 2;
   const double wide = (tiles + pairs - 1) / pairs * (1.5 + 0.43 * h->KB);
   const double shared = tiles <= h->max_tiles && h->KB >= 4 ? 5.0 + 0.43 * h->KB / 2 : wide;
-  if (narrow < wide && narrow < shared) return;
+  if (narrow < wide && narrow < shared && M <= 65535) return;
   *tile = 256;
   *split = shared < wide ? 2 : 1;
 }
@@ -235,6 +235,7 @@ int klt_linear_forward(klt_linear* h, const uint8_t* xq, int64_t ld_xq, const fl
     if (dbg->force_split) split = dbg->force_split;
     if (split != 1 && split != 2 && split != 4 && split != 8) return KLT_ERR_INVALID_ARG;
     if (split > h->KB || (tile == 256 && split > 2)) return KLT_ERR_UNSUPPORTED;
+    if (tile < 256 && (M + tile - 1) / tile > 65535) return KLT_ERR_UNSUPPORTED;
   }
 
   LinParams p = {};
@@ -274,7 +275,9 @@ int klt_linear_forward(klt_linear* h, const uint8_t* xq, int64_t ld_xq, const fl
   } else {
     e = launch_linear_narrow(tok, p, tile, split, act, s);
   }
-  return e == cudaSuccess ? KLT_OK : KLT_ERR_CUDA;
+  if (e == cudaSuccess) return KLT_OK;
+  cudaGetLastError();  // reported here, not to the caller's next call
+  return KLT_ERR_CUDA;
 }
 
 int klt_linear_tile(const klt_linear* h, int32_t M) {

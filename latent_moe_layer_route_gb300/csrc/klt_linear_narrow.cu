@@ -24,7 +24,7 @@ template <int BN, int ACT>
 struct Narrow {
   static constexpr int AT = ACT ? 2 : 1;  // weight tiles per k-block
   static constexpr int STAGE_BYTES = AT * LIN_TILE_BYTES + BN * 128;
-  static constexpr int SLOTS = 4;  // with two, 128 tokens took 652 cycles per k-block
+  static constexpr int SLOTS = 4;  // products on their way from the MMA to the registers
   static constexpr int COLS = AT * BN;  // columns of a slot: token t of tile a at a * BN + t
   static constexpr int TMEM_COLS = SLOTS * COLS;  // a power of two, 64 .. 512
   // warps: epilogue (two per TMEM quadrant, half of the columns each, from 32 columns on),
@@ -153,11 +153,12 @@ __global__ void __launch_bounds__(Narrow<BN, ACT>::THREADS)
       // L2 (16 x 4096 x 7168 SwiGLU 8.4 -> 7.2 us).
       const int pre = n < C::STAGES ? n : C::STAGES;
       for (int i = 0; i < pre; ++i) weights(i, i);
-      if (!C::ALONE && blockIdx.y == 0)
-        for (int a = 0; a < C::AT && pre < n; ++a)
+      const int ahead = n - pre < 32 ? n - pre : 32;
+      if (!C::ALONE && blockIdx.y == 0 && ahead > 0)
+        for (int a = 0; a < C::AT; ++a)
           bulk_prefetch_l2(
               p.w + (static_cast<int64_t>(rb + a * p.up) * p.KB + k0 + pre) * LIN_TILE_BYTES,
-              (n - pre) * LIN_TILE_BYTES);
+              ahead * LIN_TILE_BYTES);
       pdl_wait();
       for (int i = 0; i < pre; ++i) tokens(i, i);
       int st = pre % C::STAGES, ph = pre / C::STAGES, i = pre;

@@ -265,6 +265,29 @@ def test_block_norm_in_place_and_allocating():
     assert (np.abs(_f64(n0) - ref[2]) <= HALF[BF16] * np.abs(ref[2]) + 1.01 * ref[3]).all()
 
 
+@pytest.mark.parametrize("M,H", [(40, 333), (300, 1029), (2000, 512)])
+def test_block_norm_chain_in_place(M, H):
+    """A residual stream updated in place by many calls in a row, whose rows share cache lines
+    (odd widths): launches overlap, and each sees what the one before wrote."""
+    rng = _gen(9, M, H)
+    g = _cuda(rng.uniform(0.5, 1.5, H), BF16)
+    y = _cuda(rng.standard_normal((M, H)), BF16)
+    layer = B.BlockNorm(H, g, g, res_scale=0.9, branch_scale=0.7)
+
+    def chain(sync):
+        h, n = _cuda(_gen(10).standard_normal((M, H)), BF16), y.clone()
+        for _ in range(60):
+            layer(h, n, h_out=h, n=n)
+            if sync:
+                torch.cuda.synchronize()
+        return h, n
+
+    want = chain(True)
+    for _ in range(3):
+        got = chain(False)
+        assert _same(got[0], want[0]) and _same(got[1], want[1])
+
+
 def test_block_norm_zero_and_non_finite_rows():
     M, H = 4, 384
     h = torch.zeros((M, H), device="cuda")
