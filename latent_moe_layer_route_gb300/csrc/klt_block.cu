@@ -11,6 +11,7 @@
 // e4m3 once each, n from the unrounded h' (one rounding on each path, not two in a row).
 #include "klt_linear.cuh"
 
+
 #include "../../include/klt.h"
 
 namespace klt {
@@ -209,6 +210,102 @@ KLT_DEV void put8(void* base, int64_t off, const float* v) {
 // by more of them, and an instruction does two.
 typedef unsigned long long f32x2;
 
+// t[0 .. N-1] = the N words from byte `bytes` (0 .. 15) of t[0 .. N+3] on.
+template <int N>
+KLT_DEV void shift_words(uint32_t* t, int bytes) {
+  if (bytes & 8) {
+#pragma unroll
+    for (int i = 0; i < N + 2; ++i) t[i] = t[i + 2];
+  }
+  if (bytes & 4) {
+#pragma unroll
+    for (int i = 0; i < N + 1; ++i) t[i] = t[i + 1];
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) t[i] = __funnelshift_r(t[i], t[i + 1], (bytes & 3) * 8);
+}
+
+KLT_DEV int clamp16(int64_t x) { return x < 0 ? 0 : x > 16 ? 16 : static_cast<int>(x); }
+// Bytes [first, last) of the aligned vector at v, of elements of two bytes or more; the others
+// are 0, and not read.  A front or a back part is read in pieces of 8, 4 and 2 bytes.
+KLT_DEV uint4 load_part(const char* v, int first, int last) {
+  uint4 q = make_uint4(0, 0, 0, 0);
+  if (first >= last) return q;
+  if (first == 0) {
+    const uint32_t x = last & 4 ? *reinterpret_cast<const uint32_t*>(v + (last & 8)) : 0;
+    const uint32_t y = last & 2 ? *reinterpret_cast<const uint16_t*>(v + (last & 12)) : 0;
+    const uint32_t a = last & 4 ? x : y, b = last & 4 ? y : 0;
+    if (last & 8) {
+      const uint2 u = *reinterpret_cast<const uint2*>(v);
+      q = make_uint4(u.x, u.y, a, b);
+    } else {
+      q.x = a, q.y = b;
+    }
+  } else if (last == 16) {
+    const int n = 16 - first;
+    const uint32_t x = n & 4 ? *reinterpret_cast<const uint32_t*>(v + 16 - (n & 12)) : 0;
+    const uint32_t y = n & 2 ? *reinterpret_cast<const uint16_t*>(v + 16 - (n & 14)) << 16 : 0;
+    const uint32_t b = n & 4 ? x : y, a = n & 4 ? y : 0;
+    if (n & 8) {
+      const uint2 u = *reinterpret_cast<const uint2*>(v + 8);
+      q = make_uint4(a, b, u.x, u.y);
+    } else {
+      q.z = a, q.w = b;
+    }
+  } else {
+    uint32_t t[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (2 * e >= first && 2 * e < last)
+        t[e / 2] |= reinterpret_cast<const uint16_t*>(v)[e] << e % 2 * 16;
+    q = make_uint4(t[0], t[1], t[2], t[3]);
+  }
+  return q;
+}
+// The same, written; elements of ES bytes.
+template <int ES>
+KLT_DEV void store_part(char* v, int first, int last, uint4 q) {
+  if (first >= last) return;
+  if (first == 0) {
+    if (last & 8) {
+      *reinterpret_cast<uint2*>(v) = make_uint2(q.x, q.y);
+      q.x = q.z, q.y = q.w;
+    }
+    if (last & 4) {
+      *reinterpret_cast<uint32_t*>(v + (last & 8)) = q.x;
+      q.x = q.y;
+    }
+    if (ES <= 2 && last & 2) {
+      *reinterpret_cast<uint16_t*>(v + (last & 12)) = static_cast<uint16_t>(q.x);
+      q.x >>= 16;
+    }
+    if (ES == 1 && last & 1)
+      *reinterpret_cast<uint8_t*>(v + (last & 14)) = static_cast<uint8_t>(q.x);
+  } else if (last == 16) {
+    const int n = 16 - first;
+    if (n & 8) {
+      *reinterpret_cast<uint2*>(v + 8) = make_uint2(q.z, q.w);
+      q.z = q.x, q.w = q.y;
+    }
+    if (n & 4) {
+      *reinterpret_cast<uint32_t*>(v + 16 - (n & 12)) = q.w;
+      q.w = q.z;
+    }
+    if (ES <= 2 && n & 2) {
+      *reinterpret_cast<uint16_t*>(v + 16 - (n & 14)) = static_cast<uint16_t>(q.w >> 16);
+      q.w <<= 16;
+    }
+    if (ES == 1 && n & 1)
+      *reinterpret_cast<uint8_t*>(v + 16 - n) = static_cast<uint8_t>(q.w >> 24);
+  } else {
+    const uint32_t t[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      if (e >= first && e < last)
+        reinterpret_cast<uint8_t*>(v)[e] = static_cast<uint8_t>(t[e / 4] >> e % 4 * 8);
+  }
+}
+
 template <bool F32>
 struct Raw16 {
   uint4 w[F32 ? 4 : 2];
@@ -233,6 +330,28 @@ struct Raw16 {
   KLT_DEV void clear() {
 #pragma unroll
     for (int i = 0; i < (F32 ? 4 : 2); ++i) w[i] = make_uint4(0, 0, 0, 0);
+  }
+  // Columns c .. c + 15 of a row of C that starts on any element; those past C are 0.  From
+  // the aligned vectors that hold them, of which only what lies inside the row is read.
+  KLT_DEV void load_any(const void* row, int c, int C) {
+    constexpr int N = F32 ? 16 : 8;  // words
+    const char* lo = static_cast<const char*>(row);
+    const char *hi = lo + static_cast<int64_t>(C) * (F32 ? 4 : 2), *at = lo + c * (F32 ? 4 : 2);
+    const int r = static_cast<int>(reinterpret_cast<uintptr_t>(at) & 15);
+    uint32_t t[N + 4];
+#pragma unroll
+    for (int i = 0; i < N / 4 + 1; ++i) {
+      if (i < N / 4 || r) {
+        const char* v = at - r + 16 * i;
+        const uint4 q = v >= lo && v + 16 <= hi ? *reinterpret_cast<const uint4*>(v)
+                                                : load_part(v, clamp16(lo - v), clamp16(hi - v));
+        t[4 * i] = q.x, t[4 * i + 1] = q.y, t[4 * i + 2] = q.z, t[4 * i + 3] = q.w;
+      }
+    }
+    if (r) shift_words<N>(t, r);
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i)
+      w[i] = make_uint4(t[4 * i], t[4 * i + 1], t[4 * i + 2], t[4 * i + 3]);
   }
   KLT_DEV f32x2 get(int i) const {  // values 2i and 2i + 1
     if (F32) {
@@ -267,6 +386,88 @@ KLT_DEV void put16(void* base, int64_t off, const f32x2* v) {  // rows on 32 byt
                  "r"(t[0]), "r"(t[1]), "r"(t[2]), "r"(t[3]), "r"(t[4]), "r"(t[5]), "r"(t[6]),
                  "r"(t[7])
                  : "memory");
+  }
+}
+// Columns of a row of C that starts on any element: the whole warp's, NW words (16 elements of
+// ES bytes) per lane from column c on; those past C are not written.  Each lane writes the vectors
+// that end inside its own words, and takes their fronts from its neighbour; the warp's first and
+// last vectors and the row's last are written in part.
+template <int NW, int ES>
+KLT_DEV void store_any(void* row, int c, int C, const uint32_t* w) {
+  const int lane = threadIdx.x & 31;
+  char* at = static_cast<char*>(row) + static_cast<int64_t>(c) * ES;
+  const int r = static_cast<int>(reinterpret_cast<uintptr_t>(at) & 15);
+  // of the vector at `at - r`: the bytes from the warp's first on, to the row's end
+  const int first = lane == 0 ? r : 0, end = (C - c) * ES + r;
+  char* v = at - r;
+  uint32_t t[NW + 4];
+#pragma unroll
+  for (int i = 0; i < NW; ++i) t[i] = w[i];
+  if (r) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t[i] = __shfl_up_sync(0xFFFFFFFFu, w[NW - 4 + i], 1);
+#pragma unroll
+    for (int i = 0; i < NW; ++i) t[4 + i] = w[i];
+    shift_words<NW>(t, 16 - r);
+  }
+#pragma unroll
+  for (int k = 0; k < NW / 4; ++k) {
+    const uint4 q = make_uint4(t[4 * k], t[4 * k + 1], t[4 * k + 2], t[4 * k + 3]);
+    if ((k > 0 || first == 0) && end >= 16 * k + 16)
+      *reinterpret_cast<uint4*>(v + 16 * k) = q;
+    else
+      store_part<ES>(v + 16 * k, k ? 0 : first, clamp16(end - 16 * k), q);
+  }
+  if (r && lane == 31) {
+    uint32_t z[8] = {w[NW - 4], w[NW - 3], w[NW - 2], w[NW - 1], 0, 0, 0, 0};
+    shift_words<4>(z, 16 - r);
+    const int last = end - NW * 4;
+    store_part<ES>(v + NW * 4, 0, last < r ? last : r, make_uint4(z[0], z[1], z[2], z[3]));
+  }
+}
+template <bool F32>
+KLT_DEV void put16_any(void* row, int c, int C, const f32x2* v) {
+  uint32_t t[F32 ? 16 : 8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    float lo, hi;
+    unpack2(v[j], lo, hi);
+    if (F32) {
+      t[F32 ? 2 * j : 0] = __float_as_uint(lo);
+      t[F32 ? 2 * j + 1 : 0] = __float_as_uint(hi);
+    } else {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+      t[j] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+  }
+  store_any<F32 ? 16 : 8, F32 ? 4 : 2>(row, c, C, t);
+}
+template <bool F32>
+KLT_DEV void* byte_offset(const void* p, int64_t elements) {
+  return const_cast<char*>(static_cast<const char*>(p)) + elements * (F32 ? 4 : 2);
+}
+template <bool ANY, bool F32 = false, bool WIDE = false>
+KLT_DEV void load16(Raw16<F32>& v, const void* base, int64_t off, int c, int C) {
+  if (ANY)
+    v.load_any(byte_offset<F32>(base, off), c, C);
+  else
+    v.template load<WIDE>(base, off + c);
+}
+// Sixteen codes of a row of C that starts on any byte, from column c on, by this lane alone.
+KLT_DEV void store_codes16(uint8_t* row, int c, int C, uint4 codes) {
+  uint8_t* at = row + c;
+  const int r = static_cast<int>(reinterpret_cast<uintptr_t>(at) & 15);
+  char* v = reinterpret_cast<char*>(at - r);
+  if (r == 0) {
+    if (c + 16 <= C)
+      *reinterpret_cast<uint4*>(v) = codes;
+    else
+      store_part<1>(v, 0, clamp16(C - c), codes);
+  } else {
+    uint32_t t[12] = {0, 0, 0, 0, codes.x, codes.y, codes.z, codes.w, 0, 0, 0, 0};
+    shift_words<8>(t, 16 - r);
+    store_part<1>(v, r, clamp16(C - c + r), make_uint4(t[0], t[1], t[2], t[3]));
+    store_part<1>(v + 16, 0, min(clamp16(C - c + r - 16), r), make_uint4(t[4], t[5], t[6], t[7]));
   }
 }
 // The largest magnitude of the group that this lane's eight lanes hold, NaN if it holds one.
@@ -325,7 +526,7 @@ KLT_DEV void quant_store(const Half& hw, const QuantParams& p, uint32_t it, uint
   store_codes(hw, p.q, row * p.ld_q, c, p.K, p.wide_q, codes8(v, s));
   if (hw.lane == 0) p.s[it] = s;
 }
-// Any strides and widths: one group of 128 columns per half warp.
+// Few groups, any strides and widths: one group of 128 columns per half warp.
 __global__ void __launch_bounds__(256) quant_kernel(QuantParams p) {
   __shared__ float bufs[16 * 128];
   pdl_trigger();
@@ -340,9 +541,9 @@ __global__ void __launch_bounds__(256) quant_kernel(QuantParams p) {
   load8(hw, p.x, p.f32, row * p.ld_x, c, p.K, p.wide_x, v);
   quant_store(hw, p, it, row, c, v);
 }
-// Vectors throughout (K a multiple of 128, aligned rows): eight lanes per group, U groups each,
-// their loads in flight together.
-template <int U, bool F32>
+// Eight lanes per group, U groups each, their loads in flight together.  Vectors throughout (K a
+// multiple of 128, aligned rows), or (ANY) any strides and widths.
+template <int U, bool F32, bool ANY>
 __global__ void __launch_bounds__(256) quant_vec_kernel(QuantParams p) {
   pdl_trigger();
   const uint32_t base = blockIdx.x * (32u * U) + (threadIdx.x >> 3);
@@ -354,7 +555,8 @@ __global__ void __launch_bounds__(256) quant_vec_kernel(QuantParams p) {
   for (int u = 0; u < U; ++u) quant_item(p, min(base + 32 * u, p.items - 1), row[u], c[u]);
   pdl_wait();
 #pragma unroll
-  for (int u = 0; u < U; ++u) raw[u].load(p.x, row[u] * p.ld_x + c[u] + lane * 16);
+  for (int u = 0; u < U; ++u)
+    load16<ANY>(raw[u], p.x, row[u] * p.ld_x, c[u] + lane * 16, p.K);
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     f32x2 v[8];
@@ -363,7 +565,11 @@ __global__ void __launch_bounds__(256) quant_vec_kernel(QuantParams p) {
     const float s = group_scale(group_amax16(v));
     const uint4 codes = codes16(v, s);
     if (base + 32 * u < p.items) {
-      *reinterpret_cast<uint4*>(p.q + row[u] * p.ld_q + c[u] + lane * 16) = codes;
+      uint8_t* q = p.q + row[u] * p.ld_q;
+      if (ANY)
+        store_codes16(q, c[u] + lane * 16, p.K, codes);
+      else
+        *reinterpret_cast<uint4*>(q + c[u] + lane * 16) = codes;
       if (lane == 0) p.s[base + 32 * u] = s;
     }
   }
@@ -614,9 +820,9 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) norm_vec_kernel(NormPar
   }
 }
 
-// Many rows of vectors that start on 32 bytes: one block per row, VPT times 16 columns per
-// thread, pairs throughout.
-template <int VPT, bool HF32>
+// Many rows: one block per row, VPT times 16 columns per thread, pairs throughout.  Of vectors
+// that start on 32 bytes, or (ANY) of any start and length.
+template <int VPT, bool HF32, bool ANY>
 __global__ void __launch_bounds__(512) norm_many_kernel(NormParams p) {
   __shared__ float part[2][32];
   const int64_t row = blockIdx.x;
@@ -631,8 +837,8 @@ __global__ void __launch_bounds__(512) norm_many_kernel(NormParams p) {
     hr[i].clear();
     yr[i].clear();
     if (c < p.H) {
-      if (p.y) yr[i].template load<true>(p.y, row * p.ld_y + c);
-      hr[i].template load<true>(p.h, row * p.ld_h + c);
+      if (p.y) load16<ANY, false, true>(yr[i], p.y, row * p.ld_y, c, p.H);
+      load16<ANY, HF32, true>(hr[i], p.h, row * p.ld_h, c, p.H);
     }
   }
   float lo, hi, scale = p.branch_scale;
@@ -665,12 +871,12 @@ __global__ void __launch_bounds__(512) norm_many_kernel(NormParams p) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) u[j] = yr[i].get(j);
         if (p.gamma_post) {
-          g.load(p.gamma_post, c);
+          load16<ANY>(g, p.gamma_post, 0, c, p.H);
 #pragma unroll
           for (int j = 0; j < 8; ++j) u[j] = mul2(u[j], g.get(j));
         }
         if (p.gate && p.gate_col != 0) {
-          g.load(p.gate, row * p.gate_row + c);
+          load16<ANY>(g, p.gate, row * p.gate_row, c, p.H);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             f32x2 w = g.get(j);
@@ -684,10 +890,19 @@ __global__ void __launch_bounds__(512) norm_many_kernel(NormParams p) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) h[i][j] = fmaf2(scale2, u[j], h[i][j]);
       }
-      if (p.h_out) put16<HF32>(p.h_out, row * p.ld_h_out + c, h[i]);
+      if (ANY && c + 16 > p.H) {  // columns past H stay 0 whatever the scales are
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          unpack2(h[i][j], lo, hi);
+          h[i][j] = pack2(c + 2 * j < p.H ? lo : 0.f, c + 2 * j + 1 < p.H ? hi : 0.f);
+        }
+      }
+      if (!ANY && p.h_out) put16<HF32>(p.h_out, row * p.ld_h_out + c, h[i]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) ss = fmaf2(h[i][j], h[i][j], ss);
     }
+    if (ANY && p.h_out)
+      put16_any<HF32>(byte_offset<HF32>(p.h_out, row * p.ld_h_out), c, p.H, h[i]);
   }
   if (!p.n && !p.q) return;
   float r = 1.0f;
@@ -699,7 +914,7 @@ __global__ void __launch_bounds__(512) norm_many_kernel(NormParams p) {
   for (int i = 0; i < VPT; ++i) {
     const int c = c0 + i * step;
     if (p.gamma_pre && c < p.H) {
-      g.load(p.gamma_pre, c);
+      load16<ANY>(g, p.gamma_pre, 0, c, p.H);
 #pragma unroll
       for (int j = 0; j < 8; ++j) h[i][j] = mul2(h[i][j], g.get(j));
     }
@@ -708,15 +923,21 @@ __global__ void __launch_bounds__(512) norm_many_kernel(NormParams p) {
       float s = d * r;
       uint4 codes = codes16(h[i], d == 0.f ? 1.0f : d);
       if (s == 0.f) s = 1.0f, codes = make_uint4(0, 0, 0, 0);
-      if (c < p.H) {
+      if (ANY) {
+        const uint32_t t[4] = {codes.x, codes.y, codes.z, codes.w};
+        store_any<4, 1>(p.q + row * p.ld_q, c, p.H, t);
+      } else if (c < p.H) {
         *reinterpret_cast<uint4*>(p.q + row * p.ld_q + c) = codes;
-        if ((threadIdx.x & 7) == 0) p.s[row * p.G + c / 128] = s;
       }
+      if (c < p.H && (threadIdx.x & 7) == 0) p.s[row * p.G + c / 128] = s;
     }
-    if (p.n && c < p.H) {
+    if (p.n && (ANY || c < p.H)) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) h[i][j] = mul2(h[i][j], pack2(r, r));
-      put16<false>(p.n, row * p.ld_n + c, h[i]);
+      if (ANY)
+        put16_any<false>(byte_offset<false>(p.n, row * p.ld_n), c, p.H, h[i]);
+      else
+        put16<false>(p.n, row * p.ld_n + c, h[i]);
     }
   }
 }
@@ -735,6 +956,13 @@ cudaError_t launch_pdl(Kernel k, unsigned grid, unsigned block, size_t smem, cud
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, k, p...);
+}
+
+template <bool HF32, bool ANY>
+cudaError_t launch_many(bool twice, unsigned grid, unsigned lanes, cudaStream_t st,
+                        const NormParams& p) {
+  return twice ? launch_pdl(norm_many_kernel<2, HF32, ANY>, grid, lanes, 0, st, p)
+               : launch_pdl(norm_many_kernel<1, HF32, ANY>, grid, lanes, 0, st, p);
 }
 
 int status_of(cudaError_t e) {
@@ -786,19 +1014,25 @@ extern "C" int klt_quantize(const void* x, int32_t x_dtype, int64_t ld_x, int32_
   p.f32 = x_dtype == KLT_DT_F32;
   p.wide_x = wide(x, ld_x, esize(x_dtype), 16);
   p.wide_q = wide(q, ld_q, 1, 8);
-  // vectors throughout, and enough groups to fill the device four times over: 16 values per
-  // lane and two groups in flight; else one group per half warp, spread over more SMs
-  const bool many = K % 128 == 0 && p.wide_x && wide(q, ld_q, 1, 16) && items >= 4 * 16 * 152 * 4;
-  const int64_t blocks = (items + (many ? 64 : 16) - 1) / (many ? 64 : 16);
-  const unsigned grid = static_cast<unsigned>(blocks);
+  // 16 values per lane once there are enough groups to fill the device: vectors throughout, two
+  // groups in flight, from four groups per half warp on (8192 x 7168 27.6 us, one group per half
+  // warp 38); other rows from 4096 groups on (8000 x 5003 24.8 and 47.1 us, 300 x 5003 3.1 and
+  // 3.6, 1021 x 301 even; two groups in flight 29.4).  Else one group per half warp, spread over
+  // more SMs.
+  const bool vectors = K % 128 == 0 && p.wide_x && wide(q, ld_q, 1, 16);
+  const bool many = items >= (vectors ? 4 * 16 * 152 * 4 : 4096);
+  const int per = many ? vectors ? 64 : 32 : 16;
+  const unsigned grid = static_cast<unsigned>((items + per - 1) / per);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (!many)
     e = launch_pdl(quant_kernel, grid, 256, 0, st, p);
-  else if (p.f32)
-    e = launch_pdl(quant_vec_kernel<2, true>, grid, 256, 0, st, p);
+  else if (vectors)
+    e = p.f32 ? launch_pdl(quant_vec_kernel<2, true, false>, grid, 256, 0, st, p)
+              : launch_pdl(quant_vec_kernel<2, false, false>, grid, 256, 0, st, p);
   else
-    e = launch_pdl(quant_vec_kernel<2, false>, grid, 256, 0, st, p);
+    e = p.f32 ? launch_pdl(quant_vec_kernel<1, true, true>, grid, 256, 0, st, p)
+              : launch_pdl(quant_vec_kernel<1, false, true>, grid, 256, 0, st, p);
   return status_of(e);
 }
 
@@ -859,8 +1093,8 @@ extern "C" int klt_block_norm(const klt_block_norm_args* a, void* stream) {
   p.wide_n = wide(a->n, a->ld_n, 2, 16);
   p.wide_q = wide(a->q, a->ld_q, 1, 8);
   // Up to 8 rows per SM: one group per half warp, the shortest path through a row (1021 x 2901
-  // ragged: 14.5 us, two groups 15.9, four 23.6); more: two, which leave fewer blocks to start
-  // and stop (4000 x 7001 ragged: 178 us, one group 201, four 258)
+  // element by element: 14.5 us, two groups 15.9, four 23.6); more: two, which leave fewer
+  // blocks to start and stop (4000 x 7001: 178 us, one group 201, four 258)
   int vpt = M <= 8 * 152 ? 1 : 2;
   while (p.G > vpt * (vpt == 1 ? 64 : 32)) vpt *= 2;
   const int threads = ((p.G + vpt - 1) / vpt * 16 + 31) / 32 * 32;
@@ -870,7 +1104,8 @@ extern "C" int klt_block_norm(const klt_block_norm_args* a, void* stream) {
                        (!p.gate || p.gate_col != 1 || p.wide_gate) && p.wide_gpost &&
                        p.wide_gpre && (!p.h_out || p.wide_h_out) && (!p.n || p.wide_n) &&
                        (!p.q || p.wide_q);
-  const bool plain = (a->y && p.y_f32) || (a->gate && p.gate_col != 0 && (p.gate_col != 1 || p.gate_f32));
+  const bool plain = (a->y && p.y_f32) ||
+                     (a->gate && p.gate_col != 0 && (p.gate_col != 1 || p.gate_f32));
   const size_t smem = vectors ? 0 : threads / 16 * 512;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
@@ -882,16 +1117,22 @@ extern "C" int klt_block_norm(const klt_block_norm_args* a, void* stream) {
                     (!a->y || wide(a->y, a->ld_y, ye, 32)) &&
                     (!a->h_out || wide(a->h_out, a->ld_h_out, he, 32)) &&
                     (!a->n || wide(a->n, a->ld_n, 2, 32)) && (!a->q || wide(a->q, a->ld_q, 1, 16));
+  // Rows of any start and length: the same with 16 per thread (1021 x 2901 11.6 us, norm_kernel
+  // 14.4; 4000 x 7001 94 and 156; 160 x 2901 6.6 and 7.4; 16 x 12001 10.2 and 16.7), but for few
+  // values (16 x 2901 5.8 and 5.1; 160 x 300 5.6 and 4.3 us); 32 per thread took 150 us for the
+  // 4000 x 7001.
+  const bool any = !vectors && !plain && (H > 4096 || static_cast<int64_t>(M) * H > 1 << 18);
   if (many) {
     const bool twice = H > 8192 || (M > 8 * 152 && H > (p.h_f32 ? 6144 : 2560));
     const int per = twice ? 32 : 16;
     const unsigned lanes = ((H + per - 1) / per + 31) / 32 * 32;
-    if (p.h_f32)
-      e = twice ? launch_pdl(norm_many_kernel<2, true>, grid, lanes, 0, st, p)
-                : launch_pdl(norm_many_kernel<1, true>, grid, lanes, 0, st, p);
-    else
-      e = twice ? launch_pdl(norm_many_kernel<2, false>, grid, lanes, 0, st, p)
-                : launch_pdl(norm_many_kernel<1, false>, grid, lanes, 0, st, p);
+    e = p.h_f32 ? launch_many<true, false>(twice, grid, lanes, st, p)
+                : launch_many<false, false>(twice, grid, lanes, st, p);
+  } else if (any) {
+    const bool twice = H > 8192;
+    const unsigned lanes = ((H + (twice ? 31 : 15)) / (twice ? 32 : 16) + 31) / 32 * 32;
+    e = p.h_f32 ? launch_many<true, true>(twice, grid, lanes, st, p)
+                : launch_many<false, true>(twice, grid, lanes, st, p);
   } else if (!vectors || plain) {
     switch (vpt) {
       case 1: e = launch_pdl(norm_kernel<1>, grid, threads, smem, st, p); break;

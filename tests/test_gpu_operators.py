@@ -67,6 +67,19 @@ def _same(a, b):
     return torch.equal(_bits(a), _bits(b))
 
 
+def _offset_rows(M, C, dtype, pad, off, fill):
+    """Rows that start `off` elements into their buffer and end `pad` before the next one."""
+    base = torch.full((off + M * (C + pad) + 16,), fill, device="cuda",
+                      dtype=torch.uint8 if dtype is None else dtype)
+    return base.as_strided((M, C), (C + pad, 1), off), base
+
+
+def _untouched(view, base, fill):
+    rest = base.clone()
+    rest.as_strided(view.shape, view.stride(), view.storage_offset()).fill_(fill)
+    return bool((rest == fill).all())
+
+
 # ---------------------------------------------------------------- quantiser
 
 def _quant_ref(x32):
@@ -103,6 +116,23 @@ def test_quantize(M, K, dtype, pad):
     assert (q._base[:, K:] == 0xA5).all()
     q2, s2 = B.quantize_fp8(xt)  # outputs allocated by the call
     assert torch.equal(q2.view(torch.uint8), q) and torch.equal(s2, s)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("M,K,pad", [(5000, 5, 0), (2100, 129, 1), (300, 2901, 0),
+                                     (1100, 500, 3), (40, 16383, 2), (33, 128 * 128, 5)])
+def test_quantize_rows_of_any_start(M, K, pad, dtype):
+    rng = _gen(22, M, K, pad)
+    x, _ = _offset_rows(M, K, dtype, pad, 3, float("nan"))
+    x.copy_(torch.from_numpy(rng.standard_normal((M, K)) * np.exp(rng.standard_normal((M, 1)))))
+    codes, scales = _quant_ref(x.cpu().float().numpy())
+    for off in (0, 5, 16):
+        q, base = _offset_rows(M, K, None, (off - K) % 16 if off == 16 else pad, off, 0xA5)
+        s = torch.full((M, -(-K // 128)), -1.0, device="cuda")
+        B.quantize_fp8(x, q, s)
+        np.testing.assert_array_equal(s.cpu().numpy(), scales)
+        np.testing.assert_array_equal(q.cpu().numpy(), codes)
+        assert _untouched(q, base, 0xA5)
 
 
 def test_quantize_extreme_groups():
@@ -286,6 +316,44 @@ def test_block_norm_chain_in_place(M, H):
     for _ in range(3):
         got = chain(False)
         assert _same(got[0], want[0]) and _same(got[1], want[1])
+
+
+@pytest.mark.parametrize("hd", [BF16, F32])
+@pytest.mark.parametrize("M,H,pad", [
+    (600, 500, 0), (2100, 129, 1), (70000, 5, 0), (600, 517, 3), (9, 4099, 0), (7, 4616, 8),
+    (5, 8200, 7), (3, 12001, 0), (2, 16384, 5), (130, 2560, 8)])
+def test_block_norm_rows_of_any_start(M, H, pad, hd):
+    """Every tensor's rows start on another element, and nothing around them is written."""
+    rng = _gen(21, M, H, pad)
+
+    def given(shape, dtype, off):
+        v, _ = _offset_rows(*shape, dtype, pad, off, 7.0)
+        v.copy_(torch.from_numpy(rng.standard_normal(shape)))
+        return v
+
+    h, y = given((M, H), hd, 1), given((M, H), BF16, 3)
+    gate = given((M, H), BF16, 5)
+    gpost, gpre = given((1, H), BF16, 1)[0], given((1, H), BF16, 2)[0]
+    h2, h2_base = _offset_rows(M, H, hd, pad, 3, 7.0)
+    n, n_base = _offset_rows(M, H, BF16, pad, 6, 7.0)
+    q, q_base = _offset_rows(M, H, None, pad, 5, 0xA5)
+    s = torch.full((M, -(-H // 128)), -1.0, device="cuda")
+    layer = B.BlockNorm(H, gpost, gpre, 1e-6, 0.75, 1.25, True)
+    layer(h, y, gate, h_out=h2, n=n, q=q, s=s)
+    ref = _norm_ref(_f64(h), _f64(y), _f64(gate), _f64(gpost), _f64(gpre),
+                    float(np.float32(1e-6)), 0.75, 1.25, True)
+    assert (np.abs(_f64(h2) - ref[0]) <= HALF[hd] * np.abs(ref[0]) + 1.01 * ref[1]).all()
+    assert (np.abs(_f64(n) - ref[2]) <= HALF[BF16] * np.abs(ref[2]) + 1.01 * ref[3]).all()
+    sr = np.repeat(s.cpu().numpy().astype(np.float64), 128, axis=1)[:, :H]
+    codes = q.contiguous().view(torch.float8_e4m3fn)
+    err = np.abs(_f64(codes) * sr - ref[2])
+    assert (err <= 1.01 * np.maximum(2.0 ** -4 * np.abs(ref[2]), 2.0 ** -10 * sr)
+            + 1.1 * ref[3]).all()
+    assert _untouched(h2, h2_base, 7.0) and _untouched(n, n_base, 7.0)
+    assert _untouched(q, q_base, 0xA5)
+    # in place, the same bits
+    layer(h, y, gate, h_out=h, n=y)
+    assert _same(h, h2) and _same(y, n)
 
 
 def test_block_norm_zero_and_non_finite_rows():
