@@ -395,14 +395,15 @@ typedef struct klt_linear_debug {
   int32_t timeout_ms;          /* bound of every on-device wait (0 = 1000 ms)             */
   int32_t force_tile;          /* token tile: 16, 32, 64, 128 = feature-major kernel, 256 =
                                   token-major kernel, 0 = chosen from the sizes           */
-  int32_t force_split;         /* parts that K is split into: 1, 2, 4, 8; 0 = chosen      */
+  int32_t force_split;         /* parts that K is split into: 1, 2, 4, 8 (tile 256: 1, 2),
+                                  at most K / 128 rounded up; 0 = chosen                  */
 } klt_linear_debug;
 
 /* Create a linear layer on the current device.  w: e4m3 [N, K] row-major; w_scale: fp32
  * [ceil(N / 128), ceil(K / 128)]; both device memory, copied (re-laid out) into memory the
  * handle owns; the caller's buffers are not referenced after the call returns.
- * Synchronous.  Errors: KLT_ERR_INVALID_ARG (null pointer), KLT_ERR_UNSUPPORTED (shape or
- * format rules above; N or K above 2^20; device is not compute capability 10.3),
+ * Synchronous, on the legacy default stream, and not during a stream's capture.
+ * Errors: KLT_ERR_INVALID_ARG (null pointer), KLT_ERR_UNSUPPORTED (shape or format rules above; N or K above 2^20; device is not compute capability 10.3),
  * KLT_ERR_ALIGN (w_scale not 4-byte aligned), KLT_ERR_OOM, KLT_ERR_CUDA.  On error *out is
  * left NULL. */
 int klt_linear_create(const klt_linear_dims* d, const void* w, const float* w_scale,
@@ -414,9 +415,9 @@ int klt_linear_create(const klt_linear_dims* d, const void* w, const float* w_sc
  * handle has no workspace: calls on several streams may overlap.  One launch.
  * Errors: KLT_ERR_INVALID_ARG (null handle or pointer, M < 0 or M > 2^22, a stride shorter
  * than a row, another device current than at creation, bad debug value), KLT_ERR_UNSUPPORTED
- * (M * ceil(K / 128) above 2^31 - 1; debug: a tile and split that do not go together),
- * KLT_ERR_ALIGN (xq or ld_xq not 16-byte,
- * out not element aligned), KLT_ERR_CUDA.  Expired device waits: klt_linear_status. */
+ * (M * ceil(K / 128) above 2^31 - 1; debug: a tile and split that do not go together or
+ * more than 65535 token tiles), KLT_ERR_ALIGN (xq or ld_xq not 16-byte, out, xs or out_s not
+ * element aligned), KLT_ERR_CUDA.  Expired device waits: klt_linear_status. */
 int klt_linear_forward(klt_linear* h, const uint8_t* xq, int64_t ld_xq, const float* xs,
                        int32_t M, void* out, int64_t ld_out, float* out_s,
                        const klt_linear_debug* dbg, void* stream);
