@@ -15,11 +15,12 @@ struct klt_linear {
   klt_linear_dims d;
   int device;
   int num_sms;
-  int max_tiles;   // tiles of the token-major kernel that two pairs each share at once
-  int NB, KB;      // row blocks and k-blocks of W
-  uint8_t* w;      // tile-major image [NB, KB, 16384]
-  float* ws;       // [NB + 1, KB], the last row zero
-  int* err;        // device error word
+  int max_tiles;     // tiles of the token-major kernel that two pairs each share at once
+  int clusters[4];   // clusters of 2^i CTAs of the feature-major kernel, one per SM, at once
+  int NB, KB;        // row blocks and k-blocks of W
+  uint8_t* w;        // tile-major image [NB, KB, 16384]
+  float* ws;         // [NB + 1, KB], the last row zero
+  int* err;          // device error word
   CUtensorMap wmap;  // the image as [NB * KB * 128, 128] bytes
 };
 
@@ -106,44 +107,50 @@ void free_all(klt_linear* h) {
   delete h;
 }
 
-// Token tile and K split for M tokens: the fastest by a model of the three ways, in us, whose
-// constants are fits to measurements (the largest of 26 sizes off by 25 %; the runner-up is
-// close wherever it picks the wrong one):
-//   narrow kernel, tile bn:  a wave of CTAs costs 2.5 + its k-blocks x the time of one, which
-//     grows with the tokens (0.20 for 16, 0.34 for 128), + 1.5 to bring the parts together;
-//   wide kernel: 1.5 + 0.43 per k-block and wave of pairs; + 3.5 where two pairs share a tile.
-// E.g. 256 x 7168 x 7168: narrow 25.5, wide 27.9, wide by two pairs 21.0 us; 777 x 1003 x 2090:
-// 9.4, 14.3 and 14.9 us; 1024 x 2048 x 3584: 15.5, 15.7 and 14.4 us.
+// Token tile and K split for M tokens: the fastest by a model of every form, in us.  Its
+// constants are fits to 106 sizes x 6 to 18 forms (all within 1 x 64 x 64 .. 8192 x 8192 x 8192);
+// over those and 120 more its choices take 0.6 % longer than the fastest form, 29 % at worst.
+//   narrow kernel: the waves that its clusters need, each of a start (first: longer for wider
+//     tiles) and its k-blocks, which take longer where two CTAs share an SM;
+//   wide kernel: 1.5 + per wave of pairs its tile's end and k-blocks; two pairs that share a
+//     tile take half of the k-blocks, and bring their parts together.
+// E.g. 1 x 7168 x 2048: 4 parts 4.8 us, 8 parts 6.9; 98 x 256 x 429 SwiGLU: tiles of 16 in 4
+// parts 3.1, of 64 in 4 parts 5.4; 2368 x 194 x 4096: tiles of 64 in 4 parts 8.7, of 128 in 4
+// parts 15.5 (they run alone on their SMs, and 38 clusters of 4 are two waves), wide 17.6; 256 x
+// 7168 x 7168: narrow 25.5, wide 27.9, by two pairs 21.0.
 void choose(const klt_linear* h, int M, int* tile, int* split) {
   const bool act = h->d.act == KLT_ACT_SWIGLU;
-  const int most = act ? 64 : 128;
-  int bn = 16;
-  while (bn < M && bn < most) bn *= 2;
-  // two tiles of 32 SwiGLU tokens share an SM, a tile of 64 runs alone (64 x 4096 x 7168: 10.3
-  // and 12.1 us)
-  if (act && M > 32 && M <= 64) bn = 32;
-  *tile = bn;
-  *split = 1;
-  // Parts of K while the CTAs stay below 256, about 1.7 per SM (one per SM for the tiles that
-  // run alone on theirs, half in clusters of 8, which have to fit in their part of the chip):
-  // all resident at once, with room for the first CTAs of the next launch (1 x 7168 x 2048: 4
-  // parts, 224 CTAs, 4.8 us; 8 parts, 448 CTAs, 6.9 us; 2 parts 5.2 us).
-  const bool alone = bn == most;
-  const int64_t units = static_cast<int64_t>(act ? h->NB / 2 : h->NB) * ((M + bn - 1) / bn);
-  while (*split < 8 && h->KB >= *split * 2 &&
-         units * *split * 2 <= (!alone ? 256 : *split < 4 ? h->num_sms : h->num_sms / 2))
-    *split *= 2;
-  if (M <= 128) return;
-
-  const int64_t waves = (units * *split + h->num_sms - 1) / h->num_sms;
-  const double narrow = waves * (2.5 + 0.34 * h->KB / *split) + (*split > 1 ? 1.5 : 0.0);
+  struct Cost {
+    double first, kblock;
+  };
+  static const Cost costs[2][4] = {{{2.51, 0.29}, {3.01, 0.29}, {4.28, 0.34}, {5.65, 0.39}},
+                                   {{2.80, 0.42}, {3.60, 0.47}, {4.78, 0.55}, {}}};
+  double best = 0.0;
+  auto offer = [&](int t, int parts, double us) {
+    if (best == 0.0 || us < best) best = us, *tile = t, *split = parts;
+  };
+  for (int i = 0; i < (act ? 3 : 4); ++i) {
+    const int bn = 16 << i;
+    if (i > 0 && M <= bn / 4) break;  // three quarters of it empty: the smaller one is as good
+    const int64_t units = static_cast<int64_t>(act ? h->NB / 2 : h->NB) * ((M + bn - 1) / bn);
+    const bool alone = bn == (act ? 64 : 128);  // one CTA per SM
+    if ((M + bn - 1) / bn > 65535) continue;    // the grid's second dimension
+    for (int j = 0; j < 4 && (1 << j) <= h->KB; ++j) {
+      const int one = h->clusters[j];
+      // two per SM: leftovers of the GPCs make up two more clusters (74 of 4 and 32 of 8 run at
+      // once, 75 and 36 do not)
+      const int64_t room = alone ? one : 2 * one + (j >= 2 ? 2 : 0);
+      const int64_t waves = (units + room - 1) / room;
+      const int kb = (h->KB + (1 << j) - 1) >> j;
+      offer(bn, 1 << j, costs[act][i].first + (waves - 1) * 3.4 +
+                            waves * kb * costs[act][i].kblock * (alone || units <= one ? 1 : 1.47));
+    }
+  }
   const int64_t tiles = static_cast<int64_t>((M + 255) / 256) * ((h->NB + 1) / 2);
   const int64_t pairs = h->num_sms / 2;
-  const double wide = (tiles + pairs - 1) / pairs * (1.5 + 0.43 * h->KB);
-  const double shared = tiles <= h->max_tiles && h->KB >= 4 ? 5.0 + 0.43 * h->KB / 2 : wide;
-  if (narrow < wide && narrow < shared && M <= 65535) return;
-  *tile = 256;
-  *split = shared < wide ? 2 : 1;
+  const double end = act ? 2.71 : 4.99;
+  offer(256, 1, 1.5 + ((tiles + pairs - 1) / pairs) * (end + 0.43 * h->KB));
+  if (h->KB >= 4 && tiles <= h->max_tiles) offer(256, 2, 5.63 + end + 0.43 * h->KB / 2);
 }
 
 }  // namespace
@@ -164,8 +171,9 @@ int klt_linear_create(const klt_linear_dims* d, const void* w, const float* w_sc
   if (cudaGetDeviceProperties(&prop, dev) != cudaSuccess) return KLT_ERR_CUDA;
   if (prop.major != 10 || prop.minor != 3) return KLT_ERR_UNSUPPORTED;
   if (!get_encode()) return KLT_ERR_CUDA;
-  int max_tiles = 0;
-  if (!prepare_linear_narrow() || !prepare_linear_wide(&max_tiles)) return KLT_ERR_UNSUPPORTED;
+  int max_tiles = 0, clusters[4] = {};
+  if (!prepare_linear_narrow(clusters) || !prepare_linear_wide(&max_tiles))
+    return KLT_ERR_UNSUPPORTED;
 
   klt_linear* h = new (std::nothrow) klt_linear();
   if (!h) return KLT_ERR_OOM;
@@ -173,6 +181,7 @@ int klt_linear_create(const klt_linear_dims* d, const void* w, const float* w_sc
   h->device = dev;
   h->num_sms = prop.multiProcessorCount;
   h->max_tiles = max_tiles;
+  for (int i = 0; i < 4; ++i) h->clusters[i] = clusters[i];
   h->NB = (d->N + 127) / 128;
   h->KB = (d->K + 127) / 128;
   const int64_t tiles = static_cast<int64_t>(h->NB) * h->KB;

@@ -285,7 +285,8 @@ cudaError_t launch_linear_wide(const CUtensorMap& tok, const CUtensorMap& wmap,
                                int parts, int num_sms, cudaStream_t s);
 // Once per device, before the first launch: shared-memory sizes, and whether the kernels are
 // what their launches expect.
-bool prepare_linear_narrow();
+// clusters[i]: clusters of 2^i CTAs, one per SM, that are resident at once
+bool prepare_linear_narrow(int clusters[4]);
 bool prepare_linear_wide(int* max_tiles);  // tiles that two pairs each share at once
 
 }  // namespace klt

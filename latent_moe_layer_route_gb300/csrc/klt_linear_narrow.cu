@@ -411,9 +411,27 @@ cudaError_t launch(const CUtensorMap& tok, const LinParams& p, int split, cudaSt
 
 }  // namespace
 
-bool prepare_linear_narrow() {
-  return prepare<16, 0>() && prepare<32, 0>() && prepare<64, 0>() && prepare<128, 0>() &&
-         prepare<16, 1>() && prepare<32, 1>() && prepare<64, 1>();
+bool prepare_linear_narrow(int clusters[4]) {
+  if (!prepare<16, 0>() || !prepare<32, 0>() || !prepare<64, 0>() || !prepare<128, 0>() ||
+      !prepare<16, 1>() || !prepare<32, 1>() || !prepare<64, 1>())
+    return false;
+  for (int i = 0; i < 4; ++i) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1 << i, 1, 1);
+    cfg.blockDim = dim3(Narrow<128, 0>::THREADS);
+    cfg.dynamicSmemBytes = Narrow<128, 0>::SMEM;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1 << i;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&clusters[i], narrow_kernel<128, 0>, &cfg) != cudaSuccess)
+      return false;
+    if (clusters[i] < 1) clusters[i] = 1;
+  }
+  return true;
 }
 
 cudaError_t launch_linear_narrow(const CUtensorMap& tok, const LinParams& p, int bn, int split,
