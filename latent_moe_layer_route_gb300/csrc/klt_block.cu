@@ -21,10 +21,9 @@ namespace {
 // A half warp holds one group of 128 columns of a row, eight neighbouring ones per lane.
 // Where the tensor's rows start on 16 bytes (8 for codes) a lane's eight are one or two vector
 // accesses.  Else, and for the short group at a row's end, the half warp moves them element by
-// element, neighbouring lanes neighbouring elements (whole sectors: written eight apart, a
-// ragged 1021 x 2901 batch took 26 us), through 512 bytes of shared memory.  Plain loads, not
-// the read-only path: the launch may begin while the kernel that writes these tensors still
-// runs, and h_out may be h.
+// element, neighbouring lanes neighbouring elements (whole sectors), through 512 bytes of shared
+// memory.  Plain loads, not the read-only path: the launch may begin while the kernel that
+// writes these tensors still runs, and h_out may be h.
 struct Half {
   uint32_t mask;  // the lanes of this half warp
   int lane;       // 0 .. 15
@@ -32,14 +31,14 @@ struct Half {
 };
 KLT_DEV Half half_warp(float* bufs) {
   const int h = threadIdx.x >> 4;
-  return {0xFFFFu << (16 * (h & 1)), static_cast<int>(threadIdx.x & 15), bufs + h * 128};
+  return {0xFFFFu << (16 * (h & 1)), static_cast<int>(threadIdx.x & 15),
+          bufs ? bufs + h * 128 : nullptr};
 }
 
 // This lane's eight values of columns c .. c + 127 (c < C) of the row at element `off`; those
-// past C are 0.  In two steps, so that the loads of a whole row are in flight together: fetch8
-// as they are loaded, settle8 to their lanes.
-KLT_DEV void fetch8(const Half& hw, const void* base, bool f32, int64_t off, int c, int C,
-                    bool wide, float* v) {
+// past C are 0.
+KLT_DEV void load8(const Half& hw, const void* base, bool f32, int64_t off, int c, int C, bool wide,
+                   float* v) {
   if (wide && c + 128 <= C) {
     off += c + hw.lane * 8;
     if (f32) {
@@ -57,7 +56,9 @@ KLT_DEV void fetch8(const Half& hw, const void* base, bool f32, int64_t off, int
         v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
       }
     }
-  } else if (f32) {
+    return;
+  }
+  if (f32) {
     const float* p = static_cast<const float*>(base) + off + c;
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = c + i * 16 + hw.lane < C ? p[i * 16 + hw.lane] : 0.f;
@@ -67,9 +68,6 @@ KLT_DEV void fetch8(const Half& hw, const void* base, bool f32, int64_t off, int
     for (int i = 0; i < 8; ++i)
       v[i] = c + i * 16 + hw.lane < C ? __bfloat162float(p[i * 16 + hw.lane]) : 0.f;
   }
-}
-KLT_DEV void settle8(const Half& hw, int c, int C, bool wide, float* v) {
-  if (wide && c + 128 <= C) return;
 #pragma unroll
   for (int i = 0; i < 8; ++i) hw.buf[i * 16 + hw.lane] = v[i];
   __syncwarp(hw.mask);
@@ -77,46 +75,6 @@ KLT_DEV void settle8(const Half& hw, int c, int C, bool wide, float* v) {
   const float4 b = reinterpret_cast<const float4*>(hw.buf)[hw.lane * 2 + 1];
   v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
   v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  __syncwarp(hw.mask);
-}
-KLT_DEV void load8(const Half& hw, const void* base, bool f32, int64_t off, int c, int C, bool wide,
-                   float* v) {
-  fetch8(hw, base, f32, off, c, C, wide, v);
-  settle8(hw, c, C, wide, v);
-}
-KLT_DEV void store8(const Half& hw, void* base, bool f32, int64_t off, int c, int C, bool wide,
-                    const float* v) {
-  if (wide && c + 128 <= C) {
-    off += c + hw.lane * 8;
-    if (f32) {
-      float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + off);
-      p[0] = make_float4(v[0], v[1], v[2], v[3]);
-      p[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-      uint32_t w[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t*>(&b);
-      }
-      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(base) + off) =
-          make_uint4(w[0], w[1], w[2], w[3]);
-    }
-    return;
-  }
-  reinterpret_cast<float4*>(hw.buf)[hw.lane * 2] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(hw.buf)[hw.lane * 2 + 1] = make_float4(v[4], v[5], v[6], v[7]);
-  __syncwarp(hw.mask);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int e = i * 16 + hw.lane;
-    if (c + e < C) {
-      if (f32)
-        static_cast<float*>(base)[off + c + e] = hw.buf[e];
-      else
-        static_cast<__nv_bfloat16*>(base)[off + c + e] = __float2bfloat16(hw.buf[e]);
-    }
-  }
   __syncwarp(hw.mask);
 }
 KLT_DEV void store_codes(const Half& hw, uint8_t* q, int64_t off, int c, int C, bool wide,
@@ -144,20 +102,22 @@ KLT_DEV float group_amax(const Half& hw, const float* v) {
   for (int o = 8; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(hw.mask, m, o));
   return m;
 }
-// Codes of eight values of a group with scale s.
-KLT_DEV uint2 codes8(const float* v, float s) {
-  float t[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) t[i] = v[i];
+// Codes of four or eight values of a group with scale s.
+KLT_DEV uint32_t codes4(const float* v, float s) {
+  float t[4];
   const float k = rescale(s), inv = __frcp_rn(s);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) t[i] = v[i];
   if (k != 1.0f) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] *= k;
+    for (int i = 0; i < 4; ++i) t[i] *= k;
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) t[i] = quot_group(t[i], s, inv);
-  return make_uint2(f32x2_to_e4m3x2(t[0], t[1]) | (f32x2_to_e4m3x2(t[2], t[3]) << 16),
-                    f32x2_to_e4m3x2(t[4], t[5]) | (f32x2_to_e4m3x2(t[6], t[7]) << 16));
+  for (int i = 0; i < 4; ++i) t[i] = quot_group(t[i], s, inv);
+  return f32x2_to_e4m3x2(t[0], t[1]) | (f32x2_to_e4m3x2(t[2], t[3]) << 16);
+}
+KLT_DEV uint2 codes8(const float* v, float s) {
+  return make_uint2(codes4(v, s), codes4(v + 4, s));
 }
 
 // Eight neighbouring values as they lie in memory, of a tensor whose rows are vectors: the
@@ -585,7 +545,6 @@ struct NormParams {
   int H, G;
   float eps, inv_h, res_scale, branch_scale;
   bool h_f32, y_f32, gate_f32, sigmoid;
-  bool wide_h, wide_y, wide_gate, wide_gpost, wide_gpre, wide_h_out, wide_n, wide_q;
 };
 
 // Sum over the block of one value per thread; `part` is 32 floats of its own.
@@ -604,14 +563,6 @@ KLT_DEV float block_sum(float v, float* part) {
 KLT_DEV float rms_inverse(float sum, float inv_h, float eps) {
   return rsqrtf(fmaf(sum, inv_h, eps));
 }
-KLT_DEV float row_rms_inverse(const float (*v)[8], int vpt, float inv_h, float eps, float* part) {
-  float ss = 0.f;
-#pragma unroll
-  for (int i = 0; i < vpt; ++i)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
-  return rms_inverse(block_sum(ss, part), inv_h, eps);
-}
 KLT_DEV float gate_value(float g, bool sigmoid) {
   // the divisor of the fast divide stays in its range: for g < -80 the gate is below 2e-35
   return sigmoid ? __fdividef(1.0f, 1.0f + __expf(-fmaxf(g, -80.0f))) : g;
@@ -621,101 +572,142 @@ KLT_DEV float load1(const void* p, bool f32, int64_t i) {
              : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
 }
 
-// Codes and scale of a group of n = t r (t = h' gamma): t against its own largest magnitude,
-// so r enters the scale alone.
-KLT_DEV void store_norm_codes(const Half& hw, const NormParams& p, int64_t row, int c, float r,
-                              const float* t) {
-  const float d = over_448(group_amax(hw, t));
-  float s = d * r;
-  uint2 codes = codes8(t, d == 0.f ? 1.0f : d);
-  if (s == 0.f) s = 1.0f, codes = make_uint2(0, 0);  // n is 0 throughout, or rounds to it
-  store_codes(hw, p.q, row * p.ld_q, c, p.H, p.wide_q, codes);
-  if (hw.lane == 0) p.s[row * p.G + c / 128] = s;
+// An element as it lies in memory, 0 where c >= end: without a branch, so that the loads of a
+// row are in flight together (where each tensor's loads and conversions stood in branches on its
+// type, a row waited for every tensor in turn: 16 x 1016 5.6 us).
+template <bool F32>
+KLT_DEV uint32_t load_raw(const char* at, int c, int end) {
+  uint32_t r;
+  if (F32)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.lt.s32 p, %2, %3;\n mov.b32 %0, 0;\n"
+        " @p ld.global.b32 %0, [%1];\n}"
+        : "=r"(r)
+        : "l"(at), "r"(c), "r"(end)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.lt.s32 p, %2, %3;\n mov.b32 %0, 0;\n"
+        " @p ld.global.u16 %0, [%1];\n}"
+        : "=r"(r)
+        : "l"(at), "r"(c), "r"(end)
+        : "memory");
+  return r;
+}
+// A row of a tensor.  TYPE: 0 bf16, 1 fp32, 2 either.
+template <int TYPE>
+struct Row {
+  const char* at;
+  int end;  // columns to read
+  bool f32;
+  KLT_DEV Row(const void* base, bool f, int64_t off, int n)
+      : at(static_cast<const char*>(base)), end(base ? n : 0), f32(TYPE == 2 ? f : TYPE == 1) {
+    at += off * (f32 ? 4 : 2);
+  }
+  // column c, the i-th element from the row's start
+  KLT_DEV uint32_t raw(int c, int64_t i) const {
+    if (TYPE == 0) return load_raw<false>(at + i * 2, c, end);
+    if (TYPE == 1) return load_raw<true>(at + i * 4, c, end);
+    return load_raw<false>(at + i * 2, c, f32 ? 0 : end) |
+           load_raw<true>(at + i * 4, c, f32 ? end : 0);
+  }
+  KLT_DEV float value(uint32_t r) const { return __uint_as_float(f32 ? r : r << 16); }
+};
+KLT_DEV void store1(void* p, bool f32, int64_t i, float v) {
+  if (f32)
+    static_cast<float*>(p)[i] = v;
+  else
+    static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16(v);
 }
 
-// One block per row, VPT groups of 128 columns per half warp.  The row's scalars (1/rms and
-// the scales) multiply last: y gamma gate is exact up to its final rounding for bf16 tensors,
-// and h' is one multiply-add of it.
-template <int VPT>
-__global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) norm_kernel(NormParams p) {
+// Rows of any strides and widths, few of them: one block per row, VPT groups of 128 columns per
+// warp, whose lanes hold every 32nd column of a group, so that every access is one element per
+// lane and needs no alignment.  TYPE of the residual stream; 2: of y and of a gate across
+// channels too, with any stride.  The row's scalars (1/rms and the scales) multiply last: y
+// gamma gate is exact up to its final rounding for bf16 tensors, and h' is one multiply-add of
+// it.
+template <int VPT, int TYPE>
+__global__ void __launch_bounds__(1024) norm_kernel(NormParams p) {
+  constexpr int OTHER = TYPE == 2 ? 2 : 0;
   __shared__ float part[2][32];
-  extern __shared__ float bufs[];  // 128 per half warp where a row needs them
-  const Half hw = half_warp(bufs);
   const int64_t row = blockIdx.x;
-  const int c0 = static_cast<int>(threadIdx.x >> 4) * 128, step = static_cast<int>(blockDim.x) * 8;
-  float u[VPT][8], h[VPT][8], g[8];
+  const int lane = threadIdx.x & 31;
+  const int c0 = static_cast<int>(threadIdx.x >> 5) * 128 + lane;
+  const int step = static_cast<int>(blockDim.x) * 4;
+  const bool columns = p.gate && p.gate_col != 0;
+  const Row<OTHER> yr(p.y, p.y_f32, row * p.ld_y, p.H);
+  const Row<TYPE> hr(p.h, p.h_f32, row * p.ld_h, p.H);
+  const Row<OTHER> gr(p.gate, p.gate_f32, row * p.gate_row, columns ? p.H : 0);
+  const Row<0> post(p.gamma_post, false, 0, p.H), pre(p.gamma_pre, false, 0, p.H);
+  uint32_t ur[VPT][4], xr[VPT][4], gate[VPT][4], gpost[VPT][4], gpre[VPT][4];
   pdl_trigger();
   pdl_wait();
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int c = c0 + i * step;
+  for (int i = 0; i < VPT; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) u[i][j] = h[i][j] = 0.f;
-    if (c < p.H) {
-      if (p.y) fetch8(hw, p.y, p.y_f32, row * p.ld_y, c, p.H, p.wide_y, u[i]);
-      fetch8(hw, p.h, p.h_f32, row * p.ld_h, c, p.H, p.wide_h, h[i]);
+    for (int j = 0; j < 4; ++j) {
+      const int c = c0 + i * step + 32 * j;
+      ur[i][j] = yr.raw(c, c);
+      xr[i][j] = hr.raw(c, c);
+      gpost[i][j] = post.raw(c, c);
+      gate[i][j] = gr.raw(c, TYPE == 2 ? c * p.gate_col : c);
+      gpre[i][j] = pre.raw(c, c);
     }
-  }
-#pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int c = c0 + i * step;
-    if (c < p.H) {
-      if (p.y) settle8(hw, c, p.H, p.wide_y, u[i]);
-      settle8(hw, c, p.H, p.wide_h, h[i]);
-    }
-  }
   float scale = p.branch_scale;
-  if (p.gamma_post) scale *= row_rms_inverse(u, VPT, p.inv_h, p.eps, part[0]);
-  if (p.gate && p.gate_col == 0)
+  if (p.gate && !columns)
     scale *= gate_value(load1(p.gate, p.gate_f32, row * p.gate_row), p.sigmoid);
+  if (p.gamma_post) {
+    float ss = 0.f;
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int c = c0 + i * step;
-    if (c < p.H) {
-      if (p.gamma_post) {
-        load8(hw, p.gamma_post, false, 0, c, p.H, p.wide_gpost, g);
+    for (int i = 0; i < VPT; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) u[i][j] *= g[j];
-      }
-      if (p.gate && p.gate_col != 0) {
-        if (p.gate_col == 1) {
-          load8(hw, p.gate, p.gate_f32, row * p.gate_row, c, p.H, p.wide_gate, g);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int e = c + hw.lane * 8 + j;
-            g[j] = e < p.H ? load1(p.gate, p.gate_f32, row * p.gate_row + e * p.gate_col) : 0.f;
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) u[i][j] *= gate_value(g[j], p.sigmoid);
-      }
-      // columns past H are 0 in every operand; they stay 0 whatever the scales are
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float r = p.res_scale * h[i][j];
-        h[i][j] = c + hw.lane * 8 + j < p.H ? (p.y ? fmaf(scale, u[i][j], r) : r) : 0.f;
-      }
-      if (p.h_out) store8(hw, p.h_out, p.h_f32, row * p.ld_h_out, c, p.H, p.wide_h_out, h[i]);
-    }
+      for (int j = 0; j < 4; ++j) ss = fmaf(yr.value(ur[i][j]), yr.value(ur[i][j]), ss);
+    scale *= rms_inverse(block_sum(ss, part[0]), p.inv_h, p.eps);
   }
+  float h[VPT][4], ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int c = c0 + i * step + 32 * j;
+      float u = yr.value(ur[i][j]), v = p.res_scale * hr.value(xr[i][j]);
+      if (p.gamma_post) u *= post.value(gpost[i][j]);
+      if (columns) u *= gate_value(gr.value(gate[i][j]), p.sigmoid);
+      if (p.y) v = fmaf(scale, u, v);
+      v = c < p.H ? v : 0.f;  // columns past H stay 0 whatever the scales are
+      h[i][j] = v;
+      ss = fmaf(v, v, ss);
+      if (p.h_out && c < p.H) store1(p.h_out, p.h_f32, row * p.ld_h_out + c, v);
+    }
   if (!p.n && !p.q) return;
-  const float r = p.gamma_pre ? row_rms_inverse(h, VPT, p.inv_h, p.eps, part[1]) : 1.0f;
+  const float r = p.gamma_pre ? rms_inverse(block_sum(ss, part[1]), p.inv_h, p.eps) : 1.0f;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int c = c0 + i * step;
-    if (c < p.H) {
-      if (p.gamma_pre) {
-        load8(hw, p.gamma_pre, false, 0, c, p.H, p.wide_gpre, g);
+    if (c - lane >= p.H) break;
+    if (p.gamma_pre) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) h[i][j] *= g[j];
-      }
-      if (p.q) store_norm_codes(hw, p, row, c, r, h[i]);
-      if (p.n) {
+      for (int j = 0; j < 4; ++j) h[i][j] *= pre.value(gpre[i][j]);
+    }
+    if (p.q) {
+      // n = t r with t = h' gamma: t against its own largest magnitude, r enters the scale alone
+      float m = max_nan(max_nan(h[i][0], h[i][1]), max_nan(h[i][2], h[i][3]));
 #pragma unroll
-        for (int j = 0; j < 8; ++j) h[i][j] *= r;
-        store8(hw, p.n, false, row * p.ld_n, c, p.H, p.wide_n, h[i]);
-      }
+      for (int o = 16; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+      const float d = over_448(m);
+      float s = d * r;
+      uint32_t codes = codes4(h[i], d == 0.f ? 1.0f : d);
+      if (s == 0.f) s = 1.0f, codes = 0;  // n is 0 throughout, or rounds to it
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (c + 32 * j < p.H)
+          p.q[row * p.ld_q + c + 32 * j] = static_cast<uint8_t>(codes >> 8 * j);
+      if (lane == 0) p.s[row * p.G + c / 128] = s;
+    }
+    if (p.n) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (c + 32 * j < p.H) store1(p.n, false, row * p.ld_n + c + 32 * j, h[i][j] * r);
     }
   }
 }
@@ -747,6 +739,8 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) norm_vec_kernel(NormPar
       }
     }
   }
+  const float token =
+      p.gate && p.gate_col == 0 ? load1(p.gate, p.gate_f32, row * p.gate_row) : 0.f;
   float scale = p.branch_scale;
   if (p.gamma_post) {
     float ss = 0.f, v[8];
@@ -759,7 +753,7 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) norm_vec_kernel(NormPar
     scale *= rms_inverse(block_sum(ss, part[0]), p.inv_h, p.eps);
   }
   if (p.gate && p.gate_col == 0)
-    scale *= gate_value(load1(p.gate, p.gate_f32, row * p.gate_row), p.sigmoid);
+    scale *= gate_value(token, p.sigmoid);
   float h[VPT][8], ss = 0.f;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
@@ -810,7 +804,14 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) norm_vec_kernel(NormPar
 #pragma unroll
         for (int j = 0; j < 8; ++j) h[i][j] *= g[j];
       }
-      if (p.q) store_norm_codes(hw, p, row, c - hw.lane * 8, r, h[i]);
+      if (p.q) {  // as norm_kernel
+        const float d = over_448(group_amax(hw, h[i]));
+        float s = d * r;
+        uint2 codes = codes8(h[i], d == 0.f ? 1.0f : d);
+        if (s == 0.f) s = 1.0f, codes = make_uint2(0, 0);
+        *reinterpret_cast<uint2*>(p.q + row * p.ld_q + c) = codes;
+        if (hw.lane == 0) p.s[row * p.G + c / 128] = s;
+      }
       if (p.n) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) h[i][j] *= r;
@@ -918,7 +919,7 @@ __global__ void __launch_bounds__(512) norm_many_kernel(NormParams p) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) h[i][j] = mul2(h[i][j], g.get(j));
     }
-    if (p.q) {  // as store_norm_codes
+    if (p.q) {  // as norm_kernel
       const float d = over_448(group_amax16(h[i]));
       float s = d * r;
       uint4 codes = codes16(h[i], d == 0.f ? 1.0f : d);
@@ -943,12 +944,11 @@ __global__ void __launch_bounds__(512) norm_many_kernel(NormParams p) {
 }
 
 template <typename Kernel, typename... Params>
-cudaError_t launch_pdl(Kernel k, unsigned grid, unsigned block, size_t smem, cudaStream_t s,
+cudaError_t launch_pdl(Kernel k, unsigned grid, unsigned block, cudaStream_t s,
                        const Params&... p) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -958,11 +958,20 @@ cudaError_t launch_pdl(Kernel k, unsigned grid, unsigned block, size_t smem, cud
   return cudaLaunchKernelEx(&cfg, k, p...);
 }
 
+template <int TYPE>
+cudaError_t launch_row(unsigned grid, cudaStream_t st, const NormParams& p) {
+  const int groups = p.G <= 32 ? 1 : p.G <= 64 ? 2 : 4;
+  const unsigned lanes = (p.G + groups - 1) / groups * 32;
+  return groups == 1   ? launch_pdl(norm_kernel<1, TYPE>, grid, lanes, st, p)
+         : groups == 2 ? launch_pdl(norm_kernel<2, TYPE>, grid, lanes, st, p)
+                       : launch_pdl(norm_kernel<4, TYPE>, grid, lanes, st, p);
+}
+
 template <bool HF32, bool ANY>
 cudaError_t launch_many(bool twice, unsigned grid, unsigned lanes, cudaStream_t st,
                         const NormParams& p) {
-  return twice ? launch_pdl(norm_many_kernel<2, HF32, ANY>, grid, lanes, 0, st, p)
-               : launch_pdl(norm_many_kernel<1, HF32, ANY>, grid, lanes, 0, st, p);
+  return twice ? launch_pdl(norm_many_kernel<2, HF32, ANY>, grid, lanes, st, p)
+               : launch_pdl(norm_many_kernel<1, HF32, ANY>, grid, lanes, st, p);
 }
 
 int status_of(cudaError_t e) {
@@ -1026,13 +1035,13 @@ extern "C" int klt_quantize(const void* x, int32_t x_dtype, int64_t ld_x, int32_
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (!many)
-    e = launch_pdl(quant_kernel, grid, 256, 0, st, p);
+    e = launch_pdl(quant_kernel, grid, 256, st, p);
   else if (vectors)
-    e = p.f32 ? launch_pdl(quant_vec_kernel<2, true, false>, grid, 256, 0, st, p)
-              : launch_pdl(quant_vec_kernel<2, false, false>, grid, 256, 0, st, p);
+    e = p.f32 ? launch_pdl(quant_vec_kernel<2, true, false>, grid, 256, st, p)
+              : launch_pdl(quant_vec_kernel<2, false, false>, grid, 256, st, p);
   else
-    e = p.f32 ? launch_pdl(quant_vec_kernel<1, true, true>, grid, 256, 0, st, p)
-              : launch_pdl(quant_vec_kernel<1, false, true>, grid, 256, 0, st, p);
+    e = p.f32 ? launch_pdl(quant_vec_kernel<1, true, true>, grid, 256, st, p)
+              : launch_pdl(quant_vec_kernel<1, false, true>, grid, 256, st, p);
   return status_of(e);
 }
 
@@ -1084,29 +1093,23 @@ extern "C" int klt_block_norm(const klt_block_norm_args* a, void* stream) {
   p.y_f32 = a->y_dtype == KLT_DT_F32;
   p.gate_f32 = a->gate_dtype == KLT_DT_F32;
   p.sigmoid = a->gate_sigmoid != 0;
-  p.wide_h = wide(a->h, a->ld_h, he, 16);
-  p.wide_y = wide(a->y, a->ld_y, ye, 16);
-  p.wide_gate = wide(a->gate, a->gate_row, ge, 16);
-  p.wide_gpost = aligned(a->gamma_post, 16);
-  p.wide_gpre = aligned(a->gamma_pre, 16);
-  p.wide_h_out = wide(a->h_out, a->ld_h_out, he, 16);
-  p.wide_n = wide(a->n, a->ld_n, 2, 16);
-  p.wide_q = wide(a->q, a->ld_q, 1, 8);
-  // Up to 8 rows per SM: one group per half warp, the shortest path through a row (1021 x 2901
-  // element by element: 14.5 us, two groups 15.9, four 23.6); more: two, which leave fewer
-  // blocks to start and stop (4000 x 7001: 178 us, one group 201, four 258)
-  int vpt = M <= 8 * 152 ? 1 : 2;
-  while (p.G > vpt * (vpt == 1 ? 64 : 32)) vpt *= 2;
+  // One group per half warp, the shortest path through a row (2000 x 1024 5.4 us, two groups 6.8);
+  // of many long rows as many as leave 8 warps a block (8000 x 7168 four groups 107, two 128,
+  // one 193; 4000 x 2944 two groups 27.9, one 31, four 29.9)
+  int vpt = 1;
+  while (vpt < 4 && (p.G > vpt * (vpt == 1 ? 64 : 32) || (M > 8 * 152 && p.G > vpt * 16)))
+    vpt *= 2;
   const int threads = ((p.G + vpt - 1) / vpt * 16 + 31) / 32 * 32;
   const unsigned grid = static_cast<unsigned>(M);
-  // element-by-element rows pass through shared memory
-  const bool vectors = H % 128 == 0 && p.wide_h && (!p.y || p.wide_y) &&
-                       (!p.gate || p.gate_col != 1 || p.wide_gate) && p.wide_gpost &&
-                       p.wide_gpre && (!p.h_out || p.wide_h_out) && (!p.n || p.wide_n) &&
-                       (!p.q || p.wide_q);
+  const bool vectors = H % 128 == 0 && wide(a->h, a->ld_h, he, 16) &&
+                       (!a->y || wide(a->y, a->ld_y, ye, 16)) &&
+                       (!a->gate || a->gate_col != 1 || wide(a->gate, a->gate_row, ge, 16)) &&
+                       aligned(a->gamma_post, 16) && aligned(a->gamma_pre, 16) &&
+                       (!a->h_out || wide(a->h_out, a->ld_h_out, he, 16)) &&
+                       (!a->n || wide(a->n, a->ld_n, 2, 16)) &&
+                       (!a->q || wide(a->q, a->ld_q, 1, 8));
   const bool plain = (a->y && p.y_f32) ||
                      (a->gate && p.gate_col != 0 && (p.gate_col != 1 || p.gate_f32));
-  const size_t smem = vectors ? 0 : threads / 16 * 512;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   // Enough values to fill the device (160 x 7168: 3.6 us, eight per thread 4.6; 400 x 2048: 3.3
@@ -1117,11 +1120,11 @@ extern "C" int klt_block_norm(const klt_block_norm_args* a, void* stream) {
                     (!a->y || wide(a->y, a->ld_y, ye, 32)) &&
                     (!a->h_out || wide(a->h_out, a->ld_h_out, he, 32)) &&
                     (!a->n || wide(a->n, a->ld_n, 2, 32)) && (!a->q || wide(a->q, a->ld_q, 1, 16));
-  // Rows of any start and length: the same with 16 per thread (1021 x 2901 11.6 us, norm_kernel
-  // 14.4; 4000 x 7001 94 and 156; 160 x 2901 6.6 and 7.4; 16 x 12001 10.2 and 16.7), but for few
-  // values (16 x 2901 5.8 and 5.1; 160 x 300 5.6 and 4.3 us); 32 per thread took 150 us for the
-  // 4000 x 7001.
-  const bool any = !vectors && !plain && (H > 4096 || static_cast<int64_t>(M) * H > 1 << 18);
+  // Rows of any start and length: the same with 16 per thread from about a million values on
+  // (1021 x 2901 11.6 us, norm_kernel 18.2; 1000 x 7001 31 and 38; 300 x 7001 8.2 and 9.8; but
+  // 1000 x 1016 8.0 and 5.8, 16 x 2901 6.3 and 3.1); 32 per thread took 150 us for 4000 x 7001,
+  // 16 per thread 94.
+  const bool any = !vectors && !plain && static_cast<int64_t>(M) * H > 5 << 18;
   if (many) {
     const bool twice = H > 8192 || (M > 8 * 152 && H > (p.h_f32 ? 6144 : 2560));
     const int per = twice ? 32 : 16;
@@ -1134,22 +1137,19 @@ extern "C" int klt_block_norm(const klt_block_norm_args* a, void* stream) {
     e = p.h_f32 ? launch_many<true, true>(twice, grid, lanes, st, p)
                 : launch_many<false, true>(twice, grid, lanes, st, p);
   } else if (!vectors || plain) {
-    switch (vpt) {
-      case 1: e = launch_pdl(norm_kernel<1>, grid, threads, smem, st, p); break;
-      case 2: e = launch_pdl(norm_kernel<2>, grid, threads, smem, st, p); break;
-      default: e = launch_pdl(norm_kernel<4>, grid, threads, smem, st, p); break;
-    }
+    e = plain ? launch_row<2>(grid, st, p) : p.h_f32 ? launch_row<1>(grid, st, p)
+                                                     : launch_row<0>(grid, st, p);
   } else if (p.h_f32) {
     switch (vpt) {
-      case 1: e = launch_pdl(norm_vec_kernel<1, true>, grid, threads, 0, st, p); break;
-      case 2: e = launch_pdl(norm_vec_kernel<2, true>, grid, threads, 0, st, p); break;
-      default: e = launch_pdl(norm_vec_kernel<4, true>, grid, threads, 0, st, p); break;
+      case 1: e = launch_pdl(norm_vec_kernel<1, true>, grid, threads, st, p); break;
+      case 2: e = launch_pdl(norm_vec_kernel<2, true>, grid, threads, st, p); break;
+      default: e = launch_pdl(norm_vec_kernel<4, true>, grid, threads, st, p); break;
     }
   } else {
     switch (vpt) {
-      case 1: e = launch_pdl(norm_vec_kernel<1, false>, grid, threads, 0, st, p); break;
-      case 2: e = launch_pdl(norm_vec_kernel<2, false>, grid, threads, 0, st, p); break;
-      default: e = launch_pdl(norm_vec_kernel<4, false>, grid, threads, 0, st, p); break;
+      case 1: e = launch_pdl(norm_vec_kernel<1, false>, grid, threads, st, p); break;
+      case 2: e = launch_pdl(norm_vec_kernel<2, false>, grid, threads, st, p); break;
+      default: e = launch_pdl(norm_vec_kernel<4, false>, grid, threads, st, p); break;
     }
   }
   return status_of(e);

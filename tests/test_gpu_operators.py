@@ -295,7 +295,7 @@ def test_block_norm_in_place_and_allocating():
     assert (np.abs(_f64(n0) - ref[2]) <= HALF[BF16] * np.abs(ref[2]) + 1.01 * ref[3]).all()
 
 
-@pytest.mark.parametrize("M,H", [(40, 333), (300, 1029), (2000, 512)])
+@pytest.mark.parametrize("M,H", [(40, 333), (300, 1029), (2000, 512), (1400, 1029)])
 def test_block_norm_chain_in_place(M, H):
     """A residual stream updated in place by many calls in a row, whose rows share cache lines
     (odd widths): launches overlap, and each sees what the one before wrote."""
@@ -321,7 +321,10 @@ def test_block_norm_chain_in_place(M, H):
 @pytest.mark.parametrize("hd", [BF16, F32])
 @pytest.mark.parametrize("M,H,pad", [
     (600, 500, 0), (2100, 129, 1), (70000, 5, 0), (600, 517, 3), (9, 4099, 0), (7, 4616, 8),
-    (5, 8200, 7), (3, 12001, 0), (2, 16384, 5), (130, 2560, 8)])
+    (5, 8200, 7), (3, 12001, 0), (2, 16384, 5), (130, 2560, 8),
+    # many values
+    (2700, 517, 3), (300000, 5, 0), (11000, 129, 1), (2700, 500, 0), (350, 4099, 0),
+    (300, 4616, 8), (170, 8200, 7), (120, 12001, 0), (90, 16383, 2), (530, 2560, 5)])
 def test_block_norm_rows_of_any_start(M, H, pad, hd):
     """Every tensor's rows start on another element, and nothing around them is written."""
     rng = _gen(21, M, H, pad)
