@@ -151,6 +151,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.klt_linear_status.restype = ctypes.c_int
     lib.klt_linear_destroy.argtypes = [vp]
     lib.klt_linear_destroy.restype = ctypes.c_int
+    import torch  # noqa: F401  (the module below links to its libraries)
+
     from . import _marshal as marshal
     _marshal = marshal
     _LIB = lib

@@ -8,6 +8,7 @@ module beside it marshals the arguments of the operators around the tail.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -62,22 +63,40 @@ def build(verbose: bool = False, force: bool = False, ptxas_info: bool = False) 
                 sys.stderr.write(res.stdout + res.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    # the CPython module of the operators' calls, against torch's headers
+    gxx = shutil.which("g++") or "g++"
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+
+    def compile_marshal() -> str:
+        path, obj = os.path.join(CSRC, "klt_marshal.cpp"), os.path.join(OUT_DIR, "klt_marshal.o")
+        if force or _stale(obj, [path, hdrs[-1]]):
+            cmd = [gxx, "-O2", "-std=c++17", "-fPIC", "-Wall", "-c", path, "-o", obj]
+            cmd += ["-I" + d for d in (os.path.join(torch_dir, "include"),
+                                       os.path.join(cuda, "include"),
+                                       sysconfig.get_paths()["include"])]
+            res = subprocess.run(cmd, capture_output=True, text=True)
+            if res.returncode != 0:
+                raise RuntimeError(f"g++ failed for klt_marshal.cpp:\n{res.stdout}\n{res.stderr}")
+        return obj
+
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        marshal = ex.submit(compile_marshal)
         objs = list(ex.map(compile_one, SOURCES))
+        marshal_obj = marshal.result()
     if force or _stale(LIB_PATH, objs):
         cmd = [nvcc, *ARCH, "-shared", "-cudart", "shared", "-o", LIB_PATH, *objs]
         res = subprocess.run(cmd, capture_output=True, text=True)
         if res.returncode != 0:
             raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
-    marshal = os.path.join(CSRC, "klt_marshal.cpp")
-    if force or _stale(MARSHAL_PATH, [marshal, LIB_PATH]):
-        cmd = [nvcc, "-O2", "-std=c++17", "-shared", "-cudart", "shared", "-Xcompiler",
-               "-fPIC,-Wall", "-I" + sysconfig.get_paths()["include"], marshal, "-o",
-               MARSHAL_PATH, "-L" + PKG_DIR, "-Xlinker", "-l:libklt.so", "-Xlinker",
-               "-rpath=$ORIGIN"]
+    if force or _stale(MARSHAL_PATH, [marshal_obj, LIB_PATH]):
+        cmd = [gxx, "-shared", marshal_obj, "-o", MARSHAL_PATH, "-L" + PKG_DIR, "-l:libklt.so",
+               "-L" + os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+               "-lc10_cuda", "-L" + os.path.join(cuda, "lib64"), "-lcudart",
+               "-Wl,-rpath,$ORIGIN:" + os.path.join(torch_dir, "lib")]
         res = subprocess.run(cmd, capture_output=True, text=True)
         if res.returncode != 0:
-            raise RuntimeError(f"nvcc failed for klt_marshal.cpp:\n{res.stdout}\n{res.stderr}")
+            raise RuntimeError(f"link failed for _marshal:\n{res.stdout}\n{res.stderr}")
     return LIB_PATH
 
 

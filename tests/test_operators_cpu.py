@@ -109,6 +109,22 @@ def test_binding_refuses_host_tensors(lib):
         B.Fp8Linear(torch.zeros(256, 256, dtype=torch.uint8), torch.ones(2, 2))
 
 
+def test_binding_refuses_what_is_no_strided_tensor(lib):
+    class Lookalike:
+        dtype, shape = torch.bfloat16, (4, 256)
+
+    q, s = torch.zeros(4, 256, dtype=torch.uint8), torch.zeros(4, 2)
+    for x in (None, 3, [1.0], Lookalike()):
+        with pytest.raises(TypeError):
+            B.quantize_fp8(x, q, s)
+    with pytest.raises(TypeError):
+        B.quantize_fp8(torch.zeros(4, 256, dtype=torch.float16), q, s)
+    with pytest.raises(ValueError):
+        B.quantize_fp8(torch.zeros(4, 256).to_sparse(), q, s)
+    with pytest.raises(ValueError):
+        B.quantize_fp8(torch.zeros(4, 256, device="meta"), q, s)
+
+
 def test_fp8_codes_rows_start_on_16_bytes():
     q = B.fp8_codes(3, 130, "cpu")
     assert q.shape == (3, 130) and q.stride() == (144, 1) and q.dtype == torch.float8_e4m3fn
