@@ -308,7 +308,8 @@ int klt_route_noalloc(const float* logits, int32_t M, int32_t E, int32_t topk, i
  * graphs; none of them keeps state between calls, so calls on several streams may overlap
  * as long as their outputs differ.  Strides (ld_*) count elements from one row to the next;
  * columns are contiguous.  Tensors of these calls need the alignment of their element type
- * only, except where a rule is given; rows that start on 16 bytes are faster. */
+ * only, except where a rule is given; rows that start on 16 bytes are faster.  What lies
+ * between two rows of an input may be read; between rows of an output nothing is written. */
 
 /* Element types of activations. */
 enum klt_dtype {
@@ -403,9 +404,9 @@ typedef struct klt_linear_debug {
  * [ceil(N / 128), ceil(K / 128)]; both device memory, copied (re-laid out) into memory the
  * handle owns; the caller's buffers are not referenced after the call returns.
  * Synchronous, on the legacy default stream, and not during a stream's capture.
- * Errors: KLT_ERR_INVALID_ARG (null pointer), KLT_ERR_UNSUPPORTED (shape or format rules above; N or K above 2^20; device is not compute capability 10.3),
- * KLT_ERR_ALIGN (w_scale not 4-byte aligned), KLT_ERR_OOM, KLT_ERR_CUDA.  On error *out is
- * left NULL. */
+ * Errors: KLT_ERR_INVALID_ARG (null pointer), KLT_ERR_UNSUPPORTED (shape or format rules
+ * above; N or K above 2^20; device is not compute capability 10.3), KLT_ERR_ALIGN (w_scale not
+ * 4-byte aligned), KLT_ERR_OOM, KLT_ERR_CUDA.  On error *out is left NULL. */
 int klt_linear_create(const klt_linear_dims* d, const void* w, const float* w_scale,
                       klt_linear** out);
 

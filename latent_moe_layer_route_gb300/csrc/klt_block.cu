@@ -11,6 +11,8 @@
 // e4m3 once each, n from the unrounded h' (one rounding on each path, not two in a row).
 #include "klt_linear.cuh"
 
+#include <type_traits>
+
 
 #include "../../include/klt.h"
 
@@ -324,6 +326,53 @@ struct Raw16 {
     return pack2(__uint_as_float(t << 16), __uint_as_float(t & 0xFFFF0000u));
   }
 };
+// Columns of a row of C that starts on any element, in two steps: load() issues the loads of the
+// aligned vectors that hold them; settle(), once all of a row's are in flight, shifts the values
+// into place and makes those past C 0 (load_any does both at once: 4000 x 2901 44.4 us, so 41.5).
+// A vector may hold bytes of a neighbouring row, but none outside the tensor's span lo .. hi: of
+// its first and last only what is in there is read.
+template <bool F32>
+struct Any16 : Raw16<F32> {
+  static constexpr int ES = F32 ? 4 : 2, N = 4 * ES;  // words
+  uint32_t t[N + 4];
+  int r;
+  KLT_DEV void load(const char* lo, const char* hi, int64_t off, int c, int C) {
+    const char* at = lo + (off + c) * ES;
+    r = static_cast<int>(reinterpret_cast<uintptr_t>(at) & 15);
+#pragma unroll
+    for (int i = 0; i < N / 4 + 1; ++i) {
+      const char* v = at - r + 16 * i;
+      uint4 q = make_uint4(0, 0, 0, 0);
+      if (16 * i - r < (C - c) * ES && (i < N / 4 || r)) {
+        if (v >= lo && v + 16 <= hi)
+          q = *reinterpret_cast<const uint4*>(v);
+        else
+          q = load_part(v, clamp16(lo - v), clamp16(hi - v));
+      }
+      t[4 * i] = q.x, t[4 * i + 1] = q.y, t[4 * i + 2] = q.z, t[4 * i + 3] = q.w;
+    }
+  }
+  KLT_DEV void settle(int c, int C) {
+    if (r) shift_words<N>(t, r);
+    if (c + 16 > C) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        if (F32)
+          t[i] = c + i < C ? t[i] : 0;
+        else
+          t[i] = c + 2 * i + 1 < C ? t[i] : c + 2 * i < C ? t[i] & 0xFFFFu : 0;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i)
+      this->w[i] = make_uint4(t[4 * i], t[4 * i + 1], t[4 * i + 2], t[4 * i + 3]);
+  }
+};
+// The end of `rows` rows of C columns.
+template <bool F32>
+KLT_DEV const char* span_end(const void* base, int64_t rows, int64_t ld, int C) {
+  return static_cast<const char*>(base) + ((rows - 1) * ld + C) * (F32 ? 4 : 2);
+}
 template <bool F32>
 KLT_DEV void put16(void* base, int64_t off, const f32x2* v) {  // rows on 32 bytes
   char* p = static_cast<char*>(base) + off * (F32 ? 4 : 2);
@@ -828,8 +877,9 @@ __global__ void __launch_bounds__(512) norm_many_kernel(NormParams p) {
   __shared__ float part[2][32];
   const int64_t row = blockIdx.x;
   const int c0 = static_cast<int>(threadIdx.x) * 16, step = static_cast<int>(blockDim.x) * 16;
-  Raw16<HF32> hr[VPT];
-  Raw16<false> yr[VPT], g;
+  typename std::conditional<ANY, Any16<HF32>, Raw16<HF32>>::type hr[VPT];
+  typename std::conditional<ANY, Any16<false>, Raw16<false>>::type yr[VPT];
+  Raw16<false> g;
   pdl_trigger();
   pdl_wait();
 #pragma unroll
@@ -838,8 +888,26 @@ __global__ void __launch_bounds__(512) norm_many_kernel(NormParams p) {
     hr[i].clear();
     yr[i].clear();
     if (c < p.H) {
-      if (p.y) load16<ANY, false, true>(yr[i], p.y, row * p.ld_y, c, p.H);
-      load16<ANY, HF32, true>(hr[i], p.h, row * p.ld_h, c, p.H);
+      if constexpr (ANY) {
+        if (p.y)
+          yr[i].load(static_cast<const char*>(p.y), span_end<false>(p.y, gridDim.x, p.ld_y, p.H),
+                     row * p.ld_y, c, p.H);
+        hr[i].load(static_cast<const char*>(p.h), span_end<HF32>(p.h, gridDim.x, p.ld_h, p.H),
+                   row * p.ld_h, c, p.H);
+      } else {
+        if (p.y) yr[i].template load<true>(p.y, row * p.ld_y + c);
+        hr[i].template load<true>(p.h, row * p.ld_h + c);
+      }
+    }
+  }
+  if constexpr (ANY) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = c0 + i * step;
+      if (c < p.H) {
+        if (p.y) yr[i].settle(c, p.H);
+        hr[i].settle(c, p.H);
+      }
     }
   }
   float lo, hi, scale = p.branch_scale;
@@ -1121,9 +1189,9 @@ extern "C" int klt_block_norm(const klt_block_norm_args* a, void* stream) {
                     (!a->h_out || wide(a->h_out, a->ld_h_out, he, 32)) &&
                     (!a->n || wide(a->n, a->ld_n, 2, 32)) && (!a->q || wide(a->q, a->ld_q, 1, 16));
   // Rows of any start and length: the same with 16 per thread from about a million values on
-  // (1021 x 2901 11.6 us, norm_kernel 18.2; 1000 x 7001 31 and 38; 300 x 7001 8.2 and 9.8; but
+  // (1021 x 2901 11.2 us, norm_kernel 18.2; 1000 x 7001 31 and 38; 300 x 7001 8.2 and 9.8; but
   // 1000 x 1016 8.0 and 5.8, 16 x 2901 6.3 and 3.1); 32 per thread took 150 us for 4000 x 7001,
-  // 16 per thread 94.
+  // 16 per thread 89.
   const bool any = !vectors && !plain && static_cast<int64_t>(M) * H > 5 << 18;
   if (many) {
     const bool twice = H > 8192 || (M > 8 * 152 && H > (p.h_f32 ? 6144 : 2560));
