@@ -323,9 +323,10 @@ enum klt_dtype {
  * that is 0), codes e4m3(fp32(x / s)), nearest even, saturating; the last group may be
  * short.  The same values as the tail's own latent quantisation.  A group that
  * holds an infinity or a NaN gets a scale that is not finite.
- * Any K >= 1; M == 0 launches nothing.  Bytes of q between K and ld_q are left as they are.
+ * Any K from 1 to 2^28; M == 0 launches nothing.  Bytes of q between K and ld_q are left as
+ * they are.
  * Errors: KLT_ERR_INVALID_ARG (M < 0, K < 1, null pointer, negative or overlapping output
- * stride), KLT_ERR_UNSUPPORTED (unknown x_dtype, more than 2^31 launch blocks),
+ * stride), KLT_ERR_UNSUPPORTED (unknown x_dtype, K too large, more than 2^31 groups),
  * KLT_ERR_ALIGN (element alignment), KLT_ERR_CUDA. */
 int klt_quantize(const void* x, int32_t x_dtype, int64_t ld_x, int32_t M, int32_t K,
                  uint8_t* q, int64_t ld_q, float* s, void* stream);

@@ -1067,7 +1067,8 @@ using namespace klt;
 extern "C" int klt_quantize(const void* x, int32_t x_dtype, int64_t ld_x, int32_t M, int32_t K,
                             uint8_t* q, int64_t ld_q, float* s, void* stream) {
   if (M < 0 || K < 1) return KLT_ERR_INVALID_ARG;
-  if (!known(x_dtype)) return KLT_ERR_UNSUPPORTED;
+  // offsets within a row are 32 bits
+  if (!known(x_dtype) || K > (1 << 28)) return KLT_ERR_UNSUPPORTED;
   if (M == 0) return KLT_OK;
   if (!x || !q || !s) return KLT_ERR_INVALID_ARG;
   if (ld_x < 0 || !rows_ok(ld_q, M, K)) return KLT_ERR_INVALID_ARG;

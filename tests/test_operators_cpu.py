@@ -28,6 +28,7 @@ def _quant(lib, x=PTR, dtype=B.KLT_DT_BF16, ld_x=256, M=4, K=256, q=PTR, ld_q=25
     (dict(s=None), B.KLT_ERR_INVALID_ARG), (dict(ld_q=255), B.KLT_ERR_INVALID_ARG),
     (dict(ld_x=-256), B.KLT_ERR_INVALID_ARG), (dict(dtype=2), B.KLT_ERR_UNSUPPORTED),
     (dict(dtype=9), B.KLT_ERR_UNSUPPORTED), (dict(x=PTR + 1), B.KLT_ERR_ALIGN),
+    (dict(M=1, K=2 ** 28 + 1, ld_q=2 ** 29), B.KLT_ERR_UNSUPPORTED),
     (dict(x=PTR + 2, dtype=B.KLT_DT_F32), B.KLT_ERR_ALIGN), (dict(s=PTR + 2), B.KLT_ERR_ALIGN),
     (dict(M=0, x=None), B.KLT_OK)])
 def test_quantize_arguments(lib, kw, code):
