@@ -879,7 +879,14 @@ __global__ void __launch_bounds__(512) norm_many_kernel(NormParams p) {
   const int c0 = static_cast<int>(threadIdx.x) * 16, step = static_cast<int>(blockDim.x) * 16;
   typename std::conditional<ANY, Any16<HF32>, Raw16<HF32>>::type hr[VPT];
   typename std::conditional<ANY, Any16<false>, Raw16<false>>::type yr[VPT];
-  Raw16<false> g;
+  // One set of columns per thread: the weights' loads go out with the row's (8192 x 2048 25.1 us,
+  // so 23.1; with two sets their registers cost more than that saves: 8192 x 7168 88 and 107 us).
+  // Else the gate's go with the weight's where there are registers (88 and 86.4; fp32 rows 117
+  // and 135).
+  constexpr bool EARLY = VPT == 1 && !ANY, TOGETHER = !HF32 && !ANY;
+  Raw16<false> post, other, g;
+  Raw16<false>& gate = EARLY || TOGETHER ? other : post;
+  const bool columns = p.gate && p.gate_col != 0;
   pdl_trigger();
   pdl_wait();
 #pragma unroll
@@ -897,6 +904,10 @@ __global__ void __launch_bounds__(512) norm_many_kernel(NormParams p) {
       } else {
         if (p.y) yr[i].template load<true>(p.y, row * p.ld_y + c);
         hr[i].template load<true>(p.h, row * p.ld_h + c);
+      }
+      if (EARLY) {
+        if (p.gamma_post) load16<ANY>(post, p.gamma_post, 0, c, p.H);
+        if (columns) load16<ANY>(gate, p.gate, row * p.gate_row, c, p.H);
       }
     }
   }
@@ -939,16 +950,19 @@ __global__ void __launch_bounds__(512) norm_many_kernel(NormParams p) {
         f32x2 u[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) u[j] = yr[i].get(j);
-        if (p.gamma_post) {
-          load16<ANY>(g, p.gamma_post, 0, c, p.H);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) u[j] = mul2(u[j], g.get(j));
+        if (!EARLY) {
+          if (p.gamma_post) load16<ANY>(post, p.gamma_post, 0, c, p.H);
+          if (columns && TOGETHER) load16<ANY>(gate, p.gate, row * p.gate_row, c, p.H);
         }
-        if (p.gate && p.gate_col != 0) {
-          load16<ANY>(g, p.gate, row * p.gate_row, c, p.H);
+        if (p.gamma_post) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) u[j] = mul2(u[j], post.get(j));
+        }
+        if (columns) {
+          if (!EARLY && !TOGETHER) load16<ANY>(gate, p.gate, row * p.gate_row, c, p.H);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            f32x2 w = g.get(j);
+            f32x2 w = gate.get(j);
             if (p.sigmoid) {
               unpack2(w, lo, hi);
               w = pack2(gate_value(lo, true), gate_value(hi, true));
@@ -1182,8 +1196,9 @@ extern "C" int klt_block_norm(const klt_block_norm_args* a, void* stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   // Enough values to fill the device (160 x 7168: 3.6 us, eight per thread 4.6; 400 x 2048: 3.3
-  // and 2.9 us), in rows that start on 32 bytes: 16 per thread, and twice that once there are
-  // many long rows (8192 x 7168 to codes 79 and 91 us, 8192 x 2048 23.5 and 22.9 us).
+  // and 2.9 us), in rows that start on 32 bytes: 16 per thread, and twice that for many long rows
+  // of bf16 (8192 x 7168 to codes 86.8 and 96.6 us; 8192 x 2048 25.9 and 23.1, fp32 rows of 7168
+  // 117 either way), but with a gate of their own (8192 x 7168 119 and 108).
   const bool many = M > 152 && static_cast<int64_t>(M) * H > 1 << 20 && vectors && !plain &&
                     wide(a->h, a->ld_h, he, 32) &&
                     (!a->y || wide(a->y, a->ld_y, ye, 32)) &&
@@ -1195,7 +1210,8 @@ extern "C" int klt_block_norm(const klt_block_norm_args* a, void* stream) {
   // 16 per thread 89.
   const bool any = !vectors && !plain && static_cast<int64_t>(M) * H > 5 << 18;
   if (many) {
-    const bool twice = H > 8192 || (M > 8 * 152 && H > (p.h_f32 ? 6144 : 2560));
+    const bool full = a->gate && a->gate_col != 0 && a->gate_row != 0;
+    const bool twice = H > 8192 || (M > 8 * 152 && H > 4096 && !p.h_f32 && !full);
     const int per = twice ? 32 : 16;
     const unsigned lanes = ((H + per - 1) / per + 31) / 32 * 32;
     e = p.h_f32 ? launch_many<true, false>(twice, grid, lanes, st, p)
