@@ -98,8 +98,7 @@ KLT_DEV void store_codes(const Half& hw, uint8_t* q, int64_t off, int c, int C, 
 
 // The largest magnitude of a group, NaN if it holds one.
 KLT_DEV float group_amax(const Half& hw, const float* v) {
-  float m = max_nan(max_nan(max_nan(v[0], v[1]), max_nan(v[2], v[3])),
-                    max_nan(max_nan(v[4], v[5]), max_nan(v[6], v[7])));
+  float m = max_nan(max_nan(v[0], v[1], v[2]), max_nan(v[3], v[4], v[5]), max_nan(v[6], v[7]));
 #pragma unroll
   for (int o = 8; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(hw.mask, m, o));
   return m;
@@ -486,7 +485,7 @@ KLT_DEV float group_amax16(const f32x2* v) {
   for (int i = 0; i < 8; ++i) {
     float lo, hi;
     unpack2(v[i], lo, hi);
-    m = max_nan(m, max_nan(lo, hi));
+    m = max_nan(m, lo, hi);
   }
 #pragma unroll
   for (int o = 4; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
@@ -740,7 +739,7 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormParams p) {
     }
     if (p.q) {
       // n = t r with t = h' gamma: t against its own largest magnitude, r enters the scale alone
-      float m = max_nan(max_nan(h[i][0], h[i][1]), max_nan(h[i][2], h[i][3]));
+      float m = max_nan(max_nan(h[i][0], h[i][1], h[i][2]), h[i][3]);
 #pragma unroll
       for (int o = 16; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
       const float d = over_448(m);

@@ -277,6 +277,13 @@ KLT_DEV float max_nan(float a, float b) {
   return r;
 }
 
+// The same of three.
+KLT_DEV float max_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // ------------------------------------------------------------------ launches
 cudaError_t launch_linear_narrow(const CUtensorMap& tok, const LinParams& p, int bn, int split,
                                  bool swiglu, cudaStream_t s);

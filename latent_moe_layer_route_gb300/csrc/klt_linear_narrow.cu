@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(Narrow<BN, ACT>::THREADS)
                                      silu_fast(g.z) * u.z, silu_fast(g.w) * u.w);
         if (p.out_dtype == KLT_DT_E4M3) {
           // the warp holds one group of 128 columns
-          float amax = max_nan(max_nan(v.x, v.y), max_nan(v.z, v.w));
+          float amax = max_nan(max_nan(v.x, v.y, v.z), v.w);
 #pragma unroll
           for (int o = 16; o; o >>= 1)
             amax = max_nan(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
