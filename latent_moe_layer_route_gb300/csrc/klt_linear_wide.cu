@@ -405,15 +405,16 @@ __global__ void __launch_bounds__(THREADS, 1)
               acc[0][i] = pack2(q0 * k, q1 * k);
             }
           }
+          // negated codes: two quotients at a time
+          const unsigned long long s2 = pack2(s, s), ninv2 = pack2(-inv, -inv);
           uint32_t w[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             float q[4];
-            unpack2(acc[0][2 * j], q[0], q[1]);
-            unpack2(acc[0][2 * j + 1], q[2], q[3]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) q[e] = quot_group(q[e], s, inv);
-            w[j] = f32x2_to_e4m3x2(q[0], q[1]) | (f32x2_to_e4m3x2(q[2], q[3]) << 16);
+            unpack2(neg_quot_group2(acc[0][2 * j], s2, ninv2), q[0], q[1]);
+            unpack2(neg_quot_group2(acc[0][2 * j + 1], s2, ninv2), q[2], q[3]);
+            w[j] = (f32x2_to_e4m3x2(q[0], q[1]) | (f32x2_to_e4m3x2(q[2], q[3]) << 16)) ^
+                   0x80808080u;
           }
           if (finish && m0 < p.M) {
             const int c = tn0 * 128 + half * 64;
