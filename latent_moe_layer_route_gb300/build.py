@@ -70,7 +70,7 @@ def build(verbose: bool = False, force: bool = False, ptxas_info: bool = False) 
 
     def compile_marshal() -> str:
         path, obj = os.path.join(CSRC, "klt_marshal.cpp"), os.path.join(OUT_DIR, "klt_marshal.o")
-        if force or _stale(obj, [path, hdrs[-1]]):
+        if force or _stale(obj, [path, hdrs[-1], os.path.join(torch_dir, "version.py")]):
             cmd = [gxx, "-O2", "-std=c++17", "-fPIC", "-Wall", "-c", path, "-o", obj]
             cmd += ["-I" + d for d in (os.path.join(torch_dir, "include"),
                                        os.path.join(cuda, "include"),
