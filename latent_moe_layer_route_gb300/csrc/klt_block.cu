@@ -534,7 +534,8 @@ KLT_DEV void quant_store(const Half& hw, const QuantParams& p, uint32_t it, uint
   store_codes(hw, p.q, row * p.ld_q, c, p.K, p.wide_q, codes8(v, s));
   if (hw.lane == 0) p.s[it] = s;
 }
-// Few groups, any strides and widths: one group of 128 columns per half warp.
+// Few groups, any strides and widths: one group of 128 columns per half warp (16 x 3584 1.4 us,
+// the hand-off between launches).
 __global__ void __launch_bounds__(256) quant_kernel(QuantParams p) {
   __shared__ float bufs[16 * 128];
   pdl_trigger();
@@ -550,7 +551,8 @@ __global__ void __launch_bounds__(256) quant_kernel(QuantParams p) {
   quant_store(hw, p, it, row, c, v);
 }
 // Eight lanes per group, U groups each, their loads in flight together.  Vectors throughout (K a
-// multiple of 128, aligned rows), or (ANY) any strides and widths.
+// multiple of 128, aligned rows: 8192 x 7168 27.3 us, 6.5 TB/s), or (ANY) any strides and widths
+// (8000 x 5003 24.8 us).
 template <int U, bool F32, bool ANY>
 __global__ void __launch_bounds__(256) quant_vec_kernel(QuantParams p) {
   pdl_trigger();

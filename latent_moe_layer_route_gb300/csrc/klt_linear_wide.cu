@@ -8,7 +8,9 @@
 //
 // The scales are general fp32 per 128 columns, so every k-block's product is read from TMEM
 // and added into registers times xs[m, kb] * ws[rb, kb]: that reading (128 KB per CTA and
-// k-block, two 256-column slots in turn), not the multiplication, bounds the kernel.
+// k-block, two 256-column slots in turn), not the multiplication, bounds the kernel: 830 cycles
+// per k-block, where multiplications and copies alone take 734.  4096 x 7168 x 3584 in 81 us
+// (2.6 PFLOP/s), 8192 x 4096 x 7168 SwiGLU to codes in 183 to 191 us, under the power limit.
 //
 // Persistent: one pair per two SMs, tiles dealt round robin, token tiles fastest (the pairs
 // that run together share weight tiles in L2).  Where there are too few tiles for that, two
