@@ -675,7 +675,7 @@ KLT_DEV void store1(void* p, bool f32, int64_t i, float v) {
 // lane and needs no alignment.  TYPE of the residual stream; 2: of y and of a gate across
 // channels too, with any stride.  The row's scalars (1/rms and the scales) multiply last: y
 // gamma gate is exact up to its final rounding for bf16 tensors, and h' is one multiply-add of
-// it.
+// it.  16 x 2901 in 3.1 us, the latency of one block.
 template <int VPT, int TYPE>
 __global__ void __launch_bounds__(1024) norm_kernel(NormParams p) {
   constexpr int OTHER = TYPE == 2 ? 2 : 0;
@@ -764,6 +764,8 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormParams p) {
 
 // The same for rows that are vectors throughout (H a multiple of 128, aligned; y and gates
 // across channels in bf16): the row's loads are in flight together and stay packed until used.
+// Few rows: 1 x 7168 2.6 us, 16 x 7168 of fp32 to codes 3.8 us, the latency of one block and the
+// hand-off between launches.
 template <int VPT, bool HF32>
 __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) norm_vec_kernel(NormParams p) {
   __shared__ float part[2][32];
@@ -872,7 +874,9 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) norm_vec_kernel(NormPar
 }
 
 // Many rows: one block per row, VPT times 16 columns per thread, pairs throughout.  Of vectors
-// that start on 32 bytes, or (ANY) of any start and length.
+// that start on 32 bytes (8192 x 7168 to bf16 73.6 us, 6.4 TB/s; to codes with a gate 85.7, 4.8
+// TB/s: instructions, and registers that limit an SM to three rows), or (ANY) of any start and
+// length (1021 x 2901 11.1 us).
 template <int VPT, bool HF32, bool ANY>
 __global__ void __launch_bounds__(512) norm_many_kernel(NormParams p) {
   __shared__ float part[2][32];

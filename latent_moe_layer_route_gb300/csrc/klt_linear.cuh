@@ -94,10 +94,11 @@ KLT_DEV void tma_load_2d_pair(void* dst, const CUtensorMap* map, uint32_t bar, i
 // Stores the shared-memory box at (c0 = inner element index, c1 = row) of a tensor; parts
 // outside of it are not written.  Completion is tracked per thread (bulk groups).
 KLT_DEV void tma_store_2d(const CUtensorMap* map, const void* src, int c0, int c1) {
-  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(smem_u32(src)), "r"(c0), "r"(c1)
-               : "memory");
+  asm volatile(
+      "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(smem_u32(src)), "r"(c0), "r"(c1)
+      : "memory");
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 // All but this thread's last N bulk stores have read their shared memory.
