@@ -762,18 +762,20 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormParams p) {
   }
 }
 
-// The same for rows that are vectors throughout (H a multiple of 128, aligned; y and gates
-// across channels in bf16): the row's loads are in flight together and stay packed until used.
-// Few rows: 1 x 7168 2.6 us, 16 x 7168 of fp32 to codes 3.8 us, the latency of one block and the
-// hand-off between launches.
-template <int VPT, bool HF32>
+// The same for rows that are vectors throughout (H a multiple of 128, aligned), of any types: the
+// row's loads are in flight together and stay packed until used.  Few rows: 1 x 7168 2.6 us, 16 x
+// 7168 of fp32 to codes 3.8 us, the latency of one block and the hand-off between launches; many:
+// those of fp32 y or gate (8192 x 7168 of fp32 y to bf16 86 us, 6.8 TB/s; norm_kernel 258).
+template <int VPT, bool HF32, bool YF32, bool GF32>
 __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) norm_vec_kernel(NormParams p) {
   __shared__ float part[2][32];
   const Half hw = half_warp(nullptr);
   const int64_t row = blockIdx.x;
   const int c0 = static_cast<int>(threadIdx.x) * 8, step = static_cast<int>(blockDim.x) * 8;
   Raw8<HF32> hr[VPT];
-  Raw8<false> yr[VPT], g1[VPT], g2[VPT], gt[VPT];
+  Raw8<YF32> yr[VPT];
+  Raw8<false> g1[VPT], g2[VPT];
+  Raw8<GF32> gt[VPT];
   pdl_trigger();
   pdl_wait();
 #pragma unroll
@@ -781,6 +783,7 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) norm_vec_kernel(NormPar
     const int c = c0 + i * step;
     hr[i].w[0] = yr[i].w[0] = make_uint4(0, 0, 0, 0);
     if (HF32) hr[i].w[HF32] = make_uint4(0, 0, 0, 0);
+    if (YF32) yr[i].w[YF32] = make_uint4(0, 0, 0, 0);
     if (c < p.H) {
       if (p.y) yr[i].load(p.y, row * p.ld_y + c);
       hr[i].load(p.h, row * p.ld_h + c);
@@ -1054,6 +1057,16 @@ cudaError_t launch_row(unsigned grid, cudaStream_t st, const NormParams& p) {
                        : launch_pdl(norm_kernel<4, TYPE>, grid, lanes, st, p);
 }
 
+template <bool HF32, bool YF32, bool GF32>
+cudaError_t launch_vec(int vpt, unsigned grid, unsigned threads, cudaStream_t st,
+                       const NormParams& p) {
+  switch (vpt) {
+    case 1: return launch_pdl(norm_vec_kernel<1, HF32, YF32, GF32>, grid, threads, st, p);
+    case 2: return launch_pdl(norm_vec_kernel<2, HF32, YF32, GF32>, grid, threads, st, p);
+    default: return launch_pdl(norm_vec_kernel<4, HF32, YF32, GF32>, grid, threads, st, p);
+  }
+}
+
 template <bool HF32, bool ANY>
 cudaError_t launch_many(bool twice, unsigned grid, unsigned lanes, cudaStream_t st,
                         const NormParams& p) {
@@ -1196,8 +1209,10 @@ extern "C" int klt_block_norm(const klt_block_norm_args* a, void* stream) {
                        (!a->h_out || wide(a->h_out, a->ld_h_out, he, 16)) &&
                        (!a->n || wide(a->n, a->ld_n, 2, 16)) &&
                        (!a->q || wide(a->q, a->ld_q, 1, 8));
-  const bool plain = (a->y && p.y_f32) ||
-                     (a->gate && p.gate_col != 0 && (p.gate_col != 1 || p.gate_f32));
+  // stride of a gate across channels, 0 if there is none: neighbouring columns, or any
+  const int64_t columns = a->gate ? a->gate_col : 0;
+  // types and strides that only some of the kernels take
+  const bool plain = (a->y && p.y_f32) || columns > 1 || (columns == 1 && p.gate_f32);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   // Enough values to fill the device (160 x 7168: 3.6 us, eight per thread 4.6; 400 x 2048: 3.3
@@ -1226,21 +1241,19 @@ extern "C" int klt_block_norm(const klt_block_norm_args* a, void* stream) {
     const unsigned lanes = ((H + (twice ? 31 : 15)) / (twice ? 32 : 16) + 31) / 32 * 32;
     e = p.h_f32 ? launch_many<true, true>(twice, grid, lanes, st, p)
                 : launch_many<false, true>(twice, grid, lanes, st, p);
-  } else if (!vectors || plain) {
+  } else if (!vectors || columns > 1) {
     e = plain ? launch_row<2>(grid, st, p) : p.h_f32 ? launch_row<1>(grid, st, p)
                                                      : launch_row<0>(grid, st, p);
-  } else if (p.h_f32) {
-    switch (vpt) {
-      case 1: e = launch_pdl(norm_vec_kernel<1, true>, grid, threads, st, p); break;
-      case 2: e = launch_pdl(norm_vec_kernel<2, true>, grid, threads, st, p); break;
-      default: e = launch_pdl(norm_vec_kernel<4, true>, grid, threads, st, p); break;
-    }
   } else {
-    switch (vpt) {
-      case 1: e = launch_pdl(norm_vec_kernel<1, false>, grid, threads, st, p); break;
-      case 2: e = launch_pdl(norm_vec_kernel<2, false>, grid, threads, st, p); break;
-      default: e = launch_pdl(norm_vec_kernel<4, false>, grid, threads, st, p); break;
-    }
+    const bool yf = a->y && p.y_f32, gf = columns == 1 && p.gate_f32;
+    auto vec = [&](auto hf32) {
+      constexpr bool H32 = decltype(hf32)::value;
+      if (yf && gf) return launch_vec<H32, true, true>(vpt, grid, threads, st, p);
+      if (yf) return launch_vec<H32, true, false>(vpt, grid, threads, st, p);
+      if (gf) return launch_vec<H32, false, true>(vpt, grid, threads, st, p);
+      return launch_vec<H32, false, false>(vpt, grid, threads, st, p);
+    };
+    e = p.h_f32 ? vec(std::true_type()) : vec(std::false_type());
   }
   return status_of(e);
 }

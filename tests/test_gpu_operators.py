@@ -219,6 +219,13 @@ CASES = [  # M, H, h dtype, y dtype, gate shape, gate dtype, sigmoid, post, pre,
     (650, 1024, BF16, BF16, "f", BF16, False, True, False, "hqs", 0),
     (620, 1408, F32, BF16, None, BF16, False, False, False, "hnqs", 0),
     (650, 1024, BF16, F32, "f", F32, True, True, True, "hnqs", 16),
+    # fp32 block outputs and gates in aligned rows
+    (9, 2048, F32, F32, "c", BF16, True, True, True, "hnqs", 0),
+    (1300, 2560, BF16, F32, None, BF16, False, True, True, "hnqs", 0),
+    (1300, 2560, F32, BF16, "f", F32, True, True, True, "hnqs", 8),
+    (3, 16384, BF16, F32, "t", F32, True, True, True, "hnqs", 8),
+    (3, 12800, F32, F32, "f", F32, False, True, True, "hnqs", 0),
+    (1300, 640, BF16, F32, "x", F32, True, True, True, "hnqs", 0),
 ]
 
 
