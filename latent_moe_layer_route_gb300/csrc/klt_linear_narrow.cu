@@ -378,7 +378,13 @@ __global__ void __launch_bounds__(Narrow<BN, ACT>::THREADS)
   }
   tc_fence_before();
   __syncwarp();
-  cluster_wait();  // nothing more is stored into this CTA's memory, and its TMEM has been read
+  cluster_wait();  // every store into this CTA's memory has been issued, its TMEM has been read
+  // An asynchronous store is complete on its barrier alone, which a CTA whose waits ran out has not
+  // seen: its memory is the next CTA's only once they have all arrived.
+  if (threadIdx.x == 0) {
+    int none = 0;
+    mbar_wait(got, 0, &none, p.err, p.timeout);
+  }
   if (warp == C::EPI + 1) {
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM_COLS);

@@ -1,0 +1,36 @@
+"""klt_quantize, klt_block_norm and klt_linear_* on the GPU: the ends of their ranges, and what a
+call leaves to the next one when its waits run out."""
+import numpy as np
+import pytest
+import torch
+
+from latent_moe_layer_route_gb300 import binding as B
+from test_gpu_operators import Lin, _lib, _same  # noqa: F401  (_lib: the module's fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------- waits that run out
+
+@pytest.mark.parametrize("tile,split,act,out", [
+    (16, 2, "swiglu", "fp8"), (16, 8, "swiglu", "fp8"), (32, 4, "none", "bf16"),
+    (64, 8, "swiglu", "bf16"), (64, 2, "none", "f32"), (128, 2, "none", "bf16"),
+    (128, 4, "none", "f32")])
+@pytest.mark.parametrize("stall", [1, 3])
+def test_narrow_parts_that_come_late(tile, split, act, out, stall):
+    """The CTAs of a cluster give up and still store their parts into one another's memory; the
+    launches right behind them, which take over that memory, have the right results."""
+    bad, ok = (Lin(130, 512, 128 * 40, act, out, seed=s) for s in (2, 3))
+    form = dict(force_tile=tile, force_split=split)
+    want = ok.layer(ok.xq, ok.xs, debug=B.KltLinearDebug(**form))
+    ok.check(want)
+    torch.cuda.synchronize()
+    bad.layer(bad.xq, bad.xs, debug=B.KltLinearDebug(stall_after_kblocks=stall, timeout_ms=5, **form))
+    got = [ok.layer(ok.xq, ok.xs, debug=B.KltLinearDebug(**form)) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert bad.layer.status() == B.KLT_ERR_DEVICE_TIMEOUT
+    pick = (lambda g: g) if out == "fp8" else (lambda g: (g,))
+    for g in got:
+        assert all(_same(a, b) for a, b in zip(pick(g), pick(want)))
+    bad.layer.close()
+    ok.close()
