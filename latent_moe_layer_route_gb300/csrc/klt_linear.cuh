@@ -62,6 +62,12 @@ KLT_DEV void st_async_f4(uint32_t addr, float a, float b, float c, float d, uint
       "r"(__float_as_uint(d)), "r"(bar)
       : "memory");
 }
+KLT_DEV void st_async_u32(uint32_t addr, uint32_t v, uint32_t bar) {  // one value, 4 bytes
+  asm volatile(
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr),
+      "r"(v), "r"(bar)
+      : "memory");
+}
 KLT_DEV ulonglong2 ld_shared_u64x2(uint32_t addr) {
   ulonglong2 v;
   asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(v.x), "=l"(v.y) : "r"(addr) : "memory");

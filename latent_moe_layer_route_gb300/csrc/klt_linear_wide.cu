@@ -39,8 +39,8 @@ static_assert(SMEM <= 232448, "shared memory of a block");
 struct Smem {
   uint8_t *ring, *stage;
   float* amax;  // [2][128]
-  uint64_t *full, *done, *tempty, *drain;
-  uint32_t* tmem_holder;
+  uint64_t *full, *done, *tempty, *drain, *ended;
+  uint32_t *tmem_holder, *copies;
   volatile int* abort_flag;
 };
 
@@ -158,9 +158,11 @@ __global__ void __launch_bounds__(THREADS, 1)
   sm.done = sm.full + STAGES;
   sm.tempty = sm.done + STAGES;
   sm.drain = sm.tempty + 2;
-  sm.tmem_holder = reinterpret_cast<uint32_t*>(sm.drain + 1);
+  sm.ended = sm.drain + 1;
+  sm.tmem_holder = reinterpret_cast<uint32_t*>(sm.ended + 1);
   sm.abort_flag = reinterpret_cast<volatile int*>(sm.tmem_holder + 1);
-  static_assert((2 * STAGES + 3) * 8 + 8 <= 256, "barrier space");
+  sm.copies = sm.tmem_holder + 2;
+  static_assert((2 * STAGES + 4) * 8 + 12 <= 256, "barrier space");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // this CTA's half of the pair's tokens and weight rows, the pair's first CTA, its part of K
@@ -188,8 +190,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int i = 0; i < 2; ++i)
       mbar_init(&sm.tempty[i], 16);  // first CTA's: the epilogue warps of both CTAs
     mbar_init(sm.drain, 1);
+    mbar_init(sm.ended, 1);  // first CTA's: the second has issued its last copy
     *sm.abort_flag = 0;
     fence_barrier_init();
+    mbar_arrive_expect_tx(sm.ended, 4);
   }
   if (warp == 2) tmem_alloc_pair(sm.tmem_holder, 512);
   tc_fence_before();
@@ -228,11 +232,23 @@ __global__ void __launch_bounds__(THREADS, 1)
                            (rb * p.KB + kb) * LIN_TILE);
         }
       }
-      // no copy of the pair is in flight past this point (both CTAs' complete here)
+      // No copy of the pair is in flight past this point: both CTAs' complete here.  After a wait
+      // that ran out the second CTA may have issued up to STAGES that the first has not expected.
       if (rank == 0) {
         int none = 0;
         for (int j = it > STAGES ? it - STAGES : 0; j < it; ++j)
           mbar_wait(&sm.full[j % STAGES], (j / STAGES) & 1, &none, p.err, p.timeout);
+        // its waits are bounded and began before this CTA's last ones ended
+        if (mbar_wait(sm.ended, 0, &none, p.err, 3 * p.timeout)) {
+          const int last = static_cast<int>(*static_cast<volatile uint32_t*>(sm.copies));
+          for (; it < last; ++it) {
+            mbar_arrive_expect_tx(&sm.full[it % STAGES], STAGE_BYTES);
+            mbar_wait(&sm.full[it % STAGES], (it / STAGES) & 1, &none, p.err, p.timeout);
+          }
+        }
+      } else {
+        st_async_u32(map_to_rank(smem_u32(sm.copies), leader), it,
+                     map_to_rank(smem_u32(sm.ended), leader));
       }
     } else if (warp == 1 && lane == 0 && rank == 0) {
       constexpr uint32_t idesc = idesc_make(0, 256, 256);
@@ -442,8 +458,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncwarp();
   }
   __syncthreads();
-  cluster_arrive();  // nothing of the pair still reads or signals across
+  cluster_arrive();  // nothing of the pair still reads across, and no MMA of it runs
   cluster_wait();
+  if (threadIdx.x == 0) {  // nor is a signal of its MMAs to this CTA on its way
+    int none = 0;
+    mbar_wait(sm.drain, 0, &none, p.err, p.timeout);
+  }
   if (warp == 2) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);

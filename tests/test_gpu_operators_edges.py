@@ -34,3 +34,26 @@ def test_narrow_parts_that_come_late(tile, split, act, out, stall):
         assert all(_same(a, b) for a, b in zip(pick(g), pick(want)))
     bad.layer.close()
     ok.close()
+
+
+@pytest.mark.parametrize("act,out", [("none", "f32"), ("swiglu", "fp8")])
+@pytest.mark.parametrize("M,N,split,stall", [
+    (600, 512, 1, 1), (600, 512, 1, 4), (600, 512, 1, 7),  # before, at and after the stages' reuse
+    (600, 512, 2, 1), (600, 512, 2, 4),  # parts of 4 and 5 k-blocks: the second one stops
+    (2600, 2048, 1, 12)])  # in the second tile of the pairs that have one
+def test_wide_pairs_that_give_up(M, N, split, stall, act, out):
+    """The same for the CTA pairs of the token-major kernel."""
+    bad, ok = (Lin(M, N, 128 * 9, act, out, seed=s) for s in (2, 3))
+    form = dict(force_tile=256, force_split=split)
+    want = ok.layer(ok.xq, ok.xs, debug=B.KltLinearDebug(**form))
+    ok.check(want)
+    torch.cuda.synchronize()
+    bad.layer(bad.xq, bad.xs, debug=B.KltLinearDebug(stall_after_kblocks=stall, timeout_ms=5, **form))
+    got = [ok.layer(ok.xq, ok.xs, debug=B.KltLinearDebug(**form)) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert bad.layer.status() == B.KLT_ERR_DEVICE_TIMEOUT
+    pick = (lambda g: g) if out == "fp8" else (lambda g: (g,))
+    for g in got:
+        assert all(_same(a, b) for a, b in zip(pick(g), pick(want)))
+    bad.layer.close()
+    ok.close()
