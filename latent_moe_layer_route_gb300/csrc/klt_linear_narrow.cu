@@ -180,6 +180,7 @@ __global__ void __launch_bounds__(Narrow<BN, ACT>::THREADS)
     __syncwarp();
   } else if (warp == C::EPI + 1) {
     if (lane == 0) {
+      pdl_wait();  // the bounds of the waits below begin when the tokens are there
       constexpr uint32_t idesc = idesc_make(0, 128, BN);
       int i = 0;
       for (; i < nk; ++i) {

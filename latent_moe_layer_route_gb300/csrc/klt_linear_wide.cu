@@ -251,6 +251,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                      map_to_rank(smem_u32(sm.ended), leader));
       }
     } else if (warp == 1 && lane == 0 && rank == 0) {
+      pdl_wait();  // the bounds of the waits below begin when the tokens are there
       constexpr uint32_t idesc = idesc_make(0, 256, 256);
       int it = 0;
       bool ok = true;

@@ -57,3 +57,33 @@ def test_wide_pairs_that_give_up(M, N, split, stall, act, out):
         assert all(_same(a, b) for a, b in zip(pick(g), pick(want)))
     bad.layer.close()
     ok.close()
+
+
+@pytest.mark.parametrize("tile", [16, 256])
+def test_the_bound_of_a_wait_does_not_count_the_launch_before(tile):
+    """A launch that outlasts the next one's bound on its waits and leaves SMs free for it: one tile
+    of 8192 k-blocks, some 3 ms, before a layer whose waits are bounded by 1 ms."""
+    K = 1 << 20
+    codes = torch.randint(0x30, 0x38, (256, K), dtype=torch.uint8, device="cuda")
+    x = torch.randint(0x30, 0x38, (200, K), dtype=torch.uint8, device="cuda")
+    slow = B.Fp8Linear(codes, torch.ones(2, K // 128, device="cuda"), out="f32")
+    xs = torch.ones(200, K // 128, device="cuda")
+    c = Lin(100, 256, 640, "none", "f32")
+    dbg = B.KltLinearDebug(force_tile=tile, force_split=1, timeout_ms=1)
+    c.check(c.layer(c.xq, c.xs, debug=dbg))
+    torch.cuda.synchronize()
+    out = torch.empty(200, 256, device="cuda")
+    first, last = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    first.record()
+    slow(x, xs, out, debug=B.KltLinearDebug(force_tile=256, force_split=1))
+    last.record()
+    torch.cuda.synchronize()
+    assert first.elapsed_time(last) > 1.5  # ms
+    for _ in range(3):
+        slow(x, xs, out, debug=B.KltLinearDebug(force_tile=256, force_split=1))
+        got = c.layer(c.xq, c.xs, debug=dbg)
+        torch.cuda.synchronize()
+        assert c.layer.status() == B.KLT_OK
+        c.check(got)
+    slow.close()
+    c.close()
