@@ -6,6 +6,7 @@ library cannot be loaded, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Dict, Optional
@@ -167,6 +168,17 @@ def _ptr(t) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
+def _memory_of(stream: Optional[int], like):
+    """Context in which torch allocates the outputs of a call on `stream` (a handle, or None for
+    the current one): on the current stream's memory, work queued there may still be running."""
+    if stream is None or not like.is_cuda:
+        return contextlib.nullcontext()
+    import torch
+    if stream in (0, 1):  # the legacy default stream
+        return torch.cuda.stream(torch.cuda.default_stream(like.device))
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=like.device))
+
+
 def dims_of(cfg, max_tokens: Optional[int] = None) -> KltDims:
     fmt = {"nvfp4": KLT_FMT_NVFP4, "mxfp8": KLT_FMT_MXFP8,
            "nvfp4_w4a4": KLT_FMT_NVFP4_W4A4}.get(cfg.routed_fmt, KLT_FMT_FP8_B128)
@@ -256,7 +268,8 @@ class LatentMoETail:
         import torch
         M = x.shape[0]
         if out is None:
-            out = torch.empty((M, self.cfg.H), dtype=torch.bfloat16, device=x.device)
+            with _memory_of(stream, x):
+                out = torch.empty((M, self.cfg.H), dtype=torch.bfloat16, device=x.device)
         if stream is None:
             stream = torch.cuda.current_stream(x.device).cuda_stream
         rc = klt_forward(self.handle, x, z, logits, M, out, routing, debug, stream)
@@ -273,7 +286,8 @@ class LatentMoETail:
         import torch
         M = x.shape[0]
         if out is None:
-            out = torch.empty((M, self.cfg.H), dtype=torch.bfloat16, device=x.device)
+            with _memory_of(stream, x):
+                out = torch.empty((M, self.cfg.H), dtype=torch.bfloat16, device=x.device)
         if stream is None:
             stream = torch.cuda.current_stream(x.device).cuda_stream
         rc = klt_forward_hidden(self.handle, x, M, out, routing, debug, stream)
@@ -306,7 +320,9 @@ class LatentMoETail:
 # ---------------------------------------------------------------- operators around the tail
 #
 # The checks that C cannot make of bare pointers (types, shapes, devices) and the calls are in
-# the _marshal module; what is here allocates what the caller did not give.
+# the _marshal module; what is here allocates what the caller did not give.  `stream` is a
+# stream's handle, or None for torch's current stream; outputs that a call allocates belong to the
+# stream it runs on, and inputs given from another stream's memory must outlive the call's work.
 
 def fp8_codes(M: int, K: int, device):
     """An uninitialised e4m3 tensor [M, K] whose rows start on 16 bytes, as the linear layer
@@ -326,10 +342,11 @@ def quantize_fp8(x, q=None, s=None, stream: Optional[int] = None):
         if x.dim() != 2:
             raise ValueError("x: not a matrix")
         M, K = x.shape
-        if q is None:
-            q = fp8_codes(M, K, x.device)
-        if s is None:
-            s = torch.empty((M, -(-K // 128)), dtype=torch.float32, device=x.device)
+        with _memory_of(stream, x):
+            if q is None:
+                q = fp8_codes(M, K, x.device)
+            if s is None:
+                s = torch.empty((M, -(-K // 128)), dtype=torch.float32, device=x.device)
     rc = _marshal.quantize(x, q, s, stream)
     if rc:
         raise KltError(rc, "klt_quantize")
@@ -373,9 +390,10 @@ class BlockNorm:
         the block is skipped.  Returns (h_out, n, q, s)."""
         if h_out is None and n is None and q is None and s is None:
             import torch
-            if y is not None:
-                h_out = torch.empty((h.shape[0], self.H), dtype=h.dtype, device=h.device)
-            n = torch.empty((h.shape[0], self.H), dtype=torch.bfloat16, device=h.device)
+            with _memory_of(stream, h):
+                if y is not None:
+                    h_out = torch.empty((h.shape[0], self.H), dtype=h.dtype, device=h.device)
+                n = torch.empty((h.shape[0], self.H), dtype=torch.bfloat16, device=h.device)
         rc = _marshal.block_norm(self._address, self._device, h, y, gate, h_out, n, q, s, stream)
         if rc:
             raise KltError(rc, "klt_block_norm")
@@ -432,12 +450,13 @@ class Fp8Linear:
         if out is None or (self.fp8 and out_s is None):
             import torch
             M = xq.shape[0]
-            if out is None:
-                out = fp8_codes(M, self.width, xq.device) if self.fp8 else \
-                    torch.empty((M, self.width), dtype=self._torch_dtype, device=xq.device)
-            if self.fp8 and out_s is None:
-                out_s = torch.empty((M, self.width // 128), dtype=torch.float32,
-                                    device=xq.device)
+            with _memory_of(stream, xq):
+                if out is None:
+                    out = fp8_codes(M, self.width, xq.device) if self.fp8 else \
+                        torch.empty((M, self.width), dtype=self._torch_dtype, device=xq.device)
+                if self.fp8 and out_s is None:
+                    out_s = torch.empty((M, self.width // 128), dtype=torch.float32,
+                                        device=xq.device)
         rc = _marshal.linear(self._address, self.device, self.K, self.width, self._dtype, xq, xs,
                              out, out_s, 0 if debug is None else ctypes.addressof(debug), stream)
         if rc:

@@ -4,7 +4,9 @@ import numpy as np
 import pytest
 import torch
 
+import parity_util as PU
 from latent_moe_layer_route_gb300 import binding as B
+from latent_moe_layer_route_gb300 import configs, inputs
 from test_gpu_operators import Lin, _lib, _same  # noqa: F401  (_lib: the module's fixture)
 
 pytestmark = pytest.mark.gpu
@@ -87,3 +89,57 @@ def test_the_bound_of_a_wait_does_not_count_the_launch_before(tile):
         c.check(got)
     slow.close()
     c.close()
+
+
+# ---------------------------------------------------------------- streams
+
+def _late_writer(nbytes):
+    """Memory of `nbytes` that torch may hand out again on the current stream, on which work that
+    writes it is still queued."""
+    torch.empty(64, dtype=torch.uint8, device="cuda").fill_(0)  # loads the kernel
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    blocks = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in nbytes]
+    torch.cuda._sleep(100_000_000)  # some 50 ms
+    for b in blocks:
+        b.fill_(0x55)
+
+
+@pytest.mark.parametrize("op", ["quantize", "norm", "linear", "linear_codes", "tail", "hidden"])
+def test_outputs_of_a_call_on_a_given_stream(op):
+    """What a call with `stream` allocates belongs to that stream: not to the current one, where
+    work that still uses it may be queued."""
+    M, H = 2048, 8192
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn((M, H), device="cuda", generator=g).bfloat16()
+    close = lambda: None  # noqa: E731
+    if op == "quantize":
+        sizes, call = (M * H, M * H // 32), lambda **k: B.quantize_fp8(x, **k)
+    elif op == "norm":
+        sizes, layer = (2 * M * H, 2 * M * H), B.BlockNorm(H, res_scale=0.5)
+        call = lambda **k: layer(x, x, **k)[:2]  # noqa: E731
+    elif op.startswith("linear"):
+        act, out, N = ("swiglu", "fp8", 8192) if op == "linear_codes" else ("none", "f32", 4096)
+        c = Lin(M, N, 256, act, out)
+        sizes = (M * N // 2, M * N // 64) if out == "fp8" else (M * N * 4,)
+        call, close = (lambda **k: c.layer(c.xq, c.xs, **k)), c.close
+    else:
+        cfg = configs.SMALL.with_(M=3000, E=8, topk=3, seed=41)
+        act, w = inputs.make_inputs(cfg)
+        w.update(inputs.make_projection_weights(cfg))
+        tail = B.LatentMoETail(cfg, PU.to_cuda(w), flags=B.KLT_FLAG_DETERMINISTIC)
+        a = PU.to_cuda(act)
+        sizes, close = (2 * cfg.M * cfg.H,), tail.close
+        call = (lambda **k: tail.forward(a["x"], a["z"], a["logits"], **k)) if op == "tail" else \
+            (lambda **k: tail.forward_hidden(a["x"], **k))
+    outs = lambda r: r if isinstance(r, tuple) else (r,)  # noqa: E731
+    want = [t.clone() for t in outs(call())]
+    side = torch.cuda.Stream()
+    _late_writer(sizes)
+    got = outs(call(stream=side.cuda_stream))
+    torch.cuda.synchronize()
+    assert all(_same(a, b) for a, b in zip(got, want))
+    got = outs(call(stream=0))  # the default stream
+    torch.cuda.synchronize()
+    assert all(_same(a, b) for a, b in zip(got, want))
+    close()
