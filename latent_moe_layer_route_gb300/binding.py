@@ -404,7 +404,8 @@ class BlockNorm:
 
 class Fp8Linear:
     """y = x W^T with e4m3 weights and a scale per 128 x 128 block (klt_linear_*); owns a
-    handle with its own copy of the weights, on the weights' device.
+    handle with its own copy of the weights, on the weights' device.  Threads may share it, but
+    close() must not overlap a call.
 
     w_q: e4m3 (or uint8 codes) [N, K]; w_s: fp32 [ceil(N/128), ceil(K/128)].  act "none" or
     "swiglu" (gate rows first; N/2 outputs); out "bf16", "f32" or, for SwiGLU, "fp8"."""

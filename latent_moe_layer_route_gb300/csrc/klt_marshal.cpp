@@ -86,7 +86,9 @@ bool read_rows(PyObject* t, const char* name, int kinds, long long* device, long
   return true;
 }
 
-// `fn` with `device` current, on `stream` (None: torch's current one there); its status.
+// `fn` with `device` current, on `stream` (None: torch's current one there); its status.  The
+// interpreter's lock is free meanwhile: a launch waits where the stream's queue is full, and what
+// has to run before it may be a host function that takes the lock.
 template <typename Fn>
 PyObject* launch(long long device, PyObject* stream, Fn fn) {
   void* s;
@@ -96,13 +98,14 @@ PyObject* launch(long long device, PyObject* stream, Fn fn) {
     s = reinterpret_cast<void*>(static_cast<uintptr_t>(PyLong_AsUnsignedLongLong(stream)));
     if (PyErr_Occurred()) return nullptr;
   }
-  int now = 0;
-  if (cudaGetDevice(&now) != cudaSuccess) return PyLong_FromLong(KLT_ERR_CUDA);
-  const bool other = now != device;
-  if (other && cudaSetDevice(static_cast<int>(device)) != cudaSuccess)
-    return PyLong_FromLong(KLT_ERR_CUDA);
-  const int rc = fn(s);
-  if (other) cudaSetDevice(now);
+  int now = 0, rc = KLT_ERR_CUDA;
+  Py_BEGIN_ALLOW_THREADS
+  if (cudaGetDevice(&now) == cudaSuccess) {
+    const bool other = now != device;
+    if (!other || cudaSetDevice(static_cast<int>(device)) == cudaSuccess) rc = fn(s);
+    if (other) cudaSetDevice(now);
+  }
+  Py_END_ALLOW_THREADS
   return PyLong_FromLong(rc);
 }
 

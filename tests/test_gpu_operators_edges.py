@@ -1,5 +1,8 @@
 """klt_quantize, klt_block_norm and klt_linear_* on the GPU: the ends of their ranges, and what a
 call leaves to the next one when its waits run out."""
+import threading
+import time
+
 import numpy as np
 import pytest
 import torch
@@ -143,3 +146,43 @@ def test_outputs_of_a_call_on_a_given_stream(op):
     torch.cuda.synchronize()
     assert all(_same(a, b) for a, b in zip(got, want))
     close()
+
+
+@pytest.mark.parametrize("op", ["quantize", "norm", "linear"])
+def test_other_threads_run_while_a_launch_waits(op):
+    """A call that waits for room in the stream's queue does not stop Python's other threads."""
+    c = Lin(4, 256, 256, "none", "f32")
+    x = torch.zeros((4, 256), device="cuda")
+    layer, n = B.BlockNorm(256), torch.empty((4, 256), device="cuda", dtype=torch.bfloat16)
+    q, s = B.fp8_codes(4, 256, "cuda"), torch.empty((4, 2), device="cuda")
+    out = torch.empty((4, 256), device="cuda")
+    call = {"quantize": lambda: B.quantize_fp8(x, q, s), "norm": lambda: layer(x, n=n),
+            "linear": lambda: c.layer(c.xq, c.xs, out)}[op]
+    for _ in range(3):
+        call()
+    torch.cuda._sleep(1)
+    torch.cuda.synchronize()
+    stop, gaps = threading.Event(), []
+
+    def tick():
+        last = time.perf_counter()
+        while not stop.is_set():
+            time.sleep(0.001)
+            now = time.perf_counter()
+            gaps.append(now - last)
+            last = now
+
+    clock = threading.Thread(target=tick)
+    clock.start()
+    torch.cuda._sleep(1_000_000_000)  # some 0.5 s
+    slowest = 0.0
+    for _ in range(4000):
+        t0 = time.perf_counter()
+        call()
+        slowest = max(slowest, time.perf_counter() - t0)
+    torch.cuda.synchronize()
+    stop.set()
+    clock.join()
+    c.close()
+    assert slowest > 0.2  # a call did wait
+    assert max(gaps) < 0.1
