@@ -92,7 +92,8 @@ class KltLinearDebug(ctypes.Structure):
 
 
 _LIB: Optional[ctypes.CDLL] = None
-_marshal = None  # the CPython module of the operators around the tail, loaded with the library
+_LIB_FILE: Optional[str] = None
+_marshal = None  # the CPython module of the operators around the tail, loaded by their first use
 
 
 class KltError(RuntimeError):
@@ -103,10 +104,10 @@ class KltError(RuntimeError):
 
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load libklt.so (built by ``build.build()``); raises if it is missing."""
-    global _LIB, _marshal
+    global _LIB, _LIB_FILE
     if _LIB is not None:
         return _LIB
-    if not os.path.exists(path) or not os.path.exists(MARSHAL_PATH):
+    if not os.path.exists(path):
         raise RuntimeError(f"libklt.so not built at {path}; run "
                            "latent_moe_layer_route_gb300.build.build() first")
     lib = ctypes.CDLL(path)
@@ -152,12 +153,24 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.klt_linear_status.restype = ctypes.c_int
     lib.klt_linear_destroy.argtypes = [vp]
     lib.klt_linear_destroy.restype = ctypes.c_int
-    import torch  # noqa: F401  (the module below links to its libraries)
+    _LIB, _LIB_FILE = lib, os.path.realpath(path)
+    return lib
+
+
+def _load_marshal():
+    """Load the module that the operators' calls go through.  It is linked to the libklt.so beside
+    it, so it works with that copy of the library alone."""
+    global _marshal
+    load_library()
+    if _LIB_FILE != os.path.realpath(LIB_PATH):
+        raise RuntimeError(f"the operators work with {LIB_PATH} only; loaded is {_LIB_FILE}")
+    if not os.path.exists(MARSHAL_PATH):
+        raise RuntimeError(f"the operators' module is not built at {MARSHAL_PATH}; run "
+                           "latent_moe_layer_route_gb300.build.build() first")
+    import torch  # noqa: F401  (the module links to its libraries)
 
     from . import _marshal as marshal
     _marshal = marshal
-    _LIB = lib
-    return lib
 
 
 def strerror(code: int) -> str:
@@ -335,8 +348,8 @@ def fp8_codes(M: int, K: int, device):
 def quantize_fp8(x, q=None, s=None, stream: Optional[int] = None):
     """e4m3 codes q [M, K] and fp32 scales s [M, ceil(K/128)] of x [M, K] (bf16 or fp32; rows
     may be strided) per row and 128 columns (klt_quantize)."""
-    if _LIB is None:
-        load_library()
+    if _marshal is None:
+        _load_marshal()
     if q is None or s is None:
         import torch
         if x.dim() != 2:
@@ -363,7 +376,8 @@ class BlockNorm:
                  res_scale: float = 1.0, branch_scale: float = 1.0,
                  gate_sigmoid: bool = False):
         import torch
-        load_library()
+        if _marshal is None:
+            _load_marshal()
         self.H = H
         self.gamma_post, self.gamma_pre = gamma_post, gamma_pre
         self._device = -1
@@ -413,7 +427,9 @@ class Fp8Linear:
     def __init__(self, w_q, w_s, act: str = "none", out: str = "bf16"):
         import torch
         self.handle = None
-        self._lib = load_library()
+        if _marshal is None:
+            _load_marshal()
+        self._lib = _LIB
         acts = {"none": KLT_ACT_NONE, "swiglu": KLT_ACT_SWIGLU}
         outs = {"bf16": KLT_DT_BF16, "f32": KLT_DT_F32, "fp8": KLT_DT_E4M3}
         if act not in acts or out not in outs:
