@@ -4,7 +4,8 @@ Each .cu file compiles to an object in parallel, then one shared-library link.  
 library links the CUDA runtime dynamically and reaches the driver's tensor-map encoder
 through the runtime's entry-point query, so it loads on a machine without a GPU driver
 (its entry points then fail with a CUDA status instead of refusing to load).  A small CPython
-module beside it marshals the arguments of the operators around the tail.
+module beside it marshals the arguments of the operators around the tail; the library and the tail
+need neither it nor torch's headers.
 """
 from __future__ import annotations
 
@@ -14,6 +15,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -21,7 +23,8 @@ ROOT = os.path.dirname(PKG_DIR)
 CSRC = os.path.join(PKG_DIR, "csrc")
 OUT_DIR = os.path.join(PKG_DIR, "_build")
 LIB_PATH = os.path.join(PKG_DIR, "libklt.so")
-MARSHAL_PATH = os.path.join(PKG_DIR, "_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))
+EXT_SUFFIX = sysconfig.get_config_var("EXT_SUFFIX")  # names the interpreter and the machine
+MARSHAL_PATH = os.path.join(PKG_DIR, "_marshal" + EXT_SUFFIX)
 SOURCES = ["klt_api.cu", "klt_route.cu", "klt_gemm.cu", "klt_wide.cu", "klt_noalloc.cu",
            "klt_block.cu", "klt_linear.cu", "klt_linear_narrow.cu", "klt_linear_wide.cu"]
 HEADERS = ["klt_device.cuh", "klt_internal.h", "klt_linear.cuh"]
@@ -44,6 +47,49 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _torch_dir() -> str:
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise ImportError("torch is not installed")
+    return spec.submodule_search_locations[0]
+
+
+def _gxx(cmd, what: str) -> None:
+    res = subprocess.run([shutil.which("g++") or "g++", *cmd], capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed for {what}:\n{res.stdout}\n{res.stderr}")
+
+
+def _cuda_dir(nvcc: str) -> str:
+    return os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
+
+
+def _compile_marshal(nvcc: str, header: str, force: bool) -> str:
+    """The CPython module of the operators' calls, against torch's and this interpreter's
+    headers."""
+    torch_dir = _torch_dir()
+    path = os.path.join(CSRC, "klt_marshal.cpp")
+    obj = os.path.join(OUT_DIR, "klt_marshal" + EXT_SUFFIX + ".o")
+    if force or _stale(obj, [path, header, os.path.join(torch_dir, "version.py")]):
+        import torch
+        includes = (os.path.join(torch_dir, "include"), os.path.join(_cuda_dir(nvcc), "include"),
+                    sysconfig.get_paths()["include"])
+        _gxx(["-O2", "-std=c++17", "-fPIC", "-Wall",
+              f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+              *("-I" + d for d in includes), "-c", path, "-o", obj], "klt_marshal.cpp")
+    return obj
+
+
+def _link_marshal(nvcc: str, obj: str, force: bool) -> None:
+    if not force and not _stale(MARSHAL_PATH, [obj, LIB_PATH]):
+        return
+    torch_lib = os.path.join(_torch_dir(), "lib")
+    _gxx(["-shared", obj, "-o", MARSHAL_PATH, "-L" + os.path.dirname(LIB_PATH), "-l:libklt.so",
+          "-L" + torch_lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+          "-L" + os.path.join(_cuda_dir(nvcc), "lib64"), "-lcudart",
+          "-Wl,-rpath,$ORIGIN:" + torch_lib], "_marshal")
+
+
 def build(verbose: bool = False, force: bool = False, ptxas_info: bool = False) -> str:
     nvcc = _nvcc()
     os.makedirs(OUT_DIR, exist_ok=True)
@@ -63,40 +109,21 @@ def build(verbose: bool = False, force: bool = False, ptxas_info: bool = False) 
                 sys.stderr.write(res.stdout + res.stderr)
         return obj
 
-    # the CPython module of the operators' calls, against torch's headers
-    gxx = shutil.which("g++") or "g++"
-    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
-    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
-
-    def compile_marshal() -> str:
-        path, obj = os.path.join(CSRC, "klt_marshal.cpp"), os.path.join(OUT_DIR, "klt_marshal.o")
-        if force or _stale(obj, [path, hdrs[-1], os.path.join(torch_dir, "version.py")]):
-            cmd = [gxx, "-O2", "-std=c++17", "-fPIC", "-Wall", "-c", path, "-o", obj]
-            cmd += ["-I" + d for d in (os.path.join(torch_dir, "include"),
-                                       os.path.join(cuda, "include"),
-                                       sysconfig.get_paths()["include"])]
-            res = subprocess.run(cmd, capture_output=True, text=True)
-            if res.returncode != 0:
-                raise RuntimeError(f"g++ failed for klt_marshal.cpp:\n{res.stdout}\n{res.stderr}")
-        return obj
-
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        marshal = ex.submit(compile_marshal)
+        marshal = ex.submit(_compile_marshal, nvcc, hdrs[-1], force)
         objs = list(ex.map(compile_one, SOURCES))
-        marshal_obj = marshal.result()
     if force or _stale(LIB_PATH, objs):
         cmd = [nvcc, *ARCH, "-shared", "-cudart", "shared", "-o", LIB_PATH, *objs]
         res = subprocess.run(cmd, capture_output=True, text=True)
         if res.returncode != 0:
             raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
-    if force or _stale(MARSHAL_PATH, [marshal_obj, LIB_PATH]):
-        cmd = [gxx, "-shared", marshal_obj, "-o", MARSHAL_PATH, "-L" + PKG_DIR, "-l:libklt.so",
-               "-L" + os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
-               "-lc10_cuda", "-L" + os.path.join(cuda, "lib64"), "-lcudart",
-               "-Wl,-rpath,$ORIGIN:" + os.path.join(torch_dir, "lib")]
-        res = subprocess.run(cmd, capture_output=True, text=True)
-        if res.returncode != 0:
-            raise RuntimeError(f"link failed for _marshal:\n{res.stdout}\n{res.stderr}")
+    try:
+        _link_marshal(nvcc, marshal.result(), force)
+    except (RuntimeError, ImportError, OSError) as e:
+        # the library is complete; the operators' Python calls say that their module is missing
+        if os.path.exists(MARSHAL_PATH):
+            os.remove(MARSHAL_PATH)
+        warnings.warn(f"the operators' Python module is not built: {e}", RuntimeWarning)
     return LIB_PATH
 
 

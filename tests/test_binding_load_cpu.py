@@ -74,3 +74,34 @@ except ValueError as e:  # a host tensor
     assert "CUDA" in str(e), e
 """, link)
     assert r.returncode == 0, r.stdout + r.stderr
+
+
+@pytest.mark.parametrize("broken", ["torch", "compiler"])
+def test_the_library_builds_where_the_operators_module_does_not(tmp_path, broken):
+    """Without torch, or where the module's compiler fails, build() still makes libklt.so, and no
+    module of an earlier build stays beside it."""
+    r = _python("""
+import os, sys, warnings
+from latent_moe_layer_route_gb300 import build as b
+out, broken = sys.argv[1:]
+b.OUT_DIR, b.LIB_PATH = out, os.path.join(out, "libklt.so")
+b.MARSHAL_PATH = os.path.join(out, "_marshal.so")
+b.SOURCES = ["klt_noalloc.cu"]  # one of them will do
+open(b.MARSHAL_PATH, "w").close()
+os.utime(b.MARSHAL_PATH, (0, 0))
+if broken == "torch":
+    find = b.importlib.util.find_spec
+    b.importlib.util.find_spec = lambda name, *a: None if name == "torch" else find(name, *a)
+else:
+    b._gxx = lambda cmd, what: (_ for _ in ()).throw(RuntimeError("no compiler"))
+with warnings.catch_warnings(record=True) as seen:
+    warnings.simplefilter("always")
+    assert b.build() == b.LIB_PATH
+assert os.path.exists(b.LIB_PATH) and not os.path.exists(b.MARSHAL_PATH)
+assert any("not built" in str(w.message) for w in seen), [str(w.message) for w in seen]
+""", tmp_path, broken)
+    assert r.returncode == 0, r.stdout + r.stderr
+
+
+def test_the_modules_object_belongs_to_one_interpreter():
+    assert os.path.exists(os.path.join(build.OUT_DIR, "klt_marshal" + build.EXT_SUFFIX + ".o"))
