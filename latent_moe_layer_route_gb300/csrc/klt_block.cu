@@ -614,8 +614,8 @@ KLT_DEV float rms_inverse(float sum, float inv_h, float eps) {
   return rsqrtf(fmaf(sum, inv_h, eps));
 }
 KLT_DEV float gate_value(float g, bool sigmoid) {
-  // the divisor of the fast divide stays in its range: for g < -80 the gate is below 2e-35
-  return sigmoid ? __fdividef(1.0f, 1.0f + __expf(-fmaxf(g, -80.0f))) : g;
+  // (a divisor beyond the fast divide's range makes it 0, as the gate is there to 1e-38)
+  return sigmoid ? __fdividef(1.0f, 1.0f + __expf(-g)) : g;
 }
 KLT_DEV float load1(const void* p, bool f32, int64_t i) {
   return f32 ? static_cast<const float*>(p)[i]

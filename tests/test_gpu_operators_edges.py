@@ -186,3 +186,26 @@ def test_other_threads_run_while_a_launch_waits(op):
     c.close()
     assert slowest > 0.2  # a call did wait
     assert max(gaps) < 0.1
+
+
+# ---------------------------------------------------------------- sigmoid gates
+
+@pytest.mark.parametrize("gate", ["channel", "token", "full", "strided"])
+@pytest.mark.parametrize("M,H,pad", [(3, 256, 0), (5, 301, 0), (200, 8192, 0), (1400, 1001, 0),
+                                     (1300, 6144, 0), (200, 8192, 8)])
+@pytest.mark.parametrize("gd", [torch.bfloat16, torch.float32])
+def test_sigmoid_gates_that_are_no_numbers(M, H, pad, gate, gd):
+    """A gate of NaN gives NaN, an infinite one 0 or 1, whichever kernel takes the row."""
+    shape = {"channel": (1, H), "token": (M, 1), "full": (M, H), "strided": (M, 2 * H)}[gate]
+    g = torch.zeros(shape, device="cuda", dtype=gd)
+    if gate == "strided":
+        g = g[:, ::2]
+    rows, cols = g.shape
+    for i, v in enumerate((float("nan"), float("inf"), -float("inf"))):
+        g[i % rows, (3 + 5 * i) % cols] = v
+    h = torch.zeros((M, H + pad), device="cuda")[:, :H]
+    y = torch.ones((M, H + pad), device="cuda", dtype=torch.bfloat16)[:, :H]
+    out = torch.empty((M, H), device="cuda")
+    B.BlockNorm(H, gate_sigmoid=True)(h, y, g, h_out=out)
+    torch.testing.assert_close(out, torch.sigmoid(g.float()).expand(M, H), rtol=1e-6, atol=0,
+                               equal_nan=True)
