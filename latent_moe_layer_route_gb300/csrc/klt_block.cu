@@ -613,10 +613,7 @@ KLT_DEV float block_sum(float v, float* part) {
 KLT_DEV float rms_inverse(float sum, float inv_h, float eps) {
   return rsqrtf(fmaf(sum, inv_h, eps));
 }
-KLT_DEV float gate_value(float g, bool sigmoid) {
-  // (a divisor beyond the fast divide's range makes it 0, as the gate is there to 1e-38)
-  return sigmoid ? __fdividef(1.0f, 1.0f + __expf(-g)) : g;
-}
+KLT_DEV float gate_value(float g, bool sigmoid) { return sigmoid ? klt::sigmoid(g) : g; }
 KLT_DEV float load1(const void* p, bool f32, int64_t i) {
   return f32 ? static_cast<const float*>(p)[i]
              : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
@@ -881,7 +878,7 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) norm_vec_kernel(NormPar
 // TB/s: instructions, and registers that limit an SM to three rows), or (ANY) of any start and
 // length (1021 x 2901 11.1 us).
 template <int VPT, bool HF32, bool ANY>
-__global__ void __launch_bounds__(512) norm_many_kernel(NormParams p) {
+KLT_DEV void norm_many_row(const NormParams& p) {
   __shared__ float part[2][32];
   const int64_t row = blockIdx.x;
   const int c0 = static_cast<int>(threadIdx.x) * 16, step = static_cast<int>(blockDim.x) * 16;
@@ -1033,6 +1030,14 @@ __global__ void __launch_bounds__(512) norm_many_kernel(NormParams p) {
   }
 }
 
+template <int VPT, bool HF32, bool ANY>
+__global__ void __launch_bounds__(512) norm_many_kernel(NormParams p) {
+  norm_many_row<VPT, HF32, ANY>(p);
+}
+// Long bf16 rows: with one register more an SM takes two rows instead of three (8192 x 7168 to
+// codes 112 us, so 86).
+__global__ void __maxnreg__(80) norm_long_kernel(NormParams p) { norm_many_row<2, false, false>(p); }
+
 template <typename Kernel, typename... Params>
 cudaError_t launch_pdl(Kernel k, unsigned grid, unsigned block, cudaStream_t s,
                        const Params&... p) {
@@ -1070,8 +1075,11 @@ cudaError_t launch_vec(int vpt, unsigned grid, unsigned threads, cudaStream_t st
 template <bool HF32, bool ANY>
 cudaError_t launch_many(bool twice, unsigned grid, unsigned lanes, cudaStream_t st,
                         const NormParams& p) {
-  return twice ? launch_pdl(norm_many_kernel<2, HF32, ANY>, grid, lanes, st, p)
-               : launch_pdl(norm_many_kernel<1, HF32, ANY>, grid, lanes, st, p);
+  if (!twice) return launch_pdl(norm_many_kernel<1, HF32, ANY>, grid, lanes, st, p);
+  if constexpr (!HF32 && !ANY)
+    return launch_pdl(norm_long_kernel, grid, lanes, st, p);
+  else
+    return launch_pdl(norm_many_kernel<2, HF32, ANY>, grid, lanes, st, p);
 }
 
 int status_of(cudaError_t e) {

@@ -10,7 +10,7 @@ import torch
 import parity_util as PU
 from latent_moe_layer_route_gb300 import binding as B
 from latent_moe_layer_route_gb300 import configs, inputs
-from test_gpu_operators import Lin, _lib, _same  # noqa: F401  (_lib: the module's fixture)
+from test_gpu_operators import EPS, Lin, _lib, _same  # noqa: F401  (_lib: the module's fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -209,3 +209,23 @@ def test_sigmoid_gates_that_are_no_numbers(M, H, pad, gate, gd):
     B.BlockNorm(H, gate_sigmoid=True)(h, y, g, h_out=out)
     torch.testing.assert_close(out, torch.sigmoid(g.float()).expand(M, H), rtol=1e-6, atol=0,
                                equal_nan=True)
+
+
+@pytest.mark.parametrize("gate", ["channel", "token", "full", "strided"])
+@pytest.mark.parametrize("M,H,pad", [(3, 256, 0), (5, 301, 0), (200, 8192, 0), (1400, 1001, 0),
+                                     (1300, 6144, 0), (200, 8192, 8)])
+def test_sigmoid_gates_over_their_range(M, H, pad, gate):
+    """u sigmoid(g) of u = 1 into an fp32 stream.  An exponential within 2 ulp (4 EPS) and a
+    reciprocal within 1 (2 EPS), an addition, a product of the two and a multiply-add: 9 EPS of the
+    value, with one more for the product with u; where e^g is subnormal, its steps of 2^-149 too."""
+    shape = {"channel": (1, H), "token": (M, 1), "full": (M, H), "strided": (M, 2 * H)}[gate]
+    rng = np.random.default_rng([7, M, H, pad])
+    g = torch.from_numpy(rng.uniform(-104, 104, shape).astype(np.float32)).cuda()
+    if gate == "strided":
+        g = g[:, ::2]
+    h = torch.zeros((M, H + pad), device="cuda")[:, :H]
+    y = torch.ones((M, H + pad), device="cuda", dtype=torch.bfloat16)[:, :H]
+    out = torch.empty((M, H + pad), device="cuda")[:, :H]
+    B.BlockNorm(H, gate_sigmoid=True)(h, y, g, h_out=out)
+    want = torch.sigmoid(g.double()).expand(M, H)
+    assert ((out.double() - want).abs() <= 10 * EPS * want + 2.0 ** -148).all()
