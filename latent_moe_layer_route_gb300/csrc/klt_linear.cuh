@@ -241,11 +241,11 @@ KLT_DEV float sigmoid(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
   return x < 0.f ? e * r : r;
 }
-// SiLU g / (1 + e^-g) with the fast exponential and reciprocal (each within 2 ulp); the
-// exponent is clamped so that the divisor stays finite (below -80 the result is under 1e-32).
-KLT_DEV float silu_rcp(float g) {
+// SiLU g / (1 + e^-g) with the fast exponential and reciprocal.  No clamp: far below 0 the divisor
+// is infinite and its reciprocal 0, so that g, however large, leaves nothing.
+KLT_DEV float silu(float g) {
   float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + __expf(-fmaxf(g, -80.0f))));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + __expf(-g)));
   return g * r;
 }
 

@@ -344,8 +344,8 @@ __global__ void __launch_bounds__(Narrow<BN, ACT>::THREADS)
       const int c = rb * 128 + lane * 4;
       if (ACT) {
         const float4 g = sum[0], u = sum[C::AT - 1];
-        const float4 v = make_float4(silu_fast(g.x) * u.x, silu_fast(g.y) * u.y,
-                                     silu_fast(g.z) * u.z, silu_fast(g.w) * u.w);
+        const float4 v = make_float4(silu(g.x) * u.x, silu(g.y) * u.y,
+                                     silu(g.z) * u.z, silu(g.w) * u.w);
         if (p.out_dtype == KLT_DT_E4M3) {
           // the warp holds one group of 128 columns
           float amax = max_nan(max_nan(v.x, v.y, v.z), v.w);

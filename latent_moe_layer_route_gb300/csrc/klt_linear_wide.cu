@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           float g0, g1, u0, u1;
           unpack2(acc[0][i], g0, g1);
           unpack2(acc[1][i], u0, u1);
-          const float a0 = silu_rcp(g0) * u0, a1 = silu_rcp(g1) * u1;
+          const float a0 = silu(g0) * u0, a1 = silu(g1) * u1;
           big = max_nan(big, a0, a1);
           acc[0][i] = pack2(a0, a1);
         }

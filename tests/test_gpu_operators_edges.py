@@ -229,3 +229,35 @@ def test_sigmoid_gates_over_their_range(M, H, pad, gate):
     B.BlockNorm(H, gate_sigmoid=True)(h, y, g, h_out=out)
     want = torch.sigmoid(g.double()).expand(M, H)
     assert ((out.double() - want).abs() <= 10 * EPS * want + 2.0 ** -148).all()
+
+
+# ---------------------------------------------------------------- SwiGLU
+
+def _swiglu_of_scales(g, u_over_g, tile):
+    """silu(g) u of gates g and up values u = g * u_over_g: codes of 1, so that a product is its
+    scale.  Returns (bf16 outputs, codes, scales); all 128 columns of a row are equal."""
+    M = len(g)
+    one = torch.zeros((256, 128), dtype=torch.uint8, device="cuda")
+    one[:, 0] = 0x38
+    xq = torch.zeros((M, 128), dtype=torch.uint8, device="cuda")
+    xq[:, 0] = 0x38
+    xs = torch.from_numpy(np.asarray(g, dtype=np.float32)).cuda()[:, None]
+    ws = torch.tensor([[1.0], [u_over_g]], device="cuda")
+    dbg = B.KltLinearDebug(force_tile=tile)
+    out = B.Fp8Linear(one, ws, "swiglu", "bf16")(xq, xs, debug=dbg)
+    q, s = B.Fp8Linear(one, ws, "swiglu", "fp8")(xq, xs, debug=dbg)
+    assert (out.view(torch.int16) == out.view(torch.int16)[:, :1]).all()
+    return out[:, 0].double().cpu().numpy(), q[:, 0].cpu(), s[:, 0].double().cpu().numpy()
+
+
+@pytest.mark.parametrize("tile", [16, 32, 64, 256])
+def test_swiglu_of_gates_far_below_zero(tile):
+    """silu runs to 0 there: nothing is left of it, whatever the up value, and a group of it is
+    zeros with a scale of 1; of an infinite gate the definition is NaN."""
+    far = np.array([-200.0, -600.0, -1e4, -1e10, -1e30, -3e38])
+    out, q, s = _swiglu_of_scales(np.concatenate([far, [-np.inf, np.nan, 1e4]]), 1.0, tile)
+    n = len(far)
+    assert (out[:n] == 0).all() and (s[:n] == 1).all()
+    assert (q[:n].view(torch.uint8) & 0x7F == 0).all()
+    assert np.isnan(out[n:n + 2]).all() and not np.isfinite(s[n:n + 2]).any()
+    assert abs(out[-1] / 1e8 - 1) <= 2.0 ** -8 and abs(s[-1] * 448 / 1e8 - 1) <= 4 * EPS
