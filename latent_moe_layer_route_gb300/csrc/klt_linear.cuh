@@ -241,13 +241,8 @@ KLT_DEV float sigmoid(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
   return x < 0.f ? e * r : r;
 }
-// SiLU g / (1 + e^-g) with the fast exponential and reciprocal.  No clamp: far below 0 the divisor
-// is infinite and its reciprocal 0, so that g, however large, leaves nothing.
-KLT_DEV float silu(float g) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + __expf(-g)));
-  return g * r;
-}
+// SiLU; far below 0 the factor is 0, so that g, however large, leaves nothing.
+KLT_DEV float silu(float g) { return g * sigmoid(g); }
 
 // amax / 448, correctly rounded: the quotient by the rounded 1/448 corrected by its residual,
 // or by division where that would leave the normal range.

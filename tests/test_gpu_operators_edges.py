@@ -261,3 +261,19 @@ def test_swiglu_of_gates_far_below_zero(tile):
     assert (q[:n].view(torch.uint8) & 0x7F == 0).all()
     assert np.isnan(out[n:n + 2]).all() and not np.isfinite(s[n:n + 2]).any()
     assert abs(out[-1] / 1e8 - 1) <= 2.0 ** -8 and abs(s[-1] * 448 / 1e8 - 1) <= 4 * EPS
+
+
+@pytest.mark.parametrize("tile", [16, 32, 64, 256])
+def test_swiglu_over_the_gates_range(tile):
+    """The scale of a group of equal values is their magnitude over 448, in fp32: an exponential
+    within 2 ulp (4 EPS), a reciprocal within 1 (2 EPS), an addition, three products, the division
+    by 448 and its inputs' own products with their scales (exact here): 12 EPS, and the steps of
+    2^-149 of a subnormal e^g times |g u| / 448, and of the scale itself."""
+    rng = np.random.default_rng([8, tile])
+    g = np.concatenate([rng.uniform(-104, 104, 900), rng.uniform(-20, 5, 900)]).astype(np.float32)
+    out, q, s = _swiglu_of_scales(g, 0.5, tile)
+    g = g.astype(np.float64)
+    want = np.abs(g / (1 + np.exp(-g)) * g * 0.5) / 448
+    err = 12 * EPS * want + 2.0 ** -148 * (g * g * 0.5 / 448 + 1)
+    zero = want + err < 2.0 ** -148  # the scale of nothing is 1
+    assert ((np.abs(s - want) <= err) | (zero & (s == 1))).all()
