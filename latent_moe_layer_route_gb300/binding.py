@@ -378,6 +378,8 @@ class BlockNorm:
         import torch
         if _marshal is None:
             _load_marshal()
+        if not 1 <= H <= KLT_BLOCK_NORM_MAX_H:  # here: ctypes would cut it to 32 bits
+            raise KltError(KLT_ERR_INVALID_ARG if H < 1 else KLT_ERR_UNSUPPORTED, "BlockNorm")
         self.H = H
         self.gamma_post, self.gamma_pre = gamma_post, gamma_pre
         self._device = -1
@@ -447,6 +449,8 @@ class Fp8Linear:
         self.fp8 = out == "fp8"
         self._dtype = outs[out]
         self._torch_dtype = torch.float32 if out == "f32" else torch.bfloat16
+        if max(self.N, self.K) > 0x7FFFFFFF:  # ctypes would cut it to 32 bits
+            raise KltError(KLT_ERR_UNSUPPORTED, "klt_linear_create")
         d = KltLinearDims(self.N, self.K, acts[act], outs[out])
         h = ctypes.c_void_p()
         # the create copies on the legacy default stream; what wrote the weights may have run

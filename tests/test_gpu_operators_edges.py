@@ -277,3 +277,15 @@ def test_swiglu_over_the_gates_range(tile):
     err = 12 * EPS * want + 2.0 ** -148 * (g * g * 0.5 / 448 + 1)
     zero = want + err < 2.0 ** -148  # the scale of nothing is 1
     assert ((np.abs(s - want) <= err) | (zero & (s == 1))).all()
+
+
+# ---------------------------------------------------------------- sizes beyond 32 bits
+
+def test_a_layers_sizes_are_not_cut_to_32_bits():
+    """2^32 + 256 rows of weights are more than a layer takes; cut to 32 bits they would be 256."""
+    N = (1 << 32) + 256
+    w = torch.zeros((N, 1), dtype=torch.uint8, device="cuda")
+    s = torch.ones((N // 128, 1), device="cuda")
+    with pytest.raises(B.KltError) as e:
+        B.Fp8Linear(w, s)
+    assert e.value.code == B.KLT_ERR_UNSUPPORTED
