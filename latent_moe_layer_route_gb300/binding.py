@@ -370,7 +370,8 @@ class BlockNorm:
     """The norms before and after a block with its gate and residual scale (klt_block_norm).
 
     gamma_post, gamma_pre: bf16 [H] or None (that norm is left out).  The object keeps the
-    weights and scales; it has no other state."""
+    weights and scales; it has no other state.  New weights are copied into the tensors it was
+    given, or go into a new object."""
 
     def __init__(self, H: int, gamma_post=None, gamma_pre=None, eps: float = 1e-6,
                  res_scale: float = 1.0, branch_scale: float = 1.0,
@@ -380,8 +381,7 @@ class BlockNorm:
             _load_marshal()
         if not 1 <= H <= KLT_BLOCK_NORM_MAX_H:  # here: ctypes would cut it to 32 bits
             raise KltError(KLT_ERR_INVALID_ARG if H < 1 else KLT_ERR_UNSUPPORTED, "BlockNorm")
-        self.H = H
-        self.gamma_post, self.gamma_pre = gamma_post, gamma_pre
+        self._H, self._gamma_post, self._gamma_pre = H, gamma_post, gamma_pre
         self._device = -1
         for name, g in (("gamma_post", gamma_post), ("gamma_pre", gamma_pre)):
             if g is None:
@@ -396,6 +396,11 @@ class BlockNorm:
                                       res_scale=res_scale, branch_scale=branch_scale,
                                       gamma_post=_ptr(gamma_post), gamma_pre=_ptr(gamma_pre))
         self._address = ctypes.addressof(self._args)
+
+    # read-only: the calls read the weights at the addresses in _args
+    H = property(lambda self: self._H)
+    gamma_post = property(lambda self: self._gamma_post)
+    gamma_pre = property(lambda self: self._gamma_pre)
 
     def forward(self, h, y=None, gate=None, *, h_out=None, n=None, q=None, s=None,
                 stream: Optional[int] = None):

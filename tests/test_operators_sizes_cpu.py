@@ -19,3 +19,14 @@ def test_block_norm_of_a_width_that_no_call_takes(H):
 
 def test_block_norm_of_the_widest_rows():
     assert B.BlockNorm(B.KLT_BLOCK_NORM_MAX_H).H == B.KLT_BLOCK_NORM_MAX_H
+
+
+@pytest.mark.parametrize("name", ["H", "gamma_post", "gamma_pre"])
+def test_block_norm_keeps_what_it_was_made_with(name):
+    """A call reads the weights by the address they had at creation: other tensors are another
+    layer's, and giving them to this one must not free the ones it reads."""
+    layer = B.BlockNorm(256)
+    before = getattr(layer, name)
+    with pytest.raises(AttributeError):
+        setattr(layer, name, None)
+    assert getattr(layer, name) is before
