@@ -357,9 +357,13 @@ typedef struct klt_block_norm_args {
   const void* gamma_pre;  /* bf16 [H] or NULL                                             */
   void* h_out;            /* h' [M, H], or NULL; may be h itself with the same stride     */
   void* n;                /* bf16 [M, H], or NULL; may be y (bf16) with the same stride   */
-  uint8_t* q;             /* e4m3 codes of n [M, H], or NULL (as klt_quantize, from the
-                             unrounded n)                                                 */
-  float* s;               /* scales of q [M, ceil(H / 128)], with q                       */
+  uint8_t* q;             /* e4m3 codes of n [M, H], or NULL: n = t / rms with t = h' gamma_pre;
+                             codes e4m3(fp32(t / d)) with d = fp32(amax of t / 448) per row
+                             and 128 columns, both unrounded, so the row's 1 / rms enters
+                             the scale alone                                              */
+  float* s;               /* scales of q [M, ceil(H / 128)], with q: fp32(d / rms) (1, with
+                             codes of 0, where that is 0).  klt_quantize of the same n differs
+                             by the scale's last bit and by codes next to a tie           */
   int64_t ld_h, ld_y, gate_row, gate_col, ld_h_out, ld_n, ld_q;
 } klt_block_norm_args;
 
@@ -373,7 +377,8 @@ int klt_block_norm(const klt_block_norm_args* a, void* stream);
 
 /* A linear layer with FP8 weights, y = x W^T:  out[m, o] = sum over k of
  * (xq[m, k] xs[m, k / 128]) (wq[o, k] ws[o / 128, k / 128]); products of 128 columns are
- * summed by the tensor core in fp32, scaled and added up in fp32, and rounded once. */
+ * summed by the tensor core in fp32, multiplied by the fp32 product of their two scales (which
+ * is to stay in the normal range), added up in fp32, and rounded once. */
 enum klt_linear_act {
   KLT_ACT_NONE = 0,
   KLT_ACT_SWIGLU = 1 /* out[m, i] = silu(y[m, i]) * y[m, N/2 + i]: the gate rows of W come

@@ -534,8 +534,8 @@ KLT_DEV void quant_store(const Half& hw, const QuantParams& p, uint32_t it, uint
   store_codes(hw, p.q, row * p.ld_q, c, p.K, p.wide_q, codes8(v, s));
   if (hw.lane == 0) p.s[it] = s;
 }
-// Few groups, any strides and widths: one group of 128 columns per half warp (16 x 3584 1.4 us,
-// the hand-off between launches).
+// Few groups, any strides and widths: one group of 128 columns per half warp (16 x 3584 1.4 us in
+// a captured graph, the hand-off between launches).
 __global__ void __launch_bounds__(256) quant_kernel(QuantParams p) {
   __shared__ float bufs[16 * 128];
   pdl_trigger();
@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(256) quant_kernel(QuantParams p) {
 }
 // Eight lanes per group, U groups each, their loads in flight together.  Vectors throughout (K a
 // multiple of 128, aligned rows: 8192 x 7168 27.3 us, 6.5 TB/s), or (ANY) any strides and widths
-// (8000 x 5003 24.8 us).
+// (8000 x 5003 24.3 us: instructions, 80 % issue, for the shifts of both sides).
 template <int U, bool F32, bool ANY>
 __global__ void __launch_bounds__(256) quant_vec_kernel(QuantParams p) {
   pdl_trigger();
@@ -874,9 +874,9 @@ __global__ void __launch_bounds__(VPT == 1 ? 1024 : 512) norm_vec_kernel(NormPar
 }
 
 // Many rows: one block per row, VPT times 16 columns per thread, pairs throughout.  Of vectors
-// that start on 32 bytes (8192 x 7168 to bf16 73.6 us, 6.4 TB/s; to codes with a gate 85.7, 4.8
-// TB/s: instructions, and registers that limit an SM to three rows), or (ANY) of any start and
-// length (1021 x 2901 11.1 us).
+// that start on 32 bytes (8192 x 7168 to bf16 72 us, 6.5 TB/s; to codes with a gate 86, 4.8 TB/s,
+// with a sigmoid gate 101: occupancy, as registers limit an SM to three rows, 52 % issue), or (ANY)
+// of any start and length (1021 x 2901 11.2 us).
 template <int VPT, bool HF32, bool ANY>
 KLT_DEV void norm_many_row(const NormParams& p) {
   __shared__ float part[2][32];

@@ -108,8 +108,9 @@ void free_all(klt_linear* h) {
 }
 
 // Token tile and K split for M tokens: the fastest by a model of every form, in us.  Its
-// constants are fits to 106 sizes x 6 to 18 forms (all within 1 x 64 x 64 .. 8192 x 8192 x 8192);
-// over those and 120 more its choices take 0.6 % longer than the fastest form, 29 % at worst.
+// constants are fits to sizes within 1 x 64 x 64 .. 8192 x 8192 x 8192, 6 to 18 forms each; over 298
+// sizes, 118 of them not fitted to, its choices take 0.5 % longer than the fastest form on average,
+// 28 % at worst (a short K, many tokens and few columns).
 //   narrow kernel: the waves that its clusters need, each of a start (first: longer for wider
 //     tiles) and its k-blocks, which take longer where two CTAs share an SM;
 //   wide kernel: 1.5 + per wave of pairs its tile's end and k-blocks; two pairs that share a

@@ -14,7 +14,7 @@ constexpr int LIN_TILE_BYTES = LIN_TILE * LIN_TILE;
 
 struct LinParams {
   const uint8_t* w;   // tile-major image
-  const float* ws;    // [NB (rounded up to even), KB]
+  const float* ws;    // [NB + 1, KB], the last row zero
   const float* xs;    // [M, KB]
   void* out;          // bf16 / fp32 / e4m3
   float* out_s;       // e4m3 outputs: [M, width / 128]

@@ -14,9 +14,10 @@
 // do so from 32 columns on: with four, 128 columns took 1600 cycles per k-block, six times
 // their multiplication.
 //
-// Few tokens are bound by the multiplications' issue (93 cycles each however few the tokens)
-// and by the hand-off between launches, more by the weight stream: 1 x 7168 x 2048 4.8 us, 16 x
-// 4096 x 7168 SwiGLU to codes 7.2 us (4.1 TB/s), 128 x 7168 x 7168 16.1 us.
+// Few tokens are bound by latency: the hand-off between launches, the first copies, the joining of
+// the parts, and multiplications that take 93 cycles each however few the tokens are.  1 x 7168 x
+// 2048 4.8 us (16 of them in turn, 0.8 us), 16 x 4096 x 7168 SwiGLU to codes 7.3 us (56 in turn, 2.6
+// us; 4.0 TB/s), 128 x 7168 x 7168 16.3 us (112 of the SMs, each with the token tile of its own).
 #include "klt_linear.cuh"
 
 #include "../../include/klt.h"

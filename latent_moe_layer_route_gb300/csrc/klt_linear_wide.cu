@@ -7,10 +7,12 @@
 // rows (first CTA) with the 128 matching up rows (second CTA).
 //
 // The scales are general fp32 per 128 columns, so every k-block's product is read from TMEM
-// and added into registers times xs[m, kb] * ws[rb, kb]: that reading (128 KB per CTA and
-// k-block, two 256-column slots in turn), not the multiplication, bounds the kernel: 830 cycles
-// per k-block, where multiplications and copies alone take 734.  4096 x 7168 x 3584 in 81 us
-// (2.6 PFLOP/s), 8192 x 4096 x 7168 SwiGLU to codes in 183 to 191 us, under the power limit.
+// and added into registers times xs[m, kb] * ws[rb, kb] (128 KB per CTA and k-block, two
+// 256-column slots in turn).  Multiplications and copies alone take 734 cycles per k-block, with
+// the reading it is 830, and the end of a tile takes 2,700 (SwiGLU to codes some 5,800, 4,700 of
+// them but for the exponentials).  4096 x 7168 x 3584 in 81 us, 8192 x 4096 x 7168 SwiGLU to codes
+// in 187 us (2.6 PFLOP/s) in a burst at full clock; 87 and 200 us (2.4) in a run of seconds, which
+// the power limit holds at 1.9 GHz.
 //
 // Persistent: one pair per two SMs, tiles dealt round robin, token tiles fastest (the pairs
 // that run together share weight tiles in L2).  Where there are too few tiles for that, two
