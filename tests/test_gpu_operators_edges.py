@@ -185,7 +185,7 @@ def test_other_threads_run_while_a_launch_waits(op):
     clock.join()
     c.close()
     assert slowest > 0.2  # a call did wait
-    assert max(gaps) < 0.1
+    assert max(gaps) < slowest / 2
 
 
 # ---------------------------------------------------------------- sigmoid gates
