@@ -440,6 +440,156 @@ int klt_linear_status(klt_linear* h);
 /* Free everything the handle owns (synchronises the device first).  NULL is a no-op. */
 int klt_linear_destroy(klt_linear* h);
 
+/* ------------------------------------------------- latent attention
+ *
+ * The attention that stands in front of a latent-MoE tail in its layer.  A token's keys and
+ * values all come from one row [c | r]: c, the normed latent vector that the heads share, and r,
+ * the part that carries the position (rotated), also shared.  With the heads' up-projections
+ * W_uk, W_uv the scores are
+ *     s = scale * (q_nope . W_uk c + q_rope . r),  values W_uv c.
+ * The absorbed form reads the rows themselves from a paged cache: its queries are
+ * [W_uk^T q_nope | q_rope], its values c, and W_uv is applied to its result.  The expanded form
+ * takes every head's keys and values as their projection left them.  Conventions as for the
+ * operators above, except that rows start on 16 bytes: pointers are 16-byte aligned and strides
+ * (elements) multiples of 8 where they are of bf16 rows, of 4 where of fp32 rows. */
+enum klt_rope_pairs {
+  KLT_ROPE_HALVES = 0,    /* element i turns with i + rope / 2                             */
+  KLT_ROPE_NEIGHBOURS = 1 /* element 2 i turns with 2 i + 1                                */
+};
+typedef struct klt_latent_dims {
+  int32_t heads;  /* 1 .. 256                                                             */
+  int32_t latent; /* width of c: 128, 256, 384 or 512                                     */
+  int32_t rope;   /* width of r: 16, 32, 48 or 64                                         */
+  int32_t nope;   /* expanded form: width of a head's key beside r, 64 or 128             */
+  int32_t value;  /* expanded form: width of a head's value, 64 or 128                    */
+  int32_t page;   /* tokens per page of the cache: a power of two, 16 .. 1024             */
+  int32_t pairs;  /* enum klt_rope_pairs                                                  */
+  float eps;      /* of the norm of c                                                     */
+  float scale;    /* of the scores, finite and > 0                                        */
+} klt_latent_dims;
+
+typedef struct klt_latent klt_latent;
+
+/* Create the latent attention of one layer on the current device.  inv_freq: device fp32
+ * [rope / 2], the angle of pair i at position p is p * inv_freq[i]; gamma: device bf16 [latent], or
+ * NULL for 1.  Both are copied; the caller's buffers are not referenced after the call returns.
+ * Synchronous, on the legacy default stream, and not during a stream's capture.
+ * Errors: KLT_ERR_INVALID_ARG (null d, inv_freq or out; heads < 1; eps negative or NaN; scale not
+ * finite or <= 0), KLT_ERR_UNSUPPORTED (the other rules above; device is not compute capability
+ * 10.3), KLT_ERR_ALIGN (inv_freq or gamma not element aligned), KLT_ERR_OOM, KLT_ERR_CUDA.  On
+ * error *out is left NULL. */
+int klt_latent_create(const klt_latent_dims* d, const float* inv_freq, const void* gamma,
+                      klt_latent** out);
+
+/* Test hooks of klt_latent_attend and klt_latent_prefill (NULL or zeros = none). */
+typedef struct klt_latent_debug {
+  int32_t stall_after_tiles; /* > 0: every copy producer stops after that many tiles of keys, so
+                                the waits on its data run out (klt_latent_status)         */
+  int32_t timeout_ms;        /* bound of every on-device wait (0 = 1000 ms)               */
+} klt_latent_debug;
+
+/* New tokens' rows, normed and rotated, into the cache, and the queries' position parts rotated:
+ *     n = c / sqrt(mean(c^2) + eps) * gamma,   r' and q' turned by position * inv_freq,
+ * in fp32 (angles in fp64: right for any position up to 2^31), each output rounded once. */
+typedef struct klt_latent_append_args {
+  int32_t T;                /* tokens                                                      */
+  int32_t kv_dtype;         /* KLT_DT_BF16 or KLT_DT_F32                                   */
+  const void* kv;           /* [T, latent + rope]: c and r before norm and rotation        */
+  const int64_t* positions; /* [T]                                                         */
+  const int64_t* slots;     /* [T] page * tokens per page + row; tokens whose slot lies outside the
+                               cache (-1, say) are not stored.  No slot twice in one call   */
+  void* cache;              /* bf16 [pages, page, latent + rope], or NULL (then no slots)  */
+  void* kv_out;             /* bf16 [T, latent + rope]: the same rows, or NULL             */
+  const void* q;            /* bf16 [T, heads, rope], or NULL                              */
+  void* q_out;              /* bf16 [T, heads, rope], with q; may be q with its strides    */
+  int64_t pages;
+  int64_t ld_kv, page_stride, row_stride, ld_kv_out;
+  int64_t q_token, q_head, q_out_token, q_out_head; /* strides                             */
+} klt_latent_append_args;
+
+/* Run klt_latent_append_args on `stream`; one launch.  T == 0 launches nothing.  Outputs overlap
+ * neither each other nor the inputs except as above.
+ * Errors: KLT_ERR_INVALID_ARG (null handle, args, kv or positions; T < 0; no output at all; cache
+ * without slots or slots without cache; q without q_out or q_out without q; pages < 0; negative
+ * stride; output rows that overlap; another device current than at creation),
+ * KLT_ERR_UNSUPPORTED (unknown dtype, more than 2^31 - 1 slots), KLT_ERR_ALIGN, KLT_ERR_CUDA. */
+int klt_latent_append(klt_latent* h, const klt_latent_append_args* a, void* stream);
+
+/* Attention in absorbed form over a paged cache.  Sequence b has seq_lens[b] tokens in the cache,
+ * token j in row j % page of page block_table[b, j / page]; its queries are the tokens cu_q[b] ..
+ * cu_q[b + 1] - 1 of q, the last tokens of the sequence in order: the last query sees all tokens,
+ * the one before it all but one, and so on.
+ *     out = softmax(scale * q . rows) c,   lse = log(sum(exp(scale * q . rows)))
+ * A query that sees no token gets zeros and a lse of minus infinity.  Rows of out and lse outside
+ * of the sequences' ranges stay as they are.  What lies in a page behind the sequence's last token
+ * does not matter, whatever it is; a row of the sequence that is not finite spreads to all of the
+ * sequence's queries.  Lengths beyond max_pages * page are cut to it, negative ones to 0; ranges
+ * of queries are cut to 0 .. T; pages outside of the cache read as rows of zeros. */
+typedef struct klt_latent_attend_args {
+  int32_t B, T;               /* sequences; queries in all                                 */
+  int32_t max_pages;          /* columns of block_table                                    */
+  const void* q;              /* bf16 [T, heads, latent + rope]                            */
+  const void* cache;          /* bf16 [pages, page, latent + rope]                         */
+  const int32_t* block_table; /* [B, max_pages]                                            */
+  const int32_t* seq_lens;    /* [B]                                                       */
+  const int32_t* cu_q;        /* [B + 1] ascending from 0, or NULL: one query a sequence (T = B) */
+  void* out;                  /* bf16 [T, heads, latent]                                   */
+  float* lse;                 /* [T, heads] contiguous, or NULL                            */
+  void* workspace;            /* klt_latent_workspace bytes, 16-byte aligned; calls that may
+                                 overlap need one each                                     */
+  uint64_t workspace_bytes;
+  int64_t pages;
+  int64_t q_token, q_head, page_stride, row_stride, ld_table, out_token, out_head;
+} klt_latent_attend_args;
+
+/* Bytes of workspace that klt_latent_attend needs on this device for B sequences and T queries,
+ * whatever their lengths. */
+int klt_latent_workspace(const klt_latent* h, int32_t B, int32_t T, uint64_t* bytes);
+
+/* Run klt_latent_attend_args on `stream`.  T == 0 launches nothing.
+ * Errors: KLT_ERR_INVALID_ARG (null handle, args or pointer; B < 1 or T < 0; T != B without cu_q;
+ * max_pages or pages < 0; workspace too small; negative stride or table stride shorter than a
+ * row; cache or output rows that overlap; bad debug value; another device current than at
+ * creation), KLT_ERR_UNSUPPORTED (more than 2^31 - 1 slots of the cache, tokens of a table's row,
+ * or query rows; a stride of 2^38 or more), KLT_ERR_ALIGN, KLT_ERR_CUDA.  Expired device waits:
+ * klt_latent_status. */
+int klt_latent_attend(klt_latent* h, const klt_latent_attend_args* a, const klt_latent_debug* dbg,
+                      void* stream);
+
+/* Attention in expanded form over packed sequences: sequence b has the queries cu_q[b] ..
+ * cu_q[b + 1] - 1 and the keys cu_k[b] .. cu_k[b + 1] - 1;
+ *     s = scale * (q[:nope] . k + q[nope:] . k_rope),  out = softmax(s) v
+ * With `causal` the queries are the last tokens of the keys, as for klt_latent_attend.  Queries
+ * that see no key, rows outside of the ranges, and values that are not finite are treated as
+ * there; ranges are cut to 0 .. T and 0 .. S. */
+typedef struct klt_latent_prefill_args {
+  int32_t B, T, S;     /* sequences; queries; keys                                         */
+  int32_t causal;
+  const void* q;       /* bf16 [T, heads, nope + rope]                                     */
+  const void* k;       /* bf16 [S, heads, nope]                                            */
+  const void* v;       /* bf16 [S, heads, value]                                           */
+  const void* k_rope;  /* bf16 [S, rope]                                                   */
+  const int32_t* cu_q; /* [B + 1], ascending from 0                                        */
+  const int32_t* cu_k; /* [B + 1], ascending from 0                                        */
+  void* out;           /* bf16 [T, heads, value]                                           */
+  float* lse;          /* [T, heads] contiguous, or NULL                                   */
+  int64_t q_token, q_head, k_token, k_head, v_token, v_head, ld_k_rope, out_token, out_head;
+} klt_latent_prefill_args;
+
+/* Run klt_latent_prefill_args on `stream`; one launch.  T == 0 launches nothing.
+ * Errors: as klt_latent_attend; KLT_ERR_INVALID_ARG also for a stride of 0 of an input with more
+ * than one row in that direction; KLT_ERR_UNSUPPORTED (T * heads above 2^31 - 1, more query tiles
+ * than a grid takes, a stride of 2^38 or more). */
+int klt_latent_prefill(klt_latent* h, const klt_latent_prefill_args* a,
+                       const klt_latent_debug* dbg, void* stream);
+
+/* Sticky device status, as klt_status: KLT_OK or KLT_ERR_DEVICE_TIMEOUT, read synchronously; call
+ * it after the calls' streams have been synchronised. */
+int klt_latent_status(klt_latent* h);
+
+/* Free everything the handle owns (synchronises the device first).  NULL is a no-op. */
+int klt_latent_destroy(klt_latent* h);
+
 #ifdef __cplusplus
 }
 #endif

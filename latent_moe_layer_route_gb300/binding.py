@@ -35,11 +35,15 @@ KLT_DT_E4M3 = 2
 KLT_ACT_NONE = 0
 KLT_ACT_SWIGLU = 1
 KLT_BLOCK_NORM_MAX_H = 16384
+KLT_ROPE_HALVES = 0
+KLT_ROPE_NEIGHBOURS = 1
 
 EXPORTS = ("klt_create", "klt_forward", "klt_forward_hidden", "klt_status", "klt_destroy",
            "klt_strerror", "klt_launch_count", "klt_gemm_tile", "klt_route_noalloc",
            "klt_quantize", "klt_block_norm", "klt_linear_create", "klt_linear_forward",
-           "klt_linear_tile", "klt_linear_status", "klt_linear_destroy")
+           "klt_linear_tile", "klt_linear_status", "klt_linear_destroy", "klt_latent_create",
+           "klt_latent_append", "klt_latent_workspace", "klt_latent_attend",
+           "klt_latent_prefill", "klt_latent_status", "klt_latent_destroy")
 
 
 class KltDims(ctypes.Structure):
@@ -89,6 +93,40 @@ class KltLinearDims(ctypes.Structure):
 class KltLinearDebug(ctypes.Structure):
     _fields_ = [("stall_after_kblocks", ctypes.c_int32), ("timeout_ms", ctypes.c_int32),
                 ("force_tile", ctypes.c_int32), ("force_split", ctypes.c_int32)]
+
+
+class KltLatentDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("heads", "latent", "rope", "nope", "value", "page",
+                                              "pairs")] + [
+        ("eps", ctypes.c_float), ("scale", ctypes.c_float)]
+
+
+class KltLatentDebug(ctypes.Structure):
+    _fields_ = [("stall_after_tiles", ctypes.c_int32), ("timeout_ms", ctypes.c_int32)]
+
+
+class KltLatentAppendArgs(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("kv_dtype", ctypes.c_int32)] + [
+        (n, ctypes.c_void_p) for n in ("kv", "positions", "slots", "cache", "kv_out", "q",
+                                       "q_out")] + [
+        (n, ctypes.c_int64) for n in ("pages", "ld_kv", "page_stride", "row_stride", "ld_kv_out",
+                                      "q_token", "q_head", "q_out_token", "q_out_head")]
+
+
+class KltLatentAttendArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "T", "max_pages")] + [
+        (n, ctypes.c_void_p) for n in ("q", "cache", "block_table", "seq_lens", "cu_q", "out",
+                                       "lse", "workspace")] + [
+        ("workspace_bytes", ctypes.c_uint64)] + [
+        (n, ctypes.c_int64) for n in ("pages", "q_token", "q_head", "page_stride", "row_stride",
+                                      "ld_table", "out_token", "out_head")]
+
+
+class KltLatentPrefillArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "T", "S", "causal")] + [
+        (n, ctypes.c_void_p) for n in ("q", "k", "v", "k_rope", "cu_q", "cu_k", "out", "lse")] + [
+        (n, ctypes.c_int64) for n in ("q_token", "q_head", "k_token", "k_head", "v_token",
+                                      "v_head", "ld_k_rope", "out_token", "out_head")]
 
 
 _LIB: Optional[ctypes.CDLL] = None
@@ -153,6 +191,17 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.klt_linear_status.restype = ctypes.c_int
     lib.klt_linear_destroy.argtypes = [vp]
     lib.klt_linear_destroy.restype = ctypes.c_int
+    P = ctypes.POINTER
+    lib.klt_latent_create.argtypes = [P(KltLatentDims), vp, vp, P(vp)]
+    lib.klt_latent_append.argtypes = [vp, P(KltLatentAppendArgs), vp]
+    lib.klt_latent_workspace.argtypes = [vp, i32, i32, P(ctypes.c_uint64)]
+    lib.klt_latent_attend.argtypes = [vp, P(KltLatentAttendArgs), P(KltLatentDebug), vp]
+    lib.klt_latent_prefill.argtypes = [vp, P(KltLatentPrefillArgs), P(KltLatentDebug), vp]
+    lib.klt_latent_status.argtypes = [vp]
+    lib.klt_latent_destroy.argtypes = [vp]
+    for name in EXPORTS:
+        if name.startswith("klt_latent_"):
+            getattr(lib, name).restype = ctypes.c_int
     _LIB, _LIB_FILE = lib, os.path.realpath(path)
     return lib
 
@@ -501,6 +550,157 @@ class Fp8Linear:
     def close(self):
         if self.handle is not None and self.handle.value:
             self._lib.klt_linear_destroy(self.handle)
+        self.handle, self._address = None, 0
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class LatentAttention:
+    """Latent attention of one layer (klt_latent_*): the step that fills the paged cache of latent
+    rows, attention over it in absorbed form, and attention in expanded form.  Owns a handle with
+    its own copy of inv_freq and gamma, on inv_freq's device.  Threads may share it, but close()
+    must not overlap a call.
+
+    inv_freq: fp32 [rope / 2], the angle of pair i at position p is p * inv_freq[i]; gamma: bf16
+    [latent] or None; scale: of the scores, None for 1 / sqrt(nope + rope); pairs "halves" (element
+    i turns with i + rope / 2) or "neighbours" (2 i with 2 i + 1).  A cache is bf16
+    [pages, page, latent + rope]."""
+
+    def __init__(self, heads: int, latent: int = 512, rope: int = 64, nope: int = 128,
+                 value: int = 128, page: int = 64, *, inv_freq, gamma=None,
+                 scale: Optional[float] = None, eps: float = 1e-6, pairs: str = "halves"):
+        import torch
+        self.handle = None
+        if _marshal is None:
+            _load_marshal()
+        self._lib = _LIB
+        kinds = {"halves": KLT_ROPE_HALVES, "neighbours": KLT_ROPE_NEIGHBOURS}
+        if pairs not in kinds:
+            raise ValueError(f"pairs {pairs!r}: not known")
+        sizes = (heads, latent, rope, nope, value, page)
+        if not all(0 <= v <= 0x7FFFFFFF for v in sizes):  # ctypes would cut it to 32 bits
+            raise KltError(KLT_ERR_INVALID_ARG, "klt_latent_create")
+        for name, t, n, dtype in (("inv_freq", inv_freq, rope // 2, torch.float32),
+                                  ("gamma", gamma, latent, torch.bfloat16)):
+            if t is None and name == "gamma":
+                continue
+            if t.dtype != dtype or tuple(t.shape) != (n,) or not t.is_cuda or \
+                    not t.is_contiguous():
+                raise ValueError(f"{name}: not a contiguous CUDA vector of {n}, {dtype}")
+        self.device = inv_freq.get_device()
+        if gamma is not None and gamma.get_device() != self.device:
+            raise ValueError("inv_freq and gamma are on different devices")
+        if scale is None:
+            scale = max(nope + rope, 1) ** -0.5
+        self.dims = KltLatentDims(*sizes, kinds[pairs], eps, scale)
+        h = ctypes.c_void_p()
+        # the create copies on the legacy default stream; what wrote the vectors may have run on
+        # another
+        torch.cuda.current_stream(self.device).synchronize()
+        with torch.cuda.device(self.device):
+            rc = self._lib.klt_latent_create(ctypes.byref(self.dims), _ptr(inv_freq), _ptr(gamma),
+                                             ctypes.byref(h))
+        if rc != KLT_OK:
+            raise KltError(rc, "klt_latent_create")
+        self.handle = h
+        self._address, self._dims = h.value, ctypes.addressof(self.dims)
+
+    def append(self, kv, positions, slots=None, cache=None, *, kv_out=None, q=None, q_out=None,
+               stream: Optional[int] = None):
+        """Rows kv [T, latent + rope] (bf16 or fp32) of tokens at `positions` (int64 [T]), normed
+        and rotated, into `slots` (int64 [T]; outside of the cache: not stored) of the cache
+        and/or into kv_out (bf16 [T, latent + rope]); q [T, heads, rope] (bf16) rotated into q_out
+        (may be q).  Allocates q_out when q is given without it, and kv_out when there is no cache.
+        Returns (kv_out, q_out)."""
+        if (kv_out is None and cache is None) or (q is not None and q_out is None):
+            import torch
+            with _memory_of(stream, kv):
+                if kv_out is None and cache is None:
+                    kv_out = torch.empty(kv.shape, dtype=torch.bfloat16, device=kv.device)
+                if q is not None and q_out is None:
+                    q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        rc = _marshal.latent_append(self._address, self._dims, self.device, kv, positions, slots,
+                                    cache, kv_out, q, q_out, stream)
+        if rc:
+            raise KltError(rc, "klt_latent_append")
+        return kv_out, q_out
+
+    def workspace(self, B: int, T: Optional[int] = None):
+        """A workspace for attend() calls of B sequences and T queries (None: B), uint8.  Calls
+        that may overlap need one each, and so do two captured graphs that may run at once."""
+        import torch
+        n = self._workspace_bytes(B, B if T is None else T)
+        return torch.empty(n, dtype=torch.uint8, device=f"cuda:{self.device}")
+
+    def _workspace_bytes(self, B: int, T: int) -> int:
+        n = ctypes.c_uint64()
+        if not (0 <= B <= 0x7FFFFFFF and 0 <= T <= 0x7FFFFFFF):
+            raise KltError(KLT_ERR_INVALID_ARG, "klt_latent_workspace")
+        rc = self._lib.klt_latent_workspace(self.handle, B, T, ctypes.byref(n))
+        if rc:
+            raise KltError(rc, "klt_latent_workspace")
+        return n.value
+
+    def attend(self, q, cache, block_table, seq_lens, cu_q=None, *, out=None, lse=None,
+               workspace=None, stream: Optional[int] = None,
+               debug: Optional[KltLatentDebug] = None):
+        """q bf16 [T, heads, latent + rope] over the cache; block_table int32 [B, max_pages],
+        seq_lens int32 [B] (the queries' own tokens counted), cu_q int32 [B + 1] or None for one
+        query a sequence.  Returns out bf16 [T, heads, latent] and lse fp32 [T, heads]; what is
+        allocated here is zeros and minus infinity outside of cu_q's ranges."""
+        if out is None or lse is None or workspace is None:
+            import torch
+            T = q.shape[0]
+            with _memory_of(stream, q):
+                shape = (T, self.dims.heads, self.dims.latent)
+                if out is None:
+                    out = torch.empty(shape, dtype=torch.bfloat16, device=q.device) \
+                        if cu_q is None else \
+                        torch.zeros(shape, dtype=torch.bfloat16, device=q.device)
+                if lse is None:
+                    lse = torch.empty(shape[:2], device=q.device) if cu_q is None else \
+                        torch.full(shape[:2], -float("inf"), device=q.device)
+                if workspace is None:
+                    workspace = torch.empty(self._workspace_bytes(seq_lens.shape[0], T),
+                                            dtype=torch.uint8, device=q.device)
+        rc = _marshal.latent_attend(self._address, self._dims, self.device, q, cache, block_table,
+                                    seq_lens, cu_q, out, lse, workspace,
+                                    0 if debug is None else ctypes.addressof(debug), stream)
+        if rc:
+            raise KltError(rc, "klt_latent_attend")
+        return out, lse
+
+    def prefill(self, q, k, v, k_rope, cu_q, cu_k, *, causal: bool = True, out=None, lse=None,
+                stream: Optional[int] = None, debug: Optional[KltLatentDebug] = None):
+        """q bf16 [T, heads, nope + rope], k bf16 [S, heads, nope], v bf16 [S, heads, value], k_rope
+        bf16 [S, rope], cu_q and cu_k int32 [B + 1].  Returns out bf16 [T, heads, value] and lse
+        fp32 [T, heads]; what is allocated here is zeros and minus infinity outside of cu_q's
+        ranges."""
+        if out is None or lse is None:
+            import torch
+            shape = (q.shape[0], self.dims.heads, self.dims.value)
+            with _memory_of(stream, q):
+                if out is None:
+                    out = torch.zeros(shape, dtype=torch.bfloat16, device=q.device)
+                if lse is None:
+                    lse = torch.full(shape[:2], -float("inf"), device=q.device)
+        rc = _marshal.latent_prefill(self._address, self._dims, self.device, q, k, v, k_rope, cu_q,
+                                     cu_k, bool(causal), out, lse,
+                                     0 if debug is None else ctypes.addressof(debug), stream)
+        if rc:
+            raise KltError(rc, "klt_latent_prefill")
+        return out, lse
+
+    def status(self) -> int:
+        return self._lib.klt_latent_status(self.handle)
+
+    def close(self):
+        if self.handle is not None and self.handle.value:
+            self._lib.klt_latent_destroy(self.handle)
         self.handle, self._address = None, 0
 
     def __del__(self):

@@ -26,8 +26,9 @@ LIB_PATH = os.path.join(PKG_DIR, "libklt.so")
 EXT_SUFFIX = sysconfig.get_config_var("EXT_SUFFIX")  # names the interpreter and the machine
 MARSHAL_PATH = os.path.join(PKG_DIR, "_marshal" + EXT_SUFFIX)
 SOURCES = ["klt_api.cu", "klt_route.cu", "klt_gemm.cu", "klt_wide.cu", "klt_noalloc.cu",
-           "klt_block.cu", "klt_linear.cu", "klt_linear_narrow.cu", "klt_linear_wide.cu"]
-HEADERS = ["klt_device.cuh", "klt_internal.h", "klt_linear.cuh"]
+           "klt_block.cu", "klt_linear.cu", "klt_linear_narrow.cu", "klt_linear_wide.cu",
+           "klt_latent.cu", "klt_latent_attend.cu", "klt_latent_prefill.cu"]
+HEADERS = ["klt_device.cuh", "klt_internal.h", "klt_linear.cuh", "klt_latent.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr", "-I" + os.path.join(ROOT, "include")]

@@ -1,0 +1,138 @@
+// Shared parts of latent attention: the parameters of its kernels, and the tensor-core
+// descriptors and TMEM accesses that only they use.
+#pragma once
+
+#include "klt_linear.cuh"
+
+namespace klt {
+
+struct AttendParams {
+  const __nv_bfloat16* q;
+  const int* table;
+  const int* lens;
+  const int* cu_q;       // or null: one query a sequence
+  __nv_bfloat16* out;
+  float* lse;
+  float* part;           // workspace
+  int64_t q_token, q_head, ld_table, out_token, out_head;
+  int B, T, H;
+  int R, rope;           // latent, position part
+  int page_log2, max_pages, pages;
+  float scale;           // of the scores, times log2(e)
+  int stall;             // test hook: copies stop after this many tiles (0 = never)
+  int* err;
+  long long timeout;     // SM cycles
+};
+
+struct PrefillParams {
+  const int* cu_q;
+  const int* cu_k;
+  __nv_bfloat16* out;
+  float* lse;
+  int64_t out_token, out_head;
+  int B, T, S, H;
+  int nope, rope, value;
+  int causal;
+  float scale;           // as above
+  int stall;
+  int* err;
+  long long timeout;
+};
+
+// The range cu[b] .. cu[b + 1] cut to 0 .. n (whatever cu holds).
+KLT_DEV void range_of(const int* cu, int b, int n, int& lo, int& hi) {
+  lo = min(max(cu[b], 0), n);
+  hi = min(max(cu[b + 1], lo), n);
+}
+
+// ------------------------------------------------------------------ tcgen05
+// Shared-memory descriptor of an operand whose rows (its M or N direction) are contiguous: boxes
+// of 64 columns x k rows of 128 bytes in the 128-byte swizzle, 8 rows (1024 bytes) to an atom,
+// boxes `box_bytes` apart.  Its instruction descriptor has the operand's transpose bit set.
+KLT_DEV uint64_t sdesc_sw128_mn(uint32_t saddr, uint32_t box_bytes) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) |
+         (static_cast<uint64_t>(box_bytes >> 4) << 16) |
+         (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
+         (static_cast<uint64_t>(2) << 61);
+}
+constexpr uint32_t IDESC_A_MN = 1u << 15, IDESC_B_MN = 1u << 16;
+
+// D (+)= A B^T with A in TMEM: bf16, two to a column, K = 16 in eight columns.
+KLT_DEV void mma_bf16_ta(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc,
+                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// 3-D tiled load of the box at (c0 = inner element, c1, c2).
+KLT_DEV void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1,
+                         int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
+// 64 columns of the 64 rows of an M = 64 accumulator: warp w of a warpgroup holds rows 16 w ..
+// 16 w + 15 in its first 16 lanes.  Register 4 g + 2 i + j is row lane / 4 + 8 i, column
+// 8 g + 2 (lane % 4) + j.
+KLT_DEV void tmem_ld_rows16(uint32_t taddr, float* v) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+        "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+KLT_DEV void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+// 2^x by the hardware approximation (2 ulp; subnormal results flushed, far below what a sum of
+// weights of at least one holds).
+KLT_DEV float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+KLT_DEV uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&t);
+}
+
+// ------------------------------------------------------------------ launches
+uint64_t attend_workspace(int num_sms);
+cudaError_t launch_attend(const CUtensorMap& cache, const AttendParams& p, int num_sms,
+                          cudaStream_t s);
+cudaError_t launch_prefill(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                           const CUtensorMap& k_rope, const PrefillParams& p, unsigned tiles,
+                           cudaStream_t s);
+constexpr int PREFILL_ROWS = 128;  // queries of a tile
+// Once per device, before the first launch; false when a kernel is not what its launch expects.
+bool prepare_attend();
+bool prepare_prefill();
+
+}  // namespace klt

@@ -250,6 +250,214 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// A tensor of latent attention: its type, device and sizes are checked (a size < 0: any, which it
+// sets), its last direction is contiguous; the strides of the others.
+struct Strided {
+  void* ptr = nullptr;
+  int64_t size[3] = {1, 1, 1};
+  int64_t stride[3] = {};
+};
+bool read_nd(PyObject* o, const char* name, at::ScalarType type, at::ScalarType other,
+             long long device, int dims, const int64_t* want, Strided* v, bool whole = false) {
+  if (!THPVariable_Check(o)) {
+    PyErr_Format(PyExc_TypeError, "%s: not a tensor", name);
+    return false;
+  }
+  const at::Tensor& t = THPVariable_Unpack(o);
+  if (t.scalar_type() != type && t.scalar_type() != other) {
+    PyErr_Format(PyExc_TypeError, "%s: dtype %s is not taken here", name,
+                 c10::toString(t.scalar_type()));
+    return false;
+  }
+  if (!t.is_cuda() || t.layout() != at::kStrided) {
+    PyErr_Format(PyExc_ValueError, "%s: not a CUDA tensor with strides", name);
+    return false;
+  }
+  if (t.get_device() != device) {
+    PyErr_Format(PyExc_ValueError, "%s: on CUDA device %lld, not %lld", name,
+                 static_cast<long long>(t.get_device()), device);
+    return false;
+  }
+  if (t.dim() != dims) {
+    PyErr_Format(PyExc_ValueError, "%s: %lld dimensions, not %d", name,
+                 static_cast<long long>(t.dim()), dims);
+    return false;
+  }
+  for (int i = 0; i < dims; ++i) {
+    v->size[i] = t.size(i);
+    v->stride[i] = t.stride(i);
+    if ((want[i] >= 0 && v->size[i] != want[i]) || v->size[i] > INT32_MAX) {
+      PyErr_Format(PyExc_ValueError, "%s: size %lld in dimension %d, not %lld", name,
+                   static_cast<long long>(v->size[i]), i,
+                   static_cast<long long>(want[i] >= 0 ? want[i] : INT32_MAX));
+      return false;
+    }
+  }
+  if ((v->stride[dims - 1] != 1 && v->size[dims - 1] > 1) || (whole && !t.is_contiguous())) {
+    PyErr_Format(PyExc_ValueError, "%s: not contiguous", name);
+    return false;
+  }
+  v->ptr = t.data_ptr();
+  return true;
+}
+bool read_nd(PyObject* o, const char* name, at::ScalarType type, long long device, int dims,
+             const int64_t (&want)[3], Strided* v, bool whole = false) {
+  return read_nd(o, name, type, type, device, dims, want, v, whole);
+}
+struct Latent {
+  klt_latent* h;
+  const klt_latent_dims* d;
+  long long dev;
+};
+bool read_latent(PyObject* const* a, Latent* l) {
+  l->h = static_cast<klt_latent*>(PyLong_AsVoidPtr(a[0]));
+  l->d = static_cast<const klt_latent_dims*>(PyLong_AsVoidPtr(a[1]));
+  return !PyErr_Occurred() && as_int(a[2], &l->dev);
+}
+
+// latent_append(handle, address of its klt_latent_dims, device, kv, positions, slots, cache, kv_out,
+// q, q_out, stream) -> status; slots to q_out may be None
+PyObject* latent_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  Latent l;
+  if (!arity(n, 11) || !read_latent(a, &l)) return nullptr;
+  const int64_t width = l.d->latent + l.d->rope, H = l.d->heads;
+  klt_latent_append_args p = {};
+  Strided t;
+  const int64_t kv_size[2] = {-1, width};
+  if (!read_nd(a[3], "kv", at::kBFloat16, at::kFloat, l.dev, 2, kv_size, &t))
+    return nullptr;
+  const int64_t T = t.size[0];
+  p.T = static_cast<int32_t>(T);
+  p.kv = t.ptr;
+  p.ld_kv = t.stride[0];
+  p.kv_dtype =
+      THPVariable_Unpack(a[3]).scalar_type() == at::kFloat ? KLT_DT_F32 : KLT_DT_BF16;
+  if (T <= 1) p.ld_kv = 0;  // the stride of a single row says nothing
+  if (!read_nd(a[4], "positions", at::kLong, l.dev, 1, {T}, &t, true)) return nullptr;
+  p.positions = static_cast<const int64_t*>(t.ptr);
+  if (a[5] != Py_None) {
+    if (!read_nd(a[5], "slots", at::kLong, l.dev, 1, {T}, &t, true)) return nullptr;
+    p.slots = static_cast<const int64_t*>(t.ptr);
+  }
+  if (a[6] != Py_None) {
+    if (!read_nd(a[6], "cache", at::kBFloat16, l.dev, 3, {-1, l.d->page, width}, &t))
+      return nullptr;
+    p.cache = t.ptr;
+    p.pages = t.size[0];
+    p.page_stride = p.pages > 1 ? t.stride[0] : 0;
+    p.row_stride = t.stride[1];
+  }
+  if (a[7] != Py_None) {
+    if (!read_nd(a[7], "kv_out", at::kBFloat16, l.dev, 2, {T, width}, &t)) return nullptr;
+    p.kv_out = t.ptr;
+    p.ld_kv_out = T > 1 ? t.stride[0] : 0;
+  }
+  if (a[8] != Py_None) {
+    if (!read_nd(a[8], "q", at::kBFloat16, l.dev, 3, {T, H, l.d->rope}, &t)) return nullptr;
+    p.q = t.ptr;
+    p.q_token = T > 1 ? t.stride[0] : 0;
+    p.q_head = H > 1 ? t.stride[1] : 0;
+  }
+  if (a[9] != Py_None) {
+    if (!read_nd(a[9], "q_out", at::kBFloat16, l.dev, 3, {T, H, l.d->rope}, &t)) return nullptr;
+    p.q_out = t.ptr;
+    p.q_out_token = T > 1 ? t.stride[0] : 0;
+    p.q_out_head = H > 1 ? t.stride[1] : 0;
+  }
+  return launch(l.dev, a[10], [&](void* s) { return klt_latent_append(l.h, &p, s); });
+}
+
+// latent_attend(handle, dims, device, q, cache, block_table, seq_lens, cu_q or None, out, lse,
+// workspace, address of a klt_latent_debug or 0, stream) -> status
+PyObject* latent_attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  Latent l;
+  if (!arity(n, 13) || !read_latent(a, &l)) return nullptr;
+  const int64_t width = l.d->latent + l.d->rope, H = l.d->heads;
+  const auto* dbg = static_cast<const klt_latent_debug*>(PyLong_AsVoidPtr(a[11]));
+  if (PyErr_Occurred()) return nullptr;
+  klt_latent_attend_args p = {};
+  Strided t;
+  if (!read_nd(a[3], "q", at::kBFloat16, l.dev, 3, {-1, H, width}, &t)) return nullptr;
+  const int64_t T = t.size[0];
+  p.T = static_cast<int32_t>(T);
+  p.q = t.ptr;
+  p.q_token = T > 1 ? t.stride[0] : 0;
+  p.q_head = H > 1 ? t.stride[1] : 0;
+  if (!read_nd(a[4], "cache", at::kBFloat16, l.dev, 3, {-1, l.d->page, width}, &t)) return nullptr;
+  p.cache = t.ptr;
+  p.pages = t.size[0];
+  p.page_stride = p.pages > 1 ? t.stride[0] : 0;
+  p.row_stride = t.stride[1];
+  if (!read_nd(a[5], "block_table", at::kInt, l.dev, 2, {-1, -1}, &t)) return nullptr;
+  const int64_t B = t.size[0];
+  p.B = static_cast<int32_t>(B);
+  p.max_pages = static_cast<int32_t>(t.size[1]);
+  p.block_table = static_cast<const int32_t*>(t.ptr);
+  p.ld_table = B > 1 ? t.stride[0] : 0;
+  if (!read_nd(a[6], "seq_lens", at::kInt, l.dev, 1, {B}, &t, true)) return nullptr;
+  p.seq_lens = static_cast<const int32_t*>(t.ptr);
+  if (a[7] != Py_None) {
+    if (!read_nd(a[7], "cu_q", at::kInt, l.dev, 1, {B + 1}, &t, true)) return nullptr;
+    p.cu_q = static_cast<const int32_t*>(t.ptr);
+  }
+  if (!read_nd(a[8], "out", at::kBFloat16, l.dev, 3, {T, H, l.d->latent}, &t)) return nullptr;
+  p.out = t.ptr;
+  p.out_token = T > 1 ? t.stride[0] : 0;
+  p.out_head = H > 1 ? t.stride[1] : 0;
+  if (!read_nd(a[9], "lse", at::kFloat, l.dev, 2, {T, H}, &t, true)) return nullptr;
+  p.lse = static_cast<float*>(t.ptr);
+  if (!read_nd(a[10], "workspace", at::kByte, l.dev, 1, {-1}, &t, true)) return nullptr;
+  p.workspace = t.ptr;
+  p.workspace_bytes = static_cast<uint64_t>(t.size[0]);
+  return launch(l.dev, a[12], [&](void* s) { return klt_latent_attend(l.h, &p, dbg, s); });
+}
+
+// latent_prefill(handle, dims, device, q, k, v, k_rope, cu_q, cu_k, causal, out, lse, address of a
+// klt_latent_debug or 0, stream) -> status
+PyObject* latent_prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  Latent l;
+  if (!arity(n, 14) || !read_latent(a, &l)) return nullptr;
+  const int64_t H = l.d->heads;
+  const auto* dbg = static_cast<const klt_latent_debug*>(PyLong_AsVoidPtr(a[12]));
+  if (PyErr_Occurred()) return nullptr;
+  klt_latent_prefill_args p = {};
+  Strided t;
+  if (!read_nd(a[3], "q", at::kBFloat16, l.dev, 3, {-1, H, l.d->nope + l.d->rope}, &t))
+    return nullptr;
+  const int64_t T = t.size[0];
+  p.T = static_cast<int32_t>(T);
+  p.q = t.ptr;
+  p.q_token = T > 1 ? t.stride[0] : 0;
+  p.q_head = H > 1 ? t.stride[1] : 0;
+  if (!read_nd(a[4], "k", at::kBFloat16, l.dev, 3, {-1, H, l.d->nope}, &t)) return nullptr;
+  const int64_t S = t.size[0];
+  p.S = static_cast<int32_t>(S);
+  p.k = t.ptr;
+  p.k_token = S > 1 ? t.stride[0] : 0;
+  p.k_head = H > 1 ? t.stride[1] : 0;
+  if (!read_nd(a[5], "v", at::kBFloat16, l.dev, 3, {S, H, l.d->value}, &t)) return nullptr;
+  p.v = t.ptr;
+  p.v_token = S > 1 ? t.stride[0] : 0;
+  p.v_head = H > 1 ? t.stride[1] : 0;
+  if (!read_nd(a[6], "k_rope", at::kBFloat16, l.dev, 2, {S, l.d->rope}, &t)) return nullptr;
+  p.k_rope = t.ptr;
+  p.ld_k_rope = S > 1 ? t.stride[0] : 0;
+  if (!read_nd(a[7], "cu_q", at::kInt, l.dev, 1, {-1}, &t, true)) return nullptr;
+  const int64_t starts = t.size[0];
+  p.cu_q = static_cast<const int32_t*>(t.ptr);
+  p.B = static_cast<int32_t>(starts - 1);
+  if (!read_nd(a[8], "cu_k", at::kInt, l.dev, 1, {starts}, &t, true)) return nullptr;
+  p.cu_k = static_cast<const int32_t*>(t.ptr);
+  p.causal = PyObject_IsTrue(a[9]);
+  if (!read_nd(a[10], "out", at::kBFloat16, l.dev, 3, {T, H, l.d->value}, &t)) return nullptr;
+  p.out = t.ptr;
+  p.out_token = T > 1 ? t.stride[0] : 0;
+  p.out_head = H > 1 ? t.stride[1] : 0;
+  if (!read_nd(a[11], "lse", at::kFloat, l.dev, 2, {T, H}, &t, true)) return nullptr;
+  p.lse = static_cast<float*>(t.ptr);
+  return launch(l.dev, a[13], [&](void* s) { return klt_latent_prefill(l.h, &p, dbg, s); });
+}
+
 // An entry point from which no C++ exception leaves (a tensor without memory throws one).
 template <PyObject* (*FN)(PyObject*, PyObject* const*, Py_ssize_t)>
 PyObject* guarded(PyObject* self, PyObject* const* a, Py_ssize_t n) {
@@ -267,6 +475,9 @@ PyCFunction entry() {
 PyMethodDef methods[] = {{"quantize", entry<quantize>(), METH_FASTCALL, nullptr},
                          {"block_norm", entry<block_norm>(), METH_FASTCALL, nullptr},
                          {"linear", entry<linear>(), METH_FASTCALL, nullptr},
+                         {"latent_append", entry<latent_append>(), METH_FASTCALL, nullptr},
+                         {"latent_attend", entry<latent_attend>(), METH_FASTCALL, nullptr},
+                         {"latent_prefill", entry<latent_prefill>(), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods,
                       nullptr,               nullptr,    nullptr, nullptr};
