@@ -357,7 +357,7 @@ int klt_latent_append(klt_latent* h, const klt_latent_append_args* a, void* stre
 
 int klt_latent_workspace(const klt_latent* h, int32_t B, int32_t T, uint64_t* bytes) {
   if (!h || !bytes || B < 1 || T < 0) return KLT_ERR_INVALID_ARG;
-  *bytes = attend_workspace(h->num_sms);
+  *bytes = attend_workspace(h->num_sms, h->d.latent);
   return KLT_OK;
 }
 
@@ -380,7 +380,7 @@ int klt_latent_attend(klt_latent* h, const klt_latent_attend_args* a, const klt_
       !disjoint(a->pages, a->page_stride, d.page, a->row_stride, width) ||
       !disjoint(a->T, a->out_token, d.heads, a->out_head, d.latent))
     return KLT_ERR_INVALID_ARG;
-  const int64_t most = 0x7FFFFFFFll;
+  const int64_t most = 0x7FFFFFFFll - 4096;  // room to round up to tiles
   if (a->pages > (most >> h->page_log2) || a->max_pages > (most >> h->page_log2) ||
       a->T > most / d.heads || a->page_stride >= MAX_STRIDE || a->row_stride >= MAX_STRIDE)
     return KLT_ERR_UNSUPPORTED;
@@ -389,7 +389,7 @@ int klt_latent_attend(klt_latent* h, const klt_latent_attend_args* a, const klt_
       !aligned(a->seq_lens, 4) || !aligned(a->cu_q, 4) || a->q_token % 8 || a->q_head % 8 ||
       a->page_stride % 8 || a->row_stride % 8 || a->out_token % 8 || a->out_head % 8)
     return KLT_ERR_ALIGN;
-  if (a->workspace_bytes < attend_workspace(h->num_sms)) return KLT_ERR_INVALID_ARG;
+  if (a->workspace_bytes < attend_workspace(h->num_sms, h->d.latent)) return KLT_ERR_INVALID_ARG;
   const int rc = check_device(h);
   if (rc) return rc;
   AttendParams p = {};

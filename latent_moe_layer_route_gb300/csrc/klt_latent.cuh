@@ -16,6 +16,7 @@ struct AttendParams {
   float* part;           // workspace
   int64_t q_token, q_head, ld_table, out_token, out_head;
   int B, T, H;
+  int members;           // row tiles of a sequence that are computed side by side
   int R, rope;           // latent, position part
   int page_log2, max_pages, pages;
   float scale;           // of the scores, times log2(e)
@@ -124,9 +125,8 @@ KLT_DEV uint32_t pack_bf16(float lo, float hi) {
 }
 
 // ------------------------------------------------------------------ launches
-uint64_t attend_workspace(int num_sms);
-cudaError_t launch_attend(const CUtensorMap& cache, const AttendParams& p, int num_sms,
-                          cudaStream_t s);
+uint64_t attend_workspace(int num_sms, int latent);
+cudaError_t launch_attend(const CUtensorMap& cache, AttendParams p, int num_sms, cudaStream_t s);
 cudaError_t launch_prefill(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                            const CUtensorMap& k_rope, const PrefillParams& p, unsigned tiles,
                            cudaStream_t s);

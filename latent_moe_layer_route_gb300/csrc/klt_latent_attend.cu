@@ -1,9 +1,20 @@
 // Latent attention in absorbed form over a paged cache (sm_103a).
 //
-// 64 query rows (token, head) at a time against 64 keys at a time: S = Q K^T (M = 64 rows, N = 64
-// keys), softmax in registers, O^T += V^T P^T (M = 128 latent columns, N = 64 rows).  A key's row
-// is its value too, so each tile of keys is loaded once and read by both products: K-major by the
-// first, and by the second with its columns as rows.
+// 64 query rows (token, head) against 64 keys at a time: S = Q K^T (M = 64 rows, N = 64 keys),
+// softmax in registers, O^T += V^T P^T (M = 128 latent columns, N = rows).  A key's row is its
+// value too, so a tile of keys is loaded once and read by both products: K-major by the first,
+// with its columns as rows by the second.  O^T rather than O, since 512 columns x 64 rows fill
+// half of TMEM that way and the products have M = 128.
+//
+// Roles: warp 0 copies tiles (two stages of 72 KB in blocks of 128 columns, each handed back on
+// its own), warp 1 issues products (a tile's scores before the values of the tile before it),
+// warps 2 and 3 load the queries, warps 4 to 7 do the softmax and write results.
+//
+// The work is cut evenly: with W tiles of keys over all (sequence, row tile) items, group g of G
+// computes tiles g W / G .. (g + 1) W / G, whatever the lengths.  An item that several groups share
+// leaves its parts (O, running maximum and sum, fp32) in the workspace, and a second kernel brings
+// them together in order; so results do not depend on timing.  Each CTA records what its parts
+// belong to on every call: the workspace holds no state between calls.
 #include "klt_latent.cuh"
 
 #include "../../include/klt.h"
@@ -11,8 +22,113 @@
 namespace klt {
 namespace {
 
-constexpr int ROWS = 64, KEYS = 64;
+constexpr int ROWS = 64, KEYS = 64, STAGES = 2;
 constexpr int BOX = KEYS * 128;  // 64 rows x 128 bytes
+constexpr int MAX_BOXES = 9;     // of a row: 512 columns and the position part
+constexpr int THREADS = 256;
+constexpr int SMEM = 1024 + (MAX_BOXES * (1 + STAGES) + 1) * BOX;
+constexpr int MIN_TILES = 2;     // a group's least share
+constexpr int UNITS = 8;         // joining blocks per part
+constexpr int JOIN = 128;        // their threads
+static_assert(SMEM <= 232448 - 1664, "shared memory of a block");
+
+// What a part of an item in the workspace belongs to.
+struct Record {
+  int valid;   // 0: no part here
+  int token;   // the sequence's first query
+  int row;     // the item's first row in the sequence
+  int rows;    // its rows
+  int first;   // group of its first part
+  int last;    // ... and of its last
+  int slot;    // of its first part
+  int member;
+};
+static_assert(sizeof(Record) == 32, "");
+
+struct Space {  // the workspace: 2 slots per CTA
+  Record* records;  // [slots]
+  float* ml;        // [slots][2][ROWS]: maximum (times scale log2 e), sum
+  float* o;         // [slots][ROWS][R]
+};
+__host__ __device__ inline Space space_of(float* base, int ctas) {
+  Space s;
+  s.records = reinterpret_cast<Record*>(base);
+  s.ml = base + 2 * ctas * (sizeof(Record) / 4);
+  s.o = s.ml + 2 * ctas * 2 * ROWS;
+  return s;
+}
+
+// One sequence's share of the work.
+struct Seq {
+  int q0, n, len;
+  int supers;     // items: sets of `members` row tiles
+  int tiles;      // tiles of keys of each
+  KLT_DEV void load(const AttendParams& p, int b) {
+    q0 = b;
+    int q1 = b + 1;
+    if (p.cu_q) range_of(p.cu_q, b, p.T, q0, q1);
+    n = q1 - q0;
+    len = static_cast<int>(max(0ll, min(static_cast<long long>(p.lens[b]),
+                                        static_cast<long long>(p.max_pages) << p.page_log2)));
+    const int per = ROWS * p.members;
+    supers = (n * p.H + per - 1) / per;
+    tiles = max(1, (len + KEYS - 1) / KEYS);
+  }
+  KLT_DEV long long cost() const { return static_cast<long long>(supers) * tiles; }
+};
+
+// A CTA's part of an item.
+struct Piece {
+  int b, q0, n, len;
+  int row, rows;       // first row of the row tile in the sequence, rows of it (may be 0)
+  int t0, t1;          // tiles of keys that some row sees, in this part
+  bool whole;          // the item is this CTA's alone
+  int slot;            // else: where its part goes
+  long long start;     // the item's first tile in the flat order
+  int tiles;
+};
+struct Walk {
+  long long pos, lo, hi, base;
+  int b;
+  Seq s;
+  KLT_DEV bool next(const AttendParams& p, Piece& w) {
+    if (pos >= hi) return false;
+    while (pos >= base + s.cost()) {
+      base += s.cost();
+      s.load(p, ++b);
+    }
+    const long long local = pos - base;
+    const int super = static_cast<int>(local / s.tiles);
+    const int t = static_cast<int>(local - static_cast<long long>(super) * s.tiles);
+    const int e = static_cast<int>(min(static_cast<long long>(s.tiles), t + (hi - pos)));
+    const int member = blockIdx.x % p.members;
+    w.b = b;
+    w.q0 = s.q0;
+    w.n = s.n;
+    w.len = s.len;
+    w.row = (super * p.members + member) * ROWS;
+    w.rows = max(0, min(ROWS, s.n * p.H - w.row));
+    const int last = (w.row + max(w.rows, 1) - 1) / p.H;  // the tile's last query
+    const int seen = max(0, s.len - (s.n - 1 - last));
+    w.t0 = t;
+    w.t1 = max(t, min(e, (seen + KEYS - 1) / KEYS));
+    w.whole = t == 0 && e == s.tiles;
+    w.slot = 2 * blockIdx.x + (pos == lo ? 0 : 1);
+    w.start = base + static_cast<long long>(super) * s.tiles;
+    w.tiles = s.tiles;
+    pos += e - t;
+    return true;
+  }
+};
+
+struct Bars {
+  uint64_t full[STAGES][5], empty[STAGES][5];  // blocks of a tile: 128 columns; position part
+  uint64_t s_full[2], s_empty[2];
+  uint64_t p_full, pv_done;  // weights are written; the products that read them are done
+  uint64_t o_free;           // O has been read
+  uint64_t q_full, q_free;
+  uint64_t drain;
+};
 
 KLT_DEV float quad_max(float v) {
   v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 1));
@@ -22,242 +138,571 @@ KLT_DEV float quad_sum(float v) {
   v += __shfl_xor_sync(0xFFFFFFFFu, v, 1);
   return v + __shfl_xor_sync(0xFFFFFFFFu, v, 2);
 }
+// Barrier of the softmax warps; whether any of their threads says so.
+KLT_DEV bool softmax_any(bool v) {
+  int r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<int>(v))
+      : "memory");
+  return r != 0;
+}
 
-__global__ void __launch_bounds__(128, 1)
+__global__ void __launch_bounds__(THREADS, 1)
     attend_kernel(const __grid_constant__ CUtensorMap cache, const AttendParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* qs = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  const int NB = p.R / 64, KB = NB + 1;  // boxes of a row: latent, and position part
-  uint8_t* ks = qs + 9 * BOX;
-  uint8_t* ps = ks + 9 * BOX;
-  __shared__ float factor[ROWS];
-  __shared__ uint64_t full, done;
+  const int NJ = p.R / 128, NB = p.R / 64, KB = NB + 1;
+  uint8_t* ks = qs + MAX_BOXES * BOX;
+  uint8_t* ps = ks + STAGES * MAX_BOXES * BOX;
+  __shared__ Bars bars;
+  __shared__ float factor[2][ROWS];
+  __shared__ int64_t out_at[ROWS];
+  __shared__ long long sums[THREADS / 32];
+  __shared__ long long found_base;
+  __shared__ int found_b;
   __shared__ uint32_t tmem_holder;
   __shared__ int abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
-    mbar_init(&full, 1);
-    mbar_init(&done, 1);
+    for (int s = 0; s < STAGES; ++s)
+      for (int i = 0; i < 5; ++i) {
+        mbar_init(&bars.full[s][i], 1);
+        mbar_init(&bars.empty[s][i], 1);
+      }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars.s_full[i], 1);
+      mbar_init(&bars.s_empty[i], 4);
+    }
+    mbar_init(&bars.p_full, 4);
+    mbar_init(&bars.pv_done, 1);
+    mbar_init(&bars.o_free, 4);
+    mbar_init(&bars.q_full, 64);
+    mbar_init(&bars.q_free, 1);
+    mbar_init(&bars.drain, 1);
     abort_flag = 0;
     fence_barrier_init();
+    tma_prefetch_desc(&cache);
   }
-  if (warp == 0) {
+  if (warp == 1) {
     tmem_alloc(&tmem_holder, 512);
     tmem_relinquish();
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = tmem_holder;
   pdl_trigger();
   pdl_wait();
-  volatile int* stop = &abort_flag;
 
-  const int b = blockIdx.x;
-  int q0 = b, q1 = b + 1;
-  if (p.cu_q) range_of(p.cu_q, b, p.T, q0, q1);
-  const int n = q1 - q0;
-  const int len =
-      static_cast<int>(max(0ll, min(static_cast<long long>(p.lens[b]),
-                                    static_cast<long long>(p.max_pages) << p.page_log2)));
-  const int box_keys = p.page_log2 < 6 ? 1 << p.page_log2 : 64;
-  const int64_t rows = static_cast<int64_t>(n) * p.H;
-  int phase = 0, dphase = 0, copies = 0;
-  bool ok = true;
-  for (int64_t r0 = blockIdx.y * static_cast<int64_t>(ROWS); r0 < rows && ok;
-       r0 += static_cast<int64_t>(gridDim.y) * ROWS) {
-    // queries
-    for (int i = tid; i < ROWS * KB * 8; i += 128) {
-      const int r = i / (KB * 8), c = i - r * KB * 8;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (r0 + r < rows && c * 8 < p.R + p.rope) {
-        const int t = static_cast<int>((r0 + r) / p.H), h = static_cast<int>((r0 + r) % p.H);
-        v = *reinterpret_cast<const uint4*>(p.q + (q0 + t) * p.q_token + h * p.q_head + c * 8);
-      }
-      *reinterpret_cast<uint4*>(qs + (c >> 3) * BOX + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+  // the work of all, and this group's share
+  const int group = blockIdx.x / p.members;
+  long long W = 0, mine = 0, excl = 0;
+  Walk walk;
+  {
+    Seq s;
+    s.supers = 0, s.tiles = 1;
+    for (int b = tid; b < p.B; b += THREADS) {
+      s.load(p, b);
+      mine += s.cost();
     }
-    fence_proxy_async_shared();
-    __syncthreads();
-    // this thread's rows: warp * 16 + lane / 4, and 8 further on
-    int limit[2];
-    float m[2], l[2] = {0.f, 0.f};
-    int most = 0;
+    // block-wide sum; where one pass covers the batch, also this sequence's place in it
+    long long incl = mine;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int64_t r = r0 + warp * 16 + lane / 4 + 8 * i;
-      limit[i] = r < rows ? len - (n - 1 - static_cast<int>(r / p.H)) : 0;
-      m[i] = -INFINITY;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += v;
     }
-    {
-      const int64_t last = min(r0 + ROWS, rows) - 1;
-      most = len - (n - 1 - static_cast<int>(last / p.H));
-    }
-    const int tiles = most > 0 ? (most + KEYS - 1) / KEYS : 0;
-    for (int kt = 0; kt < tiles; ++kt) {
-      const int left = min(KEYS, len - kt * KEYS);
-      if (tid == 0 && (p.stall == 0 || copies < p.stall)) {
-        const int boxes = (left + box_keys - 1) / box_keys;
-        mbar_arrive_expect_tx(&full, boxes * KB * box_keys * 128);
-        for (int x = 0; x < boxes; ++x) {
-          const int key = kt * KEYS + x * box_keys;
-          int page = p.table[b * p.ld_table + (key >> p.page_log2)];
-          if (page < 0 || page >= p.pages) page = p.pages;
-          for (int kb = 0; kb < KB; ++kb)
-            tma_load_3d(ks + kb * BOX + x * box_keys * 128, &cache, &full, kb * 64,
-                        key & ((1 << p.page_log2) - 1), page);
-        }
-      }
-      ++copies;
-      ok = mbar_wait(&full, phase, stop, p.err, p.timeout);
-      phase ^= 1;
-      if (!__syncthreads_and(ok)) {
-        ok = false;
-        break;
-      }
-      if (left < KEYS) {  // rows behind the last token hold anything
-        for (int i = tid; i < (KEYS - left) * NB * 8; i += 128) {
-          const int r = left + i / (NB * 8), c = i % (NB * 8);
-          *reinterpret_cast<uint4*>(ks + (c >> 3) * BOX + r * 128 + ((c & 7) << 4)) =
-              make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async_shared();
-        __syncthreads();
-      }
-      if (tid == 0) {
-        tc_fence_after();
-        for (int kb = 0; kb < KB; ++kb) {
-          const int steps = kb < NB ? 4 : p.rope / 16;
-          for (int s = 0; s < steps; ++s)
-            mma_bf16(tmem + 256, sdesc_sw128(smem_u32(qs + kb * BOX)) + 2 * s,
-                     sdesc_sw128(smem_u32(ks + kb * BOX)) + 2 * s, idesc_make(1, 64, 64),
-                     kb | s);
-        }
-        tc_commit(&done);
-      }
-      ok = mbar_wait(&done, dphase, stop, p.err, p.timeout);
-      dphase ^= 1;
-      if (!__syncthreads_and(ok)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      float v[32];
-      tmem_ld_rows16(tmem + 256 + (static_cast<uint32_t>(warp * 32) << 16), v);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float top = m[i];
-#pragma unroll
-        for (int g = 0; g < 8; ++g)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int key = kt * KEYS + 8 * g + 2 * (lane & 3) + j;
-            float& s = v[4 * g + 2 * i + j];
-            s = key < limit[i] ? s * p.scale : -INFINITY;
-            top = fmaxf(top, s);
-          }
-        top = quad_max(top);
-        const float base = top == -INFINITY ? 0.f : top;
-        const float f = exp2_fast(m[i] - base);
-        m[i] = top;
-        const int row = warp * 16 + lane / 4 + 8 * i;
-        if ((lane & 3) == 0) factor[row] = f;
-        l[i] *= f;
-#pragma unroll
-        for (int g = 0; g < 8; ++g) {
-          const float a = exp2_fast(v[4 * g + 2 * i] - base),
-                      c = exp2_fast(v[4 * g + 2 * i + 1] - base);
-          l[i] += a + c;
-          *reinterpret_cast<uint32_t*>(ps + row * 128 + ((g ^ (row & 7)) << 4) + (lane & 3) * 4) =
-              pack_bf16(a, c);
-        }
-      }
-      fence_proxy_async_shared();
-      tc_fence_before();
-      __syncthreads();
-      if (kt > 0) {
-        tc_fence_after();
-        for (int c = 0; c < p.R / 128 * 64; c += 16) {
-          float o[16];
-          const uint32_t at = tmem + (static_cast<uint32_t>(warp * 32) << 16) + c;
-          tmem_ld16(at, o);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] *= factor[(c & 63) + i];
-          tmem_st16(at, o);
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncthreads();
-      }
-      if (tid == 0) {
-        tc_fence_after();
-        for (int j = 0; j < p.R / 128; ++j)
-          for (int s = 0; s < 4; ++s)
-            mma_bf16(tmem + j * 64, sdesc_sw128_mn(smem_u32(ks + 2 * j * BOX + s * 2048), BOX),
-                     sdesc_sw128(smem_u32(ps)) + 2 * s, idesc_make(1, 128, 64) | IDESC_A_MN,
-                     kt | s);
-        tc_commit(&done);
-      }
-      ok = mbar_wait(&done, dphase, stop, p.err, p.timeout);
-      dphase ^= 1;
-      if (!__syncthreads_and(ok)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-    }
-    if (!ok) break;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float sum = quad_sum(l[i]);
-      const int64_t r = r0 + warp * 16 + lane / 4 + 8 * i;
-      if ((lane & 3) == 0) {
-        factor[r - r0] = sum > 0.f || sum != sum ? 1.0f / sum : 0.f;
-        if (p.lse && r < rows)
-          p.lse[static_cast<int64_t>(q0) * p.H + r] =
-              sum == 0.f ? -INFINITY : (m[i] + log2f(sum)) * 0.6931471805599453f;
-      }
-    }
-    __syncthreads();
-    for (int c = 0; c < p.R / 128 * 64; c += 16) {
-      float o[16] = {};
-      if (tiles > 0) tmem_ld16(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c, o);
-      for (int i = 0; i < 16; ++i) {
-        const int64_t r = r0 + (c & 63) + i;
-        if (r < rows) {
-          const float f = factor[(c & 63) + i];
-          p.out[(q0 + r / p.H) * p.out_token + r % p.H * p.out_head + (c >> 6) * 128 + warp * 32 +
-                lane] = __float2bfloat16(f == 0.f ? 0.f : o[i] * f);
-        }
-      }
-    }
+    if (lane == 31) sums[warp] = incl;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    for (int i = 0; i < THREADS / 32; ++i) {
+      if (i == warp) excl = W + incl - mine;
+      W += sums[i];
+    }
+    const long long groups = max(1ll, min(static_cast<long long>(gridDim.x / p.members),
+                                          W / MIN_TILES));
+    walk.lo = walk.pos = group < groups ? W * group / groups : 0;
+    walk.hi = group < groups ? W * (group + 1) / groups : 0;
+    if (p.B <= THREADS) {
+      if (mine > 0 && walk.lo >= excl && walk.lo < excl + mine) found_b = tid, found_base = excl;
+      __syncthreads();
+    } else {  // pass by pass
+      long long before = 0;
+      for (int b0 = 0; b0 < p.B; b0 += THREADS) {
+        long long c = 0;
+        if (b0 + tid < p.B) {
+          s.load(p, b0 + tid);
+          c = s.cost();
+        }
+        long long in = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long v = __shfl_up_sync(0xFFFFFFFFu, in, o);
+          if (lane >= o) in += v;
+        }
+        __syncthreads();
+        if (lane == 31) sums[warp] = in;
+        __syncthreads();
+        for (int i = 0; i < warp; ++i) in += sums[i];
+        in += before;
+        if (c > 0 && walk.lo >= in - c && walk.lo < in) found_b = b0 + tid, found_base = in - c;
+        for (int i = 0; i < THREADS / 32; ++i) before += sums[i];
+      }
+      __syncthreads();
+    }
+    if (walk.lo < walk.hi) {
+      walk.b = found_b;
+      walk.base = found_base;
+      walk.s.load(p, walk.b);
+    }
+    excl = groups;  // kept for the records
+  }
+  const long long groups = excl;
+  const uint32_t tmem = tmem_holder, S = tmem + 256;
+  volatile int* stop = &abort_flag;
+  const Space ws = space_of(p.part, gridDim.x);
+  auto wait = [&](uint64_t* bar, int phase) {
+    return mbar_wait_spin(bar, phase & 1, stop, p.err, p.timeout);
+  };
+  Piece w;
+
+  if (warp == 0) {
+    // ------------------------------------------------ copies
+    if (lane == 0) {
+      const int box_log2 = min(p.page_log2, 6), box_keys = 1 << box_log2;
+      const int page_mask = (1 << p.page_log2) - 1;
+      int it = 0, cut = 0;  // tiles; blocks of the last one, where it was cut short
+      bool ok = true;
+      while (ok && walk.next(p, w)) {
+        if (w.rows == 0) continue;
+        const int* table = p.table + w.b * p.ld_table;
+        auto pages_of = [&](int t, int* page) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int key = t * KEYS + (x << box_log2);
+            if (x << box_log2 < KEYS && key < w.len && t < w.t1) page[x] = table[key >> p.page_log2];
+          }
+        };
+        int page[4], ahead[4];
+        pages_of(w.t0, ahead);
+        for (int t = w.t0; t < w.t1; ++t, ++it) {
+          if (p.stall > 0 && it >= p.stall) ok = false;
+          if (!ok) break;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) page[x] = ahead[x];
+          pages_of(t + 1, ahead);
+          const int st = it % STAGES, left = min(KEYS, w.len - t * KEYS);
+          const int boxes = (left + box_keys - 1) >> box_log2;
+          for (cut = 0; cut <= NJ; ++cut) {
+            const int i = cut;
+            ok = wait(&bars.empty[st][i], (it / STAGES) + 1);
+            if (!ok) break;
+            const int wide = i < NJ ? 2 : 1;
+            mbar_arrive_expect_tx(&bars.full[st][i], boxes * wide * (box_keys * 128));
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              if (x >= boxes) break;
+              const int key = t * KEYS + (x << box_log2);
+              const int at = page[x] >= 0 && page[x] < p.pages ? page[x] : p.pages;
+              for (int c = 2 * i; c < 2 * i + wide; ++c)
+                tma_load_3d(ks + (st * MAX_BOXES + c) * BOX + x * box_keys * 128, &cache,
+                            &bars.full[st][i], c * 64, key & page_mask, at);
+            }
+          }
+          if (!ok) break;
+          cut = 0;
+        }
+      }
+      // no copy of this CTA is in flight past this point
+      int none = 0;
+      for (int i = 0; i <= NJ; ++i)
+        for (int s = 0; s < STAGES; ++s) {
+          const int j = (i < cut ? it : it - 1) - s;
+          if (j >= 0)
+            mbar_wait(&bars.full[j % STAGES][i], (j / STAGES) & 1, &none, p.err, p.timeout);
+        }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------ products
+    if (lane == 0) {
+      int it = 0, piece = 0;  // tiles; pieces with rows and tiles
+      bool ok = true;
+      while (ok && walk.next(p, w)) {
+        if (w.rows == 0 || w.t0 == w.t1) continue;
+        const uint32_t pv = idesc_make(1, 128, (w.rows + 15) & ~15) | IDESC_A_MN;
+        const int nt = w.t1 - w.t0;
+        ok = wait(&bars.q_full, piece);
+        for (int t = 0; t <= nt && ok; ++t) {
+          if (t < nt) {  // scores of tile t
+            const int i = it + t, st = i % STAGES, buf = i & 1;
+            ok = wait(&bars.s_empty[buf], (i >> 1) + 1);
+            const uint32_t qa = smem_u32(qs), ka = smem_u32(ks + st * MAX_BOXES * BOX);
+            for (int j = 0; j <= NJ && ok; ++j) {
+              ok = wait(&bars.full[st][j], i / STAGES);
+              if (!ok) break;
+              tc_fence_after();
+              if (j < NJ) {
+                mma4_bf16(S + buf * 64, sdesc_sw128(qa + 2 * j * BOX),
+                          sdesc_sw128(ka + 2 * j * BOX), idesc_make(1, 64, 64), j);
+                mma4_bf16(S + buf * 64, sdesc_sw128(qa + (2 * j + 1) * BOX),
+                          sdesc_sw128(ka + (2 * j + 1) * BOX), idesc_make(1, 64, 64), 1);
+              } else {
+                for (int s = 0; s < p.rope / 16; ++s)
+                  mma_bf16(S + buf * 64, sdesc_sw128(qa + NB * BOX) + 2 * s,
+                           sdesc_sw128(ka + NB * BOX) + 2 * s, idesc_make(1, 64, 64), 1);
+              }
+            }
+            if (!ok) break;
+            tc_commit(&bars.s_full[buf]);
+            tc_commit(&bars.empty[st][NJ]);
+            if (t == nt - 1) tc_commit(&bars.q_free);
+          }
+          if (t > 0) {  // values of the tile before
+            const int i = it + t - 1, st = i % STAGES;
+            ok = wait(&bars.p_full, i) && (t > 1 || wait(&bars.o_free, piece + 1));
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t va = smem_u32(ks + st * MAX_BOXES * BOX), pa = smem_u32(ps);
+            for (int j = 0; j < NJ; ++j) {
+#pragma unroll
+              for (int s = 0; s < 4; ++s)
+                mma_bf16(tmem + j * 64, sdesc_sw128_mn(va + 2 * j * BOX + s * 2048, BOX),
+                         sdesc_sw128(pa) + 2 * s, pv, (t > 1) | s);
+              tc_commit(&bars.empty[st][j]);
+            }
+            tc_commit(&bars.pv_done);
+          }
+        }
+        it += nt;
+        ++piece;
+      }
+      tc_commit(&bars.drain);  // no product runs past this point
+      int none = 0;
+      mbar_wait(&bars.drain, 0, &none, p.err, p.timeout);
+    }
+  } else if (warp < 4) {
+    // ------------------------------------------------ queries
+    const int me = tid - 64;
+    int piece = 0;
+    bool ok = true;
+    while (ok && walk.next(p, w)) {
+      if (w.rows == 0 || w.t0 == w.t1) continue;
+      ok = wait(&bars.q_free, piece + 1);
+      if (!ok) break;
+      // a warp takes a row at a time, lanes neighbouring chunks of 8
+      const int chunks = (p.R + p.rope) >> 3;
+      for (int r = me >> 5; r < ROWS; r += 2) {
+        const int row = w.row + r;
+        const bool there = r < w.rows;
+        const int t = there ? row / p.H : 0, h = there ? row - t * p.H : 0;
+        const __nv_bfloat16* src =
+            p.q + static_cast<int64_t>(w.q0 + t) * p.q_token + static_cast<int64_t>(h) * p.q_head;
+        for (int c = lane; c < KB * 8; c += 32) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (there && c < chunks) v = reinterpret_cast<const uint4*>(src)[c];
+          *reinterpret_cast<uint4*>(qs + (c >> 3) * BOX + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+        }
+      }
+      fence_proxy_async_shared();
+      mbar_arrive(&bars.q_full);
+      ++piece;
+    }
+  } else {
+    // ------------------------------------------------ softmax and results
+    const int sw = warp - 4, st = tid - 128;
+    const uint32_t lanes = static_cast<uint32_t>(sw * 32) << 16;
+    int it = 0;
+    bool ok = true;
+    bool left_part[2] = {false, false};
+    while (walk.next(p, w)) {
+      if (w.rows == 0) continue;
+      // rows of this thread: sw * 16 + lane / 4, and 8 further on
+      int limit[2];
+      float m[2], l[2] = {0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = sw * 16 + (lane >> 2) + 8 * i;
+        limit[i] = r < w.rows ? w.len - (w.n - 1 - (w.row + r) / p.H) : 0;
+        m[i] = -INFINITY;
+      }
+      if (st < ROWS) {
+        const int row = w.row + st, t = row / p.H;
+        out_at[st] = (w.q0 + t) * p.out_token + (row - t * p.H) * p.out_head;
+      }
+      for (int t = w.t0; t < w.t1; ++t, ++it) {
+        const int buf = it & 1, first = t * KEYS;
+        // a warp that gave up still meets the others' barriers
+        ok = ok && wait(&bars.s_full[buf], it >> 1);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        float v[32];
+        if (ok) {
+          tc_fence_after();
+          tmem_ld_rows16(S + buf * 64 + lanes, v);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.s_empty[buf]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = 0.f;
+        }
+        float top[2];
+        bool grows = false;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (first + KEYS > limit[i]) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const int at = 4 * (e >> 1) + 2 * i + (e & 1);
+              if (first + 8 * (e >> 1) + 2 * (lane & 3) + (e & 1) >= limit[i]) v[at] = -INFINITY;
+            }
+          }
+          float x = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) x = fmaxf(x, v[4 * (e >> 1) + 2 * i + (e & 1)]);
+          top[i] = quad_max(x) * p.scale;
+          // the maximum in use may lag by 8: weights stay below 2^8, and O is rarely rescaled
+          grows = grows || top[i] > m[i] + 8.f;
+        }
+        // O's columns are all warps' rows; two buffers, since a warp may be a tile ahead
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float base = fmaxf(m[i], top[i]);
+          if ((lane & 3) == 0)
+            factor[it & 1][sw * 16 + (lane >> 2) + 8 * i] =
+                base == -INFINITY ? 1.f : exp2_fast(m[i] - base);
+        }
+        const bool rescale = softmax_any(grows);
+        // the products of the tile before have read the weights
+        ok = ok && wait(&bars.pv_done, it + 1);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) continue;
+        if (rescale) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            l[i] *= factor[it & 1][sw * 16 + (lane >> 2) + 8 * i];
+            m[i] = fmaxf(m[i], top[i]);
+          }
+          if (t > w.t0) {
+            tc_fence_after();
+            for (int c = 0; c < NJ * 64; c += 16) {
+              float o[16];
+              tmem_ld16(tmem + lanes + c, o);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] *= factor[it & 1][(c & 63) + i];
+              tmem_st16(tmem + lanes + c, o);
+            }
+            tmem_wait_st();
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float base = m[i] == -INFINITY ? 0.f : m[i];
+          const int row = sw * 16 + (lane >> 2) + 8 * i;
+#pragma unroll
+          for (int g = 0; g < 8; ++g) {
+            const float a = exp2_fast(fmaf(v[4 * g + 2 * i], p.scale, -base)),
+                        c = exp2_fast(fmaf(v[4 * g + 2 * i + 1], p.scale, -base));
+            l[i] += a + c;
+            *reinterpret_cast<uint32_t*>(ps + row * 128 + ((g ^ (row & 7)) << 4) +
+                                         (lane & 3) * 4) = pack_bf16(a, c);
+          }
+        }
+        if (w.len - first < KEYS) {  // rows behind the last token hold anything
+          const int behind = w.len - first;
+          uint8_t* vs = ks + (it % STAGES) * MAX_BOXES * BOX;
+          for (int i = st; i < (KEYS - behind) * NB * 8; i += 128) {
+            const int r = behind + i / (NB * 8), c = i % (NB * 8);
+            *reinterpret_cast<uint4*>(vs + (c >> 3) * BOX + r * 128 + ((c & 7) << 4)) =
+                make_uint4(0, 0, 0, 0);
+          }
+        }
+        fence_proxy_async_shared();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.p_full);
+      }
+      // the part's result
+      if (ok && w.t0 < w.t1) ok = wait(&bars.pv_done, it - 1);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (softmax_any(!ok)) {
+        ok = false;
+        continue;
+      }
+      tc_fence_after();
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float sum = quad_sum(l[i]);
+        const int r = sw * 16 + (lane >> 2) + 8 * i;
+        if ((lane & 3) == 0) {
+          factor[0][r] = !w.whole ? 1.f : sum != 0.f ? 1.0f / sum : 0.f;
+          if (!w.whole) {
+            ws.ml[w.slot * 2 * ROWS + r] = m[i];
+            ws.ml[(w.slot * 2 + 1) * ROWS + r] = sum;
+          } else if (p.lse && r < w.rows) {
+            p.lse[static_cast<int64_t>(w.q0) * p.H + w.row + r] =
+                sum == 0.f ? -INFINITY : (m[i] + log2f(sum)) * 0.6931471805599453f;
+          }
+        }
+      }
+      softmax_any(false);
+      for (int c = 0; c < NJ * 64; c += 16) {
+        const int col = (c >> 6) * 128 + sw * 32 + lane, r0 = c & 63;
+        if (r0 >= w.rows) continue;
+        float o[16];
+        if (w.t0 < w.t1) {
+          tmem_ld16(tmem + lanes + c, o);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] = 0.f;
+        }
+        if (w.whole) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (r0 + i < w.rows) {
+              const float f = factor[0][r0 + i];
+              p.out[out_at[r0 + i] + col] = __float2bfloat16(f == 0.f ? 0.f : o[i] * f);
+            }
+        } else if (w.t0 < w.t1) {
+          float* dst = ws.o + (static_cast<int64_t>(w.slot) * ROWS + r0) * p.R + col;
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (r0 + i < w.rows) dst[i * p.R] = o[i];
+        }
+      }
+      if (w.t0 < w.t1) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.o_free);
+      }
+      if (!w.whole) {
+        left_part[w.slot & 1] = true;
+        if (st == 0) {
+          Record r;
+          r.valid = 1;
+          r.token = w.q0;
+          r.row = w.row;
+          r.rows = w.rows;
+          r.first = static_cast<int>(((w.start + 1) * groups - 1) / W);
+          r.last = static_cast<int>(((w.start + w.tiles) * groups - 1) / W);
+          r.member = blockIdx.x % p.members;
+          const int cta = r.first * p.members + r.member;
+          r.slot = 2 * cta + (W * r.first / groups == w.start ? 0 : 1);
+          ws.records[w.slot] = r;
+        }
+      }
+      softmax_any(false);  // factor and out_at are free
+    }
+    if (st < 2 && !left_part[st]) ws.records[2 * blockIdx.x + st].valid = 0;
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 0) {
+  if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
 }
 
-constexpr int SMEM = 1024 + 19 * BOX;
+// Brings an item's parts together: weights 2^(m_i - M) / L per row, with M the largest maximum and
+// L the weighted sum.  The item's float4s are shared out over UNITS blocks per part; where there
+// are many parts a block has few of them, and several threads share each one's parts, so a block's
+// time hardly depends on their number.
+__global__ void __launch_bounds__(JOIN) join_kernel(const AttendParams p, int ctas) {
+  __shared__ float weight[512];
+  pdl_trigger();
+  pdl_wait();
+  const Space ws = space_of(p.part, ctas);
+  const int slot = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
+  const Record rec = ws.records[slot];
+  if (!rec.valid) return;
+  const int parts = rec.last - rec.first + 1;
+  const int unit = (slot / 2 / p.members - rec.first) * UNITS + blockIdx.y, units = parts * UNITS;
+  const int per_row = p.R >> 2, total = rec.rows * per_row;
+  const int per = (total + units - 1) / units;
+  const int o0 = unit * per, o1 = min(total, o0 + per);
+  if (o0 >= o1) return;
+  auto slot_of = [&](int i) {
+    return i == 0 ? rec.slot : 2 * ((rec.first + i) * p.members + rec.member);
+  };
+  const int row0 = o0 / per_row, rows = (o1 - 1) / per_row - row0 + 1;
+  for (int r = tid >> 5; r < rows; r += JOIN / 32) {
+    float top = -INFINITY;
+    for (int i = lane; i < parts; i += 32) {
+      const float m = ws.ml[slot_of(i) * 2 * ROWS + row0 + r];
+      weight[r * parts + i] = m;
+      top = fmaxf(top, m);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    float sum = 0.f;
+    for (int i = lane; i < parts; i += 32) {
+      const float m = weight[r * parts + i];
+      const float f = m == -INFINITY ? 0.f : exp2_fast(m - top);
+      weight[r * parts + i] = f;
+      const float l = ws.ml[(slot_of(i) * 2 + 1) * ROWS + row0 + r];
+      sum += l == 0.f ? 0.f : f * l;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    const float inv = sum != 0.f ? 1.0f / sum : 0.f;
+    for (int i = lane; i < parts; i += 32) weight[r * parts + i] *= inv;
+    if (lane == 0 && p.lse && (row0 + r) * per_row >= o0)
+      p.lse[static_cast<int64_t>(rec.token) * p.H + rec.row + row0 + r] =
+          sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+  }
+  __syncthreads();
+  int split = 1;  // threads that share one float4's parts
+  while (split < 32 && 2 * split <= parts && JOIN / (2 * split) >= per) split *= 2;
+  const int at = tid / split, share = tid - at * split;
+  for (int o = o0; o < o1; o += JOIN / split) {
+    const int x = o + at;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int row = x / per_row, col = x - row * per_row;
+    if (x < o1) {
+#pragma unroll 4
+      for (int i = share; i < parts; i += split) {
+        const float f = weight[(row - row0) * parts + i];
+        if (f == 0.f) continue;  // a part without keys has left no O
+        const float4 v = reinterpret_cast<const float4*>(
+            ws.o + (static_cast<int64_t>(slot_of(i)) * ROWS + row) * p.R)[col];
+        acc.x = fmaf(f, v.x, acc.x);
+        acc.y = fmaf(f, v.y, acc.y);
+        acc.z = fmaf(f, v.z, acc.z);
+        acc.w = fmaf(f, v.w, acc.w);
+      }
+    }
+    for (int d = split >> 1; d; d >>= 1) {
+      acc.x += __shfl_down_sync(0xFFFFFFFFu, acc.x, d, split);
+      acc.y += __shfl_down_sync(0xFFFFFFFFu, acc.y, d, split);
+      acc.z += __shfl_down_sync(0xFFFFFFFFu, acc.z, d, split);
+      acc.w += __shfl_down_sync(0xFFFFFFFFu, acc.w, d, split);
+    }
+    if (share == 0 && x < o1) {
+      const int t = (rec.row + row) / p.H, h = rec.row + row - t * p.H;
+      *reinterpret_cast<uint2*>(p.out + (rec.token + t) * p.out_token + h * p.out_head +
+                                col * 4) =
+          make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
+    }
+  }
+}
 
 }  // namespace
 
-uint64_t attend_workspace(int num_sms) { return 16; }
+uint64_t attend_workspace(int num_sms, int latent) {
+  return 2ull * num_sms * (sizeof(Record) + 2 * ROWS * 4 + ROWS * 4ull * latent);
+}
 
 bool prepare_attend() {
   return cudaFuncSetAttribute(attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) ==
          cudaSuccess;
 }
 
-cudaError_t launch_attend(const CUtensorMap& cache, const AttendParams& p, int num_sms,
-                          cudaStream_t s) {
+cudaError_t launch_attend(const CUtensorMap& cache, AttendParams p, int num_sms, cudaStream_t s) {
+  // two row tiles of a sequence read the same keys at the same time, the second from L2
+  p.members = static_cast<int64_t>(p.T) * p.H > static_cast<int64_t>(ROWS) * p.B ? 2 : 1;
+  const int ctas = min(num_sms, 240) / p.members * p.members;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.B, 4);
-  cfg.blockDim = dim3(128);
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = SMEM;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -265,7 +710,12 @@ cudaError_t launch_attend(const CUtensorMap& cache, const AttendParams& p, int n
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attend_kernel, cache, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, attend_kernel, cache, p);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(2 * ctas, UNITS);
+  cfg.blockDim = dim3(JOIN);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, join_kernel, static_cast<const AttendParams>(p), ctas);
 }
 
 }  // namespace klt
