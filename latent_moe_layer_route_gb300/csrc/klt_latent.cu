@@ -382,7 +382,8 @@ int klt_latent_attend(klt_latent* h, const klt_latent_attend_args* a, const klt_
     return KLT_ERR_INVALID_ARG;
   const int64_t most = 0x7FFFFFFFll - 4096;  // room to round up to tiles
   if (a->pages > (most >> h->page_log2) || a->max_pages > (most >> h->page_log2) ||
-      a->T > most / d.heads || a->page_stride >= MAX_STRIDE || a->row_stride >= MAX_STRIDE)
+      a->T > most / d.heads || a->page_stride >= MAX_STRIDE ||
+      a->row_stride >= MAX_STRIDE || a->q_token >= MAX_STRIDE || a->q_head >= MAX_STRIDE)
     return KLT_ERR_UNSUPPORTED;
   if (!aligned(a->q, 16) || !aligned(a->cache, 16) || !aligned(a->out, 16) ||
       !aligned(a->workspace, 16) || !aligned(a->lse, 4) || !aligned(a->block_table, 4) ||
@@ -422,7 +423,25 @@ int klt_latent_attend(klt_latent* h, const klt_latent_attend_args* a, const klt_
       !encode_rows(&cache, a->cache, width, d.page, a->row_stride, a->pages, a->page_stride,
                    d.page < 64 ? d.page : 64, 1))
     return KLT_ERR_CUDA;
-  return outcome(launch_attend(cache, p, h->num_sms, static_cast<cudaStream_t>(stream)));
+  // queries by bulk copies: 64 rows where (token, head) is one direction, else the heads that a
+  // token's 64 rows are made of; heads that are no multiple of 8 at other strides are copied by
+  // threads (7 us a tile of rows)
+  CUtensorMap queries = {};
+  const int heads = d.heads & -d.heads;  // largest power of two that divides them
+  if (d.heads == 1 ? a->T == 1 || a->q_token > 0
+                   : a->q_head > 0 && (a->T == 1 || a->q_token == d.heads * a->q_head)) {
+    p.q_packed = true;
+    p.q_box = 64;
+    if (!encode_rows(&queries, a->q, width, static_cast<int64_t>(a->T) * d.heads,
+                     d.heads > 1 ? a->q_head : a->q_token, 1, 0, 64, 1))
+      return KLT_ERR_CUDA;
+  } else if (heads >= 8 && a->q_token > 0 && a->q_head > 0) {
+    p.q_box = heads < 64 ? heads : 64;
+    if (!encode_rows(&queries, a->q, width, d.heads, a->q_head, a->T, a->q_token, p.q_box, 1))
+      return KLT_ERR_CUDA;
+  }
+  return outcome(
+      launch_attend(cache, queries, p, h->num_sms, static_cast<cudaStream_t>(stream)));
 }
 
 int klt_latent_prefill(klt_latent* h, const klt_latent_prefill_args* a,

@@ -17,6 +17,8 @@ struct AttendParams {
   int64_t q_token, q_head, ld_table, out_token, out_head;
   int B, T, H;
   int members;           // row tiles of a sequence that are computed side by side
+  int q_box;             // rows of the queries' map that a bulk copy takes, 0: none can
+  bool q_packed;         // that map's rows are (token, head) in one direction
   int R, rope;           // latent, position part
   int page_log2, max_pages, pages;
   float scale;           // of the scores, times log2(e)
@@ -112,6 +114,37 @@ KLT_DEV void tmem_st32(uint32_t taddr, const uint32_t* r) {
       : "memory");
 }
 
+// One lane of a converged warp, in a form that the compiler knows to be one: the operands of bulk
+// copies and products then stay in uniform registers (64 x 64 x 16 products 47 -> 35 cycles each).
+KLT_DEV bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
+// Whether phase `phase` (its parity counts) of `bar` is complete.
+KLT_DEV bool mbar_test(uint64_t* bar, int phase) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(phase & 1)
+      : "memory");
+  return ok != 0;
+}
+
+// Asynchronous copy of `bytes` (16 or 0) from global to shared memory; the rest of 16 is zeros.
+KLT_DEV void cp_async16(void* dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(bytes)
+               : "memory");
+}
+KLT_DEV void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // 2^x by the hardware approximation (2 ulp; subnormal results flushed, far below what a sum of
 // weights of at least one holds).
 KLT_DEV float exp2_fast(float x) {
@@ -126,7 +159,8 @@ KLT_DEV uint32_t pack_bf16(float lo, float hi) {
 
 // ------------------------------------------------------------------ launches
 uint64_t attend_workspace(int num_sms, int latent);
-cudaError_t launch_attend(const CUtensorMap& cache, AttendParams p, int num_sms, cudaStream_t s);
+cudaError_t launch_attend(const CUtensorMap& cache, const CUtensorMap& queries, AttendParams p,
+                          int num_sms, cudaStream_t s);
 cudaError_t launch_prefill(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                            const CUtensorMap& k_rope, const PrefillParams& p, unsigned tiles,
                            cudaStream_t s);

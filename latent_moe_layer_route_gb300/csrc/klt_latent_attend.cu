@@ -30,6 +30,7 @@ constexpr int SMEM = 1024 + (MAX_BOXES * (1 + STAGES) + 1) * BOX;
 constexpr int MIN_TILES = 2;     // a group's least share
 constexpr int UNITS = 8;         // joining blocks per part
 constexpr int JOIN = 128;        // their threads
+constexpr int MAX_PARTS = 224;   // of an item
 static_assert(SMEM <= 232448 - 1664, "shared memory of a block");
 
 // What a part of an item in the workspace belongs to.
@@ -151,7 +152,8 @@ KLT_DEV bool softmax_any(bool v) {
 }
 
 __global__ void __launch_bounds__(THREADS, 1)
-    attend_kernel(const __grid_constant__ CUtensorMap cache, const AttendParams p) {
+    attend_kernel(const __grid_constant__ CUtensorMap cache,
+                  const __grid_constant__ CUtensorMap queries, const AttendParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* qs = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const int NJ = p.R / 128, NB = p.R / 64, KB = NB + 1;
@@ -179,7 +181,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     mbar_init(&bars.p_full, 4);
     mbar_init(&bars.pv_done, 1);
     mbar_init(&bars.o_free, 4);
-    mbar_init(&bars.q_full, 64);
+    mbar_init(&bars.q_full, p.q_box ? 1 : 64);
     mbar_init(&bars.q_free, 1);
     mbar_init(&bars.drain, 1);
     abort_flag = 0;
@@ -262,13 +264,13 @@ __global__ void __launch_bounds__(THREADS, 1)
   volatile int* stop = &abort_flag;
   const Space ws = space_of(p.part, gridDim.x);
   auto wait = [&](uint64_t* bar, int phase) {
-    return mbar_wait_spin(bar, phase & 1, stop, p.err, p.timeout);
+    return mbar_wait(bar, phase & 1, stop, p.err, p.timeout);
   };
   Piece w;
 
   if (warp == 0) {
     // ------------------------------------------------ copies
-    if (lane == 0) {
+    if (elect_one()) {
       const int box_log2 = min(p.page_log2, 6), box_keys = 1 << box_log2;
       const int page_mask = (1 << p.page_log2) - 1;
       int it = 0, cut = 0;  // tiles; blocks of the last one, where it was cut short
@@ -324,53 +326,74 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------ products
-    if (lane == 0) {
+    if (elect_one()) {
       int it = 0, piece = 0;  // tiles; pieces with rows and tiles
       bool ok = true;
       while (ok && walk.next(p, w)) {
         if (w.rows == 0 || w.t0 == w.t1) continue;
         const uint32_t pv = idesc_make(1, 128, (w.rows + 15) & ~15) | IDESC_A_MN;
         const int nt = w.t1 - w.t0;
-        ok = wait(&bars.q_full, piece);
-        for (int t = 0; t <= nt && ok; ++t) {
-          if (t < nt) {  // scores of tile t
-            const int i = it + t, st = i % STAGES, buf = i & 1;
-            ok = wait(&bars.s_empty[buf], (i >> 1) + 1);
-            const uint32_t qa = smem_u32(qs), ka = smem_u32(ks + st * MAX_BOXES * BOX);
-            for (int j = 0; j <= NJ && ok; ++j) {
-              ok = wait(&bars.full[st][j], i / STAGES);
-              if (!ok) break;
-              tc_fence_after();
-              if (j < NJ) {
-                mma4_bf16(S + buf * 64, sdesc_sw128(qa + 2 * j * BOX),
-                          sdesc_sw128(ka + 2 * j * BOX), idesc_make(1, 64, 64), j);
-                mma4_bf16(S + buf * 64, sdesc_sw128(qa + (2 * j + 1) * BOX),
-                          sdesc_sw128(ka + (2 * j + 1) * BOX), idesc_make(1, 64, 64), 1);
-              } else {
-                for (int s = 0; s < p.rope / 16; ++s)
-                  mma_bf16(S + buf * 64, sdesc_sw128(qa + NB * BOX) + 2 * s,
-                           sdesc_sw128(ka + NB * BOX) + 2 * s, idesc_make(1, 64, 64), 1);
-              }
-            }
-            if (!ok) break;
-            tc_commit(&bars.s_full[buf]);
-            tc_commit(&bars.empty[st][NJ]);
-            if (t == nt - 1) tc_commit(&bars.q_free);
-          }
-          if (t > 0) {  // values of the tile before
-            const int i = it + t - 1, st = i % STAGES;
-            ok = wait(&bars.p_full, i) && (t > 1 || wait(&bars.o_free, piece + 1));
-            if (!ok) break;
+        // Whichever is ready: the values of the oldest tile whose weights are written, else the next
+        // block of the next tile's scores.  In a fixed order (scores of tile t + 1 before the values
+        // of t) a stage was handed back only after the copy of the tile behind it, 2.7 us a tile.
+        int ts = 0, tv = 0, block = 0;  // next tile of scores and of values, next block of scores
+        const uint32_t qa = smem_u32(qs), pa = smem_u32(ps);
+        long long since = 0;
+        bool start = false;
+        while (tv < nt) {
+          if (tv < ts && mbar_test(&bars.p_full, it + tv) &&
+              (tv > 0 || mbar_test(&bars.o_free, piece + 1))) {
             tc_fence_after();
-            const uint32_t va = smem_u32(ks + st * MAX_BOXES * BOX), pa = smem_u32(ps);
+            const int st = (it + tv) % STAGES;
+            const uint32_t va = smem_u32(ks + st * MAX_BOXES * BOX);
             for (int j = 0; j < NJ; ++j) {
 #pragma unroll
               for (int s = 0; s < 4; ++s)
                 mma_bf16(tmem + j * 64, sdesc_sw128_mn(va + 2 * j * BOX + s * 2048, BOX),
-                         sdesc_sw128(pa) + 2 * s, pv, (t > 1) | s);
+                         sdesc_sw128(pa) + 2 * s, pv, tv | s);
               tc_commit(&bars.empty[st][j]);
             }
             tc_commit(&bars.pv_done);
+            ++tv;
+            since = 0;
+            continue;
+          }
+          if (ts < nt) {
+            const int i = it + ts, st = i % STAGES, buf = i & 1;
+            if (!start)
+              start = mbar_test(&bars.s_empty[buf], (i >> 1) + 1) &&
+                      (ts > 0 || mbar_test(&bars.q_full, piece));
+            if (start && mbar_test(&bars.full[st][block], i / STAGES)) {
+              tc_fence_after();
+              const uint32_t ka = smem_u32(ks + st * MAX_BOXES * BOX);
+              if (block < NJ) {
+                mma4_bf16(S + buf * 64, sdesc_sw128(qa + 2 * block * BOX),
+                          sdesc_sw128(ka + 2 * block * BOX), idesc_make(1, 64, 64), block);
+                mma4_bf16(S + buf * 64, sdesc_sw128(qa + (2 * block + 1) * BOX),
+                          sdesc_sw128(ka + (2 * block + 1) * BOX), idesc_make(1, 64, 64), 1);
+                ++block;
+              } else {
+                for (int s = 0; s < p.rope / 16; ++s)
+                  mma_bf16(S + buf * 64, sdesc_sw128(qa + NB * BOX) + 2 * s,
+                           sdesc_sw128(ka + NB * BOX) + 2 * s, idesc_make(1, 64, 64), 1);
+                tc_commit(&bars.s_full[buf]);
+                tc_commit(&bars.empty[st][NJ]);
+                block = 0;
+                start = false;
+                if (++ts == nt) tc_commit(&bars.q_free);
+              }
+              since = 0;
+              continue;
+            }
+          }
+          if (since == 0) since = clock64();
+          if (*stop || clock64() - since > p.timeout) {
+            if (!*stop) {
+              *stop = 1;
+              atomicOr(p.err, DEV_ERR_TIMEOUT);
+            }
+            ok = false;
+            break;
           }
         }
         it += nt;
@@ -389,7 +412,23 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (w.rows == 0 || w.t0 == w.t1) continue;
       ok = wait(&bars.q_free, piece + 1);
       if (!ok) break;
-      // a warp takes a row at a time, lanes neighbouring chunks of 8
+      ++piece;
+      if (p.q_box) {
+        if (me == 0) {
+          mbar_arrive_expect_tx(&bars.q_full, KB * BOX);
+          for (int r = 0; r < ROWS; r += p.q_box) {
+            // rows past the item are other queries' or lie outside: their scores are masked
+            const int row = w.row + r, t = w.q0 + row / p.H, h = row % p.H;
+            const int at = p.q_packed ? w.q0 * p.H + row : h;
+            for (int c = 0; c < KB; ++c)
+              tma_load_3d(qs + c * BOX + r * 128, &queries, &bars.q_full, c * 64, at,
+                          p.q_packed ? 0 : t);
+          }
+        }
+        continue;
+      }
+      // a warp takes a row at a time, lanes neighbouring chunks of 8; all copies of the tile are in
+      // flight at once (a load and a store in turn took 35 us)
       const int chunks = (p.R + p.rope) >> 3;
       for (int r = me >> 5; r < ROWS; r += 2) {
         const int row = w.row + r;
@@ -398,15 +437,18 @@ __global__ void __launch_bounds__(THREADS, 1)
         const __nv_bfloat16* src =
             p.q + static_cast<int64_t>(w.q0 + t) * p.q_token + static_cast<int64_t>(h) * p.q_head;
         for (int c = lane; c < KB * 8; c += 32) {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (there && c < chunks) v = reinterpret_cast<const uint4*>(src)[c];
-          *reinterpret_cast<uint4*>(qs + (c >> 3) * BOX + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+          const bool inside = there && c < chunks;
+          cp_async16(qs + (c >> 3) * BOX + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+                     inside ? src + c * 8 : p.q, inside ? 16 : 0);
         }
       }
+      cp_async_wait();
       fence_proxy_async_shared();
       mbar_arrive(&bars.q_full);
-      ++piece;
     }
+    int none = 0;
+    if (piece > 0 && p.q_box && me == 0)  // no copy is in flight past this point
+      mbar_wait(&bars.q_full, (piece - 1) & 1, &none, p.err, p.timeout);
   } else {
     // ------------------------------------------------ softmax and results
     const int sw = warp - 4, st = tid - 128;
@@ -625,26 +667,31 @@ __global__ void __launch_bounds__(JOIN) join_kernel(const AttendParams p, int ct
   };
   const int row0 = o0 / per_row, rows = (o1 - 1) / per_row - row0 + 1;
   for (int r = tid >> 5; r < rows; r += JOIN / 32) {
-    float top = -INFINITY;
-    for (int i = lane; i < parts; i += 32) {
-      const float m = ws.ml[slot_of(i) * 2 * ROWS + row0 + r];
-      weight[r * parts + i] = m;
-      top = fmaxf(top, m);
+    float m[MAX_PARTS / 32], l[MAX_PARTS / 32], top = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < MAX_PARTS / 32; ++j) {  // all loads at once
+      const int i = j * 32 + lane;
+      m[j] = -INFINITY, l[j] = 0.f;
+      if (i < parts) {
+        const float* ml = ws.ml + slot_of(i) * 2 * ROWS + row0 + r;
+        m[j] = ml[0], l[j] = ml[ROWS];
+      }
     }
 #pragma unroll
+    for (int j = 0; j < MAX_PARTS / 32; ++j) top = fmaxf(top, m[j]);
+#pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    float sum = 0.f;
-    for (int i = lane; i < parts; i += 32) {
-      const float m = weight[r * parts + i];
-      const float f = m == -INFINITY ? 0.f : exp2_fast(m - top);
-      weight[r * parts + i] = f;
-      const float l = ws.ml[(slot_of(i) * 2 + 1) * ROWS + row0 + r];
-      sum += l == 0.f ? 0.f : f * l;
+#pragma unroll
+    for (int j = 0; j < MAX_PARTS / 32; ++j) {
+      m[j] = m[j] == -INFINITY ? 0.f : exp2_fast(m[j] - top);
+      sum += l[j] == 0.f ? 0.f : m[j] * l[j];
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
     const float inv = sum != 0.f ? 1.0f / sum : 0.f;
-    for (int i = lane; i < parts; i += 32) weight[r * parts + i] *= inv;
+#pragma unroll
+    for (int j = 0; j < MAX_PARTS / 32; ++j)
+      if (j * 32 + lane < parts) weight[r * parts + j * 32 + lane] = m[j] * inv;
     if (lane == 0 && p.lse && (row0 + r) * per_row >= o0)
       p.lse[static_cast<int64_t>(rec.token) * p.H + rec.row + row0 + r] =
           sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
@@ -658,12 +705,14 @@ __global__ void __launch_bounds__(JOIN) join_kernel(const AttendParams p, int ct
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     const int row = x / per_row, col = x - row * per_row;
     if (x < o1) {
-#pragma unroll 4
+#pragma unroll 6
       for (int i = share; i < parts; i += split) {
         const float f = weight[(row - row0) * parts + i];
-        if (f == 0.f) continue;  // a part without keys has left no O
-        const float4 v = reinterpret_cast<const float4*>(
-            ws.o + (static_cast<int64_t>(slot_of(i)) * ROWS + row) * p.R)[col];
+        // a part without keys has left no O
+        const float4 v = f == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                  : reinterpret_cast<const float4*>(
+                                        ws.o + (static_cast<int64_t>(slot_of(i)) * ROWS + row) *
+                                                   p.R)[col];
         acc.x = fmaf(f, v.x, acc.x);
         acc.y = fmaf(f, v.y, acc.y);
         acc.z = fmaf(f, v.z, acc.z);
@@ -696,10 +745,11 @@ bool prepare_attend() {
          cudaSuccess;
 }
 
-cudaError_t launch_attend(const CUtensorMap& cache, AttendParams p, int num_sms, cudaStream_t s) {
+cudaError_t launch_attend(const CUtensorMap& cache, const CUtensorMap& queries, AttendParams p,
+                          int num_sms, cudaStream_t s) {
   // two row tiles of a sequence read the same keys at the same time, the second from L2
   p.members = static_cast<int64_t>(p.T) * p.H > static_cast<int64_t>(ROWS) * p.B ? 2 : 1;
-  const int ctas = min(num_sms, 240) / p.members * p.members;
+  const int ctas = min(num_sms, MAX_PARTS) / p.members * p.members;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(THREADS);
@@ -710,7 +760,7 @@ cudaError_t launch_attend(const CUtensorMap& cache, AttendParams p, int num_sms,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, attend_kernel, cache, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, attend_kernel, cache, queries, p);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3(2 * ctas, UNITS);
   cfg.blockDim = dim3(JOIN);
