@@ -224,6 +224,23 @@ bool encode_rows(CUtensorMap* m, const void* base, int64_t n0, int64_t n1, int64
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// bf16 [n2, n1, 64 blocks] as [n2, blocks, n1, 64], in swizzled boxes of [1, b2, b1, 64].
+bool encode_columns(CUtensorMap* m, const void* base, int64_t blocks, int64_t n1, int64_t s1,
+                    int64_t n2, int64_t s2, uint32_t b1, uint32_t b2) {
+  EncodeTiledFn enc = get_encode();
+  if (!enc) return false;
+  const cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(n1), static_cast<cuuint64_t>(blocks),
+                              static_cast<cuuint64_t>(n2)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(n1 > 1 ? s1 * 2 : 1024), 128,
+                                 static_cast<cuuint64_t>(n2 > 1 ? s2 * 2 : 1024)};
+  const cuuint32_t box[4] = {64, b1, b2, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int outcome(cudaError_t e) {
   if (e == cudaSuccess) return KLT_OK;
   cudaGetLastError();  // reported here, not to the caller's next call
@@ -418,10 +435,15 @@ int klt_latent_attend(klt_latent* h, const klt_latent_attend_args* a, const klt_
   p.stall = dbg ? dbg->stall_after_tiles : 0;
   p.err = h->err;
   p.timeout = timeout_cycles(dbg);
-  CUtensorMap cache = {};
+  // the cache's latent part by 64 columns as a direction of its own, so that one copy brings two
+  // boxes of them, and its position part, which may be narrower than a box
+  const uint32_t keys = d.page < 64 ? d.page : 64;
+  CUtensorMap latents = {}, ropes = {};
   if (a->pages > 0 &&
-      !encode_rows(&cache, a->cache, width, d.page, a->row_stride, a->pages, a->page_stride,
-                   d.page < 64 ? d.page : 64, 1))
+      (!encode_columns(&latents, a->cache, d.latent / 64, d.page, a->row_stride, a->pages,
+                       a->page_stride, keys, keys == 64 ? 2 : 1) ||
+       !encode_rows(&ropes, static_cast<const __nv_bfloat16*>(a->cache) + d.latent, d.rope, d.page,
+                    a->row_stride, a->pages, a->page_stride, keys, 1)))
     return KLT_ERR_CUDA;
   // queries by bulk copies: 64 rows where (token, head) is one direction, else the heads that a
   // token's 64 rows are made of; heads that are no multiple of 8 at other strides are copied by
@@ -441,7 +463,7 @@ int klt_latent_attend(klt_latent* h, const klt_latent_attend_args* a, const klt_
       return KLT_ERR_CUDA;
   }
   return outcome(
-      launch_attend(cache, queries, p, h->num_sms, static_cast<cudaStream_t>(stream)));
+      launch_attend(latents, ropes, queries, p, h->num_sms, static_cast<cudaStream_t>(stream)));
 }
 
 int klt_latent_prefill(klt_latent* h, const klt_latent_prefill_args* a,

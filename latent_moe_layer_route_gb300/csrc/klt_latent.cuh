@@ -80,26 +80,22 @@ KLT_DEV void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int c
       : "memory");
 }
 
-// 64 columns of the 64 rows of an M = 64 accumulator: warp w of a warpgroup holds rows 16 w ..
+// 32 columns of the 64 rows of an M = 64 accumulator: warp w of a warpgroup holds rows 16 w ..
 // 16 w + 15 in its first 16 lanes.  Register 4 g + 2 i + j is row lane / 4 + 8 i, column
 // 8 g + 2 (lane % 4) + j.
 KLT_DEV void tmem_ld_rows16(uint32_t taddr, float* v) {
-  uint32_t r[32];
+  uint32_t r[16];
   asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-        "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
-        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
-        "=r"(r[31])
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr)
       : "memory");
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 KLT_DEV void tmem_st32(uint32_t taddr, const uint32_t* r) {
   asm volatile(
@@ -124,6 +120,14 @@ KLT_DEV bool elect_one() {
   return r != 0;
 }
 
+KLT_DEV void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2,
+                         int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
 // Whether phase `phase` (its parity counts) of `bar` is complete.
 KLT_DEV bool mbar_test(uint64_t* bar, int phase) {
   uint32_t ok;
@@ -159,8 +163,9 @@ KLT_DEV uint32_t pack_bf16(float lo, float hi) {
 
 // ------------------------------------------------------------------ launches
 uint64_t attend_workspace(int num_sms, int latent);
-cudaError_t launch_attend(const CUtensorMap& cache, const CUtensorMap& queries, AttendParams p,
-                          int num_sms, cudaStream_t s);
+cudaError_t launch_attend(const CUtensorMap& latents, const CUtensorMap& ropes,
+                          const CUtensorMap& queries, AttendParams p, int num_sms,
+                          cudaStream_t s);
 cudaError_t launch_prefill(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                            const CUtensorMap& k_rope, const PrefillParams& p, unsigned tiles,
                            cudaStream_t s);

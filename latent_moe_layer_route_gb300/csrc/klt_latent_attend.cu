@@ -8,7 +8,8 @@
 //
 // Roles: warp 0 copies tiles (two stages of 72 KB in blocks of 128 columns, each handed back on
 // its own), warp 1 issues products (a tile's scores before the values of the tile before it),
-// warps 2 and 3 load the queries, warps 4 to 7 do the softmax and write results.
+// warps 2 and 3 load the queries, warps 4 to 11 do the softmax (32 of a tile's keys each) and write
+// results.
 //
 // The work is cut evenly: with W tiles of keys over all (sequence, row tile) items, group g of G
 // computes tiles g W / G .. (g + 1) W / G, whatever the lengths.  An item that several groups share
@@ -25,13 +26,15 @@ namespace {
 constexpr int ROWS = 64, KEYS = 64, STAGES = 2;
 constexpr int BOX = KEYS * 128;  // 64 rows x 128 bytes
 constexpr int MAX_BOXES = 9;     // of a row: 512 columns and the position part
-constexpr int THREADS = 256;
+constexpr int SOFTMAX = 256;      // threads of the softmax: two warps per 16 rows
+constexpr int THREADS = 128 + SOFTMAX;
 constexpr int SMEM = 1024 + (MAX_BOXES * (1 + STAGES) + 1) * BOX;
 constexpr int MIN_TILES = 2;     // a group's least share
 constexpr int UNITS = 8;         // joining blocks per part
-constexpr int JOIN = 128;        // their threads
+constexpr int JOIN = 128;        // their threads: a warp to each of four rows' weights
+static_assert(2 * UNITS >= ROWS / 4 && JOIN == 4 * 32, "");
 constexpr int MAX_PARTS = 224;   // of an item
-static_assert(SMEM <= 232448 - 1664, "shared memory of a block");
+static_assert(SMEM <= 232448 - 2048, "shared memory of a block");
 
 // What a part of an item in the workspace belongs to.
 struct Record {
@@ -48,14 +51,14 @@ static_assert(sizeof(Record) == 32, "");
 
 struct Space {  // the workspace: 2 slots per CTA
   Record* records;  // [slots]
-  float* ml;        // [slots][2][ROWS]: maximum (times scale log2 e), sum
-  float* o;         // [slots][ROWS][R]
+  float2* ml;       // [ROWS][slots]: maximum (times scale log2 e), sum
+  float4* o;        // [slots][ROWS / 4][R]: four rows of a latent column
 };
 __host__ __device__ inline Space space_of(float* base, int ctas) {
   Space s;
   s.records = reinterpret_cast<Record*>(base);
-  s.ml = base + 2 * ctas * (sizeof(Record) / 4);
-  s.o = s.ml + 2 * ctas * 2 * ROWS;
+  s.ml = reinterpret_cast<float2*>(s.records + 2 * ctas);
+  s.o = reinterpret_cast<float4*>(s.ml + 2 * ctas * ROWS);
   return s;
 }
 
@@ -78,6 +81,12 @@ struct Seq {
   KLT_DEV long long cost() const { return static_cast<long long>(supers) * tiles; }
 };
 
+// a b / c for c <= 2^8 or so, without a 64-bit division where 32 bits hold a b.
+KLT_DEV long long share(long long a, int b, int c) {
+  const unsigned long long v = static_cast<unsigned long long>(a) * b;
+  return v >> 32 ? static_cast<long long>(v / c) : static_cast<uint32_t>(v) / c;
+}
+
 // A CTA's part of an item.
 struct Piece {
   int b, q0, n, len;
@@ -99,7 +108,8 @@ struct Walk {
       s.load(p, ++b);
     }
     const long long local = pos - base;
-    const int super = static_cast<int>(local / s.tiles);
+    const int super = static_cast<int>(local >> 32 ? local / s.tiles
+                                                   : static_cast<uint32_t>(local) / s.tiles);
     const int t = static_cast<int>(local - static_cast<long long>(super) * s.tiles);
     const int e = static_cast<int>(min(static_cast<long long>(s.tiles), t + (hi - pos)));
     const int member = blockIdx.x % p.members;
@@ -144,15 +154,16 @@ KLT_DEV bool softmax_any(bool v) {
   int r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      "barrier.cta.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"(static_cast<int>(v))
+      : "r"(static_cast<int>(v)), "n"(SOFTMAX)
       : "memory");
   return r != 0;
 }
 
 __global__ void __launch_bounds__(THREADS, 1)
-    attend_kernel(const __grid_constant__ CUtensorMap cache,
+    attend_kernel(const __grid_constant__ CUtensorMap latents,
+                  const __grid_constant__ CUtensorMap ropes,
                   const __grid_constant__ CUtensorMap queries, const AttendParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* qs = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -160,7 +171,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint8_t* ks = qs + MAX_BOXES * BOX;
   uint8_t* ps = ks + STAGES * MAX_BOXES * BOX;
   __shared__ Bars bars;
-  __shared__ float factor[2][ROWS];
+  __shared__ float factor[ROWS];
+  __shared__ float tops[2][ROWS];  // of each half of a tile's keys: maxima; at the end sums
   __shared__ int64_t out_at[ROWS];
   __shared__ long long sums[THREADS / 32];
   __shared__ long long found_base;
@@ -176,17 +188,19 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.s_full[i], 1);
-      mbar_init(&bars.s_empty[i], 4);
+      mbar_init(&bars.s_empty[i], SOFTMAX / 32);
     }
-    mbar_init(&bars.p_full, 4);
+    mbar_init(&bars.p_full, SOFTMAX / 32);
     mbar_init(&bars.pv_done, 1);
-    mbar_init(&bars.o_free, 4);
+    mbar_init(&bars.o_free, SOFTMAX / 32);
     mbar_init(&bars.q_full, p.q_box ? 1 : 64);
     mbar_init(&bars.q_free, 1);
     mbar_init(&bars.drain, 1);
     abort_flag = 0;
     fence_barrier_init();
-    tma_prefetch_desc(&cache);
+    tma_prefetch_desc(&latents);
+    tma_prefetch_desc(&ropes);
+    if (p.q_box) tma_prefetch_desc(&queries);
   }
   if (warp == 1) {
     tmem_alloc(&tmem_holder, 512);
@@ -198,6 +212,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   // the work of all, and this group's share
   const int group = blockIdx.x / p.members;
   long long W = 0, mine = 0, excl = 0;
+  int groups;
   Walk walk;
   {
     Seq s;
@@ -221,10 +236,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (i == warp) excl = W + incl - mine;
       W += sums[i];
     }
-    const long long groups = max(1ll, min(static_cast<long long>(gridDim.x / p.members),
-                                          W / MIN_TILES));
-    walk.lo = walk.pos = group < groups ? W * group / groups : 0;
-    walk.hi = group < groups ? W * (group + 1) / groups : 0;
+    groups = static_cast<int>(max(1ll, min(static_cast<long long>(gridDim.x / p.members),
+                                           W / MIN_TILES)));
+    walk.lo = walk.pos = group < groups ? share(W, group, groups) : 0;
+    walk.hi = group < groups ? share(W, group + 1, groups) : 0;
     if (p.B <= THREADS) {
       if (mine > 0 && walk.lo >= excl && walk.lo < excl + mine) found_b = tid, found_base = excl;
       __syncthreads();
@@ -257,9 +272,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       walk.base = found_base;
       walk.s.load(p, walk.b);
     }
-    excl = groups;  // kept for the records
   }
-  const long long groups = excl;
   const uint32_t tmem = tmem_holder, S = tmem + 256;
   volatile int* stop = &abort_flag;
   const Space ws = space_of(p.part, gridDim.x);
@@ -306,9 +319,15 @@ __global__ void __launch_bounds__(THREADS, 1)
               if (x >= boxes) break;
               const int key = t * KEYS + (x << box_log2);
               const int at = page[x] >= 0 && page[x] < p.pages ? page[x] : p.pages;
-              for (int c = 2 * i; c < 2 * i + wide; ++c)
-                tma_load_3d(ks + (st * MAX_BOXES + c) * BOX + x * box_keys * 128, &cache,
-                            &bars.full[st][i], c * 64, key & page_mask, at);
+              uint8_t* dst = ks + (st * MAX_BOXES + 2 * i) * BOX + x * box_keys * 128;
+              if (i == NJ) {
+                tma_load_3d(dst, &ropes, &bars.full[st][i], 0, key & page_mask, at);
+              } else {  // both boxes of 64 columns where a page fills their rows
+                tma_load_4d(dst, &latents, &bars.full[st][i], 0, key & page_mask, 2 * i, at);
+                if (box_keys < KEYS)
+                  tma_load_4d(dst + BOX, &latents, &bars.full[st][i], 0, key & page_mask,
+                              2 * i + 1, at);
+              }
             }
           }
           if (!ok) break;
@@ -407,11 +426,29 @@ __global__ void __launch_bounds__(THREADS, 1)
     // ------------------------------------------------ queries
     const int me = tid - 64;
     int piece = 0;
-    bool ok = true;
-    while (ok && walk.next(p, w)) {
-      if (w.rows == 0 || w.t0 == w.t1) continue;
+    bool ok = true, left[2] = {false, false};
+    while (walk.next(p, w)) {
+      if (w.rows == 0) continue;
+      if (!w.whole) {
+        left[0] = left[0] || !(w.slot & 1);
+        left[1] = left[1] || (w.slot & 1);
+        if (me == 32) {
+          Record r;
+          r.valid = 1;
+          r.token = w.q0;
+          r.row = w.row;
+          r.rows = w.rows;
+          r.first = static_cast<int>(((w.start + 1) * groups - 1) / W);
+          r.last = static_cast<int>(((w.start + w.tiles) * groups - 1) / W);
+          r.member = blockIdx.x % p.members;
+          const int cta = r.first * p.members + r.member;
+          r.slot = 2 * cta + (share(W, r.first, groups) == w.start ? 0 : 1);
+          ws.records[w.slot] = r;
+        }
+      }
+      if (!ok || w.t0 == w.t1) continue;
       ok = wait(&bars.q_free, piece + 1);
-      if (!ok) break;
+      if (!ok) continue;
       ++piece;
       if (p.q_box) {
         if (me == 0) {
@@ -446,24 +483,29 @@ __global__ void __launch_bounds__(THREADS, 1)
       fence_proxy_async_shared();
       mbar_arrive(&bars.q_full);
     }
+    if (me == 32) {
+      if (!left[0]) ws.records[2 * blockIdx.x].valid = 0;
+      if (!left[1]) ws.records[2 * blockIdx.x + 1].valid = 0;
+    }
     int none = 0;
     if (piece > 0 && p.q_box && me == 0)  // no copy is in flight past this point
       mbar_wait(&bars.q_full, (piece - 1) & 1, &none, p.err, p.timeout);
   } else {
     // ------------------------------------------------ softmax and results
-    const int sw = warp - 4, st = tid - 128;
-    const uint32_t lanes = static_cast<uint32_t>(sw * 32) << 16;
+    // This warp: rows 16 quad .. + 15 of the scores, keys 32 half .. + 31 of a tile; of O^T latent
+    // columns 32 quad .. + 31 of every 128, those of every second 128 or rows.
+    const int quad = warp & 3, half = (warp - 4) >> 2, st = tid - 128;
+    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+    const int r0 = quad * 16 + (lane >> 2);  // this thread's rows: r0 and r0 + 8
     int it = 0;
     bool ok = true;
-    bool left_part[2] = {false, false};
     while (walk.next(p, w)) {
       if (w.rows == 0) continue;
-      // rows of this thread: sw * 16 + lane / 4, and 8 further on
       int limit[2];
       float m[2], l[2] = {0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int r = sw * 16 + (lane >> 2) + 8 * i;
+        const int r = r0 + 8 * i;
         limit[i] = r < w.rows ? w.len - (w.n - 1 - (w.row + r) / p.H) : 0;
         m[i] = -INFINITY;
       }
@@ -472,91 +514,88 @@ __global__ void __launch_bounds__(THREADS, 1)
         out_at[st] = (w.q0 + t) * p.out_token + (row - t * p.H) * p.out_head;
       }
       for (int t = w.t0; t < w.t1; ++t, ++it) {
-        const int buf = it & 1, first = t * KEYS;
+        const int buf = it & 1, first = t * KEYS + half * 32;
         // a warp that gave up still meets the others' barriers
         ok = ok && wait(&bars.s_full[buf], it >> 1);
         ok = __all_sync(0xFFFFFFFFu, ok);
-        float v[32];
+        float v[16];
         if (ok) {
           tc_fence_after();
-          tmem_ld_rows16(S + buf * 64 + lanes, v);
+          tmem_ld_rows16(S + buf * 64 + half * 32 + lanes, v);
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars.s_empty[buf]);
         } else {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0.f;
+          for (int i = 0; i < 16; ++i) v[i] = 0.f;
         }
+        // The maximum in use may lag by 2^8: weights stay below that, and O is rarely rescaled.
+        // Either half of the keys can make it grow, so the halves' maxima and the vote share one
+        // barrier.  They are read only where there is a second barrier behind.
         float top[2];
         bool grows = false;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          if (first + KEYS > limit[i]) {
+          if (first + 32 > limit[i]) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int at = 4 * (e >> 1) + 2 * i + (e & 1);
-              if (first + 8 * (e >> 1) + 2 * (lane & 3) + (e & 1) >= limit[i]) v[at] = -INFINITY;
-            }
+            for (int e = 0; e < 8; ++e)
+              if (first + 8 * (e >> 1) + 2 * (lane & 3) + (e & 1) >= limit[i])
+                v[4 * (e >> 1) + 2 * i + (e & 1)] = -INFINITY;
           }
           float x = -INFINITY;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) x = fmaxf(x, v[4 * (e >> 1) + 2 * i + (e & 1)]);
+          for (int e = 0; e < 8; ++e) x = fmaxf(x, v[4 * (e >> 1) + 2 * i + (e & 1)]);
           top[i] = quad_max(x) * p.scale;
-          // the maximum in use may lag by 8: weights stay below 2^8, and O is rarely rescaled
           grows = grows || top[i] > m[i] + 8.f;
-        }
-        // O's columns are all warps' rows; two buffers, since a warp may be a tile ahead
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float base = fmaxf(m[i], top[i]);
-          if ((lane & 3) == 0)
-            factor[it & 1][sw * 16 + (lane >> 2) + 8 * i] =
-                base == -INFINITY ? 1.f : exp2_fast(m[i] - base);
+          if ((lane & 3) == 0) tops[half][r0 + 8 * i] = top[i];
         }
         const bool rescale = softmax_any(grows);
         // the products of the tile before have read the weights
         ok = ok && wait(&bars.pv_done, it + 1);
         ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) continue;
-        if (rescale) {
+        if (rescale) {  // O's columns are all warps' rows
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            l[i] *= factor[it & 1][sw * 16 + (lane >> 2) + 8 * i];
-            m[i] = fmaxf(m[i], top[i]);
+            const float now = fmaxf(m[i], fmaxf(top[i], tops[half ^ 1][r0 + 8 * i]));
+            const float f = now == -INFINITY ? 1.f : exp2_fast(m[i] - now);
+            l[i] *= f;
+            m[i] = now;
+            if (half == 0 && (lane & 3) == 0) factor[r0 + 8 * i] = f;
           }
-          if (t > w.t0) {
+          softmax_any(false);
+          if (t > w.t0 && ok) {
             tc_fence_after();
-            for (int c = 0; c < NJ * 64; c += 16) {
+#pragma unroll 1
+            for (int c = half * 16; c < NJ * 64; c += 32) {
               float o[16];
               tmem_ld16(tmem + lanes + c, o);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] *= factor[it & 1][(c & 63) + i];
+              for (int i = 0; i < 16; ++i) o[i] *= factor[(c & 63) + i];
               tmem_st16(tmem + lanes + c, o);
             }
             tmem_wait_st();
           }
         }
+        if (!ok) continue;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const float base = m[i] == -INFINITY ? 0.f : m[i];
-          const int row = sw * 16 + (lane >> 2) + 8 * i;
+          uint8_t* row = ps + (r0 + 8 * i) * 128 + (lane & 3) * 4;
 #pragma unroll
-          for (int g = 0; g < 8; ++g) {
+          for (int g = 0; g < 4; ++g) {
             const float a = exp2_fast(fmaf(v[4 * g + 2 * i], p.scale, -base)),
                         c = exp2_fast(fmaf(v[4 * g + 2 * i + 1], p.scale, -base));
             l[i] += a + c;
-            *reinterpret_cast<uint32_t*>(ps + row * 128 + ((g ^ (row & 7)) << 4) +
-                                         (lane & 3) * 4) = pack_bf16(a, c);
+            *reinterpret_cast<uint32_t*>(row + (((4 * half + g) ^ (r0 & 7)) << 4)) =
+                pack_bf16(a, c);
           }
         }
-        if (w.len - first < KEYS) {  // rows behind the last token hold anything
-          const int behind = w.len - first;
+        if (w.len - t * KEYS < KEYS) {  // rows behind the last token hold anything
           uint8_t* vs = ks + (it % STAGES) * MAX_BOXES * BOX;
-          for (int i = st; i < (KEYS - behind) * NB * 8; i += 128) {
-            const int r = behind + i / (NB * 8), c = i % (NB * 8);
-            *reinterpret_cast<uint4*>(vs + (c >> 3) * BOX + r * 128 + ((c & 7) << 4)) =
-                make_uint4(0, 0, 0, 0);
-          }
+          for (int r = w.len - t * KEYS + (warp - 4); r < KEYS; r += SOFTMAX / 32)
+            for (int c = lane; c < NB * 8; c += 32)
+              *reinterpret_cast<uint4*>(vs + (c >> 3) * BOX + r * 128 + ((c & 7) << 4)) =
+                  make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_shared();
         tc_fence_before();
@@ -564,6 +603,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (lane == 0) mbar_arrive(&bars.p_full);
       }
       // the part's result
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        l[i] = quad_sum(l[i]);
+        if ((lane & 3) == 0) tops[half][r0 + 8 * i] = l[i];
+      }
       if (ok && w.t0 < w.t1) ok = wait(&bars.pv_done, it - 1);
       ok = __all_sync(0xFFFFFFFFu, ok);
       if (softmax_any(!ok)) {
@@ -571,15 +615,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         continue;
       }
       tc_fence_after();
+      if (half == 0 && (lane & 3) == 0) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float sum = quad_sum(l[i]);
-        const int r = sw * 16 + (lane >> 2) + 8 * i;
-        if ((lane & 3) == 0) {
-          factor[0][r] = !w.whole ? 1.f : sum != 0.f ? 1.0f / sum : 0.f;
+        for (int i = 0; i < 2; ++i) {
+          const int r = r0 + 8 * i;
+          const float sum = l[i] + tops[1][r];
+          factor[r] = !w.whole ? 1.f : sum != 0.f ? 1.0f / sum : 0.f;
           if (!w.whole) {
-            ws.ml[w.slot * 2 * ROWS + r] = m[i];
-            ws.ml[(w.slot * 2 + 1) * ROWS + r] = sum;
+            ws.ml[r * 2 * gridDim.x + w.slot] = make_float2(m[i], sum);
           } else if (p.lse && r < w.rows) {
             p.lse[static_cast<int64_t>(w.q0) * p.H + w.row + r] =
                 sum == 0.f ? -INFINITY : (m[i] + log2f(sum)) * 0.6931471805599453f;
@@ -587,9 +630,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
       softmax_any(false);
-      for (int c = 0; c < NJ * 64; c += 16) {
-        const int col = (c >> 6) * 128 + sw * 32 + lane, r0 = c & 63;
-        if (r0 >= w.rows) continue;
+#pragma unroll 1
+      for (int c = half * 16; c < NJ * 64; c += 32) {
+        const int col = (c >> 6) * 128 + quad * 32 + lane, r = c & 63;
+        if (r >= w.rows) continue;
         float o[16];
         if (w.t0 < w.t1) {
           tmem_ld16(tmem + lanes + c, o);
@@ -599,16 +643,16 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         if (w.whole) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (r0 + i < w.rows) {
-              const float f = factor[0][r0 + i];
-              p.out[out_at[r0 + i] + col] = __float2bfloat16(f == 0.f ? 0.f : o[i] * f);
-            }
+          for (int i = 0; i < 16; ++i) {
+            const float f = factor[r + i];
+            if (r + i < w.rows)
+              p.out[out_at[r + i] + col] = __float2bfloat16(f == 0.f ? 0.f : o[i] * f);
+          }
         } else if (w.t0 < w.t1) {
-          float* dst = ws.o + (static_cast<int64_t>(w.slot) * ROWS + r0) * p.R + col;
+          float4* dst = ws.o + static_cast<int64_t>(w.slot * (ROWS / 4) + (r >> 2)) * p.R + col;
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (r0 + i < w.rows) dst[i * p.R] = o[i];
+          for (int i = 0; i < 4; ++i)
+            dst[i * p.R] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
         }
       }
       if (w.t0 < w.t1) {
@@ -616,25 +660,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.o_free);
       }
-      if (!w.whole) {
-        left_part[w.slot & 1] = true;
-        if (st == 0) {
-          Record r;
-          r.valid = 1;
-          r.token = w.q0;
-          r.row = w.row;
-          r.rows = w.rows;
-          r.first = static_cast<int>(((w.start + 1) * groups - 1) / W);
-          r.last = static_cast<int>(((w.start + w.tiles) * groups - 1) / W);
-          r.member = blockIdx.x % p.members;
-          const int cta = r.first * p.members + r.member;
-          r.slot = 2 * cta + (W * r.first / groups == w.start ? 0 : 1);
-          ws.records[w.slot] = r;
-        }
-      }
-      softmax_any(false);  // factor and out_at are free
+      softmax_any(false);  // factor, tops and out_at are free
     }
-    if (st < 2 && !left_part[st]) ws.records[2 * blockIdx.x + st].valid = 0;
   }
   tc_fence_before();
   __syncthreads();
@@ -644,79 +671,85 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
-// Brings an item's parts together: weights 2^(m_i - M) / L per row, with M the largest maximum and
-// L the weighted sum.  The item's float4s are shared out over UNITS blocks per part; where there
-// are many parts a block has few of them, and several threads share each one's parts, so a block's
-// time hardly depends on their number.
-__global__ void __launch_bounds__(JOIN) join_kernel(const AttendParams p, int ctas) {
-  __shared__ float weight[512];
-  pdl_trigger();
-  pdl_wait();
-  const Space ws = space_of(p.part, ctas);
-  const int slot = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
-  const Record rec = ws.records[slot];
-  if (!rec.valid) return;
+// Brings an item's parts together: weights 2^(m_i - M) per row and part, with M the largest maximum,
+// and the sum of weighted O over the sum of weighted sums.  Four rows of the item and some of their
+// columns are a block's, UNITS blocks per part: where there are many parts a block has few columns,
+// and several threads share each one's parts, so its time hardly depends on their number.  The
+// first loads of O go out before the weights are known.
+KLT_DEV void join_item(const AttendParams& p, const Space& ws, int ctas, const Record& rec,
+                       float4* weight, float4* inverse) {
+  constexpr int BATCH = 8;  // parts in flight in a thread
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int parts = rec.last - rec.first + 1;
-  const int unit = (slot / 2 / p.members - rec.first) * UNITS + blockIdx.y, units = parts * UNITS;
-  const int per_row = p.R >> 2, total = rec.rows * per_row;
-  const int per = (total + units - 1) / units;
-  const int o0 = unit * per, o1 = min(total, o0 + per);
-  if (o0 >= o1) return;
+  const int unit = (static_cast<int>(blockIdx.x) / p.members - rec.first) * UNITS + blockIdx.y;
+  const int fours = (rec.rows + 3) >> 2, chunks = parts * UNITS / fours;  // >= 1: UNITS parts >= 16
+  const int four = unit % fours, chunk = unit / fours;
+  const int per = (p.R + chunks - 1) / chunks;  // columns of a block
+  const int c0 = chunk * per, c1 = min(p.R, c0 + per);
+  if (chunk >= chunks || c0 >= c1) return;
   auto slot_of = [&](int i) {
     return i == 0 ? rec.slot : 2 * ((rec.first + i) * p.members + rec.member);
   };
-  const int row0 = o0 / per_row, rows = (o1 - 1) / per_row - row0 + 1;
-  for (int r = tid >> 5; r < rows; r += JOIN / 32) {
-    float m[MAX_PARTS / 32], l[MAX_PARTS / 32], top = -INFINITY, sum = 0.f;
+  int split = 1;  // threads that share a column's parts
+  while (split < 32 && 2 * split <= parts && JOIN / (2 * split) >= per) split *= 2;
+  const int at = tid / split, mine = tid & (split - 1);
+  float4 v[BATCH];
+  auto load = [&](int c, int i0) {
+    const float4* src = ws.o + four * p.R + min(c, p.R - 1);
 #pragma unroll
-    for (int j = 0; j < MAX_PARTS / 32; ++j) {  // all loads at once
-      const int i = j * 32 + lane;
-      m[j] = -INFINITY, l[j] = 0.f;
-      if (i < parts) {
-        const float* ml = ws.ml + slot_of(i) * 2 * ROWS + row0 + r;
-        m[j] = ml[0], l[j] = ml[ROWS];
-      }
+    for (int k = 0; k < BATCH; ++k) {
+      const int i = i0 + k * split;
+      if (i < parts) v[k] = src[static_cast<int64_t>(slot_of(i)) * (ROWS / 4) * p.R];
     }
+  };
+  load(c0 + at, mine);
+  float* const weights = reinterpret_cast<float*>(weight);
+  {
+    const int row = four * 4 + warp;  // this warp's row
+    const float2* ml = ws.ml + row * 2 * ctas;
+    float top = -INFINITY, sum = 0.f;
+    float2 x[MAX_PARTS / 32];
 #pragma unroll
-    for (int j = 0; j < MAX_PARTS / 32; ++j) top = fmaxf(top, m[j]);
+    for (int j = 0; j < MAX_PARTS / 32; ++j) {
+      x[j] = make_float2(-INFINITY, 0.f);
+      if (j * 32 + lane < parts) x[j] = ml[slot_of(j * 32 + lane)];
+      top = fmaxf(top, x[j].x);
+    }
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
 #pragma unroll
     for (int j = 0; j < MAX_PARTS / 32; ++j) {
-      m[j] = m[j] == -INFINITY ? 0.f : exp2_fast(m[j] - top);
-      sum += l[j] == 0.f ? 0.f : m[j] * l[j];
+      const float f = x[j].x == -INFINITY ? 0.f : exp2_fast(x[j].x - top);
+      sum += x[j].y == 0.f ? 0.f : f * x[j].y;
+      if (j * 32 + lane < parts) weights[(j * 32 + lane) * 4 + warp] = f;
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    const float inv = sum != 0.f ? 1.0f / sum : 0.f;
-#pragma unroll
-    for (int j = 0; j < MAX_PARTS / 32; ++j)
-      if (j * 32 + lane < parts) weight[r * parts + j * 32 + lane] = m[j] * inv;
-    if (lane == 0 && p.lse && (row0 + r) * per_row >= o0)
-      p.lse[static_cast<int64_t>(rec.token) * p.H + rec.row + row0 + r] =
-          sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+    if (lane == 0) {
+      reinterpret_cast<float*>(inverse)[warp] = sum != 0.f ? 1.0f / sum : 0.f;
+      if (p.lse && chunk == 0 && row < rec.rows)
+        p.lse[static_cast<int64_t>(rec.token) * p.H + rec.row + row] =
+            sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+    }
   }
   __syncthreads();
-  int split = 1;  // threads that share one float4's parts
-  while (split < 32 && 2 * split <= parts && JOIN / (2 * split) >= per) split *= 2;
-  const int at = tid / split, share = tid - at * split;
-  for (int o = o0; o < o1; o += JOIN / split) {
-    const int x = o + at;
+  const float4 inv = *inverse;
+#pragma unroll 1
+  for (int c = c0 + at; c - at < c1; c += JOIN / split) {
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int row = x / per_row, col = x - row * per_row;
-    if (x < o1) {
-#pragma unroll 6
-      for (int i = share; i < parts; i += split) {
-        const float f = weight[(row - row0) * parts + i];
-        // a part without keys has left no O
-        const float4 v = f == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                  : reinterpret_cast<const float4*>(
-                                        ws.o + (static_cast<int64_t>(slot_of(i)) * ROWS + row) *
-                                                   p.R)[col];
-        acc.x = fmaf(f, v.x, acc.x);
-        acc.y = fmaf(f, v.y, acc.y);
-        acc.z = fmaf(f, v.z, acc.z);
-        acc.w = fmaf(f, v.w, acc.w);
+#pragma unroll 1
+    for (int i0 = mine; i0 < parts; i0 += BATCH * split) {
+      if (c != c0 + at || i0 != mine) load(c, i0);
+#pragma unroll
+      for (int k = 0; k < BATCH; ++k) {
+        const int i = i0 + k * split;
+        if (i < parts) {  // a part in which a row sees no key may have left no O
+          const float4 f = weight[i];
+          acc.x = f.x == 0.f ? acc.x : fmaf(f.x, v[k].x, acc.x);
+          acc.y = f.y == 0.f ? acc.y : fmaf(f.y, v[k].y, acc.y);
+          acc.z = f.z == 0.f ? acc.z : fmaf(f.z, v[k].z, acc.z);
+          acc.w = f.w == 0.f ? acc.w : fmaf(f.w, v[k].w, acc.w);
+        }
       }
     }
     for (int d = split >> 1; d; d >>= 1) {
@@ -725,12 +758,29 @@ __global__ void __launch_bounds__(JOIN) join_kernel(const AttendParams p, int ct
       acc.z += __shfl_down_sync(0xFFFFFFFFu, acc.z, d, split);
       acc.w += __shfl_down_sync(0xFFFFFFFFu, acc.w, d, split);
     }
-    if (share == 0 && x < o1) {
-      const int t = (rec.row + row) / p.H, h = rec.row + row - t * p.H;
-      *reinterpret_cast<uint2*>(p.out + (rec.token + t) * p.out_token + h * p.out_head +
-                                col * 4) =
-          make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
+    if (mine == 0 && c < c1) {
+      const float out[4] = {acc.x * inv.x, acc.y * inv.y, acc.z * inv.z, acc.w * inv.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = rec.row + four * 4 + i, t = r / p.H, h = r - t * p.H;
+        if (four * 4 + i < rec.rows)
+          p.out[(rec.token + t) * p.out_token + h * p.out_head + c] = __float2bfloat16(out[i]);
+      }
     }
+  }
+}
+
+__global__ void __launch_bounds__(JOIN) join_kernel(const AttendParams p, int ctas) {
+  __shared__ float4 weight[MAX_PARTS], inverse;
+  pdl_trigger();
+  pdl_wait();
+  const Space ws = space_of(p.part, ctas);
+  const Record both[2] = {ws.records[2 * blockIdx.x], ws.records[2 * blockIdx.x + 1]};
+#pragma unroll 1
+  for (int i = 0; i < 2; ++i) {
+    const Record rec = i ? both[1] : both[0];
+    if (rec.valid) join_item(p, ws, ctas, rec, weight, &inverse);
+    if (i == 0) __syncthreads();
   }
 }
 
@@ -745,8 +795,9 @@ bool prepare_attend() {
          cudaSuccess;
 }
 
-cudaError_t launch_attend(const CUtensorMap& cache, const CUtensorMap& queries, AttendParams p,
-                          int num_sms, cudaStream_t s) {
+cudaError_t launch_attend(const CUtensorMap& latents, const CUtensorMap& ropes,
+                          const CUtensorMap& queries, AttendParams p, int num_sms,
+                          cudaStream_t s) {
   // two row tiles of a sequence read the same keys at the same time, the second from L2
   p.members = static_cast<int64_t>(p.T) * p.H > static_cast<int64_t>(ROWS) * p.B ? 2 : 1;
   const int ctas = min(num_sms, MAX_PARTS) / p.members * p.members;
@@ -760,9 +811,9 @@ cudaError_t launch_attend(const CUtensorMap& cache, const CUtensorMap& queries, 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, attend_kernel, cache, queries, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, attend_kernel, latents, ropes, queries, p);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(2 * ctas, UNITS);
+  cfg.gridDim = dim3(ctas, UNITS);
   cfg.blockDim = dim3(JOIN);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, join_kernel, static_cast<const AttendParams>(p), ctas);
