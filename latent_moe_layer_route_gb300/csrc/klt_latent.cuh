@@ -169,7 +169,7 @@ cudaError_t launch_attend(const CUtensorMap& latents, const CUtensorMap& ropes,
 cudaError_t launch_prefill(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                            const CUtensorMap& k_rope, const PrefillParams& p, unsigned tiles,
                            cudaStream_t s);
-constexpr int PREFILL_ROWS = 128;  // queries of a tile
+constexpr int PREFILL_ROWS = 256;  // queries of a CTA
 // Once per device, before the first launch; false when a kernel is not what its launch expects.
 bool prepare_attend();
 bool prepare_prefill();
