@@ -482,7 +482,7 @@ int klt_latent_prefill(klt_latent* h, const klt_latent_prefill_args* a,
     return KLT_ERR_INVALID_ARG;
   if (!disjoint(a->T, a->out_token, d.heads, a->out_head, d.value)) return KLT_ERR_INVALID_ARG;
   const int64_t tiles = (a->T + PREFILL_ROWS - 1ll) / PREFILL_ROWS + a->B;
-  if (a->T > 0x7FFFFFFFll / d.heads || tiles > 0x7FFFFFFFll / d.heads ||
+  if (a->T > 0x7FFFFFFFll / d.heads || tiles > 0x3FFFFFFFll ||
       a->q_token >= MAX_STRIDE || a->q_head >= MAX_STRIDE || a->k_token >= MAX_STRIDE ||
       a->k_head >= MAX_STRIDE || a->v_token >= MAX_STRIDE || a->v_head >= MAX_STRIDE ||
       a->ld_k_rope >= MAX_STRIDE)
@@ -518,9 +518,9 @@ int klt_latent_prefill(klt_latent* h, const klt_latent_prefill_args* a,
   if (!encode_rows(&q, a->q, d.nope + d.rope, d.heads, a->q_head, a->T, a->q_token, 1, 128))
     return KLT_ERR_CUDA;
   if (a->S > 0 &&
-      (!encode_rows(&k, a->k, d.nope, d.heads, a->k_head, a->S, a->k_token, 1, 128) ||
+      (!encode_rows(&k, a->k, d.nope, d.heads, a->k_head, a->S, a->k_token, 1, 64) ||
        !encode_rows(&v, a->v, d.value, d.heads, a->v_head, a->S, a->v_token, 1, 128) ||
-       !encode_rows(&k_rope, a->k_rope, d.rope, 1, 0, a->S, a->ld_k_rope, 1, 128)))
+       !encode_rows(&k_rope, a->k_rope, d.rope, 1, 0, a->S, a->ld_k_rope, 1, 64)))
     return KLT_ERR_CUDA;
   return outcome(launch_prefill(q, k, v, k_rope, p, static_cast<unsigned>(tiles),
                                 static_cast<cudaStream_t>(stream)));

@@ -60,16 +60,11 @@ KLT_DEV uint64_t sdesc_sw128_mn(uint32_t saddr, uint32_t box_bytes) {
 }
 constexpr uint32_t IDESC_A_MN = 1u << 15, IDESC_B_MN = 1u << 16;
 
-// D (+)= A B^T with A in TMEM: bf16, two to a column, K = 16 in eight columns.
-KLT_DEV void mma_bf16_ta(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc,
-                         uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
+// Arrive on a barrier of any CTA of the cluster, publishing this thread's writes to the cluster.
+KLT_DEV void mbar_arrive_cluster_release(uint32_t addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr)
+               : "memory");
 }
-
 // 3-D tiled load of the box at (c0 = inner element, c1, c2).
 KLT_DEV void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1,
                          int c2) {
@@ -169,7 +164,7 @@ cudaError_t launch_attend(const CUtensorMap& latents, const CUtensorMap& ropes,
 cudaError_t launch_prefill(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                            const CUtensorMap& k_rope, const PrefillParams& p, unsigned tiles,
                            cudaStream_t s);
-constexpr int PREFILL_ROWS = 256;  // queries of a CTA
+constexpr int PREFILL_ROWS = 512;  // queries of a pair of CTAs
 // Once per device, before the first launch; false when a kernel is not what its launch expects.
 bool prepare_attend();
 bool prepare_prefill();
