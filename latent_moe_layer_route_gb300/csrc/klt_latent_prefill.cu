@@ -9,7 +9,10 @@
 // tiles take turns: while the threads of one do its softmax, the tensor core works on the other.
 //
 // Roles in a CTA: warp 0 copies (three stages of 40 KB), warp 1 of the first CTA issues products,
-// warps 4 to 7 and 8 to 11 do the tiles' softmax.  Their code is kept short (S is read twice, 64
+// warp 3 finds the next unit (512 queries of a sequence and head), warps 4 to 7 and 8 to 11 do the
+// tiles' softmax.  The grid has a pair for every unit; a running pair takes over units that have not
+// started (clusterlaunchcontrol), so that it loads the next one's operands and computes its first
+// scores while it writes the results of this one, and long and short sequences even out.  Their code is kept short (S is read twice, 64
 // columns at a time): unrolled over the 128 columns it pushed the issuing thread's out of the
 // instruction caches, which then took 5,500 cycles for the 2,560 of a round.  O is rescaled only
 // when a row's maximum has grown by 2^8 (by the row's own thread, which knows that no product runs
@@ -29,18 +32,100 @@ constexpr int THREADS = 384;
 constexpr int SMEM = 1024 + 2 * Q_BOXES * BOX + STAGES * STAGE;
 static_assert(4 * ROWS == PREFILL_ROWS, "");
 
+// 512 queries of a sequence and head.
+struct Unit {
+  int q0, n;           // the sequence's first query, its queries
+  int k0, len;         // ... keys
+  int r0, h;           // the unit's first query in the sequence, its head
+  int tiles0, tiles1;  // tiles of keys that the last query of each tile of queries sees
+  int last;            // no unit: the pair is done
+};
+
 // The first CTA's unless it says "each".
 struct Bars {
   uint64_t k_full[STAGES], v_full[STAGES];    // bytes of both CTAs
   uint64_t k_empty[STAGES], v_empty[STAGES];  // each
-  uint64_t q_full[2];
+  uint64_t q_full[2], q_empty[2];             // q_empty: each
   uint64_t s_full[2], pv_done[2];             // each
-  uint64_t p_full[2];                         // the softmax warps of both
-  uint64_t v_last;                            // each: values of the last tile, where it is ragged
+  uint64_t p_full[2], o_free[2];              // the softmax warps of both
+  uint64_t v_last;                            // each: values of a sequence's ragged last tile
   uint64_t cleared;                           // ... cleared behind the sequence in both
+  uint64_t unit_full[2], unit_empty[2];       // each
+  uint64_t loaded;                            // each: a unit's copies are issued
+  uint64_t next_full[2];                      // each: the answer about the next unit
+  uint64_t next_read;                         // the second CTA has read it
   uint64_t drain;                             // each
   uint64_t ended;                             // the second CTA has issued its last copy
 };
+
+// Asks for a cluster of the grid that has not started; the answer (16 bytes) and its signal go to
+// the same places in both CTAs.
+KLT_DEV void ask_next(void* answer, uint64_t* bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes"
+      ".multicast::cluster::all.b128 [%0], [%1];" ::"r"(smem_u32(answer)),
+      "r"(smem_u32(bar))
+      : "memory");
+}
+// The first CTA of the cluster that was given, or false.
+KLT_DEV bool read_next(const void* answer, int& x, int& y) {
+  uint32_t ok, a, b;
+  asm volatile(
+      "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t"
+      "ld.shared.b128 r, [%3];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::y.b32.b128 %2, r;\n\t}"
+      : "=r"(ok), "=r"(a), "=r"(b)
+      : "r"(smem_u32(answer))
+      : "memory");
+  x = static_cast<int>(a);
+  y = static_cast<int>(b);
+  return ok != 0;
+}
+// Unit number `unit` of head h, by a whole warp, 32 sequences at a time; a sequence's last units,
+// which see most keys, come first.  Numbers past the last unit have no tiles.
+KLT_DEV Unit find_unit(const PrefillParams& p, int unit, int h) {
+  const int lane = lane_id();
+  Unit u = {};
+  u.h = h;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    int lo = 0, hi = 0, n = 0;
+    if (b0 + lane < p.B) {
+      range_of(p.cu_q, b0 + lane, p.T, lo, hi);
+      n = (hi - lo + PREFILL_ROWS - 1) / PREFILL_ROWS;
+    }
+    int in = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, in, o);
+      if (lane >= o) in += v;
+    }
+    const uint32_t past = __ballot_sync(0xFFFFFFFFu, unit < in);
+    if (past) {
+      const int src = __ffs(past) - 1;
+      int k1;
+      u.r0 = (__shfl_sync(0xFFFFFFFFu, in, src) - 1 - unit) * PREFILL_ROWS;
+      u.q0 = __shfl_sync(0xFFFFFFFFu, lo, src);
+      u.n = __shfl_sync(0xFFFFFFFFu, hi, src) - u.q0;
+      range_of(p.cu_k, b0 + src, p.S, u.k0, k1);
+      u.len = k1 - u.k0;
+      auto tiles_of = [&](int w) {
+        const int last = min(u.r0 + (w + 1) * 2 * ROWS, u.n) - 1;
+        const int seen = last < u.r0 + w * 2 * ROWS ? 0
+                         : p.causal                 ? u.len - (u.n - 1 - last)
+                                                    : u.len;
+        return max(0, (seen + KEYS - 1) / KEYS);
+      };
+      u.tiles0 = tiles_of(0);
+      u.tiles1 = tiles_of(1);
+      break;
+    }
+    unit -= __shfl_sync(0xFFFFFFFFu, in, 31);
+  }
+  return u;
+}
 
 KLT_DEV void tma_load_3d_pair(void* dst, const CUtensorMap* map, uint32_t bar, int c0, int c1,
                               int c2) {
@@ -103,6 +188,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   uint8_t* qs = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t* ring = qs + 2 * Q_BOXES * BOX;
   __shared__ Bars bars;
+  __shared__ Unit units[2];
+  __shared__ uint4 answers[2];
   __shared__ uint32_t tmem_holder, copies;
   __shared__ int abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -116,10 +203,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.q_full[i], 1);
+      mbar_init(&bars.q_empty[i], 1);
       mbar_init(&bars.s_full[i], 1);
       mbar_init(&bars.p_full[i], 8);
+      mbar_init(&bars.o_free[i], 8);
       mbar_init(&bars.pv_done[i], 1);
+      mbar_init(&bars.unit_full[i], 1);
+      mbar_init(&bars.unit_empty[i], rank == 0 ? 10 : 9);  // copies, products, softmax warps
+      mbar_init(&bars.next_full[i], 1);
     }
+    mbar_init(&bars.loaded, 1);
+    mbar_init(&bars.next_read, 1);
     mbar_init(&bars.v_last, 1);
     mbar_init(&bars.cleared, 8);
     mbar_init(&bars.drain, 1);
@@ -135,116 +229,135 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   if (warp == 2) tmem_alloc_pair(&tmem_holder, 512);
   pdl_trigger();
   pdl_wait();
-
-  // this unit's sequence, 32 sequences at a time; a sequence's last units, which see most keys, first
-  int unit = blockIdx.x >> 1, q0 = 0, q1 = 0, k0 = 0, k1 = 0;
-  bool found = false;
-  for (int b0 = 0; b0 < p.B && !found; b0 += 32) {
-    int lo = 0, hi = 0, n = 0;
-    if (b0 + lane < p.B) {
-      range_of(p.cu_q, b0 + lane, p.T, lo, hi);
-      n = (hi - lo + PREFILL_ROWS - 1) / PREFILL_ROWS;
-    }
-    int in = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xFFFFFFFFu, in, o);
-      if (lane >= o) in += v;
-    }
-    const uint32_t past = __ballot_sync(0xFFFFFFFFu, unit < in);
-    if (past) {
-      const int src = __ffs(past) - 1;
-      found = true;
-      unit = __shfl_sync(0xFFFFFFFFu, in, src) - 1 - unit;
-      q0 = __shfl_sync(0xFFFFFFFFu, lo, src);
-      q1 = __shfl_sync(0xFFFFFFFFu, hi, src);
-      range_of(p.cu_k, b0 + src, p.S, k0, k1);
-    } else {
-      unit -= __shfl_sync(0xFFFFFFFFu, in, 31);
-    }
-  }
-  const int h = blockIdx.y;
-  const int n = q1 - q0, len = k1 - k0, r0 = unit * PREFILL_ROWS;
-  const int nb = p.nope / 64;
-  // tiles of keys that the last query of each tile of queries sees
-  auto tiles_of = [&](int w) {
-    const int last = min(r0 + (w + 1) * 2 * ROWS, n) - 1;
-    const int seen =
-        !found || last < r0 + w * 2 * ROWS ? 0 : p.causal ? len - (n - 1 - last) : len;
-    return max(0, (seen + KEYS - 1) / KEYS);
-  };
-  const int tiles0 = tiles_of(0), tiles1 = tiles_of(1), nt = max(tiles0, tiles1);
-  const bool ragged = nt * KEYS > len;  // the last tile of keys ends behind the sequence
   tc_fence_before();
   __syncthreads();
   cluster_arrive();  // the other CTA's barriers exist
   cluster_wait();
   tc_fence_after();
   const uint32_t tmem = tmem_holder;
+  const int nb = p.nope / 64;
   volatile int* stop = &abort_flag;
   auto wait = [&](uint64_t* bar, int phase) {
     return mbar_wait(bar, phase & 1, stop, p.err, p.timeout);
   };
   auto first = [&](uint64_t* bar) { return map_to_rank(smem_u32(bar), 0); };  // in the first CTA
+  // the pair's unit number i, read by every role; false: there is none, or a wait ran out
+  auto next_unit = [&](int i, Unit& u) {
+    if (!wait(&bars.unit_full[i & 1], i >> 1)) return false;
+    u = units[i & 1];
+    return u.last == 0;
+  };
+  auto unit_read = [&](int i) { mbar_arrive(&bars.unit_empty[i & 1]); };
 
-  if (warp == 0) {
+  if (warp == 3) {
+    // ------------------------------------------------ units
+    // The next one is asked for when this one's copies are issued, not earlier: other pairs may be
+    // free first.  Numbers without tiles and queries are passed over.
+    Unit u = find_unit(p, blockIdx.x >> 1, blockIdx.y);
+    bool ok = true, more = true;
+    for (int i = 0, k = 0; more; ++i) {  // units; answers
+      if (i > 0) ok = wait(&bars.loaded, i - 1);
+      while (ok && more && (i > 0 || u.n == 0)) {
+        uint64_t* bar = &bars.next_full[k & 1];
+        if (rank == 0 && k > 0) ok = wait(&bars.next_read, k - 1);
+        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar, 16);
+          if (rank == 0) ask_next(&answers[k & 1], bar);
+        }
+        __syncwarp();
+        ok = __all_sync(0xFFFFFFFFu, wait(bar, k >> 1));
+        if (!ok) break;
+        int x, y;
+        more = read_next(&answers[k & 1], x, y);
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (rank == 1 && lane == 0) mbar_arrive_cluster_release(first(&bars.next_read));
+        ++k;
+        if (more) {
+          u = find_unit(p, x >> 1, y);
+          if (u.n > 0) break;
+        }
+      }
+      ok = __all_sync(0xFFFFFFFFu, ok && wait(&bars.unit_empty[i & 1], (i >> 1) + 1));
+      if (!ok) break;
+      u.last = !more;
+      if (lane == 0) {
+        units[i & 1] = u;
+        mbar_arrive(&bars.unit_full[i & 1]);
+      }
+      __syncwarp();
+    }
+  } else if (warp == 0) {
     if (elect_one()) {
       // ---------------------------------------------- copies
-      for (int w = 0; w < 2; ++w)
-        if ((w ? tiles1 : tiles0) > 0) {
-          if (rank == 0) mbar_arrive_expect_tx(&bars.q_full[w], 2 * (nb + 1) * BOX);
-          for (int i = 0; i <= nb; ++i)
-            tma_load_3d_pair(qs + (w * Q_BOXES + i) * BOX, &qmap, first(&bars.q_full[w]), i * 64, h,
-                             q0 + r0 + (2 * w + rank) * ROWS);
-        }
-      int it = 0;  // keys of tile it / 2, then its values
+      int nq[2] = {0, 0};  // tiles of queries so far
+      int g = 0, nl = 0;   // tiles of keys; ragged ones
+      int it = 0;          // keys of tile it / 2, then its values
       bool ok = true;
-      const int loads = 2 * (p.stall > 0 ? min(nt, p.stall) : nt);
-      const int last = ragged ? 2 * nt - 1 : -1;
-      for (; it < loads; ++it) {
-        const int t = it >> 1, st = t % STAGES, row = k0 + t * KEYS;
-        uint8_t* dst = ring + st * STAGE;
-        if (!(it & 1)) {
-          ok = wait(&bars.k_empty[st], t / STAGES + 1);
+      Unit u;
+      for (int i = 0; ok && next_unit(i, u); ++i) {
+        unit_read(i);
+        const int nt = max(u.tiles0, u.tiles1);
+        const bool ragged = nt * KEYS > u.len;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          if ((w ? u.tiles1 : u.tiles0) <= 0 || !ok) continue;
+          ok = wait(&bars.q_empty[w], nq[w] + 1);
+          if (!ok) break;
+          ++nq[w];
+          if (rank == 0) mbar_arrive_expect_tx(&bars.q_full[w], 2 * (nb + 1) * BOX);
+          for (int c = 0; c <= nb; ++c)
+            tma_load_3d_pair(qs + (w * Q_BOXES + c) * BOX, &qmap, first(&bars.q_full[w]), c * 64,
+                             u.h, u.q0 + u.r0 + (2 * w + rank) * ROWS);
+        }
+        for (int t = 0; t < nt && ok; ++t, ++g) {
+          if (p.stall > 0 && g >= p.stall) ok = false;
+          if (!ok) break;
+          const int st = g % STAGES, row = u.k0 + t * KEYS;
+          uint8_t* dst = ring + st * STAGE;
+          ok = wait(&bars.k_empty[st], g / STAGES + 1);
           if (!ok) break;
           if (rank == 0) mbar_arrive_expect_tx(&bars.k_full[st], (nb + 1) * BOX);
           const uint32_t bar = first(&bars.k_full[st]);
-          for (int i = 0; i < nb; ++i)
-            tma_load_3d_pair(dst + i * (BOX / 2), &kmap, bar, i * 64, h, row + rank * (KEYS / 2));
+          for (int c = 0; c < nb; ++c)
+            tma_load_3d_pair(dst + c * (BOX / 2), &kmap, bar, c * 64, u.h, row + rank * (KEYS / 2));
           tma_load_3d_pair(dst + nb * (BOX / 2), &rmap, bar, 0, 0, row + rank * (KEYS / 2));
-        } else {
-          ok = wait(&bars.v_empty[st], t / STAGES + 1);
+          ++it;
+          ok = wait(&bars.v_empty[st], g / STAGES + 1);
           if (!ok) break;
-          if (it == last) {
+          if (ragged && t == nt - 1) {
+            ++nl;
             mbar_arrive_expect_tx(&bars.v_last, BOX);
-            tma_load_3d(dst + K_BYTES, &vmap, &bars.v_last, rank * 64, h, row);
+            tma_load_3d(dst + K_BYTES, &vmap, &bars.v_last, rank * 64, u.h, row);
+            if (rank == 0) mbar_arrive(&bars.v_full[st]);  // a phase without bytes
           } else {
             if (rank == 0) mbar_arrive_expect_tx(&bars.v_full[st], 2 * BOX);
-            tma_load_3d_pair(dst + K_BYTES, &vmap, first(&bars.v_full[st]), rank * 64, h, row);
+            tma_load_3d_pair(dst + K_BYTES, &vmap, first(&bars.v_full[st]), rank * 64, u.h, row);
           }
+          ++it;
         }
+        mbar_arrive(&bars.loaded);
       }
       // No copy of the pair is in flight past this point.  The first CTA waits for all, those too
       // that the second has issued beyond its own after a wait that ran out.
       int none = 0;
-      if (last >= 0 && it > last) mbar_wait(&bars.v_last, 0, &none, p.err, p.timeout);
+      if (nl > 0) mbar_wait(&bars.v_last, (nl - 1) & 1, &none, p.err, p.timeout);
       auto landed = [&](int j) {
         const int t = j >> 1;
-        if (j != last)
-          mbar_wait(j & 1 ? &bars.v_full[t % STAGES] : &bars.k_full[t % STAGES], (t / STAGES) & 1,
-                    &none, p.err, p.timeout);
+        mbar_wait(j & 1 ? &bars.v_full[t % STAGES] : &bars.k_full[t % STAGES], (t / STAGES) & 1,
+                  &none, p.err, p.timeout);
       };
       if (rank == 0) {
+#pragma unroll
         for (int w = 0; w < 2; ++w)
-          if ((w ? tiles1 : tiles0) > 0)
-            mbar_wait(&bars.q_full[w], 0, &none, p.err, p.timeout);
+          if (nq[w] > 0) mbar_wait(&bars.q_full[w], (nq[w] - 1) & 1, &none, p.err, p.timeout);
         for (int j = max(0, it - 2 * STAGES); j < it; ++j) landed(j);
         // its waits are bounded and began before this CTA's last ones ended
         if (mbar_wait(&bars.ended, 0, &none, p.err, 3 * p.timeout)) {
           const int others = static_cast<int>(*static_cast<volatile uint32_t*>(&copies));
           for (; it < others; ++it) {
             const int t = it >> 1;
-            if (it == last) continue;
             if (it & 1)
               mbar_arrive_expect_tx(&bars.v_full[t % STAGES], BOX);
             else
@@ -262,10 +375,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       constexpr uint32_t sdesc = idesc_make(1, 256, 128);
       constexpr uint32_t vdesc = idesc_make(1, 256, 128) | IDESC_B_MN;
       bool ok = true;
+      int g = 0, nl = 0;         // tiles of keys before this unit; ragged units
+      int nq0 = 0, nq1 = 0;      // tiles of queries
+      int n0 = 0, n1 = 0;        // their tiles of keys
       // of tile t of keys with tile w of queries; the last user hands the stage back
-      auto scores = [&](int w, int t, bool wanted, bool last) {
-        const int st = t % STAGES;
-        if (wanted) ok = wait(&bars.k_full[st], t / STAGES);
+      auto scores = [&](int w, int t, bool wanted, bool last, bool q_last) {
+        const int st = (g + t) % STAGES;
+        if (wanted) ok = wait(&bars.k_full[st], (g + t) / STAGES);
         if (!ok) return;
         tc_fence_after();
         const uint64_t qa = sdesc_sw128(smem_u32(qs + w * Q_BOXES * BOX)),
@@ -280,12 +396,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           for (int s = 0; s < p.rope / 16; ++s) mma_pair(d, qr + 2 * s, kr + 2 * s, sdesc);
         tc_commit_pair(&bars.s_full[w], 3);
         if (last) tc_commit_pair(&bars.k_empty[st], 3);
+        if (q_last) tc_commit_pair(&bars.q_empty[w], 3);
       };
-      auto values = [&](int w, int t, bool wanted, bool last) {
-        const int st = t % STAGES;
+      auto values = [&](int w, int t, int tiles_before, int q_before, bool wanted, bool last,
+                        bool tail) {
+        const int st = (g + t) % STAGES;
         if (wanted)
-          ok = ragged && t == nt - 1 ? wait(&bars.cleared, 0) : wait(&bars.v_full[st], t / STAGES);
-        ok = ok && wait(&bars.p_full[w], t);
+          ok = wait(&bars.v_full[st], (g + t) / STAGES) && (!tail || wait(&bars.cleared, nl));
+        ok = ok && wait(&bars.p_full[w], tiles_before + t) &&
+             (t > 0 || wait(&bars.o_free[w], q_before + 1));
         if (!ok) return;
         tc_fence_after();
         const uint64_t va = sdesc_sw128_mn(smem_u32(ring + st * STAGE + K_BYTES), BOX);
@@ -295,161 +414,189 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         tc_commit_pair(&bars.pv_done[w], 3);
         if (last) tc_commit_pair(&bars.v_empty[st], 3);
       };
-      if (tiles0 > 0) {
-        ok = wait(&bars.q_full[0], 0);
-        if (ok) scores(0, 0, true, tiles1 <= 0);
-      }
-      if (tiles1 > 0 && ok) {
-        ok = wait(&bars.q_full[1], 0);
-        if (ok) scores(1, 0, tiles0 <= 0, true);
-      }
-      for (int t = 0; t < nt && ok; ++t) {
-        if (t < tiles0) values(0, t, true, t >= tiles1);
-        if (ok && t + 1 < tiles0) scores(0, t + 1, true, t + 1 >= tiles1);
-        if (ok && t < tiles1) values(1, t, t >= tiles0, true);
-        if (ok && t + 1 < tiles1) scores(1, t + 1, t + 1 >= tiles0, true);
+      Unit u;
+      for (int i = 0; ok && next_unit(i, u); ++i) {
+        unit_read(i);
+        const int t0 = u.tiles0, t1 = u.tiles1, nt = max(t0, t1);
+        const bool ragged_last = nt * KEYS > u.len;
+        if (t0 > 0) {
+          ok = wait(&bars.q_full[0], nq0);
+          if (ok) scores(0, 0, true, t1 <= 0, t0 == 1);
+        }
+        if (t1 > 0 && ok) {
+          ok = wait(&bars.q_full[1], nq1);
+          if (ok) scores(1, 0, t0 <= 0, true, t1 == 1);
+        }
+        for (int t = 0; t < nt && ok; ++t) {
+          const bool tail = ragged_last && t == nt - 1;
+          if (t < t0) values(0, t, n0, nq0, true, t >= t1, tail);
+          if (ok && t + 1 < t0) scores(0, t + 1, true, t + 1 >= t1, t + 2 == t0);
+          if (ok && t < t1) values(1, t, n1, nq1, t >= t0, true, tail);
+          if (ok && t + 1 < t1) scores(1, t + 1, t + 1 >= t0, true, t + 2 == t1);
+        }
+        g += nt;
+        nl += ragged_last && nt > 0;
+        nq0 += t0 > 0;
+        nq1 += t1 > 0;
+        n0 += t0;
+        n1 += t1;
       }
       tc_commit_pair(&bars.drain, 3);  // no product of the pair runs past this point
     }
   } else if (warp >= 4) {
     // ------------------------------------------------ softmax: a row per thread
     const int w = (warp - 4) >> 2, quad = warp & 3;
-    const int row = r0 + (2 * w + rank) * ROWS + quad * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t S = tmem + w * 128 + lanes, O = tmem + 256 + w * 128 + lanes;
-    const int limit = row >= n ? 0 : p.causal ? len - (n - 1 - row) : len;
-    float m = -INFINITY, l = 0.f;
+    const uint32_t p_full = first(&bars.p_full[w]), o_free = first(&bars.o_free[w]);
+    int g = 0, nl = 0;  // tiles of keys before this unit; ragged units
+    int done = 0;       // tiles of keys of this tile of queries before this unit
     bool ok = true;
-    const int mine = w ? tiles1 : tiles0;
-    const uint32_t p_full = first(&bars.p_full[w]);
-    for (int t = 0; t < mine; ++t) {
-      ok = wait(&bars.s_full[w], t);
+    Unit u;
+    for (int i = 0;; ++i) {
+      ok = __all_sync(0xFFFFFFFFu, ok && next_unit(i, u));
+      if (!ok) break;
+      const int nt = max(u.tiles0, u.tiles1), mine = w ? u.tiles1 : u.tiles0;
+      const bool ragged = nt > 0 && nt * KEYS > u.len;
+      const int row = u.r0 + (2 * w + rank) * ROWS + quad * 32 + lane;
+      const int limit = row >= u.n ? 0 : p.causal ? u.len - (u.n - 1 - row) : u.len;
+      float m = -INFINITY, l = 0.f;
+      for (int t = 0; t < mine; ++t) {
+        ok = wait(&bars.s_full[w], done + t);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        if (ragged && t == nt - 1 && (w == 1 || u.tiles1 < nt)) {
+          // what the values hold behind the sequence is cleared: it may not be finite
+          ok = wait(&bars.v_last, nl);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+          uint8_t* vs = ring + ((g + t) % STAGES) * STAGE + K_BYTES;
+          for (int c = (u.len - t * KEYS) * 8 + quad * 32 + lane; c < KEYS * 8; c += 128)
+            *reinterpret_cast<uint4*>(vs + c * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster_release(first(&bars.cleared));
+        }
+        float top = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < KEYS; c += 64) {
+          uint32_t v[2][32];
+          load64(S + c, limit - t * KEYS - c, v);
+          float x[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            x[k] = __uint_as_float(v[k >> 1][(k & 1) * 16]);
+#pragma unroll
+            for (int j = 1; j < 15; j += 2)
+              x[k] = fmaxf(fmaxf(x[k], __uint_as_float(v[k >> 1][(k & 1) * 16 + j])),
+                           __uint_as_float(v[k >> 1][(k & 1) * 16 + j + 1]));
+            x[k] = fmaxf(x[k], __uint_as_float(v[k >> 1][(k & 1) * 16 + 15]));
+          }
+          top = fmaxf(fmaxf(top, fmaxf(x[0], x[1])), fmaxf(x[2], x[3]));
+        }
+        top *= p.scale;
+        // the maximum in use may lag by 8: weights stay below 2^8
+        if (__any_sync(0xFFFFFFFFu, top > m + 8.f)) {
+          const float now = fmaxf(m, top);
+          const float f = now == -INFINITY ? 1.f : exp2_fast(m - now);
+          m = now;
+          l *= f;
+          if (t > 0) {  // the row's last product has to be done
+            ok = wait(&bars.pv_done[w], done + t - 1);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < p.value; c += 16) {
+              float o[16];
+              tmem_ld16(O + c, o);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) o[k] *= f;
+              tmem_st16(O + c, o);
+            }
+          }
+        }
+        const float base = m == -INFINITY ? 0.f : m;
+        const unsigned long long s2 = pack2(p.scale, p.scale), b2 = pack2(-base, -base);
+        unsigned long long sum[2] = {0ull, 0ull};
+#pragma unroll 1
+        for (int c = 0; c < KEYS; c += 64) {
+          uint32_t v[2][32], pk[32];
+          load64(S + c, limit - t * KEYS - c, v);
+#pragma unroll
+          for (int k = 0; k < 64; k += 2) {
+            float a, b;
+            unpack2(fmaf2(pack2(__uint_as_float(v[k >> 5][k & 31]),
+                                __uint_as_float(v[k >> 5][(k & 31) + 1])),
+                          s2, b2),
+                    a, b);
+            a = exp2_fast(a);
+            b = exp2_fast(b);
+            add2(sum[k >> 1 & 1], pack2(a, b));
+            pk[k / 2] = pack_bf16(a, b);
+          }
+          tmem_st32(S + c / 2, pk);  // over columns that have been read
+        }
+        add2(sum[0], sum[1]);
+        float a, b;
+        unpack2(sum[0], a, b);
+        l += a + b;
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(p_full);
+      }
+      if (ok && mine > 0) ok = wait(&bars.pv_done[w], done + mine - 1);
       ok = __all_sync(0xFFFFFFFFu, ok);
       if (!ok) break;
       tc_fence_after();
-      if (ragged && t == nt - 1 && (w == 1 || tiles1 < nt)) {
-        // what the values hold behind the sequence is cleared: it may not be finite
-        ok = wait(&bars.v_last, 0);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
-        uint8_t* vs = ring + (t % STAGES) * STAGE + K_BYTES;
-        for (int c = (len - t * KEYS) * 8 + quad * 32 + lane; c < KEYS * 8; c += 128)
-          *reinterpret_cast<uint4*>(vs + c * 16) = make_uint4(0, 0, 0, 0);
-        fence_proxy_async_shared();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster_release(first(&bars.cleared));
-      }
-      float top = -INFINITY;
+      if (row - lane < u.n) {
+        const float f = l != 0.f ? 1.0f / l : 0.f;
+        if (p.lse && row < u.n)
+          p.lse[static_cast<int64_t>(u.q0 + row) * p.H + u.h] =
+              l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+        // 16 columns at a time; neighbouring lanes swap halves, so that a pair of them stores 32
+        // bytes of a row
+        __nv_bfloat16* dst = p.out + static_cast<int64_t>(u.q0 + row - (lane & 1)) * p.out_token +
+                             static_cast<int64_t>(u.h) * p.out_head + (lane & 1) * 8;
+        const bool there0 = row - (lane & 1) < u.n, there1 = row - (lane & 1) + 1 < u.n;
 #pragma unroll 1
-      for (int c = 0; c < KEYS; c += 64) {
-        uint32_t v[2][32];
-        load64(S + c, limit - t * KEYS - c, v);
-        float x[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[i] = __uint_as_float(v[i >> 1][(i & 1) * 16]);
-#pragma unroll
-          for (int j = 1; j < 15; j += 2)
-            x[i] = fmaxf(fmaxf(x[i], __uint_as_float(v[i >> 1][(i & 1) * 16 + j])),
-                         __uint_as_float(v[i >> 1][(i & 1) * 16 + j + 1]));
-          x[i] = fmaxf(x[i], __uint_as_float(v[i >> 1][(i & 1) * 16 + 15]));
-        }
-        top = fmaxf(fmaxf(top, fmaxf(x[0], x[1])), fmaxf(x[2], x[3]));
-      }
-      top *= p.scale;
-      // the maximum in use may lag by 8: weights stay below 2^8
-      if (__any_sync(0xFFFFFFFFu, top > m + 8.f)) {
-        const float now = fmaxf(m, top);
-        const float f = now == -INFINITY ? 1.f : exp2_fast(m - now);
-        m = now;
-        l *= f;
-        if (t > 0) {  // the row's last product has to be done
-          ok = wait(&bars.pv_done[w], t - 1);
-          ok = __all_sync(0xFFFFFFFFu, ok);
-          if (!ok) break;
-          tc_fence_after();
-#pragma unroll 1
-          for (int c = 0; c < p.value; c += 16) {
-            float o[16];
+        for (int c = 0; c < p.value; c += 16) {
+          float o[16];
+          if (mine > 0) {
             tmem_ld16(O + c, o);
+          } else {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] *= f;
-            tmem_st16(O + c, o);
+            for (int k = 0; k < 16; ++k) o[k] = 0.f;
           }
+          uint32_t x[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            x[k] = f == 0.f ? 0u : pack_bf16(o[2 * k] * f, o[2 * k + 1] * f);
+          uint32_t y[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            y[k] = __shfl_xor_sync(0xFFFFFFFFu, lane & 1 ? x[k] : x[k + 4], 1);
+          // the even lane's row: its first half from itself, its second goes to the odd lane
+          if (there0)
+            *reinterpret_cast<uint4*>(dst + c) = lane & 1 ? make_uint4(y[0], y[1], y[2], y[3])
+                                                          : make_uint4(x[0], x[1], x[2], x[3]);
+          if (there1)
+            *reinterpret_cast<uint4*>(dst + p.out_token + c) =
+                lane & 1 ? make_uint4(x[4], x[5], x[6], x[7]) : make_uint4(y[0], y[1], y[2], y[3]);
         }
       }
-      const float base = m == -INFINITY ? 0.f : m;
-      const unsigned long long s2 = pack2(p.scale, p.scale), b2 = pack2(-base, -base);
-      unsigned long long sum[2] = {0ull, 0ull};
-#pragma unroll 1
-      for (int c = 0; c < KEYS; c += 64) {
-        uint32_t v[2][32], pk[32];
-        load64(S + c, limit - t * KEYS - c, v);
-#pragma unroll
-        for (int i = 0; i < 64; i += 2) {
-          float a, b;
-          unpack2(fmaf2(pack2(__uint_as_float(v[i >> 5][i & 31]),
-                              __uint_as_float(v[i >> 5][(i & 31) + 1])),
-                        s2, b2),
-                  a, b);
-          a = exp2_fast(a);
-          b = exp2_fast(b);
-          add2(sum[i >> 1 & 1], pack2(a, b));
-          pk[i / 2] = pack_bf16(a, b);
-        }
-        tmem_st32(S + c / 2, pk);  // over columns that have been read
-      }
-      add2(sum[0], sum[1]);
-      float a, b;
-      unpack2(sum[0], a, b);
-      l += a + b;
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(p_full);
-    }
-    if (ok && mine > 0) ok = wait(&bars.pv_done[w], mine - 1);
-    ok = __all_sync(0xFFFFFFFFu, ok);
-    const int from = row - lane;  // this warp's first row
-    if (ok && from < n) {
-      tc_fence_after();
-      const float f = l != 0.f ? 1.0f / l : 0.f;
-      if (p.lse && row < n)
-        p.lse[static_cast<int64_t>(q0 + row) * p.H + h] =
-            l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-      // through this warp's part of the queries' memory, which no product reads any more, so that
-      // whole rows are stored: 16 bytes at chunk c ^ row of a row
-      const int chunks = p.value / 8;
-      uint8_t* stage = qs + (w * Q_BOXES * BOX) + quad * 32 * 256;
-#pragma unroll 1
-      for (int c = 0; c < p.value; c += 32) {
-        uint32_t o[32];
-        if (mine > 0) {
-          tmem_start_ld32(O + c, o);
-          tmem_wait_ld32(o);
-        }
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (mine == 0 || f == 0.f) o[i] = 0;
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          uint32_t x[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            x[i] = pack_bf16(__uint_as_float(o[8 * g + 2 * i]) * f,
-                             __uint_as_float(o[8 * g + 2 * i + 1]) * f);
-          *reinterpret_cast<uint4*>(stage + lane * 256 + (((c / 8 + g) ^ (lane & 7)) << 4)) =
-              make_uint4(x[0], x[1], x[2], x[3]);
-        }
+      if (mine > 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(o_free);
       }
       __syncwarp();
-      for (int i = lane; i < 32 * chunks; i += 32) {
-        const int r = i / chunks, c = i % chunks;
-        if (from + r < n)
-          *reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(q0 + from + r) * p.out_token +
-                                    h * p.out_head + c * 8) =
-              *reinterpret_cast<const uint4*>(stage + r * 256 + ((c ^ (r & 7)) << 4));
-      }
+      if (lane == 0) unit_read(i);
+      g += nt;
+      nl += ragged;
+      done += mine;
     }
   }
   tc_fence_before();
