@@ -47,8 +47,9 @@ struct Bars {
   uint64_t k_empty[STAGES], v_empty[STAGES];  // each
   uint64_t q_full[2], q_empty[2];             // q_empty: each
   uint64_t s_full[2], pv_done[2];             // each
-  uint64_t p_full[2], o_free[2];              // the softmax warps of both
-  uint64_t v_last;                            // each: values of a sequence's ragged last tile
+  uint64_t p_half[2], p_full[2], o_free[2];   // the softmax warps of both
+  uint64_t pv_half[2];                        // each: products with the first half of a tile
+  uint64_t v_last[STAGES];                    // each: values of a sequence's ragged last tile
   uint64_t cleared;                           // ... cleared behind the sequence in both
   uint64_t unit_full[2], unit_empty[2];       // each
   uint64_t loaded;                            // each: a unit's copies are issued
@@ -180,6 +181,27 @@ KLT_DEV void load64(uint32_t taddr, int seen, uint32_t (*v)[32]) {
   }
 }
 
+// The weights of 64 scores, 2^(s scale - m), as bf16, and their sums (to be added up); returns the
+// largest of s scale.
+KLT_DEV float weights64(const uint32_t (*v)[32], float scale, float m, unsigned long long* sum,
+                        uint32_t* out) {
+  const float base = m == -INFINITY ? 0.f : m;
+  const unsigned long long s2 = pack2(scale, scale), b2 = pack2(-base, -base);
+  sum[0] = sum[1] = 0ull;
+  float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int k = 0; k < 64; k += 2) {
+    float a = __uint_as_float(v[k >> 5][k & 31]), b = __uint_as_float(v[k >> 5][(k & 31) + 1]);
+    top[k >> 1 & 3] = fmaxf(fmaxf(top[k >> 1 & 3], a), b);
+    unpack2(fmaf2(pack2(a, b), s2, b2), a, b);
+    a = exp2_fast(a);
+    b = exp2_fast(b);
+    add2(sum[k >> 1 & 1], pack2(a, b));
+    out[k / 2] = pack_bf16(a, b);
+  }
+  return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
+}
+
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap,
@@ -200,11 +222,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       mbar_init(&bars.v_full[i], 1);
       mbar_init(&bars.k_empty[i], 1);
       mbar_init(&bars.v_empty[i], 1);
+      mbar_init(&bars.v_last[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.q_full[i], 1);
       mbar_init(&bars.q_empty[i], 1);
       mbar_init(&bars.s_full[i], 1);
+      mbar_init(&bars.p_half[i], 8);
+      mbar_init(&bars.pv_half[i], 1);
       mbar_init(&bars.p_full[i], 8);
       mbar_init(&bars.o_free[i], 8);
       mbar_init(&bars.pv_done[i], 1);
@@ -214,7 +239,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
     mbar_init(&bars.loaded, 1);
     mbar_init(&bars.next_read, 1);
-    mbar_init(&bars.v_last, 1);
     mbar_init(&bars.cleared, 8);
     mbar_init(&bars.drain, 1);
     mbar_init(&bars.ended, 1);
@@ -239,6 +263,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   volatile int* stop = &abort_flag;
   auto wait = [&](uint64_t* bar, int phase) {
     return mbar_wait(bar, phase & 1, stop, p.err, p.timeout);
+  };
+  auto wait_spin = [&](uint64_t* bar, int phase) {
+    return mbar_wait_spin(bar, phase & 1, stop, p.err, p.timeout);
   };
   auto first = [&](uint64_t* bar) { return map_to_rank(smem_u32(bar), 0); };  // in the first CTA
   // the pair's unit number i, read by every role; false: there is none, or a wait ran out
@@ -292,8 +319,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     if (elect_one()) {
       // ---------------------------------------------- copies
       int nq[2] = {0, 0};  // tiles of queries so far
-      int g = 0, nl = 0;   // tiles of keys; ragged ones
+      int g = 0;           // tiles of keys
       int it = 0;          // keys of tile it / 2, then its values
+      uint32_t lasts = 0, odd = 0;  // stages that have had a ragged last tile; an odd number of them
       bool ok = true;
       Unit u;
       for (int i = 0; ok && next_unit(i, u); ++i) {
@@ -327,9 +355,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           ok = wait(&bars.v_empty[st], g / STAGES + 1);
           if (!ok) break;
           if (ragged && t == nt - 1) {
-            ++nl;
-            mbar_arrive_expect_tx(&bars.v_last, BOX);
-            tma_load_3d(dst + K_BYTES, &vmap, &bars.v_last, rank * 64, u.h, row);
+            lasts |= 1u << st;
+            odd ^= 1u << st;
+            mbar_arrive_expect_tx(&bars.v_last[st], BOX);
+            tma_load_3d(dst + K_BYTES, &vmap, &bars.v_last[st], rank * 64, u.h, row);
             if (rank == 0) mbar_arrive(&bars.v_full[st]);  // a phase without bytes
           } else {
             if (rank == 0) mbar_arrive_expect_tx(&bars.v_full[st], 2 * BOX);
@@ -342,7 +371,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       // No copy of the pair is in flight past this point.  The first CTA waits for all, those too
       // that the second has issued beyond its own after a wait that ran out.
       int none = 0;
-      if (nl > 0) mbar_wait(&bars.v_last, (nl - 1) & 1, &none, p.err, p.timeout);
+      for (int st = 0; st < STAGES; ++st)
+        if (lasts >> st & 1)
+          mbar_wait(&bars.v_last[st], (odd >> st & 1) ^ 1, &none, p.err, p.timeout);
       auto landed = [&](int j) {
         const int t = j >> 1;
         mbar_wait(j & 1 ? &bars.v_full[t % STAGES] : &bars.k_full[t % STAGES], (t / STAGES) & 1,
@@ -403,13 +434,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const int st = (g + t) % STAGES;
         if (wanted)
           ok = wait(&bars.v_full[st], (g + t) / STAGES) && (!tail || wait(&bars.cleared, nl));
-        ok = ok && wait(&bars.p_full[w], tiles_before + t) &&
+        ok = ok && wait_spin(&bars.p_half[w], tiles_before + t) &&
              (t > 0 || wait(&bars.o_free[w], q_before + 1));
         if (!ok) return;
         tc_fence_after();
         const uint64_t va = sdesc_sw128_mn(smem_u32(ring + st * STAGE + K_BYTES), BOX);
         const uint32_t d = tmem + 256 + w * 128, a = tmem + w * 128;
         mma4_pair_ta(d, a, va, vdesc, t);
+        tc_commit_pair(&bars.pv_half[w], 3);
+        ok = wait_spin(&bars.p_full[w], tiles_before + t);
+        if (!ok) return;
+        tc_fence_after();
         mma4_pair_ta(d, a + 32, va + 512, vdesc, 1);
         tc_commit_pair(&bars.pv_done[w], 3);
         if (last) tc_commit_pair(&bars.v_empty[st], 3);
@@ -448,8 +483,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const int w = (warp - 4) >> 2, quad = warp & 3;
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t S = tmem + w * 128 + lanes, O = tmem + 256 + w * 128 + lanes;
-    const uint32_t p_full = first(&bars.p_full[w]), o_free = first(&bars.o_free[w]);
-    int g = 0, nl = 0;  // tiles of keys before this unit; ragged units
+    const uint32_t p_half = first(&bars.p_half[w]), p_full = first(&bars.p_full[w]),
+                   o_free = first(&bars.o_free[w]);
+    int g = 0;          // tiles of keys before this unit
+    uint32_t odd = 0;   // stages that have had an odd number of ragged last tiles
     int done = 0;       // tiles of keys of this tile of queries before this unit
     bool ok = true;
     Unit u;
@@ -462,90 +499,68 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const int limit = row >= u.n ? 0 : p.causal ? u.len - (u.n - 1 - row) : u.len;
       float m = -INFINITY, l = 0.f;
       for (int t = 0; t < mine; ++t) {
-        ok = wait(&bars.s_full[w], done + t);
+        ok = wait_spin(&bars.s_full[w], done + t);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
         tc_fence_after();
         if (ragged && t == nt - 1 && (w == 1 || u.tiles1 < nt)) {
           // what the values hold behind the sequence is cleared: it may not be finite
-          ok = wait(&bars.v_last, nl);
+          const int st = (g + t) % STAGES;
+          ok = wait(&bars.v_last[st], odd >> st & 1);
           ok = __all_sync(0xFFFFFFFFu, ok);
           if (!ok) break;
-          uint8_t* vs = ring + ((g + t) % STAGES) * STAGE + K_BYTES;
+          uint8_t* vs = ring + st * STAGE + K_BYTES;
           for (int c = (u.len - t * KEYS) * 8 + quad * 32 + lane; c < KEYS * 8; c += 128)
             *reinterpret_cast<uint4*>(vs + c * 16) = make_uint4(0, 0, 0, 0);
           fence_proxy_async_shared();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster_release(first(&bars.cleared));
         }
-        float top = -INFINITY;
-#pragma unroll 1
-        for (int c = 0; c < KEYS; c += 64) {
-          uint32_t v[2][32];
-          load64(S + c, limit - t * KEYS - c, v);
-          float x[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            x[k] = __uint_as_float(v[k >> 1][(k & 1) * 16]);
-#pragma unroll
-            for (int j = 1; j < 15; j += 2)
-              x[k] = fmaxf(fmaxf(x[k], __uint_as_float(v[k >> 1][(k & 1) * 16 + j])),
-                           __uint_as_float(v[k >> 1][(k & 1) * 16 + j + 1]));
-            x[k] = fmaxf(x[k], __uint_as_float(v[k >> 1][(k & 1) * 16 + 15]));
-          }
-          top = fmaxf(fmaxf(top, fmaxf(x[0], x[1])), fmaxf(x[2], x[3]));
-        }
-        top *= p.scale;
-        // the maximum in use may lag by 8: weights stay below 2^8
-        if (__any_sync(0xFFFFFFFFu, top > m + 8.f)) {
-          const float now = fmaxf(m, top);
-          const float f = now == -INFINITY ? 1.f : exp2_fast(m - now);
-          m = now;
-          l *= f;
-          if (t > 0) {  // the row's last product has to be done
-            ok = wait(&bars.pv_done[w], done + t - 1);
-            ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < p.value; c += 16) {
-              float o[16];
-              tmem_ld16(O + c, o);
-#pragma unroll
-              for (int k = 0; k < 16; ++k) o[k] *= f;
-              tmem_st16(O + c, o);
-            }
-          }
-        }
-        const float base = m == -INFINITY ? 0.f : m;
-        const unsigned long long s2 = pack2(p.scale, p.scale), b2 = pack2(-base, -base);
-        unsigned long long sum[2] = {0ull, 0ull};
+        // 64 keys at a time, weighted by the maximum in use while their own is found; it may lag by
+        // 8, so weights stay below 2^8.  Where it lags by more O and the sum are rescaled and the
+        // weights computed once more, from scores that are still in registers.
 #pragma unroll 1
         for (int c = 0; c < KEYS; c += 64) {
           uint32_t v[2][32], pk[32];
           load64(S + c, limit - t * KEYS - c, v);
+          float a, b;
+          unsigned long long sum[2];
+          float top = weights64(v, p.scale, m, sum, pk);
+          if (__any_sync(0xFFFFFFFFu, top > m + 8.f)) {
+            const float now = fmaxf(m, top);
+            const float f = now == -INFINITY ? 1.f : exp2_fast(m - now);
+            m = now;
+            l *= f;
+            // O holds what came before; the products of the tile before are done (these scores
+            // were issued behind them), those of this tile's first half may not be
+            if (c > 0) {
+              ok = wait(&bars.pv_half[w], done + t);
+              ok = __all_sync(0xFFFFFFFFu, ok);
+              if (!ok) break;
+              tc_fence_after();
+            }
+            if (t > 0 || c > 0) {
+#pragma unroll 1
+              for (int o = 0; o < p.value; o += 16) {
+                float x[16];
+                tmem_ld16(O + o, x);
 #pragma unroll
-          for (int k = 0; k < 64; k += 2) {
-            float a, b;
-            unpack2(fmaf2(pack2(__uint_as_float(v[k >> 5][k & 31]),
-                                __uint_as_float(v[k >> 5][(k & 31) + 1])),
-                          s2, b2),
-                    a, b);
-            a = exp2_fast(a);
-            b = exp2_fast(b);
-            add2(sum[k >> 1 & 1], pack2(a, b));
-            pk[k / 2] = pack_bf16(a, b);
+                for (int k = 0; k < 16; ++k) x[k] *= f;
+                tmem_st16(O + o, x);
+              }
+            }
+            weights64(v, p.scale, m, sum, pk);
           }
+          add2(sum[0], sum[1]);
+          unpack2(sum[0], a, b);
+          l += a + b;
           tmem_st32(S + c / 2, pk);  // over columns that have been read
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(c == 0 ? p_half : p_full);
         }
-        add2(sum[0], sum[1]);
-        float a, b;
-        unpack2(sum[0], a, b);
-        l += a + b;
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(p_full);
+        if (!ok) break;
       }
       if (ok && mine > 0) ok = wait(&bars.pv_done[w], done + mine - 1);
       ok = __all_sync(0xFFFFFFFFu, ok);
@@ -595,7 +610,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       __syncwarp();
       if (lane == 0) unit_read(i);
       g += nt;
-      nl += ragged;
+      if (ragged) odd ^= 1u << ((g - 1) % STAGES);
       done += mine;
     }
   }

@@ -221,3 +221,11 @@ def test_prefill_sequences(heads, queries, keys, causal):
 @pytest.mark.parametrize("spread", [0.0, 8.0, 60.0])
 def test_prefill_score_ranges(spread):
     run_prefill(2, [260, 40], [300, 40], seed=9, spread=spread)
+
+
+def test_prefill_many_units():
+    """More units than pairs of CTAs, short and long ones, ragged ends in every stage of the ring:
+    a pair takes over many units, and its copies run ahead of its products."""
+    lens = [1, 700, 130, 40, 515, 129, 3, 260, 90, 1030, 5, 384]
+    run_prefill(40, lens, [n + 3 * i for i, n in enumerate(lens)], nope=64, rope=16, value=64,
+                seed=77)
