@@ -123,6 +123,20 @@ KLT_DEV void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int c
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
       : "memory");
 }
+// A value that all lanes of a converged warp share, in a form that the compiler knows to be so.
+template <typename T>
+KLT_DEV T uniform(T v) {
+  return static_cast<T>(__shfl_sync(0xFFFFFFFFu, static_cast<int>(v), 0));
+}
+// Four products of K = 16 whose A has its rows contiguous: 16 rows of K (2048 bytes) apart, B's 32
+// bytes.
+KLT_DEV void mma4_bf16_mn(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                          uint32_t accumulate) {
+  mma_bf16(d, a, b, idesc, accumulate);
+  mma_bf16(d, a + 128, b + 2, idesc, 1);
+  mma_bf16(d, a + 256, b + 4, idesc, 1);
+  mma_bf16(d, a + 384, b + 6, idesc, 1);
+}
 // Whether phase `phase` (its parity counts) of `bar` is complete.
 KLT_DEV bool mbar_test(uint64_t* bar, int phase) {
   uint32_t ok;

@@ -8,7 +8,7 @@
 //
 // Roles: warp 0 copies tiles (two stages of 72 KB in blocks of 128 columns, each handed back on
 // its own), warp 1 issues products (a tile's scores before the values of the tile before it),
-// warps 2 and 3 load the queries, warps 4 to 11 do the softmax (32 of a tile's keys each) and write
+// warp 2 loads the queries, warp 3 records what the parts are, warps 4 to 11 do the softmax (32 of a tile's keys each) and write
 // results.
 //
 // The work is cut evenly: with W tiles of keys over all (sequence, row tile) items, group g of G
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   __shared__ int found_b;
   __shared__ uint32_t tmem_holder;
   __shared__ int abort_flag;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
   if (tid == 0) {
     for (int s = 0; s < STAGES; ++s)
       for (int i = 0; i < 5; ++i) {
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     mbar_init(&bars.p_full, SOFTMAX / 32);
     mbar_init(&bars.pv_done, 1);
     mbar_init(&bars.o_free, SOFTMAX / 32);
-    mbar_init(&bars.q_full, p.q_box ? 1 : 64);
+    mbar_init(&bars.q_full, p.q_box ? 1 : 32);
     mbar_init(&bars.q_free, 1);
     mbar_init(&bars.drain, 1);
     abort_flag = 0;
@@ -345,113 +345,106 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------ products
-    if (elect_one()) {
-      int it = 0, piece = 0;  // tiles; pieces with rows and tiles
-      bool ok = true;
-      while (ok && walk.next(p, w)) {
-        if (w.rows == 0 || w.t0 == w.t1) continue;
-        const uint32_t pv = idesc_make(1, 128, (w.rows + 15) & ~15) | IDESC_A_MN;
-        const int nt = w.t1 - w.t0;
-        // Whichever is ready: the values of the oldest tile whose weights are written, else the next
-        // block of the next tile's scores.  In a fixed order (scores of tile t + 1 before the values
-        // of t) a stage was handed back only after the copy of the tile behind it, 2.7 us a tile.
-        int ts = 0, tv = 0, block = 0;  // next tile of scores and of values, next block of scores
-        const uint32_t qa = smem_u32(qs), pa = smem_u32(ps);
-        long long since = 0;
-        bool start = false;
-        while (tv < nt) {
-          if (tv < ts && mbar_test(&bars.p_full, it + tv) &&
-              (tv > 0 || mbar_test(&bars.o_free, piece + 1))) {
-            tc_fence_after();
-            const int st = (it + tv) % STAGES;
-            const uint32_t va = smem_u32(ks + st * MAX_BOXES * BOX);
-            for (int j = 0; j < NJ; ++j) {
-#pragma unroll
-              for (int s = 0; s < 4; ++s)
-                mma_bf16(tmem + j * 64, sdesc_sw128_mn(va + 2 * j * BOX + s * 2048, BOX),
-                         sdesc_sw128(pa) + 2 * s, pv, tv | s);
+    // The whole warp goes through the loop and one lane issues: so the compiler knows the loop to be
+    // uniform and keeps descriptors in uniform registers, where the products take them from (in one
+    // lane's branch a product took 64 cycles to issue, for 35 of work).
+    int it = 0, piece = 0;  // tiles; pieces with rows and tiles
+    const uint32_t base = uniform(tmem), qa = uniform(smem_u32(qs)), pa = uniform(smem_u32(ps)),
+                   k0 = uniform(smem_u32(ks));
+    auto test = [&](uint64_t* bar, int phase) {
+      return __all_sync(0xFFFFFFFFu, mbar_test(bar, phase)) != 0;
+    };
+    bool ok = true;
+    while (ok && uniform(walk.next(p, w))) {
+      const int nt = uniform(w.rows == 0 ? 0 : w.t1 - w.t0);
+      if (nt == 0) continue;
+      const uint32_t pv = idesc_make(1, 128, (uniform(w.rows) + 15) & ~15) | IDESC_A_MN;
+      // Whichever is ready: the values of the oldest tile whose weights are written, else the next
+      // block of the next tile's scores.  In a fixed order (scores of tile t + 1 before the values
+      // of t) a stage was handed back only after the copy of the tile behind it, 2.7 us a tile.
+      int ts = 0, tv = 0, block = 0;  // next tile of scores and of values, next block of scores
+      long long since = 0;
+      bool start = false;
+      while (tv < nt) {
+        if (tv < ts && test(&bars.p_full, it + tv) && (tv > 0 || test(&bars.o_free, piece + 1))) {
+          tc_fence_after();
+          const int st = (it + tv) % STAGES;
+          const uint64_t va = sdesc_sw128_mn(k0 + st * (MAX_BOXES * BOX), BOX),
+                         pd = sdesc_sw128(pa);
+          for (int j = 0; j < NJ; ++j) {
+            if (elect_one()) {
+              mma4_bf16_mn(base + j * 64, va + j * (2 * BOX / 16), pd, pv, tv);
               tc_commit(&bars.empty[st][j]);
             }
-            tc_commit(&bars.pv_done);
-            ++tv;
+            __syncwarp();
+          }
+          if (elect_one()) tc_commit(&bars.pv_done);
+          __syncwarp();
+          ++tv;
+          since = 0;
+          continue;
+        }
+        if (ts < nt) {
+          const int i = it + ts, st = i % STAGES, buf = i & 1;
+          if (!start)
+            start = test(&bars.s_empty[buf], (i >> 1) + 1) && (ts > 0 || test(&bars.q_full, piece));
+          if (start && test(&bars.full[st][block], i / STAGES)) {
+            tc_fence_after();
+            const uint64_t kd = sdesc_sw128(k0 + (st * MAX_BOXES + 2 * block) * BOX),
+                           qd = sdesc_sw128(qa + 2 * block * BOX);
+            const uint32_t d = base + 256 + buf * 64;
+            if (block < NJ) {
+              if (elect_one()) {
+                mma4_bf16(d, qd, kd, idesc_make(1, 64, 64), block);
+                mma4_bf16(d, qd + BOX / 16, kd + BOX / 16, idesc_make(1, 64, 64), 1);
+              }
+              __syncwarp();
+              ++block;
+            } else {
+              if (elect_one()) {
+                for (int s = 0; s < p.rope / 16; ++s)
+                  mma_bf16(d, qd + 2 * s, kd + 2 * s, idesc_make(1, 64, 64), 1);
+                tc_commit(&bars.s_full[buf]);
+                tc_commit(&bars.empty[st][NJ]);
+                if (ts + 1 == nt) tc_commit(&bars.q_free);
+              }
+              __syncwarp();
+              block = 0;
+              start = false;
+              ++ts;
+            }
             since = 0;
             continue;
           }
-          if (ts < nt) {
-            const int i = it + ts, st = i % STAGES, buf = i & 1;
-            if (!start)
-              start = mbar_test(&bars.s_empty[buf], (i >> 1) + 1) &&
-                      (ts > 0 || mbar_test(&bars.q_full, piece));
-            if (start && mbar_test(&bars.full[st][block], i / STAGES)) {
-              tc_fence_after();
-              const uint32_t ka = smem_u32(ks + st * MAX_BOXES * BOX);
-              if (block < NJ) {
-                mma4_bf16(S + buf * 64, sdesc_sw128(qa + 2 * block * BOX),
-                          sdesc_sw128(ka + 2 * block * BOX), idesc_make(1, 64, 64), block);
-                mma4_bf16(S + buf * 64, sdesc_sw128(qa + (2 * block + 1) * BOX),
-                          sdesc_sw128(ka + (2 * block + 1) * BOX), idesc_make(1, 64, 64), 1);
-                ++block;
-              } else {
-                for (int s = 0; s < p.rope / 16; ++s)
-                  mma_bf16(S + buf * 64, sdesc_sw128(qa + NB * BOX) + 2 * s,
-                           sdesc_sw128(ka + NB * BOX) + 2 * s, idesc_make(1, 64, 64), 1);
-                tc_commit(&bars.s_full[buf]);
-                tc_commit(&bars.empty[st][NJ]);
-                block = 0;
-                start = false;
-                if (++ts == nt) tc_commit(&bars.q_free);
-              }
-              since = 0;
-              continue;
-            }
-          }
-          if (since == 0) since = clock64();
-          if (*stop || clock64() - since > p.timeout) {
-            if (!*stop) {
-              *stop = 1;
-              atomicOr(p.err, DEV_ERR_TIMEOUT);
-            }
-            ok = false;
-            break;
-          }
         }
-        it += nt;
-        ++piece;
+        if (since == 0) since = clock64();
+        if (__any_sync(0xFFFFFFFFu, *stop || clock64() - since > p.timeout)) {
+          if (!*stop) {
+            *stop = 1;
+            atomicOr(p.err, DEV_ERR_TIMEOUT);
+          }
+          ok = false;
+          break;
+        }
       }
-      tc_commit(&bars.drain);  // no product runs past this point
-      int none = 0;
-      mbar_wait(&bars.drain, 0, &none, p.err, p.timeout);
+      it += nt;
+      ++piece;
     }
-  } else if (warp < 4) {
+    if (elect_one()) tc_commit(&bars.drain);  // no product runs past this point
+    __syncwarp();
+    int none = 0;
+    mbar_wait(&bars.drain, 0, &none, p.err, p.timeout);
+  } else if (warp == 2) {
     // ------------------------------------------------ queries
-    const int me = tid - 64;
     int piece = 0;
-    bool ok = true, left[2] = {false, false};
-    while (walk.next(p, w)) {
-      if (w.rows == 0) continue;
-      if (!w.whole) {
-        left[0] = left[0] || !(w.slot & 1);
-        left[1] = left[1] || (w.slot & 1);
-        if (me == 32) {
-          Record r;
-          r.valid = 1;
-          r.token = w.q0;
-          r.row = w.row;
-          r.rows = w.rows;
-          r.first = static_cast<int>(((w.start + 1) * groups - 1) / W);
-          r.last = static_cast<int>(((w.start + w.tiles) * groups - 1) / W);
-          r.member = blockIdx.x % p.members;
-          const int cta = r.first * p.members + r.member;
-          r.slot = 2 * cta + (share(W, r.first, groups) == w.start ? 0 : 1);
-          ws.records[w.slot] = r;
-        }
-      }
-      if (!ok || w.t0 == w.t1) continue;
+    bool ok = true;
+    while (ok && walk.next(p, w)) {
+      if (w.rows == 0 || w.t0 == w.t1) continue;
       ok = wait(&bars.q_free, piece + 1);
-      if (!ok) continue;
+      if (!ok) break;
       ++piece;
       if (p.q_box) {
-        if (me == 0) {
+        if (lane == 0) {
           mbar_arrive_expect_tx(&bars.q_full, KB * BOX);
           for (int r = 0; r < ROWS; r += p.q_box) {
             // rows past the item are other queries' or lie outside: their scores are masked
@@ -464,10 +457,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         continue;
       }
-      // a warp takes a row at a time, lanes neighbouring chunks of 8; all copies of the tile are in
-      // flight at once (a load and a store in turn took 35 us)
+      // a row at a time, lanes neighbouring chunks of 8; all copies are in flight at once
       const int chunks = (p.R + p.rope) >> 3;
-      for (int r = me >> 5; r < ROWS; r += 2) {
+      for (int r = 0; r < ROWS; ++r) {
         const int row = w.row + r;
         const bool there = r < w.rows;
         const int t = there ? row / p.H : 0, h = there ? row - t * p.H : 0;
@@ -483,13 +475,34 @@ __global__ void __launch_bounds__(THREADS, 1)
       fence_proxy_async_shared();
       mbar_arrive(&bars.q_full);
     }
-    if (me == 32) {
+    int none = 0;
+    if (piece > 0 && p.q_box && lane == 0)  // no copy is in flight past this point
+      mbar_wait(&bars.q_full, (piece - 1) & 1, &none, p.err, p.timeout);
+  } else if (warp == 3) {
+    // ------------------------------------------------ records
+    if (elect_one()) {
+      bool left[2] = {false, false};
+      while (walk.next(p, w)) {
+        if (w.rows == 0) continue;
+        if (!w.whole) {
+          left[0] = left[0] || !(w.slot & 1);
+          left[1] = left[1] || (w.slot & 1);
+          Record r;
+          r.valid = 1;
+          r.token = w.q0;
+          r.row = w.row;
+          r.rows = w.rows;
+          r.first = static_cast<int>(((w.start + 1) * groups - 1) / W);
+          r.last = static_cast<int>(((w.start + w.tiles) * groups - 1) / W);
+          r.member = blockIdx.x % p.members;
+          const int cta = r.first * p.members + r.member;
+          r.slot = 2 * cta + (share(W, r.first, groups) == w.start ? 0 : 1);
+          ws.records[w.slot] = r;
+        }
+      }
       if (!left[0]) ws.records[2 * blockIdx.x].valid = 0;
       if (!left[1]) ws.records[2 * blockIdx.x + 1].valid = 0;
     }
-    int none = 0;
-    if (piece > 0 && p.q_box && me == 0)  // no copy is in flight past this point
-      mbar_wait(&bars.q_full, (piece - 1) & 1, &none, p.err, p.timeout);
   } else {
     // ------------------------------------------------ softmax and results
     // This warp: rows 16 quad .. + 15 of the scores, keys 32 half .. + 31 of a tile; of O^T latent
