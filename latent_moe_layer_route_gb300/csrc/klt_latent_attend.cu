@@ -11,8 +11,8 @@
 // warp 2 loads the queries, warp 3 records what the parts are, warps 4 to 11 do the softmax (32 of a tile's keys each) and write
 // results.
 //
-// The work is cut evenly: with W tiles of keys over all (sequence, row tile) items, group g of G
-// computes tiles g W / G .. (g + 1) W / G, whatever the lengths.  An item that several groups share
+// The work is cut evenly over the SMs, whatever the lengths.  An item (a sequence's row tile, or
+// two side by side, a CTA of the group each) that several groups share
 // leaves its parts (O, running maximum and sum, fp32) in the workspace, and a second kernel brings
 // them together in order; so results do not depend on timing.  Each CTA records what its parts
 // belong to on every call: the workspace holds no state between calls.
@@ -100,6 +100,7 @@ struct Piece {
 struct Walk {
   long long pos, lo, hi, base;
   int b;
+  int first, parts;  // items shared out one by one: the group of this one's first part, its parts
   Seq s;
   KLT_DEV bool next(const AttendParams& p, Piece& w) {
     if (pos >= hi) return false;
@@ -175,6 +176,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   __shared__ float tops[2][ROWS];  // of each half of a tile's keys: maxima; at the end sums
   __shared__ int64_t out_at[ROWS];
   __shared__ long long sums[THREADS / 32];
+  __shared__ int counts[THREADS / 32];
   __shared__ long long found_base;
   __shared__ int found_b;
   __shared__ uint32_t tmem_holder;
@@ -209,17 +211,25 @@ __global__ void __launch_bounds__(THREADS, 1)
   pdl_trigger();
   pdl_wait();
 
-  // the work of all, and this group's share
+  // The work of all, and this group's share of it.  Where there are fewer items than groups, each
+  // item has groups of its own: the smallest share t with sum(ceil(tiles / t)) <= groups is found,
+  // twelve candidates at once, a warp each, between W / groups and W / (groups - items), which is
+  // always enough.  Else the tiles of all items in a row are cut into equal shares, and a group may
+  // have the end of one item and the start of the next (which costs it some 10 us of work: 32
+  // ragged sequences took 67 us that way, 59 by items).
   const int group = blockIdx.x / p.members;
   long long W = 0, mine = 0, excl = 0;
-  int groups;
+  int groups = gridDim.x / p.members, items = 0;
   Walk walk;
   {
+    constexpr int WARPS = THREADS / 32;
+    int2* seqs = reinterpret_cast<int2*>(ps);  // items and tiles of each sequence, one pass's
     Seq s;
-    s.supers = 0, s.tiles = 1;
     for (int b = tid; b < p.B; b += THREADS) {
       s.load(p, b);
       mine += s.cost();
+      items += s.supers;
+      seqs[tid] = make_int2(s.supers, s.tiles);
     }
     // block-wide sum; where one pass covers the batch, also this sequence's place in it
     long long incl = mine;
@@ -228,50 +238,103 @@ __global__ void __launch_bounds__(THREADS, 1)
       const long long v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
       if (lane >= o) incl += v;
     }
-    if (lane == 31) sums[warp] = incl;
+    items = __reduce_add_sync(0xFFFFFFFFu, items);
+    if (lane == 31) sums[warp] = incl, counts[warp] = items;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    for (int i = 0; i < THREADS / 32; ++i) {
+    items = 0;
+    for (int i = 0; i < WARPS; ++i) {
       if (i == warp) excl = W + incl - mine;
       W += sums[i];
+      items += counts[i];
     }
-    groups = static_cast<int>(max(1ll, min(static_cast<long long>(gridDim.x / p.members),
-                                           W / MIN_TILES)));
-    walk.lo = walk.pos = group < groups ? share(W, group, groups) : 0;
-    walk.hi = group < groups ? share(W, group + 1, groups) : 0;
-    if (p.B <= THREADS) {
-      if (mine > 0 && walk.lo >= excl && walk.lo < excl + mine) found_b = tid, found_base = excl;
+    walk.parts = 0;
+    walk.lo = walk.hi = 0;
+    if (p.B <= THREADS && items < groups) {
+      const long long least = max(static_cast<long long>(MIN_TILES), (W + groups - 1) / groups);
+      const long long most = max(least, (W + groups - items - 1) / (groups - items));
+      auto candidate = [&](int i) {
+        return static_cast<int>(min(least + (most - least) * i / (WARPS - 1), 0x7FFFFFFFll));
+      };
+      int t = candidate(warp), need = 0;
+      for (int b = lane; b < p.B; b += 32) need += seqs[b].x * ((seqs[b].y + t - 1) / t);
+      need = __reduce_add_sync(0xFFFFFFFFu, need);
+      __syncthreads();  // counts have been read
+      if (lane == 0) counts[warp] = need;
       __syncthreads();
-    } else {  // pass by pass
-      long long before = 0;
-      for (int b0 = 0; b0 < p.B; b0 += THREADS) {
-        long long c = 0;
-        if (b0 + tid < p.B) {
-          s.load(p, b0 + tid);
-          c = s.cost();
-        }
-        long long in = c;
+      int i = 0;
+      while (i < WARPS - 1 && counts[i] > groups) ++i;
+      t = candidate(i);
+      int before = 0;
+      for (int b0 = 0; b0 < p.B; b0 += 32) {
+        const int2 q = b0 + lane < p.B ? seqs[b0 + lane] : make_int2(0, 1);
+        const int parts = (q.y + t - 1) / t;
+        int in = q.x * parts;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const long long v = __shfl_up_sync(0xFFFFFFFFu, in, o);
+          const int v = __shfl_up_sync(0xFFFFFFFFu, in, o);
           if (lane >= o) in += v;
         }
-        __syncthreads();
-        if (lane == 31) sums[warp] = in;
-        __syncthreads();
-        for (int i = 0; i < warp; ++i) in += sums[i];
-        in += before;
-        if (c > 0 && walk.lo >= in - c && walk.lo < in) found_b = b0 + tid, found_base = in - c;
-        for (int i = 0; i < THREADS / 32; ++i) before += sums[i];
+        const uint32_t past = __ballot_sync(0xFFFFFFFFu, group < before + in);
+        if (past) {
+          const int src = __ffs(past) - 1;
+          walk.b = b0 + src;
+          walk.parts = __shfl_sync(0xFFFFFFFFu, parts, src);
+          const int at =  // this group's number among the sequence's
+              group - before - __shfl_sync(0xFFFFFFFFu, in - q.x * parts, src);
+          const int super = at / walk.parts, part = at - super * walk.parts;
+          walk.first = group - part;
+          walk.s.load(p, walk.b);
+          walk.base = 0;
+          const long long start = static_cast<long long>(super) * walk.s.tiles;
+          walk.lo = start + share(walk.s.tiles, part, walk.parts);
+          walk.hi = start + share(walk.s.tiles, part + 1, walk.parts);
+          break;
+        }
+        before += __shfl_sync(0xFFFFFFFFu, in, 31);
       }
-      __syncthreads();
+    } else {
+      groups = static_cast<int>(max(1ll, min(static_cast<long long>(groups), W / MIN_TILES)));
+      if (group < groups) {
+        walk.lo = share(W, group, groups);
+        walk.hi = share(W, group + 1, groups);
+      }
+      if (p.B <= THREADS) {
+        if (mine > 0 && walk.lo >= excl && walk.lo < excl + mine) found_b = tid, found_base = excl;
+        __syncthreads();
+      } else {  // pass by pass
+        long long before = 0;
+        for (int b0 = 0; b0 < p.B; b0 += THREADS) {
+          long long c = 0;
+          if (b0 + tid < p.B) {
+            s.load(p, b0 + tid);
+            c = s.cost();
+          }
+          long long in = c;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const long long v = __shfl_up_sync(0xFFFFFFFFu, in, o);
+            if (lane >= o) in += v;
+          }
+          __syncthreads();
+          if (lane == 31) sums[warp] = in;
+          __syncthreads();
+          for (int i = 0; i < warp; ++i) in += sums[i];
+          in += before;
+          if (c > 0 && walk.lo >= in - c && walk.lo < in) found_b = b0 + tid, found_base = in - c;
+          for (int i = 0; i < WARPS; ++i) before += sums[i];
+        }
+        __syncthreads();
+      }
+      if (walk.lo < walk.hi) {
+        walk.b = found_b;
+        walk.base = found_base;
+        walk.s.load(p, walk.b);
+      }
     }
-    if (walk.lo < walk.hi) {
-      walk.b = found_b;
-      walk.base = found_base;
-      walk.s.load(p, walk.b);
-    }
+    walk.pos = walk.lo;
+    __syncthreads();  // the weights' memory is free
   }
   const uint32_t tmem = tmem_holder, S = tmem + 256;
   volatile int* stop = &abort_flag;
@@ -492,11 +555,16 @@ __global__ void __launch_bounds__(THREADS, 1)
           r.token = w.q0;
           r.row = w.row;
           r.rows = w.rows;
-          r.first = static_cast<int>(((w.start + 1) * groups - 1) / W);
-          r.last = static_cast<int>(((w.start + w.tiles) * groups - 1) / W);
           r.member = blockIdx.x % p.members;
-          const int cta = r.first * p.members + r.member;
-          r.slot = 2 * cta + (share(W, r.first, groups) == w.start ? 0 : 1);
+          if (walk.parts > 0) {
+            r.first = walk.first;
+            r.last = walk.first + walk.parts - 1;
+          } else {
+            r.first = static_cast<int>(((w.start + 1) * groups - 1) / W);
+            r.last = static_cast<int>(((w.start + w.tiles) * groups - 1) / W);
+          }
+          r.slot = 2 * (r.first * p.members + r.member) +
+                   (walk.parts > 0 || share(W, r.first, groups) == w.start ? 0 : 1);
           ws.records[w.slot] = r;
         }
       }
@@ -691,7 +759,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 // first loads of O go out before the weights are known.
 KLT_DEV void join_item(const AttendParams& p, const Space& ws, int ctas, const Record& rec,
                        float4* weight, float4* inverse) {
-  constexpr int BATCH = 8;  // parts in flight in a thread
+  constexpr int BATCH = 4;  // parts in flight in a thread
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int parts = rec.last - rec.first + 1;
   const int unit = (static_cast<int>(blockIdx.x) / p.members - rec.first) * UNITS + blockIdx.y;
@@ -783,7 +851,7 @@ KLT_DEV void join_item(const AttendParams& p, const Space& ws, int ctas, const R
   }
 }
 
-__global__ void __launch_bounds__(JOIN) join_kernel(const AttendParams p, int ctas) {
+__global__ void __launch_bounds__(JOIN, 8) join_kernel(const AttendParams p, int ctas) {
   __shared__ float4 weight[MAX_PARTS], inverse;
   pdl_trigger();
   pdl_wait();
