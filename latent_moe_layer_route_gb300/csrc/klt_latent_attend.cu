@@ -7,8 +7,9 @@
 // half of TMEM that way and the products have M = 128.
 //
 // Roles: warp 0 copies tiles (two stages of 72 KB in blocks of 128 columns, each handed back on
-// its own), warp 1 issues products (a tile's scores before the values of the tile before it),
-// warp 2 loads the queries, warp 3 records what the parts are, warps 4 to 11 do the softmax (32 of a tile's keys each) and write
+// its own), warp 1 issues the products of scores and warp 3 those of values (one thread for both
+// took longer over its waits and signals than these small products take: 4,000 cycles a tile, for
+// 2,000 of work), warp 2 loads the queries and records what the parts are, warps 4 to 11 do the softmax (32 of a tile's keys each) and write
 // results.
 //
 // The work is cut evenly over the SMs, whatever the lengths.  An item (a sequence's row tile, or
@@ -197,7 +198,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     mbar_init(&bars.o_free, SOFTMAX / 32);
     mbar_init(&bars.q_full, p.q_box ? 1 : 32);
     mbar_init(&bars.q_free, 1);
-    mbar_init(&bars.drain, 1);
+    mbar_init(&bars.drain, 2);
     abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&latents);
@@ -407,104 +408,103 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
     }
   } else if (warp == 1) {
-    // ------------------------------------------------ products
-    // The whole warp goes through the loop and one lane issues: so the compiler knows the loop to be
-    // uniform and keeps descriptors in uniform registers, where the products take them from (in one
-    // lane's branch a product took 64 cycles to issue, for 35 of work).
-    int it = 0, piece = 0;  // tiles; pieces with rows and tiles
-    const uint32_t base = uniform(tmem), qa = uniform(smem_u32(qs)), pa = uniform(smem_u32(ps)),
-                   k0 = uniform(smem_u32(ks));
-    auto test = [&](uint64_t* bar, int phase) {
-      return __all_sync(0xFFFFFFFFu, mbar_test(bar, phase)) != 0;
-    };
-    bool ok = true;
-    while (ok && uniform(walk.next(p, w))) {
-      const int nt = uniform(w.rows == 0 ? 0 : w.t1 - w.t0);
-      if (nt == 0) continue;
-      const uint32_t pv = idesc_make(1, 128, (uniform(w.rows) + 15) & ~15) | IDESC_A_MN;
-      // Whichever is ready: the values of the oldest tile whose weights are written, else the next
-      // block of the next tile's scores.  In a fixed order (scores of tile t + 1 before the values
-      // of t) a stage was handed back only after the copy of the tile behind it, 2.7 us a tile.
-      int ts = 0, tv = 0, block = 0;  // next tile of scores and of values, next block of scores
-      long long since = 0;
-      bool start = false;
-      while (tv < nt) {
-        if (tv < ts && test(&bars.p_full, it + tv) && (tv > 0 || test(&bars.o_free, piece + 1))) {
-          tc_fence_after();
-          const int st = (it + tv) % STAGES;
-          const uint64_t va = sdesc_sw128_mn(k0 + st * (MAX_BOXES * BOX), BOX),
-                         pd = sdesc_sw128(pa);
-          for (int j = 0; j < NJ; ++j) {
-            if (elect_one()) {
-              mma4_bf16_mn(base + j * 64, va + j * (2 * BOX / 16), pd, pv, tv);
-              tc_commit(&bars.empty[st][j]);
-            }
-            __syncwarp();
-          }
-          if (elect_one()) tc_commit(&bars.pv_done);
-          __syncwarp();
-          ++tv;
-          since = 0;
-          continue;
-        }
-        if (ts < nt) {
-          const int i = it + ts, st = i % STAGES, buf = i & 1;
-          if (!start)
-            start = test(&bars.s_empty[buf], (i >> 1) + 1) && (ts > 0 || test(&bars.q_full, piece));
-          if (start && test(&bars.full[st][block], i / STAGES)) {
+    // ------------------------------------------------ scores
+    if (elect_one()) {
+      int it = 0, piece = 0;  // tiles; pieces with rows and tiles
+      bool ok = true;
+      const uint32_t qa = smem_u32(qs);
+      while (ok && walk.next(p, w)) {
+        if (w.rows == 0 || w.t0 == w.t1) continue;
+        ok = wait(&bars.q_full, piece++);
+        for (int t = w.t0; t < w.t1 && ok; ++t, ++it) {
+          const int st = it % STAGES, buf = it & 1;
+          const uint32_t ka = smem_u32(ks + st * MAX_BOXES * BOX), d = S + buf * 64;
+          ok = wait(&bars.s_empty[buf], (it >> 1) + 1);
+          for (int j = 0; j < NJ && ok; ++j) {
+            ok = wait(&bars.full[st][j], it / STAGES);
+            if (!ok) break;
             tc_fence_after();
-            const uint64_t kd = sdesc_sw128(k0 + (st * MAX_BOXES + 2 * block) * BOX),
-                           qd = sdesc_sw128(qa + 2 * block * BOX);
-            const uint32_t d = base + 256 + buf * 64;
-            if (block < NJ) {
-              if (elect_one()) {
-                mma4_bf16(d, qd, kd, idesc_make(1, 64, 64), block);
-                mma4_bf16(d, qd + BOX / 16, kd + BOX / 16, idesc_make(1, 64, 64), 1);
-              }
-              __syncwarp();
-              ++block;
-            } else {
-              if (elect_one()) {
-                for (int s = 0; s < p.rope / 16; ++s)
-                  mma_bf16(d, qd + 2 * s, kd + 2 * s, idesc_make(1, 64, 64), 1);
-                tc_commit(&bars.s_full[buf]);
-                tc_commit(&bars.empty[st][NJ]);
-                if (ts + 1 == nt) tc_commit(&bars.q_free);
-              }
-              __syncwarp();
-              block = 0;
-              start = false;
-              ++ts;
-            }
-            since = 0;
-            continue;
+            const uint64_t qd = sdesc_sw128(qa + 2 * j * BOX), kd = sdesc_sw128(ka + 2 * j * BOX);
+            mma4_bf16(d, qd, kd, idesc_make(1, 64, 64), j);
+            mma4_bf16(d, qd + BOX / 16, kd + BOX / 16, idesc_make(1, 64, 64), 1);
           }
+          ok = ok && wait(&bars.full[st][NJ], it / STAGES);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t qd = sdesc_sw128(qa + NB * BOX), kd = sdesc_sw128(ka + NB * BOX);
+          if (p.rope == 64)
+            mma4_bf16(d, qd, kd, idesc_make(1, 64, 64), 1);
+          else
+            for (int s = 0; s < p.rope / 16; ++s)
+              mma_bf16(d, qd + 2 * s, kd + 2 * s, idesc_make(1, 64, 64), 1);
+          tc_commit(&bars.s_full[buf]);
+          tc_commit(&bars.empty[st][NJ]);
         }
-        if (since == 0) since = clock64();
-        if (__any_sync(0xFFFFFFFFu, *stop || clock64() - since > p.timeout)) {
-          if (!*stop) {
-            *stop = 1;
-            atomicOr(p.err, DEV_ERR_TIMEOUT);
+        if (ok) tc_commit(&bars.q_free);
+      }
+      tc_commit(&bars.drain);  // none of this thread's products runs past this point
+      int none = 0;
+      mbar_wait(&bars.drain, 0, &none, p.err, 3 * p.timeout);
+    }
+  } else if (warp == 3) {
+    // ------------------------------------------------ values
+    if (elect_one()) {
+      int it = 0, piece = 0;
+      bool ok = true;
+      const uint64_t pd = sdesc_sw128(smem_u32(ps));
+      while (ok && walk.next(p, w)) {
+        if (w.rows == 0 || w.t0 == w.t1) continue;
+        const uint32_t idesc = idesc_make(1, 128, (w.rows + 15) & ~15) | IDESC_A_MN;
+        ++piece;
+        for (int t = w.t0; t < w.t1; ++t, ++it) {
+          const int st = it % STAGES;
+          ok = wait(&bars.p_full, it) && (t > w.t0 || wait(&bars.o_free, piece));
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t va = sdesc_sw128_mn(smem_u32(ks + st * MAX_BOXES * BOX), BOX);
+          for (int j = 0; j < NJ; ++j) {
+            mma4_bf16_mn(tmem + j * 64, va + j * (2 * BOX / 16), pd, idesc, t > w.t0);
+            tc_commit(&bars.empty[st][j]);
           }
-          ok = false;
-          break;
+          tc_commit(&bars.pv_done);
         }
       }
-      it += nt;
-      ++piece;
+      tc_commit(&bars.drain);
+      int none = 0;
+      mbar_wait(&bars.drain, 0, &none, p.err, 3 * p.timeout);
     }
-    if (elect_one()) tc_commit(&bars.drain);  // no product runs past this point
-    __syncwarp();
-    int none = 0;
-    mbar_wait(&bars.drain, 0, &none, p.err, p.timeout);
   } else if (warp == 2) {
     // ------------------------------------------------ queries
     int piece = 0;
-    bool ok = true;
-    while (ok && walk.next(p, w)) {
-      if (w.rows == 0 || w.t0 == w.t1) continue;
+    bool ok = true, left[2] = {false, false};
+    while (walk.next(p, w)) {
+      if (w.rows == 0) continue;
+      if (!w.whole) {  // record what the part belongs to
+        left[0] = left[0] || !(w.slot & 1);
+        left[1] = left[1] || (w.slot & 1);
+        if (lane == 31) {
+          Record r;
+          r.valid = 1;
+          r.token = w.q0;
+          r.row = w.row;
+          r.rows = w.rows;
+          r.member = blockIdx.x % p.members;
+          if (walk.parts > 0) {
+            r.first = walk.first;
+            r.last = walk.first + walk.parts - 1;
+          } else {
+            r.first = static_cast<int>(((w.start + 1) * groups - 1) / W);
+            r.last = static_cast<int>(((w.start + w.tiles) * groups - 1) / W);
+          }
+          r.slot = 2 * (r.first * p.members + r.member) +
+                   (walk.parts > 0 || share(W, r.first, groups) == w.start ? 0 : 1);
+          ws.records[w.slot] = r;
+        }
+      }
+      if (!ok || w.t0 == w.t1) continue;
       ok = wait(&bars.q_free, piece + 1);
-      if (!ok) break;
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (!ok) continue;
       ++piece;
       if (p.q_box) {
         if (lane == 0) {
@@ -538,39 +538,13 @@ __global__ void __launch_bounds__(THREADS, 1)
       fence_proxy_async_shared();
       mbar_arrive(&bars.q_full);
     }
-    int none = 0;
-    if (piece > 0 && p.q_box && lane == 0)  // no copy is in flight past this point
-      mbar_wait(&bars.q_full, (piece - 1) & 1, &none, p.err, p.timeout);
-  } else if (warp == 3) {
-    // ------------------------------------------------ records
-    if (elect_one()) {
-      bool left[2] = {false, false};
-      while (walk.next(p, w)) {
-        if (w.rows == 0) continue;
-        if (!w.whole) {
-          left[0] = left[0] || !(w.slot & 1);
-          left[1] = left[1] || (w.slot & 1);
-          Record r;
-          r.valid = 1;
-          r.token = w.q0;
-          r.row = w.row;
-          r.rows = w.rows;
-          r.member = blockIdx.x % p.members;
-          if (walk.parts > 0) {
-            r.first = walk.first;
-            r.last = walk.first + walk.parts - 1;
-          } else {
-            r.first = static_cast<int>(((w.start + 1) * groups - 1) / W);
-            r.last = static_cast<int>(((w.start + w.tiles) * groups - 1) / W);
-          }
-          r.slot = 2 * (r.first * p.members + r.member) +
-                   (walk.parts > 0 || share(W, r.first, groups) == w.start ? 0 : 1);
-          ws.records[w.slot] = r;
-        }
-      }
+    if (lane == 31) {
       if (!left[0]) ws.records[2 * blockIdx.x].valid = 0;
       if (!left[1]) ws.records[2 * blockIdx.x + 1].valid = 0;
     }
+    int none = 0;
+    if (piece > 0 && p.q_box && lane == 0)  // no copy is in flight past this point
+      mbar_wait(&bars.q_full, (piece - 1) & 1, &none, p.err, p.timeout);
   } else {
     // ------------------------------------------------ softmax and results
     // This warp: rows 16 quad .. + 15 of the scores, keys 32 half .. + 31 of a tile; of O^T latent
