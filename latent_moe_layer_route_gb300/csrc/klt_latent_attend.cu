@@ -32,6 +32,7 @@ constexpr int THREADS = 128 + SOFTMAX;
 constexpr int SMEM = 1024 + (MAX_BOXES * (1 + STAGES) + 1) * BOX;
 constexpr int MIN_TILES = 2;     // a group's least share
 constexpr int UNITS = 8;         // joining blocks per part
+constexpr int EXTRA = 4;         // what an item costs besides its tiles, in tiles
 constexpr int JOIN = 128;        // their threads: a warp to each of four rows' weights
 static_assert(2 * UNITS >= ROWS / 4 && JOIN == 4 * 32, "");
 constexpr int MAX_PARTS = 224;   // of an item
@@ -79,7 +80,7 @@ struct Seq {
     supers = (n * p.H + per - 1) / per;
     tiles = max(1, (len + KEYS - 1) / KEYS);
   }
-  KLT_DEV long long cost() const { return static_cast<long long>(supers) * tiles; }
+  KLT_DEV long long cost() const { return static_cast<long long>(supers) * (tiles + EXTRA); }
 };
 
 // a b / c for c <= 2^8 or so, without a 64-bit division where 32 bits hold a b.
@@ -95,7 +96,7 @@ struct Piece {
   int t0, t1;          // tiles of keys that some row sees, in this part
   bool whole;          // the item is this CTA's alone
   int slot;            // else: where its part goes
-  long long start;     // the item's first tile in the flat order
+  long long start;     // the item's first tile's place in the flat order
   int tiles;
 };
 struct Walk {
@@ -109,11 +110,16 @@ struct Walk {
       base += s.cost();
       s.load(p, ++b);
     }
+    // An item is EXTRA units and then its tiles.  A border within the first ones is as good as at
+    // the item's start: the group before it stops there, the one behind it starts there.
     const long long local = pos - base;
-    const int super = static_cast<int>(local >> 32 ? local / s.tiles
-                                                   : static_cast<uint32_t>(local) / s.tiles);
-    const int t = static_cast<int>(local - static_cast<long long>(super) * s.tiles);
-    const int e = static_cast<int>(min(static_cast<long long>(s.tiles), t + (hi - pos)));
+    const int units = s.tiles + EXTRA;
+    const int super = static_cast<int>(local >> 32 ? local / units
+                                                   : static_cast<uint32_t>(local) / units);
+    const int u = static_cast<int>(local - static_cast<long long>(super) * units);
+    const int end = static_cast<int>(min(static_cast<long long>(units), u + (hi - pos)));
+    if (end <= EXTRA) return false;
+    const int t = max(0, u - EXTRA), e = end - EXTRA;
     const int member = blockIdx.x % p.members;
     w.b = b;
     w.q0 = s.q0;
@@ -127,9 +133,9 @@ struct Walk {
     w.t1 = max(t, min(e, (seen + KEYS - 1) / KEYS));
     w.whole = t == 0 && e == s.tiles;
     w.slot = 2 * blockIdx.x + (pos == lo ? 0 : 1);
-    w.start = base + static_cast<long long>(super) * s.tiles;
+    w.start = base + static_cast<long long>(super) * units + EXTRA;
     w.tiles = s.tiles;
-    pos += e - t;
+    pos += end - u;
     return true;
   }
 };
@@ -253,8 +259,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     walk.parts = 0;
     walk.lo = walk.hi = 0;
     if (p.B <= THREADS && items < groups) {
-      const long long least = max(static_cast<long long>(MIN_TILES), (W + groups - 1) / groups);
-      const long long most = max(least, (W + groups - items - 1) / (groups - items));
+      const long long all = W - static_cast<long long>(items) * EXTRA;  // tiles
+      const long long least = max(static_cast<long long>(MIN_TILES), (all + groups - 1) / groups);
+      const long long most = max(least, (all + groups - items - 1) / (groups - items));
       auto candidate = [&](int i) {
         return static_cast<int>(min(least + (most - least) * i / (WARPS - 1), 0x7FFFFFFFll));
       };
@@ -288,7 +295,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           walk.first = group - part;
           walk.s.load(p, walk.b);
           walk.base = 0;
-          const long long start = static_cast<long long>(super) * walk.s.tiles;
+          const long long start = static_cast<long long>(super) * (walk.s.tiles + EXTRA) + EXTRA;
           walk.lo = start + share(walk.s.tiles, part, walk.parts);
           walk.hi = start + share(walk.s.tiles, part + 1, walk.parts);
           break;
@@ -497,7 +504,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             r.last = static_cast<int>(((w.start + w.tiles) * groups - 1) / W);
           }
           r.slot = 2 * (r.first * p.members + r.member) +
-                   (walk.parts > 0 || share(W, r.first, groups) == w.start ? 0 : 1);
+                   (walk.parts > 0 || share(W, r.first, groups) >= w.start - EXTRA ? 0 : 1);
           ws.records[w.slot] = r;
         }
       }
@@ -728,15 +735,23 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 // Brings an item's parts together: weights 2^(m_i - M) per row and part, with M the largest maximum,
 // and the sum of weighted O over the sum of weighted sums.  Four rows of the item and some of their
-// columns are a block's, UNITS blocks per part: where there are many parts a block has few columns,
-// and several threads share each one's parts, so its time hardly depends on their number.  The
-// first loads of O go out before the weights are known.
-KLT_DEV void join_item(const AttendParams& p, const Space& ws, int ctas, const Record& rec,
-                       float4* weight, float4* inverse) {
-  constexpr int BATCH = 4;  // parts in flight in a thread
+// columns are a block's, UNITS blocks per part, which makes 8 loads a thread however many parts
+// there are: of several columns where the parts are few, of one column, shared by several threads,
+// where they are many.  The first eight go out before the weights are known.
+__global__ void __launch_bounds__(JOIN, 8)
+    join_kernel(const AttendParams p, int ctas, int slots) {
+  __shared__ float4 weight[MAX_PARTS], inverse;
+  constexpr int BATCH = 8;
+  pdl_trigger();
+  pdl_wait();
+  const Space ws = space_of(p.part, ctas);
+  const int cta = blockIdx.x / slots;
+  const Record rec = ws.records[2 * cta + (blockIdx.x - cta * slots)];
+  if (!rec.valid) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int parts = rec.last - rec.first + 1;
-  const int unit = (static_cast<int>(blockIdx.x) / p.members - rec.first) * UNITS + blockIdx.y;
+  const int unit =
+      (cta / p.members - rec.first) * UNITS + blockIdx.y;
   const int fours = (rec.rows + 3) >> 2, chunks = parts * UNITS / fours;  // >= 1: UNITS parts >= 16
   const int four = unit % fours, chunk = unit / fours;
   const int per = (p.R + chunks - 1) / chunks;  // columns of a block
@@ -747,95 +762,103 @@ KLT_DEV void join_item(const AttendParams& p, const Space& ws, int ctas, const R
   };
   int split = 1;  // threads that share a column's parts
   while (split < 32 && 2 * split <= parts && JOIN / (2 * split) >= per) split *= 2;
-  const int at = tid / split, mine = tid & (split - 1);
+  const int mine = tid & (split - 1), step = JOIN / split;
+  const int columns = (per + step - 1) / step, most = (parts + split - 1) / split;
+  // this thread's loads in a row: its parts of a column, then those of its next column
+  const int first = c0 + tid / split;
   float4 v[BATCH];
-  auto load = [&](int c, int i0) {
-    const float4* src = ws.o + four * p.R + min(c, p.R - 1);
+  auto load = [&](int c, int i) {
+    const float4* src = ws.o + four * p.R;
 #pragma unroll
     for (int k = 0; k < BATCH; ++k) {
-      const int i = i0 + k * split;
-      if (i < parts) v[k] = src[static_cast<int64_t>(slot_of(i)) * (ROWS / 4) * p.R];
+      if (c < c1 && i < parts)
+        v[k] = src[static_cast<int64_t>(slot_of(i)) * (ROWS / 4) * p.R + c];
+      i += split;
+      if (i - mine >= most * split) i = mine, c += step;
     }
   };
-  load(c0 + at, mine);
-  float* const weights = reinterpret_cast<float*>(weight);
+  load(first, mine);
   {
     const int row = four * 4 + warp;  // this warp's row
     const float2* ml = ws.ml + row * 2 * ctas;
+    float* const weights = reinterpret_cast<float*>(weight) + warp;
     float top = -INFINITY, sum = 0.f;
     float2 x[MAX_PARTS / 32];
 #pragma unroll
     for (int j = 0; j < MAX_PARTS / 32; ++j) {
+      if (j * 32 >= parts) break;
       x[j] = make_float2(-INFINITY, 0.f);
       if (j * 32 + lane < parts) x[j] = ml[slot_of(j * 32 + lane)];
+    }
+#pragma unroll
+    for (int j = 0; j < MAX_PARTS / 32; ++j) {
+      if (j * 32 >= parts) break;
       top = fmaxf(top, x[j].x);
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
 #pragma unroll
     for (int j = 0; j < MAX_PARTS / 32; ++j) {
+      if (j * 32 >= parts) break;
       const float f = x[j].x == -INFINITY ? 0.f : exp2_fast(x[j].x - top);
       sum += x[j].y == 0.f ? 0.f : f * x[j].y;
-      if (j * 32 + lane < parts) weights[(j * 32 + lane) * 4 + warp] = f;
+      if (j * 32 + lane < parts) weights[(j * 32 + lane) * 4] = f;
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
     if (lane == 0) {
-      reinterpret_cast<float*>(inverse)[warp] = sum != 0.f ? 1.0f / sum : 0.f;
+      reinterpret_cast<float*>(&inverse)[warp] = sum != 0.f ? 1.0f / sum : 0.f;
       if (p.lse && chunk == 0 && row < rec.rows)
         p.lse[static_cast<int64_t>(rec.token) * p.H + rec.row + row] =
             sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
     }
   }
   __syncthreads();
-  const float4 inv = *inverse;
-#pragma unroll 1
-  for (int c = c0 + at; c - at < c1; c += JOIN / split) {
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-    for (int i0 = mine; i0 < parts; i0 += BATCH * split) {
-      if (c != c0 + at || i0 != mine) load(c, i0);
+  const float4 inv = inverse;
+  __nv_bfloat16* out[4];
 #pragma unroll
-      for (int k = 0; k < BATCH; ++k) {
-        const int i = i0 + k * split;
-        if (i < parts) {  // a part in which a row sees no key may have left no O
-          const float4 f = weight[i];
-          acc.x = f.x == 0.f ? acc.x : fmaf(f.x, v[k].x, acc.x);
-          acc.y = f.y == 0.f ? acc.y : fmaf(f.y, v[k].y, acc.y);
-          acc.z = f.z == 0.f ? acc.z : fmaf(f.z, v[k].z, acc.z);
-          acc.w = f.w == 0.f ? acc.w : fmaf(f.w, v[k].w, acc.w);
-        }
-      }
-    }
-    for (int d = split >> 1; d; d >>= 1) {
-      acc.x += __shfl_down_sync(0xFFFFFFFFu, acc.x, d, split);
-      acc.y += __shfl_down_sync(0xFFFFFFFFu, acc.y, d, split);
-      acc.z += __shfl_down_sync(0xFFFFFFFFu, acc.z, d, split);
-      acc.w += __shfl_down_sync(0xFFFFFFFFu, acc.w, d, split);
-    }
-    if (mine == 0 && c < c1) {
-      const float out[4] = {acc.x * inv.x, acc.y * inv.y, acc.z * inv.z, acc.w * inv.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = rec.row + four * 4 + i, t = r / p.H, h = r - t * p.H;
-        if (four * 4 + i < rec.rows)
-          p.out[(rec.token + t) * p.out_token + h * p.out_head + c] = __float2bfloat16(out[i]);
-      }
-    }
+  for (int k = 0; k < 4; ++k) {
+    const int r = rec.row + four * 4 + k, t = r / p.H, h = r - t * p.H;
+    out[k] = four * 4 + k < rec.rows
+                 ? p.out + (rec.token + t) * p.out_token + h * p.out_head
+                 : nullptr;
   }
-}
-
-__global__ void __launch_bounds__(JOIN, 8) join_kernel(const AttendParams p, int ctas) {
-  __shared__ float4 weight[MAX_PARTS], inverse;
-  pdl_trigger();
-  pdl_wait();
-  const Space ws = space_of(p.part, ctas);
-  const Record both[2] = {ws.records[2 * blockIdx.x], ws.records[2 * blockIdx.x + 1]};
-#pragma unroll 1
-  for (int i = 0; i < 2; ++i) {
-    const Record rec = i ? both[1] : both[0];
-    if (rec.valid) join_item(p, ws, ctas, rec, weight, &inverse);
-    if (i == 0) __syncthreads();
+  // every thread of a warp goes through as many columns and parts as its first one
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  int c = first, i = mine;
+  for (int done = 0; done < columns * most; done += BATCH) {
+    if (done > 0) load(c, i);
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      if (done + k >= columns * most) break;
+      // where parts do not divide evenly some threads' last turn is empty
+      const bool there = c < c1 && i < parts;
+      if (there) {  // a part in which a row sees no key may have left no O
+        const float4 f = weight[i];
+        acc.x = f.x == 0.f ? acc.x : fmaf(f.x, v[k].x, acc.x);
+        acc.y = f.y == 0.f ? acc.y : fmaf(f.y, v[k].y, acc.y);
+        acc.z = f.z == 0.f ? acc.z : fmaf(f.z, v[k].z, acc.z);
+        acc.w = f.w == 0.f ? acc.w : fmaf(f.w, v[k].w, acc.w);
+      }
+      i += split;
+      if (i - mine >= most * split) {  // the column is done
+        for (int d = split >> 1; d; d >>= 1) {
+          acc.x += __shfl_down_sync(0xFFFFFFFFu, acc.x, d, split);
+          acc.y += __shfl_down_sync(0xFFFFFFFFu, acc.y, d, split);
+          acc.z += __shfl_down_sync(0xFFFFFFFFu, acc.z, d, split);
+          acc.w += __shfl_down_sync(0xFFFFFFFFu, acc.w, d, split);
+        }
+        if (mine == 0 && c < c1) {
+          const float x[4] = {acc.x * inv.x, acc.y * inv.y, acc.z * inv.z, acc.w * inv.w};
+#pragma unroll
+          for (int o = 0; o < 4; ++o)
+            if (out[o]) out[o][c] = __float2bfloat16(x[o]);
+        }
+        acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        i = mine;
+        c += step;
+      }
+    }
   }
 }
 
@@ -855,7 +878,15 @@ cudaError_t launch_attend(const CUtensorMap& latents, const CUtensorMap& ropes,
                           cudaStream_t s) {
   // two row tiles of a sequence read the same keys at the same time, the second from L2
   p.members = static_cast<int64_t>(p.T) * p.H > static_cast<int64_t>(ROWS) * p.B ? 2 : 1;
-  const int ctas = min(num_sms, MAX_PARTS) / p.members * p.members;
+  // at most as many items and parts of one as the sizes allow, whatever the lengths are
+  const int64_t per = ROWS * p.members, rows = static_cast<int64_t>(p.T) * p.H;
+  const int64_t items = p.cu_q ? rows / per + min(p.B, p.T) : p.B * ((p.H + per - 1) / per);
+  const int64_t tiles = ((static_cast<int64_t>(p.max_pages) << p.page_log2) + KEYS - 1) / KEYS;
+  const int64_t parts = max(int64_t{1}, (tiles + MIN_TILES - 1) / MIN_TILES);
+  int groups = min(num_sms, MAX_PARTS) / p.members;
+  const bool by_items = p.B <= THREADS && items < groups;
+  if (by_items && items * parts < groups) groups = static_cast<int>(max(items * parts, items + 1));
+  const int ctas = groups * p.members;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(THREADS);
@@ -867,11 +898,12 @@ cudaError_t launch_attend(const CUtensorMap& latents, const CUtensorMap& ropes,
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, attend_kernel, latents, ropes, queries, p);
-  if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(ctas, UNITS);
+  if (e != cudaSuccess || (by_items && parts == 1)) return e;
+  const int slots = by_items ? 1 : 2;
+  cfg.gridDim = dim3(slots * ctas, UNITS);
   cfg.blockDim = dim3(JOIN);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, join_kernel, static_cast<const AttendParams>(p), ctas);
+  return cudaLaunchKernelEx(&cfg, join_kernel, static_cast<const AttendParams>(p), ctas, slots);
 }
 
 }  // namespace klt
