@@ -34,7 +34,7 @@ constexpr int MIN_TILES = 2;     // a group's least share
 constexpr int UNITS = 8;         // joining blocks per part
 constexpr int EXTRA = 4;         // what an item costs besides its tiles, in tiles
 constexpr int JOIN = 128;        // their threads: a warp to each of four rows' weights
-static_assert(2 * UNITS >= ROWS / 4 && JOIN == 4 * 32, "");
+static_assert(2 * UNITS >= ROWS / 4 && JOIN == 4 * 32 && JOIN == 1 << 7, "");
 constexpr int MAX_PARTS = 224;   // of an item
 static_assert(SMEM <= 232448 - 2048, "shared memory of a block");
 
@@ -735,60 +735,60 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 // Brings an item's parts together: weights 2^(m_i - M) per row and part, with M the largest maximum,
 // and the sum of weighted O over the sum of weighted sums.  Four rows of the item and some of their
-// columns are a block's, UNITS blocks per part, which makes 8 loads a thread however many parts
+// columns are a block's, eight blocks to a part, so a thread has some eight loads however many parts
 // there are: of several columns where the parts are few, of one column, shared by several threads,
-// where they are many.  The first eight go out before the weights are known.
+// where they are many.  The first go out before the weights are known.  Lean on purpose: with
+// divisions and 64-bit addresses per load this was bound by its instructions (11 us for 152 parts).
 __global__ void __launch_bounds__(JOIN, 8)
     join_kernel(const AttendParams p, int ctas, int slots) {
   __shared__ float4 weight[MAX_PARTS], inverse;
-  constexpr int BATCH = 8;
+  __shared__ int64_t out_at[4];
   pdl_trigger();
   pdl_wait();
   const Space ws = space_of(p.part, ctas);
-  const int cta = blockIdx.x / slots;
-  const Record rec = ws.records[2 * cta + (blockIdx.x - cta * slots)];
+  const int cta = blockIdx.x >> (slots - 1);
+  const Record rec = ws.records[2 * cta + (blockIdx.x & (slots - 1))];
   if (!rec.valid) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int parts = rec.last - rec.first + 1;
-  const int unit =
-      (cta / p.members - rec.first) * UNITS + blockIdx.y;
-  const int fours = (rec.rows + 3) >> 2, chunks = parts * UNITS / fours;  // >= 1: UNITS parts >= 16
-  const int four = unit % fours, chunk = unit / fours;
-  const int per = (p.R + chunks - 1) / chunks;  // columns of a block
+  const int unit = ((cta >> (p.members - 1)) - rec.first) * UNITS + blockIdx.y;
+  const int four = unit & (ROWS / 4 - 1), chunk = unit / (ROWS / 4);
+  const int chunks = parts * UNITS / (ROWS / 4);  // >= 1: at least two parts
+  const int per = (p.R + chunks - 1) / chunks;    // columns of a block
   const int c0 = chunk * per, c1 = min(p.R, c0 + per);
-  if (chunk >= chunks || c0 >= c1) return;
-  auto slot_of = [&](int i) {
-    return i == 0 ? rec.slot : 2 * ((rec.first + i) * p.members + rec.member);
-  };
-  int split = 1;  // threads that share a column's parts
-  while (split < 32 && 2 * split <= parts && JOIN / (2 * split) >= per) split *= 2;
-  const int mine = tid & (split - 1), step = JOIN / split;
-  const int columns = (per + step - 1) / step, most = (parts + split - 1) / split;
-  // this thread's loads in a row: its parts of a column, then those of its next column
-  const int first = c0 + tid / split;
-  float4 v[BATCH];
-  auto load = [&](int c, int i) {
-    const float4* src = ws.o + four * p.R;
+  if (chunk >= chunks || c0 >= c1 || four * 4 >= rec.rows) return;
+  // threads that share a column's parts: a power of two, so that the block's columns just fit
+  const int step_log2 = per >= JOIN ? 7 : max(2, 32 - __clz(per - 1));
+  const int split = JOIN >> step_log2, step = 1 << step_log2;
+  const int mine = tid & (split - 1), first = c0 + (tid >> (7 - step_log2));
+  // part i is in slot 2 CTA of its group, the first one perhaps in the slot behind
+  const int cta0 = rec.first * p.members + rec.member;
+  const int64_t part_step = static_cast<int64_t>(2 * p.members) * (ROWS / 4) * p.R;
+  const float4* const o0 = ws.o + (2 * cta0 * (ROWS / 4) + four) * static_cast<int64_t>(p.R);
+  const int64_t odd = static_cast<int64_t>(rec.slot & 1) * (ROWS / 4) * p.R;
+  float4 v[2][4];
+  auto load = [&](int c, int i) {  // two columns, four parts
 #pragma unroll
-    for (int k = 0; k < BATCH; ++k) {
-      if (c < c1 && i < parts)
-        v[k] = src[static_cast<int64_t>(slot_of(i)) * (ROWS / 4) * p.R + c];
-      i += split;
-      if (i - mine >= most * split) i = mine, c += step;
+    for (int k = 0; k < 4; ++k, i += split) {
+      if (i >= parts) break;
+      const float4* src = o0 + i * part_step + (i == 0 ? odd : 0);
+      if (c < c1) v[0][k] = src[c];
+      if (c + step < c1) v[1][k] = src[c + step];
     }
   };
   load(first, mine);
   {
     const int row = four * 4 + warp;  // this warp's row
-    const float2* ml = ws.ml + row * 2 * ctas;
+    const float2* ml = ws.ml + (row * 2 * ctas + 2 * cta0);
     float* const weights = reinterpret_cast<float*>(weight) + warp;
     float top = -INFINITY, sum = 0.f;
     float2 x[MAX_PARTS / 32];
 #pragma unroll
     for (int j = 0; j < MAX_PARTS / 32; ++j) {
       if (j * 32 >= parts) break;
+      const int i = j * 32 + lane;
       x[j] = make_float2(-INFINITY, 0.f);
-      if (j * 32 + lane < parts) x[j] = ml[slot_of(j * 32 + lane)];
+      if (i < parts) x[j] = ml[i == 0 ? rec.slot & 1 : i * 2 * p.members];
     }
 #pragma unroll
     for (int j = 0; j < MAX_PARTS / 32; ++j) {
@@ -807,57 +807,54 @@ __global__ void __launch_bounds__(JOIN, 8)
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
     if (lane == 0) {
+      const int r = rec.row + row, t = r / p.H;
+      out_at[warp] = row < rec.rows
+                         ? (rec.token + t) * p.out_token + (r - t * p.H) * p.out_head
+                         : -1;
       reinterpret_cast<float*>(&inverse)[warp] = sum != 0.f ? 1.0f / sum : 0.f;
       if (p.lse && chunk == 0 && row < rec.rows)
-        p.lse[static_cast<int64_t>(rec.token) * p.H + rec.row + row] =
+        p.lse[static_cast<int64_t>(rec.token) * p.H + r] =
             sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
     }
   }
   __syncthreads();
-  const float4 inv = inverse;
-  __nv_bfloat16* out[4];
+#pragma unroll 1
+  for (int c = first; c - (tid >> (7 - step_log2)) < c1; c += 2 * step) {
+    float acc[2][4] = {};
+#pragma unroll 1
+    for (int i0 = mine; i0 - mine < parts; i0 += 4 * split) {
+      if (c != first || i0 != mine) load(c, i0);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int r = rec.row + four * 4 + k, t = r / p.H, h = r - t * p.H;
-    out[k] = four * 4 + k < rec.rows
-                 ? p.out + (rec.token + t) * p.out_token + h * p.out_head
-                 : nullptr;
-  }
-  // every thread of a warp goes through as many columns and parts as its first one
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  int c = first, i = mine;
-  for (int done = 0; done < columns * most; done += BATCH) {
-    if (done > 0) load(c, i);
-#pragma unroll
-    for (int k = 0; k < BATCH; ++k) {
-      if (done + k >= columns * most) break;
-      // where parts do not divide evenly some threads' last turn is empty
-      const bool there = c < c1 && i < parts;
-      if (there) {  // a part in which a row sees no key may have left no O
+      for (int k = 0; k < 4; ++k) {
+        const int i = i0 + k * split;
+        if (i >= parts) break;
         const float4 f = weight[i];
-        acc.x = f.x == 0.f ? acc.x : fmaf(f.x, v[k].x, acc.x);
-        acc.y = f.y == 0.f ? acc.y : fmaf(f.y, v[k].y, acc.y);
-        acc.z = f.z == 0.f ? acc.z : fmaf(f.z, v[k].z, acc.z);
-        acc.w = f.w == 0.f ? acc.w : fmaf(f.w, v[k].w, acc.w);
-      }
-      i += split;
-      if (i - mine >= most * split) {  // the column is done
-        for (int d = split >> 1; d; d >>= 1) {
-          acc.x += __shfl_down_sync(0xFFFFFFFFu, acc.x, d, split);
-          acc.y += __shfl_down_sync(0xFFFFFFFFu, acc.y, d, split);
-          acc.z += __shfl_down_sync(0xFFFFFFFFu, acc.z, d, split);
-          acc.w += __shfl_down_sync(0xFFFFFFFFu, acc.w, d, split);
-        }
-        if (mine == 0 && c < c1) {
-          const float x[4] = {acc.x * inv.x, acc.y * inv.y, acc.z * inv.z, acc.w * inv.w};
+        const float w[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-          for (int o = 0; o < 4; ++o)
-            if (out[o]) out[o][c] = __float2bfloat16(x[o]);
+        for (int n = 0; n < 2; ++n) {
+          if (c + n * step >= c1) break;
+          const float x[4] = {v[n][k].x, v[n][k].y, v[n][k].z, v[n][k].w};
+#pragma unroll
+          for (int r = 0; r < 4; ++r)  // a part in which a row sees no key may have left no O
+            acc[n][r] = w[r] == 0.f ? acc[n][r] : fmaf(w[r], x[r], acc[n][r]);
         }
-        acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        i = mine;
-        c += step;
       }
+    }
+    for (int d = split >> 1; d; d >>= 1)
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          acc[n][r] += __shfl_down_sync(0xFFFFFFFFu, acc[n][r], d, split);
+    if (mine == 0) {
+      const float inv[4] = {inverse.x, inverse.y, inverse.z, inverse.w};
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (out_at[r] >= 0) {
+          __nv_bfloat16* out = p.out + out_at[r] + c;
+          if (c < c1) out[0] = __float2bfloat16(acc[0][r] * inv[r]);
+          if (c + step < c1) out[step] = __float2bfloat16(acc[1][r] * inv[r]);
+        }
     }
   }
 }
