@@ -25,11 +25,14 @@ struct klt_latent {
 namespace {
 
 // ------------------------------------------------------------------ append
-// One block per token.  The latent part (R / 8 lanes of 8 values) is normed in registers between
-// the sum of its squares and its outputs; angles are fp64 up to the reduced turn (a position of
-// 10^6 leaves fp32 angles off by 0.03), one lane per pair, shared by the block; then the block's
-// threads turn the row's and the queries' pairs, 16 elements a thread.
-// Bound by memory: every value is read and written once.
+// A block takes one token, or two where there are many.  The latent part (R / 8 lanes of 8 values) is
+// normed in registers between the sum of its squares and its outputs; angles are fp64 up to the
+// reduced turn (at position 10^6 fp32 angles are off by 0.03), one lane per pair, shared by the block;
+// then the block's threads turn the row's and the queries' pairs, 16 elements a thread, whose loads
+// went out first.  Every value is read and written once: 8192 tokens of 512 + 64 columns and 64 heads
+// take 31 us (5.2 TB/s), bound by what six blocks an SM keep in flight (one token to a block, loads
+// behind the norm: 37; four or eight blocks an SM by registers: 33, 35); 16 tokens take 2.7.
+constexpr int APPEND_TWO = 1500;  // tokens from which on a block takes two
 struct AppendParams {
   const void* kv;
   const int64_t* positions;
@@ -42,8 +45,7 @@ struct AppendParams {
   __nv_bfloat16* q_out;
   int64_t ld_kv, page_stride, row_stride, ld_kv_out, q_token, q_head, q_out_token, q_out_head;
   int64_t n_slots;
-  int R, rope, H, page_log2;
-  bool neighbours;
+  int T, R, rope, H, page_log2;
   float eps;
 };
 
@@ -71,68 +73,90 @@ KLT_DEV void load8(const void* base, int64_t off, float* v) {
   }
 }
 // Turns the eight pairs of unit u: halves (a[e], b[e]), neighbours (a's four, then b's).
-KLT_DEV void turn8(float* a, float* b, const float2* cs, bool neighbours) {
+KLT_DEV void turn8(float* a, float* b, const float4* cs, bool neighbours) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     float* x = !neighbours ? &a[e] : e < 4 ? &a[2 * e] : &b[2 * e - 8];
     float* y = !neighbours ? &b[e] : x + 1;
-    const float2 w = cs[e];
-    const float t = *x * w.x - *y * w.y;
-    *y = *y * w.x + *x * w.y;
+    const float4 w = cs[e >> 1];
+    const float c = e & 1 ? w.z : w.x, s = e & 1 ? w.w : w.y;
+    const float t = *x * c - *y * s;
+    *y = *y * c + *x * s;
     *x = t;
   }
 }
 
-template <bool F32, bool NEIGHBOURS>
-__global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
-  __shared__ float2 turns[32];  // cos, sin
-  __shared__ float sums[2];
+template <bool F32, bool NEIGHBOURS, int TOKENS>
+__global__ void __launch_bounds__(256, 6) append_kernel(const AppendParams p) {
+  __shared__ float4 turns[TOKENS][16];  // cos, sin of two pairs
+  __shared__ float sums[TOKENS][2];
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t t = blockIdx.x;
-  const int chunks = p.R >> 3, units = p.rope >> 4, half = p.rope >> 1;
+  const int chunks = p.R >> 3, units = p.rope >> 4, half = p.rope >> 1, queries = p.H * units;
   // first element of a unit's second eight, from the first's
   const int second = NEIGHBOURS ? 8 : half, step = NEIGHBOURS ? 16 : 8;
+  const int t0 = blockIdx.x * TOKENS;
+  // the first units of this thread's queries are on their way while the rows are normed
+  const int h0 = tid / units, u0 = tid - h0 * units;
+  auto query = [&](int k, int64_t token, int64_t head, int h, int u) {
+    return (t0 + k) * token + h * head + u * step;
+  };
+  uint4 qa[TOKENS], qb[TOKENS];
+#pragma unroll
+  for (int k = 0; k < TOKENS; ++k)
+    if (p.q && tid < queries && t0 + k < p.T) {
+      const __nv_bfloat16* src = p.q + query(k, p.q_token, p.q_head, h0, u0);
+      qa[k] = *reinterpret_cast<const uint4*>(src);
+      qb[k] = *reinterpret_cast<const uint4*>(src + second);
+    }
+  // two warps norm a row, the last ones find the angles
+  const int mine = warp >> 1, at = tid & 63;
   float c[8] = {};
-  if (warp < 2) {
-    if (tid < chunks) load8<F32>(p.kv, t * p.ld_kv + tid * 8, c);
+  if (mine < TOKENS && t0 + mine < p.T) {
+    if (at < chunks) load8<F32>(p.kv, (t0 + mine) * p.ld_kv + at * 8, c);
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) s = fmaf(c[i], c[i], s);
 #pragma unroll
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-    if (lane == 0) sums[warp] = s;
-  } else if (warp == 7 && lane < half) {
-    const double turn = static_cast<double>(p.positions[t]) *
+    if (lane == 0) sums[mine][warp & 1] = s;
+  }
+  const int turner = static_cast<int>(blockDim.x >> 5) - 1 - warp;
+  if (turner < TOKENS && t0 + turner < p.T && lane < half) {
+    const double turn = static_cast<double>(p.positions[t0 + turner]) *
                         static_cast<double>(p.inv_freq[lane]) * 0.15915494309189535;
     float s, cosine;
     sincospif(2.0f * static_cast<float>(turn - rint(turn)), &s, &cosine);
-    turns[lane] = make_float2(cosine, s);
+    reinterpret_cast<float2*>(turns[turner])[lane] = make_float2(cosine, s);
   }
   __syncthreads();
-  const int64_t slot = p.cache ? p.slots[t] : -1;
-  const bool stored = slot >= 0 && slot < p.n_slots;
-  __nv_bfloat16* row =
-      stored ? p.cache + (slot >> p.page_log2) * p.page_stride +
-                   (slot & ((1ll << p.page_log2) - 1)) * p.row_stride
-             : nullptr;
-  __nv_bfloat16* dense = p.kv_out ? p.kv_out + t * p.ld_kv_out : nullptr;
-  if (tid < chunks) {
-    const float r = 1.0f / sqrtf((sums[0] + sums[1]) / static_cast<float>(p.R) + p.eps);
+  auto row_of = [&](int k) -> __nv_bfloat16* {
+    const int64_t slot = p.cache ? p.slots[t0 + k] : -1;
+    if (slot < 0 || slot >= p.n_slots) return nullptr;
+    return p.cache + (slot >> p.page_log2) * p.page_stride +
+           (slot & ((1ll << p.page_log2) - 1)) * p.row_stride;
+  };
+  const int part = tid - 64 * TOKENS;  // threads that turn the rows' position parts
+  if (mine < TOKENS && t0 + mine < p.T && at < chunks) {
+    __nv_bfloat16* const row = row_of(mine);
+    __nv_bfloat16* const dense = p.kv_out ? p.kv_out + (t0 + mine) * p.ld_kv_out : nullptr;
+    const float r = 1.0f / sqrtf((sums[mine][0] + sums[mine][1]) / static_cast<float>(p.R) + p.eps);
     float g[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
-    if (p.gamma) unpack8(*reinterpret_cast<const uint4*>(p.gamma + tid * 8), g);
+    if (p.gamma) unpack8(*reinterpret_cast<const uint4*>(p.gamma + at * 8), g);
 #pragma unroll
     for (int i = 0; i < 8; ++i) c[i] = c[i] * r * g[i];
     const uint4 w = pack8(c);
-    if (row) *reinterpret_cast<uint4*>(row + tid * 8) = w;
-    if (dense) *reinterpret_cast<uint4*>(dense + tid * 8) = w;
-  } else if (tid < chunks + units && (row || dense)) {
-    const int u = tid - chunks, e = p.R + u * step;
+    if (row) *reinterpret_cast<uint4*>(row + at * 8) = w;
+    if (dense) *reinterpret_cast<uint4*>(dense + at * 8) = w;
+  } else if (part >= 0 && part < TOKENS * units && t0 + part / units < p.T) {
+    const int k = part / units, u = part - k * units, e = p.R + u * step;
+    __nv_bfloat16* const row = row_of(k);
+    __nv_bfloat16* const dense = p.kv_out ? p.kv_out + (t0 + k) * p.ld_kv_out : nullptr;
     float a[8], b[8];
-    load8<F32>(p.kv, t * p.ld_kv + e, a);
-    load8<F32>(p.kv, t * p.ld_kv + e + second, b);
-    turn8(a, b, turns + u * 8, NEIGHBOURS);
+    load8<F32>(p.kv, (t0 + k) * p.ld_kv + e, a);
+    load8<F32>(p.kv, (t0 + k) * p.ld_kv + e + second, b);
+    turn8(a, b, turns[k] + u * 4, NEIGHBOURS);
     const uint4 wa = pack8(a), wb = pack8(b);
     if (row) {
       *reinterpret_cast<uint4*>(row + e) = wa;
@@ -144,16 +168,25 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
     }
   }
   if (!p.q) return;
-  for (int i = tid; i < p.H * units; i += 256) {
-    const int h = i / units, u = i - h * units;
-    const __nv_bfloat16* src = p.q + t * p.q_token + h * p.q_head + u * step;
-    __nv_bfloat16* dst = p.q_out + t * p.q_out_token + h * p.q_out_head + u * step;
-    float a[8], b[8];
-    load8<false>(src, 0, a);
-    load8<false>(src, second, b);
-    turn8(a, b, turns + u * 8, NEIGHBOURS);
-    *reinterpret_cast<uint4*>(dst) = pack8(a);
-    *reinterpret_cast<uint4*>(dst + second) = pack8(b);
+#pragma unroll
+  for (int k = 0; k < TOKENS; ++k) {
+    if (t0 + k >= p.T) break;
+    int h = h0, u = u0;
+    for (int i = tid; i < queries; i += blockDim.x) {
+      if (i != tid) {
+        h = i / units, u = i - h * units;
+        const __nv_bfloat16* src = p.q + query(k, p.q_token, p.q_head, h, u);
+        qa[k] = *reinterpret_cast<const uint4*>(src);
+        qb[k] = *reinterpret_cast<const uint4*>(src + second);
+      }
+      float a[8], b[8];
+      unpack8(qa[k], a);
+      unpack8(qb[k], b);
+      turn8(a, b, turns[k] + u * 4, NEIGHBOURS);
+      __nv_bfloat16* dst = p.q_out + query(k, p.q_out_token, p.q_out_head, h, u);
+      *reinterpret_cast<uint4*>(dst) = pack8(a);
+      *reinterpret_cast<uint4*>(dst + second) = pack8(b);
+    }
   }
 }
 
@@ -359,6 +392,7 @@ int klt_latent_append(klt_latent* h, const klt_latent_append_args* a, void* stre
   p.q_out_token = a->q_out_token;
   p.q_out_head = a->q_out_head;
   p.n_slots = a->pages << h->page_log2;
+  p.T = a->T;
   p.R = d.latent;
   p.rope = d.rope;
   p.H = d.heads;
@@ -366,10 +400,17 @@ int klt_latent_append(klt_latent* h, const klt_latent_append_args* a, void* stre
   p.eps = d.eps;
   const bool f32 = a->kv_dtype == KLT_DT_F32, nb = d.pairs == KLT_ROPE_NEIGHBOURS;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return outcome(f32 ? nb ? launch_pdl(append_kernel<true, true>, a->T, 256, s, p)
-                          : launch_pdl(append_kernel<true, false>, a->T, 256, s, p)
-                 : nb ? launch_pdl(append_kernel<false, true>, a->T, 256, s, p)
-                      : launch_pdl(append_kernel<false, false>, a->T, 256, s, p));
+  // four warps where the queries' units are no more; two tokens to a block where there are enough
+  // of them to fill the SMs that way
+  const unsigned threads = p.q && d.heads * (d.rope / 16) > 128 ? 256 : 128;
+  const bool two = threads == 256 && a->T > APPEND_TWO;
+  const unsigned grid = two ? (a->T + 1u) / 2 : a->T;
+  auto launch = [&](auto kernel) { return outcome(launch_pdl(kernel, grid, threads, s, p)); };
+  if (two)
+    return f32 ? nb ? launch(append_kernel<true, true, 2>) : launch(append_kernel<true, false, 2>)
+               : nb ? launch(append_kernel<false, true, 2>) : launch(append_kernel<false, false, 2>);
+  return f32 ? nb ? launch(append_kernel<true, true, 1>) : launch(append_kernel<true, false, 1>)
+             : nb ? launch(append_kernel<false, true, 1>) : launch(append_kernel<false, false, 1>);
 }
 
 int klt_latent_workspace(const klt_latent* h, int32_t B, int32_t T, uint64_t* bytes) {

@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   __shared__ float tops[2][ROWS];  // of each half of a tile's keys: maxima; at the end sums
   __shared__ int64_t out_at[ROWS];
   __shared__ long long sums[THREADS / 32];
-  __shared__ int counts[THREADS / 32];
+  __shared__ int counts[THREADS / 32], needs[THREADS / 32];
   __shared__ long long found_base;
   __shared__ int found_b;
   __shared__ uint32_t tmem_holder;
@@ -259,20 +259,23 @@ __global__ void __launch_bounds__(THREADS, 1)
     walk.parts = 0;
     walk.lo = walk.hi = 0;
     if (p.B <= THREADS && items < groups) {
-      const long long all = W - static_cast<long long>(items) * EXTRA;  // tiles
-      const long long least = max(static_cast<long long>(MIN_TILES), (all + groups - 1) / groups);
-      const long long most = max(least, (all + groups - items - 1) / (groups - items));
+      // the tiles, in units of 8 where 32 bits do not hold them
+      const long long all = W - static_cast<long long>(items) * EXTRA;
+      const int shift = all >> 31 ? 3 : 0;
+      const uint32_t sum = static_cast<uint32_t>((all + (1 << shift) - 1) >> shift);
+      const uint32_t least = max(static_cast<uint32_t>(MIN_TILES), (sum + groups - 1) / groups);
+      const uint32_t most = max(least, (sum + groups - items - 1) / (groups - items));
       auto candidate = [&](int i) {
-        return static_cast<int>(min(least + (most - least) * i / (WARPS - 1), 0x7FFFFFFFll));
+        return static_cast<int>((least + (most - least) / (WARPS - 1) * i +
+                                 (most - least) % (WARPS - 1) * i / (WARPS - 1)) << shift);
       };
       int t = candidate(warp), need = 0;
       for (int b = lane; b < p.B; b += 32) need += seqs[b].x * ((seqs[b].y + t - 1) / t);
       need = __reduce_add_sync(0xFFFFFFFFu, need);
-      __syncthreads();  // counts have been read
-      if (lane == 0) counts[warp] = need;
+      if (lane == 0) needs[warp] = need;
       __syncthreads();
       int i = 0;
-      while (i < WARPS - 1 && counts[i] > groups) ++i;
+      while (i < WARPS - 1 && needs[i] > groups) ++i;
       t = candidate(i);
       int before = 0;
       for (int b0 = 0; b0 < p.B; b0 += 32) {
@@ -377,6 +380,13 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
           for (int x = 0; x < 4; ++x) page[x] = ahead[x];
           pages_of(t + 1, ahead);
+          if (it >= STAGES && box_keys == KEYS && page[0] >= 0 && page[0] < p.pages) {
+            // into L2 while its stage is still in use (3 % off large batches; small pages take too
+            // many of these to gain)
+            for (int c = 0; c < NB; c += 2)
+              tma_prefetch_4d(&latents, 0, t * KEYS & page_mask, c, page[0]);
+            tma_prefetch_3d(&ropes, 0, t * KEYS & page_mask, page[0]);
+          }
           const int st = it % STAGES, left = min(KEYS, w.len - t * KEYS);
           const int boxes = (left + box_keys - 1) >> box_log2;
           for (cut = 0; cut <= NJ; ++cut) {

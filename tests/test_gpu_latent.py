@@ -41,7 +41,10 @@ def randn(seed, *shape, dtype=torch.bfloat16):
     (5, 3, 384, 48, 32, torch.float32, "neighbours", True),
     (33, 128, 256, 32, 1024, torch.bfloat16, "neighbours", False),
     (70, 40, 512, 64, 16, torch.float32, "halves", False),
-    (19, 256, 128, 48, 128, torch.bfloat16, "halves", True)])
+    (19, 256, 128, 48, 128, torch.bfloat16, "halves", True),
+    # two tokens to a block, the last one alone
+    (1601, 36, 128, 64, 32, torch.bfloat16, "halves", True),
+    (1512, 65, 256, 48, 16, torch.float32, "neighbours", False)])
 def test_append(T, heads, latent, rope, page, dtype, pairs, gamma):
     g = randn(1, latent).abs() + 0.5 if gamma else None
     at = layer(heads, latent, rope, page=page, gamma=g, pairs=pairs)
