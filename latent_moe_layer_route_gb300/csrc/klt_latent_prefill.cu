@@ -12,11 +12,15 @@
 // warp 3 finds the next unit (512 queries of a sequence and head), warps 4 to 7 and 8 to 11 do the
 // tiles' softmax.  The grid has a pair for every unit; a running pair takes over units that have not
 // started (clusterlaunchcontrol), so that it loads the next one's operands and computes its first
-// scores while it writes the results of this one, and long and short sequences even out.  Their code is kept short (S is read twice, 64
-// columns at a time): unrolled over the 128 columns it pushed the issuing thread's out of the
-// instruction caches, which then took 5,500 cycles for the 2,560 of a round.  O is rescaled only
-// when a row's maximum has grown by 2^8 (by the row's own thread, which knows that no product runs
-// on it).
+// scores while it writes the results of this one, and long and short sequences even out.
+//
+// The softmax goes over a tile's scores once, 64 keys at a time: they are weighted by the maximum in
+// use while their own is found, and once more in the rare case that it has grown by 2^8 (then O is
+// rescaled too).  Each half's weights are handed to the tensor core as they are written.  8192 tokens
+// of 64 heads take 807 us (1.70 PFLOP/s, 88 % of a large library product's rate), with the maximum
+// found in a pass of its own 895; a quarter of the exponentials by a polynomial 937, two threads to a
+// row 986: the exponential unit is not what bounds this on sm_103a, the way of a tile through scores,
+// softmax and values is.
 #include "klt_latent.cuh"
 
 #include "../../include/klt.h"
@@ -85,13 +89,20 @@ KLT_DEV bool read_next(const void* answer, int& x, int& y) {
   y = static_cast<int>(b);
   return ok != 0;
 }
-// Unit number `unit` of head h, by a whole warp, 32 sequences at a time; a sequence's last units,
-// which see most keys, come first.  Numbers past the last unit have no tiles.
-KLT_DEV Unit find_unit(const PrefillParams& p, int unit, int h) {
+// Where a search was: 32 sequences from b0 on, units before them.
+struct Place {
+  int b0 = 0, before = 0;
+};
+// Unit number `number` of head h, by a whole warp, 32 sequences at a time from where the search
+// before ended (numbers mostly ascend); a sequence's last units, which see most keys, come first.
+// Numbers past the last unit have no queries.
+KLT_DEV Unit find_unit(const PrefillParams& p, int number, int h, Place& at) {
   const int lane = lane_id();
   Unit u = {};
   u.h = h;
-  for (int b0 = 0; b0 < p.B; b0 += 32) {
+  if (number < at.before) at = Place();
+  for (; at.b0 < p.B; at.b0 += 32) {
+    const int b0 = at.b0, unit = number - at.before;
     int lo = 0, hi = 0, n = 0;
     if (b0 + lane < p.B) {
       range_of(p.cu_q, b0 + lane, p.T, lo, hi);
@@ -123,7 +134,7 @@ KLT_DEV Unit find_unit(const PrefillParams& p, int unit, int h) {
       u.tiles1 = tiles_of(1);
       break;
     }
-    unit -= __shfl_sync(0xFFFFFFFFu, in, 31);
+    at.before += __shfl_sync(0xFFFFFFFFu, in, 31);
   }
   return u;
 }
@@ -280,7 +291,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     // ------------------------------------------------ units
     // The next one is asked for when this one's copies are issued, not earlier: other pairs may be
     // free first.  Numbers without tiles and queries are passed over.
-    Unit u = find_unit(p, blockIdx.x >> 1, blockIdx.y);
+    Place place;
+    Unit u = find_unit(p, blockIdx.x >> 1, blockIdx.y, place);
     bool ok = true, more = true;
     for (int i = 0, k = 0; more; ++i) {  // units; answers
       if (i > 0) ok = wait(&bars.loaded, i - 1);
@@ -302,7 +314,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         if (rank == 1 && lane == 0) mbar_arrive_cluster_release(first(&bars.next_read));
         ++k;
         if (more) {
-          u = find_unit(p, x >> 1, y);
+          u = find_unit(p, x >> 1, y, place);
           if (u.n > 0) break;
         }
       }
