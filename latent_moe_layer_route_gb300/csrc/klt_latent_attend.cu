@@ -387,27 +387,40 @@ __global__ void __launch_bounds__(THREADS, 1)
               tma_prefetch_4d(&latents, 0, t * KEYS & page_mask, c, page[0]);
             tma_prefetch_3d(&ropes, 0, t * KEYS & page_mask, page[0]);
           }
-          const int st = it % STAGES, left = min(KEYS, w.len - t * KEYS);
-          const int boxes = (left + box_keys - 1) >> box_log2;
-          for (cut = 0; cut <= NJ; ++cut) {
-            const int i = cut;
-            ok = wait(&bars.empty[st][i], (it / STAGES) + 1);
-            if (!ok) break;
-            const int wide = i < NJ ? 2 : 1;
-            mbar_arrive_expect_tx(&bars.full[st][i], boxes * wide * (box_keys * 128));
+          const int st = it % STAGES;
+          uint8_t* const stage = ks + st * MAX_BOXES * BOX;
+          if (box_keys == KEYS) {  // both boxes of 128 columns by one copy
+            const int row = t * KEYS & page_mask;
+            const int at = page[0] >= 0 && page[0] < p.pages ? page[0] : p.pages;
+            for (cut = 0; cut <= NJ; ++cut) {
+              ok = wait(&bars.empty[st][cut], (it / STAGES) + 1);
+              if (!ok) break;
+              uint64_t* full = &bars.full[st][cut];
+              mbar_arrive_expect_tx(full, cut < NJ ? 2 * BOX : BOX);
+              if (cut < NJ)
+                tma_load_4d(stage + 2 * cut * BOX, &latents, full, 0, row, 2 * cut, at);
+              else
+                tma_load_3d(stage + 2 * cut * BOX, &ropes, full, 0, row, at);
+            }
+          } else {
+            const int boxes = (min(KEYS, w.len - t * KEYS) + box_keys - 1) >> box_log2;
+            for (cut = 0; cut <= NJ; ++cut) {
+              ok = wait(&bars.empty[st][cut], (it / STAGES) + 1);
+              if (!ok) break;
+              uint64_t* full = &bars.full[st][cut];
+              mbar_arrive_expect_tx(full, boxes * (cut < NJ ? 2 : 1) * (box_keys * 128));
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              if (x >= boxes) break;
-              const int key = t * KEYS + (x << box_log2);
-              const int at = page[x] >= 0 && page[x] < p.pages ? page[x] : p.pages;
-              uint8_t* dst = ks + (st * MAX_BOXES + 2 * i) * BOX + x * box_keys * 128;
-              if (i == NJ) {
-                tma_load_3d(dst, &ropes, &bars.full[st][i], 0, key & page_mask, at);
-              } else {  // both boxes of 64 columns where a page fills their rows
-                tma_load_4d(dst, &latents, &bars.full[st][i], 0, key & page_mask, 2 * i, at);
-                if (box_keys < KEYS)
-                  tma_load_4d(dst + BOX, &latents, &bars.full[st][i], 0, key & page_mask,
-                              2 * i + 1, at);
+              for (int x = 0; x < 4; ++x) {
+                if (x >= boxes) break;
+                const int row = (t * KEYS + (x << box_log2)) & page_mask;
+                const int at = page[x] >= 0 && page[x] < p.pages ? page[x] : p.pages;
+                uint8_t* dst = stage + 2 * cut * BOX + x * box_keys * 128;
+                if (cut < NJ) {
+                  tma_load_4d(dst, &latents, full, 0, row, 2 * cut, at);
+                  tma_load_4d(dst + BOX, &latents, full, 0, row, 2 * cut + 1, at);
+                } else {
+                  tma_load_3d(dst, &ropes, full, 0, row, at);
+                }
               }
             }
           }
