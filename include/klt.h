@@ -449,9 +449,10 @@ int klt_linear_destroy(klt_linear* h);
  *     s = scale * (q_nope . W_uk c + q_rope . r),  values W_uv c.
  * The absorbed form reads the rows themselves from a paged cache: its queries are
  * [W_uk^T q_nope | q_rope], its values c, and W_uv is applied to its result.  The expanded form
- * takes every head's keys and values as their projection left them.  Conventions as for the
- * operators above, except that rows start on 16 bytes: pointers are 16-byte aligned and strides
- * (elements) multiples of 8 where they are of bf16 rows, of 4 where of fp32 rows. */
+ * takes every head's keys and values as their projection left them.  Forward only: there are no
+ * gradients.  Conventions as for the operators above, except that rows start on 16 bytes: pointers
+ * are 16-byte aligned and strides (elements) multiples of 8 where they are of bf16 rows, of 4 where
+ * of fp32 rows. */
 enum klt_rope_pairs {
   KLT_ROPE_HALVES = 0,    /* element i turns with i + rope / 2                             */
   KLT_ROPE_NEIGHBOURS = 1 /* element 2 i turns with 2 i + 1                                */
@@ -485,7 +486,8 @@ int klt_latent_create(const klt_latent_dims* d, const float* inv_freq, const voi
 typedef struct klt_latent_debug {
   int32_t stall_after_tiles; /* > 0: every copy producer stops after that many tiles of keys, so
                                 the waits on its data run out (klt_latent_status)         */
-  int32_t timeout_ms;        /* bound of every on-device wait (0 = 1000 ms)               */
+  int32_t timeout_ms;        /* bound of every on-device wait (0 = 1000 ms); waits that may last
+                                for a sequence's keys are given some 8 us more per tile   */
 } klt_latent_debug;
 
 /* New tokens' rows, normed and rotated, into the cache, and the queries' position parts rotated:
@@ -550,8 +552,8 @@ int klt_latent_workspace(const klt_latent* h, int32_t B, int32_t T, uint64_t* by
  * Errors: KLT_ERR_INVALID_ARG (null handle, args or pointer; B < 1 or T < 0; T != B without cu_q;
  * max_pages or pages < 0; workspace too small; negative stride or table stride shorter than a
  * row; cache or output rows that overlap; bad debug value; another device current than at
- * creation), KLT_ERR_UNSUPPORTED (more than 2^31 - 1 slots of the cache, tokens of a table's row,
- * or query rows; a stride of 2^38 or more), KLT_ERR_ALIGN, KLT_ERR_CUDA.  Expired device waits:
+ * creation), KLT_ERR_UNSUPPORTED (more than 2^31 - 4097 slots of the cache, tokens of a table's
+ * row, or T * heads; a stride of 2^38 or more), KLT_ERR_ALIGN, KLT_ERR_CUDA.  Expired device waits:
  * klt_latent_status. */
 int klt_latent_attend(klt_latent* h, const klt_latent_attend_args* a, const klt_latent_debug* dbg,
                       void* stream);
@@ -578,8 +580,8 @@ typedef struct klt_latent_prefill_args {
 
 /* Run klt_latent_prefill_args on `stream`; one launch.  T == 0 launches nothing.
  * Errors: as klt_latent_attend; KLT_ERR_INVALID_ARG also for a stride of 0 of an input with more
- * than one row in that direction; KLT_ERR_UNSUPPORTED (T * heads above 2^31 - 1, more query tiles
- * than a grid takes, a stride of 2^38 or more). */
+ * than one row in that direction; KLT_ERR_UNSUPPORTED (T * heads or S above 2^31 - 4097, more
+ * query tiles than a grid takes, a stride of 2^38 or more). */
 int klt_latent_prefill(klt_latent* h, const klt_latent_prefill_args* a,
                        const klt_latent_debug* dbg, void* stream);
 

@@ -202,6 +202,7 @@ bool disjoint(int64_t n, int64_t a, int64_t m, int64_t b, int64_t width) {
   }
   return a < b ? a >= width && (b - width) / a >= n - 1 : b >= width && (a - width) / b >= m - 1;
 }
+constexpr int64_t MOST = 0x7FFFFFFFll - 4096;  // rows, with room to round up to tiles
 constexpr int64_t MAX_STRIDE = 1ll << 38;  // elements: the tensor maps' strides end at 2^40 bytes
 
 int check_dims(const klt_latent_dims* d) {
@@ -438,9 +439,8 @@ int klt_latent_attend(klt_latent* h, const klt_latent_attend_args* a, const klt_
       !disjoint(a->pages, a->page_stride, d.page, a->row_stride, width) ||
       !disjoint(a->T, a->out_token, d.heads, a->out_head, d.latent))
     return KLT_ERR_INVALID_ARG;
-  const int64_t most = 0x7FFFFFFFll - 4096;  // room to round up to tiles
-  if (a->pages > (most >> h->page_log2) || a->max_pages > (most >> h->page_log2) ||
-      a->T > most / d.heads || a->page_stride >= MAX_STRIDE ||
+  if (a->pages > (MOST >> h->page_log2) || a->max_pages > (MOST >> h->page_log2) ||
+      a->T > MOST / d.heads || a->page_stride >= MAX_STRIDE ||
       a->row_stride >= MAX_STRIDE || a->q_token >= MAX_STRIDE || a->q_head >= MAX_STRIDE)
     return KLT_ERR_UNSUPPORTED;
   if (!aligned(a->q, 16) || !aligned(a->cache, 16) || !aligned(a->out, 16) ||
@@ -523,7 +523,7 @@ int klt_latent_prefill(klt_latent* h, const klt_latent_prefill_args* a,
     return KLT_ERR_INVALID_ARG;
   if (!disjoint(a->T, a->out_token, d.heads, a->out_head, d.value)) return KLT_ERR_INVALID_ARG;
   const int64_t tiles = (a->T + PREFILL_ROWS - 1ll) / PREFILL_ROWS + a->B;
-  if (a->T > 0x7FFFFFFFll / d.heads || tiles > 0x3FFFFFFFll ||
+  if (a->T > MOST / d.heads || a->S > MOST || tiles > 0x3FFFFFFFll ||
       a->q_token >= MAX_STRIDE || a->q_head >= MAX_STRIDE || a->k_token >= MAX_STRIDE ||
       a->k_head >= MAX_STRIDE || a->v_token >= MAX_STRIDE || a->v_head >= MAX_STRIDE ||
       a->ld_k_rope >= MAX_STRIDE)
@@ -555,6 +555,8 @@ int klt_latent_prefill(klt_latent* h, const klt_latent_prefill_args* a,
   p.stall = dbg ? dbg->stall_after_tiles : 0;
   p.err = h->err;
   p.timeout = timeout_cycles(dbg);
+  // several of its waits last for a unit: its threads that have no queries, the next unit's search
+  p.timeout += (a->S / 128 + 1) * TILE_CYCLES;
   CUtensorMap q, k = {}, v = {}, k_rope = {};
   if (!encode_rows(&q, a->q, d.nope + d.rope, d.heads, a->q_head, a->T, a->q_token, 1, 128))
     return KLT_ERR_CUDA;

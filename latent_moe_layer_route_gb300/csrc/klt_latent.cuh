@@ -42,6 +42,10 @@ struct PrefillParams {
   long long timeout;
 };
 
+// Added per tile of keys to the bounds of waits that last for all of a sequence's: some five times
+// what a tile takes.
+constexpr long long TILE_CYCLES = 16384;
+
 // The range cu[b] .. cu[b + 1] cut to 0 .. n (whatever cu holds).
 KLT_DEV void range_of(const int* cu, int b, int n, int& lo, int& hi) {
   lo = min(max(cu[b], 0), n);
@@ -150,19 +154,6 @@ KLT_DEV void mma4_bf16_mn(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
   mma_bf16(d, a + 256, b + 4, idesc, 1);
   mma_bf16(d, a + 384, b + 6, idesc, 1);
 }
-// Whether phase `phase` (its parity counts) of `bar` is complete.
-KLT_DEV bool mbar_test(uint64_t* bar, int phase) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(phase & 1)
-      : "memory");
-  return ok != 0;
-}
-
 // Asynchronous copy of `bytes` (16 or 0) from global to shared memory; the rest of 16 is zeros.
 KLT_DEV void cp_async16(void* dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),

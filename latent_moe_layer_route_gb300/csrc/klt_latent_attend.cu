@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   } else if (warp == 2) {
     // ------------------------------------------------ queries
-    int piece = 0;
+    int piece = 0, tiles = 0;  // pieces so far; tiles of the last one
     bool ok = true, left[2] = {false, false};
     while (walk.next(p, w)) {
       if (w.rows == 0) continue;
@@ -532,8 +532,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
       if (!ok || w.t0 == w.t1) continue;
-      ok = wait(&bars.q_free, piece + 1);
+      // until the piece before is through, however long it is
+      ok = mbar_wait(&bars.q_free, (piece + 1) & 1, stop, p.err, p.timeout + tiles * TILE_CYCLES);
       ok = __all_sync(0xFFFFFFFFu, ok);
+      tiles = w.t1 - w.t0;
       if (!ok) continue;
       ++piece;
       if (p.q_box) {

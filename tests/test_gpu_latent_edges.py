@@ -346,6 +346,27 @@ def test_waits_that_run_out(op, stall):
     bad.at.close()
 
 
+def test_bounds_of_waits_grow_with_a_sequence():
+    """Waits that last for all keys of a sequence do not run out for its length alone: the queries'
+    copies of a group's second item, and threads of the expanded form without queries."""
+    dbg = B.KltLatentDebug(timeout_ms=1)
+    at, length = layer(64, 512, 64), 1 << 17  # 2048 tiles of some 1.4 us
+    cache = randn(91, 8, 64, 576).cuda()
+    args = [randn(92, 160, 64, 576).cuda(), cache, i32([[i % 8 for i in range(length // 64)]]),
+            i32([length]), i32([0, 160])]
+    want = [t.clone() for t in at.attend(*args)]
+    got = at.attend(*args, debug=dbg)
+    torch.cuda.synchronize()
+    assert at.status() == B.KLT_OK and all(torch.equal(x, y) for x, y in zip(got, want))
+    at, length = layer(1, nope=64, value=64), 1 << 20  # 8192 tiles of some 0.5 us
+    row = randn(93, 1 << 14, 1, 64).cuda().repeat(length >> 14, 1, 1)
+    args = [randn(94, 1, 1, 128).cuda(), row, row, row[:, 0], i32([0, 1]), i32([0, length])]
+    want = [t.clone() for t in at.prefill(*args)]
+    got = at.prefill(*args, debug=dbg)
+    torch.cuda.synchronize()
+    assert at.status() == B.KLT_OK and all(torch.equal(x, y) for x, y in zip(got, want))
+
+
 # ---------------------------------------------------------------- refusals
 
 def test_binding_refuses(lib=None):

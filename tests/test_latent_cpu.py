@@ -162,6 +162,15 @@ def test_prefill_arguments(lib, handle, kw, code):
     assert _prefill(lib, handle, **kw) == code
 
 
+@pytest.mark.parametrize("n", [2**31 - 1, 2**31 - 4096])
+def test_sizes_leave_room_to_round_up(lib, handle, n):
+    """Rows are counted in 32 bits, rounded up to whole tiles."""
+    assert _prefill(lib, handle, S=n) == UNSUPPORTED
+    assert _prefill(lib, handle, T=n // 4 + 1) == UNSUPPORTED
+    assert _attend(lib, handle, T=n // 4 + 1) == UNSUPPORTED
+    assert _attend(lib, handle, pages=n // 64 + 1) == UNSUPPORTED
+
+
 @pytest.mark.parametrize("dbg", [dict(stall_after_tiles=-1), dict(timeout_ms=-1)])
 def test_debug_arguments(lib, handle, dbg):
     dbg = B.KltLatentDebug(**dbg)
