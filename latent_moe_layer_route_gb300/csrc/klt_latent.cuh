@@ -36,6 +36,7 @@ struct PrefillParams {
   int B, T, S, H;
   int nope, rope, value;
   int causal;
+  int side;              // heads whose units are started side by side
   float scale;           // as above
   int stall;
   int* err;

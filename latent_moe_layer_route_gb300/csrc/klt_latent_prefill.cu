@@ -7,6 +7,9 @@
 // which the tensor core reads from both: half of the copies, and half of the shared-memory reads
 // that bound these products in one CTA (128 x 128 x 16 reads 8 KB in its 64 cycles).  The two
 // tiles take turns: while the threads of one do its softmax, the tensor core works on the other.
+// Up to 256 queries (a sequence's last ones, or all of a short one) are one tile whose keys are shared
+// out between the two groups of threads, even and odd tiles; at the end either takes half of the
+// columns of both results (128 queries of 4 x 16 K keys, 32 heads: 247 us, one group alone 435).
 //
 // Roles in a CTA: warp 0 copies (three stages of 40 KB), warp 1 of the first CTA issues products,
 // warp 3 finds the next unit (512 queries of a sequence and head), warps 4 to 7 and 8 to 11 do the
@@ -17,10 +20,13 @@
 // The softmax goes over a tile's scores once, 64 keys at a time: they are weighted by the maximum in
 // use while their own is found, and once more in the rare case that it has grown by 2^8 (then O is
 // rescaled too).  Each half's weights are handed to the tensor core as they are written.  8192 tokens
-// of 64 heads take 807 us (1.70 PFLOP/s, 88 % of a large library product's rate), with the maximum
-// found in a pass of its own 895; a quarter of the exponentials by a polynomial 937, two threads to a
-// row 986: the exponential unit is not what bounds this on sm_103a, the way of a tile through scores,
-// softmax and values is.
+// of 64 heads take 780 us (1.76 PFLOP/s, 91 % of a large library product's rate).  With the maximum
+// found in a pass of its own, the kernel of 807 us before took 895; a quarter of the exponentials by
+// a polynomial 937, two threads to a row 986: the exponential unit is not what bounds this on
+// sm_103a, the way of a tile through scores, softmax and values is (some 4,300 cycles where a group
+// is alone, of which its softmax 2,300).  Hence short sequences cost most: 12 ragged ones of up to
+// 2500 tokens 262 us (0.93 PFLOP/s).  First scores of the next unit issued while the second group
+// ends this one: no gain; the first tile's maximum found ahead of its weights: 5 % slower.
 #include "klt_latent.cuh"
 
 #include "../../include/klt.h"
@@ -36,12 +42,15 @@ constexpr int THREADS = 384;
 constexpr int SMEM = 1024 + 2 * Q_BOXES * BOX + STAGES * STAGE;
 static_assert(4 * ROWS == PREFILL_ROWS, "");
 
-// 512 queries of a sequence and head.
+// 512 queries of a sequence and head as two tiles that go over the same keys; or up to 256 as one,
+// whose even tiles of keys are the first softmax group's and odd ones the second's.
 struct Unit {
   int q0, n;           // the sequence's first query, its queries
   int k0, len;         // ... keys
   int r0, h;           // the unit's first query in the sequence, its head
-  int tiles0, tiles1;  // tiles of keys that the last query of each tile of queries sees
+  int split;           // one tile of queries
+  int nt;              // tiles of keys that the last query sees
+  int tiles0, tiles1;  // ... of each group
   int last;            // no unit: the pair is done
 };
 
@@ -56,6 +65,7 @@ struct Bars {
   uint64_t v_last[STAGES];                    // each: values of a sequence's ragged last tile
   uint64_t cleared;                           // ... cleared behind the sequence in both
   uint64_t unit_full[2], unit_empty[2];       // each
+  uint64_t shared[2], shared_read[2];         // each: a group's sums are there, are read
   uint64_t loaded;                            // each: a unit's copies are issued
   uint64_t next_full[2];                      // each: the answer about the next unit
   uint64_t next_read;                         // the second CTA has read it
@@ -73,20 +83,18 @@ KLT_DEV void ask_next(void* answer, uint64_t* bar) {
       : "memory");
 }
 // The first CTA of the cluster that was given, or false.
-KLT_DEV bool read_next(const void* answer, int& x, int& y) {
-  uint32_t ok, a, b;
+KLT_DEV bool read_next(const void* answer, int& x) {
+  uint32_t ok, a;
   asm volatile(
       "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t"
-      "ld.shared.b128 r, [%3];\n\t"
+      "ld.shared.b128 r, [%2];\n\t"
       "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\t"
-      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t"
-      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::y.b32.b128 %2, r;\n\t}"
-      : "=r"(ok), "=r"(a), "=r"(b)
+      "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+      : "=r"(ok), "=r"(a)
       : "r"(smem_u32(answer))
       : "memory");
   x = static_cast<int>(a);
-  y = static_cast<int>(b);
   return ok != 0;
 }
 // Where a search was: 32 sequences from b0 on, units before them.
@@ -125,13 +133,13 @@ KLT_DEV Unit find_unit(const PrefillParams& p, int number, int h, Place& at) {
       u.len = k1 - u.k0;
       auto tiles_of = [&](int w) {
         const int last = min(u.r0 + (w + 1) * 2 * ROWS, u.n) - 1;
-        const int seen = last < u.r0 + w * 2 * ROWS ? 0
-                         : p.causal                 ? u.len - (u.n - 1 - last)
-                                                    : u.len;
+        const int seen = p.causal ? u.len - (u.n - 1 - last) : u.len;
         return max(0, (seen + KEYS - 1) / KEYS);
       };
-      u.tiles0 = tiles_of(0);
-      u.tiles1 = tiles_of(1);
+      u.split = u.n - u.r0 <= 2 * ROWS;
+      u.nt = tiles_of(u.split ? 0 : 1);
+      u.tiles0 = u.split ? (u.nt + 1) / 2 : tiles_of(0);
+      u.tiles1 = u.split ? u.nt / 2 : u.nt;
       break;
     }
     at.before += __shfl_sync(0xFFFFFFFFu, in, 31);
@@ -222,6 +230,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   uint8_t* ring = qs + 2 * Q_BOXES * BOX;
   __shared__ Bars bars;
   __shared__ Unit units[2];
+  __shared__ float2 shares[2][ROWS];  // maximum and sum of each group's part of the keys
   __shared__ uint4 answers[2];
   __shared__ uint32_t tmem_holder, copies;
   __shared__ int abort_flag;
@@ -247,6 +256,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       mbar_init(&bars.unit_full[i], 1);
       mbar_init(&bars.unit_empty[i], rank == 0 ? 10 : 9);  // copies, products, softmax warps
       mbar_init(&bars.next_full[i], 1);
+      mbar_init(&bars.shared[i], 4);
+      mbar_init(&bars.shared_read[i], 4);
     }
     mbar_init(&bars.loaded, 1);
     mbar_init(&bars.next_read, 1);
@@ -292,7 +303,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     // The next one is asked for when this one's copies are issued, not earlier: other pairs may be
     // free first.  Numbers without tiles and queries are passed over.
     Place place;
-    Unit u = find_unit(p, blockIdx.x >> 1, blockIdx.y, place);
+    auto unit_of = [&](uint32_t x) {  // by groups of heads; in a group a number's heads side by side
+      uint32_t at = x >> 1, h0 = 0, heads = p.H;
+      if (p.side < p.H) {
+        const uint32_t span = gridDim.x / (2 * heads) * p.side, group = at / span;
+        at -= group * span;
+        h0 = group * p.side;
+        heads = min(p.side, p.H - h0);
+      }
+      const uint32_t number = at / heads;
+      return find_unit(p, number, h0 + at - number * heads, place);
+    };
+    Unit u = unit_of(blockIdx.x);
     bool ok = true, more = true;
     for (int i = 0, k = 0; more; ++i) {  // units; answers
       if (i > 0) ok = wait(&bars.loaded, i - 1);
@@ -307,14 +329,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         __syncwarp();
         ok = __all_sync(0xFFFFFFFFu, wait(bar, k >> 1));
         if (!ok) break;
-        int x, y;
-        more = read_next(&answers[k & 1], x, y);
+        int x;
+        more = read_next(&answers[k & 1], x);
         fence_proxy_async_shared();
         __syncwarp();
         if (rank == 1 && lane == 0) mbar_arrive_cluster_release(first(&bars.next_read));
         ++k;
         if (more) {
-          u = find_unit(p, x >> 1, y, place);
+          u = unit_of(x);
           if (u.n > 0) break;
         }
       }
@@ -338,11 +360,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       Unit u;
       for (int i = 0; ok && next_unit(i, u); ++i) {
         unit_read(i);
-        const int nt = max(u.tiles0, u.tiles1);
+        const int nt = u.nt;
         const bool ragged = nt * KEYS > u.len;
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
-          if ((w ? u.tiles1 : u.tiles0) <= 0 || !ok) continue;
+          if ((w ? u.split ? 0 : u.tiles1 : u.tiles0) <= 0 || !ok) continue;
           ok = wait(&bars.q_empty[w], nq[w] + 1);
           if (!ok) break;
           ++nq[w];
@@ -420,14 +442,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       bool ok = true;
       int g = 0, nl = 0;         // tiles of keys before this unit; ragged units
       int nq0 = 0, nq1 = 0;      // tiles of queries
+      int no0 = 0, no1 = 0;      // results
       int n0 = 0, n1 = 0;        // their tiles of keys
-      // of tile t of keys with tile w of queries; the last user hands the stage back
-      auto scores = [&](int w, int t, bool wanted, bool last, bool q_last) {
+      // of tile t of keys with tile q of queries, for group w; the last user hands the stage back
+      auto scores = [&](int w, int q, int t, bool wanted, bool last, bool q_last) {
         const int st = (g + t) % STAGES;
         if (wanted) ok = wait(&bars.k_full[st], (g + t) / STAGES);
         if (!ok) return;
         tc_fence_after();
-        const uint64_t qa = sdesc_sw128(smem_u32(qs + w * Q_BOXES * BOX)),
+        const uint64_t qa = sdesc_sw128(smem_u32(qs + q * Q_BOXES * BOX)),
                        ka = sdesc_sw128(smem_u32(ring + st * STAGE));
         const uint32_t d = tmem + w * 128;
         mma4_pair(d, qa, ka, sdesc, 0);
@@ -439,22 +462,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           for (int s = 0; s < p.rope / 16; ++s) mma_pair(d, qr + 2 * s, kr + 2 * s, sdesc);
         tc_commit_pair(&bars.s_full[w], 3);
         if (last) tc_commit_pair(&bars.k_empty[st], 3);
-        if (q_last) tc_commit_pair(&bars.q_empty[w], 3);
+        if (q_last) tc_commit_pair(&bars.q_empty[q], 3);
       };
-      auto values = [&](int w, int t, int tiles_before, int q_before, bool wanted, bool last,
+      // ... tile i of the group's
+      auto values = [&](int w, int t, int i, int tiles_before, int before, bool wanted, bool last,
                         bool tail) {
         const int st = (g + t) % STAGES;
         if (wanted)
           ok = wait(&bars.v_full[st], (g + t) / STAGES) && (!tail || wait(&bars.cleared, nl));
-        ok = ok && wait_spin(&bars.p_half[w], tiles_before + t) &&
-             (t > 0 || wait(&bars.o_free[w], q_before + 1));
+        ok = ok && wait_spin(&bars.p_half[w], tiles_before + i) &&
+             (i > 0 || wait(&bars.o_free[w], before + 1));
         if (!ok) return;
         tc_fence_after();
         const uint64_t va = sdesc_sw128_mn(smem_u32(ring + st * STAGE + K_BYTES), BOX);
         const uint32_t d = tmem + 256 + w * 128, a = tmem + w * 128;
-        mma4_pair_ta(d, a, va, vdesc, t);
+        mma4_pair_ta(d, a, va, vdesc, i);
         tc_commit_pair(&bars.pv_half[w], 3);
-        ok = wait_spin(&bars.p_full[w], tiles_before + t);
+        ok = wait_spin(&bars.p_full[w], tiles_before + i);
         if (!ok) return;
         tc_fence_after();
         mma4_pair_ta(d, a + 32, va + 512, vdesc, 1);
@@ -464,27 +488,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       Unit u;
       for (int i = 0; ok && next_unit(i, u); ++i) {
         unit_read(i);
-        const int t0 = u.tiles0, t1 = u.tiles1, nt = max(t0, t1);
+        const int t0 = u.tiles0, t1 = u.tiles1, nt = u.nt;
         const bool ragged_last = nt * KEYS > u.len;
+        const int split = u.split, q1 = split ^ 1;  // the second group's tile of queries
+        auto tile = [&](int w, int i) { return split ? 2 * i + w : i; };
+        auto ends = [&](int w, int i, int n) { return split ? tile(w, i) == nt - 1 : i == n - 1; };
         if (t0 > 0) {
           ok = wait(&bars.q_full[0], nq0);
-          if (ok) scores(0, 0, true, t1 <= 0, t0 == 1);
+          if (ok) scores(0, 0, 0, true, split || t1 <= 0, ends(0, 0, t0));
         }
         if (t1 > 0 && ok) {
-          ok = wait(&bars.q_full[1], nq1);
-          if (ok) scores(1, 0, t0 <= 0, true, t1 == 1);
+          if (!split) ok = wait(&bars.q_full[1], nq1);
+          if (ok) scores(1, q1, split, split || t0 <= 0, true, ends(1, 0, t1));
         }
-        for (int t = 0; t < nt && ok; ++t) {
-          const bool tail = ragged_last && t == nt - 1;
-          if (t < t0) values(0, t, n0, nq0, true, t >= t1, tail);
-          if (ok && t + 1 < t0) scores(0, t + 1, true, t + 1 >= t1, t + 2 == t0);
-          if (ok && t < t1) values(1, t, n1, nq1, t >= t0, true, tail);
-          if (ok && t + 1 < t1) scores(1, t + 1, t + 1 >= t0, true, t + 2 == t1);
+        for (int i = 0; i < max(t0, t1) && ok; ++i) {
+          const int a = tile(0, i), b = tile(1, i), step = 1 + split;
+          if (i < t0) values(0, a, i, n0, no0, true, split || i >= t1, ragged_last && a == nt - 1);
+          if (ok && i + 1 < t0)
+            scores(0, 0, a + step, true, split || i + 1 >= t1, ends(0, i + 1, t0));
+          if (ok && i < t1)
+            values(1, b, i, n1, no1, split || i >= t0, true, ragged_last && b == nt - 1);
+          if (ok && i + 1 < t1)
+            scores(1, q1, b + step, split || i + 1 >= t0, true, ends(1, i + 1, t1));
         }
         g += nt;
         nl += ragged_last && nt > 0;
         nq0 += t0 > 0;
-        nq1 += t1 > 0;
+        nq1 += t1 > 0 && !split;
+        no0 += t0 > 0;
+        no1 += t1 > 0;
         n0 += t0;
         n1 += t1;
       }
@@ -499,30 +531,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                    o_free = first(&bars.o_free[w]);
     int g = 0;          // tiles of keys before this unit
     uint32_t odd = 0;   // stages that have had an odd number of ragged last tiles
-    int done = 0;       // tiles of keys of this tile of queries before this unit
+    int done = 0;       // this group's tiles before this unit
+    int merged = 0;     // units whose keys both groups had
     bool ok = true;
     Unit u;
     for (int i = 0;; ++i) {
       ok = __all_sync(0xFFFFFFFFu, ok && next_unit(i, u));
       if (!ok) break;
-      const int nt = max(u.tiles0, u.tiles1), mine = w ? u.tiles1 : u.tiles0;
+      const int nt = u.nt, mine = w ? u.tiles1 : u.tiles0;
       const bool ragged = nt > 0 && nt * KEYS > u.len;
-      const int row = u.r0 + (2 * w + rank) * ROWS + quad * 32 + lane;
+      const int row = u.r0 + ((u.split ? 0 : 2 * w) + rank) * ROWS + quad * 32 + lane;
       const int limit = row >= u.n ? 0 : p.causal ? u.len - (u.n - 1 - row) : u.len;
-      float m = -INFINITY, l = 0.f;
-      for (int t = 0; t < mine; ++t) {
-        ok = wait_spin(&bars.s_full[w], done + t);
+      float m = -INFINITY, l = 0.f, f;
+      // the keys' ragged last tile is cleared by the group whose products with it come last
+      const int ragged_at =
+          ragged && (u.split ? ((nt - 1) & 1) == w : w == 1 || u.tiles1 < nt) ? mine - 1 : -1;
+      int seen = u.split && w ? limit - KEYS : limit;  // keys from the tile's first on
+      const int seen_step = u.split ? 2 * KEYS : KEYS;
+      for (int j = 0; j < mine; ++j, seen -= seen_step) {
+        ok = wait_spin(&bars.s_full[w], done + j);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
         tc_fence_after();
-        if (ragged && t == nt - 1 && (w == 1 || u.tiles1 < nt)) {
+        if (j == ragged_at) {
           // what the values hold behind the sequence is cleared: it may not be finite
-          const int st = (g + t) % STAGES;
+          const int st = (g + nt - 1) % STAGES;
           ok = wait(&bars.v_last[st], odd >> st & 1);
           ok = __all_sync(0xFFFFFFFFu, ok);
           if (!ok) break;
           uint8_t* vs = ring + st * STAGE + K_BYTES;
-          for (int c = (u.len - t * KEYS) * 8 + quad * 32 + lane; c < KEYS * 8; c += 128)
+          for (int c = (u.len - (nt - 1) * KEYS) * 8 + quad * 32 + lane; c < KEYS * 8; c += 128)
             *reinterpret_cast<uint4*>(vs + c * 16) = make_uint4(0, 0, 0, 0);
           fence_proxy_async_shared();
           __syncwarp();
@@ -534,7 +572,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 #pragma unroll 1
         for (int c = 0; c < KEYS; c += 64) {
           uint32_t v[2][32], pk[32];
-          load64(S + c, limit - t * KEYS - c, v);
+          load64(S + c, seen - c, v);
           float a, b;
           unsigned long long sum[2];
           float top = weights64(v, p.scale, m, sum, pk);
@@ -546,12 +584,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             // O holds what came before; the products of the tile before are done (these scores
             // were issued behind them), those of this tile's first half may not be
             if (c > 0) {
-              ok = wait(&bars.pv_half[w], done + t);
+              ok = wait(&bars.pv_half[w], done + j);
               ok = __all_sync(0xFFFFFFFFu, ok);
               if (!ok) break;
               tc_fence_after();
             }
-            if (t > 0 || c > 0) {
+            if (j > 0 || c > 0) {
 #pragma unroll 1
               for (int o = 0; o < p.value; o += 16) {
                 float x[16];
@@ -578,9 +616,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       ok = __all_sync(0xFFFFFFFFu, ok);
       if (!ok) break;
       tc_fence_after();
-      if (row - lane < u.n) {
-        const float f = l != 0.f ? 1.0f / l : 0.f;
-        if (p.lse && row < u.n)
+      // the two groups' shares of the keys come together: each takes half of the columns
+      const bool both = u.split && u.tiles1 > 0;
+      float f2 = 0.f;
+      if (both) {
+        shares[w][quad * 32 + lane] = make_float2(m, l);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.shared[w]);
+        ok = wait(&bars.shared[w ^ 1], merged);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const float2 other = shares[w ^ 1][quad * 32 + lane];
+        const float now = fmaxf(m, other.x);
+        const float a = m == -INFINITY ? 0.f : exp2_fast(m - now);
+        f2 = other.x == -INFINITY ? 0.f : exp2_fast(other.x - now);
+        l = l * a + other.y * f2;
+        m = now;
+        f2 = l != 0.f ? f2 / l : 0.f;
+        f = l != 0.f ? a / l : 0.f;
+      } else {
+        f = l != 0.f ? 1.0f / l : 0.f;
+      }
+      if (row - lane < u.n && (both || !u.split || w == 0)) {
+        if (p.lse && row < u.n && !(both && w))
           p.lse[static_cast<int64_t>(u.q0 + row) * p.H + u.h] =
               l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
         // 16 columns at a time; neighbouring lanes swap halves, so that a pair of them stores 32
@@ -588,8 +648,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         __nv_bfloat16* dst = p.out + static_cast<int64_t>(u.q0 + row - (lane & 1)) * p.out_token +
                              static_cast<int64_t>(u.h) * p.out_head + (lane & 1) * 8;
         const bool there0 = row - (lane & 1) < u.n, there1 = row - (lane & 1) + 1 < u.n;
+        const int c0 = both && w ? p.value / 2 : 0, c1 = both && !w ? p.value / 2 : p.value;
 #pragma unroll 1
-        for (int c = 0; c < p.value; c += 16) {
+        for (int c = c0; c < c1; c += 16) {
           float o[16];
           if (mine > 0) {
             tmem_ld16(O + c, o);
@@ -597,10 +658,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 #pragma unroll
             for (int k = 0; k < 16; ++k) o[k] = 0.f;
           }
+#pragma unroll
+          for (int k = 0; k < 16; ++k) o[k] *= f;
+          if (both) {
+            float o2[16];
+            tmem_ld16(tmem + 256 + (w ^ 1) * 128 + lanes + c, o2);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] = fmaf(o2[k], f2, o[k]);
+          }
           uint32_t x[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            x[k] = f == 0.f ? 0u : pack_bf16(o[2 * k] * f, o[2 * k + 1] * f);
+          for (int k = 0; k < 8; ++k) x[k] = l == 0.f ? 0u : pack_bf16(o[2 * k], o[2 * k + 1]);
           uint32_t y[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k)
@@ -613,6 +681,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             *reinterpret_cast<uint4*>(dst + p.out_token + c) =
                 lane & 1 ? make_uint4(x[4], x[5], x[6], x[7]) : make_uint4(y[0], y[1], y[2], y[3]);
         }
+      }
+      if (both) {  // ... and neither's result and sums are overwritten before the other has read them
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.shared_read[w]);
+        ok = wait(&bars.shared_read[w ^ 1], merged);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        ++merged;
       }
       if (mine > 0) {
         tc_fence_before();
@@ -651,7 +729,7 @@ cudaError_t launch_prefill(const CUtensorMap& q, const CUtensorMap& k, const CUt
                            const CUtensorMap& k_rope, const PrefillParams& p, unsigned tiles,
                            cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * tiles, p.H);
+  cfg.gridDim = dim3(2 * tiles * p.H);
   cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = SMEM;
   cfg.stream = s;

@@ -226,6 +226,26 @@ def test_prefill_score_ranges(spread):
     run_prefill(2, [260, 40], [300, 40], seed=9, spread=spread)
 
 
+@pytest.mark.parametrize("value", [64, 128])
+@pytest.mark.parametrize("n,m,causal", [
+    (1, 1, True), (1, 129, True), (1, 256, True), (200, 257, True), (256, 384, True),
+    (256, 385, False), (129, 640, True), (40, 900, False), (255, 1300, True)])
+def test_prefill_few_queries(n, m, causal, value):
+    """One tile of queries: its tiles of keys are shared out between two groups, an even or odd
+    number of them, whose last one is either's."""
+    run_prefill(3, [n, n], [m, m], causal, value=value, seed=n + m)
+
+
+def test_prefill_few_queries_score_ranges():
+    for spread in (0.0, 8.0, 60.0):
+        run_prefill(2, [70, 200], [700, 1100], seed=10, spread=spread)
+
+
+def test_prefill_groups_of_heads():
+    """Keys and values of 16 heads and more fill half of L2: heads are taken by groups."""
+    run_prefill(19, [260, 3, 40], [300, 9000, 40], nope=64, rope=16, seed=11)
+
+
 def test_prefill_many_units():
     """More units than pairs of CTAs, short and long ones, ragged ends in every stage of the ring:
     a pair takes over many units, and its copies run ahead of its products."""
