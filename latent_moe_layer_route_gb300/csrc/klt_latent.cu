@@ -25,13 +25,14 @@ struct klt_latent {
 namespace {
 
 // ------------------------------------------------------------------ append
-// A block takes one token, or two where there are many.  The latent part (R / 8 lanes of 8 values) is
-// normed in registers between the sum of its squares and its outputs; angles are fp64 up to the
-// reduced turn (at position 10^6 fp32 angles are off by 0.03), one lane per pair, shared by the block;
-// then the block's threads turn the row's and the queries' pairs, 16 elements a thread, whose loads
-// went out first.  Every value is read and written once: 8192 tokens of 512 + 64 columns and 64 heads
-// take 31 us (5.2 TB/s), bound by what six blocks an SM keep in flight (one token to a block, loads
-// behind the norm: 37; four or eight blocks an SM by registers: 33, 35); 16 tokens take 2.7.
+// A block takes one token, or two where there are many.  The latent part (R / 8 lanes of 8 values)
+// is normed in registers between the sum of its squares and its outputs; angles are fp64 up to the
+// reduced turn (at position 10^6 fp32 angles are off by 0.03), one lane per pair, shared by the
+// block; then the block's threads turn the row's and the queries' pairs, 16 elements a thread, whose
+// loads went out first.  Every value is read and written once: 8192 tokens of 512 + 64 columns and
+// 64 heads take 31 us (5.2 TB/s), bound by what six blocks an SM keep in flight (one token to a
+// block, loads behind the norm: 37; four or eight blocks an SM by registers: 33, 35); 16 tokens take
+// 2.7.
 constexpr int APPEND_TWO = 1500;  // tokens from which on a block takes two
 struct AppendParams {
   const void* kv;
@@ -409,7 +410,8 @@ int klt_latent_append(klt_latent* h, const klt_latent_append_args* a, void* stre
   auto launch = [&](auto kernel) { return outcome(launch_pdl(kernel, grid, threads, s, p)); };
   if (two)
     return f32 ? nb ? launch(append_kernel<true, true, 2>) : launch(append_kernel<true, false, 2>)
-               : nb ? launch(append_kernel<false, true, 2>) : launch(append_kernel<false, false, 2>);
+               : nb ? launch(append_kernel<false, true, 2>)
+                    : launch(append_kernel<false, false, 2>);
   return f32 ? nb ? launch(append_kernel<true, true, 1>) : launch(append_kernel<true, false, 1>)
              : nb ? launch(append_kernel<false, true, 1>) : launch(append_kernel<false, false, 1>);
 }

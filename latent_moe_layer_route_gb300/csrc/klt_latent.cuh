@@ -110,8 +110,8 @@ KLT_DEV void tmem_st32(uint32_t taddr, const uint32_t* r) {
       : "memory");
 }
 
-// One lane of a converged warp, in a form that the compiler knows to be one: the operands of bulk
-// copies and products then stay in uniform registers (64 x 64 x 16 products 47 -> 35 cycles each).
+// One lane of a converged warp, in a form that the compiler knows to be one (64 x 64 x 16 products
+// issued one after another: 35 cycles each, under lane == 0 47).
 KLT_DEV bool elect_one() {
   uint32_t r;
   asm volatile(

@@ -9,14 +9,25 @@
 // Roles: warp 0 copies tiles (two stages of 72 KB in blocks of 128 columns, each handed back on
 // its own), warp 1 issues the products of scores and warp 3 those of values (one thread for both
 // took longer over its waits and signals than these small products take: 4,000 cycles a tile, for
-// 2,000 of work), warp 2 loads the queries and records what the parts are, warps 4 to 11 do the softmax (32 of a tile's keys each) and write
-// results.
+// 2,000 of work), warp 2 loads the queries and records what the parts are, warps 4 to 11 do the
+// softmax (32 of a tile's keys each) and write results.
 //
 // The work is cut evenly over the SMs, whatever the lengths.  An item (a sequence's row tile, or
-// two side by side, a CTA of the group each) that several groups share
-// leaves its parts (O, running maximum and sum, fp32) in the workspace, and a second kernel brings
-// them together in order; so results do not depend on timing.  Each CTA records what its parts
-// belong to on every call: the workspace holds no state between calls.
+// two side by side, a CTA of the group each) that several groups share leaves its parts (O, running
+// maximum and sum, fp32) in the workspace, and a second kernel brings them together in order; so
+// results do not depend on timing.  Each CTA records what its parts belong to on every call: the
+// workspace holds no state between calls.
+//
+// What bounds it.  A tile of 512 + 64 columns moves 72 KB from memory (3,130 cycles at an SM's share
+// of its rate) and 325 KB through shared memory: 147 KB of operands of the scores, 98 KB of the
+// values, 72 KB of the copy, 8 KB of weights, 2,540 cycles at 128 bytes a cycle; with its copies left
+// out a tile takes 2,720.  130,001 keys of 64 heads take 49 us (3.0 TB/s; 14 tiles to an SM), 32
+// ragged sequences 51 (3.2 TB/s): the stream itself is some 23, starting (2.7), the first copy (2.5),
+// the end of a part (3) and the second kernel (6 to 8, 20 MB of fp32 parts through L2) are the rest.
+// 128 sequences of 128 heads take 118 (605 TFLOP/s): two row tiles to a sequence, 60 tiles to an SM,
+// bound by shared memory.  77 keys of 16 heads take 12.6, all of it such steps.  Nothing else was it:
+// a quarter of the products of scores or values took 7 and 4 us off those 118, no exponentials none,
+// keys multicast to both row tiles 3 us more, spinning waits none.
 #include "klt_latent.cuh"
 
 #include "../../include/klt.h"
@@ -27,13 +38,15 @@ namespace {
 constexpr int ROWS = 64, KEYS = 64, STAGES = 2;
 constexpr int BOX = KEYS * 128;  // 64 rows x 128 bytes
 constexpr int MAX_BOXES = 9;     // of a row: 512 columns and the position part
-constexpr int SOFTMAX = 256;      // threads of the softmax: two warps per 16 rows
+constexpr int SOFTMAX = 256;     // threads of the softmax: two warps per 16 rows
 constexpr int THREADS = 128 + SOFTMAX;
 constexpr int SMEM = 1024 + (MAX_BOXES * (1 + STAGES) + 1) * BOX;
 constexpr int MIN_TILES = 2;     // a group's least share
 constexpr int UNITS = 8;         // joining blocks per part
-constexpr int EXTRA = 4;         // what an item costs besides its tiles, in tiles
-constexpr int JOIN = 128;        // their threads: a warp to each of four rows' weights
+// What an item costs besides its tiles, in tiles: its queries' copy, its first scores, its results
+// (128 x 128 heads: 142 us at 0, 126 at 3 and 4, 127 at 8).
+constexpr int EXTRA = 4;
+constexpr int JOIN = 128;        // threads of a joining block: a warp to each of four rows' weights
 static_assert(2 * UNITS >= ROWS / 4 && JOIN == 4 * 32 && JOIN == 1 << 7, "");
 constexpr int MAX_PARTS = 224;   // of an item
 static_assert(SMEM <= 232448 - 2048, "shared memory of a block");
@@ -552,7 +565,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         continue;
       }
-      // a row at a time, lanes neighbouring chunks of 8; all copies are in flight at once
+      // a row at a time, lanes neighbouring chunks of 8; all copies are in flight at once (some 7 us
+      // where a bulk copy takes 2)
       const int chunks = (p.R + p.rope) >> 3;
       for (int r = 0; r < ROWS; ++r) {
         const int row = w.row + r;
@@ -763,7 +777,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 // columns are a block's, eight blocks to a part, so a thread has some eight loads however many parts
 // there are: of several columns where the parts are few, of one column, shared by several threads,
 // where they are many.  The first go out before the weights are known.  Lean on purpose: with
-// divisions and 64-bit addresses per load this was bound by its instructions (11 us for 152 parts).
+// divisions and 64-bit addresses per load this was bound by its instructions (11 us for 152 parts of
+// 64 x 512, 20 MB; now 6 to 8).
 __global__ void __launch_bounds__(JOIN, 8)
     join_kernel(const AttendParams p, int ctas, int slots) {
   __shared__ float4 weight[MAX_PARTS], inverse;
