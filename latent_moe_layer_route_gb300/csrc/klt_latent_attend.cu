@@ -89,8 +89,8 @@ struct Seq {
     n = q1 - q0;
     len = static_cast<int>(max(0ll, min(static_cast<long long>(p.lens[b]),
                                         static_cast<long long>(p.max_pages) << p.page_log2)));
-    const int per = ROWS * p.members;
-    supers = (n * p.H + per - 1) / per;
+    const int shift = p.members == 2 ? 7 : 6;  // rows of an item
+    supers = (n * p.H + (1 << shift) - 1) >> shift;
     tiles = max(1, (len + KEYS - 1) / KEYS);
   }
   KLT_DEV long long cost() const { return static_cast<long long>(supers) * (tiles + EXTRA); }
@@ -132,8 +132,13 @@ struct Walk {
     const int u = static_cast<int>(local - static_cast<long long>(super) * units);
     const int end = static_cast<int>(min(static_cast<long long>(units), u + (hi - pos)));
     if (end <= EXTRA) return false;
-    const int t = max(0, u - EXTRA), e = end - EXTRA;
-    const int member = blockIdx.x % p.members;
+    fill(p, w, super, max(0, u - EXTRA), end - EXTRA);
+    pos += end - u;
+    return true;
+  }
+  // The piece of tiles t .. e of an item of this sequence.
+  KLT_DEV void fill(const AttendParams& p, Piece& w, int super, int t, int e) const {
+    const int member = blockIdx.x & (p.members - 1);
     w.b = b;
     w.q0 = s.q0;
     w.n = s.n;
@@ -145,11 +150,9 @@ struct Walk {
     w.t0 = t;
     w.t1 = max(t, min(e, (seen + KEYS - 1) / KEYS));
     w.whole = t == 0 && e == s.tiles;
-    w.slot = 2 * blockIdx.x + (pos == lo ? 0 : 1);
-    w.start = base + static_cast<long long>(super) * units + EXTRA;
+    w.slot = 2 * blockIdx.x + (pos == lo ? 0 : 1);  // by its place in this group's share
+    w.start = base + static_cast<long long>(super) * (s.tiles + EXTRA) + EXTRA;
     w.tiles = s.tiles;
-    pos += end - u;
-    return true;
   }
 };
 
@@ -237,19 +240,22 @@ __global__ void __launch_bounds__(THREADS, 1)
   // always enough.  Else the tiles of all items in a row are cut into equal shares, and a group may
   // have the end of one item and the start of the next (which costs it some 10 us of work: 32
   // ragged sequences took 67 us that way, 59 by items).
-  const int group = blockIdx.x / p.members;
+  const int group = blockIdx.x >> (p.members - 1);  // one or two members
   long long W = 0, mine = 0, excl = 0;
-  int groups = gridDim.x / p.members, items = 0;
+  int groups = gridDim.x >> (p.members - 1), items = 0;
   Walk walk;
+  Piece w;
+  bool more = false;  // w is a piece
   {
     constexpr int WARPS = THREADS / 32;
-    int2* seqs = reinterpret_cast<int2*>(ps);  // items and tiles of each sequence, one pass's
+    static_assert(THREADS * sizeof(Seq) <= BOX, "");
+    Seq* seqs = reinterpret_cast<Seq*>(ps);  // of one pass over the batch
     Seq s;
     for (int b = tid; b < p.B; b += THREADS) {
       s.load(p, b);
       mine += s.cost();
       items += s.supers;
-      seqs[tid] = make_int2(s.supers, s.tiles);
+      seqs[tid] = s;
     }
     // block-wide sum; where one pass covers the batch, also this sequence's place in it
     long long incl = mine;
@@ -270,7 +276,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       items += counts[i];
     }
     walk.parts = 0;
-    walk.lo = walk.hi = 0;
+    walk.pos = walk.lo = walk.hi = 0;
     if (p.B <= THREADS && items < groups) {
       // the tiles, in units of 8 where 32 bits do not hold them
       const long long all = W - static_cast<long long>(items) * EXTRA;
@@ -283,7 +289,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                                  (most - least) % (WARPS - 1) * i / (WARPS - 1)) << shift);
       };
       int t = candidate(warp), need = 0;
-      for (int b = lane; b < p.B; b += 32) need += seqs[b].x * ((seqs[b].y + t - 1) / t);
+      for (int b = lane; b < p.B; b += 32) need += seqs[b].supers * ((seqs[b].tiles + t - 1) / t);
       need = __reduce_add_sync(0xFFFFFFFFu, need);
       if (lane == 0) needs[warp] = need;
       __syncthreads();
@@ -292,9 +298,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       t = candidate(i);
       int before = 0;
       for (int b0 = 0; b0 < p.B; b0 += 32) {
-        const int2 q = b0 + lane < p.B ? seqs[b0 + lane] : make_int2(0, 1);
-        const int parts = (q.y + t - 1) / t;
-        int in = q.x * parts;
+        const bool there = b0 + lane < p.B;
+        const int supers = there ? seqs[b0 + lane].supers : 0;
+        const int parts = there ? (seqs[b0 + lane].tiles + t - 1) / t : 1;
+        int in = supers * parts;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const int v = __shfl_up_sync(0xFFFFFFFFu, in, o);
@@ -304,16 +311,16 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (past) {
           const int src = __ffs(past) - 1;
           walk.b = b0 + src;
+          walk.s = seqs[walk.b];
+          walk.base = 0;
           walk.parts = __shfl_sync(0xFFFFFFFFu, parts, src);
           const int at =  // this group's number among the sequence's
-              group - before - __shfl_sync(0xFFFFFFFFu, in - q.x * parts, src);
+              group - before - __shfl_sync(0xFFFFFFFFu, in - supers * parts, src);
           const int super = at / walk.parts, part = at - super * walk.parts;
           walk.first = group - part;
-          walk.s.load(p, walk.b);
-          walk.base = 0;
-          const long long start = static_cast<long long>(super) * (walk.s.tiles + EXTRA) + EXTRA;
-          walk.lo = start + share(walk.s.tiles, part, walk.parts);
-          walk.hi = start + share(walk.s.tiles, part + 1, walk.parts);
+          walk.fill(p, w, super, static_cast<int>(share(walk.s.tiles, part, walk.parts)),
+                    static_cast<int>(share(walk.s.tiles, part + 1, walk.parts)));
+          more = true;
           break;
         }
         before += __shfl_sync(0xFFFFFFFFu, in, 31);
@@ -355,9 +362,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         walk.b = found_b;
         walk.base = found_base;
         walk.s.load(p, walk.b);
+        walk.pos = walk.lo;
+        more = walk.next(p, w);
       }
     }
-    walk.pos = walk.lo;
     __syncthreads();  // the weights' memory is free
   }
   const uint32_t tmem = tmem_holder, S = tmem + 256;
@@ -366,7 +374,6 @@ __global__ void __launch_bounds__(THREADS, 1)
   auto wait = [&](uint64_t* bar, int phase) {
     return mbar_wait(bar, phase & 1, stop, p.err, p.timeout);
   };
-  Piece w;
 
   if (warp == 0) {
     // ------------------------------------------------ copies
@@ -375,7 +382,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int page_mask = (1 << p.page_log2) - 1;
       int it = 0, cut = 0;  // tiles; blocks of the last one, where it was cut short
       bool ok = true;
-      while (ok && walk.next(p, w)) {
+      for (; ok && more; more = walk.next(p, w)) {
         if (w.rows == 0) continue;
         const int* table = p.table + w.b * p.ld_table;
         auto pages_of = [&](int t, int* page) {
@@ -456,7 +463,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       int it = 0, piece = 0;  // tiles; pieces with rows and tiles
       bool ok = true;
       const uint32_t qa = smem_u32(qs);
-      while (ok && walk.next(p, w)) {
+      for (; ok && more; more = walk.next(p, w)) {
         if (w.rows == 0 || w.t0 == w.t1) continue;
         ok = wait(&bars.q_full, piece++);
         for (int t = w.t0; t < w.t1 && ok; ++t, ++it) {
@@ -495,7 +502,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       int it = 0, piece = 0;
       bool ok = true;
       const uint64_t pd = sdesc_sw128(smem_u32(ps));
-      while (ok && walk.next(p, w)) {
+      for (; ok && more; more = walk.next(p, w)) {
         if (w.rows == 0 || w.t0 == w.t1) continue;
         const uint32_t idesc = idesc_make(1, 128, (w.rows + 15) & ~15) | IDESC_A_MN;
         ++piece;
@@ -520,7 +527,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     // ------------------------------------------------ queries
     int piece = 0, tiles = 0;  // pieces so far; tiles of the last one
     bool ok = true, left[2] = {false, false};
-    while (walk.next(p, w)) {
+    for (; more; more = walk.next(p, w)) {
       if (w.rows == 0) continue;
       if (!w.whole) {  // record what the part belongs to
         left[0] = left[0] || !(w.slot & 1);
@@ -531,7 +538,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           r.token = w.q0;
           r.row = w.row;
           r.rows = w.rows;
-          r.member = blockIdx.x % p.members;
+          r.member = blockIdx.x & (p.members - 1);
           if (walk.parts > 0) {
             r.first = walk.first;
             r.last = walk.first + walk.parts - 1;
@@ -600,7 +607,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int r0 = quad * 16 + (lane >> 2);  // this thread's rows: r0 and r0 + 8
     int it = 0;
     bool ok = true;
-    while (walk.next(p, w)) {
+    for (; more; more = walk.next(p, w)) {
       if (w.rows == 0) continue;
       int limit[2];
       float m[2], l[2] = {0.f, 0.f};
