@@ -21,13 +21,14 @@
 // What bounds it.  A tile of 512 + 64 columns moves 72 KB from memory (3,130 cycles at an SM's share
 // of its rate) and 325 KB through shared memory: 147 KB of operands of the scores, 98 KB of the
 // values, 72 KB of the copy, 8 KB of weights, 2,540 cycles at 128 bytes a cycle; with its copies left
-// out a tile takes 2,720.  130,001 keys of 64 heads take 49 us (3.0 TB/s; 14 tiles to an SM), 32
-// ragged sequences 51 (3.2 TB/s): the stream itself is some 23, starting (2.7), the first copy (2.5),
-// the end of a part (3) and the second kernel (6 to 8, 20 MB of fp32 parts through L2) are the rest.
-// 128 sequences of 128 heads take 118 (605 TFLOP/s): two row tiles to a sequence, 60 tiles to an SM,
-// bound by shared memory.  77 keys of 16 heads take 12.6, all of it such steps.  Nothing else was it:
-// a quarter of the products of scores or values took 7 and 4 us off those 118, no exponentials none,
-// keys multicast to both row tiles 3 us more, spinning waits none.
+// out a tile takes 2,720.  130,001 keys of 64 heads take 47 us (3.2 TB/s; 14 tiles to an SM), 32
+// ragged sequences 47 (3.5 TB/s): the stream itself is some 23, the shares (4 until the first copy is
+// issued), the first copy (2.5), the end of a part (2.5) and the second kernel (6, 20 MB of fp32 parts
+// through L2) are the rest.  128 sequences of 128 heads take 110 (649 TFLOP/s): two row tiles to a
+// sequence, 60 tiles to an SM, bound by shared memory.  77 keys of 16 heads take 10.7, all of it such
+// steps.  Nothing else was it: a quarter of the products of scores or values took 7 and 4 us off
+// those 110 (118 then), no exponentials none, keys multicast to both row tiles 3 us more, spinning
+// waits none.
 #include "klt_latent.cuh"
 
 #include "../../include/klt.h"
@@ -750,8 +751,9 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int i = 0; i < 16; ++i) o[i] = 0.f;
         }
         if (w.whole) {
-          // eight rows' factors and places first: read between the stores, which might change them
-          // for all the compiler knows, each waited for the store before (5,400 cycles for 16 rows)
+          // eight rows' factors and places first: read between the stores, ahead of which the
+          // compiler cannot move them, they were one latency behind the other (16 rows of 512
+          // columns 5,400 cycles, now 2,300)
 #pragma unroll
           for (int i = 0; i < 16; i += 8) {
             __nv_bfloat16* dst[8];
