@@ -659,6 +659,13 @@ __global__ void __launch_bounds__(THREADS, 1)
           if ((lane & 3) == 0) tops[half][r0 + 8 * i] = top[i];
         }
         const bool rescale = softmax_any(grows);
+        if (ok && w.len - t * KEYS < KEYS) {  // rows behind the last token hold anything
+          uint8_t* vs = ks + (it % STAGES) * MAX_BOXES * BOX;
+          for (int r = w.len - t * KEYS + (warp - 4); r < KEYS; r += SOFTMAX / 32)
+            for (int c = lane; c < NB * 8; c += 32)
+              *reinterpret_cast<uint4*>(vs + (c >> 3) * BOX + r * 128 + ((c & 7) << 4)) =
+                  make_uint4(0, 0, 0, 0);
+        }
         // the products of the tile before have read the weights
         ok = ok && wait(&bars.pv_done, it + 1);
         ok = __all_sync(0xFFFFFFFFu, ok);
@@ -699,13 +706,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                 pack_bf16(a, c);
           }
         }
-        if (w.len - t * KEYS < KEYS) {  // rows behind the last token hold anything
-          uint8_t* vs = ks + (it % STAGES) * MAX_BOXES * BOX;
-          for (int r = w.len - t * KEYS + (warp - 4); r < KEYS; r += SOFTMAX / 32)
-            for (int c = lane; c < NB * 8; c += 32)
-              *reinterpret_cast<uint4*>(vs + (c >> 3) * BOX + r * 128 + ((c & 7) << 4)) =
-                  make_uint4(0, 0, 0, 0);
-        }
         fence_proxy_async_shared();
         tc_fence_before();
         __syncwarp();
@@ -717,13 +717,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         l[i] = quad_sum(l[i]);
         if ((lane & 3) == 0) tops[half][r0 + 8 * i] = l[i];
       }
-      if (ok && w.t0 < w.t1) ok = wait(&bars.pv_done, it - 1);
-      ok = __all_sync(0xFFFFFFFFu, ok);
-      if (softmax_any(!ok)) {
-        ok = false;
-        continue;
-      }
-      tc_fence_after();
+      softmax_any(false);
       if (half == 0 && (lane & 3) == 0) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -738,7 +732,13 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         }
       }
-      softmax_any(false);
+      if (ok && w.t0 < w.t1) ok = wait(&bars.pv_done, it - 1);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (softmax_any(!ok)) {
+        ok = false;
+        continue;
+      }
+      tc_fence_after();
 #pragma unroll 1
       for (int c = half * 16; c < NJ * 64; c += 32) {
         const int col = (c >> 6) * 128 + quad * 32 + lane, r = c & 63;
