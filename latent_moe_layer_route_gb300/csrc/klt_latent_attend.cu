@@ -25,7 +25,7 @@
 // ragged sequences 47 (3.5 TB/s): the stream itself is some 23, the shares (4 until the first copy is
 // issued), the first copy (2.5), the end of a part (2.5) and the second kernel (6, 20 MB of fp32 parts
 // through L2) are the rest.  128 sequences of 128 heads take 110 (649 TFLOP/s): two row tiles to a
-// sequence, 60 tiles to an SM, bound by shared memory.  77 keys of 16 heads take 10.7, all of it such
+// sequence, 60 tiles to an SM, bound by shared memory.  77 keys of 16 heads take 9.8, all of it such
 // steps.  Nothing else was it: a quarter of the products of scores or values took 7 and 4 us off
 // those 110 (118 then), no exponentials none, keys multicast to both row tiles 3 us more, spinning
 // waits none.
@@ -289,14 +289,19 @@ __global__ void __launch_bounds__(THREADS, 1)
         return static_cast<int>((least + (most - least) / (WARPS - 1) * i +
                                  (most - least) % (WARPS - 1) * i / (WARPS - 1)) << shift);
       };
-      int t = candidate(warp), need = 0;
-      for (int b = lane; b < p.B; b += 32) need += seqs[b].supers * ((seqs[b].tiles + t - 1) / t);
-      need = __reduce_add_sync(0xFFFFFFFFu, need);
-      if (lane == 0) needs[warp] = need;
-      __syncthreads();
-      int i = 0;
-      while (i < WARPS - 1 && needs[i] > groups) ++i;
-      t = candidate(i);
+      int t = candidate(0);
+      if (least != most) {  // (one sequence: nothing to search, 0.4 us)
+        t = candidate(warp);
+        int need = 0;
+        for (int b = lane; b < p.B; b += 32)
+          need += seqs[b].supers * ((seqs[b].tiles + t - 1) / t);
+        need = __reduce_add_sync(0xFFFFFFFFu, need);
+        if (lane == 0) needs[warp] = need;
+        __syncthreads();
+        int i = 0;
+        while (i < WARPS - 1 && needs[i] > groups) ++i;
+        t = candidate(i);
+      }
       int before = 0;
       for (int b0 = 0; b0 < p.B; b0 += 32) {
         const bool there = b0 + lane < p.B;
