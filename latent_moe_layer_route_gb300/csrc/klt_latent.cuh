@@ -70,6 +70,21 @@ KLT_DEV void mbar_arrive_cluster_release(uint32_t addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr)
                : "memory");
 }
+// As mbar_wait, for what a thread of another CTA of the cluster has published (mbar_wait alone
+// acquires at CTA scope).  The phase that is over stays the last one until this thread goes on.
+KLT_DEV bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                               int* err_word, long long timeout) {
+  if (!mbar_wait(bar, parity, abort_flag, err_word, timeout)) return false;
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 // 3-D tiled load of the box at (c0 = inner element, c1, c2).
 KLT_DEV void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1,
                          int c2) {

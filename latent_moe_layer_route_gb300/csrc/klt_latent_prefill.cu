@@ -289,6 +289,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   auto wait_spin = [&](uint64_t* bar, int phase) {
     return mbar_wait_spin(bar, phase & 1, stop, p.err, p.timeout);
   };
+  // ... for what the other CTA's threads have written or read
+  auto wait_cluster = [&](uint64_t* bar, int phase) {
+    return mbar_wait_cluster(bar, phase & 1, stop, p.err, p.timeout);
+  };
   auto first = [&](uint64_t* bar) { return map_to_rank(smem_u32(bar), 0); };  // in the first CTA
   // the pair's unit number i, read by every role; false: there is none, or a wait ran out
   auto next_unit = [&](int i, Unit& u) {
@@ -320,7 +324,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       if (i > 0) ok = wait(&bars.loaded, i - 1);
       while (ok && more && (i > 0 || u.n == 0)) {
         uint64_t* bar = &bars.next_full[k & 1];
-        if (rank == 0 && k > 0) ok = wait(&bars.next_read, k - 1);
+        if (rank == 0 && k > 0) ok = wait_cluster(&bars.next_read, k - 1);
         if (!__all_sync(0xFFFFFFFFu, ok)) break;
         if (lane == 0) {
           mbar_arrive_expect_tx(bar, 16);
@@ -419,7 +423,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           if (nq[w] > 0) mbar_wait(&bars.q_full[w], (nq[w] - 1) & 1, &none, p.err, p.timeout);
         for (int j = max(0, it - 2 * STAGES); j < it; ++j) landed(j);
         // its waits are bounded and began before this CTA's last ones ended
-        if (mbar_wait(&bars.ended, 0, &none, p.err, 3 * p.timeout)) {
+        if (mbar_wait_cluster(&bars.ended, 0, &none, p.err, 3 * p.timeout)) {
           const int others = static_cast<int>(*static_cast<volatile uint32_t*>(&copies));
           for (; it < others; ++it) {
             const int t = it >> 1;
@@ -469,7 +473,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                         bool tail) {
         const int st = (g + t) % STAGES;
         if (wanted)
-          ok = wait(&bars.v_full[st], (g + t) / STAGES) && (!tail || wait(&bars.cleared, nl));
+          ok = wait(&bars.v_full[st], (g + t) / STAGES) &&
+               (!tail || wait_cluster(&bars.cleared, nl));
         ok = ok && wait_spin(&bars.p_half[w], tiles_before + i) &&
              (i > 0 || wait(&bars.o_free[w], before + 1));
         if (!ok) return;
