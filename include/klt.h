@@ -484,8 +484,9 @@ int klt_latent_create(const klt_latent_dims* d, const float* inv_freq, const voi
 
 /* Test hooks of klt_latent_attend and klt_latent_prefill (NULL or zeros = none). */
 typedef struct klt_latent_debug {
-  int32_t stall_after_tiles; /* > 0: every copy producer stops after that many tiles of keys, so
-                                the waits on its data run out (klt_latent_status)         */
+  int32_t stall_after_tiles; /* > 0: every copy producer stops after that many tiles of keys (the
+                                second of a pair of CTAs one later), so the waits on its data run
+                                out (klt_latent_status)                                   */
   int32_t timeout_ms;        /* bound of every on-device wait (0 = 1000 ms); waits that may last
                                 for a sequence's keys are given some 8 us more per tile   */
 } klt_latent_debug;

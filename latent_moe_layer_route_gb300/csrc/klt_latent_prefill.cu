@@ -72,6 +72,12 @@ struct Bars {
   uint64_t drain;                             // each
   uint64_t ended;                             // the second CTA has issued its last copy
 };
+// What the second CTA has issued.
+struct Copies {
+  uint32_t it;       // keys of tile it / 2, then its values
+  uint32_t queries[2];
+  uint32_t alone;    // stages whose last values were signalled to the second CTA alone
+};
 
 // Asks for a cluster of the grid that has not started; the answer (16 bytes) and its signal go to
 // the same places in both CTAs.
@@ -232,7 +238,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   __shared__ Unit units[2];
   __shared__ float2 shares[2][ROWS];  // maximum and sum of each group's part of the keys
   __shared__ uint4 answers[2];
-  __shared__ uint32_t tmem_holder, copies;
+  __shared__ uint32_t tmem_holder;
+  __shared__ Copies copies;
   __shared__ int abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = static_cast<int>(cluster_rank());
@@ -266,7 +273,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     mbar_init(&bars.ended, 1);
     abort_flag = 0;
     fence_barrier_init();
-    mbar_arrive_expect_tx(&bars.ended, 4);
+    mbar_arrive_expect_tx(&bars.ended, sizeof(Copies));
     tma_prefetch_desc(&qmap);
     tma_prefetch_desc(&kmap);
     tma_prefetch_desc(&vmap);
@@ -360,10 +367,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       int g = 0;           // tiles of keys
       int it = 0;          // keys of tile it / 2, then its values
       uint32_t lasts = 0, odd = 0;  // stages that have had a ragged last tile; an odd number of them
+      uint32_t alone = 0;           // ... whose last tile was one
+      // the second CTA stops a tile behind the first, so that its copies beyond the first one's own
+      // are met too
+      const int stall = p.stall > 0 ? min(p.stall, 0x7FFFFFFE) + rank : 0x7FFFFFFF;
       bool ok = true;
       Unit u;
       for (int i = 0; ok && next_unit(i, u); ++i) {
         unit_read(i);
+        if (g >= stall) break;
         const int nt = u.nt;
         const bool ragged = nt * KEYS > u.len;
 #pragma unroll
@@ -378,7 +390,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                              u.h, u.q0 + u.r0 + (2 * w + rank) * ROWS);
         }
         for (int t = 0; t < nt && ok; ++t, ++g) {
-          if (p.stall > 0 && g >= p.stall) ok = false;
+          if (g >= stall) ok = false;
           if (!ok) break;
           const int st = g % STAGES, row = u.k0 + t * KEYS;
           uint8_t* dst = ring + st * STAGE;
@@ -395,10 +407,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           if (ragged && t == nt - 1) {
             lasts |= 1u << st;
             odd ^= 1u << st;
+            alone |= 1u << st;
             mbar_arrive_expect_tx(&bars.v_last[st], BOX);
             tma_load_3d(dst + K_BYTES, &vmap, &bars.v_last[st], rank * 64, u.h, row);
             if (rank == 0) mbar_arrive(&bars.v_full[st]);  // a phase without bytes
           } else {
+            alone &= ~(1u << st);
             if (rank == 0) mbar_arrive_expect_tx(&bars.v_full[st], 2 * BOX);
             tma_load_3d_pair(dst + K_BYTES, &vmap, first(&bars.v_full[st]), rank * 64, u.h, row);
           }
@@ -406,36 +420,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
         mbar_arrive(&bars.loaded);
       }
-      // No copy of the pair is in flight past this point.  The first CTA waits for all, those too
-      // that the second has issued beyond its own after a wait that ran out.
+      // No copy of the pair is in flight past this point.  Each CTA waits for the values that were
+      // signalled to it alone, and the first one for all else, that too which the second has issued
+      // beyond the first one's own after a wait that ran out.  This is a tile at most for each place
+      // in shared memory: what comes there next waits for products that lack the first CTA's part.
       int none = 0;
       for (int st = 0; st < STAGES; ++st)
         if (lasts >> st & 1)
           mbar_wait(&bars.v_last[st], (odd >> st & 1) ^ 1, &none, p.err, p.timeout);
-      auto landed = [&](int j) {
+      auto landed = [&](int j, int* stop) {
         const int t = j >> 1;
         mbar_wait(j & 1 ? &bars.v_full[t % STAGES] : &bars.k_full[t % STAGES], (t / STAGES) & 1,
-                  &none, p.err, p.timeout);
+                  stop, p.err, p.timeout);
       };
       if (rank == 0) {
 #pragma unroll
         for (int w = 0; w < 2; ++w)
           if (nq[w] > 0) mbar_wait(&bars.q_full[w], (nq[w] - 1) & 1, &none, p.err, p.timeout);
-        for (int j = max(0, it - 2 * STAGES); j < it; ++j) landed(j);
+        for (int j = max(0, it - 2 * STAGES); j < it; ++j) landed(j, &none);
         // its waits are bounded and began before this CTA's last ones ended
-        if (mbar_wait_cluster(&bars.ended, 0, &none, p.err, 3 * p.timeout)) {
-          const int others = static_cast<int>(*static_cast<volatile uint32_t*>(&copies));
-          for (; it < others; ++it) {
-            const int t = it >> 1;
+        int late = 0;
+        if (mbar_wait_cluster(&bars.ended, 0, &late, p.err, 3 * p.timeout)) {
+          const Copies second = copies;
+#pragma unroll
+          for (int w = 0; w < 2; ++w)
+            if (static_cast<int>(second.queries[w]) > nq[w]) {
+              mbar_arrive_expect_tx(&bars.q_full[w], (nb + 1) * BOX);
+              mbar_wait(&bars.q_full[w], nq[w] & 1, &late, p.err, p.timeout);
+            }
+          for (; it < static_cast<int>(second.it); ++it) {
+            const int st = (it >> 1) % STAGES;
+            if ((it & 1) && (second.alone >> st & 1)) continue;
             if (it & 1)
-              mbar_arrive_expect_tx(&bars.v_full[t % STAGES], BOX);
+              mbar_arrive_expect_tx(&bars.v_full[st], BOX);
             else
-              mbar_arrive_expect_tx(&bars.k_full[t % STAGES], (nb + 1) * (BOX / 2));
-            landed(it);
+              mbar_arrive_expect_tx(&bars.k_full[st], (nb + 1) * (BOX / 2));
+            landed(it, &late);
           }
         }
       } else {
-        st_async_u32(first(reinterpret_cast<uint64_t*>(&copies)), it, first(&bars.ended));
+        const uint32_t to = first(reinterpret_cast<uint64_t*>(&copies)), bar = first(&bars.ended);
+        st_async_u32(to, it, bar);
+        st_async_u32(to + 4, nq[0], bar);
+        st_async_u32(to + 8, nq[1], bar);
+        st_async_u32(to + 12, alone, bar);
       }
     }
   } else if (warp == 1 && rank == 0) {

@@ -38,3 +38,30 @@ def test_values_behind_a_sequence_have_no_effect(value, bad):
         got = at.prefill(*args)
         assert all(torch.equal(t[keep.cuda()], f) for t, f in zip(got, first))
     assert at.status() == B.KLT_OK
+
+
+@pytest.mark.parametrize("stall", [1, 2, 3, 4, 5, 6])
+def test_waits_that_run_out_at_different_places(stall):
+    """The second CTA's copies stop a tile behind the first one's, within a unit, at its ragged last
+    tile (whose values are signalled to each CTA alone) or with the next unit's queries: all have
+    landed when the pair ends, so nothing is left to the launches right behind it."""
+    queries, keys = [40, 300, 129, 400], [130, 300, 257, 100]
+    cu_q, cu_k = starts(queries), starts(keys)
+
+    def operands(seed):
+        kv = randn(seed, cu_k[-1], 90, 128).cuda()
+        return [randn(seed + 1, cu_q[-1], 90, 80).cuda(), kv[..., :64], kv[..., 64:],
+                randn(seed + 2, cu_k[-1], 16).cuda(), i32(cu_q), i32(cu_k)]
+
+    bad, ok = (layer(90, 128, 16, 64, 64) for _ in range(2))
+    lost, args = operands(1), operands(4)
+    want = [t.clone() for t in ok.prefill(*args)]
+    torch.cuda.synchronize()
+    bad.prefill(*lost, debug=B.KltLatentDebug(stall_after_tiles=stall, timeout_ms=5))
+    got = [ok.prefill(*args) for _ in range(3)]
+    torch.cuda.synchronize()
+    assert bad.status() == B.KLT_ERR_DEVICE_TIMEOUT
+    assert ok.status() == B.KLT_OK
+    for g in got:
+        assert all(torch.equal(x, y) for x, y in zip(g, want))
+    bad.close()
