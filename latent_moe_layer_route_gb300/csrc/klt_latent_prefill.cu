@@ -71,6 +71,7 @@ struct Bars {
   uint64_t next_read;                         // the second CTA has read it
   uint64_t drain;                             // each
   uint64_t ended;                             // the second CTA has issued its last copy
+  uint64_t asked;                             // the second's: the first has asked its last question
 };
 // What the second CTA has issued.
 struct Copies {
@@ -240,6 +241,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   __shared__ uint4 answers[2];
   __shared__ uint32_t tmem_holder;
   __shared__ Copies copies;
+  __shared__ uint32_t questions;
   __shared__ int abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = static_cast<int>(cluster_rank());
@@ -271,9 +273,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     mbar_init(&bars.cleared, 8);
     mbar_init(&bars.drain, 1);
     mbar_init(&bars.ended, 1);
+    mbar_init(&bars.asked, 1);
     abort_flag = 0;
     fence_barrier_init();
     mbar_arrive_expect_tx(&bars.ended, sizeof(Copies));
+    mbar_arrive_expect_tx(&bars.asked, 4);
     tma_prefetch_desc(&qmap);
     tma_prefetch_desc(&kmap);
     tma_prefetch_desc(&vmap);
@@ -327,7 +331,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     };
     Unit u = unit_of(blockIdx.x);
     bool ok = true, more = true;
-    for (int i = 0, k = 0; more; ++i) {  // units; answers
+    int k = 0, armed = 0;  // answers that have come, that were waited for
+    for (int i = 0; more; ++i) {
       if (i > 0) ok = wait(&bars.loaded, i - 1);
       while (ok && more && (i > 0 || u.n == 0)) {
         uint64_t* bar = &bars.next_full[k & 1];
@@ -337,6 +342,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           mbar_arrive_expect_tx(bar, 16);
           if (rank == 0) ask_next(&answers[k & 1], bar);
         }
+        armed = k + 1;
         __syncwarp();
         ok = __all_sync(0xFFFFFFFFu, wait(bar, k >> 1));
         if (!ok) break;
@@ -360,6 +366,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       }
       __syncwarp();
     }
+    // No answer to the pair is on its way past this point: after a wait that ran out the last one
+    // may not have come, and the second CTA may not know of it.
+    int none = 0, asked = armed;
+    if (rank == 0) {
+      if (lane == 0)
+        st_async_u32(map_to_rank(smem_u32(&questions), 1), asked,
+                     map_to_rank(smem_u32(&bars.asked), 1));
+    } else {
+      asked = 0;
+      if (mbar_wait_cluster(&bars.asked, 0, &none, p.err, 3 * p.timeout))
+        asked = static_cast<int>(questions);
+      asked = __shfl_sync(0xFFFFFFFFu, asked, 0);
+      if (asked > armed && lane == 0) mbar_arrive_expect_tx(&bars.next_full[k & 1], 16);
+      __syncwarp();
+    }
+    if (asked > k) mbar_wait(&bars.next_full[k & 1], (k >> 1) & 1, &none, p.err, p.timeout);
+    __syncwarp();
   } else if (warp == 0) {
     if (elect_one()) {
       // ---------------------------------------------- copies

@@ -40,20 +40,16 @@ def test_values_behind_a_sequence_have_no_effect(value, bad):
     assert at.status() == B.KLT_OK
 
 
-@pytest.mark.parametrize("stall", [1, 2, 3, 4, 5, 6])
-def test_waits_that_run_out_at_different_places(stall):
-    """The second CTA's copies stop a tile behind the first one's, within a unit, at its ragged last
-    tile (whose values are signalled to each CTA alone) or with the next unit's queries: all have
-    landed when the pair ends, so nothing is left to the launches right behind it."""
-    queries, keys = [40, 300, 129, 400], [130, 300, 257, 100]
+def gives_up(queries, keys, heads, stall):
+    """A launch whose copies stop after `stall` tiles, and others right behind it."""
     cu_q, cu_k = starts(queries), starts(keys)
 
     def operands(seed):
-        kv = randn(seed, cu_k[-1], 90, 128).cuda()
-        return [randn(seed + 1, cu_q[-1], 90, 80).cuda(), kv[..., :64], kv[..., 64:],
+        kv = randn(seed, cu_k[-1], heads, 128).cuda()
+        return [randn(seed + 1, cu_q[-1], heads, 80).cuda(), kv[..., :64], kv[..., 64:],
                 randn(seed + 2, cu_k[-1], 16).cuda(), i32(cu_q), i32(cu_k)]
 
-    bad, ok = (layer(90, 128, 16, 64, 64) for _ in range(2))
+    bad, ok = (layer(heads, 128, 16, 64, 64) for _ in range(2))
     lost, args = operands(1), operands(4)
     want = [t.clone() for t in ok.prefill(*args)]
     torch.cuda.synchronize()
@@ -65,3 +61,18 @@ def test_waits_that_run_out_at_different_places(stall):
     for g in got:
         assert all(torch.equal(x, y) for x, y in zip(g, want))
     bad.close()
+
+
+@pytest.mark.parametrize("stall", [1, 2, 3, 4, 5, 6])
+def test_waits_that_run_out_at_different_places(stall):
+    """The second CTA's copies stop a tile behind the first one's, within a unit, at its ragged last
+    tile (whose values are signalled to each CTA alone) or with the next unit's queries: all have
+    landed when the pair ends, so nothing is left to the launches right behind it."""
+    gives_up([40, 300, 129, 400], [130, 300, 257, 100], 90, stall)
+
+
+@pytest.mark.parametrize("stall", [1, 2, 3])
+def test_waits_that_run_out_between_units(stall):
+    """Units of one tile of keys: a pair gives up while its CTAs ask for the next one, and one of them
+    may not know that an answer is on its way."""
+    gives_up([20, 100, 256, 60], [20, 128, 100, 90], 130, stall)
