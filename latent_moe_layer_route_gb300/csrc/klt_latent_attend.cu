@@ -224,8 +224,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     mbar_init(&bars.drain, 2);
     abort_flag = 0;
     fence_barrier_init();
-    tma_prefetch_desc(&latents);
-    tma_prefetch_desc(&ropes);
+    if (p.max_pages > 0) {  // else they may be empty
+      tma_prefetch_desc(&latents);
+      tma_prefetch_desc(&ropes);
+    }
     if (p.q_box) tma_prefetch_desc(&queries);
   }
   if (warp == 1) {

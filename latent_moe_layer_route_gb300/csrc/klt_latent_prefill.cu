@@ -279,9 +279,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     mbar_arrive_expect_tx(&bars.ended, sizeof(Copies));
     mbar_arrive_expect_tx(&bars.asked, 4);
     tma_prefetch_desc(&qmap);
-    tma_prefetch_desc(&kmap);
-    tma_prefetch_desc(&vmap);
-    tma_prefetch_desc(&rmap);
+    if (p.S > 0) {  // else they are empty
+      tma_prefetch_desc(&kmap);
+      tma_prefetch_desc(&vmap);
+      tma_prefetch_desc(&rmap);
+    }
   }
   if (warp == 2) tmem_alloc_pair(&tmem_holder, 512);
   pdl_trigger();
