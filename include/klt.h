@@ -525,9 +525,10 @@ int klt_latent_append(klt_latent* h, const klt_latent_append_args* a, void* stre
  *     out = softmax(scale * q . rows) c,   lse = log(sum(exp(scale * q . rows)))
  * A query that sees no token gets zeros and a lse of minus infinity.  Rows of out and lse outside
  * of the sequences' ranges stay as they are.  What lies in a page behind the sequence's last token
- * does not matter, whatever it is; a row of the sequence that is not finite spreads to all of the
- * sequence's queries.  Lengths beyond max_pages * page are cut to it, negative ones to 0; ranges
- * of queries are cut to 0 .. T; pages outside of the cache read as rows of zeros. */
+ * does not matter, whatever it is; a row of the sequence that is not finite may spread to any of
+ * the sequence's queries, those too that do not see it (a masked weight of zero still multiplies
+ * the values of a tile of keys).  Lengths beyond max_pages * page are cut to it, negative ones to
+ * 0; ranges of queries are cut to 0 .. T; pages outside of the cache read as rows of zeros. */
 typedef struct klt_latent_attend_args {
   int32_t B, T;               /* sequences; queries in all                                 */
   int32_t max_pages;          /* columns of block_table                                    */

@@ -1,17 +1,67 @@
-"""Latent attention: calls without tokens or keys."""
+"""Latent attention: rows that are not finite, and calls without tokens or keys."""
 import math
 
 import pytest
 import torch
 
+import latent_util as U
 from latent_moe_layer_route_gb300 import binding as B
-from test_gpu_latent import _lib, layer, randn  # noqa: F401
+from test_gpu_latent import NAN, _lib, layer, paged, randn, starts  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
 
 def i32(v):
     return torch.tensor(v, dtype=torch.int32).cuda()
+
+
+# ---------------------------------------------------------------- rows that are not finite
+
+@pytest.mark.parametrize("bad", [NAN, math.inf])
+@pytest.mark.parametrize("columns", [slice(0, 192), slice(128, 192), slice(5, 6)])
+def test_queries_that_see_a_row_that_is_not_finite(bad, columns):
+    """They are not finite, however little of the row is; other sequences' are as ever; queries of the
+    same sequence that do not see it may be either."""
+    lens, counts, at_row = [130, 90, 200], [3, 7, 2], 86  # the second sequence's 4th to 7th query
+    at, cu = layer(16), starts(counts)
+    cache, table, seqs = paged(21, lens, 64, 192)
+    q = randn(22, cu[-1], 16, 192)
+    want, wl, ob, lb = U.attend(q, seqs, list(zip(cu, cu[1:])), 128, 192 ** -0.5)
+    cache[int(table[1, at_row // 64]), at_row % 64, columns] = bad
+    out, lse = (t.cpu() for t in at.attend(q.cuda(), cache.cuda(), table.cuda(), i32(lens), i32(cu)))
+    keep = list(range(cu[1])) + list(range(cu[2], cu[3]))
+    U.check(lse[keep], wl[keep], lb[keep], "lse")
+    U.check(out[keep], want[keep], ob[keep], "out")
+    sees = slice(cu[1] + at_row - (lens[1] - counts[1]), cu[2])
+    assert sees.stop - sees.start == 4
+    # an infinite score of either sign is a weight of nan or of zero, by the query's sign
+    touched = ~out[sees].isfinite().all(-1) | ~lse[sees].isfinite()
+    assert bool(touched.all())
+
+
+@pytest.mark.parametrize("bad", [NAN, math.inf])
+@pytest.mark.parametrize("part", ["k", "v", "k_rope"])
+def test_expanded_queries_that_see_a_row_that_is_not_finite(part, bad):
+    lens, at_row = [100, 300, 70], 137
+    cu = starts(lens)
+    at = layer(3)
+    q, kv, kr = randn(1, cu[-1], 3, 192), randn(2, cu[-1], 3, 256), randn(3, cu[-1], 64)
+    want, wl, ob, lb = U.prefill(q, kv[..., :128], kv[..., 128:], kr, cu, cu, 192 ** -0.5, True)
+    g = dict(k=kv[..., :128].cuda(), v=kv[..., 128:].cuda(), k_rope=kr.cuda())
+    g[part][cu[1] + at_row] = bad
+    out, lse = (t.cpu() for t in at.prefill(q.cuda(), g["k"], g["v"], g["k_rope"], i32(cu), i32(cu)))
+    keep = list(range(cu[1])) + list(range(cu[2], cu[3]))
+    U.check(lse[keep], wl[keep], lb[keep], "lse")
+    U.check(out[keep], want[keep], ob[keep], "out")
+    touched = ~out[cu[1] + at_row:cu[2]].isfinite().all(-1)
+    if part == "v" or math.isnan(bad):
+        assert bool(touched.all())
+    else:  # the sum of a row's infinite products has either sign, or none: nan
+        s = torch.einsum("thd,hd->th", q[cu[1] + at_row:cu[2], :, :128].float(),
+                         g["k"][cu[1] + at_row].cpu().float()) + torch.einsum(
+            "thd,d->th", q[cu[1] + at_row:cu[2], :, 128:].float(),
+            g["k_rope"][cu[1] + at_row].cpu().float())
+        assert bool(touched[s != -math.inf].all())
 
 
 # ---------------------------------------------------------------- nothing to do
