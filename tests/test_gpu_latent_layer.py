@@ -1,4 +1,5 @@
-"""Latent attention: rows that are not finite, and calls without tokens or keys."""
+"""Latent attention's calls in the layouts in which a layer chains them, a decoding step replayed from
+a graph, rows that are not finite, and calls without tokens or keys."""
 import math
 
 import pytest
@@ -85,3 +86,112 @@ def test_no_tokens_and_no_keys():
                               i32([0, 0, 0]), causal=causal)
         assert bool((out == 0).all()) and bool((lse == -math.inf).all())
     assert at.status() == B.KLT_OK
+
+
+# ---------------------------------------------------------------- in a row
+
+H, R, D, N, PAGE = 6, 256, 64, 128, 16
+
+
+class Chain:
+    """A layer's buffers: queries [N + D], absorbed queries [R + D] whose position parts the append
+    writes, dense rows whose position parts the expanded form reads where they lie."""
+
+    def __init__(self):
+        self.at = layer(H, R, D, N, N, PAGE)
+        self.pages = torch.tensor([[5, 0, 7, 2, 6], [3, 9, 1, 8, 4]])
+        self.cache = torch.full((10, PAGE, R + D), NAN, dtype=torch.bfloat16, device="cuda")
+
+    def slots(self, b, positions):
+        return self.pages[b, positions // PAGE] * PAGE + positions % PAGE
+
+    def rows(self, b, n):
+        return self.cache.view(-1, R + D)[self.slots(b, torch.arange(n)).cuda()].cpu()
+
+
+def _check_append(c, kv, q, positions, got_rows, got_q):
+    want = U.rows_of(kv, R, positions, c.at.freq, None, 1e-6, "halves")
+    size = want.abs()
+    size[:, R:] = kv[:, R:].double().abs().amax(1, keepdim=True) * 2
+    U.check(got_rows, want, U.HALF_STEP * want.abs() + 2.0 ** -19 * size + 1e-30, "rows")
+    want = U.rotate(q.double(), positions, c.at.freq, "halves")
+    U.check(got_q, want, U.HALF_STEP * want.abs() +
+            2.0 ** -18 * q.double().abs().amax(-1, keepdim=True), "queries")
+
+
+def test_a_prompt_without_copies_between_calls():
+    c, lens = Chain(), [75, 33]
+    T, cu = sum(lens), starts(lens)
+    kv, q, up = randn(1, T, R + D), randn(2, T, H, N + D), randn(3, T, H, R)
+    positions = torch.cat([torch.arange(n) for n in lens])
+    slots = torch.cat([c.slots(b, torch.arange(n)) for b, n in enumerate(lens)])
+    absorbed = torch.full((T, H, R + D), NAN, dtype=torch.bfloat16, device="cuda")
+    absorbed[..., :R] = up.cuda()
+    rows = torch.empty(T, R + D, dtype=torch.bfloat16, device="cuda")
+    c.at.append(kv.cuda(), positions.cuda(), slots.cuda(), c.cache, kv_out=rows,
+                q=q.cuda()[..., N:], q_out=absorbed[..., R:])
+    _check_append(c, kv, q[..., N:], positions, rows, absorbed[..., R:])
+    assert torch.equal(absorbed[..., :R].cpu(), up)
+    assert torch.equal(c.cache.view(-1, R + D)[slots.cuda()], rows)
+    out, lse = c.at.attend(absorbed, c.cache, c.pages.int().cuda(), i32(lens), i32(cu))
+    want, wl, ob, lb = U.attend(absorbed.cpu(), [c.rows(b, n) for b, n in enumerate(lens)],
+                                list(zip(cu, cu[1:])), R, (N + D) ** -0.5)
+    U.check(lse, wl, lb, "absorbed: lse")
+    U.check(out, want, ob, "absorbed")
+    turned = q.cuda()
+    turned[..., N:] = absorbed[..., R:]
+    k, v = randn(4, T, H, N), randn(5, T, H, N)
+    out, lse = c.at.prefill(turned, k.cuda(), v.cuda(), rows[:, R:], i32(cu), i32(cu))
+    want, wl, ob, lb = U.prefill(turned.cpu(), k, v, rows[:, R:].cpu(), cu, cu, (N + D) ** -0.5, True)
+    U.check(lse, wl, lb, "expanded: lse")
+    U.check(out, want, ob, "expanded")
+    assert c.at.status() == B.KLT_OK
+
+
+def test_decoding_steps_replayed():
+    """Append and absorbed attention of two sequences in one graph, replayed token after token; the
+    second sequence stops growing half-way (its slot is none)."""
+    c = Chain()
+    kv = torch.zeros(2, R + D, dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros(2, H, D, dtype=torch.bfloat16, device="cuda")
+    absorbed = torch.zeros(2, H, R + D, dtype=torch.bfloat16, device="cuda")
+    positions, slots = (torch.full((2,), v, device="cuda") for v in (0, -1))
+    lens, table = i32([0, 0]), c.pages.int().cuda()
+    out = torch.empty(2, H, R, dtype=torch.bfloat16, device="cuda")
+    lse, ws = torch.empty(2, H, device="cuda"), c.at.workspace(2)
+
+    def step():
+        c.at.append(kv, positions, slots, c.cache, q=q, q_out=absorbed[..., R:])
+        c.at.attend(absorbed, c.cache, table, lens, out=out, lse=lse, workspace=ws)
+
+    step()
+    torch.cuda.synchronize()
+    assert bool((out == 0).all()) and bool((lse == -math.inf).all())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    have = [0, 0]
+    for t in range(70):
+        grows = [True, t < 33]
+        new = [randn(100 * t + i, 2, *n) for i, n in enumerate(((R + D,), (H, D), (H, R)))]
+        kv.copy_(new[0])
+        q.copy_(new[1])
+        absorbed[..., :R].copy_(new[2])
+        at = [n if g else n - 1 for n, g in zip(have, grows)]
+        positions.copy_(torch.tensor(at))
+        slots.copy_(torch.tensor([int(c.slots(b, torch.tensor(at[b]))) if grows[b] else -1
+                                  for b in range(2)]))
+        have = [n + g for n, g in zip(have, grows)]
+        lens.copy_(torch.tensor(have, dtype=torch.int32))
+        before = c.rows(1, have[1])
+        graph.replay()
+        torch.cuda.synchronize()
+        if not grows[1]:
+            assert torch.equal(c.rows(1, have[1]), before)
+        seqs = [c.rows(b, n) for b, n in enumerate(have)]
+        _check_append(c, new[0][:1], new[1][:1], torch.tensor(at[:1]), seqs[0][-1:],
+                      absorbed[:1, :, R:])
+        want, wl, ob, lb = U.attend(absorbed.cpu(), seqs, [(0, 1), (1, 2)], R, (N + D) ** -0.5)
+        U.check(lse, wl, lb, f"lse {t}")
+        U.check(out, want, ob, f"out {t}")
+    assert c.at.status() == B.KLT_OK
