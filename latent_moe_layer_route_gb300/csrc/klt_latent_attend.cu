@@ -939,8 +939,15 @@ bool prepare_attend() {
 cudaError_t launch_attend(const CUtensorMap& latents, const CUtensorMap& ropes,
                           const CUtensorMap& queries, AttendParams p, int num_sms,
                           cudaStream_t s) {
-  // two row tiles of a sequence read the same keys at the same time, the second from L2
-  p.members = static_cast<int64_t>(p.T) * p.H > static_cast<int64_t>(ROWS) * p.B ? 2 : 1;
+  // Two row tiles of a sequence side by side read the same keys at the same time, the second from
+  // L2: 128 sequences of 4096 keys and 128 heads take 185 us, 212 one by one (up to 72 sequences:
+  // the same).  But where a sequence has an odd number of tiles a CTA stands idle (one to each of 32
+  // sequences: 61.5 us, 42.7 one by one; three to each of 128: 360, 303).  The numbers of queries
+  // are on the device, so two it is where every number makes an even one, or where all sequences
+  // seem to have the same.
+  const int64_t each = static_cast<int64_t>(p.T / p.B) * p.H;
+  const bool even = p.H % (2 * ROWS) == 0 || (p.T % p.B == 0 && (each + ROWS - 1) / ROWS % 2 == 0);
+  p.members = even ? 2 : 1;
   // at most as many items and parts of one as the sizes allow, whatever the lengths are
   const int64_t per = ROWS * p.members, rows = static_cast<int64_t>(p.T) * p.H;
   const int64_t items = p.cu_q ? rows / per + min(p.B, p.T) : p.B * ((p.H + per - 1) / per);
