@@ -662,8 +662,9 @@ class LatentAttention:
                         if cu_q is None else \
                         torch.zeros(shape, dtype=torch.bfloat16, device=q.device)
                 if lse is None:
-                    lse = torch.empty(shape[:2], device=q.device) if cu_q is None else \
-                        torch.full(shape[:2], -float("inf"), device=q.device)
+                    lse = torch.empty(shape[:2], dtype=torch.float32, device=q.device) \
+                        if cu_q is None else \
+                        torch.full(shape[:2], -float("inf"), dtype=torch.float32, device=q.device)
                 if workspace is None:
                     workspace = torch.empty(self._workspace_bytes(seq_lens.shape[0], T),
                                             dtype=torch.uint8, device=q.device)
@@ -687,7 +688,8 @@ class LatentAttention:
                 if out is None:
                     out = torch.zeros(shape, dtype=torch.bfloat16, device=q.device)
                 if lse is None:
-                    lse = torch.full(shape[:2], -float("inf"), device=q.device)
+                    lse = torch.full(shape[:2], -float("inf"), dtype=torch.float32,
+                                     device=q.device)
         rc = _marshal.latent_prefill(self._address, self._dims, self.device, q, k, v, k_rope, cu_q,
                                      cu_k, bool(causal), out, lse,
                                      0 if debug is None else ctypes.addressof(debug), stream)

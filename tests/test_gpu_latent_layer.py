@@ -65,7 +65,27 @@ def test_expanded_queries_that_see_a_row_that_is_not_finite(part, bad):
         assert bool(touched[s != -math.inf].all())
 
 
-# ---------------------------------------------------------------- nothing to do
+# ---------------------------------------------------------------- nothing given, nothing to do
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float64])
+def test_what_is_allocated_here_whatever_the_default_type(dtype):
+    at, cache = layer(4), randn(1, 3, 64, 192).cuda()
+    q, kv, kr = randn(2, 2, 4, 192).cuda(), randn(3, 5, 4, 256).cuda(), randn(4, 5, 64).cuda()
+    table, lens, cu_q, cu_k = i32([[0], [1]]), i32([5, 6]), i32([0, 1, 2]), i32([0, 2, 5])
+
+    def calls():
+        return (at.attend(q, cache, table, lens) + at.attend(q, cache, table, lens, cu_q) +
+                at.prefill(q, kv[..., :128], kv[..., 128:], kr, cu_q, cu_k) +
+                at.append(kr.new_ones(2, 192), cu_k[:2].long(), q=q[..., 128:]))
+
+    want, before = calls(), torch.get_default_dtype()
+    torch.set_default_dtype(dtype)
+    try:
+        got = calls()
+    finally:
+        torch.set_default_dtype(before)
+    assert all(a.dtype == b.dtype and torch.equal(a, b) for a, b in zip(got, want))
+
 
 def test_no_tokens_and_no_keys():
     at = layer(5, 128, 32)
