@@ -603,7 +603,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       float m = -INFINITY, l = 0.f, f;
       // the keys' ragged last tile is cleared by the group whose products with it come last
       const int ragged_at =
-          ragged && (u.split ? ((nt - 1) & 1) == w : w == 1 || u.tiles1 < nt) ? mine - 1 : -1;
+          ragged && (u.split ? ((nt - 1) & 1) == w : w == 1) ? mine - 1 : -1;
       int seen = u.split && w ? limit - KEYS : limit;  // keys from the tile's first on
       const int seen_step = u.split ? 2 * KEYS : KEYS;
       for (int j = 0; j < mine; ++j, seen -= seen_step) {
