@@ -32,8 +32,13 @@ namespace {
 // loads went out first.  Every value is read and written once: 8192 tokens of 512 + 64 columns and
 // 64 heads take 31 us (5.2 TB/s), bound by what six blocks an SM keep in flight (one token to a
 // block, loads behind the norm: 37; four or eight blocks an SM by registers: 33, 35); 16 tokens take
-// 2.7.
-constexpr int APPEND_TWO = 1500;  // tokens from which on a block takes two
+// 2.7.  Six blocks leave a thread 40 registers: with two tokens to a block 24 to 60 bytes of them
+// spill, 327,680 requests of the 8192 tokens' traffic to L1, which runs at 75 % of its rate.
+// Tokens from which on a block takes two.  One and two to a block, us, 64 heads: 600 tokens 3.8, 4.4;
+// 1200 5.9, 6.4; 1500 7.2, 7.0; 3000 15.6, 13.8; 8192 35.2, 30.5.  48 heads cross there too, 40 heads
+// of 256 + 32 columns are alike from 600 on, 128 heads lose up to 5 % between 1900 and 2700 (16.5,
+// 17.2 at 2000).
+constexpr int APPEND_TWO = 1500;
 struct AppendParams {
   const void* kv;
   const int64_t* positions;
