@@ -488,7 +488,9 @@ typedef struct klt_latent_debug {
                                 second of a pair of CTAs one later), so the waits on its data run
                                 out (klt_latent_status)                                   */
   int32_t timeout_ms;        /* bound of every on-device wait (0 = 1000 ms); waits that may last
-                                for a sequence's keys are given some 8 us more per tile   */
+                                for a sequence's keys are given some 8 us more per tile, and
+                                those at a kernel's end, for what other threads have begun, three
+                                or four times the bound                                   */
 } klt_latent_debug;
 
 /* New tokens' rows, normed and rotated, into the cache, and the queries' position parts rotated:
@@ -547,7 +549,8 @@ typedef struct klt_latent_attend_args {
 } klt_latent_attend_args;
 
 /* Bytes of workspace that klt_latent_attend needs on this device for B sequences and T queries,
- * whatever their lengths. */
+ * whatever their lengths.  They are the same for all B and T: what parts on all SMs take, 40 MB at a
+ * latent of 512. */
 int klt_latent_workspace(const klt_latent* h, int32_t B, int32_t T, uint64_t* bytes);
 
 /* Run klt_latent_attend_args on `stream`.  T == 0 launches nothing.

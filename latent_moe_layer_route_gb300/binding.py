@@ -563,7 +563,8 @@ class LatentAttention:
     """Latent attention of one layer (klt_latent_*): the step that fills the paged cache of latent
     rows, attention over it in absorbed form, and attention in expanded form.  Owns a handle with
     its own copy of inv_freq and gamma, on inv_freq's device.  Threads may share it, but close()
-    must not overlap a call.
+    must not overlap a call, and graphs captured from its calls need it while they are replayed.
+    Forward only: results carry no gradient.
 
     inv_freq: fp32 [rope / 2], the angle of pair i at position p is p * inv_freq[i]; gamma: bf16
     [latent] or None; scale: of the scores, None for 1 / sqrt(nope + rope); pairs "halves" (element
@@ -651,7 +652,8 @@ class LatentAttention:
         """q bf16 [T, heads, latent + rope] over the cache; block_table int32 [B, max_pages],
         seq_lens int32 [B] (the queries' own tokens counted), cu_q int32 [B + 1] or None for one
         query a sequence.  Returns out bf16 [T, heads, latent] and lse fp32 [T, heads]; what is
-        allocated here is zeros and minus infinity outside of cu_q's ranges."""
+        allocated here is zeros and minus infinity outside of cu_q's ranges, so with cu_q it is
+        filled on every call (prefill() says what that costs)."""
         if out is None or lse is None or workspace is None:
             import torch
             T = q.shape[0]
@@ -680,7 +682,8 @@ class LatentAttention:
         """q bf16 [T, heads, nope + rope], k bf16 [S, heads, nope], v bf16 [S, heads, value], k_rope
         bf16 [S, rope], cu_q and cu_k int32 [B + 1].  Returns out bf16 [T, heads, value] and lse
         fp32 [T, heads]; what is allocated here is zeros and minus infinity outside of cu_q's
-        ranges."""
+        ranges: filled on every call (27 us of host time, 30 us of the GPU's at 8192 tokens of 64
+        heads), so a loop passes out and lse of its own."""
         if out is None or lse is None:
             import torch
             shape = (q.shape[0], self.dims.heads, self.dims.value)

@@ -18,17 +18,23 @@
 // results do not depend on timing.  Each CTA records what its parts belong to on every call: the
 // workspace holds no state between calls.
 //
+// Weights are rounded to bf16, since the tensor core multiplies them by the cache's bf16 values:
+// unnormalised, below 2^8, each by at most 2^-8 of itself.  Scores, maxima, results and the sum that
+// divides them, which is that of the unrounded weights, are fp32.  Against 64 bits results are off
+// by 0.0017 to 0.0020 (root of squares), 0.0016 to 0.0017 with fp32 weights: what is above is this
+// rounding.  Weights in two bf16 parts would double the second product.
+//
 // What bounds it.  A tile of 512 + 64 columns moves 72 KB from memory (3,130 cycles at an SM's share
 // of its rate) and 325 KB through shared memory: 147 KB of operands of the scores, 98 KB of the
 // values, 72 KB of the copy, 8 KB of weights, 2,540 cycles at 128 bytes a cycle; with its copies left
 // out a tile takes 2,720.  130,001 keys of 64 heads take 47 us (3.2 TB/s; 14 tiles to an SM), 32
-// ragged sequences 47 (3.5 TB/s): the stream itself is some 23, the shares (4 until the first copy is
-// issued), the first copy (2.5), the end of a part (2.5) and the second kernel (6, 20 MB of fp32 parts
-// through L2) are the rest.  128 sequences of 128 heads take 110 (649 TFLOP/s): two row tiles to a
-// sequence, 60 tiles to an SM, bound by shared memory.  77 keys of 16 heads take 9.8, all of it such
-// steps.  Nothing else was it: a quarter of the products of scores or values took 7 and 4 us off
-// those 110 (118 then), no exponentials none, keys multicast to both row tiles 3 us more, spinning
-// waits none.
+// ragged sequences 47 (3.5 TB/s): the stream itself is some 23.  One sequence of 64 heads over all
+// SMs takes 8.5 us + 2.0 for each tile of an SM's (2 to 14 of them; 1.65 beyond) without the second
+// kernel, which adds 10.4 (20 MB of fp32 parts out to L2 and back).  128 sequences of 128 heads take
+// 110 (649 TFLOP/s): two row tiles to a sequence, 60 tiles to an SM, bound by shared memory.  77 keys
+// of 16 heads take 9.8, all of it start and end.  Nothing else was it: a quarter of the products of
+// scores or values took 7 and 4 us off those 110 (118 then), no exponentials none, keys multicast to
+// both row tiles 3 us more, spinning waits none.
 #include "klt_latent.cuh"
 
 #include "../../include/klt.h"

@@ -19,14 +19,21 @@
 //
 // The softmax goes over a tile's scores once, 64 keys at a time: they are weighted by the maximum in
 // use while their own is found, and once more in the rare case that it has grown by 2^8 (then O is
-// rescaled too).  Each half's weights are handed to the tensor core as they are written.  8192 tokens
-// of 64 heads take 780 us (1.76 PFLOP/s, 91 % of a large library product's rate).  With the maximum
+// rescaled too).  Each half's weights are handed to the tensor core as they are written, as bf16, the
+// type of the values that they multiply: unnormalised, below 2^8, each rounded by at most 2^-8 of
+// itself.  The sum that divides results is that of the unrounded weights, and scores, maxima, sums and
+// results are fp32.  Against 64 bits results are off by 0.0018 to 0.0023 (root of squares), 0.0016 to
+// 0.0017 with fp32 weights.  8192 tokens of 64 heads take 774 to 811 us in a burst (up to 1.78
+// PFLOP/s, 92 % of a large library product's rate), 846 to 869 in runs of seconds.  With the maximum
 // found in a pass of its own, the kernel of 807 us before took 895; a quarter of the exponentials by
 // a polynomial 937, two threads to a row 986: the exponential unit is not what bounds this on
 // sm_103a, the way of a tile through scores, softmax and values is (some 4,300 cycles where a group
 // is alone, of which its softmax 2,300).  Hence short sequences cost most: 12 ragged ones of up to
-// 2500 tokens 262 us (0.93 PFLOP/s).  First scores of the next unit issued while the second group
-// ends this one: no gain; the first tile's maximum found ahead of its weights: 5 % slower.
+// 2500 tokens 262 to 275 us (0.93 PFLOP/s).  Values of 64 columns are multiplied as 128, the second
+// CTA's half as zeros: 8192 tokens of 64 + 64 + 64 columns 683 us (1.21 PFLOP/s), 128 + 64 + 64 783.
+// A unit's keys are never cut over pairs: 128 queries of 16 K keys take 124 us with 16 heads, which
+// keep 16 of the 76 pairs, and 126 with 64.  First scores of the next unit issued while the second
+// group ends this one: no gain; the first tile's maximum found ahead of its weights: 5 % slower.
 #include "klt_latent.cuh"
 
 #include "../../include/klt.h"
@@ -495,7 +502,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     if (elect_one()) {
       // ---------------------------------------------- products
       constexpr uint32_t sdesc = idesc_make(1, 256, 128);
-      constexpr uint32_t vdesc = idesc_make(1, 256, 128) | IDESC_B_MN;
+      constexpr uint32_t vdesc = idesc_make(1, 256, 128) | IDESC_B_MN;  // values of 64 columns too
       bool ok = true;
       int g = 0, nl = 0;         // tiles of keys before this unit; ragged units
       int nq0 = 0, nq1 = 0;      // tiles of queries
