@@ -292,7 +292,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int shift = all >> 31 ? 3 : 0;
       const uint32_t sum = static_cast<uint32_t>((all + (1 << shift) - 1) >> shift);
       const uint32_t least = max(static_cast<uint32_t>(MIN_TILES), (sum + groups - 1) / groups);
-      const uint32_t most = max(least, (sum + groups - items - 1) / (groups - items));
+      // no item has more tiles than 2^26
+      const uint32_t most =
+          max(least, min((sum + groups - items - 1) / (groups - items), 1u << (26 - shift)));
       auto candidate = [&](int i) {
         return static_cast<int>((least + (most - least) / (WARPS - 1) * i +
                                  (most - least) % (WARPS - 1) * i / (WARPS - 1)) << shift);
