@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   __shared__ float tops[2][ROWS];  // of each half of a tile's keys: maxima; at the end sums
   __shared__ int64_t out_at[ROWS];
   __shared__ long long sums[THREADS / 32];
-  __shared__ int counts[THREADS / 32], needs[THREADS / 32];
+  __shared__ int counts[THREADS / 32], longest[THREADS / 32], needs[THREADS / 32];
   __shared__ long long found_base;
   __shared__ int found_b;
   __shared__ uint32_t tmem_holder;
@@ -245,13 +245,17 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   // The work of all, and this group's share of it.  Where there are fewer items than groups, each
   // item has groups of its own: the smallest share t with sum(ceil(tiles / t)) <= groups is found,
-  // twelve candidates at once, a warp each, between W / groups and W / (groups - items), which is
-  // always enough.  Else the tiles of all items in a row are cut into equal shares, and a group may
-  // have the end of one item and the start of the next (which costs it some 10 us of work: 32
-  // ragged sequences took 67 us that way, 59 by items).
+  // twelve candidates at once, a warp each, between W / groups and W / (groups - items) or the
+  // longest item, which are always enough.  Else, and where t is above 1.2 equal shares, the tiles of
+  // all items in a row are cut into equal shares, and a group may have the end of one item and the
+  // start of the next.  That costs some us: 32 ragged sequences of up to 8192 keys take 43.3 by items
+  // and 44.8 in equal shares, 130 of 4096 112 and 122.  But items of their own leave groups idle (77
+  // of 4096 105 and 80) or a long sequence with one group (130 ragged ones 177 and 122, 150 short ones
+  // and one of 30,000 keys 339 and 48).  At 1.2 both take the same (120 of 4096 110 and 115, 110 of
+  // them, at 1.3, 109 and 106).
   const int group = blockIdx.x >> (p.members - 1);  // one or two members
   long long W = 0, mine = 0, excl = 0;
-  int groups = gridDim.x >> (p.members - 1), items = 0;
+  int groups = gridDim.x >> (p.members - 1), items = 0, top = 0;
   Walk walk;
   Piece w;
   bool more = false;  // w is a piece
@@ -264,6 +268,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       s.load(p, b);
       mine += s.cost();
       items += s.supers;
+      if (s.supers > 0) top = max(top, s.tiles);
       seqs[tid] = s;
     }
     // block-wide sum; where one pass covers the batch, also this sequence's place in it
@@ -274,7 +279,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (lane >= o) incl += v;
     }
     items = __reduce_add_sync(0xFFFFFFFFu, items);
-    if (lane == 31) sums[warp] = incl, counts[warp] = items;
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    if (lane == 31) sums[warp] = incl, counts[warp] = items, longest[warp] = top;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -283,23 +289,25 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (i == warp) excl = W + incl - mine;
       W += sums[i];
       items += counts[i];
+      top = max(top, longest[i]);
     }
     walk.parts = 0;
     walk.pos = walk.lo = walk.hi = 0;
-    if (p.B <= THREADS && items < groups) {
+    bool apart = p.B <= THREADS && items < groups;
+    int t = 0;
+    if (apart) {
       // the tiles, in units of 8 where 32 bits do not hold them
       const long long all = W - static_cast<long long>(items) * EXTRA;
       const int shift = all >> 31 ? 3 : 0;
       const uint32_t sum = static_cast<uint32_t>((all + (1 << shift) - 1) >> shift);
       const uint32_t least = max(static_cast<uint32_t>(MIN_TILES), (sum + groups - 1) / groups);
-      // no item has more tiles than 2^26
-      const uint32_t most =
-          max(least, min((sum + groups - items - 1) / (groups - items), 1u << (26 - shift)));
+      const uint32_t most = max(least, min((sum + groups - items - 1) / (groups - items),
+                                           (top + (1u << shift) - 1) >> shift));
       auto candidate = [&](int i) {
         return static_cast<int>((least + (most - least) / (WARPS - 1) * i +
                                  (most - least) % (WARPS - 1) * i / (WARPS - 1)) << shift);
       };
-      int t = candidate(0);
+      t = candidate(0);
       if (least != most) {  // (one sequence: nothing to search, 0.4 us)
         t = candidate(warp);
         int need = 0;
@@ -312,6 +320,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         while (i < WARPS - 1 && needs[i] > groups) ++i;
         t = candidate(i);
       }
+      apart = 5ll * t * groups <= 6 * W + 10ll * groups;  // or two tiles more than 1.2, if all is short
+    }
+    if (apart) {
       int before = 0;
       for (int b0 = 0; b0 < p.B; b0 += 32) {
         const bool there = b0 + lane < p.B;
@@ -814,14 +825,14 @@ __global__ void __launch_bounds__(THREADS, 1)
 // divisions and 64-bit addresses per load this was bound by its instructions (11 us for 152 parts of
 // 64 x 512, 20 MB; now 6 to 8).
 __global__ void __launch_bounds__(JOIN, 8)
-    join_kernel(const AttendParams p, int ctas, int slots) {
+    join_kernel(const AttendParams p, int ctas) {
   __shared__ float4 weight[MAX_PARTS], inverse;
   __shared__ int64_t out_at[4];
   pdl_trigger();
   pdl_wait();
   const Space ws = space_of(p.part, ctas);
-  const int cta = blockIdx.x >> (slots - 1);
-  const Record rec = ws.records[2 * cta + (blockIdx.x & (slots - 1))];
+  const int cta = blockIdx.x;
+  const Record rec = ws.records[2 * cta + blockIdx.z];
   if (!rec.valid) return;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int parts = rec.last - rec.first + 1;
@@ -977,11 +988,13 @@ cudaError_t launch_attend(const CUtensorMap& latents, const CUtensorMap& ropes,
   cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, attend_kernel, latents, ropes, queries, p);
   if (e != cudaSuccess || (by_items && parts == 1)) return e;
-  const int slots = by_items ? 1 : 2;
-  cfg.gridDim = dim3(slots * ctas, UNITS);
+  // Where groups are seven times the items no share is above 7/6 of an equal one and a tile: the items
+  // have groups of their own, which leave nothing in their second slots.
+  const int slots = by_items && items * 7 <= groups ? 1 : 2;
+  cfg.gridDim = dim3(ctas, UNITS, slots);  // blocks of second slots, often empty ones, come last
   cfg.blockDim = dim3(JOIN);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, join_kernel, static_cast<const AttendParams>(p), ctas, slots);
+  return cudaLaunchKernelEx(&cfg, join_kernel, static_cast<const AttendParams>(p), ctas);
 }
 
 }  // namespace klt
